@@ -239,6 +239,92 @@ spec_status_t spec_kv_commit(void *cache, const void *staged, int NL, int B, int
                              const int32_t *accept_len, int32_t *seq_len, int32_t *device_status,
                              void *stream);
 
+/* The KV cache in 8 bits.  An entry of a layer is [2][Hkv][D]: the keys, then
+ * the values, of Hkv heads of D elements (D = 64 or 128).  Quantised, it is D
+ * e4m3 codes per head (1 sign, 4 exponent, 3 mantissa bits, largest number
+ * 448) and one scale byte per head in an array of its own, [2][Hkv] per entry:
+ *   element = code * 2^(byte - 127); byte 255: every element of the head is NaN.
+ * A head with the largest magnitude amax gets the least e >= -126 with
+ * amax <= 448 * 2^e, byte e + 127 (127 when amax == 0), and the codes
+ * e4m3(x * 2^-e), rounded to nearest even; a head with a NaN or an infinity
+ * gets byte 255.  An element is exact in bfloat16 and in float32.
+ *
+ * spec_kv_commit_quant commits the accepted entries of a verification pass as
+ * spec_kv_commit does (the same sections), quantising them on the way:
+ *   cache       [NL][B][L][2][Hkv][D]  e4m3 codes
+ *   scale       [NL][B][L][2][Hkv]     scale bytes
+ *   staged      [NL][B][K][2][Hkv][D]  the K new entries, dtype `sdt`
+ *   nodes       [B][K]  staged entries after the lead, in the order of the
+ *               commit (out_nodes of spec_verify_tree_greedy), or NULL (in order)
+ *   accept_len  [B]     accepted drafts, or < 0 for a sequence in error
+ *   seq_len     [B]     in/out: cache lengths
+ *   lead        staged entries that are committed ahead of the accepted ones:
+ *               0, or 1 when entry 0 is that of the last emitted token, the
+ *               pass's first input (a tree's root)
+ * For a = accept_len[b] >= 0, n = lead + a entries go to positions
+ * seq_len[b].. of every layer and seq_len[b] += n: entry i < lead is staged
+ * entry i, a later one is staged entry i, or nodes[b][i - lead].  a < 0 changes
+ * nothing.  n > K, seq_len[b] outside [0, L - n] or a used node outside [0, K)
+ * changes nothing and sets *device_status to SPEC_ERR_INVALID_ARG
+ * (device_status is set to 0 first; it may be NULL).  16-byte aligned arrays
+ * (scale: any); staged must not overlap cache.  Asynchronous on `stream`, two
+ * launches.                                                                   */
+spec_status_t spec_kv_commit_quant(void *cache, uint8_t *scale, const void *staged, spec_dtype_t sdt,
+                                   const int32_t *nodes, int lead, int NL, int B, int K, int L, int Hkv, int D,
+                                   const int32_t *accept_len, int32_t *seq_len, int32_t *device_status,
+                                   void *stream);
+
+/* Reads entries of an 8-bit cache back:
+ *   out [NL][B][count][2][Hkv][D], dtype `odt`: entry i of sequence b is the
+ *   cache's entry start[b] + i (start NULL: 0), zero at and past seq_len[b].
+ * seq_len[b] outside [0, L] or start[b] < 0 gives zeros and sets *device_status
+ * to SPEC_ERR_INVALID_ARG (set to 0 first; may be NULL).  Exact.  16-byte
+ * aligned arrays (scale: any).  Asynchronous on `stream`, one launch.          */
+spec_status_t spec_kv_read_quant(const void *cache, const uint8_t *scale, const int32_t *start,
+                                 const int32_t *seq_len, int NL, int B, int L, int count, int Hkv, int D, void *out,
+                                 spec_dtype_t odt, int32_t *device_status, void *stream);
+
+/* Attention of the verification pass (nextadmin.net lesson "Speculative
+ * Decoding", § KV cache management: one target forward pass over the drafts
+ * extends the cache; aiengineeringfromscratch.com Phase 10 lesson 25, § Tree
+ * attention verification: each node of a draft tree sees only its ancestors).
+ * The T query tokens of sequence b (the last emitted token and K drafts, a
+ * tree's N nodes, or the single token of plain decoding) attend to
+ *   - a prefix of P entries that every sequence of the batch shares,
+ *   - the sequence's own cache entries [0, seq_len[b]),
+ *   - the T entries of this pass, not yet committed: entry j for token t where
+ *     mask[b][t][j] != 0 (spec_tree_mask's layout), without a mask where j <= t.
+ * For query head hq, which reads key/value head hq / (Hq / Hkv):
+ *   out = sum_j w_j v_j / sum_j w_j,  w_j = exp(sm_scale q . k_j),
+ *   lse = ln sum_j w_j, over the visible entries.
+ * A row that sees nothing has out = 0 and lse = -inf.  Entries that a row does
+ * not see are never part of its result, whatever they hold.
+ *   q             [B][T][Hq][D]       bfloat16
+ *   prefix        [P][2][Hkv][D]      bfloat16, or e4m3 codes when quant != 0; NULL when P == 0
+ *   prefix_scale  [P][2][Hkv]         scale bytes (quant != 0), else NULL
+ *   cache         [B][L][2][Hkv][D]   one layer of the cache, of the prefix's type; NULL when L == 0
+ *   cache_scale   [B][L][2][Hkv]      scale bytes (quant != 0), else NULL
+ *   seq_len       [B]                 int32
+ *   staged        [B][T][2][Hkv][D]   bfloat16, or NULL: no entries of this pass (mask NULL too)
+ *   mask          [B][T][T]           uint8, or NULL
+ *   out           [B][T][Hq][D]       bfloat16
+ *   lse           [B][T][Hq]          float32 (may be NULL)
+ *   workspace     device scratch of spec_attention_workspace_bytes(...) bytes (no
+ *                 zero-fill needed), 16-byte aligned; one per call in flight
+ *   device_status [1] set to 0, or the code of one failing sequence; may be NULL
+ * seq_len[b] outside [0, L] is an error (SPEC_ERR_INVALID_ARG): that
+ * sequence's outputs are NaN.  Scores, softmax statistics and sums are float32;
+ * the weights are rounded to bfloat16 where they meet the values.
+ * Limits: D = 64 or 128, Hq a multiple of Hkv, Hq / Hkv <= 128, sm_scale finite
+ * and > 0, P, L >= 0, T <= 2048, B T Hq <= 2^30.  All arrays but the scales, mask and
+ * lse 16-byte aligned.  Asynchronous on `stream`.                              */
+size_t spec_attention_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int P, int L);
+spec_status_t spec_verify_attention(const void *q, const void *prefix, const uint8_t *prefix_scale, const void *cache,
+                                    const uint8_t *cache_scale, int quant, const int32_t *seq_len,
+                                    const void *staged, const uint8_t *mask, int B, int T, int Hq, int Hkv, int D,
+                                    int P, int L, float sm_scale, void *out, float *lse, void *workspace,
+                                    size_t workspace_bytes, int32_t *device_status, void *stream);
+
 /* Greedy tree verification (aiengineeringfromscratch.com Phase 10 lesson 25,
  * § Tree attention verification: one target pass over a draft tree under a
  * mask where each token sees only its ancestors; the output is the longest

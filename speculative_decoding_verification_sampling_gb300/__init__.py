@@ -23,6 +23,7 @@ from .build import LIB as _LIB_PATH
 __all__ = [
     "SpecVerifyError", "Aux", "spec_verify", "spec_verify_greedy", "spec_verify_shortlist",
     "spec_workspace_bytes", "spec_philox_words", "spec_draft_sample", "spec_kv_commit", "spec_verify_tree_greedy", "spec_tree_mask",
+    "spec_kv_commit_quant", "spec_kv_read_quant", "spec_verify_attention", "spec_attention_workspace_bytes",
     "spec_verify_shortlist_pos", "spec_status_string", "spec_launch_count", "spec_verify_static", "library_path", "load",
 ]
 
@@ -88,6 +89,14 @@ def load():
             lib.spec_tree_mask.restype = I
             lib.spec_kv_commit.argtypes = [P, P, I, I, I, I, Z, P, P, P, P]
             lib.spec_kv_commit.restype = I
+            lib.spec_kv_commit_quant.argtypes = [P, P, P, I, P, I, I, I, I, I, I, I, P, P, P, P]
+            lib.spec_kv_commit_quant.restype = I
+            lib.spec_kv_read_quant.argtypes = [P, P, P, P, I, I, I, I, I, I, P, I, P, P]
+            lib.spec_kv_read_quant.restype = I
+            lib.spec_attention_workspace_bytes.argtypes = [I, I, I, I, I, I, I]
+            lib.spec_attention_workspace_bytes.restype = Z
+            lib.spec_verify_attention.argtypes = [P, P, P, P, P, I, P, P, P, I, I, I, I, I, I, I, F, P, P, P, Z, P, P]
+            lib.spec_verify_attention.restype = I
             lib.spec_draft_sample.argtypes = [P, I, I, I, I, F, U64, P, P, P, P]
             lib.spec_draft_sample.restype = I
             lib.spec_launch_count.argtypes = []
@@ -366,6 +375,159 @@ def spec_kv_commit(cache: torch.Tensor, staged: torch.Tensor | None, accept_len:
     if rc:
         raise SpecVerifyError(rc, "spec_kv_commit")
     return seq_len
+
+
+def spec_kv_commit_quant(cache: torch.Tensor, scale: torch.Tensor, staged: torch.Tensor, accept_len: torch.Tensor,
+                         seq_len: torch.Tensor, *, nodes: torch.Tensor | None = None, lead: int = 0,
+                         device_status=None, stream=None):
+    """Commit the accepted drafts' KV entries to an 8-bit cache: cache
+    [NL][B][L][2][Hkv][D] float8_e4m3fn with scale [NL][B][L][2][Hkv] uint8
+    (element = code * 2^(byte - 127)), staged [NL][B][K][2][Hkv][D] float32 or
+    bfloat16, accept_len [B] int32 (as the verification returns it), seq_len [B]
+    int32 updated in place.  nodes [B][K] int32: the staged entries of an
+    accepted tree path (spec_verify_tree_greedy's out_nodes).  lead = 1: staged
+    entry 0, that of the last emitted token, is committed ahead of them."""
+    if not isinstance(cache, torch.Tensor) or cache.dim() != 6:
+        raise TypeError("cache must be a CUDA tensor [NL][B][L][2][Hkv][D]")
+    if not isinstance(staged, torch.Tensor) or staged.dim() != 6:
+        raise TypeError("staged must be a CUDA tensor [NL][B][K][2][Hkv][D]")
+    NL, B, L, _, H, D = cache.shape
+    K = staged.shape[2]
+    _check(cache, (NL, B, L, 2, H, D), (torch.float8_e4m3fn,), "cache")
+    _check(scale, (NL, B, L, 2, H), (torch.uint8,), "scale")
+    _check(staged, (NL, B, K, 2, H, D), (torch.float32, torch.bfloat16), "staged")
+    _check(accept_len, (B,), (torch.int32,), "accept_len")
+    _check(seq_len, (B,), (torch.int32,), "seq_len")
+    if nodes is not None:
+        _check(nodes, (B, K), (torch.int32,), "nodes")
+    if device_status is not None:
+        _check(device_status, (1,), (torch.int32,), "device_status")
+    rc = load().spec_kv_commit_quant(cache.data_ptr(), scale.data_ptr(), staged.data_ptr(), _dt(staged),
+                                     nodes.data_ptr() if nodes is not None else None, int(lead), NL, B, K, L, H, D,
+                                     accept_len.data_ptr(), seq_len.data_ptr(),
+                                     device_status.data_ptr() if device_status is not None else None,
+                                     _stream(cache.device, stream))
+    if rc:
+        raise SpecVerifyError(rc, "spec_kv_commit_quant")
+    return seq_len
+
+
+def spec_kv_read_quant(cache: torch.Tensor, scale: torch.Tensor, start: torch.Tensor | None, seq_len: torch.Tensor,
+                       count: int, *, dtype=torch.bfloat16, out=None, device_status=None,
+                       stream=None) -> torch.Tensor:
+    """Entries start[b] .. start[b] + count - 1 (start None: from 0) of an 8-bit
+    cache [NL][B][L][2][Hkv][D] in bfloat16 or float32 (exact), zero at and past
+    seq_len[b].  Returns [NL][B][count][2][Hkv][D]."""
+    if not isinstance(cache, torch.Tensor) or cache.dim() != 6:
+        raise TypeError("cache must be a CUDA tensor [NL][B][L][2][Hkv][D]")
+    NL, B, L, _, H, D = cache.shape
+    count = int(count)
+    _check(cache, (NL, B, L, 2, H, D), (torch.float8_e4m3fn,), "cache")
+    _check(scale, (NL, B, L, 2, H), (torch.uint8,), "scale")
+    if start is not None:
+        _check(start, (B,), (torch.int32,), "start")
+    _check(seq_len, (B,), (torch.int32,), "seq_len")
+    if out is None:
+        if count < 1:
+            raise ValueError("count must be at least 1")
+        out = torch.empty((NL, B, count, 2, H, D), dtype=dtype, device=cache.device)
+    _check(out, (NL, B, count, 2, H, D), (torch.float32, torch.bfloat16), "out")
+    if device_status is not None:
+        _check(device_status, (1,), (torch.int32,), "device_status")
+    rc = load().spec_kv_read_quant(cache.data_ptr(), scale.data_ptr(), start.data_ptr() if start is not None else None,
+                                   seq_len.data_ptr(), NL, B, L, count, H, D, out.data_ptr(), _dt(out),
+                                   device_status.data_ptr() if device_status is not None else None,
+                                   _stream(cache.device, stream))
+    if rc:
+        raise SpecVerifyError(rc, "spec_kv_read_quant")
+    return out
+
+
+def spec_attention_workspace_bytes(B: int, T: int, Hq: int, Hkv: int, D: int, P: int, L: int) -> int:
+    return int(load().spec_attention_workspace_bytes(int(B), int(T), int(Hq), int(Hkv), int(D), int(P), int(L)))
+
+
+def _scratch(nbytes, device, st):
+    """Scratch of one call, from the allocator's pool of the stream that the
+    call runs on: freed when the call returns, it is handed out again only to
+    later work of that stream."""
+    if st == torch.cuda.current_stream(device).cuda_stream:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(st, device=device)):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def spec_verify_attention(q: torch.Tensor, cache: torch.Tensor, seq_len: torch.Tensor, *,
+                          staged: torch.Tensor | None = None, mask: torch.Tensor | None = None,
+                          prefix: torch.Tensor | None = None, cache_scale: torch.Tensor | None = None,
+                          prefix_scale: torch.Tensor | None = None, sm_scale: float | None = None, out=None,
+                          lse=None, workspace=None, device_status=None, stream=None):
+    """Attention of the verification pass: q [B][T][Hq][D] bfloat16 attends to a
+    prefix [P][2][Hkv][D] that the batch shares, to the sequence's own cache
+    entries [0, seq_len[b]) (cache [B][L][2][Hkv][D], one layer) and to the
+    pass's own entries staged [B][T][2][Hkv][D], under mask [B][T][T] uint8
+    (spec_tree_mask) or causally.  Prefix and cache are bfloat16, or both
+    float8_e4m3fn with cache_scale [B][L][2][Hkv] and prefix_scale [P][2][Hkv]
+    uint8.  sm_scale defaults to 1 / sqrt(D).  Returns (out [B][T][Hq][D]
+    bfloat16, lse [B][T][Hq] float32); a row that sees nothing has 0 and -inf."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise TypeError("q must be a CUDA tensor [B][T][Hq][D]")
+    if not isinstance(cache, torch.Tensor) or cache.dim() != 5:
+        raise TypeError("cache must be a CUDA tensor [B][L][2][Hkv][D]")
+    B, T, Hq, D = q.shape
+    L, H = cache.shape[1], cache.shape[3]
+    dev = q.device
+    quant = cache.dtype == torch.float8_e4m3fn
+    kind = (cache.dtype,) if quant else (torch.bfloat16,)
+    _check(q, (B, T, Hq, D), (torch.bfloat16,), "q")
+    _check(cache, (B, L, 2, H, D), kind, "cache")
+    _check(seq_len, (B,), (torch.int32,), "seq_len")
+    if quant != (cache_scale is not None):
+        raise ValueError("cache_scale goes with a float8_e4m3fn cache")
+    if quant:
+        _check(cache_scale, (B, L, 2, H), (torch.uint8,), "cache_scale")
+    P = 0
+    if prefix is not None:
+        P = prefix.shape[0]
+        _check(prefix, (P, 2, H, D), kind, "prefix")
+    if (quant and prefix is not None) != (prefix_scale is not None):
+        raise ValueError("prefix_scale goes with a float8_e4m3fn prefix")
+    if prefix_scale is not None:
+        _check(prefix_scale, (P, 2, H), (torch.uint8,), "prefix_scale")
+    if staged is not None:
+        _check(staged, (B, T, 2, H, D), (torch.bfloat16,), "staged")
+    if mask is not None:
+        _check(mask, (B, T, T), (torch.uint8,), "mask")
+    if out is None:
+        out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _check(out, (B, T, Hq, D), (torch.bfloat16,), "out")
+    if lse is None:
+        lse = torch.empty((B, T, Hq), dtype=torch.float32, device=dev)
+    else:
+        _check(lse, (B, T, Hq), (torch.float32,), "lse")
+    if device_status is not None:
+        _check(device_status, (1,), (torch.int32,), "device_status")
+    st = _stream(dev, stream)
+    lib = load()
+    if workspace is None:
+        nbytes = lib.spec_attention_workspace_bytes(B, T, Hq, H, D, P, L)
+        if nbytes == 0:
+            raise SpecVerifyError(1, "spec_verify_attention")
+        workspace = _scratch(nbytes, dev, st)
+    elif not isinstance(workspace, torch.Tensor) or not workspace.is_cuda:
+        raise TypeError("workspace must be a CUDA tensor")
+
+    def ptr(t):
+        return t.data_ptr() if t is not None else None
+    rc = lib.spec_verify_attention(q.data_ptr(), ptr(prefix), ptr(prefix_scale), cache.data_ptr(), ptr(cache_scale),
+                                   int(quant), seq_len.data_ptr(), ptr(staged), ptr(mask), B, T, Hq, H, D, P, L,
+                                   float(sm_scale) if sm_scale is not None else D ** -0.5, out.data_ptr(),
+                                   lse.data_ptr(), workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), ptr(device_status), st)
+    if rc:
+        raise SpecVerifyError(rc, "spec_verify_attention")
+    return out, lse
 
 
 def spec_verify_tree_greedy(target: torch.Tensor, tree_tokens: torch.Tensor, parent: torch.Tensor, *,

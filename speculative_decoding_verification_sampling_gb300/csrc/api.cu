@@ -148,6 +148,33 @@ bool sizes_ok(int B, int K, int V, int S)
     return rows * chunks < (1LL << 31);
 }
 
+bool misaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+
+// Sizes of the 8-bit KV cache calls: K entries of NL x B caches.
+spec_status_t quant_cache_check(int NL, int B, int K, int L, int H, int D)
+{
+    if (NL < 1 || B < 1 || K < 1 || L < 1 || H < 1 || (D != 64 && D != 128))
+        return SPEC_ERR_INVALID_ARG;
+    // cache and staged arrays within 2^48 bytes, so every offset fits 64 bits
+    if ((double)NL * B * ((double)L + K) * 2.0 * H * D * 4.0 > 281474976710656.0)
+        return SPEC_ERR_INVALID_ARG;
+    // one entry array of a (layer, sequence) and the grid within 31 bits
+    if ((double)K * 2.0 * H * D > 2147483647.0 || (double)NL * B * (double)sv::kvq_chunks(K, H, D) > 2147483647.0)
+        return SPEC_ERR_UNSUPPORTED;
+    return SPEC_OK;
+}
+
+bool attention_sizes_ok(int B, int T, int Hq, int Hkv, int D, int P, int L)
+{
+    if (B < 1 || T < 1 || T > 2048 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq / Hkv > 128 || (D != 64 && D != 128) ||
+        P < 0 || L < 0)
+        return false;
+    if ((double)B * T * Hq > 1073741824.0)
+        return false;
+    // every byte offset of the prefix and the caches below 2^48
+    return ((double)B * L + P) * 4.0 * Hkv * D <= 281474976710656.0;
+}
+
 // Row-parallel verification (k_rows.cu): logit draft rows (or greedy), no
 // shortlist.  Serves the per-position outputs too (then every row is read).
 // A shortlisted draft for run_rows: the list of (b, i) is the len[i] entries at
@@ -674,6 +701,119 @@ spec_status_t spec_kv_commit(void *cache, const void *staged, int NL, int B, int
         return SPEC_ERR_CUDA;
     g_launches.fetch_add((uint64_t)launches, std::memory_order_relaxed);
     return SPEC_OK;
+}
+
+spec_status_t spec_kv_commit_quant(void *cache, uint8_t *scale, const void *staged, spec_dtype_t sdt,
+                                   const int32_t *nodes, int lead, int NL, int B, int K, int L, int Hkv, int D,
+                                   const int32_t *accept_len, int32_t *seq_len, int32_t *device_status, void *stream)
+{
+    if (!cache || !scale || !staged || !accept_len || !seq_len || (sdt != SPEC_F32 && sdt != SPEC_BF16) ||
+        lead < 0 || lead > 1)
+        return SPEC_ERR_INVALID_ARG;
+    const spec_status_t st = quant_cache_check(NL, B, K, L, Hkv, D);
+    if (st != SPEC_OK)
+        return st;
+    if (misaligned(cache) || misaligned(staged))
+        return SPEC_ERR_INVALID_ARG;
+    sv::KvQuantParams P{};
+    P.cache = static_cast<uint8_t *>(cache);
+    P.scale = scale;
+    P.staged = staged;
+    P.acc = accept_len;
+    P.nodes = nodes;
+    P.len = seq_len;
+    P.status = device_status;
+    P.NL = NL;
+    P.B = B;
+    P.K = K;
+    P.L = L;
+    P.H = Hkv;
+    P.D = D;
+    P.lead = lead;
+    int launches = 0;
+    const cudaError_t e = sv::launch_kvq_commit(P, sdt == SPEC_F32, static_cast<cudaStream_t>(stream), &launches);
+    g_launches.fetch_add((uint64_t)launches, std::memory_order_relaxed);
+    return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+spec_status_t spec_kv_read_quant(const void *cache, const uint8_t *scale, const int32_t *start,
+                                 const int32_t *seq_len, int NL, int B, int L, int count, int Hkv, int D, void *out,
+                                 spec_dtype_t odt, int32_t *device_status, void *stream)
+{
+    if (!cache || !scale || !seq_len || !out || (odt != SPEC_F32 && odt != SPEC_BF16))
+        return SPEC_ERR_INVALID_ARG;
+    const spec_status_t st = quant_cache_check(NL, B, count, L, Hkv, D);
+    if (st != SPEC_OK)
+        return st;
+    if (misaligned(cache) || misaligned(out))
+        return SPEC_ERR_INVALID_ARG;
+    sv::KvQuantParams P{};
+    P.cache = static_cast<uint8_t *>(const_cast<void *>(cache));   // read only here
+    P.scale = const_cast<uint8_t *>(scale);
+    P.start = start;
+    P.len_in = seq_len;
+    P.out = out;
+    P.status = device_status;
+    P.NL = NL;
+    P.B = B;
+    P.K = count;
+    P.L = L;
+    P.H = Hkv;
+    P.D = D;
+    if (sv::launch_kvq_read(P, odt == SPEC_F32, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return SPEC_ERR_CUDA;
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return SPEC_OK;
+}
+
+size_t spec_attention_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int P, int L)
+{
+    if (!attention_sizes_ok(B, T, Hq, Hkv, D, P, L))
+        return 0;
+    return 256;
+}
+
+spec_status_t spec_verify_attention(const void *q, const void *prefix, const uint8_t *prefix_scale, const void *cache,
+                                    const uint8_t *cache_scale, int quant, const int32_t *seq_len,
+                                    const void *staged, const uint8_t *mask, int B, int T, int Hq, int Hkv, int D,
+                                    int P, int L, float sm_scale, void *out, float *lse, void *workspace,
+                                    size_t workspace_bytes, int32_t *device_status, void *stream)
+{
+    const size_t need = spec_attention_workspace_bytes(B, T, Hq, Hkv, D, P, L);
+    if (need == 0 || !q || !seq_len || !out || !workspace || workspace_bytes < need || !std::isfinite(sm_scale) ||
+        sm_scale <= 0.0f)
+        return SPEC_ERR_INVALID_ARG;
+    if ((P > 0 && (!prefix || (quant && !prefix_scale))) || (L > 0 && (!cache || (quant && !cache_scale))) ||
+        (mask && !staged))
+        return SPEC_ERR_INVALID_ARG;
+    if (misaligned(q) || misaligned(out) || misaligned(workspace) || (P > 0 && misaligned(prefix)) ||
+        (L > 0 && misaligned(cache)) || (staged && misaligned(staged)))
+        return SPEC_ERR_INVALID_ARG;
+    sv::AttnParams A{};
+    A.q = q;
+    A.prefix = prefix;
+    A.pscale = prefix_scale;
+    A.cache = cache;
+    A.cscale = cache_scale;
+    A.len = seq_len;
+    A.staged = staged;
+    A.mask = mask;
+    A.out = out;
+    A.lse = lse;
+    A.status = device_status;
+    A.B = B;
+    A.T = T;
+    A.Hq = Hq;
+    A.H = Hkv;
+    A.G = Hq / Hkv;
+    A.D = D;
+    A.P = P;
+    A.L = L;
+    A.c = (float)(1.4426950408889634 * (double)sm_scale);
+    int launches = 0;
+    const cudaError_t e = sv::launch_attention(A, quant != 0, static_cast<cudaStream_t>(stream), &launches);
+    g_launches.fetch_add((uint64_t)launches, std::memory_order_relaxed);
+    return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 size_t spec_tree_workspace_bytes(int B, int N, int V)

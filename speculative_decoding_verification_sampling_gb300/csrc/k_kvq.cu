@@ -1,0 +1,271 @@
+// k_kvq.cu -- the KV cache in 8 bits: the commit that quantises, and reading
+// back.
+//
+// One head's D elements of an entry (a key or a value) share a power of two:
+// with amax the largest magnitude, e is the least integer with
+// amax <= 448 * 2^e (448 is the largest e4m3 number), clamped to >= -126; the
+// entry holds code(x) = e4m3(x * 2^-e), rounded to nearest even, and the byte
+// e + 127.  x * 2^-e is exact in float32, so a code is off by at most half a
+// step of its format and nothing else, and it depends on no order of
+// evaluation.  code * 2^e is exact in bfloat16 as well as in float32 (4
+// significant bits), so reading back and attending to the cache lose nothing.
+// A head whose elements include a NaN or an infinity gets the byte 255, which
+// reads back as NaN everywhere.
+//
+// Both kernels are bound by HBM: the commit reads 2 D (or 4 D) bytes and
+// writes D + 1 per head, reading back the reverse.  A thread takes pieces of
+// eight elements: a warp's 16-byte loads (8-byte for codes) cover contiguous
+// memory, a head's amax is a shuffle reduction over D / 8 lanes, and QU pieces
+// are in flight per thread.
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "sv_fp8.cuh"
+#include "sv_launch.h"
+
+namespace sv {
+namespace {
+
+constexpr int QT = 256;   // threads of a CTA
+constexpr int QU = 4;     // pieces in flight per thread
+
+// ---------------------------------------------------------------- commit
+__device__ __forceinline__ int commit_count(const KvQuantParams &P, int b)
+{
+    // entries that sequence b commits, -1 for one that reports an error
+    const int a = __ldg(P.acc + b), n = P.len[b];
+    if (a < 0)
+        return 0;
+    const long long m = (long long)a + P.lead;
+    if (m > P.K || n < 0 || (long long)n + m > P.L)
+        return -1;
+    return (int)m;
+}
+
+template <class E>
+__device__ __forceinline__ void load_piece(const void *src, size_t at, float (&x)[8], uint32_t &top)
+{
+    // eight elements and the largest of their absolute values' bits
+    if constexpr (sizeof(E) == 2) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(src) + at));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            m = __vmaxu2(m, w[k] & 0x7fff7fffu);
+            x[2 * k] = __uint_as_float(w[k] << 16);
+            x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        }
+        top = max(m << 16, m & 0xffff0000u);
+    } else {
+        const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(src) + at);
+        const float4 lo = __ldg(s), hi = __ldg(s + 1);
+        x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w;
+        x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
+        top = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            top = max(top, __float_as_uint(x[k]) & 0x7fffffffu);
+    }
+}
+
+template <class E, int D>
+__global__ void __launch_bounds__(QT) kvq_commit(const __grid_constant__ KvQuantParams P)
+{
+    constexpr int G = D / 8;   // lanes of a head
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (blockIdx.x == 0 && threadIdx.x == 0 && P.status)
+        *P.status = 0;   // only the length update, after this launch, reports
+    const int ch = blockIdx.x % P.nch;
+    const long long lb = blockIdx.x / P.nch;   // layer * B + b
+    const int b = (int)(lb % P.B);
+    const int n = commit_count(P, b);
+    if (n <= 0)
+        return;
+    const int32_t *nodes = P.nodes ? P.nodes + (size_t)b * P.K : nullptr;
+    if (nodes) {
+        bool bad = false;
+        for (int i = threadIdx.x; i < n - P.lead; i += QT)
+            bad |= (unsigned)__ldg(nodes + i) >= (unsigned)P.K;
+        if (__syncthreads_or(bad))
+            return;
+    }
+    const int per = 2 * P.H * G;                 // pieces of an entry
+    const int total = n * per;                   // a multiple of G: heads never end inside a lane group
+    const int p0 = ch * QT * QU;
+    if (p0 >= total)
+        return;
+    const size_t entry = (size_t)2 * P.H * D;    // elements of an entry
+    const size_t src0 = (size_t)lb * P.K, dst0 = (size_t)lb * P.L + P.len[b];
+    float x[QU][8];
+    uint32_t top[QU];
+    int ent[QU], off[QU];
+#pragma unroll
+    for (int u = 0; u < QU; ++u) {
+        const int p = p0 + u * QT + threadIdx.x;
+        ent[u] = -1;
+        top[u] = 0;
+        off[u] = 0;
+        if (p < total) {
+            const int i = p / per;
+            off[u] = p - i * per;
+            ent[u] = i;
+            const int s = (nodes && i >= P.lead) ? __ldg(nodes + i - P.lead) : i;
+            load_piece<E>(P.staged, (src0 + s) * entry + (size_t)off[u] * 8, x[u], top[u]);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < QU; ++u) {
+#pragma unroll
+        for (int o = G / 2; o; o >>= 1)
+            top[u] = max(top[u], __shfl_xor_sync(0xffffffffu, top[u], o));
+        if (ent[u] < 0)
+            continue;
+        float inv;
+        const uint32_t byte = fp8_scale(top[u], inv);
+        uint2 c;
+        c.x = pack_e4m3(x[u][0] * inv, x[u][1] * inv, x[u][2] * inv, x[u][3] * inv);
+        c.y = pack_e4m3(x[u][4] * inv, x[u][5] * inv, x[u][6] * inv, x[u][7] * inv);
+        const size_t e = dst0 + ent[u];
+        *reinterpret_cast<uint2 *>(P.cache + e * entry + (size_t)off[u] * 8) = c;
+        if (off[u] % G == 0)
+            P.scale[e * (2 * P.H) + off[u] / G] = (uint8_t)byte;
+    }
+}
+
+// One warp per sequence: the length update.
+__global__ void kvq_len(const __grid_constant__ KvQuantParams P)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // every copy has read the old lengths
+    const int b = (blockIdx.x * blockDim.x + threadIdx.x) / 32, lane = threadIdx.x % 32;
+    if (b >= P.B)
+        return;
+    const int n = commit_count(P, b);
+    bool bad = n < 0;
+    if (P.nodes)
+        for (int i = lane; i < n - P.lead; i += 32)
+            bad |= (unsigned)__ldg(P.nodes + (size_t)b * P.K + i) >= (unsigned)P.K;
+    bad = __any_sync(0xffffffffu, bad);
+    if (lane != 0)
+        return;
+    if (!bad)
+        P.len[b] += n;
+    else if (P.status)
+        atomicCAS(P.status, 0, 1);   // past the capacity, above K, or a node outside [0, K)
+}
+
+// ---------------------------------------------------------------- read back
+template <class E, int D>
+__global__ void __launch_bounds__(QT) kvq_read(const __grid_constant__ KvQuantParams P)
+{
+    constexpr int G = D / 8;
+    const int ch = blockIdx.x % P.nch;
+    const long long lb = blockIdx.x / P.nch;
+    const int b = (int)(lb % P.B);
+    const int len = __ldg(P.len_in + b), start = P.start ? __ldg(P.start + b) : 0;
+    const bool bad = len < 0 || len > P.L || start < 0;
+    if (bad && threadIdx.x == 0 && P.status)
+        atomicCAS(P.status, 0, 1);
+    const int per = 2 * P.H * G;
+    const long long total = (long long)P.K * per;                       // K: entries of the window
+    const long long have = bad || start >= len ? 0 : (long long)min(P.K, len - start) * per;
+    const long long p0 = (long long)ch * QT * QU + threadIdx.x;
+    const uint8_t *codes = P.cache + ((size_t)lb * P.L + start) * per * 8;
+    const uint8_t *scale = P.scale + ((size_t)lb * P.L + start) * (2 * P.H);
+    E *out = static_cast<E *>(P.out) + (size_t)lb * total * 8;
+    uint2 c[QU];
+    uint32_t byte[QU];
+#pragma unroll
+    for (int u = 0; u < QU; ++u) {
+        const long long p = p0 + u * QT;
+        c[u] = make_uint2(0, 0);
+        byte[u] = 127;
+        if (p < have) {
+            c[u] = __ldg(reinterpret_cast<const uint2 *>(codes) + p);
+            byte[u] = __ldg(scale + p / G);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < QU; ++u) {
+        const long long p = p0 + u * QT;
+        if (p >= total)
+            continue;
+        float x[8];
+        const float f = fp8_factor(byte[u]);
+        unpack_e4m3(c[u].x, x);
+        unpack_e4m3(c[u].y, x + 4);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            x[k] *= f;
+        if constexpr (sizeof(E) == 2) {
+            uint4 w;   // exact: four significant bits
+            w.x = pack_bf16(x[0], x[1]);
+            w.y = pack_bf16(x[2], x[3]);
+            w.z = pack_bf16(x[4], x[5]);
+            w.w = pack_bf16(x[6], x[7]);
+            *reinterpret_cast<uint4 *>(out + p * 8) = w;
+        } else {
+            float4 *o = reinterpret_cast<float4 *>(out + p * 8);
+            o[0] = make_float4(x[0], x[1], x[2], x[3]);
+            o[1] = make_float4(x[4], x[5], x[6], x[7]);
+        }
+    }
+}
+
+template <class E>
+cudaError_t commit_any(const KvQuantParams &P, unsigned grid, cudaStream_t stream)
+{
+    if (P.D == 128)
+        kvq_commit<E, 128><<<grid, QT, 0, stream>>>(P);
+    else
+        kvq_commit<E, 64><<<grid, QT, 0, stream>>>(P);
+    return cudaGetLastError();
+}
+
+template <class E>
+cudaError_t read_any(const KvQuantParams &P, unsigned grid, cudaStream_t stream)
+{
+    if (P.D == 128)
+        kvq_read<E, 128><<<grid, QT, 0, stream>>>(P);
+    else
+        kvq_read<E, 64><<<grid, QT, 0, stream>>>(P);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+long long kvq_chunks(int K, int H, int D)
+{
+    const long long pieces = (long long)K * 2 * H * (D / 8);
+    return (pieces + QT * QU - 1) / (QT * QU);
+}
+
+cudaError_t launch_kvq_commit(KvQuantParams P, bool wide, cudaStream_t stream, int *launches)
+{
+    P.nch = (int)kvq_chunks(P.K, P.H, P.D);
+    const unsigned grid = (unsigned)((long long)P.NL * P.B * P.nch);
+    *launches = 0;
+    const cudaError_t e = wide ? commit_any<float>(P, grid, stream) : commit_any<__nv_bfloat16>(P, grid, stream);
+    if (e != cudaSuccess)
+        return e;
+    ++*launches;
+    const cudaError_t f = launch_after(kvq_len, (P.B + 7) / 8, 256, 0, stream, P);
+    if (f == cudaSuccess)
+        ++*launches;
+    return f;
+}
+
+cudaError_t launch_kvq_read(KvQuantParams P, bool wide, cudaStream_t stream)
+{
+    P.nch = (int)kvq_chunks(P.K, P.H, P.D);
+    if (P.status) {
+        const cudaError_t e = cudaMemsetAsync(P.status, 0, sizeof(int32_t), stream);
+        if (e != cudaSuccess)
+            return e;
+    }
+    const unsigned grid = (unsigned)((long long)P.NL * P.B * P.nch);
+    return wide ? read_any<float>(P, grid, stream) : read_any<__nv_bfloat16>(P, grid, stream);
+}
+
+}  // namespace sv

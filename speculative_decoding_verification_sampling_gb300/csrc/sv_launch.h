@@ -66,6 +66,15 @@ cudaError_t launch_greedy_rows(const RowsParams &P, int tdt, cudaStream_t stream
 cudaError_t launch_kv_commit(void *cache, const void *staged, int NL, int B, int K, int L, long long W,
                              const int32_t *acc, int32_t *len, int32_t *status, cudaStream_t stream, int *launches);
 
+// The KV cache in 8 bits (k_kvq.cu): quantising commit (two launches), read
+// back (one).  `wide`: float32 entries instead of bfloat16.
+long long kvq_chunks(int K, int H, int D);   // CTAs of one (layer, sequence)
+cudaError_t launch_kvq_commit(KvQuantParams P, bool wide, cudaStream_t stream, int *launches);
+cudaError_t launch_kvq_read(KvQuantParams P, bool wide, cudaStream_t stream);
+
+// Verification attention (k_attn.cu).
+cudaError_t launch_attention(const AttnParams &P, bool quant, cudaStream_t stream, int *launches);
+
 // Greedy tree verification and the tree mask (k_tree.cu).
 int tree_max_nodes();
 cudaError_t launch_tree_walk(const int32_t *tokens, const int32_t *parent, const int32_t *g, int B, int N, int V,

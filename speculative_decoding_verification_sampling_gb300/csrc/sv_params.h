@@ -243,4 +243,39 @@ inline WsLayout ws_layout(int B, int K, int V, int S)
     return w;
 }
 
+// Quantised KV cache (k_kvq.cu): H key/value heads of D elements; an entry is
+// [2][H][D] codes and [2][H] scale bytes.
+struct KvQuantParams {
+    uint8_t *cache;          // [NL][B][L][2][H][D] e4m3 codes
+    uint8_t *scale;          // [NL][B][L][2][H] scale bytes
+    const void *staged;      // commit: [NL][B][K][2][H][D] float32 or bfloat16
+    const int32_t *acc;      // commit: [B]
+    const int32_t *nodes;    // commit: [B][K] staged entries after the lead, or nullptr
+    int32_t *len;            // commit: [B], updated
+    const int32_t *len_in;   // read: [B]
+    const int32_t *start;    // read: [B] or nullptr (0)
+    void *out;               // read: [NL][B][K][2][H][D]
+    int32_t *status;         // [1] or nullptr
+    int NL, B, K, L, H, D, lead, nch;
+};
+
+// Verification attention (k_attn.cu): T query tokens of Hq = H G heads for
+// each of B sequences, over a shared prefix of P entries, the sequence's own
+// cache and its T staged entries.
+struct AttnParams {
+    const void *q;              // [B][T][Hq][D] bfloat16
+    const void *prefix;         // [P][2][H][D] bfloat16, or e4m3 codes
+    const uint8_t *pscale;      // [P][2][H] scale bytes (8-bit cache)
+    const void *cache;          // [B][L][2][H][D]
+    const uint8_t *cscale;      // [B][L][2][H]
+    const int32_t *len;         // [B]
+    const void *staged;         // [B][T][2][H][D] bfloat16 or nullptr
+    const uint8_t *mask;        // [B][T][T] or nullptr (staged j visible to j <= t)
+    void *out;                  // [B][T][Hq][D] bfloat16
+    float *lse;                 // [B][T][Hq] or nullptr
+    int32_t *status;            // [1] or nullptr
+    int B, T, Hq, H, G, D, P, L;
+    float c;                    // scale * log2(e)
+};
+
 }  // namespace sv
