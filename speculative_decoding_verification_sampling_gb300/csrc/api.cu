@@ -148,6 +148,23 @@ bool sizes_ok(int B, int K, int V, int S)
     return rows * chunks < (1LL << 31);
 }
 
+// SMs of the current device.
+bool device_sms(int *sms)
+{
+    static std::atomic<int> known[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
+        return false;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return false;
+        known[dev].store(n, std::memory_order_relaxed);
+    }
+    *sms = n;
+    return true;
+}
+
 bool misaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
 // Sizes of the 8-bit KV cache calls: K entries of NL x B caches.
@@ -172,7 +189,8 @@ bool attention_sizes_ok(int B, int T, int Hq, int Hkv, int D, int P, int L)
     if ((double)B * T * Hq > 1073741824.0)
         return false;
     // every byte offset of the prefix and the caches below 2^48
-    return ((double)B * L + P) * 4.0 * Hkv * D <= 281474976710656.0;
+    return ((double)B * L + P) * 4.0 * Hkv * D <= 281474976710656.0 &&
+           sv::attention_fits(B, T, Hkv, Hq / Hkv, D, P, L);
 }
 
 // Row-parallel verification (k_rows.cu): logit draft rows (or greedy), no
@@ -770,7 +788,7 @@ size_t spec_attention_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int 
 {
     if (!attention_sizes_ok(B, T, Hq, Hkv, D, P, L))
         return 0;
-    return 256;
+    return sv::attention_workspace(B, T, Hkv, Hq / Hkv, D, P, L);
 }
 
 spec_status_t spec_verify_attention(const void *q, const void *prefix, const uint8_t *prefix_scale, const void *cache,
@@ -811,7 +829,11 @@ spec_status_t spec_verify_attention(const void *q, const void *prefix, const uin
     A.L = L;
     A.c = (float)(1.4426950408889634 * (double)sm_scale);
     int launches = 0;
-    const cudaError_t e = sv::launch_attention(A, quant != 0, static_cast<cudaStream_t>(stream), &launches);
+    int sms = 0;
+    if (!device_sms(&sms))
+        return SPEC_ERR_CUDA;
+    const cudaError_t e = sv::launch_attention(A, quant != 0, workspace, sms, spin_limit(),
+                                               static_cast<cudaStream_t>(stream), &launches);
     g_launches.fetch_add((uint64_t)launches, std::memory_order_relaxed);
     return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }

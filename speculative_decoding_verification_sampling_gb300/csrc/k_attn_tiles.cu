@@ -1,0 +1,868 @@
+// k_attn_tiles.cu -- the verification attention over the shared prefix and the
+// sequences' caches, on the tensor cores.
+//
+// For a tile of up to 128 query rows (the tokens and heads that read one
+// key/value head) and 128 entries at a time:
+//   S = Q K^T           tcgen05.mma, operands in shared memory, S in TMEM
+//   P = 2^(c S - m)     one thread per row; P goes back to TMEM as bfloat16, over S
+//   O = O + P V         tcgen05.mma, P from TMEM, V from shared memory, O in TMEM
+// m is a reference exponent per row: it follows the row's maximum only once
+// that has passed it by more than 8, so O is rescaled a few times per stretch
+// and 2^(c S - m) stays below 2^8.  The sum l takes the unrounded weights.
+// Rounding P to bfloat16 is what the tensor cores ask for when V is bfloat16:
+// 2^-8 of each weight, in random directions, beside the output's own 2^-8.
+//
+// Two softmax groups of four warps keep the tensor cores busy during each
+// other's exponentials.  Where the rows fill more than one tile, both groups
+// work on the same entries (each K and V tile read once for 256 rows); where
+// they do not, the groups take alternate units of the same rows and leave a
+// partial result each.  A loader thread feeds a ring of K and V tiles with
+// TMA; one warp issues every tcgen05.mma.  Entries in 8 bits are copied as
+// they are, and four more warps turn them into the bfloat16 numbers they
+// stand for (exact) in the swizzled layout that TMA would have written.
+//
+// The last unit of a stretch is ragged: scores past its end become -inf, and
+// V's rows past it are zeroed in shared memory, since 0 * NaN would reach O.
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "sv_attn.cuh"
+#include "sv_cluster.cuh"
+#include "sv_fp8.cuh"
+#include "sv_launch.h"
+
+namespace sv {
+namespace {
+
+// ------------------------------------------------------------------ PTX
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *map, unsigned long long *bar, int x, int y,
+                                       int z, int w)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+                 "l"(map), "r"(saddr(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap *map, unsigned long long *bar, int x, int y,
+                                       int z, int w, int v)
+{
+    asm volatile("cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+                 "l"(map), "r"(saddr(bar)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v)
+                 : "memory");
+}
+
+// Shared-memory operand with 128-byte rows, 128-byte swizzle: start address,
+// leading and stride offsets in 16-byte units, descriptor version 1, swizzle
+// code 2.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride)
+{
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+// Instruction descriptor: bfloat16 operands, float32 accumulator, M = 128.
+__host__ __device__ constexpr uint32_t mma_desc(int n, bool b_mn_major)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+           ((128u >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(acc)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(acc)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_commit(unsigned long long *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+#define R4(f, i) f(i), f(i + 1), f(i + 2), f(i + 3)
+#define R16(f, i) R4(f, i), R4(f, i + 4), R4(f, i + 8), R4(f, i + 12)
+#define R32(f, i) R16(f, i), R16(f, i + 16)
+
+// 32 columns of this warp's 32 lanes; the wait is part of the instruction
+// block, so no use of x can be moved ahead of it.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float *x)
+{
+#define OUT(i) "=f"(x[i])
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : R32(OUT, 0)
+                 : "r"(addr)
+                 : "memory");
+#undef OUT
+}
+__device__ __forceinline__ void tmem_ld128(uint32_t addr, float *x)
+{
+#define OUT(i) "=f"(x[i])
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%128];\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+                 "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%129];\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
+                 "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95}, [%130];\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
+                 "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%131];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : R32(OUT, 0), R32(OUT, 32), R32(OUT, 64), R32(OUT, 96)
+                 : "r"(addr), "r"(addr + 32), "r"(addr + 64), "r"(addr + 96)
+                 : "memory");
+#undef OUT
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *x)
+{
+#define IN(i) "r"(x[i])
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::R32(IN, 0),
+                 "r"(addr)
+                 : "memory");
+#undef IN
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void store8(float *p, const float *x)
+{
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]),
+                 "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
+}
+
+// ------------------------------------------------------------------ layout
+template <int D, bool Q8>
+struct TileCfg {
+    static constexpr uint32_t TILE = 128 * D * 2;     // a bfloat16 tile: 128 rows of D, in blocks of 64 columns
+    static constexpr uint32_t BLOCK = 128 * 128;      // one such block: 128 rows of 128 bytes
+    static constexpr uint32_t RAW = 128 * D;          // a tile of codes
+    static constexpr int NS = Q8 ? (D == 128 ? 3 : 5) : (D == 128 ? 4 : 8);   // K / V tiles in flight
+    static constexpr int NR = Q8 ? (D == 128 ? 4 : 8) : 0;                    // tiles of codes in flight
+    static constexpr int THREADS = Q8 ? 512 : 384;
+    // registers per thread: at launch, then of the softmax groups and of the
+    // other warpgroups (their sum over the warpgroups stays within the launch's)
+    static constexpr int REGS = Q8 ? 128 : 168, REGS_SOFT = Q8 ? 176 : 208, REGS_REST = 80;
+    static_assert(2 * REGS_SOFT + (THREADS / 128 - 2) * REGS_REST <= THREADS / 128 * REGS, "register split");
+    static constexpr uint32_t SMEM = 2 * TILE + NS * TILE + NR * RAW + 1024;
+};
+
+constexpr int W_LOAD = 8, W_MMA = 9, W_CVT = 12;   // warps 0-7: softmax, two groups
+
+struct TileShared {
+    unsigned long long q_full[2], q_empty[2], kv_full[8], kv_empty[8], raw_full[8], raw_empty[8];
+    unsigned long long s_full[2], p_ready[2], o_full[2], drain;
+    uint32_t tmem;
+    volatile int abort;
+    int total, b0, base0;        // units of all sequences (one pair's worth); where the CTA's line starts
+    int sums[16];                // per warp
+};
+
+struct TileParams {
+    AttnParams A;
+    AttnWork W;
+    uint32_t spin_limit;
+};
+
+__device__ __forceinline__ int seq_units(const AttnParams &A, int b)
+{
+    const int n = __ldg(A.len + b);
+    return n < 0 || n > A.L ? 0 : (n + AT_UNIT - 1) / AT_UNIT;
+}
+
+// One stretch of one pair, as a CTA works on it.
+struct Item {
+    int n;           // units
+    int h, b;        // key/value head; sequence (-1: the prefix)
+    int row0;        // first (sequence, token) row of the item's tiles
+    int tokens;      // rows of that kind in the pair from row0 on
+    int e0, left;    // first entry, entries from there to the end of the stretch
+    int two;
+    int slot;
+};
+
+// The items of one CTA, in order.  Every role walks them by itself.
+struct Walk {
+    const TileParams &P;
+    int cur, end, b, base, ub, HS, UP;
+    __device__ Walk(const TileParams &p, const TileShared &sh) : P(p)
+    {
+        HS = P.A.H * P.W.own.tiles;
+        UP = P.W.ppairs * P.W.pu;
+        const long long U = UP + (long long)HS * sh.total;
+        cur = attn_start(blockIdx.x, U, gridDim.x);
+        end = attn_start(blockIdx.x + 1, U, gridDim.x);
+        b = sh.b0;
+        base = sh.base0;
+        ub = b < P.A.B ? seq_units(P.A, b) : 0;
+    }
+    __device__ bool next(Item &it)
+    {
+        if (cur >= end)
+            return false;
+        int off, units;
+        if (cur < UP) {
+            const int p = cur / P.W.pu, tile = p % P.W.pre.tiles;
+            off = cur - p * P.W.pu;
+            units = P.W.pu;
+            it.h = p / P.W.pre.tiles;
+            it.b = -1;
+            it.two = P.W.pre.two;
+            it.row0 = tile * P.W.pre.tq * (it.two ? 2 : 1);
+            it.tokens = P.A.B * P.A.T - it.row0;
+            it.left = P.A.P - off * AT_UNIT;
+            it.slot = blockIdx.x + p;
+        } else {
+            while (cur >= base + ub * HS) {
+                base += ub * HS;
+                ub = seq_units(P.A, ++b);
+            }
+            const int i = (cur - base) / ub, tile = i % P.W.own.tiles;
+            off = cur - base - i * ub;
+            units = ub;
+            it.h = i / P.W.own.tiles;
+            it.b = b;
+            it.two = P.W.own.two;
+            const int t0 = tile * P.W.own.tq * (it.two ? 2 : 1);
+            it.row0 = b * P.A.T + t0;
+            it.tokens = P.A.T - t0;
+            it.left = __ldg(P.A.len + b) - off * AT_UNIT;
+            it.slot = blockIdx.x + b * HS + i;
+        }
+        it.e0 = off * AT_UNIT;
+        it.n = min(units - off, end - cur);
+        cur += it.n;
+        return true;
+    }
+};
+
+// A place in a ring of n slots and the parity of its current pass.
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ void next(int n)
+    {
+        if (++slot == n) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// Bounded wait on a barrier of this CTA: false once the polls ran out or
+// another role has given up.
+__device__ __forceinline__ bool tile_wait(unsigned long long *bar, uint32_t parity, uint32_t limit, TileShared &sh)
+{
+    for (uint32_t it = 0;; ++it) {
+        if (mbar_test_hint(bar, parity))
+            return true;
+        if (it >= limit || sh.abort) {
+            sh.abort = 1;
+            return false;
+        }
+    }
+}
+
+// The same for a whole warp: every lane waits, and all come to one answer.
+__device__ __forceinline__ bool tile_wait_warp(unsigned long long *bar, uint32_t parity, uint32_t limit, TileShared &sh)
+{
+    return __all_sync(0xffffffffu, tile_wait(bar, parity, limit, sh));
+}
+
+// ------------------------------------------------------------------ roles
+// The loader: one thread.  Q tiles as an item begins, then K and V tiles in
+// the order in which the tensor cores use them.
+template <int D, bool Q8>
+__device__ void load_role(const TileParams &P, const CUtensorMap *mq_pre, const CUtensorMap *mq_own,
+                          const CUtensorMap *m_pre, const CUtensorMap *m_own, TileShared &sh, uint32_t sq, uint32_t skv,
+                          uint32_t sraw, uint32_t limit)
+{
+    using C = TileCfg<D, Q8>;
+    constexpr int N = Q8 ? C::NR : C::NS;
+    unsigned long long *const full = Q8 ? sh.raw_full : sh.kv_full, *const empty = Q8 ? sh.raw_empty : sh.kv_empty;
+    Ring q, r;
+    int nq = 0, nr = 0;   // copies issued
+    Walk walk(P, sh);
+    Item it;
+    bool ok = true;
+    while (ok && walk.next(it)) {
+        const CUtensorMap *mq = it.b < 0 ? mq_pre : mq_own;
+        const int tq = it.b < 0 ? P.W.pre.tq : P.W.own.tq;
+        for (int g = 0; ok && g <= it.two; ++g) {
+            ok = tile_wait(&sh.q_empty[q.slot], q.phase ^ 1, limit, sh);
+            if (!ok)
+                break;
+            mbar_arrive_tx(&sh.q_full[q.slot], (uint32_t)tq * P.A.G * D * 2);
+            for (int k = 0; k < D / 64; ++k)
+                tma_4d(sq + q.slot * C::TILE + k * C::BLOCK, mq, &sh.q_full[q.slot], k * 64, 0, it.h,
+                       it.row0 + g * tq);
+            q.next(2);
+            ++nq;
+        }
+        auto load = [&](int j, int kv) {
+            if (!ok || !(ok = tile_wait(&empty[r.slot], r.phase ^ 1, limit, sh)))
+                return;
+            const int e = it.e0 + j * AT_UNIT;
+            if constexpr (Q8) {
+                mbar_arrive_tx(&full[r.slot], C::RAW);
+                const uint32_t dst = sraw + r.slot * C::RAW;
+                if (it.b < 0)
+                    tma_4d(dst, m_pre, &full[r.slot], 0, it.h, kv, e);
+                else
+                    tma_5d(dst, m_own, &full[r.slot], 0, it.h, kv, e, it.b);
+            } else {
+                mbar_arrive_tx(&full[r.slot], C::TILE);
+                for (int k = 0; k < D / 64; ++k) {
+                    const uint32_t dst = skv + r.slot * C::TILE + k * C::BLOCK;
+                    if (it.b < 0)
+                        tma_4d(dst, m_pre, &full[r.slot], k * 64, it.h, kv, e);
+                    else
+                        tma_5d(dst, m_own, &full[r.slot], k * 64, it.h, kv, e, it.b);
+                }
+            }
+            r.next(N);
+            ++nr;
+        };
+        const int ahead = it.two ? 1 : 2;
+        for (int j = 0; j < min(ahead, it.n); ++j)
+            load(j, 0);
+        for (int j = 0; j < it.n; ++j) {
+            load(j, 1);
+            if (j + ahead < it.n)
+                load(j + ahead, 0);
+        }
+    }
+    if (!ok) {
+        // copies in flight land before the CTA ends
+        for (int k = 0; k < 2 && k < nq; ++k)
+            (void)ring_wait(&sh.q_full[(nq - 1 - k) % 2], ((nq - 1 - k) / 2) & 1, limit);
+        for (int k = 0; k < N && k < nr; ++k)
+            (void)ring_wait(&full[(nr - 1 - k) % N], ((nr - 1 - k) / N) & 1, limit);
+    }
+}
+
+// The issuer of every tcgen05.mma: one warp, lane 0 issues.
+template <int D, bool Q8>
+__device__ void mma_role(const TileParams &P, TileShared &sh, uint32_t sq, uint8_t *kv_ptr, uint32_t skv, uint32_t limit)
+{
+    using C = TileCfg<D, Q8>;
+    constexpr uint32_t IS = mma_desc(128, false), IO = mma_desc(D, true);
+    const int lane = threadIdx.x & 31;
+    const uint32_t tmem = sh.tmem;
+    Ring q, r;
+    uint32_t pphase[2] = {0, 0};
+    bool ok = true;
+    auto scores = [&](int g, int qs, int ks, bool last) {
+        if (lane == 0) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t at = (k / 4) * C::BLOCK + (k % 4) * 32;
+                mma_ss(tmem + g * 128, smem_desc(sq + qs * C::TILE + at, 16, 1024),
+                       smem_desc(skv + ks * C::TILE + at, 16, 1024), IS, k > 0);
+            }
+            mma_commit(&sh.s_full[g]);
+            if (last)
+                mma_commit(&sh.q_empty[qs]);
+        }
+        __syncwarp();
+    };
+    auto values = [&](int g, int vs, bool first, bool last) {
+        // P of this group is in TMEM
+        if (!(ok = tile_wait_warp(&sh.p_ready[g], pphase[g], limit, sh)))
+            return;
+        pphase[g] ^= 1;
+        tc_after();
+        if (lane == 0) {
+#pragma unroll
+            for (int k = 0; k < AT_UNIT / 16; ++k)
+                mma_ts(tmem + 256 + g * D, tmem + g * 128 + k * 8,
+                       smem_desc(skv + vs * C::TILE + k * 2048, C::BLOCK, 1024), IO, !first || k > 0);
+            if (last)
+                mma_commit(&sh.o_full[g]);
+        }
+        __syncwarp();
+    };
+    auto take = [&](int &slot) {
+        slot = r.slot;
+        ok = tile_wait_warp(&sh.kv_full[r.slot], r.phase, limit, sh);
+        r.next(C::NS);
+        tc_after();
+        return ok;
+    };
+    auto give = [&](unsigned long long *bar) {
+        if (lane == 0)
+            mma_commit(bar);
+        __syncwarp();
+    };
+    auto clear_tail = [&](int slot, int nv) {
+        // V's rows past the stretch (the conversion from 8 bits leaves zeros there by itself)
+        if constexpr (!Q8) {
+            if (nv >= AT_UNIT)
+                return;
+            for (int k = 0; k < D / 64; ++k)
+                for (int i = nv * 8 + lane; i < AT_UNIT * 8; i += 32)
+                    *reinterpret_cast<uint4 *>(kv_ptr + slot * C::TILE + k * C::BLOCK + i * 16) =
+                        make_uint4(0, 0, 0, 0);
+            async_fence();
+            __syncwarp();
+        }
+    };
+    Walk walk(P, sh);
+    Item it;
+    while (ok && walk.next(it)) {
+        int qs[2], ks, vs;
+        for (int g = 0; ok && g <= it.two; ++g) {
+            qs[g] = q.slot;
+            ok = tile_wait_warp(&sh.q_full[q.slot], q.phase, limit, sh);
+            q.next(2);
+        }
+        if (!ok)
+            break;
+        if (it.two) {
+            if (!take(ks))
+                break;
+            scores(0, qs[0], ks, it.n == 1);
+            scores(1, qs[1], ks, it.n == 1);
+            give(&sh.kv_empty[ks]);
+            for (int j = 0; ok && j < it.n; ++j) {
+                const bool last = j + 1 == it.n;
+                if (!take(vs))
+                    break;
+                clear_tail(vs, it.left - j * AT_UNIT);
+                values(0, vs, j == 0, last);
+                if (!ok || (!last && !take(ks)))
+                    break;
+                if (!last)
+                    scores(0, qs[0], ks, j + 2 == it.n);
+                values(1, vs, j == 0, last);
+                if (!ok)
+                    break;
+                give(&sh.kv_empty[vs]);
+                if (!last) {
+                    scores(1, qs[1], ks, j + 2 == it.n);
+                    give(&sh.kv_empty[ks]);
+                }
+            }
+        } else {
+            for (int j = 0; ok && j < min(2, it.n); ++j) {
+                if (!take(ks))
+                    break;
+                scores(j, qs[0], ks, j + 1 == it.n);
+                give(&sh.kv_empty[ks]);
+            }
+            for (int j = 0; ok && j < it.n; ++j) {
+                if (!take(vs))
+                    break;
+                clear_tail(vs, it.left - j * AT_UNIT);
+                values(j & 1, vs, j < 2, j + 2 >= it.n);
+                if (!ok)
+                    break;
+                give(&sh.kv_empty[vs]);
+                if (j + 2 < it.n) {
+                    if (!take(ks))
+                        break;
+                    scores(j & 1, qs[0], ks, j + 3 == it.n);
+                    give(&sh.kv_empty[ks]);
+                }
+            }
+        }
+    }
+    if (!ok) {
+        give(&sh.drain);
+        (void)ring_wait(&sh.drain, 0, limit);
+    }
+}
+
+// Softmax of group g: thread w * 32 + lane owns row w * 32 + lane of the
+// group's tile (a warp reaches only its own quarter of the TMEM lanes).
+template <int D>
+__device__ void softmax_role(const TileParams &P, TileShared &sh, int g, uint32_t limit)
+{
+    const int lane = threadIdx.x & 31, w = (threadIdx.x / 32) & 3, row = w * 32 + lane;
+    const uint32_t lanes = (uint32_t)(w * 32) << 16;
+    const uint32_t ts = sh.tmem + lanes + g * 128, to = sh.tmem + lanes + 256 + g * D;
+    const float c = P.A.c;
+    uint32_t sphase = 0, ophase = 0;
+    Walk walk(P, sh);
+    Item it;
+    while (walk.next(it)) {
+        const int tq = it.b < 0 ? P.W.pre.tq : P.W.own.tq, rows = tq * P.A.G;
+        // rows of this group's tile that exist
+        const int have = min(max(it.tokens - (it.two ? g * tq : 0), 0), tq) * P.A.G;
+        const bool active = w * 32 < have;
+        const int cnt = it.two ? it.n : (it.n - g + 1) / 2;
+        float m = -F_INF, l = 0.0f;
+        for (int i = 0; i < cnt; ++i) {
+            const int nv = it.left - (it.two ? i : 2 * i + g) * AT_UNIT;
+            if (!tile_wait_warp(&sh.s_full[g], sphase, limit, sh))
+                return;
+            sphase ^= 1;
+            tc_after();
+            if (active) {
+                float x[128];
+                tmem_ld128(ts, x);
+                if (nv < AT_UNIT) {
+#pragma unroll
+                    for (int k = 0; k < 128; ++k)
+                        x[k] = k < nv ? x[k] : -F_INF;
+                }
+                float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                for (int k = 4; k < 128; k += 4)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        top[u] = fmaxf(top[u], x[k + u]);
+                const float s = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+                const bool up = s > m + 8.0f;
+                if (__any_sync(0xffffffffu, up)) {
+                    const float f = up ? ex2a(m - s) : 1.0f;   // 2^(-inf) = 0 the first time
+                    if (up) {
+                        m = s;
+                        l *= f;
+                    }
+                    if (i > 0) {
+                        // this group's last P V has completed: S after it has
+#pragma unroll 1
+                        for (int k = 0; k < D; k += 32) {
+                            float o[32];
+                            tmem_ld32(to + k, o);
+#pragma unroll
+                            for (int u = 0; u < 32; ++u)
+                                o[u] *= f;
+                            tmem_st32(to + k, reinterpret_cast<uint32_t *>(o));
+                        }
+                    }
+                }
+                const float ref = m == -F_INF ? 0.0f : m;
+                const f2 cc = pk(c, c), nref = pk(-ref, -ref);
+                f2 sum[2] = {pk(0.0f, 0.0f), pk(0.0f, 0.0f)};
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const f2 e = ex2x2(fma2(pk(x[hf * 64 + 2 * k], x[hf * 64 + 2 * k + 1]), cc, nref));
+                        sum[k & 1] = add2(sum[k & 1], e);
+                        float lo, hi;
+                        upk(e, lo, hi);
+                        p[k] = pack_bf16(lo, hi);
+                    }
+                    tmem_st32(ts + hf * 32, p);
+                }
+                float lo, hi;
+                upk(add2(sum[0], sum[1]), lo, hi);
+                l += lo + hi;
+                tmem_st_wait();
+            }
+            tc_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.p_ready[g]);
+        }
+        const size_t at = ((size_t)it.slot * 2 + g) * rows + row;
+        const bool pre = it.b < 0;
+        if (row < have)
+            (pre ? P.W.ml_p : P.W.ml_s)[at] = make_float2(m, l);
+        if (cnt > 0) {
+            if (!tile_wait_warp(&sh.o_full[g], ophase, limit, sh))
+                return;
+            ophase ^= 1;
+            tc_after();
+            if (active) {
+                float *dst = (pre ? P.W.o_p : P.W.o_s) + at * D;
+#pragma unroll 1
+                for (int k = 0; k < D; k += 32) {
+                    float o[32];
+                    tmem_ld32(to + k, o);
+                    if (row < have) {
+#pragma unroll
+                        for (int u = 0; u < 32; u += 8)
+                            store8(dst + k + u, o + u);
+                    }
+                }
+            }
+            tc_before();
+        }
+    }
+}
+
+// Codes to bfloat16: warp w converts rows 32 w .. 32 w + 31 of each tile.
+template <int D>
+__device__ void convert_role(const TileParams &P, TileShared &sh, const uint8_t *raw, uint8_t *kv, uint32_t limit)
+{
+    using C = TileCfg<D, true>;
+    constexpr int CH = D / 16;          // 16-code chunks of a row
+    constexpr int RP = 32 / CH;         // rows per pass of a warp
+    const int lane = threadIdx.x & 31, w = (threadIdx.x / 32) & 3;
+    const int ch = lane % CH, sub = lane / CH;
+    Ring r, s;
+    Walk walk(P, sh);
+    Item it;
+    while (walk.next(it)) {
+        bool ok = true;
+        auto convert = [&](int j, int kind) {
+            if (!ok)
+                return;
+            const int e = it.e0 + j * AT_UNIT + w * 32 + lane, nv = it.left - j * AT_UNIT;
+            const uint8_t *sc = it.b < 0 ? P.A.pscale : P.A.cscale + (size_t)it.b * P.A.L * 2 * P.A.H;
+            uint32_t byte = 127;
+            if (w * 32 + lane < nv)
+                byte = __ldg(sc + ((size_t)e * 2 + kind) * P.A.H + it.h);
+            const float f = fp8_factor(byte);
+            ok = tile_wait_warp(&sh.raw_full[r.slot], r.phase, limit, sh) &&
+                 tile_wait_warp(&sh.kv_empty[s.slot], s.phase ^ 1, limit, sh);
+            if (!ok)
+                return;
+            const uint8_t *src = raw + r.slot * C::RAW;
+            uint8_t *dst = kv + s.slot * C::TILE + (ch / 4) * C::BLOCK;
+#pragma unroll 4
+            for (int p = 0; p < 32 / RP; ++p) {
+                const int rr = p * RP + sub, row = w * 32 + rr;
+                const float fr = __shfl_sync(0xffffffffu, f, rr);
+                uint4 v = *reinterpret_cast<const uint4 *>(src + row * D + ch * 16);
+                if (row >= nv)
+                    v = make_uint4(0, 0, 0, 0);
+                float x[16];
+                unpack_e4m3(v.x, x);
+                unpack_e4m3(v.y, x + 4);
+                unpack_e4m3(v.z, x + 8);
+                unpack_e4m3(v.w, x + 12);
+                uint32_t y[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    y[k] = pack_bf16(x[2 * k] * fr, x[2 * k + 1] * fr);
+                // two 16-byte chunks of a 128-byte row, at their swizzled places; lanes of the
+                // second block of columns store them in the other order (no bank conflicts)
+                const int c0 = (ch % 4) * 2, flip = ch / 4;
+                const uint4 a = make_uint4(y[0], y[1], y[2], y[3]), b = make_uint4(y[4], y[5], y[6], y[7]);
+                *reinterpret_cast<uint4 *>(dst + row * 128 + (((c0 + flip) ^ (row & 7)) << 4)) = flip ? b : a;
+                *reinterpret_cast<uint4 *>(dst + row * 128 + (((c0 + 1 - flip) ^ (row & 7)) << 4)) = flip ? a : b;
+            }
+            async_fence();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sh.kv_full[s.slot]);
+                mbar_arrive(&sh.raw_empty[r.slot]);
+            }
+            r.next(C::NR);
+            s.next(C::NS);
+        };
+        const int ahead = it.two ? 1 : 2;
+        for (int j = 0; j < min(ahead, it.n); ++j)
+            convert(j, 0);
+        for (int j = 0; j < it.n; ++j) {
+            convert(j, 1);
+            if (j + ahead < it.n)
+                convert(j + ahead, 0);
+        }
+        if (!ok)
+            return;
+    }
+}
+
+template <int D, bool Q8>
+__global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
+    va_tiles(const __grid_constant__ CUtensorMap mq_pre, const __grid_constant__ CUtensorMap mq_own,
+             const __grid_constant__ CUtensorMap m_pre, const __grid_constant__ CUtensorMap m_own,
+             const __grid_constant__ TileParams P)
+{
+    using C = TileCfg<D, Q8>;
+    extern __shared__ uint8_t dyn[];
+    __shared__ TileShared sh;
+    pdl_trigger();
+    const int tid = threadIdx.x, warp = tid / 32;
+    uint8_t *tiles = dyn + ((1024 - (saddr(dyn) & 1023)) & 1023);
+    uint8_t *kv = tiles + 2 * C::TILE, *raw = kv + C::NS * C::TILE;
+    const uint32_t sq = saddr(tiles), skv = saddr(kv), sraw = saddr(raw);
+    const uint32_t limit = hinted_limit(P.spin_limit > OWN_WAIT_MIN ? P.spin_limit : OWN_WAIT_MIN);
+
+    // ---- where this CTA's line starts: sums over runs of sequences, then the run
+    const int B = P.A.B, run = (B + C::THREADS - 1) / C::THREADS;
+    int sum = 0;
+    for (int b = tid * run; b < min(B, (tid + 1) * run); ++b)
+        sum += seq_units(P.A, b);
+    int upto = sum;   // inclusive scan in the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        upto += tid % 32 >= o ? y : 0;
+    }
+    if (tid % 32 == 31)
+        sh.sums[warp] = upto;
+    if (tid == 0) {
+        sh.abort = 0;
+        sh.b0 = 0;
+        sh.base0 = P.W.ppairs * P.W.pu;
+        for (int k = 0; k < 2; ++k) {
+            mbar_init(&sh.q_full[k], 1);
+            mbar_init(&sh.q_empty[k], 1);
+            mbar_init(&sh.s_full[k], 1);
+            mbar_init(&sh.p_ready[k], 4);
+            mbar_init(&sh.o_full[k], 1);
+        }
+        for (int k = 0; k < C::NS; ++k) {
+            mbar_init(&sh.kv_full[k], Q8 ? 4 : 1);
+            mbar_init(&sh.kv_empty[k], 1);
+        }
+        for (int k = 0; k < C::NR; ++k) {
+            mbar_init(&sh.raw_full[k], 1);
+            mbar_init(&sh.raw_empty[k], 4);
+        }
+        mbar_init(&sh.drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;\n\tfence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == W_MMA) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(saddr(&sh.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    {
+        int before = 0, total = 0;
+        for (int k = 0; k < C::THREADS / 32; ++k) {
+            before += k < warp ? sh.sums[k] : 0;
+            total += sh.sums[k];
+        }
+        if (tid == 0)
+            sh.total = total;
+        const int HS = P.A.H * P.W.own.tiles, UP = P.W.ppairs * P.W.pu;
+        const long long U = UP + (long long)HS * total;
+        const int start = attn_start(blockIdx.x, U, gridDim.x);
+        int at = before + upto - sum;   // units of the sequences before this thread's run
+        for (int b = tid * run; b < min(B, (tid + 1) * run); ++b) {
+            const int u = seq_units(P.A, b);
+            if (blockIdx.x == 0)
+                P.W.base[b] = at;
+            const int lo = UP + at * HS;
+            if (start >= lo && start < lo + u * HS) {
+                sh.b0 = b;
+                sh.base0 = lo;
+            }
+            at += u;
+        }
+        if (blockIdx.x == 0 && tid == 0)
+            P.W.base[B] = total;
+    }
+    __syncthreads();
+
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFT));
+        softmax_role<D>(P, sh, warp / 4, limit);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_REST));
+        if (warp == W_LOAD) {
+            if (tid % 32 == 0)
+                load_role<D, Q8>(P, &mq_pre, &mq_own, &m_pre, &m_own, sh, sq, skv, sraw, limit);
+        } else if (warp == W_MMA) {
+            mma_role<D, Q8>(P, sh, sq, kv, skv, limit);
+        } else if (Q8 && warp >= W_CVT) {
+            convert_role<D>(P, sh, raw, kv, limit);
+        }
+    }
+    __syncwarp();
+    tc_before();
+    __syncthreads();
+    tc_after();
+    if (warp == W_MMA)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sh.tmem) : "memory");
+    if (tid == 0)
+        P.W.stat[blockIdx.x] = sh.abort ? (int)ST_TIMEOUT : 0;
+}
+
+// ------------------------------------------------------------------ host
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled()
+{
+    static const EncodeTiled fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) !=
+                cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            return (EncodeTiled) nullptr;
+        return (EncodeTiled)f;
+    }();
+    return fn;
+}
+
+// A map over a row-major array of `rank` dimensions (innermost first); boxes
+// of bfloat16 are 64 wide with 128-byte swizzle, boxes of codes a whole head.
+bool make_map(CUtensorMap *map, bool codes, const void *base, int rank, const cuuint64_t *dim, const cuuint32_t *box)
+{
+    cuuint64_t stride[4];
+    cuuint64_t bytes = codes ? 1 : 2;
+    for (int k = 0; k + 1 < rank; ++k) {
+        bytes *= dim[k];
+        stride[k] = bytes;
+    }
+    const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+    return encode_tiled()(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+                          const_cast<void *>(base), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool Q8>
+cudaError_t launch_tiles(const TileParams &P, int grid, cudaStream_t stream)
+{
+    using C = TileCfg<D, Q8>;
+    if (!encode_tiled())
+        return cudaErrorNotSupported;
+    const AttnParams &A = P.A;
+    CUtensorMap mq_pre, mq_own, m_pre, m_own;
+    const cuuint64_t u = 1;
+    // q as [token row][Hkv][G][D]
+    const cuuint64_t dq[4] = {D, (cuuint64_t)A.G, (cuuint64_t)A.H, (cuuint64_t)A.B * A.T};
+    const cuuint32_t bp[4] = {64, (cuuint32_t)A.G, 1, (cuuint32_t)P.W.pre.tq};
+    const cuuint32_t bo[4] = {64, (cuuint32_t)A.G, 1, (cuuint32_t)P.W.own.tq};
+    const cuuint32_t wide = Q8 ? D : 64;
+    const cuuint64_t dp[4] = {D, (cuuint64_t)A.H, 2, A.P > 0 ? (cuuint64_t)A.P : u};
+    const cuuint64_t dc[5] = {D, (cuuint64_t)A.H, 2, A.L > 0 ? (cuuint64_t)A.L : u, (cuuint64_t)A.B};
+    const cuuint32_t box[5] = {wide, 1, 1, AT_UNIT, 1};
+    // an absent prefix or cache has no units: its map is never used
+    if (!make_map(&mq_pre, false, A.q, 4, dq, bp) || !make_map(&mq_own, false, A.q, 4, dq, bo) ||
+        !make_map(&m_pre, Q8, A.P > 0 ? A.prefix : A.cache, 4, dp, box) ||
+        !make_map(&m_own, Q8, A.L > 0 ? A.cache : A.prefix, 5, dc, box))
+        return cudaErrorInvalidValue;
+    const cudaError_t e =
+        cudaFuncSetAttribute(va_tiles<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    if (e != cudaSuccess)
+        return e;
+    va_tiles<D, Q8><<<grid, C::THREADS, C::SMEM, stream>>>(mq_pre, mq_own, m_pre, m_own, P);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tiles(const AttnParams &A, const AttnWork &W, bool quant, int grid, uint32_t spin_limit,
+                              cudaStream_t stream)
+{
+    TileParams P{A, W, spin_limit};
+    if (A.D == 128)
+        return quant ? launch_tiles<128, true>(P, grid, stream) : launch_tiles<128, false>(P, grid, stream);
+    return quant ? launch_tiles<64, true>(P, grid, stream) : launch_tiles<64, false>(P, grid, stream);
+}
+
+}  // namespace sv
