@@ -13,6 +13,7 @@ target distribution, p the draft distribution, d_i the K drafted tokens.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -152,7 +153,7 @@ class Aux:
 def _check(t, shape, dtypes, name):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
@@ -194,7 +195,8 @@ def _outs(B, K, device, out_tokens, out_accept_len):
 
 def _stream(device, stream):
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        index = device.index
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -447,14 +449,30 @@ def spec_attention_workspace_bytes(B: int, T: int, Hq: int, Hkv: int, D: int, P:
     return int(load().spec_attention_workspace_bytes(int(B), int(T), int(Hq), int(Hkv), int(D), int(P), int(L)))
 
 
-def _scratch(nbytes, device, st):
-    """Scratch of one call, from the allocator's pool of the stream that the
-    call runs on: freed when the call returns, it is handed out again only to
-    later work of that stream."""
-    if st == torch.cuda.current_stream(device).cuda_stream:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(st, device=device)):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+_attention_bytes = functools.lru_cache(maxsize=256)(spec_attention_workspace_bytes)
+
+
+_scratch_cache: dict = {}
+
+
+def _scratch(nbytes, device, st, own_stream):
+    """Scratch that needs no zero-fill, kept per (device, stream) and handed to
+    one call after another of that stream.  It comes from the allocator's pool
+    of the stream that uses it, so a smaller one that is dropped is handed out
+    again only to later work of that stream.  A call under capture gets scratch
+    of its own from the graph's pool: the graph keeps the address."""
+    def make(n):
+        if not own_stream:
+            with torch.cuda.stream(torch.cuda.ExternalStream(st, device=device)):
+                return torch.empty(n, dtype=torch.uint8, device=device)
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    if torch.cuda.is_current_stream_capturing():
+        return make(nbytes)
+    key = (device.index, st)
+    buf = _scratch_cache.get(key)
+    if buf is None or buf.numel() < nbytes:
+        buf = _scratch_cache[key] = make(max(nbytes, 1 << 20))
+    return buf
 
 
 def spec_verify_attention(q: torch.Tensor, cache: torch.Tensor, seq_len: torch.Tensor, *,
@@ -511,10 +529,10 @@ def spec_verify_attention(q: torch.Tensor, cache: torch.Tensor, seq_len: torch.T
     st = _stream(dev, stream)
     lib = load()
     if workspace is None:
-        nbytes = lib.spec_attention_workspace_bytes(B, T, Hq, H, D, P, L)
+        nbytes = _attention_bytes(B, T, Hq, H, D, P, L)
         if nbytes == 0:
             raise SpecVerifyError(1, "spec_verify_attention")
-        workspace = _scratch(nbytes, dev, st)
+        workspace = _scratch(nbytes, dev, st, stream is None)
     elif not isinstance(workspace, torch.Tensor) or not workspace.is_cuda:
         raise TypeError("workspace must be a CUDA tensor")
 

@@ -23,6 +23,7 @@
 //
 // The last unit of a stretch is ragged: scores past its end become -inf, and
 // V's rows past it are zeroed in shared memory, since 0 * NaN would reach O.
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -253,6 +254,22 @@ struct Walk {
     }
 };
 
+// The K and V tiles of an item, in the order in which the tensor cores use
+// them: the first K tile (with one set of rows the first two, one for each
+// softmax group), then V 0, the next K, V 1, the next K, ...
+struct TileRef {
+    int unit, kind;   // kind 0: K, 1: V
+};
+__device__ __forceinline__ TileRef item_tile(const Item &it, int s)
+{
+    const int ahead = min(it.two ? 1 : 2, it.n), r = s - ahead, more = it.n - ahead;
+    if (r < 0)
+        return {s, 0};
+    if (r < 2 * more)
+        return (r & 1) ? TileRef{ahead + r / 2, 0} : TileRef{r / 2, 1};
+    return {r - more, 1};
+}
+
 // A place in a ring of n slots and the parity of its current pass.
 struct Ring {
     int slot = 0;
@@ -316,9 +333,10 @@ __device__ void load_role(const TileParams &P, const CUtensorMap *mq_pre, const 
             q.next(2);
             ++nq;
         }
-        auto load = [&](int j, int kv) {
+        for (int s = 0; s < 2 * it.n; ++s) {
+            const auto [j, kv] = item_tile(it, s);
             if (!ok || !(ok = tile_wait(&empty[r.slot], r.phase ^ 1, limit, sh)))
-                return;
+                break;
             const int e = it.e0 + j * AT_UNIT;
             if constexpr (Q8) {
                 mbar_arrive_tx(&full[r.slot], C::RAW);
@@ -339,14 +357,6 @@ __device__ void load_role(const TileParams &P, const CUtensorMap *mq_pre, const 
             }
             r.next(N);
             ++nr;
-        };
-        const int ahead = it.two ? 1 : 2;
-        for (int j = 0; j < min(ahead, it.n); ++j)
-            load(j, 0);
-        for (int j = 0; j < it.n; ++j) {
-            load(j, 1);
-            if (j + ahead < it.n)
-                load(j + ahead, 0);
         }
     }
     if (!ok) {
@@ -603,7 +613,9 @@ __device__ void softmax_role(const TileParams &P, TileShared &sh, int g, uint32_
     }
 }
 
-// Codes to bfloat16: warp w converts rows 32 w .. 32 w + 31 of each tile.
+// Codes to bfloat16: warp w converts rows 32 w .. 32 w + 31 of each tile.  The
+// scale bytes of a tile (one per row, a lane each) are fetched while the tile
+// before it is converted.
 template <int D>
 __device__ void convert_role(const TileParams &P, TileShared &sh, const uint8_t *raw, uint8_t *kv, uint32_t limit)
 {
@@ -611,69 +623,73 @@ __device__ void convert_role(const TileParams &P, TileShared &sh, const uint8_t 
     constexpr int CH = D / 16;          // 16-code chunks of a row
     constexpr int RP = 32 / CH;         // rows per pass of a warp
     const int lane = threadIdx.x & 31, w = (threadIdx.x / 32) & 3;
-    const int ch = lane % CH, sub = lane / CH;
-    Ring r, s;
+    const int ch = lane % CH, sub = lane / CH, flip = ch / 4;
+    Ring r, q;
     Walk walk(P, sh);
     Item it;
-    while (walk.next(it)) {
-        bool ok = true;
-        auto convert = [&](int j, int kind) {
-            if (!ok)
-                return;
-            const int e = it.e0 + j * AT_UNIT + w * 32 + lane, nv = it.left - j * AT_UNIT;
-            const uint8_t *sc = it.b < 0 ? P.A.pscale : P.A.cscale + (size_t)it.b * P.A.L * 2 * P.A.H;
-            uint32_t byte = 127;
-            if (w * 32 + lane < nv)
-                byte = __ldg(sc + ((size_t)e * 2 + kind) * P.A.H + it.h);
-            const float f = fp8_factor(byte);
-            ok = tile_wait_warp(&sh.raw_full[r.slot], r.phase, limit, sh) &&
-                 tile_wait_warp(&sh.kv_empty[s.slot], s.phase ^ 1, limit, sh);
-            if (!ok)
-                return;
-            const uint8_t *src = raw + r.slot * C::RAW;
-            uint8_t *dst = kv + s.slot * C::TILE + (ch / 4) * C::BLOCK;
-#pragma unroll 4
-            for (int p = 0; p < 32 / RP; ++p) {
-                const int rr = p * RP + sub, row = w * 32 + rr;
-                const float fr = __shfl_sync(0xffffffffu, f, rr);
-                uint4 v = *reinterpret_cast<const uint4 *>(src + row * D + ch * 16);
-                if (row >= nv)
-                    v = make_uint4(0, 0, 0, 0);
-                float x[16];
-                unpack_e4m3(v.x, x);
-                unpack_e4m3(v.y, x + 4);
-                unpack_e4m3(v.z, x + 8);
-                unpack_e4m3(v.w, x + 12);
-                uint32_t y[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    y[k] = pack_bf16(x[2 * k] * fr, x[2 * k + 1] * fr);
-                // two 16-byte chunks of a 128-byte row, at their swizzled places; lanes of the
-                // second block of columns store them in the other order (no bank conflicts)
-                const int c0 = (ch % 4) * 2, flip = ch / 4;
-                const uint4 a = make_uint4(y[0], y[1], y[2], y[3]), b = make_uint4(y[4], y[5], y[6], y[7]);
-                *reinterpret_cast<uint4 *>(dst + row * 128 + (((c0 + flip) ^ (row & 7)) << 4)) = flip ? b : a;
-                *reinterpret_cast<uint4 *>(dst + row * 128 + (((c0 + 1 - flip) ^ (row & 7)) << 4)) = flip ? a : b;
-            }
-            async_fence();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&sh.kv_full[s.slot]);
-                mbar_arrive(&sh.raw_empty[r.slot]);
-            }
-            r.next(C::NR);
-            s.next(C::NS);
-        };
-        const int ahead = it.two ? 1 : 2;
-        for (int j = 0; j < min(ahead, it.n); ++j)
-            convert(j, 0);
-        for (int j = 0; j < it.n; ++j) {
-            convert(j, 1);
-            if (j + ahead < it.n)
-                convert(j + ahead, 0);
-        }
-        if (!ok)
+    int s = 0;
+    bool more = walk.next(it);
+    // the next tile's scale byte of this lane's row, and its valid rows
+    uint32_t byte = 127;
+    int nv = 0;
+    auto fetch = [&] {
+        if (!more)
             return;
+        const auto [j, kind] = item_tile(it, s);
+        nv = it.left - j * AT_UNIT;
+        byte = 127;
+        if (w * 32 + lane < nv) {
+            const uint8_t *sc = it.b < 0 ? P.A.pscale : P.A.cscale + (size_t)it.b * P.A.L * 2 * P.A.H;
+            byte = __ldg(sc + ((size_t)(it.e0 + j * AT_UNIT + w * 32 + lane) * 2 + kind) * P.A.H + it.h);
+        }
+        if (++s == 2 * it.n) {
+            s = 0;
+            more = walk.next(it);
+        }
+    };
+    fetch();
+    while (nv > 0) {
+        const uint32_t now = byte;
+        const int valid = nv;
+        nv = 0;
+        fetch();
+        const float f = fp8_factor(now);
+        if (!(tile_wait_warp(&sh.raw_full[r.slot], r.phase, limit, sh) &&
+              tile_wait_warp(&sh.kv_empty[q.slot], q.phase ^ 1, limit, sh)))
+            return;
+        const uint8_t *src = raw + r.slot * C::RAW;
+        uint8_t *dst = kv + q.slot * C::TILE + flip * C::BLOCK;
+#pragma unroll 4
+        for (int p = 0; p < 32 / RP; ++p) {
+            const int rr = p * RP + sub, row = w * 32 + rr;
+            const float fr = __shfl_sync(0xffffffffu, f, rr);
+            uint4 v = *reinterpret_cast<const uint4 *>(src + row * D + ch * 16);
+            if (row >= valid)
+                v = make_uint4(0, 0, 0, 0);
+            float x[16];
+            unpack_e4m3(v.x, x);
+            unpack_e4m3(v.y, x + 4);
+            unpack_e4m3(v.z, x + 8);
+            unpack_e4m3(v.w, x + 12);
+            uint32_t y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                y[k] = pack_bf16(x[2 * k] * fr, x[2 * k + 1] * fr);
+            // two 16-byte chunks of a 128-byte row, at their swizzled places; lanes of the
+            // second block of columns store them in the other order (no bank conflicts)
+            const int c0 = (ch % 4) * 2;
+            const uint4 a = make_uint4(y[0], y[1], y[2], y[3]), b = make_uint4(y[4], y[5], y[6], y[7]);
+            *reinterpret_cast<uint4 *>(dst + row * 128 + (((c0 + flip) ^ (row & 7)) << 4)) = flip ? b : a;
+            *reinterpret_cast<uint4 *>(dst + row * 128 + (((c0 + 1 - flip) ^ (row & 7)) << 4)) = flip ? a : b;
+        }
+        async_fence();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&sh.kv_full[q.slot]);
+            mbar_arrive(&sh.raw_empty[r.slot]);
+        }
+        r.next(C::NR);
+        q.next(C::NS);
     }
 }
 
@@ -832,24 +848,35 @@ cudaError_t launch_tiles(const TileParams &P, int grid, cudaStream_t stream)
         return cudaErrorNotSupported;
     const AttnParams &A = P.A;
     CUtensorMap mq_pre, mq_own, m_pre, m_own;
-    const cuuint64_t u = 1;
     // q as [token row][Hkv][G][D]
     const cuuint64_t dq[4] = {D, (cuuint64_t)A.G, (cuuint64_t)A.H, (cuuint64_t)A.B * A.T};
     const cuuint32_t bp[4] = {64, (cuuint32_t)A.G, 1, (cuuint32_t)P.W.pre.tq};
     const cuuint32_t bo[4] = {64, (cuuint32_t)A.G, 1, (cuuint32_t)P.W.own.tq};
     const cuuint32_t wide = Q8 ? D : 64;
-    const cuuint64_t dp[4] = {D, (cuuint64_t)A.H, 2, A.P > 0 ? (cuuint64_t)A.P : u};
-    const cuuint64_t dc[5] = {D, (cuuint64_t)A.H, 2, A.L > 0 ? (cuuint64_t)A.L : u, (cuuint64_t)A.B};
+    const cuuint64_t dp[4] = {D, (cuuint64_t)A.H, 2, (cuuint64_t)A.P};
+    const cuuint64_t dc[5] = {D, (cuuint64_t)A.H, 2, (cuuint64_t)A.L, (cuuint64_t)A.B};
     const cuuint32_t box[5] = {wide, 1, 1, AT_UNIT, 1};
-    // an absent prefix or cache has no units: its map is never used
-    if (!make_map(&mq_pre, false, A.q, 4, dq, bp) || !make_map(&mq_own, false, A.q, 4, dq, bo) ||
-        !make_map(&m_pre, Q8, A.P > 0 ? A.prefix : A.cache, 4, dp, box) ||
-        !make_map(&m_own, Q8, A.L > 0 ? A.cache : A.prefix, 5, dc, box))
+    if ((A.P > 0 && (!make_map(&mq_pre, false, A.q, 4, dq, bp) || !make_map(&m_pre, Q8, A.prefix, 4, dp, box))) ||
+        (A.L > 0 && (!make_map(&mq_own, false, A.q, 4, dq, bo) || !make_map(&m_own, Q8, A.cache, 5, dc, box))))
         return cudaErrorInvalidValue;
-    const cudaError_t e =
-        cudaFuncSetAttribute(va_tiles<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    // an absent prefix or cache has no units: its maps are never used
+    if (A.P == 0)
+        mq_pre = mq_own, m_pre = m_own;
+    if (A.L == 0)
+        mq_own = mq_pre, m_own = m_pre;
+    // the shared memory a launch may ask for, raised once per device
+    static std::atomic<uint64_t> raised{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(raised.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(va_tiles<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+        if (e != cudaSuccess)
+            return e;
+        raised.fetch_or(bit, std::memory_order_relaxed);
+    }
     va_tiles<D, Q8><<<grid, C::THREADS, C::SMEM, stream>>>(mq_pre, mq_own, m_pre, m_own, P);
     return cudaGetLastError();
 }
