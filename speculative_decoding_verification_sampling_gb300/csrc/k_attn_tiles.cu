@@ -17,9 +17,20 @@
 // work on the same entries (each K and V tile read once for 256 rows); where
 // they do not, the groups take alternate units of the same rows and leave a
 // partial result each.  A loader thread feeds a ring of K and V tiles with
-// TMA; one warp issues every tcgen05.mma.  Entries in 8 bits are copied as
-// they are, and four more warps turn them into the bfloat16 numbers they
-// stand for (exact) in the swizzled layout that TMA would have written.
+// TMA; one warp issues every tcgen05.mma.
+//
+// Entries in 8 bits are copied as they are, and four more warps turn them into
+// float16, in the swizzled layout that TMA would have written: one conversion
+// and one multiplication for two codes, where bfloat16 would take six
+// operations.  float16 holds a code times 2^s exactly for s in [-15, 7], so
+// the scales of a unit are taken relative to its largest, which becomes 2^7;
+// heads whose scale is more than 2^22 below it lose their last bits (at 2^-40
+// of the unit's largest element).  What the largest stands for goes back in
+// per unit, exactly: into the scores as a factor, and for V into the exponent
+// of the weights (they are 2^(c S + bv - m), and l takes them times 2^-bv).
+// Q becomes float16 too, each row times a power of two that puts its largest
+// element in [2^14, 2^15): exact for elements down to 2^-32 of it.  P is
+// rounded to float16, 2^-11 of a weight.
 //
 // The last unit of a stretch is ragged: scores past its end become -inf, and
 // V's rows past it are zeroed in shared memory, since 0 * NaN would reach O.
@@ -54,32 +65,37 @@ __device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap *map, uns
                  : "memory");
 }
 
-// Shared-memory operand with 128-byte rows, 128-byte swizzle: start address,
-// leading and stride offsets in 16-byte units, descriptor version 1, swizzle
-// code 2.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride)
+// Shared-memory operand with 128-byte rows and 128-byte swizzle: the low word
+// holds the start address and the leading offset, the high word the stride
+// offset (1024: eight rows), all in 16-byte units, descriptor version 1 and
+// swizzle code 2.  The issuing thread keeps to 32-bit additions on the low
+// word: its own instructions are what the tensor cores wait for otherwise.
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead)
 {
-    return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
-           (1ull << 46) | (2ull << 61);
+    return ((addr & 0x3ffffu) >> 4) | ((lead >> 4) << 16);
 }
-// Instruction descriptor: bfloat16 operands, float32 accumulator, M = 128.
-__host__ __device__ constexpr uint32_t mma_desc(int n, bool b_mn_major)
+// Instruction descriptor: bfloat16 or float16 operands, float32 accumulator,
+// M = 128.
+__host__ __device__ constexpr uint32_t mma_desc(int n, bool b_mn_major, bool half)
 {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+    return (1u << 4) | (half ? 0u : (1u << 7) | (1u << 10)) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
            ((128u >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(acc)
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(DESC_HI)
                  : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "l"(b), "r"(idesc), "r"(acc)
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "mov.b64 db, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(DESC_HI)
                  : "memory");
 }
 __device__ __forceinline__ void mma_commit(unsigned long long *bar)
@@ -162,19 +178,34 @@ struct TileCfg {
     // other warpgroups (their sum over the warpgroups stays within the launch's)
     static constexpr int REGS = Q8 ? 128 : 168, REGS_SOFT = Q8 ? 176 : 208, REGS_REST = 80;
     static_assert(2 * REGS_SOFT + (THREADS / 128 - 2) * REGS_REST <= THREADS / 128 * REGS, "register split");
-    static constexpr uint32_t SMEM = 2 * TILE + NS * TILE + NR * RAW + 1024;
+    static constexpr uint32_t TILES = 2 * TILE + NS * TILE + NR * RAW;   // TileShared lies behind them
 };
 
-constexpr int W_LOAD = 8, W_MMA = 9, W_CVT = 12;   // warps 0-7: softmax, two groups
+constexpr int W_LOAD = 8, W_MMA = 9, W_SCALE = 10, W_CVT = 12;   // warps 0-7: softmax, two groups
+constexpr int FAC = 4;   // units whose scale factors are ready ahead
 
 struct TileShared {
     unsigned long long q_full[2], q_empty[2], kv_full[8], kv_empty[8], raw_full[8], raw_empty[8];
+    unsigned long long q_ready[2];   // 8-bit entries: the Q tile is in float16
     unsigned long long s_full[2], p_ready[2], o_full[2], drain;
+    // 8-bit entries
+    unsigned long long f_full[FAC], f_empty[FAC];
+    float2 kv_unit[8];               // what 1 stands for in a unit's K (x), and log2 of it in its V (y); unit u in u % 8
+    uint8_t q_unit[2][AT_ROWS];      // the exponent of what 1 stands for in a row of Q
+    uint16_t fac[FAC][2][AT_ROWS];   // float16 factors of a unit's rows, K and V
     uint32_t tmem;
     volatile int abort;
     int total, b0, base0;        // units of all sequences (one pair's worth); where the CTA's line starts
     int sums[16];                // per warp
 };
+
+constexpr uint32_t SMEM_MAX = 232448;
+template <int D, bool Q8>
+constexpr uint32_t tile_smem()
+{
+    static_assert(TileCfg<D, Q8>::TILES + sizeof(TileShared) <= SMEM_MAX, "shared memory of a CTA");
+    return TileCfg<D, Q8>::TILES + (uint32_t)sizeof(TileShared);
+}
 
 struct TileParams {
     AttnParams A;
@@ -373,7 +404,7 @@ template <int D, bool Q8>
 __device__ void mma_role(const TileParams &P, TileShared &sh, uint32_t sq, uint8_t *kv_ptr, uint32_t skv, uint32_t limit)
 {
     using C = TileCfg<D, Q8>;
-    constexpr uint32_t IS = mma_desc(128, false), IO = mma_desc(D, true);
+    constexpr uint32_t IS = mma_desc(128, false, Q8), IO = mma_desc(D, true, Q8);
     const int lane = threadIdx.x & 31;
     const uint32_t tmem = sh.tmem;
     Ring q, r;
@@ -381,14 +412,14 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint32_t sq, uint8
     bool ok = true;
     auto scores = [&](int g, int qs, int ks, bool last) {
         if (lane == 0) {
+            const uint32_t a = desc_lo(sq + qs * C::TILE, 16), b = desc_lo(skv + ks * C::TILE, 16);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
-                const uint32_t at = (k / 4) * C::BLOCK + (k % 4) * 32;
-                mma_ss(tmem + g * 128, smem_desc(sq + qs * C::TILE + at, 16, 1024),
-                       smem_desc(skv + ks * C::TILE + at, 16, 1024), IS, k > 0);
+                const uint32_t at = ((k / 4) * C::BLOCK + (k % 4) * 32) >> 4;
+                mma_ss(tmem + g * 128, a + at, b + at, IS, k > 0);
             }
             mma_commit(&sh.s_full[g]);
-            if (last)
+            if (last && !Q8)
                 mma_commit(&sh.q_empty[qs]);
         }
         __syncwarp();
@@ -400,10 +431,11 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint32_t sq, uint8
         pphase[g] ^= 1;
         tc_after();
         if (lane == 0) {
+            // V is read along its rows: blocks of 64 columns lie BLOCK apart, 16 rows are 2048 bytes
+            const uint32_t b = desc_lo(skv + vs * C::TILE, C::BLOCK);
 #pragma unroll
             for (int k = 0; k < AT_UNIT / 16; ++k)
-                mma_ts(tmem + 256 + g * D, tmem + g * 128 + k * 8,
-                       smem_desc(skv + vs * C::TILE + k * 2048, C::BLOCK, 1024), IO, !first || k > 0);
+                mma_ts(tmem + 256 + g * D, tmem + g * 128 + k * 8, b + ((k * 2048) >> 4), IO, !first || k > 0);
             if (last)
                 mma_commit(&sh.o_full[g]);
         }
@@ -440,11 +472,12 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint32_t sq, uint8
         int qs[2], ks, vs;
         for (int g = 0; ok && g <= it.two; ++g) {
             qs[g] = q.slot;
-            ok = tile_wait_warp(&sh.q_full[q.slot], q.phase, limit, sh);
+            ok = tile_wait_warp(Q8 ? &sh.q_ready[q.slot] : &sh.q_full[q.slot], q.phase, limit, sh);
             q.next(2);
         }
         if (!ok)
             break;
+        tc_after();
         if (it.two) {
             if (!take(ks))
                 break;
@@ -493,6 +526,10 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint32_t sq, uint8
                 }
             }
         }
+        // 8-bit entries: the softmax groups have read the rows' units, too
+        if (Q8)
+            for (int g = 0; ok && g <= it.two; ++g)
+                give(&sh.q_empty[qs[g]]);
     }
     if (!ok) {
         give(&sh.drain);
@@ -502,17 +539,23 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint32_t sq, uint8
 
 // Softmax of group g: thread w * 32 + lane owns row w * 32 + lane of the
 // group's tile (a warp reaches only its own quarter of the TMEM lanes).
-template <int D>
+template <int D, bool Q8>
 __device__ void softmax_role(const TileParams &P, TileShared &sh, int g, uint32_t limit)
 {
     const int lane = threadIdx.x & 31, w = (threadIdx.x / 32) & 3, row = w * 32 + lane;
     const uint32_t lanes = (uint32_t)(w * 32) << 16;
     const uint32_t ts = sh.tmem + lanes + g * 128, to = sh.tmem + lanes + 256 + g * D;
-    const float c = P.A.c;
+    float c = P.A.c, bv = 0.0f, unbv = 1.0f, crow = P.A.c;
     uint32_t sphase = 0, ophase = 0;
+    Ring q;
+    int unit = 0;   // of the CTA, as the item starts
     Walk walk(P, sh);
     Item it;
-    while (walk.next(it)) {
+    for (; walk.next(it); unit += it.n) {
+        // the slot of this group's Q tile: the second of two, or the only one
+        const int qs = it.two ? (q.slot + g) & 1 : q.slot;
+        if (!it.two)
+            q.next(2);
         const int tq = it.b < 0 ? P.W.pre.tq : P.W.own.tq, rows = tq * P.A.G;
         // rows of this group's tile that exist
         const int have = min(max(it.tokens - (it.two ? g * tq : 0), 0), tq) * P.A.G;
@@ -520,12 +563,21 @@ __device__ void softmax_role(const TileParams &P, TileShared &sh, int g, uint32_
         const int cnt = it.two ? it.n : (it.n - g + 1) / 2;
         float m = -F_INF, l = 0.0f;
         for (int i = 0; i < cnt; ++i) {
-            const int nv = it.left - (it.two ? i : 2 * i + g) * AT_UNIT;
+            const int j = it.two ? i : 2 * i + g, nv = it.left - j * AT_UNIT;
             if (!tile_wait_warp(&sh.s_full[g], sphase, limit, sh))
                 return;
             sphase ^= 1;
             tc_after();
             if (active) {
+                if constexpr (Q8) {
+                    // written before the tiles were handed to the tensor cores that made S
+                    if (i == 0)
+                        crow = P.A.c * __int_as_float(sh.q_unit[qs][row] << 23);
+                    const float2 u = sh.kv_unit[(unit + j) & 7];
+                    c = crow * u.x;
+                    bv = u.y;
+                    unbv = ex2a(-bv);   // a power of two: exact
+                }
                 float x[128];
                 tmem_ld128(ts, x);
                 if (nv < AT_UNIT) {
@@ -539,7 +591,9 @@ __device__ void softmax_role(const TileParams &P, TileShared &sh, int g, uint32_
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
                         top[u] = fmaxf(top[u], x[k + u]);
-                const float s = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+                float s = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+                if constexpr (Q8)
+                    s += bv;
                 const bool up = s > m + 8.0f;
                 if (__any_sync(0xffffffffu, up)) {
                     const float f = up ? ex2a(m - s) : 1.0f;   // 2^(-inf) = 0 the first time
@@ -560,7 +614,7 @@ __device__ void softmax_role(const TileParams &P, TileShared &sh, int g, uint32_
                         }
                     }
                 }
-                const float ref = m == -F_INF ? 0.0f : m;
+                const float ref = (m == -F_INF ? 0.0f : m) - bv;
                 const f2 cc = pk(c, c), nref = pk(-ref, -ref);
                 f2 sum[2] = {pk(0.0f, 0.0f), pk(0.0f, 0.0f)};
 #pragma unroll
@@ -572,13 +626,13 @@ __device__ void softmax_role(const TileParams &P, TileShared &sh, int g, uint32_
                         sum[k & 1] = add2(sum[k & 1], e);
                         float lo, hi;
                         upk(e, lo, hi);
-                        p[k] = pack_bf16(lo, hi);
+                        p[k] = Q8 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
                     }
                     tmem_st32(ts + hf * 32, p);
                 }
                 float lo, hi;
                 upk(add2(sum[0], sum[1]), lo, hi);
-                l += lo + hi;
+                l += Q8 ? (lo + hi) * unbv : lo + hi;
                 tmem_st_wait();
             }
             tc_before();
@@ -613,83 +667,200 @@ __device__ void softmax_role(const TileParams &P, TileShared &sh, int g, uint32_
     }
 }
 
-// Codes to bfloat16: warp w converts rows 32 w .. 32 w + 31 of each tile.  The
-// scale bytes of a tile (one per row, a lane each) are fetched while the tile
-// before it is converted.
+// 8-bit entries: the scale bytes of three units are in flight in one warp's
+// registers (rows lane, lane + 32, ..), which turns them into float16 factors
+// relative to the unit's largest.
+__device__ __forceinline__ void scale_role(const TileParams &P, TileShared &sh, uint32_t limit)
+{
+    const int lane = threadIdx.x & 31;
+    Walk walk(P, sh);
+    Item it;
+    int j = 0, unit = 0;
+    bool more = walk.next(it);
+    Ring r;
+    struct Bytes {
+        int nv;
+        uint32_t b[2][4];
+    };
+    auto fetch = [&](Bytes &x) {
+        x.nv = 0;
+        if (!more)
+            return;
+        x.nv = it.left - j * AT_UNIT;
+        const uint8_t *sc = (it.b < 0 ? P.A.pscale : P.A.cscale + (size_t)it.b * P.A.L * 2 * P.A.H) +
+                            (size_t)(it.e0 + j * AT_UNIT) * 2 * P.A.H + it.h;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                x.b[k][i] = 0;
+                if (i * 32 + lane < x.nv)
+                    x.b[k][i] = __ldg(sc + ((size_t)(i * 32 + lane) * 2 + k) * P.A.H);
+            }
+        if (++j == it.n) {
+            j = 0;
+            more = walk.next(it);
+        }
+    };
+    auto publish = [&](const Bytes &x) {
+        if (x.nv <= 0 || !tile_wait_warp(&sh.f_empty[r.slot], r.phase ^ 1, limit, sh))
+            return false;
+        int ref[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                m = max(m, x.b[k][i] == 255 ? 0u : x.b[k][i]);
+            // no lower than 2^-100: l holds the weights times its reciprocal
+            ref[k] = (int)max(__reduce_max_sync(0xffffffffu, m), 27u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // 2^(byte - ref + 7) times the 2^8 that scale_e4m3 takes away
+                const int e = (int)x.b[k][i] - ref[k] + 15 + 127;
+                const float f = x.b[k][i] == 255 ? __int_as_float(0x7fc00000) : __int_as_float(max(e, 0) << 23);
+                sh.fac[r.slot][k][i * 32 + lane] = (uint16_t)pack_f16(f, 0.0f);
+            }
+        }
+        if (lane == 0)
+            sh.kv_unit[unit & 7] = make_float2(__int_as_float((ref[0] - 7) << 23), (float)(ref[1] - 7 - 127));
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&sh.f_full[r.slot]);
+        r.next(FAC);
+        ++unit;
+        return true;
+    };
+    Bytes a, b, c;
+    fetch(a);
+    fetch(b);
+    fetch(c);
+    for (;;) {
+        if (!publish(a))
+            return;
+        fetch(a);
+        if (!publish(b))
+            return;
+        fetch(b);
+        if (!publish(c))
+            return;
+        fetch(c);
+    }
+}
+
+// 8-bit entries: warp w turns rows 32 w .. 32 w + 31 of each tile into float16.
 template <int D>
-__device__ void convert_role(const TileParams &P, TileShared &sh, const uint8_t *raw, uint8_t *kv, uint32_t limit)
+__device__ void convert_role(const TileParams &P, TileShared &sh, uint8_t *qt, const uint8_t *raw, uint8_t *kv,
+                             uint32_t limit)
 {
     using C = TileCfg<D, true>;
     constexpr int CH = D / 16;          // 16-code chunks of a row
     constexpr int RP = 32 / CH;         // rows per pass of a warp
     const int lane = threadIdx.x & 31, w = (threadIdx.x / 32) & 3;
     const int ch = lane % CH, sub = lane / CH, flip = ch / 4;
-    Ring r, q;
+    Ring r, s, q;
     Walk walk(P, sh);
     Item it;
-    int s = 0;
-    bool more = walk.next(it);
-    // the next tile's scale byte of this lane's row, and its valid rows
-    uint32_t byte = 127;
-    int nv = 0;
-    auto fetch = [&] {
-        if (!more)
-            return;
-        const auto [j, kind] = item_tile(it, s);
-        nv = it.left - j * AT_UNIT;
-        byte = 127;
-        if (w * 32 + lane < nv) {
-            const uint8_t *sc = it.b < 0 ? P.A.pscale : P.A.cscale + (size_t)it.b * P.A.L * 2 * P.A.H;
-            byte = __ldg(sc + ((size_t)(it.e0 + j * AT_UNIT + w * 32 + lane) * 2 + kind) * P.A.H + it.h);
-        }
-        if (++s == 2 * it.n) {
-            s = 0;
-            more = walk.next(it);
-        }
-    };
-    fetch();
-    while (nv > 0) {
-        const uint32_t now = byte;
-        const int valid = nv;
-        nv = 0;
-        fetch();
-        const float f = fp8_factor(now);
-        if (!(tile_wait_warp(&sh.raw_full[r.slot], r.phase, limit, sh) &&
-              tile_wait_warp(&sh.kv_empty[q.slot], q.phase ^ 1, limit, sh)))
-            return;
-        const uint8_t *src = raw + r.slot * C::RAW;
-        uint8_t *dst = kv + q.slot * C::TILE + flip * C::BLOCK;
-#pragma unroll 4
-        for (int p = 0; p < 32 / RP; ++p) {
-            const int rr = p * RP + sub, row = w * 32 + rr;
-            const float fr = __shfl_sync(0xffffffffu, f, rr);
-            uint4 v = *reinterpret_cast<const uint4 *>(src + row * D + ch * 16);
-            if (row >= valid)
-                v = make_uint4(0, 0, 0, 0);
-            float x[16];
-            unpack_e4m3(v.x, x);
-            unpack_e4m3(v.y, x + 4);
-            unpack_e4m3(v.z, x + 8);
-            unpack_e4m3(v.w, x + 12);
-            uint32_t y[8];
+    int unit = 0;   // of the CTA, as the item starts
+
+    // a Q tile: bfloat16 to float16 in place, eight lanes to a row
+    auto convert_q = [&] {
+        if (!tile_wait_warp(&sh.q_full[q.slot], q.phase, limit, sh))
+            return false;
+        uint8_t *tile = qt + q.slot * C::TILE;
+#pragma unroll 2
+        for (int p = 0; p < 8; ++p) {
+            const int row = w * 32 + p * 4 + lane / 8;
+            uint4 v[D / 64];
+            uint32_t top = 0;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                y[k] = pack_bf16(x[2 * k] * fr, x[2 * k + 1] * fr);
-            // two 16-byte chunks of a 128-byte row, at their swizzled places; lanes of the
-            // second block of columns store them in the other order (no bank conflicts)
-            const int c0 = (ch % 4) * 2;
-            const uint4 a = make_uint4(y[0], y[1], y[2], y[3]), b = make_uint4(y[4], y[5], y[6], y[7]);
-            *reinterpret_cast<uint4 *>(dst + row * 128 + (((c0 + flip) ^ (row & 7)) << 4)) = flip ? b : a;
-            *reinterpret_cast<uint4 *>(dst + row * 128 + (((c0 + 1 - flip) ^ (row & 7)) << 4)) = flip ? a : b;
+            for (int k = 0; k < D / 64; ++k) {
+                v[k] = *reinterpret_cast<const uint4 *>(tile + k * C::BLOCK + row * 128 + (lane % 8) * 16);
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[k].x & 0x7fff7fffu, v[k].y & 0x7fff7fffu),
+                                             __vmaxu2(v[k].z & 0x7fff7fffu, v[k].w & 0x7fff7fffu)));
+            }
+            top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+            for (int o = 4; o; o >>= 1)
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            // the row's largest element is 1.m * 2^e; infinities, NaN and zero rows stay as they are
+            const int e = top == 0 || top >= 0x7f80u ? 14 : max((int)(top >> 7) - 127, -112);
+            const float f = __int_as_float((127 + 14 - e) << 23);
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k) {
+                uint32_t *x = reinterpret_cast<uint32_t *>(&v[k]);
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    x[u] = pack_f16(__uint_as_float(x[u] << 16) * f, __uint_as_float(x[u] & 0xffff0000u) * f);
+                *reinterpret_cast<uint4 *>(tile + k * C::BLOCK + row * 128 + (lane % 8) * 16) = v[k];
+            }
+            if (lane % 8 == 0)
+                sh.q_unit[q.slot][row] = (uint8_t)(127 - 14 + e);
         }
         async_fence();
         __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(&sh.kv_full[q.slot]);
-            mbar_arrive(&sh.raw_empty[r.slot]);
+        if (lane == 0)
+            mbar_arrive(&sh.q_ready[q.slot]);
+        q.next(2);
+        return true;
+    };
+
+    // a tile of codes: 16 of a row per lane and pass
+    auto convert = [&](const uint8_t *src, uint8_t *tile, const uint16_t *fac, int valid) {
+        uint8_t *dst = tile + flip * C::BLOCK;
+        // four passes' loads ahead of their stores: the compiler cannot tell that they do not alias
+#pragma unroll
+        for (int p0 = 0; p0 < 32 / RP; p0 += 4) {
+            uint4 v[4];
+            uint32_t f[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const int row = w * 32 + (p0 + p) * RP + sub;
+                v[p] = *reinterpret_cast<const uint4 *>(src + row * D + ch * 16);
+                f[p] = fac[row] * 0x10001u;
+            }
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const int row = w * 32 + (p0 + p) * RP + sub;
+                uint4 a, b;
+                scale_e4m3(v[p].x, f[p], a.x, a.y);
+                scale_e4m3(v[p].y, f[p], a.z, a.w);
+                scale_e4m3(v[p].z, f[p], b.x, b.y);
+                scale_e4m3(v[p].w, f[p], b.z, b.w);
+                if (row >= valid)
+                    a = b = make_uint4(0, 0, 0, 0);
+                // two 16-byte chunks of a 128-byte row, at their swizzled places; lanes of the
+                // second block of columns store them in the other order (no bank conflicts)
+                const int c0 = (ch % 4) * 2;
+                *reinterpret_cast<uint4 *>(dst + row * 128 + (((c0 + flip) ^ (row & 7)) << 4)) = flip ? b : a;
+                *reinterpret_cast<uint4 *>(dst + row * 128 + (((c0 + 1 - flip) ^ (row & 7)) << 4)) = flip ? a : b;
+            }
         }
-        r.next(C::NR);
-        q.next(C::NS);
+    };
+
+    for (; walk.next(it); unit += it.n) {
+        for (int k = 0; k <= it.two; ++k)
+            if (!convert_q())
+                return;
+        for (int at = 0; at < 2 * it.n; ++at) {
+            const auto [j, kind] = item_tile(it, at);
+            const int valid = it.left - j * AT_UNIT, fs = (unit + j) % FAC;
+            if (!(tile_wait_warp(&sh.f_full[fs], ((unit + j) / FAC) & 1, limit, sh) &&
+                  tile_wait_warp(&sh.raw_full[r.slot], r.phase, limit, sh) &&
+                  tile_wait_warp(&sh.kv_empty[s.slot], s.phase ^ 1, limit, sh)))
+                return;
+            convert(raw + r.slot * C::RAW, kv + s.slot * C::TILE, sh.fac[fs][kind], valid);
+            async_fence();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sh.kv_full[s.slot]);
+                mbar_arrive(&sh.raw_empty[r.slot]);
+                if (kind)
+                    mbar_arrive(&sh.f_empty[fs]);
+            }
+            r.next(C::NR);
+            s.next(C::NS);
+        }
     }
 }
 
@@ -700,11 +871,11 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
              const __grid_constant__ TileParams P)
 {
     using C = TileCfg<D, Q8>;
-    extern __shared__ uint8_t dyn[];
-    __shared__ TileShared sh;
+    // no static shared memory: the tiles start on a 1024-byte boundary, as their swizzle asks
+    extern __shared__ __align__(1024) uint8_t tiles[];
+    TileShared &sh = *reinterpret_cast<TileShared *>(tiles + C::TILES);
     pdl_trigger();
     const int tid = threadIdx.x, warp = tid / 32;
-    uint8_t *tiles = dyn + ((1024 - (saddr(dyn) & 1023)) & 1023);
     uint8_t *kv = tiles + 2 * C::TILE, *raw = kv + C::NS * C::TILE;
     const uint32_t sq = saddr(tiles), skv = saddr(kv), sraw = saddr(raw);
     const uint32_t limit = hinted_limit(P.spin_limit > OWN_WAIT_MIN ? P.spin_limit : OWN_WAIT_MIN);
@@ -729,6 +900,7 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
         for (int k = 0; k < 2; ++k) {
             mbar_init(&sh.q_full[k], 1);
             mbar_init(&sh.q_empty[k], 1);
+            mbar_init(&sh.q_ready[k], 4);
             mbar_init(&sh.s_full[k], 1);
             mbar_init(&sh.p_ready[k], 4);
             mbar_init(&sh.o_full[k], 1);
@@ -740,6 +912,10 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
         for (int k = 0; k < C::NR; ++k) {
             mbar_init(&sh.raw_full[k], 1);
             mbar_init(&sh.raw_empty[k], 4);
+        }
+        for (int k = 0; k < FAC; ++k) {
+            mbar_init(&sh.f_full[k], 1);
+            mbar_init(&sh.f_empty[k], 4);
         }
         mbar_init(&sh.drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;\n\tfence.proxy.async.shared::cta;" ::: "memory");
@@ -782,7 +958,7 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
 
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFT));
-        softmax_role<D>(P, sh, warp / 4, limit);
+        softmax_role<D, Q8>(P, sh, warp / 4, limit);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_REST));
         if (warp == W_LOAD) {
@@ -790,8 +966,10 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
                 load_role<D, Q8>(P, &mq_pre, &mq_own, &m_pre, &m_own, sh, sq, skv, sraw, limit);
         } else if (warp == W_MMA) {
             mma_role<D, Q8>(P, sh, sq, kv, skv, limit);
+        } else if (Q8 && warp == W_SCALE) {
+            scale_role(P, sh, limit);
         } else if (Q8 && warp >= W_CVT) {
-            convert_role<D>(P, sh, raw, kv, limit);
+            convert_role<D>(P, sh, tiles, raw, kv, limit);
         }
     }
     __syncwarp();
@@ -872,12 +1050,12 @@ cudaError_t launch_tiles(const TileParams &P, int grid, cudaStream_t stream)
         return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(raised.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(va_tiles<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+        e = cudaFuncSetAttribute(va_tiles<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tile_smem<D, Q8>());
         if (e != cudaSuccess)
             return e;
         raised.fetch_or(bit, std::memory_order_relaxed);
     }
-    va_tiles<D, Q8><<<grid, C::THREADS, C::SMEM, stream>>>(mq_pre, mq_own, m_pre, m_own, P);
+    va_tiles<D, Q8><<<grid, C::THREADS, tile_smem<D, Q8>(), stream>>>(mq_pre, mq_own, m_pre, m_own, P);
     return cudaGetLastError();
 }
 

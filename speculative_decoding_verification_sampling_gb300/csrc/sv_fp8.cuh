@@ -64,4 +64,26 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
     return r;
 }
 
+// Two float16, `a` in the low half, to nearest even.
+__device__ __forceinline__ uint32_t pack_f16(float a, float b)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+// Four codes (none the NaN code) to four float16, each times the float16 pair
+// `f` times 2^-8.  A code's exponent and mantissa bits, moved one place to the
+// right of the high byte of a float16, are the number's times 2^-8, the
+// subnormal ones too; four integer operations do it for two codes, and the
+// conversion instruction is slower.
+__device__ __forceinline__ void scale_e4m3(uint32_t w, uint32_t f, uint32_t &lo, uint32_t &hi)
+{
+    uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);   // codes in the high bytes
+    a = (a & 0x80008000u) | ((a >> 1) & 0x3f803f80u);
+    b = (b & 0x80008000u) | ((b >> 1) & 0x3f803f80u);
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(f));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(f));
+}
+
 }  // namespace sv
