@@ -103,6 +103,17 @@ __device__ __forceinline__ void mma_commit(unsigned long long *bar)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(bar))
                  : "memory");
 }
+// One lane of a converged warp, the same one every time.  A branch on it tells
+// the compiler that one thread runs what follows, so that the operands of
+// tcgen05.mma and TMA go to uniform registers directly.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// A value that all lanes hold, made known as such.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -319,9 +330,9 @@ struct Ring {
 __device__ __forceinline__ bool tile_wait(unsigned long long *bar, uint32_t parity, uint32_t limit, TileShared &sh)
 {
     for (uint32_t it = 0;; ++it) {
-        if (mbar_test_hint(bar, parity))
+        if (mbar_test(bar, parity))
             return true;
-        if (it >= limit || sh.abort) {
+        if (it >= limit * 64 || sh.abort) {
             sh.abort = 1;
             return false;
         }
@@ -399,19 +410,19 @@ __device__ void load_role(const TileParams &P, const CUtensorMap *mq_pre, const 
     }
 }
 
-// The issuer of every tcgen05.mma: one warp, lane 0 issues.
+// The issuer of every tcgen05.mma: one warp, one elected lane issues.
 template <int D, bool Q8>
 __device__ void mma_role(const TileParams &P, TileShared &sh, uint32_t sq, uint8_t *kv_ptr, uint32_t skv, uint32_t limit)
 {
     using C = TileCfg<D, Q8>;
     constexpr uint32_t IS = mma_desc(128, false, Q8), IO = mma_desc(D, true, Q8);
     const int lane = threadIdx.x & 31;
-    const uint32_t tmem = sh.tmem;
+    const uint32_t tmem = (uint32_t)uniform((int)sh.tmem);
     Ring q, r;
     uint32_t pphase[2] = {0, 0};
     bool ok = true;
     auto scores = [&](int g, int qs, int ks, bool last) {
-        if (lane == 0) {
+        if (elect_one()) {
             const uint32_t a = desc_lo(sq + qs * C::TILE, 16), b = desc_lo(skv + ks * C::TILE, 16);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
@@ -430,7 +441,7 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint32_t sq, uint8
             return;
         pphase[g] ^= 1;
         tc_after();
-        if (lane == 0) {
+        if (elect_one()) {
             // V is read along its rows: blocks of 64 columns lie BLOCK apart, 16 rows are 2048 bytes
             const uint32_t b = desc_lo(skv + vs * C::TILE, C::BLOCK);
 #pragma unroll
@@ -449,7 +460,7 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint32_t sq, uint8
         return ok;
     };
     auto give = [&](unsigned long long *bar) {
-        if (lane == 0)
+        if (elect_one())
             mma_commit(bar);
         __syncwarp();
     };
@@ -469,6 +480,8 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint32_t sq, uint8
     Walk walk(P, sh);
     Item it;
     while (ok && walk.next(it)) {
+        it.n = uniform(it.n);
+        it.two = uniform(it.two);
         int qs[2], ks, vs;
         for (int g = 0; ok && g <= it.two; ++g) {
             qs[g] = q.slot;
@@ -962,7 +975,7 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_REST));
         if (warp == W_LOAD) {
-            if (tid % 32 == 0)
+            if (elect_one())
                 load_role<D, Q8>(P, &mq_pre, &mq_own, &m_pre, &m_own, sh, sq, skv, sraw, limit);
         } else if (warp == W_MMA) {
             mma_role<D, Q8>(P, sh, sq, kv, skv, limit);
