@@ -136,7 +136,22 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float *x)
                  : "memory");
 #undef OUT
 }
-__device__ __forceinline__ void tmem_ld128(uint32_t addr, float *x)
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&x)[64])
+{
+#define OUT(i) "=f"(x[i])
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%64];\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+                 "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%65];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : R32(OUT, 0), R32(OUT, 32)
+                 : "r"(addr), "r"(addr + 32)
+                 : "memory");
+#undef OUT
+}
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&x)[128])
 {
 #define OUT(i) "=f"(x[i])
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -184,15 +199,18 @@ struct TileCfg {
     static constexpr uint32_t RAW = 128 * D;          // a tile of codes
     static constexpr int NS = Q8 ? (D == 128 ? 3 : 5) : (D == 128 ? 4 : 8);   // K / V tiles in flight
     static constexpr int NR = Q8 ? (D == 128 ? 4 : 8) : 0;                    // tiles of codes in flight
-    static constexpr int THREADS = Q8 ? 512 : 384;
+    static constexpr int THREADS = Q8 ? 640 : 384;
     // registers per thread: at launch, then of the softmax groups and of the
     // other warpgroups (their sum over the warpgroups stays within the launch's)
-    static constexpr int REGS = Q8 ? 128 : 168, REGS_SOFT = Q8 ? 176 : 208, REGS_REST = 80;
+    static constexpr int REGS = Q8 ? 96 : 168, REGS_SOFT = Q8 ? 120 : 208, REGS_REST = 80;
+    // columns of S that a softmax thread holds at a time: the 8-bit kernel's eight converting
+    // warps leave it registers for half a row, which it reads twice
+    static constexpr int COLS = Q8 ? 64 : 128;
     static_assert(2 * REGS_SOFT + (THREADS / 128 - 2) * REGS_REST <= THREADS / 128 * REGS, "register split");
     static constexpr uint32_t TILES = 2 * TILE + NS * TILE + NR * RAW;   // TileShared lies behind them
 };
 
-constexpr int W_LOAD = 8, W_MMA = 9, W_SCALE = 10, W_CVT = 12;   // warps 0-7: softmax, two groups
+constexpr int W_LOAD = 8, W_MMA = 9, W_SCALE = 10, W_CVT = 12;   // warps 0-7: softmax; 12-15, 16-19: conversion
 constexpr int FAC = 4;   // units whose scale factors are ready ahead
 
 struct TileShared {
@@ -207,7 +225,7 @@ struct TileShared {
     uint32_t tmem;
     volatile int abort;
     int total, b0, base0;        // units of all sequences (one pair's worth); where the CTA's line starts
-    int sums[16];                // per warp
+    int sums[20];                // per warp
 };
 
 constexpr uint32_t SMEM_MAX = 232448;
@@ -591,19 +609,26 @@ __device__ void softmax_role(const TileParams &P, TileShared &sh, int g, uint32_
                     bv = u.y;
                     unbv = ex2a(-bv);   // a power of two: exact
                 }
-                float x[128];
-                tmem_ld128(ts, x);
-                if (nv < AT_UNIT) {
+                constexpr int CO = TileCfg<D, Q8>::COLS;
+                float x[CO];
+                auto load = [&](int first) {
+                    tmem_ld(ts + first, x);
+                    if (nv < AT_UNIT) {
 #pragma unroll
-                    for (int k = 0; k < 128; ++k)
-                        x[k] = k < nv ? x[k] : -F_INF;
+                        for (int k = 0; k < CO; ++k)
+                            x[k] = first + k < nv ? x[k] : -F_INF;
+                    }
+                };
+                float top[4] = {-F_INF, -F_INF, -F_INF, -F_INF};
+#pragma unroll
+                for (int first = 0; first < AT_UNIT; first += CO) {
+                    load(first);
+#pragma unroll
+                    for (int k = 0; k < CO; k += 4)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            top[u] = fmaxf(top[u], x[k + u]);
                 }
-                float top[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                for (int k = 4; k < 128; k += 4)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        top[u] = fmaxf(top[u], x[k + u]);
                 float s = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
                 if constexpr (Q8)
                     s += bv;
@@ -632,10 +657,14 @@ __device__ void softmax_role(const TileParams &P, TileShared &sh, int g, uint32_
                 f2 sum[2] = {pk(0.0f, 0.0f), pk(0.0f, 0.0f)};
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
+                    // P's 64 columns lie over those of S that this thread has read
+                    if (CO < AT_UNIT)
+                        load(hf * CO);
+                    constexpr int H = CO < AT_UNIT ? 0 : 64;
                     uint32_t p[32];
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
-                        const f2 e = ex2x2(fma2(pk(x[hf * 64 + 2 * k], x[hf * 64 + 2 * k + 1]), cc, nref));
+                        const f2 e = ex2x2(fma2(pk(x[hf * H + 2 * k], x[hf * H + 2 * k + 1]), cc, nref));
                         sum[k & 1] = add2(sum[k & 1], e);
                         float lo, hi;
                         upk(e, lo, hi);
@@ -761,16 +790,14 @@ __device__ __forceinline__ void scale_role(const TileParams &P, TileShared &sh, 
     }
 }
 
-// 8-bit entries: warp w turns rows 32 w .. 32 w + 31 of each tile into float16.
+// 8-bit entries: tiles to float16, K tiles (and Q) by one group of four warps,
+// V tiles by another; warp w of a group takes rows 32 w .. 32 w + 31.
 template <int D>
-__device__ void convert_role(const TileParams &P, TileShared &sh, uint8_t *qt, const uint8_t *raw, uint8_t *kv,
-                             uint32_t limit)
+__device__ void convert_role(const TileParams &P, TileShared &sh, int group, uint8_t *qt, const uint8_t *raw,
+                             uint8_t *kv, uint32_t limit)
 {
     using C = TileCfg<D, true>;
-    constexpr int CH = D / 16;          // 16-code chunks of a row
-    constexpr int RP = 32 / CH;         // rows per pass of a warp
     const int lane = threadIdx.x & 31, w = (threadIdx.x / 32) & 3;
-    const int ch = lane % CH, sub = lane / CH, flip = ch / 4;
     Ring r, s, q;
     Walk walk(P, sh);
     Item it;
@@ -818,61 +845,77 @@ __device__ void convert_role(const TileParams &P, TileShared &sh, uint8_t *qt, c
         return true;
     };
 
-    // a tile of codes: 16 of a row per lane and pass
-    auto convert = [&](const uint8_t *src, uint8_t *tile, const uint16_t *fac, int valid) {
-        uint8_t *dst = tile + flip * C::BLOCK;
-        // four passes' loads ahead of their stores: the compiler cannot tell that they do not alias
+    // A tile of codes, 16 of a row per lane and pass.  A row's 16 codes become two 16-byte chunks
+    // of the swizzled bfloat16 layout (chunk c of row r at c ^ (r & 7)), and for D = 128 the codes
+    // are swizzled the same way.  Eight lanes take four chunks of the rows r and r ^ 5: their bit 2
+    // keeps the loads, their bit 0 the stores apart, so neither meets a bank conflict.
+    constexpr int PASSES = D / 16, STEP = D == 128 ? 2 : 1;   // passes; of them over the same eight rows
+    const int c2 = lane & 3, blk = D == 128 ? (lane >> 3) & 1 : 0, hi = D == 128 ? lane >> 4 : lane >> 3;
+    uint32_t src0[STEP], dst0[STEP];
+    int row0[STEP];
 #pragma unroll
-        for (int p0 = 0; p0 < 32 / RP; p0 += 4) {
-            uint4 v[4];
-            uint32_t f[4];
+    for (int k = 0; k < STEP; ++k) {
+        const int r7 = (D == 128 ? 2 * k + hi : hi) ^ ((lane >> 2 & 1) * 5);
+        row0[k] = w * 32 + r7;
+        src0[k] = row0[k] * D + (D == 128 ? ((blk * 4 + c2) ^ r7) : c2) * 16;
+        dst0[k] = blk * C::BLOCK + row0[k] * 128 + ((2 * c2) ^ r7) * 16;
+    }
+    auto convert = [&](const uint8_t *src, uint8_t *dst, const uint16_t *fac, int valid) {
+        // every load ahead of the stores: the compiler cannot tell that they do not alias
+        uint4 v[PASSES];
+        uint32_t f[PASSES];
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const int row = w * 32 + (p0 + p) * RP + sub;
-                v[p] = *reinterpret_cast<const uint4 *>(src + row * D + ch * 16);
-                f[p] = fac[row] * 0x10001u;
-            }
+        for (int p = 0; p < PASSES; ++p) {
+            const int k = p % STEP, o = p / STEP * 8;
+            v[p] = *reinterpret_cast<const uint4 *>(src + src0[k] + o * D);
+            f[p] = fac[row0[k] + o];
+        }
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const int row = w * 32 + (p0 + p) * RP + sub;
-                uint4 a, b;
-                scale_e4m3(v[p].x, f[p], a.x, a.y);
-                scale_e4m3(v[p].y, f[p], a.z, a.w);
-                scale_e4m3(v[p].z, f[p], b.x, b.y);
-                scale_e4m3(v[p].w, f[p], b.z, b.w);
-                if (row >= valid)
-                    a = b = make_uint4(0, 0, 0, 0);
-                // two 16-byte chunks of a 128-byte row, at their swizzled places; lanes of the
-                // second block of columns store them in the other order (no bank conflicts)
-                const int c0 = (ch % 4) * 2;
-                *reinterpret_cast<uint4 *>(dst + row * 128 + (((c0 + flip) ^ (row & 7)) << 4)) = flip ? b : a;
-                *reinterpret_cast<uint4 *>(dst + row * 128 + (((c0 + 1 - flip) ^ (row & 7)) << 4)) = flip ? a : b;
+        for (int p = 0; p < PASSES; ++p) {
+            const int k = p % STEP, o = p / STEP * 8;
+            const uint32_t ff = f[p] * 0x10001u;
+            uint4 a, b;
+            scale_e4m3(v[p].x, ff, a.x, a.y);
+            scale_e4m3(v[p].y, ff, a.z, a.w);
+            scale_e4m3(v[p].z, ff, b.x, b.y);
+            scale_e4m3(v[p].w, ff, b.z, b.w);
+            *reinterpret_cast<uint4 *>(dst + dst0[k] + o * 128) = a;
+            *reinterpret_cast<uint4 *>(dst + (dst0[k] ^ 16) + o * 128) = b;
+        }
+        if (valid < AT_UNIT) {
+            // the rows past the stretch
+#pragma unroll
+            for (int p = 0; p < PASSES; ++p) {
+                const int k = p % STEP, o = p / STEP * 8;
+                if (row0[k] + o >= valid) {
+                    *reinterpret_cast<uint4 *>(dst + dst0[k] + o * 128) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(dst + (dst0[k] ^ 16) + o * 128) = make_uint4(0, 0, 0, 0);
+                }
             }
         }
     };
 
     for (; walk.next(it); unit += it.n) {
-        for (int k = 0; k <= it.two; ++k)
+        for (int k = 0; group == 0 && k <= it.two; ++k)
             if (!convert_q())
                 return;
-        for (int at = 0; at < 2 * it.n; ++at) {
+        for (int at = 0; at < 2 * it.n; ++at, r.next(C::NR), s.next(C::NS)) {
             const auto [j, kind] = item_tile(it, at);
-            const int valid = it.left - j * AT_UNIT, fs = (unit + j) % FAC;
+            if (kind != group)
+                continue;
+            const int fs = (unit + j) % FAC;
             if (!(tile_wait_warp(&sh.f_full[fs], ((unit + j) / FAC) & 1, limit, sh) &&
                   tile_wait_warp(&sh.raw_full[r.slot], r.phase, limit, sh) &&
                   tile_wait_warp(&sh.kv_empty[s.slot], s.phase ^ 1, limit, sh)))
                 return;
-            convert(raw + r.slot * C::RAW, kv + s.slot * C::TILE, sh.fac[fs][kind], valid);
+            convert(raw + r.slot * C::RAW, kv + s.slot * C::TILE, sh.fac[fs][kind], it.left - j * AT_UNIT);
             async_fence();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&sh.kv_full[s.slot]);
                 mbar_arrive(&sh.raw_empty[r.slot]);
-                if (kind)
-                    mbar_arrive(&sh.f_empty[fs]);
+                mbar_arrive(&sh.f_empty[fs]);
             }
-            r.next(C::NR);
-            s.next(C::NS);
         }
     }
 }
@@ -928,7 +971,7 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
         }
         for (int k = 0; k < FAC; ++k) {
             mbar_init(&sh.f_full[k], 1);
-            mbar_init(&sh.f_empty[k], 4);
+            mbar_init(&sh.f_empty[k], 8);
         }
         mbar_init(&sh.drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;\n\tfence.proxy.async.shared::cta;" ::: "memory");
@@ -982,7 +1025,7 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
         } else if (Q8 && warp == W_SCALE) {
             scale_role(P, sh, limit);
         } else if (Q8 && warp >= W_CVT) {
-            convert_role<D>(P, sh, tiles, raw, kv, limit);
+            convert_role<D>(P, sh, (warp - W_CVT) / 4, tiles, raw, kv, limit);
         }
     }
     __syncwarp();
@@ -1015,7 +1058,8 @@ EncodeTiled encode_tiled()
 }
 
 // A map over a row-major array of `rank` dimensions (innermost first); boxes
-// of bfloat16 are 64 wide with 128-byte swizzle, boxes of codes a whole head.
+// of bfloat16 are 64 wide with 128-byte swizzle, boxes of codes a whole head
+// (swizzled too where that is 128 bytes).
 bool make_map(CUtensorMap *map, bool codes, const void *base, int rank, const cuuint64_t *dim, const cuuint32_t *box)
 {
     cuuint64_t stride[4];
@@ -1027,7 +1071,7 @@ bool make_map(CUtensorMap *map, bool codes, const void *base, int rank, const cu
     const cuuint32_t one[5] = {1, 1, 1, 1, 1};
     return encode_tiled()(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
                           const_cast<void *>(base), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                          codes && box[0] < 128 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
