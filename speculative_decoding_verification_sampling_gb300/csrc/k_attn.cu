@@ -15,8 +15,8 @@
 //
 // Two launches: the tile kernel (k_attn_tiles.cu) works on the prefix and the
 // caches and leaves partial results, each a reference exponent m, a sum l and
-// weighted values o of a row over some of its entries.  The kernel here, one
-// warp per row, attends to the staged entries (no partial result is awaited
+// weighted values o of a row over some of its entries.  The kernel here, four
+// rows per warp, attends to the staged entries (no partial result is awaited
 // for that, so it overlaps the tile kernel's tail), joins the partial results
 // (sums of 2^(m - max) l and 2^(m - max) o) and writes the row.
 #include <cstdint>
@@ -24,156 +24,223 @@
 #include <cuda_runtime.h>
 
 #include "sv_attn.cuh"
+#include "sv_cluster.cuh"
 #include "sv_fp8.cuh"
 #include "sv_launch.h"
 
 namespace sv {
 namespace {
 
-constexpr int RW = 4;   // rows (warps) of a row CTA
+constexpr int FW = 4;   // warps of a CTA
 
-// N = 2 or 4 elements of a bfloat16 row
-template <int N>
-__device__ __forceinline__ void load_bf16(const uint16_t *p, float *x)
+// E = D / 8 elements of a row per lane, as pairs: lane s of the row's eight
+// holds elements 8 s .. 8 s + 7 and, with E = 16, the same 64 further on (every
+// load of the row's lanes is contiguous).
+template <int E>
+struct RawRow {
+    uint32_t w[E / 2];
+};
+template <int E>
+__device__ __forceinline__ RawRow<E> load_row(const uint16_t *p)
 {
-    uint32_t w[N / 2];
-    if constexpr (N == 4) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
-        w[0] = v.x, w[1] = v.y;
-    } else {
-        w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
-    }
+    RawRow<E> r;
 #pragma unroll
-    for (int k = 0; k < N / 2; ++k) {
-        x[2 * k] = __uint_as_float(w[k] << 16);
-        x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    for (int k = 0; k < E / 8; ++k) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p + k * 64));
+        r.w[4 * k] = v.x, r.w[4 * k + 1] = v.y, r.w[4 * k + 2] = v.z, r.w[4 * k + 3] = v.w;
+    }
+    return r;
+}
+template <int E>
+__device__ __forceinline__ f2 pair_of(const RawRow<E> &r, int k)
+{
+    return pku(r.w[k] << 16, r.w[k] & 0xffff0000u);
+}
+// E float32 of a partial result's row
+template <int E>
+__device__ __forceinline__ void load_values(const float *p, float (&y)[E])
+{
+#pragma unroll
+    for (int k = 0; k < E / 4; ++k) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + (k >> 1) * 64 + (k & 1) * 4));
+        y[4 * k] = v.x, y[4 * k + 1] = v.y, y[4 * k + 2] = v.z, y[4 * k + 3] = v.w;
     }
 }
 
-// One warp per query row.
+// Eight lanes per query row: a warp works on four heads of a token, and the
+// index arithmetic and the loops over what they see serve four rows (244k rows:
+// 74 us; 147 us with a warp per row, and no faster for a thousand rows).
 template <int D>
-__global__ void __launch_bounds__(RW * 32)
-    va_finish(const __grid_constant__ AttnParams P, const __grid_constant__ AttnWork W, int ctas)
+__global__ void __launch_bounds__(FW * 32)
+    va_finish(const __grid_constant__ AttnParams P, const __grid_constant__ AttnWork W, int ctas, int per_token)
 {
-    constexpr int N = D / 32;   // elements per lane
+    constexpr int LPR = 8, E = D / LPR, NP = E / 2, AT = 8;
     const float inf = __int_as_float(0x7f800000), nan = __int_as_float(0x7fc00000);
-    const int lane = threadIdx.x & 31;
-    const long long r = (long long)blockIdx.x * RW + threadIdx.x / 32;
-    const bool real = r < (long long)P.B * P.T * P.Hq;
-    const int hq = real ? (int)(r % P.Hq) : 0, h = hq / P.G, g = hq % P.G;
-    const long long bt = real ? r / P.Hq : 0;
-    const int t = (int)(bt % P.T), b = (int)(bt / P.T);
+    const int lane = threadIdx.x & 31, sub = lane % LPR;
+    const int bt = blockIdx.x / per_token;
+    const int hq = (blockIdx.x - bt * per_token) * (FW * 32 / LPR) + threadIdx.x / LPR;
+    const bool real = hq < P.Hq;
+    const int h = real ? hq / P.G : 0, g = real ? hq - h * P.G : 0;
+    const int b = bt / P.T, t = bt - b * P.T;
+    const size_t r = (size_t)bt * P.Hq + (real ? hq : 0);
     const int len = __ldg(P.len + b);
     const bool bad = len < 0 || len > P.L;
-    float o[N] = {}, m = -inf, l = 0.0f;
-    if (real && P.staged && !bad) {
-        float q[N];
-        load_bf16<N>(static_cast<const uint16_t *>(P.q) + (size_t)r * D + lane * N, q);
+    f2 o[NP];
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-            q[k] *= P.c;
+    for (int k = 0; k < NP; ++k)
+        o[k] = pk(0.0f, 0.0f);
+    float m = -inf, l = 0.0f;
+    // joins n scores (-inf: none) and their values
+    auto rescale = [&](float top) {
+        const float mn = fmaxf(m, top), ref = mn == -inf ? 0.0f : mn, f = ex2a(m - ref);
+        const f2 ff = pk(f, f);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int k = 0; k < NP; ++k)
+            o[k] = mul2(o[k], ff);
+        return ref;
+    };
+    if (P.staged && !bad) {
+        f2 q[NP];
+        {
+            const RawRow<E> raw = load_row<E>(static_cast<const uint16_t *>(P.q) + r * D + sub * AT);
+            const f2 cc = pk(P.c, P.c);
+#pragma unroll
+            for (int k = 0; k < NP; ++k)
+                q[k] = mul2(pair_of<E>(raw, k), cc);
+        }
         const uint8_t *mask = P.mask ? P.mask + (size_t)bt * P.T : nullptr;
-        const uint16_t *x = static_cast<const uint16_t *>(P.staged);
-        for (int j = 0; j < P.T; ++j) {
-            if (mask ? !__ldg(mask + j) : j > t)
-                continue;
-            const size_t at = ((size_t)b * P.T + j) * 2 * P.H * D + (size_t)h * D + lane * N;
-            float kx[N], vx[N];
-            load_bf16<N>(x + at, kx);
-            load_bf16<N>(x + at + (size_t)P.H * D, vx);
-            float s = 0.0f;
+        const size_t step = (size_t)2 * P.H * D;
+        const uint16_t *x = static_cast<const uint16_t *>(P.staged) + (size_t)b * P.T * step + (size_t)h * D + sub * AT;
+        const int end = mask ? P.T : t + 1;
+        for (int j0 = 0; j0 < end; j0 += 32) {
+            const int j = j0 + lane;
+            unsigned seen = __ballot_sync(0xffffffffu, j < end && (!mask || __ldg(mask + j)));
+            while (seen) {
+                // two visible entries at a time
+                const int ja = __ffs(seen) - 1;
+                seen &= seen - 1;
+                const bool two = seen != 0;
+                const int jb = two ? __ffs(seen) - 1 : ja;
+                seen &= seen - 1;
+                const uint16_t *ea = x + (size_t)(j0 + ja) * step, *eb = x + (size_t)(j0 + jb) * step;
+                const RawRow<E> ka = load_row<E>(ea), kb = load_row<E>(eb);
+                const RawRow<E> va = load_row<E>(ea + (size_t)P.H * D), vb = load_row<E>(eb + (size_t)P.H * D);
+                f2 da = pk(0.0f, 0.0f), db = da;
 #pragma unroll
-            for (int k = 0; k < N; ++k)
-                s = fmaf(q[k], kx[k], s);
+                for (int k = 0; k < NP; ++k) {
+                    da = fma2(q[k], pair_of<E>(ka, k), da);
+                    db = fma2(q[k], pair_of<E>(kb, k), db);
+                }
+                float a0, a1, b0, b1;
+                upk(da, a0, a1);
+                upk(db, b0, b1);
+                float sa = a0 + a1, sb = b0 + b1;
 #pragma unroll
-            for (int w = 16; w; w >>= 1)
-                s += __shfl_xor_sync(0xffffffffu, s, w);
-            const float mn = fmaxf(m, s), ref = mn == -inf ? 0.0f : mn;
-            const float f = exp2f(m - ref), p = exp2f(s - ref);
-            m = mn;
-            l = l * f + p;
+                for (int w = LPR / 2; w; w >>= 1) {
+                    sa += __shfl_xor_sync(0xffffffffu, sa, w);
+                    sb += __shfl_xor_sync(0xffffffffu, sb, w);
+                }
+                const float ref = rescale(two ? fmaxf(sa, sb) : sa);
+                const float pa = ex2a(sa - ref), pb = two ? ex2a(sb - ref) : 0.0f;
+                l += pa + pb;
+                const f2 wa = pk(pa, pa), wb = pk(pb, pb);
 #pragma unroll
-            for (int k = 0; k < N; ++k)
-                o[k] = fmaf(p, vx[k], o[k] * f);
+                for (int k = 0; k < NP; ++k) {
+                    o[k] = fma2(wa, pair_of<E>(va, k), o[k]);
+                    if (two)
+                        o[k] = fma2(wb, pair_of<E>(vb, k), o[k]);
+                }
+            }
         }
     }
     int code = bad ? 1 : 0;
     if (ctas > 0) {
         asm volatile("griddepcontrol.wait;" ::: "memory");   // the tile kernel's results
-        if (real && !bad) {
+        if (!bad) {
             // where this row's partial results are: over the prefix, then over its cache
             const int HS = P.H * W.own.tiles, UP = W.ppairs * W.pu;
             const long long U = UP + (long long)HS * __ldcg(W.base + P.B);
-            auto owner = [&](int u) { return attn_owner(u, U, ctas); };
+            const int before = __ldcg(W.base + b);
             int cnt0 = 0, c0 = 0, pair0 = 0, grp0 = 0, row0 = 0, cnt1 = 0, c1 = 0, pair1 = 0, grp1 = 0, row1 = 0;
-            const int per0 = 2 - W.pre.two, per1 = 2 - W.own.two;   // partial results per CTA
             if (W.ppairs) {
-                const int wide = W.pre.tq * (1 + W.pre.two), in = (int)(bt % wide);
-                pair0 = h * W.pre.tiles + (int)(bt / wide);
-                grp0 = in / W.pre.tq;
-                row0 = (in % W.pre.tq) * P.G + g;
-                c0 = owner(pair0 * W.pu);
-                cnt0 = (owner((pair0 + 1) * W.pu - 1) - c0 + 1) * per0;
+                const int wide = W.pre.tq * (1 + W.pre.two), tile = bt / wide, in = bt - tile * wide;
+                pair0 = h * W.pre.tiles + tile;
+                grp0 = in >= W.pre.tq;
+                row0 = (in - grp0 * W.pre.tq) * P.G + g;
+                c0 = attn_owner(pair0 * W.pu, U, ctas);
+                cnt0 = (attn_owner((pair0 + 1) * W.pu - 1, U, ctas) - c0 + 1) << (1 - W.pre.two);
             }
             if (len > 0) {
-                const int wide = W.own.tq * (1 + W.own.two), in = t % wide, ub = (len + AT_UNIT - 1) / AT_UNIT;
-                const int i = h * W.own.tiles + t / wide, u = UP + __ldcg(W.base + b) * HS + i * ub;
+                const int wide = W.own.tq * (1 + W.own.two), tile = t / wide, in = t - tile * wide;
+                const int ub = (len + AT_UNIT - 1) / AT_UNIT, i = h * W.own.tiles + tile, u = UP + before * HS + i * ub;
                 pair1 = b * HS + i;
-                grp1 = in / W.own.tq;
-                row1 = (in % W.own.tq) * P.G + g;
-                c1 = owner(u);
-                cnt1 = (owner(u + ub - 1) - c1 + 1) * per1;
+                grp1 = in >= W.own.tq;
+                row1 = (in - grp1 * W.own.tq) * P.G + g;
+                c1 = attn_owner(u, U, ctas);
+                cnt1 = (attn_owner(u + ub - 1, U, ctas) - c1 + 1) << (1 - W.own.two);
             }
-            const int all = cnt0 + cnt1;
-            for (int i0 = 0; i0 < all; i0 += 32) {
-                // lane i looks up partial result i0 + i, then all lanes read its values
-                const int n = min(32, all - i0);
-                const bool own = i0 + lane >= cnt0;
-                const int i = i0 + lane - (own ? cnt0 : 0), per = own ? per1 : per0;
+            const int all = cnt0 + cnt1;   // may differ between the warp's rows
+            for (int i0 = 0; __any_sync(0xffffffffu, i0 < all); i0 += LPR) {
+                // lane i of a row looks up partial result i0 + i, then its lanes read the values
+                const bool own = i0 + sub >= cnt0;
+                const int i = i0 + sub - (own ? cnt0 : 0), two = own ? W.own.two : W.pre.two;
                 float pm = -inf, pl = 0.0f;
-                const float *src = nullptr;
+                size_t at = 0;
                 bool gave_up = false;
-                if (lane < n) {
-                    const int c = (own ? c1 : c0) + i / per;
-                    const int gr = per == 2 ? i % 2 : own ? grp1 : grp0;
+                if (i0 + sub < all) {
+                    // with one set of rows, both groups of a CTA leave one
+                    const int c = (own ? c1 : c0) + (two ? i : i >> 1);
+                    const int gr = two ? (own ? grp1 : grp0) : i & 1;
                     const int rows = (own ? W.own.tq : W.pre.tq) * P.G;
-                    const size_t at = ((size_t)(c + (own ? pair1 : pair0)) * 2 + gr) * rows + (own ? row1 : row0);
+                    at = ((size_t)(c + (own ? pair1 : pair0)) * 2 + gr) * rows + (own ? row1 : row0);
                     const float2 ml = __ldcg((own ? W.ml_s : W.ml_p) + at);
                     pm = ml.x;
                     pl = ml.y;
-                    src = (own ? W.o_s : W.o_p) + at * D;
                     gave_up = __ldcg(W.stat + c) != 0;
                 }
-                if (__any_sync(0xffffffffu, gave_up)) {
+                if (__any_sync(0xffffffffu, gave_up))
                     code = 7;
-                    break;
-                }
+                const float *src = (own ? W.o_s : W.o_p) + at * D;
                 float top = pm;
 #pragma unroll
-                for (int w = 16; w; w >>= 1)
+                for (int w = LPR / 2; w; w >>= 1)
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-                const float mn = fmaxf(m, top), ref = mn == -inf ? 0.0f : mn;
-                const float f = exp2f(m - ref), wt = pl == 0.0f ? 0.0f : exp2f(pm - ref);
+                const float ref = rescale(top);
+                // a partial result over no entries has no values
+                const float wt = pl == 0.0f ? 0.0f : ex2a(pm - ref);
                 float add = wt == 0.0f ? 0.0f : wt * pl;
 #pragma unroll
-                for (int w = 16; w; w >>= 1)
+                for (int w = LPR / 2; w; w >>= 1)
                     add += __shfl_xor_sync(0xffffffffu, add, w);
-                m = mn;
-                l = l * f + add;
+                l += add;
+                // the partial results that some row of the warp has
+                unsigned have = __ballot_sync(0xffffffffu, wt != 0.0f);
+                have = (have | have >> 8 | have >> 16 | have >> 24) & 0xffu;
+                while (have) {
+                    // the values of four at a time are in flight
+                    float wj[4], y[4][E];
 #pragma unroll
-                for (int k = 0; k < N; ++k)
-                    o[k] *= f;
-                for (int j = 0; j < n; ++j) {
-                    const float wj = __shfl_sync(0xffffffffu, wt, j);
-                    const float *sj = reinterpret_cast<const float *>(
-                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), j));
-                    if (wj == 0.0f)
-                        continue;   // its values are not written when it has no entries
+                    for (int n = 0; n < 4; ++n) {
+                        const int j = have ? __ffs(have) - 1 : 0;
+                        const float w = __shfl_sync(0xffffffffu, wt, j, LPR);
+                        const float *sj = reinterpret_cast<const float *>(
+                            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), j, LPR));
+                        wj[n] = have ? w : 0.0f;
+                        have &= have - 1;
 #pragma unroll
-                    for (int k = 0; k < N; k += 2) {
-                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(sj + lane * N + k));
-                        o[k] = fmaf(wj, v.x, o[k]);
-                        o[k + 1] = fmaf(wj, v.y, o[k + 1]);
+                        for (int k = 0; k < E; ++k)
+                            y[n][k] = 0.0f;
+                        if (wj[n] != 0.0f)
+                            load_values<E>(sj + sub * AT, y[n]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const f2 ww = pk(wj[n], wj[n]);
+#pragma unroll
+                        for (int k = 0; k < NP; ++k)
+                            o[k] = fma2(ww, pk(y[n][2 * k], y[n][2 * k + 1]), o[k]);
                     }
                 }
             }
@@ -181,34 +248,39 @@ __global__ void __launch_bounds__(RW * 32)
     }
     if (!real)
         return;
-    if (code && lane == 0 && P.status)
+    if (code && sub == 0 && P.status)
         atomicCAS(P.status, 0, code);
     const float inv = code ? nan : l == 0.0f ? 0.0f : 1.0f / l;
-    uint16_t *out = static_cast<uint16_t *>(P.out) + (size_t)r * D + lane * N;
+    uint16_t *out = static_cast<uint16_t *>(P.out) + r * D + sub * AT;
+    uint32_t w[NP];
 #pragma unroll
-    for (int k = 0; k < N; k += 2)
-        *reinterpret_cast<uint32_t *>(out + k) = pack_bf16(o[k] * inv, o[k + 1] * inv);
-    if (P.lse && lane == 0)
+    for (int k = 0; k < NP; ++k) {
+        float lo, hi;
+        upk(o[k], lo, hi);
+        w[k] = pack_bf16(lo * inv, hi * inv);
+    }
+#pragma unroll
+    for (int k = 0; k < E / 8; ++k)
+        *reinterpret_cast<uint4 *>(out + k * 64) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    if (P.lse && sub == 0)
         P.lse[r] = code ? nan : 0.6931471805599453f * (m + log2f(l));
 }
 
 template <int D>
-cudaError_t finish(const AttnParams &P, const AttnWork &W, int ctas, unsigned grid, cudaStream_t stream)
+cudaError_t finish(const AttnParams &P, const AttnWork &W, int ctas, cudaStream_t stream)
 {
-    if (ctas == 0) {
-        va_finish<D><<<grid, RW * 32, 0, stream>>>(P, W, 0);
-        return cudaGetLastError();
-    }
+    constexpr int rows = FW * 4;
+    const int per_token = (P.Hq + rows - 1) / rows;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(RW * 32);
+    cfg.gridDim = dim3((unsigned)(P.B * P.T * per_token));
+    cfg.blockDim = dim3(FW * 32);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, va_finish<D>, P, W, ctas);
+    cfg.numAttrs = ctas > 0 ? 1 : 0;   // behind the tile kernel; alone it starts like any other
+    return cudaLaunchKernelEx(&cfg, va_finish<D>, P, W, ctas, per_token);
 }
 
 }  // namespace
@@ -256,8 +328,7 @@ cudaError_t launch_attention(const AttnParams &P, bool quant, void *workspace, i
             return e;
         ++*launches;
     }
-    const unsigned grid = (unsigned)(((long long)P.B * P.T * P.Hq + RW - 1) / RW);
-    const cudaError_t e = P.D == 128 ? finish<128>(P, W, ctas, grid, stream) : finish<64>(P, W, ctas, grid, stream);
+    const cudaError_t e = P.D == 128 ? finish<128>(P, W, ctas, stream) : finish<64>(P, W, ctas, stream);
     if (e == cudaSuccess)
         ++*launches;
     return e;

@@ -28,7 +28,7 @@ namespace sv {
 namespace {
 
 constexpr int QT = 256;   // threads of a CTA
-constexpr int QU = 4;     // pieces in flight per thread
+constexpr int QU = 4;     // pieces in flight per thread (of a piece: 8 elements)
 
 // ---------------------------------------------------------------- commit
 __device__ __forceinline__ int commit_count(const KvQuantParams &P, int b)
@@ -43,43 +43,60 @@ __device__ __forceinline__ int commit_count(const KvQuantParams &P, int b)
     return (int)m;
 }
 
+// Eight elements as they lie in memory.
 template <class E>
-__device__ __forceinline__ void load_piece(const void *src, size_t at, float (&x)[8], uint32_t &top)
+struct Piece {
+    uint32_t w[2 * sizeof(E)];
+};
+template <class E>
+__device__ __forceinline__ Piece<E> load_piece(const void *src, size_t at)
 {
-    // eight elements and the largest of their absolute values' bits
-    if constexpr (sizeof(E) == 2) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(src) + at));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t m = 0;
+    Piece<E> x;
+    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const E *>(src) + at);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            m = __vmaxu2(m, w[k] & 0x7fff7fffu);
-            x[2 * k] = __uint_as_float(w[k] << 16);
-            x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-        }
-        top = max(m << 16, m & 0xffff0000u);
+    for (int k = 0; k < (int)sizeof(E) / 2; ++k) {
+        const uint4 v = __ldcs(p + k);   // read once
+        x.w[4 * k] = v.x, x.w[4 * k + 1] = v.y, x.w[4 * k + 2] = v.z, x.w[4 * k + 3] = v.w;
+    }
+    return x;
+}
+// The largest of the absolute values' float32 bits.
+template <class E>
+__device__ __forceinline__ uint32_t piece_top(const Piece<E> &x)
+{
+    uint32_t m = 0;
+    if constexpr (sizeof(E) == 2) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            m = __vmaxu2(m, x.w[k] & 0x7fff7fffu);
+        return max(m << 16, m & 0xffff0000u);
     } else {
-        const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(src) + at);
-        const float4 lo = __ldg(s), hi = __ldg(s + 1);
-        x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w;
-        x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
-        top = 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            top = max(top, __float_as_uint(x[k]) & 0x7fffffffu);
+            m = max(m, x.w[k] & 0x7fffffffu);
+        return m;
     }
 }
+template <class E>
+__device__ __forceinline__ float piece_at(const Piece<E> &x, int k)
+{
+    if constexpr (sizeof(E) == 2)
+        return __uint_as_float((k & 1) ? x.w[k / 2] & 0xffff0000u : x.w[k / 2] << 16);
+    else
+        return __uint_as_float(x.w[k]);
+}
 
+// One CTA per (layer, sequence): its committed entries, QU pieces in flight
+// per thread.
 template <class E, int D>
-__global__ void __launch_bounds__(QT) kvq_commit(const __grid_constant__ KvQuantParams P)
+__global__ void __launch_bounds__(QT, sizeof(E) == 2 ? 6 : 4) kvq_commit(const __grid_constant__ KvQuantParams P)
 {
     constexpr int G = D / 8;   // lanes of a head
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && threadIdx.x == 0 && P.status)
         *P.status = 0;   // only the length update, after this launch, reports
-    const int ch = blockIdx.x % P.nch;
-    const long long lb = blockIdx.x / P.nch;   // layer * B + b
-    const int b = (int)(lb % P.B);
+    const size_t lb = blockIdx.x;   // layer * B + b
+    const int b = (int)(lb % (unsigned)P.B);
     const int n = commit_count(P, b);
     if (n <= 0)
         return;
@@ -91,46 +108,45 @@ __global__ void __launch_bounds__(QT) kvq_commit(const __grid_constant__ KvQuant
         if (__syncthreads_or(bad))
             return;
     }
-    const int per = 2 * P.H * G;                 // pieces of an entry
-    const int total = n * per;                   // a multiple of G: heads never end inside a lane group
-    const int p0 = ch * QT * QU;
-    if (p0 >= total)
-        return;
+    const unsigned per = 2 * P.H * G;            // pieces of an entry
+    const unsigned total = n * per;              // a multiple of G: heads never end inside a lane group
     const size_t entry = (size_t)2 * P.H * D;    // elements of an entry
-    const size_t src0 = (size_t)lb * P.K, dst0 = (size_t)lb * P.L + P.len[b];
-    float x[QU][8];
-    uint32_t top[QU];
-    int ent[QU], off[QU];
+    const size_t src0 = lb * P.K, dst0 = lb * P.L + P.len[b];
+    for (unsigned p0 = threadIdx.x; p0 - threadIdx.x < total; p0 += QT * QU) {
+        Piece<E> x[QU];
+        uint32_t top[QU];
 #pragma unroll
-    for (int u = 0; u < QU; ++u) {
-        const int p = p0 + u * QT + threadIdx.x;
-        ent[u] = -1;
-        top[u] = 0;
-        off[u] = 0;
-        if (p < total) {
-            const int i = p / per;
-            off[u] = p - i * per;
-            ent[u] = i;
-            const int s = (nodes && i >= P.lead) ? __ldg(nodes + i - P.lead) : i;
-            load_piece<E>(P.staged, (src0 + s) * entry + (size_t)off[u] * 8, x[u], top[u]);
+        for (int u = 0; u < QU; ++u) {
+            const unsigned p = p0 + u * QT;
+            if (p < total) {
+                const unsigned i = p / per;
+                const int s = (nodes && (int)i >= P.lead) ? __ldg(nodes + i - P.lead) : (int)i;
+                x[u] = load_piece<E>(P.staged, (src0 + s) * entry + (size_t)(p - i * per) * 8);
+            } else {
+                x[u] = Piece<E>{};
+            }
         }
-    }
 #pragma unroll
-    for (int u = 0; u < QU; ++u) {
+        for (int u = 0; u < QU; ++u) {
+            top[u] = piece_top<E>(x[u]);
 #pragma unroll
-        for (int o = G / 2; o; o >>= 1)
-            top[u] = max(top[u], __shfl_xor_sync(0xffffffffu, top[u], o));
-        if (ent[u] < 0)
-            continue;
-        float inv;
-        const uint32_t byte = fp8_scale(top[u], inv);
-        uint2 c;
-        c.x = pack_e4m3(x[u][0] * inv, x[u][1] * inv, x[u][2] * inv, x[u][3] * inv);
-        c.y = pack_e4m3(x[u][4] * inv, x[u][5] * inv, x[u][6] * inv, x[u][7] * inv);
-        const size_t e = dst0 + ent[u];
-        *reinterpret_cast<uint2 *>(P.cache + e * entry + (size_t)off[u] * 8) = c;
-        if (off[u] % G == 0)
-            P.scale[e * (2 * P.H) + off[u] / G] = (uint8_t)byte;
+            for (int o = G / 2; o; o >>= 1)
+                top[u] = max(top[u], __shfl_xor_sync(0xffffffffu, top[u], o));
+            const unsigned p = p0 + u * QT;
+            if (p >= total)
+                continue;
+            float inv;
+            const uint32_t byte = fp8_scale(top[u], inv);
+            float y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                y[k] = piece_at<E>(x[u], k) * inv;
+            // entries follow one another in the cache as the pieces do
+            *reinterpret_cast<uint2 *>(P.cache + dst0 * entry + (size_t)p * 8) =
+                make_uint2(pack_e4m3(y[0], y[1], y[2], y[3]), pack_e4m3(y[4], y[5], y[6], y[7]));
+            if (p % G == 0)
+                P.scale[dst0 * (2 * P.H) + p / G] = (uint8_t)byte;
+        }
     }
 }
 
@@ -243,8 +259,7 @@ long long kvq_chunks(int K, int H, int D)
 
 cudaError_t launch_kvq_commit(KvQuantParams P, bool wide, cudaStream_t stream, int *launches)
 {
-    P.nch = (int)kvq_chunks(P.K, P.H, P.D);
-    const unsigned grid = (unsigned)((long long)P.NL * P.B * P.nch);
+    const unsigned grid = (unsigned)((long long)P.NL * P.B);
     *launches = 0;
     const cudaError_t e = wide ? commit_any<float>(P, grid, stream) : commit_any<__nv_bfloat16>(P, grid, stream);
     if (e != cudaSuccess)

@@ -86,8 +86,12 @@ __device__ __forceinline__ int attn_start(int c, long long U, int ctas)
 }
 __device__ __forceinline__ int attn_owner(int u, long long U, int ctas)
 {
-    const long long n = U < ctas ? U : ctas;
-    return (int)((((long long)u + 1) * n - 1) / U);
+    // the largest c with c U < (u + 1) n, from an estimate that is off by one at most
+    const long long n = U < ctas ? U : ctas, x = ((long long)u + 1) * n;
+    int c = (int)__fdividef((float)x, (float)U);
+    c -= c * U >= x;
+    c += (c + 1) * U < x;
+    return c;
 }
 
 // Device view of the plan.
