@@ -19,18 +19,21 @@
 // partial result each.  A loader thread feeds a ring of K and V tiles with
 // TMA; one warp issues every tcgen05.mma.
 //
-// Entries in 8 bits are copied as they are, and four more warps turn them into
-// float16, in the swizzled layout that TMA would have written: one conversion
-// and one multiplication for two codes, where bfloat16 would take six
-// operations.  float16 holds a code times 2^s exactly for s in [-15, 7], so
-// the scales of a unit are taken relative to its largest, which becomes 2^7;
-// heads whose scale is more than 2^22 below it lose their last bits (at 2^-40
-// of the unit's largest element).  What the largest stands for goes back in
-// per unit, exactly: into the scores as a factor, and for V into the exponent
-// of the weights (they are 2^(c S + bv - m), and l takes them times 2^-bv).
-// Q becomes float16 too, each row times a power of two that puts its largest
-// element in [2^14, 2^15): exact for elements down to 2^-32 of it.  P is
-// rounded to float16, 2^-11 of a weight.
+// Entries in 8 bits.  What such a kernel has least of is shared-memory
+// bandwidth: turning a tile of codes into 16-bit numbers reads and writes three
+// times its bytes there.  So K's codes go to the tensor cores as they are
+// (kind::f8f6f4), and Q meets them as a sum of two e4m3 numbers: each row times
+// a power of two that puts its largest element in (224, 448], then rounded, and
+// the remainder rounded again.  That is exact for elements down to 2^-10 of
+// the row's largest, and off by 2^-18 of the largest at most.  The scales of
+// K's rows multiply the columns of S.  V's codes become float16, by four warps,
+// in the layout that TMA would have written, with scales relative to the
+// unit's largest, which becomes 2^7: float16 holds a code times 2^s exactly
+// for s in [-15, 7], and a head whose scale is more than 2^22 below loses its
+// last bits (at 2^-40 of the unit's largest element).  What the largest stands
+// for goes back in exactly, into the exponent of the weights (they are
+// 2^(c S + bv - m), and l takes them times 2^-bv).  P is rounded to float16
+// here, 2^-11 of a weight.
 //
 // The last unit of a stretch is ragged: scores past its end become -inf, and
 // V's rows past it are zeroed in shared memory, since 0 * NaN would reach O.
@@ -65,29 +68,40 @@ __device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap *map, uns
                  : "memory");
 }
 
-// Shared-memory operand with 128-byte rows and 128-byte swizzle: the low word
-// holds the start address and the leading offset, the high word the stride
-// offset (1024: eight rows), all in 16-byte units, descriptor version 1 and
-// swizzle code 2.  The issuing thread keeps to 32-bit additions on the low
+// Shared-memory operand, swizzled: the low word holds the start address and
+// the leading offset, the high word the stride offset (eight rows), all in
+// 16-byte units, descriptor version 1 and the swizzle code (2: rows of 128
+// bytes, 4: of 64).  The issuing thread keeps to 32-bit additions on the low
 // word: its own instructions are what the tensor cores wait for otherwise.
-constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t DESC_128 = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t DESC_64 = (512u >> 4) | (1u << 14) | (4u << 29);
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead)
 {
     return ((addr & 0x3ffffu) >> 4) | ((lead >> 4) << 16);
 }
-// Instruction descriptor: bfloat16 or float16 operands, float32 accumulator,
-// M = 128.
-__host__ __device__ constexpr uint32_t mma_desc(int n, bool b_mn_major, bool half)
+// Instruction descriptor: A and B both bfloat16, float16 (kind::f16) or e4m3
+// (kind::f8f6f4), float32 accumulator, M = 128.
+enum MmaType { MMA_F16 = 0, MMA_E4M3 = 0, MMA_BF16 = 1 };
+__host__ __device__ constexpr uint32_t mma_desc(int n, bool b_mn_major, MmaType type)
 {
-    return (1u << 4) | (half ? 0u : (1u << 7) | (1u << 10)) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
-           ((128u >> 4) << 24);
+    return (1u << 4) | ((uint32_t)type << 7) | ((uint32_t)type << 10) | ((b_mn_major ? 1u : 0u) << 16) |
+           ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
 {
     asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
                  "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(DESC_HI)
+                 "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(DESC_128)
+                 : "memory");
+}
+template <uint32_t B_HI>
+__device__ __forceinline__ void mma_ss8(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %6};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(DESC_128), "r"(B_HI)
                  : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
@@ -95,7 +109,7 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
     asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
                  "mov.b64 db, {%2, %5};\n\t"
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(DESC_HI)
+                 "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(DESC_128)
                  : "memory");
 }
 __device__ __forceinline__ void mma_commit(unsigned long long *bar)
@@ -114,6 +128,10 @@ __device__ __forceinline__ bool elect_one()
 }
 // A value that all lanes hold, made known as such.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ void mbar_arrive_n(unsigned long long *bar, uint32_t n)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(bar)), "r"(n) : "memory");
+}
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -133,21 +151,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float *x)
                  "tcgen05.wait::ld.sync.aligned;"
                  : R32(OUT, 0)
                  : "r"(addr)
-                 : "memory");
-#undef OUT
-}
-__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&x)[64])
-{
-#define OUT(i) "=f"(x[i])
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%64];\n\t"
-                 "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-                 "{%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-                 "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%65];\n\t"
-                 "tcgen05.wait::ld.sync.aligned;"
-                 : R32(OUT, 0), R32(OUT, 32)
-                 : "r"(addr), "r"(addr + 32)
                  : "memory");
 #undef OUT
 }
@@ -194,46 +197,48 @@ __device__ __forceinline__ void store8(float *p, const float *x)
 // ------------------------------------------------------------------ layout
 template <int D, bool Q8>
 struct TileCfg {
-    static constexpr uint32_t TILE = 128 * D * 2;     // a bfloat16 tile: 128 rows of D, in blocks of 64 columns
-    static constexpr uint32_t BLOCK = 128 * 128;      // one such block: 128 rows of 128 bytes
-    static constexpr uint32_t RAW = 128 * D;          // a tile of codes
-    static constexpr int NS = Q8 ? (D == 128 ? 3 : 5) : (D == 128 ? 4 : 8);   // K / V tiles in flight
-    static constexpr int NR = Q8 ? (D == 128 ? 4 : 8) : 0;                    // tiles of codes in flight
-    static constexpr int THREADS = Q8 ? 640 : 384;
+    static constexpr uint32_t TILE = 128 * D * 2;            // a 16-bit tile: 128 rows of D, in blocks of 64 columns
+    static constexpr uint32_t BLOCK = 128 * 128;             // one such block: 128 rows of 128 bytes
+    static constexpr uint32_t RAW = 128 * D;                 // a tile of codes
+    static constexpr uint32_t KT = Q8 ? RAW : TILE;          // K as the tensor cores read it
+    static constexpr int NK = D == 128 ? 3 : 6;              // tiles in flight: K, V, V's codes
+    static constexpr int NV = D == 128 ? 2 : Q8 ? 4 : 6;
+    static constexpr int NR = Q8 ? (D == 128 ? 2 : 4) : 0;
+    static constexpr uint32_t K0 = 2 * TILE, V0 = K0 + NK * KT, R0 = V0 + NV * TILE;   // behind two Q tiles
+    static constexpr uint32_t TILES = R0 + NR * RAW;         // TileShared lies behind them
+    static constexpr int THREADS = Q8 ? 512 : 384;
     // registers per thread: at launch, then of the softmax groups and of the
     // other warpgroups (their sum over the warpgroups stays within the launch's)
-    static constexpr int REGS = Q8 ? 96 : 168, REGS_SOFT = Q8 ? 120 : 208, REGS_REST = 80;
-    // columns of S that a softmax thread holds at a time: the 8-bit kernel's eight converting
-    // warps leave it registers for half a row, which it reads twice
-    static constexpr int COLS = Q8 ? 64 : 128;
+    static constexpr int REGS = Q8 ? 128 : 168, REGS_SOFT = Q8 ? 176 : 208, REGS_REST = 80;
     static_assert(2 * REGS_SOFT + (THREADS / 128 - 2) * REGS_REST <= THREADS / 128 * REGS, "register split");
-    static constexpr uint32_t TILES = 2 * TILE + NS * TILE + NR * RAW;   // TileShared lies behind them
 };
 
-constexpr int W_LOAD = 8, W_MMA = 9, W_SCALE = 10, W_CVT = 12;   // warps 0-7: softmax; 12-15, 16-19: conversion
-constexpr int FAC = 4;   // units whose scale factors are ready ahead
+constexpr int W_LOAD = 8, W_MMA = 9, W_SCALE = 10, W_CVT = 12;   // warps 0-7: softmax, two groups; 12-15: conversion
+constexpr int FAC = 4;   // units whose scales are ready ahead
 
 struct TileShared {
-    unsigned long long q_full[2], q_empty[2], kv_full[8], kv_empty[8], raw_full[8], raw_empty[8];
-    unsigned long long q_ready[2];   // 8-bit entries: the Q tile is in float16
+    unsigned long long q_full[2], q_empty[2], k_full[6], k_empty[6], v_full[6], v_empty[6], r_full[4], r_empty[4];
     unsigned long long s_full[2], p_ready[2], o_full[2], drain;
-    // 8-bit entries
-    unsigned long long f_full[FAC], f_empty[FAC];
-    float2 kv_unit[8];               // what 1 stands for in a unit's K (x), and log2 of it in its V (y); unit u in u % 8
-    uint8_t q_unit[2][AT_ROWS];      // the exponent of what 1 stands for in a row of Q
-    uint16_t fac[FAC][2][AT_ROWS];   // float16 factors of a unit's rows, K and V
+    unsigned long long q_ready[2], f_full[FAC], f_empty[FAC];   // 8-bit entries: Q in e4m3, a unit's scales
     uint32_t tmem;
     volatile int abort;
     int total, b0, base0;        // units of all sequences (one pair's worth); where the CTA's line starts
-    int sums[20];                // per warp
+    int sums[16];                // per warp
+};
+struct QuantShared : TileShared {
+    alignas(16) float4 k_fac[FAC][AT_UNIT / 4];   // what a unit's rows of K stand for
+    uint16_t v_fac[FAC][AT_UNIT];                 // float16 factors of its rows of V
+    float v_unit[FAC];                            // log2 of what 1 stands for in its V
+    uint8_t q_unit[2][AT_ROWS];                   // the scale bytes of Q's rows
 };
 
 constexpr uint32_t SMEM_MAX = 232448;
 template <int D, bool Q8>
 constexpr uint32_t tile_smem()
 {
-    static_assert(TileCfg<D, Q8>::TILES + sizeof(TileShared) <= SMEM_MAX, "shared memory of a CTA");
-    return TileCfg<D, Q8>::TILES + (uint32_t)sizeof(TileShared);
+    constexpr uint32_t n = TileCfg<D, Q8>::TILES + (uint32_t)(Q8 ? sizeof(QuantShared) : sizeof(TileShared));
+    static_assert(n <= SMEM_MAX, "shared memory of a CTA");
+    return n;
 }
 
 struct TileParams {
@@ -350,7 +355,7 @@ __device__ __forceinline__ bool tile_wait(unsigned long long *bar, uint32_t pari
     for (uint32_t it = 0;; ++it) {
         if (mbar_test(bar, parity))
             return true;
-        if (it >= limit * 64 || sh.abort) {
+        if (it >= limit || sh.abort) {
             sh.abort = 1;
             return false;
         }
@@ -368,14 +373,16 @@ __device__ __forceinline__ bool tile_wait_warp(unsigned long long *bar, uint32_t
 // the order in which the tensor cores use them.
 template <int D, bool Q8>
 __device__ void load_role(const TileParams &P, const CUtensorMap *mq_pre, const CUtensorMap *mq_own,
-                          const CUtensorMap *m_pre, const CUtensorMap *m_own, TileShared &sh, uint32_t sq, uint32_t skv,
-                          uint32_t sraw, uint32_t limit)
+                          const CUtensorMap *m_pre, const CUtensorMap *m_own, TileShared &sh, uint32_t smem,
+                          uint32_t limit)
 {
     using C = TileCfg<D, Q8>;
-    constexpr int N = Q8 ? C::NR : C::NS;
-    unsigned long long *const full = Q8 ? sh.raw_full : sh.kv_full, *const empty = Q8 ? sh.raw_empty : sh.kv_empty;
-    Ring q, r;
-    int nq = 0, nr = 0;   // copies issued
+    // V tiles, or their codes
+    constexpr int NV = Q8 ? C::NR : C::NV;
+    constexpr uint32_t V0 = Q8 ? C::R0 : C::V0, VT = Q8 ? C::RAW : C::TILE;
+    unsigned long long *const vfull = Q8 ? sh.r_full : sh.v_full, *const vempty = Q8 ? sh.r_empty : sh.v_empty;
+    Ring q, k, v;
+    int nq = 0, nk = 0, nv = 0;   // copies issued
     Walk walk(P, sh);
     Item it;
     bool ok = true;
@@ -387,65 +394,76 @@ __device__ void load_role(const TileParams &P, const CUtensorMap *mq_pre, const 
             if (!ok)
                 break;
             mbar_arrive_tx(&sh.q_full[q.slot], (uint32_t)tq * P.A.G * D * 2);
-            for (int k = 0; k < D / 64; ++k)
-                tma_4d(sq + q.slot * C::TILE + k * C::BLOCK, mq, &sh.q_full[q.slot], k * 64, 0, it.h,
+            for (int x = 0; x < D / 64; ++x)
+                tma_4d(smem + q.slot * C::TILE + x * C::BLOCK, mq, &sh.q_full[q.slot], x * 64, 0, it.h,
                        it.row0 + g * tq);
             q.next(2);
             ++nq;
         }
         for (int s = 0; s < 2 * it.n; ++s) {
-            const auto [j, kv] = item_tile(it, s);
-            if (!ok || !(ok = tile_wait(&empty[r.slot], r.phase ^ 1, limit, sh)))
+            const auto [j, kind] = item_tile(it, s);
+            unsigned long long *const full = kind ? &vfull[v.slot] : &sh.k_full[k.slot];
+            if (!ok || !(ok = kind ? tile_wait(&vempty[v.slot], v.phase ^ 1, limit, sh)
+                                   : tile_wait(&sh.k_empty[k.slot], k.phase ^ 1, limit, sh)))
                 break;
+            const uint32_t dst = smem + (kind ? V0 + v.slot * VT : C::K0 + k.slot * C::KT);
             const int e = it.e0 + j * AT_UNIT;
-            if constexpr (Q8) {
-                mbar_arrive_tx(&full[r.slot], C::RAW);
-                const uint32_t dst = sraw + r.slot * C::RAW;
+            mbar_arrive_tx(full, VT);
+            for (int x = 0; x < (Q8 ? 1 : D / 64); ++x) {
                 if (it.b < 0)
-                    tma_4d(dst, m_pre, &full[r.slot], 0, it.h, kv, e);
+                    tma_4d(dst + x * C::BLOCK, m_pre, full, x * 64, it.h, kind, e);
                 else
-                    tma_5d(dst, m_own, &full[r.slot], 0, it.h, kv, e, it.b);
-            } else {
-                mbar_arrive_tx(&full[r.slot], C::TILE);
-                for (int k = 0; k < D / 64; ++k) {
-                    const uint32_t dst = skv + r.slot * C::TILE + k * C::BLOCK;
-                    if (it.b < 0)
-                        tma_4d(dst, m_pre, &full[r.slot], k * 64, it.h, kv, e);
-                    else
-                        tma_5d(dst, m_own, &full[r.slot], k * 64, it.h, kv, e, it.b);
-                }
+                    tma_5d(dst + x * C::BLOCK, m_own, full, x * 64, it.h, kind, e, it.b);
             }
-            r.next(N);
-            ++nr;
+            if (kind) {
+                v.next(NV);
+                ++nv;
+            } else {
+                k.next(C::NK);
+                ++nk;
+            }
         }
     }
     if (!ok) {
         // copies in flight land before the CTA ends
-        for (int k = 0; k < 2 && k < nq; ++k)
-            (void)ring_wait(&sh.q_full[(nq - 1 - k) % 2], ((nq - 1 - k) / 2) & 1, limit);
-        for (int k = 0; k < N && k < nr; ++k)
-            (void)ring_wait(&full[(nr - 1 - k) % N], ((nr - 1 - k) / N) & 1, limit);
+        for (int i = 1; i <= 2 && i <= nq; ++i)
+            (void)ring_wait(&sh.q_full[(nq - i) % 2], ((nq - i) / 2) & 1, limit);
+        for (int i = 1; i <= C::NK && i <= nk; ++i)
+            (void)ring_wait(&sh.k_full[(nk - i) % C::NK], ((nk - i) / C::NK) & 1, limit);
+        for (int i = 1; i <= NV && i <= nv; ++i)
+            (void)ring_wait(&vfull[(nv - i) % NV], ((nv - i) / NV) & 1, limit);
     }
 }
 
 // The issuer of every tcgen05.mma: one warp, one elected lane issues.
 template <int D, bool Q8>
-__device__ void mma_role(const TileParams &P, TileShared &sh, uint32_t sq, uint8_t *kv_ptr, uint32_t skv, uint32_t limit)
+__device__ void mma_role(const TileParams &P, TileShared &sh, uint8_t *tiles, uint32_t smem, uint32_t limit)
 {
     using C = TileCfg<D, Q8>;
-    constexpr uint32_t IS = mma_desc(128, false, Q8), IO = mma_desc(D, true, Q8);
+    constexpr uint32_t IS = mma_desc(128, false, Q8 ? MMA_E4M3 : MMA_BF16), IO = mma_desc(D, true, Q8 ? MMA_F16 : MMA_BF16);
     const int lane = threadIdx.x & 31;
     const uint32_t tmem = (uint32_t)uniform((int)sh.tmem);
-    Ring q, r;
+    Ring q, kr, vr;
     uint32_t pphase[2] = {0, 0};
     bool ok = true;
     auto scores = [&](int g, int qs, int ks, bool last) {
         if (elect_one()) {
-            const uint32_t a = desc_lo(sq + qs * C::TILE, 16), b = desc_lo(skv + ks * C::TILE, 16);
+            const uint32_t a = desc_lo(smem + qs * C::TILE, 16), b = desc_lo(smem + C::K0 + ks * C::KT, 16);
+            if constexpr (Q8) {
+                // two terms of Q: blocks of their own (D = 128), halves of a 128-byte row (D = 64)
+                constexpr uint32_t TERM = D == 128 ? C::BLOCK : 64;
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint32_t at = ((k / 4) * C::BLOCK + (k % 4) * 32) >> 4;
-                mma_ss(tmem + g * 128, a + at, b + at, IS, k > 0);
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k)
+                        mma_ss8<D == 128 ? DESC_128 : DESC_64>(tmem + g * 128, a + ((t * TERM + k * 32) >> 4),
+                                                               b + ((k * 32) >> 4), IS, t + k > 0);
+            } else {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t at = ((k / 4) * C::BLOCK + (k % 4) * 32) >> 4;
+                    mma_ss(tmem + g * 128, a + at, b + at, IS, k > 0);
+                }
             }
             mma_commit(&sh.s_full[g]);
             if (last && !Q8)
@@ -461,7 +479,7 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint32_t sq, uint8
         tc_after();
         if (elect_one()) {
             // V is read along its rows: blocks of 64 columns lie BLOCK apart, 16 rows are 2048 bytes
-            const uint32_t b = desc_lo(skv + vs * C::TILE, C::BLOCK);
+            const uint32_t b = desc_lo(smem + C::V0 + vs * C::TILE, C::BLOCK);
 #pragma unroll
             for (int k = 0; k < AT_UNIT / 16; ++k)
                 mma_ts(tmem + 256 + g * D, tmem + g * 128 + k * 8, b + ((k * 2048) >> 4), IO, !first || k > 0);
@@ -470,10 +488,17 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint32_t sq, uint8
         }
         __syncwarp();
     };
-    auto take = [&](int &slot) {
-        slot = r.slot;
-        ok = tile_wait_warp(&sh.kv_full[r.slot], r.phase, limit, sh);
-        r.next(C::NS);
+    auto take_k = [&](int &slot) {
+        slot = kr.slot;
+        ok = tile_wait_warp(&sh.k_full[kr.slot], kr.phase, limit, sh);
+        kr.next(C::NK);
+        tc_after();
+        return ok;
+    };
+    auto take_v = [&](int &slot) {
+        slot = vr.slot;
+        ok = tile_wait_warp(&sh.v_full[vr.slot], vr.phase, limit, sh);
+        vr.next(C::NV);
         tc_after();
         return ok;
     };
@@ -489,7 +514,7 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint32_t sq, uint8
                 return;
             for (int k = 0; k < D / 64; ++k)
                 for (int i = nv * 8 + lane; i < AT_UNIT * 8; i += 32)
-                    *reinterpret_cast<uint4 *>(kv_ptr + slot * C::TILE + k * C::BLOCK + i * 16) =
+                    *reinterpret_cast<uint4 *>(tiles + C::V0 + slot * C::TILE + k * C::BLOCK + i * 16) =
                         make_uint4(0, 0, 0, 0);
             async_fence();
             __syncwarp();
@@ -510,50 +535,50 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint32_t sq, uint8
             break;
         tc_after();
         if (it.two) {
-            if (!take(ks))
+            if (!take_k(ks))
                 break;
             scores(0, qs[0], ks, it.n == 1);
             scores(1, qs[1], ks, it.n == 1);
-            give(&sh.kv_empty[ks]);
+            give(&sh.k_empty[ks]);
             for (int j = 0; ok && j < it.n; ++j) {
                 const bool last = j + 1 == it.n;
-                if (!take(vs))
+                if (!take_v(vs))
                     break;
                 clear_tail(vs, it.left - j * AT_UNIT);
                 values(0, vs, j == 0, last);
-                if (!ok || (!last && !take(ks)))
+                if (!ok || (!last && !take_k(ks)))
                     break;
                 if (!last)
                     scores(0, qs[0], ks, j + 2 == it.n);
                 values(1, vs, j == 0, last);
                 if (!ok)
                     break;
-                give(&sh.kv_empty[vs]);
+                give(&sh.v_empty[vs]);
                 if (!last) {
                     scores(1, qs[1], ks, j + 2 == it.n);
-                    give(&sh.kv_empty[ks]);
+                    give(&sh.k_empty[ks]);
                 }
             }
         } else {
             for (int j = 0; ok && j < min(2, it.n); ++j) {
-                if (!take(ks))
+                if (!take_k(ks))
                     break;
                 scores(j, qs[0], ks, j + 1 == it.n);
-                give(&sh.kv_empty[ks]);
+                give(&sh.k_empty[ks]);
             }
             for (int j = 0; ok && j < it.n; ++j) {
-                if (!take(vs))
+                if (!take_v(vs))
                     break;
                 clear_tail(vs, it.left - j * AT_UNIT);
                 values(j & 1, vs, j < 2, j + 2 >= it.n);
                 if (!ok)
                     break;
-                give(&sh.kv_empty[vs]);
+                give(&sh.v_empty[vs]);
                 if (j + 2 < it.n) {
-                    if (!take(ks))
+                    if (!take_k(ks))
                         break;
                     scores(j & 1, qs[0], ks, j + 3 == it.n);
-                    give(&sh.kv_empty[ks]);
+                    give(&sh.k_empty[ks]);
                 }
             }
         }
@@ -571,15 +596,15 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint32_t sq, uint8
 // Softmax of group g: thread w * 32 + lane owns row w * 32 + lane of the
 // group's tile (a warp reaches only its own quarter of the TMEM lanes).
 template <int D, bool Q8>
-__device__ void softmax_role(const TileParams &P, TileShared &sh, int g, uint32_t limit)
+__device__ void softmax_role(const TileParams &P, QuantShared &sh, int g, uint32_t limit)
 {
     const int lane = threadIdx.x & 31, w = (threadIdx.x / 32) & 3, row = w * 32 + lane;
     const uint32_t lanes = (uint32_t)(w * 32) << 16;
     const uint32_t ts = sh.tmem + lanes + g * 128, to = sh.tmem + lanes + 256 + g * D;
-    float c = P.A.c, bv = 0.0f, unbv = 1.0f, crow = P.A.c;
+    float c = P.A.c, bv = 0.0f, unbv = 1.0f;
+    int unit = 0;   // of the CTA, as the item starts
     uint32_t sphase = 0, ophase = 0;
     Ring q;
-    int unit = 0;   // of the CTA, as the item starts
     Walk walk(P, sh);
     Item it;
     for (; walk.next(it); unit += it.n) {
@@ -599,36 +624,36 @@ __device__ void softmax_role(const TileParams &P, TileShared &sh, int g, uint32_
                 return;
             sphase ^= 1;
             tc_after();
+            const int fs = (unit + j) % FAC;
+            if (Q8 && !tile_wait_warp(&sh.f_full[fs], ((unit + j) / FAC) & 1, limit, sh))
+                return;
             if (active) {
+                float x[AT_UNIT];
+                tmem_ld(ts, x);
                 if constexpr (Q8) {
-                    // written before the tiles were handed to the tensor cores that made S
+                    // written before Q was handed to the tensor cores that made S
                     if (i == 0)
-                        crow = P.A.c * __int_as_float(sh.q_unit[qs][row] << 23);
-                    const float2 u = sh.kv_unit[(unit + j) & 7];
-                    c = crow * u.x;
-                    bv = u.y;
+                        c = P.A.c * fp8_factor(sh.q_unit[qs][row]);
+                    bv = sh.v_unit[fs];
                     unbv = ex2a(-bv);   // a power of two: exact
-                }
-                constexpr int CO = TileCfg<D, Q8>::COLS;
-                float x[CO];
-                auto load = [&](int first) {
-                    tmem_ld(ts + first, x);
-                    if (nv < AT_UNIT) {
 #pragma unroll
-                        for (int k = 0; k < CO; ++k)
-                            x[k] = first + k < nv ? x[k] : -F_INF;
+                    for (int k = 0; k < AT_UNIT; k += 4) {
+                        const float4 y = sh.k_fac[fs][k / 4];
+                        upk(mul2(pk(x[k], x[k + 1]), pk(y.x, y.y)), x[k], x[k + 1]);
+                        upk(mul2(pk(x[k + 2], x[k + 3]), pk(y.z, y.w)), x[k + 2], x[k + 3]);
                     }
-                };
-                float top[4] = {-F_INF, -F_INF, -F_INF, -F_INF};
-#pragma unroll
-                for (int first = 0; first < AT_UNIT; first += CO) {
-                    load(first);
-#pragma unroll
-                    for (int k = 0; k < CO; k += 4)
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            top[u] = fmaxf(top[u], x[k + u]);
                 }
+                if (nv < AT_UNIT) {
+#pragma unroll
+                    for (int k = 0; k < AT_UNIT; ++k)
+                        x[k] = k < nv ? x[k] : -F_INF;
+                }
+                float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                for (int k = 4; k < AT_UNIT; k += 4)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        top[u] = fmaxf(top[u], x[k + u]);
                 float s = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
                 if constexpr (Q8)
                     s += bv;
@@ -657,14 +682,11 @@ __device__ void softmax_role(const TileParams &P, TileShared &sh, int g, uint32_
                 f2 sum[2] = {pk(0.0f, 0.0f), pk(0.0f, 0.0f)};
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    // P's 64 columns lie over those of S that this thread has read
-                    if (CO < AT_UNIT)
-                        load(hf * CO);
-                    constexpr int H = CO < AT_UNIT ? 0 : 64;
+                    // P's 64 columns lie over those of S, which this thread has read
                     uint32_t p[32];
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
-                        const f2 e = ex2x2(fma2(pk(x[hf * H + 2 * k], x[hf * H + 2 * k + 1]), cc, nref));
+                        const f2 e = ex2x2(fma2(pk(x[hf * 64 + 2 * k], x[hf * 64 + 2 * k + 1]), cc, nref));
                         sum[k & 1] = add2(sum[k & 1], e);
                         float lo, hi;
                         upk(e, lo, hi);
@@ -679,8 +701,11 @@ __device__ void softmax_role(const TileParams &P, TileShared &sh, int g, uint32_
             }
             tc_before();
             __syncwarp();
-            if (lane == 0)
+            if (lane == 0) {
                 mbar_arrive(&sh.p_ready[g]);
+                if constexpr (Q8)   // eight arrivals: both groups read the unit's scales, or one does for both
+                    mbar_arrive_n(&sh.f_empty[fs], it.two ? 1 : 2);
+            }
         }
         const size_t at = ((size_t)it.slot * 2 + g) * rows + row;
         const bool pre = it.b < 0;
@@ -710,14 +735,13 @@ __device__ void softmax_role(const TileParams &P, TileShared &sh, int g, uint32_
 }
 
 // 8-bit entries: the scale bytes of three units are in flight in one warp's
-// registers (rows lane, lane + 32, ..), which turns them into float16 factors
-// relative to the unit's largest.
-__device__ __forceinline__ void scale_role(const TileParams &P, TileShared &sh, uint32_t limit)
+// registers (rows lane, lane + 32, ..), which turns them into factors.
+__device__ __forceinline__ void scale_role(const TileParams &P, QuantShared &sh, uint32_t limit)
 {
     const int lane = threadIdx.x & 31;
     Walk walk(P, sh);
     Item it;
-    int j = 0, unit = 0;
+    int j = 0;
     bool more = walk.next(it);
     Ring r;
     struct Bytes {
@@ -747,30 +771,27 @@ __device__ __forceinline__ void scale_role(const TileParams &P, TileShared &sh, 
     auto publish = [&](const Bytes &x) {
         if (x.nv <= 0 || !tile_wait_warp(&sh.f_empty[r.slot], r.phase ^ 1, limit, sh))
             return false;
-        int ref[2];
+        // V's are relative to the largest, no lower than 2^-100: l holds the weights times its reciprocal
+        uint32_t top = 27;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            uint32_t m = 0;
+        for (int i = 0; i < 4; ++i)
+            top = max(top, x.b[1][i] == 255 ? 0u : x.b[1][i]);
+        top = __reduce_max_sync(0xffffffffu, top);
+        float *kf = reinterpret_cast<float *>(sh.k_fac[r.slot]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                m = max(m, x.b[k][i] == 255 ? 0u : x.b[k][i]);
-            // no lower than 2^-100: l holds the weights times its reciprocal
-            ref[k] = (int)max(__reduce_max_sync(0xffffffffu, m), 27u);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // 2^(byte - ref + 7) times the 2^8 that scale_e4m3 takes away
-                const int e = (int)x.b[k][i] - ref[k] + 15 + 127;
-                const float f = x.b[k][i] == 255 ? __int_as_float(0x7fc00000) : __int_as_float(max(e, 0) << 23);
-                sh.fac[r.slot][k][i * 32 + lane] = (uint16_t)pack_f16(f, 0.0f);
-            }
+        for (int i = 0; i < 4; ++i) {
+            kf[i * 32 + lane] = fp8_factor(x.b[0][i]);
+            // 2^(byte - top + 7) times the 2^8 that scale_e4m3 takes away
+            const int e = (int)x.b[1][i] - (int)top + 15 + 127;
+            const float f = x.b[1][i] == 255 ? __int_as_float(0x7fc00000) : __int_as_float(max(e, 0) << 23);
+            sh.v_fac[r.slot][i * 32 + lane] = (uint16_t)pack_f16(f, 0.0f);
         }
         if (lane == 0)
-            sh.kv_unit[unit & 7] = make_float2(__int_as_float((ref[0] - 7) << 23), (float)(ref[1] - 7 - 127));
+            sh.v_unit[r.slot] = (float)((int)top - 7 - 127);
         __syncwarp();
         if (lane == 0)
             mbar_arrive(&sh.f_full[r.slot]);
         r.next(FAC);
-        ++unit;
         return true;
     };
     Bytes a, b, c;
@@ -790,11 +811,10 @@ __device__ __forceinline__ void scale_role(const TileParams &P, TileShared &sh, 
     }
 }
 
-// 8-bit entries: tiles to float16, K tiles (and Q) by one group of four warps,
-// V tiles by another; warp w of a group takes rows 32 w .. 32 w + 31.
+// 8-bit entries: Q to two e4m3 terms, V's codes to float16; warp w of the four
+// takes rows 32 w .. 32 w + 31 of each tile.
 template <int D>
-__device__ void convert_role(const TileParams &P, TileShared &sh, int group, uint8_t *qt, const uint8_t *raw,
-                             uint8_t *kv, uint32_t limit)
+__device__ void convert_role(const TileParams &P, QuantShared &sh, uint8_t *tiles, uint32_t limit)
 {
     using C = TileCfg<D, true>;
     const int lane = threadIdx.x & 31, w = (threadIdx.x / 32) & 3;
@@ -803,19 +823,20 @@ __device__ void convert_role(const TileParams &P, TileShared &sh, int group, uin
     Item it;
     int unit = 0;   // of the CTA, as the item starts
 
-    // a Q tile: bfloat16 to float16 in place, eight lanes to a row
+    // A Q tile, in place, eight lanes to a row and four rows at a time: both terms of a row go where
+    // the row was (D = 128: its two 128-byte pieces; D = 64: the two halves of its one).
     auto convert_q = [&] {
         if (!tile_wait_warp(&sh.q_full[q.slot], q.phase, limit, sh))
             return false;
-        uint8_t *tile = qt + q.slot * C::TILE;
-#pragma unroll 2
+        uint8_t *tile = tiles + q.slot * C::TILE;
         for (int p = 0; p < 8; ++p) {
-            const int row = w * 32 + p * 4 + lane / 8;
+            const int row = w * 32 + p * 4 + lane / 8, c = (lane % 8) ^ (row & 7);   // this lane's chunk of eight columns
+            uint8_t *at = tile + row * 128;
             uint4 v[D / 64];
             uint32_t top = 0;
 #pragma unroll
             for (int k = 0; k < D / 64; ++k) {
-                v[k] = *reinterpret_cast<const uint4 *>(tile + k * C::BLOCK + row * 128 + (lane % 8) * 16);
+                v[k] = *reinterpret_cast<const uint4 *>(at + k * C::BLOCK + (lane % 8) * 16);
                 top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[k].x & 0x7fff7fffu, v[k].y & 0x7fff7fffu),
                                              __vmaxu2(v[k].z & 0x7fff7fffu, v[k].w & 0x7fff7fffu)));
             }
@@ -823,19 +844,31 @@ __device__ void convert_role(const TileParams &P, TileShared &sh, int group, uin
 #pragma unroll
             for (int o = 4; o; o >>= 1)
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            // the row's largest element is 1.m * 2^e; infinities, NaN and zero rows stay as they are
-            const int e = top == 0 || top >= 0x7f80u ? 14 : max((int)(top >> 7) - 127, -112);
-            const float f = __int_as_float((127 + 14 - e) << 23);
+            float inv;
+            const uint32_t byte = fp8_scale(top << 16, inv);
+            __syncwarp();   // every lane has its part of the rows
 #pragma unroll
             for (int k = 0; k < D / 64; ++k) {
-                uint32_t *x = reinterpret_cast<uint32_t *>(&v[k]);
+                const uint32_t in[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                uint32_t t0[2], t1[2];
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    x[u] = pack_f16(__uint_as_float(x[u] << 16) * f, __uint_as_float(x[u] & 0xffff0000u) * f);
-                *reinterpret_cast<uint4 *>(tile + k * C::BLOCK + row * 128 + (lane % 8) * 16) = v[k];
+                for (int u = 0; u < 2; ++u) {
+                    const float a = __uint_as_float(in[2 * u] << 16) * inv, b = __uint_as_float(in[2 * u] & 0xffff0000u) * inv;
+                    const float x = __uint_as_float(in[2 * u + 1] << 16) * inv, y = __uint_as_float(in[2 * u + 1] & 0xffff0000u) * inv;
+                    float z[4];
+                    t0[u] = pack_e4m3(a, b, x, y);
+                    unpack_e4m3(t0[u], z);
+                    t1[u] = pack_e4m3(a - z[0], b - z[1], x - z[2], y - z[3]);   // exact differences
+                }
+                // columns 64 k + 8 c .. of a term: half c & 1 of its 16-byte chunk 4 k + c / 2
+                const int chunk = 4 * k + c / 2, half = (c & 1) * 8;
+                const uint32_t o0 = ((chunk ^ (row & 7)) << 4) + half;
+                const uint32_t o1 = D == 128 ? C::BLOCK + o0 : (((chunk + 4) ^ (row & 7)) << 4) + half;
+                *reinterpret_cast<uint2 *>(at + o0) = make_uint2(t0[0], t0[1]);
+                *reinterpret_cast<uint2 *>(at + o1) = make_uint2(t1[0], t1[1]);
             }
             if (lane % 8 == 0)
-                sh.q_unit[q.slot][row] = (uint8_t)(127 - 14 + e);
+                sh.q_unit[q.slot][row] = (uint8_t)byte;
         }
         async_fence();
         __syncwarp();
@@ -846,9 +879,9 @@ __device__ void convert_role(const TileParams &P, TileShared &sh, int group, uin
     };
 
     // A tile of codes, 16 of a row per lane and pass.  A row's 16 codes become two 16-byte chunks
-    // of the swizzled bfloat16 layout (chunk c of row r at c ^ (r & 7)), and for D = 128 the codes
-    // are swizzled the same way.  Eight lanes take four chunks of the rows r and r ^ 5: their bit 2
-    // keeps the loads, their bit 0 the stores apart, so neither meets a bank conflict.
+    // of the swizzled 16-bit layout (chunk c of row r at c ^ (r & 7)); the codes are swizzled the
+    // same way (D = 64: at c ^ (r / 2 & 3)).  Eight lanes take four chunks of the rows r and r ^ 5:
+    // their bit 2 keeps the loads, their bit 0 the stores apart, so neither meets a bank conflict.
     constexpr int PASSES = D / 16, STEP = D == 128 ? 2 : 1;   // passes; of them over the same eight rows
     const int c2 = lane & 3, blk = D == 128 ? (lane >> 3) & 1 : 0, hi = D == 128 ? lane >> 4 : lane >> 3;
     uint32_t src0[STEP], dst0[STEP];
@@ -857,7 +890,7 @@ __device__ void convert_role(const TileParams &P, TileShared &sh, int group, uin
     for (int k = 0; k < STEP; ++k) {
         const int r7 = (D == 128 ? 2 * k + hi : hi) ^ ((lane >> 2 & 1) * 5);
         row0[k] = w * 32 + r7;
-        src0[k] = row0[k] * D + (D == 128 ? ((blk * 4 + c2) ^ r7) : c2) * 16;
+        src0[k] = row0[k] * D + (D == 128 ? ((blk * 4 + c2) ^ r7) : (c2 ^ (r7 >> 1 & 3))) * 16;
         dst0[k] = blk * C::BLOCK + row0[k] * 128 + ((2 * c2) ^ r7) * 16;
     }
     auto convert = [&](const uint8_t *src, uint8_t *dst, const uint16_t *fac, int valid) {
@@ -896,26 +929,26 @@ __device__ void convert_role(const TileParams &P, TileShared &sh, int group, uin
     };
 
     for (; walk.next(it); unit += it.n) {
-        for (int k = 0; group == 0 && k <= it.two; ++k)
+        for (int k = 0; k <= it.two; ++k)
             if (!convert_q())
                 return;
-        for (int at = 0; at < 2 * it.n; ++at, r.next(C::NR), s.next(C::NS)) {
-            const auto [j, kind] = item_tile(it, at);
-            if (kind != group)
-                continue;
+        for (int j = 0; j < it.n; ++j) {
             const int fs = (unit + j) % FAC;
             if (!(tile_wait_warp(&sh.f_full[fs], ((unit + j) / FAC) & 1, limit, sh) &&
-                  tile_wait_warp(&sh.raw_full[r.slot], r.phase, limit, sh) &&
-                  tile_wait_warp(&sh.kv_empty[s.slot], s.phase ^ 1, limit, sh)))
+                  tile_wait_warp(&sh.r_full[r.slot], r.phase, limit, sh) &&
+                  tile_wait_warp(&sh.v_empty[s.slot], s.phase ^ 1, limit, sh)))
                 return;
-            convert(raw + r.slot * C::RAW, kv + s.slot * C::TILE, sh.fac[fs][kind], it.left - j * AT_UNIT);
+            convert(tiles + C::R0 + r.slot * C::RAW, tiles + C::V0 + s.slot * C::TILE, sh.v_fac[fs],
+                    it.left - j * AT_UNIT);
             async_fence();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&sh.kv_full[s.slot]);
-                mbar_arrive(&sh.raw_empty[r.slot]);
+                mbar_arrive(&sh.v_full[s.slot]);
+                mbar_arrive(&sh.r_empty[r.slot]);
                 mbar_arrive(&sh.f_empty[fs]);
             }
+            r.next(C::NR);
+            s.next(C::NV);
         }
     }
 }
@@ -929,11 +962,10 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
     using C = TileCfg<D, Q8>;
     // no static shared memory: the tiles start on a 1024-byte boundary, as their swizzle asks
     extern __shared__ __align__(1024) uint8_t tiles[];
-    TileShared &sh = *reinterpret_cast<TileShared *>(tiles + C::TILES);
+    QuantShared &sh = *reinterpret_cast<QuantShared *>(tiles + C::TILES);   // the TileShared of it without 8-bit entries
     pdl_trigger();
     const int tid = threadIdx.x, warp = tid / 32;
-    uint8_t *kv = tiles + 2 * C::TILE, *raw = kv + C::NS * C::TILE;
-    const uint32_t sq = saddr(tiles), skv = saddr(kv), sraw = saddr(raw);
+    const uint32_t smem = saddr(tiles);
     const uint32_t limit = hinted_limit(P.spin_limit > OWN_WAIT_MIN ? P.spin_limit : OWN_WAIT_MIN);
 
     // ---- where this CTA's line starts: sums over runs of sequences, then the run
@@ -961,17 +993,21 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
             mbar_init(&sh.p_ready[k], 4);
             mbar_init(&sh.o_full[k], 1);
         }
-        for (int k = 0; k < C::NS; ++k) {
-            mbar_init(&sh.kv_full[k], Q8 ? 4 : 1);
-            mbar_init(&sh.kv_empty[k], 1);
+        for (int k = 0; k < C::NK; ++k) {
+            mbar_init(&sh.k_full[k], 1);
+            mbar_init(&sh.k_empty[k], 1);
+        }
+        for (int k = 0; k < C::NV; ++k) {
+            mbar_init(&sh.v_full[k], Q8 ? 4 : 1);
+            mbar_init(&sh.v_empty[k], 1);
         }
         for (int k = 0; k < C::NR; ++k) {
-            mbar_init(&sh.raw_full[k], 1);
-            mbar_init(&sh.raw_empty[k], 4);
+            mbar_init(&sh.r_full[k], 1);
+            mbar_init(&sh.r_empty[k], 4);
         }
         for (int k = 0; k < FAC; ++k) {
             mbar_init(&sh.f_full[k], 1);
-            mbar_init(&sh.f_empty[k], 8);
+            mbar_init(&sh.f_empty[k], 12);   // eight of the softmax warps, four of the converting ones
         }
         mbar_init(&sh.drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;\n\tfence.proxy.async.shared::cta;" ::: "memory");
@@ -1019,13 +1055,13 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_REST));
         if (warp == W_LOAD) {
             if (elect_one())
-                load_role<D, Q8>(P, &mq_pre, &mq_own, &m_pre, &m_own, sh, sq, skv, sraw, limit);
+                load_role<D, Q8>(P, &mq_pre, &mq_own, &m_pre, &m_own, sh, smem, limit);
         } else if (warp == W_MMA) {
-            mma_role<D, Q8>(P, sh, sq, kv, skv, limit);
+            mma_role<D, Q8>(P, sh, tiles, smem, limit);
         } else if (Q8 && warp == W_SCALE) {
             scale_role(P, sh, limit);
         } else if (Q8 && warp >= W_CVT) {
-            convert_role<D>(P, sh, (warp - W_CVT) / 4, tiles, raw, kv, limit);
+            convert_role<D>(P, sh, tiles, limit);
         }
     }
     __syncwarp();
@@ -1058,8 +1094,8 @@ EncodeTiled encode_tiled()
 }
 
 // A map over a row-major array of `rank` dimensions (innermost first); boxes
-// of bfloat16 are 64 wide with 128-byte swizzle, boxes of codes a whole head
-// (swizzled too where that is 128 bytes).
+// of bfloat16 are 64 wide, boxes of codes a whole head: rows of 128 bytes, or of
+// 64, swizzled as the tensor cores read them.
 bool make_map(CUtensorMap *map, bool codes, const void *base, int rank, const cuuint64_t *dim, const cuuint32_t *box)
 {
     cuuint64_t stride[4];
@@ -1071,7 +1107,7 @@ bool make_map(CUtensorMap *map, bool codes, const void *base, int rank, const cu
     const cuuint32_t one[5] = {1, 1, 1, 1, 1};
     return encode_tiled()(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
                           const_cast<void *>(base), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          codes && box[0] < 128 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                          codes && box[0] < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -27,7 +27,7 @@
 namespace sv {
 namespace {
 
-constexpr int QT = 256;   // threads of a CTA
+constexpr int QT = 128;   // threads of a CTA
 constexpr int QU = 4;     // pieces in flight per thread (of a piece: 8 elements)
 
 // ---------------------------------------------------------------- commit
@@ -89,7 +89,7 @@ __device__ __forceinline__ float piece_at(const Piece<E> &x, int k)
 // One CTA per (layer, sequence): its committed entries, QU pieces in flight
 // per thread.
 template <class E, int D>
-__global__ void __launch_bounds__(QT, sizeof(E) == 2 ? 6 : 4) kvq_commit(const __grid_constant__ KvQuantParams P)
+__global__ void __launch_bounds__(QT, sizeof(E) == 2 ? 12 : 8) kvq_commit(const __grid_constant__ KvQuantParams P)
 {
     constexpr int G = D / 8;   // lanes of a head
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
