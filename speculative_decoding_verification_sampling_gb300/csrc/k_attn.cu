@@ -31,11 +31,12 @@
 namespace sv {
 namespace {
 
-constexpr int FW = 4;   // warps of a CTA
+constexpr int FW = 4;                  // warps of a CTA
+constexpr long long WIDE_ROWS = 2048;   // rows up to which each has a CTA of its own
 
-// E = D / 8 elements of a row per lane, as pairs: lane s of the row's eight
-// holds elements 8 s .. 8 s + 7 and, with E = 16, the same 64 further on (every
-// load of the row's lanes is contiguous).
+// E elements of a row per lane, as pairs.  Eight lanes to a row: lane s holds
+// elements 8 s .. 8 s + 7 and, with E = 16, the same 64 further on.  A warp to a
+// row: lane s holds E s .. E s + E - 1.  Every load of a row is contiguous.
 template <int E>
 struct RawRow {
     uint32_t w[E / 2];
@@ -44,10 +45,17 @@ template <int E>
 __device__ __forceinline__ RawRow<E> load_row(const uint16_t *p)
 {
     RawRow<E> r;
+    if constexpr (E >= 8) {
 #pragma unroll
-    for (int k = 0; k < E / 8; ++k) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p + k * 64));
-        r.w[4 * k] = v.x, r.w[4 * k + 1] = v.y, r.w[4 * k + 2] = v.z, r.w[4 * k + 3] = v.w;
+        for (int k = 0; k < E / 8; ++k) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p + k * 64));
+            r.w[4 * k] = v.x, r.w[4 * k + 1] = v.y, r.w[4 * k + 2] = v.z, r.w[4 * k + 3] = v.w;
+        }
+    } else if constexpr (E == 4) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+        r.w[0] = v.x, r.w[1] = v.y;
+    } else {
+        r.w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
     }
     return r;
 }
@@ -60,25 +68,35 @@ __device__ __forceinline__ f2 pair_of(const RawRow<E> &r, int k)
 template <int E>
 __device__ __forceinline__ void load_values(const float *p, float (&y)[E])
 {
+    if constexpr (E >= 4) {
 #pragma unroll
-    for (int k = 0; k < E / 4; ++k) {
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + (k >> 1) * 64 + (k & 1) * 4));
-        y[4 * k] = v.x, y[4 * k + 1] = v.y, y[4 * k + 2] = v.z, y[4 * k + 3] = v.w;
+        for (int k = 0; k < E / 4; ++k) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + (k >> 1) * 64 + (k & 1) * 4));
+            y[4 * k] = v.x, y[4 * k + 1] = v.y, y[4 * k + 2] = v.z, y[4 * k + 3] = v.w;
+        }
+    } else {
+        const float2 v = __ldcg(reinterpret_cast<const float2 *>(p));
+        y[0] = v.x, y[1] = v.y;
     }
 }
 
-// Eight lanes per query row: a warp works on four heads of a token, and the
-// index arithmetic and the loops over what they see serve four rows (244k rows:
-// 74 us; 147 us with a warp per row, and no faster for a thousand rows).
-template <int D>
+// Many rows (WIDE = false): eight lanes per query row.  A warp works on four
+// heads of a token, and the index arithmetic and the loops over what they see
+// serve four rows.  Few rows (WIDE): a CTA per row, each of its warps taking a
+// quarter of what the row sees and of its partial results, of which there may
+// be hundreds; the four are joined in shared memory.
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(FW * 32)
     va_finish(const __grid_constant__ AttnParams P, const __grid_constant__ AttnWork W, int ctas, int per_token)
 {
-    constexpr int LPR = 8, E = D / LPR, NP = E / 2, AT = 8;
+    constexpr int LPR = WIDE ? 32 : 8, E = D / LPR, NP = E / 2, AT = E < 8 ? E : 8;
+    constexpr int STEP = WIDE ? LPR * FW : LPR;   // partial results looked up at a time
+    constexpr int FLY = WIDE ? 8 : 4;             // of their values in flight
     const float inf = __int_as_float(0x7f800000), nan = __int_as_float(0x7fc00000);
     const int lane = threadIdx.x & 31, sub = lane % LPR;
+    const int warp = threadIdx.x / 32;
     const int bt = blockIdx.x / per_token;
-    const int hq = (blockIdx.x - bt * per_token) * (FW * 32 / LPR) + threadIdx.x / LPR;
+    const int hq = WIDE ? blockIdx.x - bt * per_token : (blockIdx.x - bt * per_token) * (FW * 4) + threadIdx.x / LPR;
     const bool real = hq < P.Hq;
     const int h = real ? hq / P.G : 0, g = real ? hq - h * P.G : 0;
     const int b = bt / P.T, t = bt - b * P.T;
@@ -117,6 +135,8 @@ __global__ void __launch_bounds__(FW * 32)
         for (int j0 = 0; j0 < end; j0 += 32) {
             const int j = j0 + lane;
             unsigned seen = __ballot_sync(0xffffffffu, j < end && (!mask || __ldg(mask + j)));
+            if constexpr (WIDE)
+                seen &= 0x11111111u << warp;   // this warp's quarter
             while (seen) {
                 // two visible entries at a time
                 const int ja = __ffs(seen) - 1;
@@ -182,14 +202,15 @@ __global__ void __launch_bounds__(FW * 32)
                 cnt1 = (attn_owner(u + ub - 1, U, ctas) - c1 + 1) << (1 - W.own.two);
             }
             const int all = cnt0 + cnt1;   // may differ between the warp's rows
-            for (int i0 = 0; __any_sync(0xffffffffu, i0 < all); i0 += LPR) {
-                // lane i of a row looks up partial result i0 + i, then its lanes read the values
-                const bool own = i0 + sub >= cnt0;
-                const int i = i0 + sub - (own ? cnt0 : 0), two = own ? W.own.two : W.pre.two;
+            for (int i0 = 0; __any_sync(0xffffffffu, i0 < all); i0 += STEP) {
+                // each lane of a row looks up a partial result, then all of them read the values
+                const int at_i = i0 + (WIDE ? sub * FW + warp : sub);
+                const bool own = at_i >= cnt0;
+                const int i = at_i - (own ? cnt0 : 0), two = own ? W.own.two : W.pre.two;
                 float pm = -inf, pl = 0.0f;
                 size_t at = 0;
                 bool gave_up = false;
-                if (i0 + sub < all) {
+                if (at_i < all) {
                     // with one set of rows, both groups of a CTA leave one
                     const int c = (own ? c1 : c0) + (two ? i : i >> 1);
                     const int gr = two ? (own ? grp1 : grp0) : i & 1;
@@ -217,12 +238,12 @@ __global__ void __launch_bounds__(FW * 32)
                 l += add;
                 // the partial results that some row of the warp has
                 unsigned have = __ballot_sync(0xffffffffu, wt != 0.0f);
-                have = (have | have >> 8 | have >> 16 | have >> 24) & 0xffu;
+                if constexpr (!WIDE)
+                    have = (have | have >> 8 | have >> 16 | have >> 24) & 0xffu;
                 while (have) {
-                    // the values of four at a time are in flight
-                    float wj[4], y[4][E];
+                    float wj[FLY], y[FLY][E];
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) {
+                    for (int n = 0; n < FLY; ++n) {
                         const int j = have ? __ffs(have) - 1 : 0;
                         const float w = __shfl_sync(0xffffffffu, wt, j, LPR);
                         const float *sj = reinterpret_cast<const float *>(
@@ -236,7 +257,7 @@ __global__ void __launch_bounds__(FW * 32)
                             load_values<E>(sj + sub * AT, y[n]);
                     }
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) {
+                    for (int n = 0; n < FLY; ++n) {
                         const f2 ww = pk(wj[n], wj[n]);
 #pragma unroll
                         for (int k = 0; k < NP; ++k)
@@ -246,31 +267,67 @@ __global__ void __launch_bounds__(FW * 32)
             }
         }
     }
-    if (!real)
-        return;
-    if (code && sub == 0 && P.status)
-        atomicCAS(P.status, 0, code);
-    const float inv = code ? nan : l == 0.0f ? 0.0f : 1.0f / l;
-    uint16_t *out = static_cast<uint16_t *>(P.out) + r * D + sub * AT;
-    uint32_t w[NP];
+    if constexpr (WIDE) {
+        __shared__ float s_o[FW][D], s_m[FW], s_l[FW];
+        __shared__ int s_code[FW];
 #pragma unroll
-    for (int k = 0; k < NP; ++k) {
-        float lo, hi;
-        upk(o[k], lo, hi);
-        w[k] = pack_bf16(lo * inv, hi * inv);
+        for (int k = 0; k < NP; ++k)
+            upk(o[k], s_o[warp][sub * E + 2 * k], s_o[warp][sub * E + 2 * k + 1]);
+        if (lane == 0) {
+            s_m[warp] = m;
+            s_l[warp] = l;
+            s_code[warp] = code;
+        }
+        __syncthreads();
+        const int d = threadIdx.x * 2;
+        if (d >= D)
+            return;
+        m = -inf;
+#pragma unroll
+        for (int w = 0; w < FW; ++w) {
+            m = fmaxf(m, s_m[w]);
+            code = max(code, s_code[w]);
+        }
+        const float ref = m == -inf ? 0.0f : m;
+        float x = 0.0f, y = 0.0f;
+        l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < FW; ++w) {
+            const float f = ex2a(s_m[w] - ref);
+            l = fmaf(s_l[w], f, l);
+            x = fmaf(s_o[w][d], f, x);
+            y = fmaf(s_o[w][d + 1], f, y);
+        }
+        const float inv = code ? nan : l == 0.0f ? 0.0f : 1.0f / l;
+        *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(P.out) + r * D + d) = pack_bf16(x * inv, y * inv);
+    } else {
+        if (!real)
+            return;
+        const float inv = code ? nan : l == 0.0f ? 0.0f : 1.0f / l;
+        uint16_t *out = static_cast<uint16_t *>(P.out) + r * D + sub * AT;
+        uint32_t w[NP];
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+            float lo, hi;
+            upk(o[k], lo, hi);
+            w[k] = pack_bf16(lo * inv, hi * inv);
+        }
+#pragma unroll
+        for (int k = 0; k < E / 8; ++k)
+            *reinterpret_cast<uint4 *>(out + k * 64) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
     }
-#pragma unroll
-    for (int k = 0; k < E / 8; ++k)
-        *reinterpret_cast<uint4 *>(out + k * 64) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-    if (P.lse && sub == 0)
-        P.lse[r] = code ? nan : 0.6931471805599453f * (m + log2f(l));
+    if (WIDE ? threadIdx.x == 0 : sub == 0) {
+        if (code && P.status)
+            atomicCAS(P.status, 0, code);
+        if (P.lse)
+            P.lse[r] = code ? nan : 0.6931471805599453f * (m + log2f(l));
+    }
 }
 
-template <int D>
+template <int D, bool WIDE>
 cudaError_t finish(const AttnParams &P, const AttnWork &W, int ctas, cudaStream_t stream)
 {
-    constexpr int rows = FW * 4;
-    const int per_token = (P.Hq + rows - 1) / rows;
+    const int per_token = WIDE ? P.Hq : (P.Hq + FW * 4 - 1) / (FW * 4);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(P.B * P.T * per_token));
     cfg.blockDim = dim3(FW * 32);
@@ -280,7 +337,7 @@ cudaError_t finish(const AttnParams &P, const AttnWork &W, int ctas, cudaStream_
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = ctas > 0 ? 1 : 0;   // behind the tile kernel; alone it starts like any other
-    return cudaLaunchKernelEx(&cfg, va_finish<D>, P, W, ctas, per_token);
+    return cudaLaunchKernelEx(&cfg, va_finish<D, WIDE>, P, W, ctas, per_token);
 }
 
 }  // namespace
@@ -328,7 +385,10 @@ cudaError_t launch_attention(const AttnParams &P, bool quant, void *workspace, i
             return e;
         ++*launches;
     }
-    const cudaError_t e = P.D == 128 ? finish<128>(P, W, ctas, stream) : finish<64>(P, W, ctas, stream);
+    const bool wide = (long long)P.B * P.T * P.Hq <= WIDE_ROWS;
+    const cudaError_t e = P.D == 128
+                              ? (wide ? finish<128, true>(P, W, ctas, stream) : finish<128, false>(P, W, ctas, stream))
+                              : (wide ? finish<64, true>(P, W, ctas, stream) : finish<64, false>(P, W, ctas, stream));
     if (e == cudaSuccess)
         ++*launches;
     return e;
