@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(FW * 32)
                 size_t at = 0;
                 bool gave_up = false;
                 if (at_i < all) {
-                    // with one set of rows, both groups of a CTA leave one
+                    // with one set of rows, a CTA has one of each group (an empty one if they were joined)
                     const int c = (own ? c1 : c0) + (two ? i : i >> 1);
                     const int gr = two ? (own ? grp1 : grp0) : i & 1;
                     const int rows = (own ? W.own.tq : W.pre.tq) * P.G;
@@ -345,13 +345,13 @@ cudaError_t finish(const AttnParams &P, const AttnWork &W, int ctas, cudaStream_
 bool attention_fits(int B, int T, int H, int G, int D, int P, int L)
 {
     // units of the whole call, and every slot index, in 31 bits
-    const AttnPlan a = attn_plan(B, T, H, G, D, P, L);
+    const AttnPlan a = attn_plan(B, T, H, G, D, P, L, false);
     return a.max_units < (1LL << 31) && (long long)B * H * a.own.tiles < (1LL << 30);
 }
 
 size_t attention_workspace(int B, int T, int H, int G, int D, int P, int L)
 {
-    return attn_plan(B, T, H, G, D, P, L).total;
+    return attn_plan(B, T, H, G, D, P, L, false).total;
 }
 
 cudaError_t launch_attention(const AttnParams &P, bool quant, void *workspace, int sms, uint32_t spin_limit,
@@ -363,7 +363,7 @@ cudaError_t launch_attention(const AttnParams &P, bool quant, void *workspace, i
         if (e != cudaSuccess)
             return e;
     }
-    const AttnPlan a = attn_plan(P.B, P.T, P.H, P.G, P.D, P.P, P.L);
+    const AttnPlan a = attn_plan(P.B, P.T, P.H, P.G, P.D, P.P, P.L, quant);
     char *w = static_cast<char *>(workspace);
     AttnWork W{};
     W.pre = a.pre;

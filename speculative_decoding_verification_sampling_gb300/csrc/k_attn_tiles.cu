@@ -33,7 +33,10 @@
 // last bits (at 2^-40 of the unit's largest element).  What the largest stands
 // for goes back in exactly, into the exponent of the weights (they are
 // 2^(c S + bv - m), and l takes them times 2^-bv).  P is rounded to float16
-// here, 2^-11 of a weight.
+// here, 2^-11 of a weight.  With few rows, where HBM is the bound, one warp's
+// pass over 128 scores per row and their scales is too long a chain: the rows
+// then lie in their tile two or four times, and each warp of a group takes the
+// columns that fall to its copy.
 //
 // The last unit of a stretch is ragged: scores past its end become -inf, and
 // V's rows past it are zeroed in shared memory, since 0 * NaN would reach O.
@@ -140,9 +143,9 @@ __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.
 #define R16(f, i) R4(f, i), R4(f, i + 4), R4(f, i + 8), R4(f, i + 12)
 #define R32(f, i) R16(f, i), R16(f, i + 16)
 
-// 32 columns of this warp's 32 lanes; the wait is part of the instruction
-// block, so no use of x can be moved ahead of it.
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, float *x)
+// Columns of this warp's 32 lanes; the wait is part of the instruction block, so
+// no use of x can be moved ahead of it.
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&x)[32])
 {
 #define OUT(i) "=f"(x[i])
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -175,7 +178,16 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&x)[128])
                  : "memory");
 #undef OUT
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *x)
+__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&x)[16])
+{
+#define IN(i) "r"(x[i])
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::R16(IN, 0),
+                 "r"(addr)
+                 : "memory");
+#undef IN
+}
+__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&x)[32])
 {
 #define IN(i) "r"(x[i])
     asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
@@ -209,12 +221,19 @@ struct TileCfg {
     static constexpr int THREADS = Q8 ? 512 : 384;
     // registers per thread: at launch, then of the softmax groups and of the
     // other warpgroups (their sum over the warpgroups stays within the launch's)
-    static constexpr int REGS = Q8 ? 128 : 168, REGS_SOFT = Q8 ? 176 : 208, REGS_REST = 80;
+    static constexpr int REGS = Q8 ? 128 : 168, REGS_SOFT = Q8 ? 152 : 208, REGS_REST = Q8 ? 104 : 80;
     static_assert(2 * REGS_SOFT + (THREADS / 128 - 2) * REGS_REST <= THREADS / 128 * REGS, "register split");
 };
 
 constexpr int W_LOAD = 8, W_MMA = 9, W_SCALE = 10, W_CVT = 12;   // warps 0-7: softmax, two groups; 12-15: conversion
 constexpr int FAC = 4;   // units whose scales are ready ahead
+
+// Where on the line of units a CTA's part starts: sequence (-1: the prefix),
+// head and tile of the pair, unit of its stretch.
+struct Place {
+    int cur, end;
+    int b, h, tile, off;
+};
 
 struct TileShared {
     unsigned long long q_full[2], q_empty[2], k_full[6], k_empty[6], v_full[6], v_empty[6], r_full[4], r_empty[4];
@@ -222,7 +241,7 @@ struct TileShared {
     unsigned long long q_ready[2], f_full[FAC], f_empty[FAC];   // 8-bit entries: Q in e4m3, a unit's scales
     uint32_t tmem;
     volatile int abort;
-    int total, b0, base0;        // units of all sequences (one pair's worth); where the CTA's line starts
+    Place start;
     int sums[16];                // per warp
 };
 struct QuantShared : TileShared {
@@ -230,6 +249,7 @@ struct QuantShared : TileShared {
     uint16_t v_fac[FAC][AT_UNIT];                 // float16 factors of its rows of V
     float v_unit[FAC];                            // log2 of what 1 stands for in its V
     uint8_t q_unit[2][AT_ROWS];                   // the scale bytes of Q's rows
+    float2 ml[2][AT_ROWS];                        // m and l of both groups' rows, as an item is joined
 };
 
 constexpr uint32_t SMEM_MAX = 232448;
@@ -253,6 +273,10 @@ __device__ __forceinline__ int seq_units(const AttnParams &A, int b)
     return n < 0 || n > A.L ? 0 : (n + AT_UNIT - 1) / AT_UNIT;
 }
 
+// Units from which a stretch of 8-bit entries with one set of rows uses copies of
+// them and joins what the groups and copies leave (a fixed cost per stretch).
+constexpr int JOIN_UNITS = 8;
+
 // One stretch of one pair, as a CTA works on it.
 struct Item {
     int n;           // units
@@ -261,60 +285,54 @@ struct Item {
     int tokens;      // rows of that kind in the pair from row0 on
     int e0, left;    // first entry, entries from there to the end of the stretch
     int two;
+    int copies;      // of the rows in a tile
+    bool join;       // both groups' and all copies' results become one
     int slot;
 };
 
 // The items of one CTA, in order.  Every role walks them by itself.
 struct Walk {
     const TileParams &P;
-    int cur, end, b, base, ub, HS, UP;
-    __device__ Walk(const TileParams &p, const TileShared &sh) : P(p)
+    Place at;
+    int units;   // of the pair's stretch
+    __device__ Walk(const TileParams &p, const Place &start) : P(p), at(start)
     {
-        HS = P.A.H * P.W.own.tiles;
-        UP = P.W.ppairs * P.W.pu;
-        const long long U = UP + (long long)HS * sh.total;
-        cur = attn_start(blockIdx.x, U, gridDim.x);
-        end = attn_start(blockIdx.x + 1, U, gridDim.x);
-        b = sh.b0;
-        base = sh.base0;
-        ub = b < P.A.B ? seq_units(P.A, b) : 0;
+        units = at.b < 0 ? P.W.pu : at.b < P.A.B ? seq_units(P.A, at.b) : 0;
     }
     __device__ bool next(Item &it)
     {
-        if (cur >= end)
+        if (at.cur >= at.end)
             return false;
-        int off, units;
-        if (cur < UP) {
-            const int p = cur / P.W.pu, tile = p % P.W.pre.tiles;
-            off = cur - p * P.W.pu;
-            units = P.W.pu;
-            it.h = p / P.W.pre.tiles;
-            it.b = -1;
-            it.two = P.W.pre.two;
-            it.row0 = tile * P.W.pre.tq * (it.two ? 2 : 1);
-            it.tokens = P.A.B * P.A.T - it.row0;
-            it.left = P.A.P - off * AT_UNIT;
-            it.slot = blockIdx.x + p;
-        } else {
-            while (cur >= base + ub * HS) {
-                base += ub * HS;
-                ub = seq_units(P.A, ++b);
+#pragma unroll 1
+        while (units == 0)   // sequences without entries
+            units = seq_units(P.A, ++at.b);
+        const bool pre = at.b < 0;
+        const AttnTiling &tl = pre ? P.W.pre : P.W.own;
+        const int t0 = at.tile * (tl.tq << tl.two);
+        it.h = at.h;
+        it.b = at.b;
+        it.two = tl.two;
+        it.row0 = pre ? t0 : at.b * P.A.T + t0;
+        it.tokens = (pre ? P.A.B * P.A.T : P.A.T) - t0;
+        it.e0 = at.off * AT_UNIT;
+        it.left = (pre ? P.A.P : __ldg(P.A.len + at.b)) - it.e0;
+        it.slot = blockIdx.x + ((pre ? 0 : at.b * P.A.H) + at.h) * tl.tiles + at.tile;
+        it.n = min(units - at.off, at.end - at.cur);
+        it.join = tl.join && it.n >= JOIN_UNITS;
+        it.copies = it.join ? tl.copies : 1;
+        at.cur += it.n;
+        at.off += it.n;
+        if (at.off == units) {
+            at.off = 0;
+            if (++at.tile == tl.tiles) {
+                at.tile = 0;
+                if (++at.h == P.A.H) {
+                    at.h = 0;
+                    ++at.b;
+                    units = at.b < P.A.B ? seq_units(P.A, at.b) : 0;
+                }
             }
-            const int i = (cur - base) / ub, tile = i % P.W.own.tiles;
-            off = cur - base - i * ub;
-            units = ub;
-            it.h = i / P.W.own.tiles;
-            it.b = b;
-            it.two = P.W.own.two;
-            const int t0 = tile * P.W.own.tq * (it.two ? 2 : 1);
-            it.row0 = b * P.A.T + t0;
-            it.tokens = P.A.T - t0;
-            it.left = __ldg(P.A.len + b) - off * AT_UNIT;
-            it.slot = blockIdx.x + b * HS + i;
         }
-        it.e0 = off * AT_UNIT;
-        it.n = min(units - off, end - cur);
-        cur += it.n;
         return true;
     }
 };
@@ -352,6 +370,7 @@ struct Ring {
 // another role has given up.
 __device__ __forceinline__ bool tile_wait(unsigned long long *bar, uint32_t parity, uint32_t limit, TileShared &sh)
 {
+#pragma unroll 1
     for (uint32_t it = 0;; ++it) {
         if (mbar_test(bar, parity))
             return true;
@@ -383,32 +402,47 @@ __device__ void load_role(const TileParams &P, const CUtensorMap *mq_pre, const 
     unsigned long long *const vfull = Q8 ? sh.r_full : sh.v_full, *const vempty = Q8 ? sh.r_empty : sh.v_empty;
     Ring q, k, v;
     int nq = 0, nk = 0, nv = 0;   // copies issued
-    Walk walk(P, sh);
-    Item it;
-    bool ok = true;
-    while (ok && walk.next(it)) {
-        const CUtensorMap *mq = it.b < 0 ? mq_pre : mq_own;
-        const int tq = it.b < 0 ? P.W.pre.tq : P.W.own.tq;
-        for (int g = 0; ok && g <= it.two; ++g) {
-            ok = tile_wait(&sh.q_empty[q.slot], q.phase ^ 1, limit, sh);
-            if (!ok)
-                break;
-            mbar_arrive_tx(&sh.q_full[q.slot], (uint32_t)tq * P.A.G * D * 2);
-            for (int x = 0; x < D / 64; ++x)
-                tma_4d(smem + q.slot * C::TILE + x * C::BLOCK, mq, &sh.q_full[q.slot], x * 64, 0, it.h,
-                       it.row0 + g * tq);
-            q.next(2);
-            ++nq;
-        }
-        for (int s = 0; s < 2 * it.n; ++s) {
+    Walk walk(P, sh.start);
+    Item it, after;
+    bool ok = true, more = walk.next(it), have_q = false;
+#pragma unroll 1
+    while (ok && more) {
+        more = walk.next(after);
+        bool early = false;
+#pragma unroll 1
+        for (int s = 0; ok && s < 2 * it.n; ++s) {
+            // the item's Q, or the next item's as soon as its place is free (with one set of rows to both)
+            const bool now = s == 0 && !have_q;
+            if (now || (!early && more && !it.two && !after.two && mbar_test(&sh.q_empty[q.slot], q.phase ^ 1))) {
+                const Item &x = now ? it : after;
+                const bool pre = x.b < 0;
+                const CUtensorMap *mq = pre ? mq_pre : mq_own;
+                const int tq = pre ? P.W.pre.tq : P.W.own.tq;
+                early = !now;
+#pragma unroll 1
+                for (int g = 0; ok && g <= x.two; ++g) {
+                    if (!(ok = tile_wait(&sh.q_empty[q.slot], q.phase ^ 1, limit, sh)))
+                        break;
+                    mbar_arrive_tx(&sh.q_full[q.slot], (uint32_t)x.copies * tq * P.A.G * D * 2);
+#pragma unroll 1
+                    for (int c = 0; c < D / 64 * x.copies; ++c) {
+                        const int blk = c % (D / 64), copy = c / (D / 64);
+                        tma_4d(smem + q.slot * C::TILE + blk * C::BLOCK + copy * (C::BLOCK / x.copies), mq,
+                               &sh.q_full[q.slot], blk * 64, 0, x.h, x.row0 + g * tq);
+                    }
+                    q.next(2);
+                    ++nq;
+                }
+            }
             const auto [j, kind] = item_tile(it, s);
             unsigned long long *const full = kind ? &vfull[v.slot] : &sh.k_full[k.slot];
-            if (!ok || !(ok = kind ? tile_wait(&vempty[v.slot], v.phase ^ 1, limit, sh)
-                                   : tile_wait(&sh.k_empty[k.slot], k.phase ^ 1, limit, sh)))
+            Ring &ring = kind ? v : k;
+            if (!ok || !(ok = tile_wait(kind ? &vempty[v.slot] : &sh.k_empty[k.slot], ring.phase ^ 1, limit, sh)))
                 break;
             const uint32_t dst = smem + (kind ? V0 + v.slot * VT : C::K0 + k.slot * C::KT);
             const int e = it.e0 + j * AT_UNIT;
             mbar_arrive_tx(full, VT);
+#pragma unroll 1
             for (int x = 0; x < (Q8 ? 1 : D / 64); ++x) {
                 if (it.b < 0)
                     tma_4d(dst + x * C::BLOCK, m_pre, full, x * 64, it.h, kind, e);
@@ -423,6 +457,8 @@ __device__ void load_role(const TileParams &P, const CUtensorMap *mq_pre, const 
                 ++nk;
             }
         }
+        have_q = early;
+        it = after;
     }
     if (!ok) {
         // copies in flight land before the CTA ends
@@ -444,148 +480,126 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint8_t *tiles, ui
     const int lane = threadIdx.x & 31;
     const uint32_t tmem = (uint32_t)uniform((int)sh.tmem);
     Ring q, kr, vr;
-    uint32_t pphase[2] = {0, 0};
+    uint32_t pphase = 0;   // a bit for each group
     bool ok = true;
-    auto scores = [&](int g, int qs, int ks, bool last) {
-        if (elect_one()) {
-            const uint32_t a = desc_lo(smem + qs * C::TILE, 16), b = desc_lo(smem + C::K0 + ks * C::KT, 16);
-            if constexpr (Q8) {
-                // two terms of Q: blocks of their own (D = 128), halves of a 128-byte row (D = 64)
-                constexpr uint32_t TERM = D == 128 ? C::BLOCK : 64;
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int k = 0; k < D / 32; ++k)
-                        mma_ss8<D == 128 ? DESC_128 : DESC_64>(tmem + g * 128, a + ((t * TERM + k * 32) >> 4),
-                                                               b + ((k * 32) >> 4), IS, t + k > 0);
-            } else {
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t at = ((k / 4) * C::BLOCK + (k % 4) * 32) >> 4;
-                    mma_ss(tmem + g * 128, a + at, b + at, IS, k > 0);
-                }
-            }
-            mma_commit(&sh.s_full[g]);
-            if (last && !Q8)
-                mma_commit(&sh.q_empty[qs]);
-        }
-        __syncwarp();
-    };
-    auto values = [&](int g, int vs, bool first, bool last) {
-        // P of this group is in TMEM
-        if (!(ok = tile_wait_warp(&sh.p_ready[g], pphase[g], limit, sh)))
-            return;
-        pphase[g] ^= 1;
-        tc_after();
-        if (elect_one()) {
-            // V is read along its rows: blocks of 64 columns lie BLOCK apart, 16 rows are 2048 bytes
-            const uint32_t b = desc_lo(smem + C::V0 + vs * C::TILE, C::BLOCK);
-#pragma unroll
-            for (int k = 0; k < AT_UNIT / 16; ++k)
-                mma_ts(tmem + 256 + g * D, tmem + g * 128 + k * 8, b + ((k * 2048) >> 4), IO, !first || k > 0);
-            if (last)
-                mma_commit(&sh.o_full[g]);
-        }
-        __syncwarp();
-    };
-    auto take_k = [&](int &slot) {
-        slot = kr.slot;
-        ok = tile_wait_warp(&sh.k_full[kr.slot], kr.phase, limit, sh);
-        kr.next(C::NK);
-        tc_after();
-        return ok;
-    };
-    auto take_v = [&](int &slot) {
-        slot = vr.slot;
-        ok = tile_wait_warp(&sh.v_full[vr.slot], vr.phase, limit, sh);
-        vr.next(C::NV);
-        tc_after();
-        return ok;
-    };
     auto give = [&](unsigned long long *bar) {
         if (elect_one())
             mma_commit(bar);
         __syncwarp();
     };
-    auto clear_tail = [&](int slot, int nv) {
-        // V's rows past the stretch (the conversion from 8 bits leaves zeros there by itself)
-        if constexpr (!Q8) {
-            if (nv >= AT_UNIT)
-                return;
-            for (int k = 0; k < D / 64; ++k)
-                for (int i = nv * 8 + lane; i < AT_UNIT * 8; i += 32)
-                    *reinterpret_cast<uint4 *>(tiles + C::V0 + slot * C::TILE + k * C::BLOCK + i * 16) =
-                        make_uint4(0, 0, 0, 0);
-            async_fence();
-            __syncwarp();
-        }
-    };
-    Walk walk(P, sh);
+    Walk walk(P, sh.start);
     Item it;
+#pragma unroll 1
     while (ok && walk.next(it)) {
         it.n = uniform(it.n);
         it.two = uniform(it.two);
-        int qs[2], ks, vs;
+        const int q0 = q.slot;
         for (int g = 0; ok && g <= it.two; ++g) {
-            qs[g] = q.slot;
             ok = tile_wait_warp(Q8 ? &sh.q_ready[q.slot] : &sh.q_full[q.slot], q.phase, limit, sh);
             q.next(2);
         }
-        if (!ok)
-            break;
         tc_after();
-        if (it.two) {
-            if (!take_k(ks))
-                break;
-            scores(0, qs[0], ks, it.n == 1);
-            scores(1, qs[1], ks, it.n == 1);
-            give(&sh.k_empty[ks]);
-            for (int j = 0; ok && j < it.n; ++j) {
-                const bool last = j + 1 == it.n;
-                if (!take_v(vs))
-                    break;
-                clear_tail(vs, it.left - j * AT_UNIT);
-                values(0, vs, j == 0, last);
-                if (!ok || (!last && !take_k(ks)))
-                    break;
-                if (!last)
-                    scores(0, qs[0], ks, j + 2 == it.n);
-                values(1, vs, j == 0, last);
-                if (!ok)
-                    break;
-                give(&sh.v_empty[vs]);
-                if (!last) {
-                    scores(1, qs[1], ks, j + 2 == it.n);
-                    give(&sh.k_empty[ks]);
+        int ks = 0, vs = 0;
+        // S of group g and unit j; with K's next tile where it is the first to use it, and its last word on it
+        auto scores = [&](int g, int j, bool takes, bool gives) {
+            if (takes) {
+                ks = kr.slot;
+                ok = ok && tile_wait_warp(&sh.k_full[ks], kr.phase, limit, sh);
+                kr.next(C::NK);
+                tc_after();
+            }
+            if (ok && elect_one()) {
+                const int qs = (q0 + (it.two ? g : 0)) & 1;
+                const uint32_t a = desc_lo(smem + qs * C::TILE, 16), b = desc_lo(smem + C::K0 + ks * C::KT, 16);
+                if constexpr (Q8) {
+                    // two terms of Q: blocks of their own (D = 128), halves of a 128-byte row (D = 64)
+                    constexpr uint32_t TERM = D == 128 ? C::BLOCK : 64;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k)
+                            mma_ss8<D == 128 ? DESC_128 : DESC_64>(tmem + g * 128, a + ((t * TERM + k * 32) >> 4),
+                                                                   b + ((k * 32) >> 4), IS, t + k > 0);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t at = ((k / 4) * C::BLOCK + (k % 4) * 32) >> 4;
+                        mma_ss(tmem + g * 128, a + at, b + at, IS, k > 0);
+                    }
                 }
+                mma_commit(&sh.s_full[g]);
+                if (gives)
+                    mma_commit(&sh.k_empty[ks]);
+                if (!Q8 && j + 1 == it.n)   // the last product with this Q
+                    mma_commit(&sh.q_empty[qs]);
+            }
+            __syncwarp();
+        };
+        // O of group g takes unit j
+        auto values = [&](int g, int j, bool takes, bool gives) {
+            if (takes) {
+                vs = vr.slot;
+                ok = ok && tile_wait_warp(&sh.v_full[vs], vr.phase, limit, sh);
+                vr.next(C::NV);
+                tc_after();
+                const int nv = it.left - j * AT_UNIT;
+                if (!Q8 && ok && nv < AT_UNIT) {
+                    // V's rows past the stretch (the conversion from 8 bits leaves zeros there by itself)
+#pragma unroll 1
+                    for (int k = 0; k < D / 64; ++k)
+#pragma unroll 1
+                        for (int x = nv * 8 + lane; x < AT_UNIT * 8; x += 32)
+                            *reinterpret_cast<uint4 *>(tiles + C::V0 + vs * C::TILE + k * C::BLOCK + x * 16) =
+                                make_uint4(0, 0, 0, 0);
+                    async_fence();
+                    __syncwarp();
+                }
+            }
+            // P of this group is in TMEM
+            ok = ok && tile_wait_warp(&sh.p_ready[g], (g ? pphase >> 1 : pphase) & 1, limit, sh);
+            pphase ^= 1u << g;
+            tc_after();
+            if (ok && elect_one()) {
+                // V is read along its rows: blocks of 64 columns lie BLOCK apart, 16 rows are 2048 bytes
+                const uint32_t b = desc_lo(smem + C::V0 + vs * C::TILE, C::BLOCK);
+                const int step = it.two ? 1 : 2;
+#pragma unroll
+                for (int k = 0; k < AT_UNIT / 16; ++k)
+                    mma_ts(tmem + 256 + g * D, tmem + g * 128 + k * 8, b + ((k * 2048) >> 4), IO, j >= step || k > 0);
+                if (gives)
+                    mma_commit(&sh.v_empty[vs]);
+                if (j + step >= it.n)
+                    mma_commit(&sh.o_full[g]);
+            }
+            __syncwarp();
+        };
+        if (it.two) {
+#pragma unroll 1
+            for (int j = -1; ok && j < it.n; ++j) {
+                const bool more = j + 1 < it.n;
+                if (j >= 0)
+                    values(0, j, true, false);
+                if (more)
+                    scores(0, j + 1, true, false);
+                if (j >= 0)
+                    values(1, j, false, true);
+                if (more)
+                    scores(1, j + 1, false, true);
             }
         } else {
-            for (int j = 0; ok && j < min(2, it.n); ++j) {
-                if (!take_k(ks))
-                    break;
-                scores(j, qs[0], ks, j + 1 == it.n);
-                give(&sh.k_empty[ks]);
-            }
-            for (int j = 0; ok && j < it.n; ++j) {
-                if (!take_v(vs))
-                    break;
-                clear_tail(vs, it.left - j * AT_UNIT);
-                values(j & 1, vs, j < 2, j + 2 >= it.n);
-                if (!ok)
-                    break;
-                give(&sh.v_empty[vs]);
-                if (j + 2 < it.n) {
-                    if (!take_k(ks))
-                        break;
-                    scores(j & 1, qs[0], ks, j + 3 == it.n);
-                    give(&sh.k_empty[ks]);
-                }
+#pragma unroll 1
+            for (int i = 0; ok && i < 2 * it.n; ++i) {
+                const auto [j, kind] = item_tile(it, i);
+                if (kind)
+                    values(j & 1, j, true, true);
+                else
+                    scores(j & 1, j, true, true);
             }
         }
-        // 8-bit entries: the softmax groups have read the rows' units, too
+        // 8-bit entries: the softmax groups have read the rows' scales, too
         if (Q8)
             for (int g = 0; ok && g <= it.two; ++g)
-                give(&sh.q_empty[qs[g]]);
+                give(&sh.q_empty[it.two ? (q0 + g) & 1 : q0]);
     }
     if (!ok) {
         give(&sh.drain);
@@ -593,111 +607,241 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint8_t *tiles, ui
     }
 }
 
-// Softmax of group g: thread w * 32 + lane owns row w * 32 + lane of the
-// group's tile (a warp reaches only its own quarter of the TMEM lanes).
-template <int D, bool Q8>
-__device__ void softmax_role(const TileParams &P, QuantShared &sh, int g, uint32_t limit)
+// Raises a row's reference exponent m to its scores' maximum s where that has
+// passed it by more than 8, and scales l and O down with it.
+template <int D>
+__device__ __forceinline__ void follow_maximum(uint32_t to, float s, bool first, bool real, float &m, float &l)
 {
-    const int lane = threadIdx.x & 31, w = (threadIdx.x / 32) & 3, row = w * 32 + lane;
+    const bool up = real && s > m + 8.0f;
+    if (!__any_sync(0xffffffffu, up))
+        return;
+    const float f = up ? ex2a(m - s) : 1.0f;   // 2^(-inf) = 0 the first time
+    if (up) {
+        m = s;
+        l *= f;
+    }
+    if (first)
+        return;
+    // this group's last P V has completed: S after it has
+#pragma unroll 1
+    for (int k = 0; k < D; k += 32) {
+        float o[32];
+        uint32_t y[32];
+        tmem_ld(to + k, o);
+#pragma unroll
+        for (int u = 0; u < 32; ++u)
+            y[u] = __float_as_uint(o[u] * f);
+        tmem_st(to + k, y);
+    }
+}
+
+// One unit of a softmax group: this thread's row (`real`: it is one) of S, of
+// which `nv` columns belong to the stretch, becomes its row of P.
+template <int D>
+__device__ __forceinline__ void softmax_unit(uint32_t ts, uint32_t to, int nv, float c, bool first, bool real,
+                                             float &m, float &l)
+{
+    float x[AT_UNIT];
+    tmem_ld(ts, x);
+    if (nv < AT_UNIT) {
+#pragma unroll
+        for (int k = 0; k < AT_UNIT; ++k)
+            x[k] = k < nv ? x[k] : -F_INF;
+    }
+    float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+    for (int k = 4; k < AT_UNIT; k += 4)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            top[u] = fmaxf(top[u], x[k + u]);
+    follow_maximum<D>(to, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c, first, real, m, l);
+    const float ref = m == -F_INF ? 0.0f : m;
+    const f2 cc = pk(c, c), nref = pk(-ref, -ref);
+    f2 sum[2] = {pk(0.0f, 0.0f), pk(0.0f, 0.0f)};
+    // P's 64 columns lie over those of S, which this thread has read
+#pragma unroll
+    for (int h = 0; h < AT_UNIT / 2; h += 32) {
+        uint32_t p[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+            const f2 e = ex2x2(fma2(pk(x[2 * (h + k)], x[2 * (h + k) + 1]), cc, nref));
+            sum[k & 1] = add2(sum[k & 1], e);
+            float lo, hi;
+            upk(e, lo, hi);
+            p[k] = pack_bf16(lo, hi);
+        }
+        tmem_st(ts + h, p);
+    }
+    float lo, hi;
+    upk(add2(sum[0], sum[1]), lo, hi);
+    l += lo + hi;
+    tmem_st_wait();
+}
+
+// The same with 8-bit entries, over this copy's `nc` columns from `col` on (nv
+// of them in the stretch): scores times the scales of their rows of K, V's unit
+// in the exponent, P in float16.  In steps of 32 columns, twice over S: the
+// loops are short on purpose, the warps of this kernel run six different
+// programs and have to share the instruction cache.
+template <int D>
+__device__ __forceinline__ void softmax_unit8(uint32_t ts, uint32_t to, int col, int nc, int nv, float c, float bv,
+                                              const float4 *k_fac, bool first, bool real, float &m, float &l)
+{
+    float x[32];
+    auto load = [&](int k0) {
+        tmem_ld(ts + col + k0, x);
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+            const float4 y = k_fac[(k0 + k) / 4];
+            upk(mul2(pk(x[k], x[k + 1]), pk(y.x, y.y)), x[k], x[k + 1]);
+            upk(mul2(pk(x[k + 2], x[k + 3]), pk(y.z, y.w)), x[k + 2], x[k + 3]);
+        }
+        if (nv < k0 + 32) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                x[k] = k0 + k < nv ? x[k] : -F_INF;
+        }
+    };
+    float top[4] = {-F_INF, -F_INF, -F_INF, -F_INF};
+#pragma unroll 1
+    for (int k0 = 0; k0 < nc; k0 += 32) {
+        load(k0);
+#pragma unroll
+        for (int k = 0; k < 32; k += 4)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                top[u] = fmaxf(top[u], x[k + u]);
+    }
+    follow_maximum<D>(to, fmaf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), c, bv), first, real, m, l);
+    const float ref = (m == -F_INF ? 0.0f : m) - bv;
+    const f2 cc = pk(c, c), nref = pk(-ref, -ref);
+    f2 sum[2] = {pk(0.0f, 0.0f), pk(0.0f, 0.0f)};
+    uint32_t p[16];
+    // a step's P lies over columns of S that this thread has read, or does not read at all
+#pragma unroll 1
+    for (int k0 = 0; k0 < nc; k0 += 32) {
+        load(k0);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const f2 e = ex2x2(fma2(pk(x[2 * k], x[2 * k + 1]), cc, nref));
+            sum[k & 1] = add2(sum[k & 1], e);
+            float lo, hi;
+            upk(e, lo, hi);
+            p[k] = pack_f16(lo, hi);
+        }
+        tmem_st(ts + (col + k0) / 2, p);
+    }
+    // nothing from the other copies' columns
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+        p[k] = 0;
+#pragma unroll 1
+    for (int k0 = nc; k0 < AT_UNIT; k0 += 32)
+        tmem_st(ts + ((col + k0) & (AT_UNIT - 1)) / 2, p);
+    float lo, hi;
+    upk(add2(sum[0], sum[1]), lo, hi);
+    l += (lo + hi) * ex2a(-bv);   // a power of two: exact
+    tmem_st_wait();
+}
+
+// The eight softmax warps.  Warps that gave up keep coming here, item by item.
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// Joins the partial results of an item with one set of rows: both groups, and
+// every copy, in chunks of columns by way of the item's Q tile, which nothing
+// reads any more.  `weight` is that of this thread's part of its row, `any`
+// whether its warp has values at all.
+template <int D>
+__device__ __forceinline__ void join_parts(uint8_t *scratch, uint32_t to, int part, int parts, int row, int have,
+                                           bool any, float weight, float *dst)
+{
+    constexpr int CW = D / 4;        // columns of a chunk: 256 rows of them fill the Q tile
+    constexpr int V = CW / 4;        // 16-byte vectors of a row's chunk
+    const int tid = threadIdx.x;     // of 256
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+        float o[32];
+        if (any)
+            tmem_ld(to + k * CW, o);
+        if (row < have) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                *reinterpret_cast<float4 *>(scratch + ((part * have + row) * V + (v ^ (row % V))) * 16) =
+                    !any || weight == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                                           : make_float4(o[4 * v] * weight, o[4 * v + 1] * weight,
+                                                         o[4 * v + 2] * weight, o[4 * v + 3] * weight);
+        }
+        softmax_sync();
+#pragma unroll 1
+        for (int i = tid; i < have * V; i += 256) {
+            const int r = i / V, v = i % V;
+            float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int p = 0; p < parts; ++p) {
+                const float4 z = *reinterpret_cast<const float4 *>(scratch + ((p * have + r) * V + (v ^ (r % V))) * 16);
+                y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
+            }
+            *reinterpret_cast<float4 *>(dst + (size_t)r * D + k * CW + v * 4) = y;
+        }
+        if (k == 3)
+            async_fence();   // the tile is TMA's next
+        softmax_sync();
+    }
+}
+
+// Softmax of group g: a thread owns a row of the group's tile (a warp reaches
+// only its own quarter of the TMEM lanes).
+template <int D, bool Q8>
+__device__ void softmax_role(const TileParams &P, QuantShared &sh, uint8_t *tiles, int g, uint32_t limit)
+{
+    using C = TileCfg<D, Q8>;
+    const int lane = threadIdx.x & 31, w = (threadIdx.x / 32) & 3;
     const uint32_t lanes = (uint32_t)(w * 32) << 16;
     const uint32_t ts = sh.tmem + lanes + g * 128, to = sh.tmem + lanes + 256 + g * D;
-    float c = P.A.c, bv = 0.0f, unbv = 1.0f;
+    float c = P.A.c, bv = 0.0f;
     int unit = 0;   // of the CTA, as the item starts
     uint32_t sphase = 0, ophase = 0;
+    bool ok = true;
     Ring q;
-    Walk walk(P, sh);
+    Walk walk(P, sh.start);
     Item it;
+#pragma unroll 1
     for (; walk.next(it); unit += it.n) {
         // the slot of this group's Q tile: the second of two, or the only one
         const int qs = it.two ? (q.slot + g) & 1 : q.slot;
         if (!it.two)
             q.next(2);
-        const int tq = it.b < 0 ? P.W.pre.tq : P.W.own.tq, rows = tq * P.A.G;
+        const bool pre = it.b < 0;
+        const int tq = pre ? P.W.pre.tq : P.W.own.tq, rows = tq * P.A.G;
+        // this warp's copy of the rows, its columns and its row of the copy
+        const int copies = Q8 ? it.copies : 1, quarters = 4 / copies, copy = w / quarters, col = copy * (AT_UNIT / copies);
+        const int row = (w - copy * quarters) * 32 + lane;
         // rows of this group's tile that exist
         const int have = min(max(it.tokens - (it.two ? g * tq : 0), 0), tq) * P.A.G;
-        const bool active = w * 32 < have;
+        const bool active = row - lane < have;
         const int cnt = it.two ? it.n : (it.n - g + 1) / 2;
         float m = -F_INF, l = 0.0f;
-        for (int i = 0; i < cnt; ++i) {
-            const int j = it.two ? i : 2 * i + g, nv = it.left - j * AT_UNIT;
-            if (!tile_wait_warp(&sh.s_full[g], sphase, limit, sh))
-                return;
+#pragma unroll 1
+        for (int i = 0; ok && i < cnt; ++i) {
+            const int j = it.two ? i : 2 * i + g, nv = it.left - j * AT_UNIT - col;
+            if (!(ok = tile_wait_warp(&sh.s_full[g], sphase, limit, sh)))
+                break;
             sphase ^= 1;
             tc_after();
             const int fs = (unit + j) % FAC;
-            if (Q8 && !tile_wait_warp(&sh.f_full[fs], ((unit + j) / FAC) & 1, limit, sh))
-                return;
+            if (Q8 && !(ok = tile_wait_warp(&sh.f_full[fs], ((unit + j) / FAC) & 1, limit, sh)))
+                break;
             if (active) {
-                float x[AT_UNIT];
-                tmem_ld(ts, x);
                 if constexpr (Q8) {
                     // written before Q was handed to the tensor cores that made S
                     if (i == 0)
-                        c = P.A.c * fp8_factor(sh.q_unit[qs][row]);
+                        c = P.A.c * fp8_factor(sh.q_unit[qs][w * 32 + lane]);
                     bv = sh.v_unit[fs];
-                    unbv = ex2a(-bv);   // a power of two: exact
-#pragma unroll
-                    for (int k = 0; k < AT_UNIT; k += 4) {
-                        const float4 y = sh.k_fac[fs][k / 4];
-                        upk(mul2(pk(x[k], x[k + 1]), pk(y.x, y.y)), x[k], x[k + 1]);
-                        upk(mul2(pk(x[k + 2], x[k + 3]), pk(y.z, y.w)), x[k + 2], x[k + 3]);
-                    }
                 }
-                if (nv < AT_UNIT) {
-#pragma unroll
-                    for (int k = 0; k < AT_UNIT; ++k)
-                        x[k] = k < nv ? x[k] : -F_INF;
-                }
-                float top[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                for (int k = 4; k < AT_UNIT; k += 4)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        top[u] = fmaxf(top[u], x[k + u]);
-                float s = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
                 if constexpr (Q8)
-                    s += bv;
-                const bool up = s > m + 8.0f;
-                if (__any_sync(0xffffffffu, up)) {
-                    const float f = up ? ex2a(m - s) : 1.0f;   // 2^(-inf) = 0 the first time
-                    if (up) {
-                        m = s;
-                        l *= f;
-                    }
-                    if (i > 0) {
-                        // this group's last P V has completed: S after it has
-#pragma unroll 1
-                        for (int k = 0; k < D; k += 32) {
-                            float o[32];
-                            tmem_ld32(to + k, o);
-#pragma unroll
-                            for (int u = 0; u < 32; ++u)
-                                o[u] *= f;
-                            tmem_st32(to + k, reinterpret_cast<uint32_t *>(o));
-                        }
-                    }
-                }
-                const float ref = (m == -F_INF ? 0.0f : m) - bv;
-                const f2 cc = pk(c, c), nref = pk(-ref, -ref);
-                f2 sum[2] = {pk(0.0f, 0.0f), pk(0.0f, 0.0f)};
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    // P's 64 columns lie over those of S, which this thread has read
-                    uint32_t p[32];
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const f2 e = ex2x2(fma2(pk(x[hf * 64 + 2 * k], x[hf * 64 + 2 * k + 1]), cc, nref));
-                        sum[k & 1] = add2(sum[k & 1], e);
-                        float lo, hi;
-                        upk(e, lo, hi);
-                        p[k] = Q8 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
-                    }
-                    tmem_st32(ts + hf * 32, p);
-                }
-                float lo, hi;
-                upk(add2(sum[0], sum[1]), lo, hi);
-                l += Q8 ? (lo + hi) * unbv : lo + hi;
-                tmem_st_wait();
+                    softmax_unit8<D>(ts, to, col, AT_UNIT / copies, nv, c, bv, sh.k_fac[fs] + col / 4, i == 0,
+                                     row < have, m, l);
+                else
+                    softmax_unit<D>(ts, to, nv, c, i == 0, row < have, m, l);
             }
             tc_before();
             __syncwarp();
@@ -707,107 +851,114 @@ __device__ void softmax_role(const TileParams &P, QuantShared &sh, int g, uint32
                     mbar_arrive_n(&sh.f_empty[fs], it.two ? 1 : 2);
             }
         }
-        const size_t at = ((size_t)it.slot * 2 + g) * rows + row;
-        const bool pre = it.b < 0;
-        if (row < have)
-            (pre ? P.W.ml_p : P.W.ml_s)[at] = make_float2(m, l);
-        if (cnt > 0) {
-            if (!tile_wait_warp(&sh.o_full[g], ophase, limit, sh))
-                return;
-            ophase ^= 1;
-            tc_after();
-            if (active) {
-                float *dst = (pre ? P.W.o_p : P.W.o_s) + at * D;
+        if (ok && cnt > 0) {
+            if ((ok = tile_wait_warp(&sh.o_full[g], ophase, limit, sh))) {
+                ophase ^= 1;
+                tc_after();
+            }
+        }
+        float2 *const ml = pre ? P.W.ml_p : P.W.ml_s;
+        float *const o_all = pre ? P.W.o_p : P.W.o_s;
+        if (Q8 && it.join) {
+            const size_t at = (size_t)it.slot * 2 * rows;
+            sh.ml[g][w * 32 + lane] = make_float2(m, l);
+            softmax_sync();
+            float top = -F_INF, sum = 0.0f;
+#pragma unroll 1
+            for (int p = 0; p < 2 * copies; ++p)
+                top = fmaxf(top, sh.ml[p & 1][(p >> 1) * (AT_ROWS / copies) + row].x);
+            const float ref = top == -F_INF ? 0.0f : top;
+#pragma unroll 1
+            for (int p = 0; p < 2 * copies; ++p) {
+                const float2 y = sh.ml[p & 1][(p >> 1) * (AT_ROWS / copies) + row];
+                sum += y.y == 0.0f ? 0.0f : y.y * ex2a(y.x - ref);
+            }
+            if (g == 0 && copy == 0 && row < have) {
+                ml[at + row] = make_float2(top, sum);
+                ml[at + rows + row] = make_float2(-F_INF, 0.0f);
+            }
+            join_parts<D>(tiles + qs * C::TILE, to, copy * 2 + g, 2 * copies, row, have, ok && cnt > 0 && active,
+                          l == 0.0f ? 0.0f : ex2a(m - ref), o_all + at * D);
+            if (ok && threadIdx.x == 0)
+                mbar_arrive(&sh.q_empty[qs]);
+        } else {
+            const size_t at = ((size_t)it.slot * 2 + g) * rows + row;
+            if (row < have)
+                ml[at] = make_float2(m, l);
+            if (ok && cnt > 0 && active) {
 #pragma unroll 1
                 for (int k = 0; k < D; k += 32) {
                     float o[32];
-                    tmem_ld32(to + k, o);
+                    tmem_ld(to + k, o);
                     if (row < have) {
 #pragma unroll
                         for (int u = 0; u < 32; u += 8)
-                            store8(dst + k + u, o + u);
+                            store8(o_all + at * D + k + u, o + u);
                     }
                 }
             }
-            tc_before();
+            if (Q8 && ok && w == 0 && lane == 0 && (it.two || g == 0))
+                mbar_arrive(&sh.q_empty[qs]);
         }
+        tc_before();
     }
 }
 
-// 8-bit entries: the scale bytes of three units are in flight in one warp's
-// registers (rows lane, lane + 32, ..), which turns them into factors.
+// 8-bit entries: one warp turns the units' scale bytes into factors, up to FAC
+// units ahead; the bytes of later units are asked into the caches meanwhile.
 __device__ __forceinline__ void scale_role(const TileParams &P, QuantShared &sh, uint32_t limit)
 {
     const int lane = threadIdx.x & 31;
-    Walk walk(P, sh);
+    const int stride = 2 * P.A.H;   // bytes from an entry to the next
+    Walk walk(P, sh.start);
     Item it;
-    int j = 0;
-    bool more = walk.next(it);
     Ring r;
-    struct Bytes {
-        int nv;
-        uint32_t b[2][4];
-    };
-    auto fetch = [&](Bytes &x) {
-        x.nv = 0;
-        if (!more)
-            return;
-        x.nv = it.left - j * AT_UNIT;
-        const uint8_t *sc = (it.b < 0 ? P.A.pscale : P.A.cscale + (size_t)it.b * P.A.L * 2 * P.A.H) +
-                            (size_t)(it.e0 + j * AT_UNIT) * 2 * P.A.H + it.h;
+#pragma unroll 1
+    while (walk.next(it)) {
+        const uint8_t *sc = (it.b < 0 ? P.A.pscale : P.A.cscale + (size_t)it.b * P.A.L * stride) + (size_t)it.e0 * stride + it.h;
+        int asked = 0;
+#pragma unroll 1
+        for (int j = 0; j < it.n; ++j) {
+#pragma unroll 1
+            for (; asked < min(it.n, j + 2 * FAC); ++asked)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i)
+                    if (asked * AT_UNIT + i * 32 + lane < it.left)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(sc + (size_t)(asked * AT_UNIT + i * 32 + lane) * stride));
+            const int nv = it.left - j * AT_UNIT;
+            uint32_t kb[4], vb[4], top = 27;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                x.b[k][i] = 0;
-                if (i * 32 + lane < x.nv)
-                    x.b[k][i] = __ldg(sc + ((size_t)(i * 32 + lane) * 2 + k) * P.A.H);
+            for (int i = 0; i < 4; ++i) {
+                kb[i] = vb[i] = 0;
+                if (i * 32 + lane < nv) {
+                    const uint8_t *p = sc + (size_t)(j * AT_UNIT + i * 32 + lane) * stride;
+                    kb[i] = __ldg(p);
+                    vb[i] = __ldg(p + P.A.H);
+                }
             }
-        if (++j == it.n) {
-            j = 0;
-            more = walk.next(it);
-        }
-    };
-    auto publish = [&](const Bytes &x) {
-        if (x.nv <= 0 || !tile_wait_warp(&sh.f_empty[r.slot], r.phase ^ 1, limit, sh))
-            return false;
-        // V's are relative to the largest, no lower than 2^-100: l holds the weights times its reciprocal
-        uint32_t top = 27;
+            // V's are relative to the largest, no lower than 2^-100: l holds the weights times its reciprocal
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            top = max(top, x.b[1][i] == 255 ? 0u : x.b[1][i]);
-        top = __reduce_max_sync(0xffffffffu, top);
-        float *kf = reinterpret_cast<float *>(sh.k_fac[r.slot]);
+            for (int i = 0; i < 4; ++i)
+                top = max(top, vb[i] == 255 ? 0u : vb[i]);
+            top = __reduce_max_sync(0xffffffffu, top);
+            if (!tile_wait_warp(&sh.f_empty[r.slot], r.phase ^ 1, limit, sh))
+                return;
+            float *kf = reinterpret_cast<float *>(sh.k_fac[r.slot]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            kf[i * 32 + lane] = fp8_factor(x.b[0][i]);
-            // 2^(byte - top + 7) times the 2^8 that scale_e4m3 takes away
-            const int e = (int)x.b[1][i] - (int)top + 15 + 127;
-            const float f = x.b[1][i] == 255 ? __int_as_float(0x7fc00000) : __int_as_float(max(e, 0) << 23);
-            sh.v_fac[r.slot][i * 32 + lane] = (uint16_t)pack_f16(f, 0.0f);
+            for (int i = 0; i < 4; ++i) {
+                kf[i * 32 + lane] = fp8_factor(kb[i]);
+                // 2^(byte - top + 7) times the 2^8 that scale_e4m3 takes away
+                const int e = (int)vb[i] - (int)top + 15 + 127;
+                const float f = vb[i] == 255 ? __int_as_float(0x7fc00000) : __int_as_float(max(e, 0) << 23);
+                sh.v_fac[r.slot][i * 32 + lane] = (uint16_t)pack_f16(f, 0.0f);
+            }
+            if (lane == 0)
+                sh.v_unit[r.slot] = (float)((int)top - 7 - 127);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.f_full[r.slot]);
+            r.next(FAC);
         }
-        if (lane == 0)
-            sh.v_unit[r.slot] = (float)((int)top - 7 - 127);
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive(&sh.f_full[r.slot]);
-        r.next(FAC);
-        return true;
-    };
-    Bytes a, b, c;
-    fetch(a);
-    fetch(b);
-    fetch(c);
-    for (;;) {
-        if (!publish(a))
-            return;
-        fetch(a);
-        if (!publish(b))
-            return;
-        fetch(b);
-        if (!publish(c))
-            return;
-        fetch(c);
     }
 }
 
@@ -819,56 +970,72 @@ __device__ void convert_role(const TileParams &P, QuantShared &sh, uint8_t *tile
     using C = TileCfg<D, true>;
     const int lane = threadIdx.x & 31, w = (threadIdx.x / 32) & 3;
     Ring r, s, q;
-    Walk walk(P, sh);
+    Walk walk(P, sh.start);
     Item it;
     int unit = 0;   // of the CTA, as the item starts
 
-    // A Q tile, in place, eight lanes to a row and four rows at a time: both terms of a row go where
-    // the row was (D = 128: its two 128-byte pieces; D = 64: the two halves of its one).
-    auto convert_q = [&] {
+    // A Q tile, in place, eight lanes to a row and eight rows at a time: both terms of a row go
+    // where the row was (D = 128: its two 128-byte pieces; D = 64: the two halves of its one).
+    auto convert_q = [&](const Item &x) {
         if (!tile_wait_warp(&sh.q_full[q.slot], q.phase, limit, sh))
             return false;
         uint8_t *tile = tiles + q.slot * C::TILE;
-        for (int p = 0; p < 8; ++p) {
-            const int row = w * 32 + p * 4 + lane / 8, c = (lane % 8) ^ (row & 7);   // this lane's chunk of eight columns
-            uint8_t *at = tile + row * 128;
-            uint4 v[D / 64];
-            uint32_t top = 0;
+        // rows of a copy in this warp's quarter
+        const int quarters = 4 / x.copies, here = (x.b < 0 ? P.W.pre.tq : P.W.own.tq) * P.A.G - (w % quarters) * 32;
+#pragma unroll 1
+        for (int p0 = 0; p0 < 8 && p0 * 4 < here; p0 += 2) {
+            uint4 v[2][D / 64];
+            uint32_t top[2];
 #pragma unroll
-            for (int k = 0; k < D / 64; ++k) {
-                v[k] = *reinterpret_cast<const uint4 *>(at + k * C::BLOCK + (lane % 8) * 16);
-                top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[k].x & 0x7fff7fffu, v[k].y & 0x7fff7fffu),
-                                             __vmaxu2(v[k].z & 0x7fff7fffu, v[k].w & 0x7fff7fffu)));
+            for (int p = 0; p < 2; ++p) {
+                const uint8_t *at = tile + (w * 32 + (p0 + p) * 4 + lane / 8) * 128 + (lane % 8) * 16;
+                top[p] = 0;
+#pragma unroll
+                for (int k = 0; k < D / 64; ++k) {
+                    v[p][k] = *reinterpret_cast<const uint4 *>(at + k * C::BLOCK);
+                    top[p] = __vmaxu2(top[p], __vmaxu2(__vmaxu2(v[p][k].x & 0x7fff7fffu, v[p][k].y & 0x7fff7fffu),
+                                                       __vmaxu2(v[p][k].z & 0x7fff7fffu, v[p][k].w & 0x7fff7fffu)));
+                }
+                top[p] = max(top[p] & 0xffffu, top[p] >> 16);
             }
-            top = max(top & 0xffffu, top >> 16);
 #pragma unroll
             for (int o = 4; o; o >>= 1)
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            float inv;
-            const uint32_t byte = fp8_scale(top << 16, inv);
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+                    top[p] = max(top[p], __shfl_xor_sync(0xffffffffu, top[p], o));
             __syncwarp();   // every lane has its part of the rows
 #pragma unroll
-            for (int k = 0; k < D / 64; ++k) {
-                const uint32_t in[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-                uint32_t t0[2], t1[2];
+            for (int p = 0; p < 2; ++p) {
+                // this lane's chunk of eight columns: half c & 1 of a term's 16-byte chunk 4 k + c / 2
+                const int row = w * 32 + (p0 + p) * 4 + lane / 8, c = (lane % 8) ^ (row & 7);
+                uint8_t *at = tile + row * 128;
+                float inv;
+                const uint32_t byte = fp8_scale(top[p] << 16, inv);
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const float a = __uint_as_float(in[2 * u] << 16) * inv, b = __uint_as_float(in[2 * u] & 0xffff0000u) * inv;
-                    const float x = __uint_as_float(in[2 * u + 1] << 16) * inv, y = __uint_as_float(in[2 * u + 1] & 0xffff0000u) * inv;
-                    float z[4];
-                    t0[u] = pack_e4m3(a, b, x, y);
-                    unpack_e4m3(t0[u], z);
-                    t1[u] = pack_e4m3(a - z[0], b - z[1], x - z[2], y - z[3]);   // exact differences
+                for (int k = 0; k < D / 64; ++k) {
+                    const uint32_t in[4] = {v[p][k].x, v[p][k].y, v[p][k].z, v[p][k].w};
+                    uint32_t t0[2], t1[2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        float y[4], z[4];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            y[2 * e] = __uint_as_float(in[2 * u + e] << 16) * inv;
+                            y[2 * e + 1] = __uint_as_float(in[2 * u + e] & 0xffff0000u) * inv;
+                        }
+                        t0[u] = pack_e4m3(y[0], y[1], y[2], y[3]);
+                        unpack_e4m3(t0[u], z);
+                        t1[u] = pack_e4m3(y[0] - z[0], y[1] - z[1], y[2] - z[2], y[3] - z[3]);   // exact differences
+                    }
+                    const int chunk = 4 * k + c / 2, half = (c & 1) * 8;
+                    const uint32_t o0 = ((chunk ^ (row & 7)) << 4) + half;
+                    const uint32_t o1 = D == 128 ? C::BLOCK + o0 : (((chunk + 4) ^ (row & 7)) << 4) + half;
+                    *reinterpret_cast<uint2 *>(at + o0) = make_uint2(t0[0], t0[1]);
+                    *reinterpret_cast<uint2 *>(at + o1) = make_uint2(t1[0], t1[1]);
                 }
-                // columns 64 k + 8 c .. of a term: half c & 1 of its 16-byte chunk 4 k + c / 2
-                const int chunk = 4 * k + c / 2, half = (c & 1) * 8;
-                const uint32_t o0 = ((chunk ^ (row & 7)) << 4) + half;
-                const uint32_t o1 = D == 128 ? C::BLOCK + o0 : (((chunk + 4) ^ (row & 7)) << 4) + half;
-                *reinterpret_cast<uint2 *>(at + o0) = make_uint2(t0[0], t0[1]);
-                *reinterpret_cast<uint2 *>(at + o1) = make_uint2(t1[0], t1[1]);
+                if (lane % 8 == 0)
+                    sh.q_unit[q.slot][row] = (uint8_t)byte;
             }
-            if (lane % 8 == 0)
-                sh.q_unit[q.slot][row] = (uint8_t)byte;
         }
         async_fence();
         __syncwarp();
@@ -928,11 +1095,26 @@ __device__ void convert_role(const TileParams &P, QuantShared &sh, uint8_t *tile
         }
     };
 
-    for (; walk.next(it); unit += it.n) {
-        for (int k = 0; k <= it.two; ++k)
-            if (!convert_q())
-                return;
+    Item after;
+    bool more = walk.next(it), ready = false;
+#pragma unroll 1
+    while (more) {
+        more = walk.next(after);
+        bool early = false;
+#pragma unroll 1
         for (int j = 0; j < it.n; ++j) {
+            // the item's Q, or (one set of rows to both) the next item's as soon as it is there
+            int todo = j == 0 && !ready ? it.two + 1 : 0;
+            const bool now = todo > 0;
+            if (!now && more && !early && !it.two && !after.two &&
+                __all_sync(0xffffffffu, mbar_test(&sh.q_full[q.slot], q.phase))) {
+                todo = 1;
+                early = true;
+            }
+#pragma unroll 1
+            for (; todo; --todo)
+                if (!convert_q(now ? it : after))
+                    return;
             const int fs = (unit + j) % FAC;
             if (!(tile_wait_warp(&sh.f_full[fs], ((unit + j) / FAC) & 1, limit, sh) &&
                   tile_wait_warp(&sh.r_full[r.slot], r.phase, limit, sh) &&
@@ -950,6 +1132,9 @@ __device__ void convert_role(const TileParams &P, QuantShared &sh, uint8_t *tile
             r.next(C::NR);
             s.next(C::NV);
         }
+        unit += it.n;
+        ready = early;
+        it = after;
     }
 }
 
@@ -983,11 +1168,9 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
         sh.sums[warp] = upto;
     if (tid == 0) {
         sh.abort = 0;
-        sh.b0 = 0;
-        sh.base0 = P.W.ppairs * P.W.pu;
         for (int k = 0; k < 2; ++k) {
             mbar_init(&sh.q_full[k], 1);
-            mbar_init(&sh.q_empty[k], 1);
+            mbar_init(&sh.q_empty[k], Q8 ? 2 : 1);   // the tensor cores, and the softmax warps' last use
             mbar_init(&sh.q_ready[k], 4);
             mbar_init(&sh.s_full[k], 1);
             mbar_init(&sh.p_ready[k], 4);
@@ -1026,20 +1209,24 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
             before += k < warp ? sh.sums[k] : 0;
             total += sh.sums[k];
         }
-        if (tid == 0)
-            sh.total = total;
         const int HS = P.A.H * P.W.own.tiles, UP = P.W.ppairs * P.W.pu;
         const long long U = UP + (long long)HS * total;
-        const int start = attn_start(blockIdx.x, U, gridDim.x);
+        const int start = attn_start(blockIdx.x, U, gridDim.x), end = attn_start(blockIdx.x + 1, U, gridDim.x);
+        if (tid == 0 && start < UP) {
+            const int p = start / P.W.pu;
+            sh.start = Place{start, end, -1, p / P.W.pre.tiles, p % P.W.pre.tiles, start - p * P.W.pu};
+        } else if (tid == 0 && start == end) {
+            sh.start = Place{start, end, B, 0, 0, 0};   // nothing here
+        }
         int at = before + upto - sum;   // units of the sequences before this thread's run
         for (int b = tid * run; b < min(B, (tid + 1) * run); ++b) {
             const int u = seq_units(P.A, b);
             if (blockIdx.x == 0)
                 P.W.base[b] = at;
             const int lo = UP + at * HS;
-            if (start >= lo && start < lo + u * HS) {
-                sh.b0 = b;
-                sh.base0 = lo;
+            if (start < end && start >= lo && start < lo + u * HS) {
+                const int p = (start - lo) / u;
+                sh.start = Place{start, end, b, p / P.W.own.tiles, p % P.W.own.tiles, start - lo - p * u};
             }
             at += u;
         }
@@ -1050,7 +1237,7 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
 
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFT));
-        softmax_role<D, Q8>(P, sh, warp / 4, limit);
+        softmax_role<D, Q8>(P, sh, tiles, warp / 4, limit);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_REST));
         if (warp == W_LOAD) {

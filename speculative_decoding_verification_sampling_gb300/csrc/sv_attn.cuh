@@ -26,11 +26,13 @@ constexpr int AT_MAX_CTAS = 192;  // CTAs that the workspace is sized for
 
 // Tiles of one kind of pair: a tile holds tq tokens (tq * G <= 128 rows), an
 // item one or two tiles (two: both halves of the kernel work on the same
-// entries; one: they take turns).
+// entries; one: they take turns).  With 8-bit entries and few rows, the rows lie
+// in their tile `copies` times in long stretches, each copy for a part of the
+// entries, and what they leave is joined (`join`).
 struct AttnTiling {
-    int tq, two, tiles;
+    int tq, two, tiles, copies, join;
 };
-inline AttnTiling attn_tiling(long long tokens, int G)
+inline AttnTiling attn_tiling(long long tokens, int G, bool quant)
 {
     AttnTiling t;
     const int cap = AT_ROWS / G;
@@ -38,6 +40,8 @@ inline AttnTiling attn_tiling(long long tokens, int G)
     t.two = tokens > cap;
     const long long per = (long long)t.tq * (t.two ? 2 : 1);
     t.tiles = (int)((tokens + per - 1) / per);
+    t.copies = !quant || t.two || t.tq * G > 64 ? 1 : t.tq * G > 32 ? 2 : 4;
+    t.join = quant && !t.two;
     return t;
 }
 
@@ -50,11 +54,11 @@ struct AttnPlan {
     size_t base, stat, ml_p, o_p, ml_s, o_s, total;
 };
 
-inline AttnPlan attn_plan(int B, int T, int H, int G, int D, int P, int L)
+inline AttnPlan attn_plan(int B, int T, int H, int G, int D, int P, int L, bool quant)
 {
     AttnPlan a{};
-    a.pre = attn_tiling((long long)B * T, G);
-    a.own = attn_tiling(T, G);
+    a.pre = attn_tiling((long long)B * T, G, quant);
+    a.own = attn_tiling(T, G, quant);
     a.pu = (P + AT_UNIT - 1) / AT_UNIT;
     a.ppairs = P > 0 ? H * a.pre.tiles : 0;
     const long long spairs = L > 0 ? (long long)B * H * a.own.tiles : 0;
