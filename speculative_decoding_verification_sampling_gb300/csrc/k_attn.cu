@@ -80,6 +80,12 @@ __device__ __forceinline__ void load_values(const float *p, float (&y)[E])
     }
 }
 
+// The launches of the tile kernel ahead: none, one for all pairs, or one for the
+// prefix and one for the caches; and their CTAs.
+struct FinishLines {
+    int launches, pre_ctas, own_ctas;
+};
+
 // Many rows (WIDE = false): eight lanes per query row.  A warp works on four
 // heads of a token, and the index arithmetic and the loops over what they see
 // serve four rows.  Few rows (WIDE): a CTA per row, each of its warps taking a
@@ -87,7 +93,7 @@ __device__ __forceinline__ void load_values(const float *p, float (&y)[E])
 // be hundreds; the four are joined in shared memory.
 template <int D, bool WIDE>
 __global__ void __launch_bounds__(FW * 32)
-    va_finish(const __grid_constant__ AttnParams P, const __grid_constant__ AttnWork W, int ctas, int per_token)
+    va_finish(const __grid_constant__ AttnParams P, const __grid_constant__ AttnWork W, FinishLines L, int per_token)
 {
     constexpr int LPR = WIDE ? 32 : 8, E = D / LPR, NP = E / 2, AT = E < 8 ? E : 8;
     constexpr int STEP = WIDE ? LPR * FW : LPR;   // partial results looked up at a time
@@ -176,30 +182,33 @@ __global__ void __launch_bounds__(FW * 32)
         }
     }
     int code = bad ? 1 : 0;
-    if (ctas > 0) {
+    if (L.launches > 0) {
         asm volatile("griddepcontrol.wait;" ::: "memory");   // the tile kernel's results
         if (!bad) {
             // where this row's partial results are: over the prefix, then over its cache
-            const int HS = P.H * W.own.tiles, UP = W.ppairs * W.pu;
-            const long long U = UP + (long long)HS * __ldcg(W.base + P.B);
-            const int before = __ldcg(W.base + b);
+            const int HS = P.H * W.own.tiles;
+            // two lines: each kind of pair has its own; one: the prefix pairs come first on both's
+            const int two_lines = L.launches == 2, UP = W.ppairs * W.pu, first = two_lines ? 0 : UP;
+            const int before = P.L > 0 ? __ldcg(W.base + b) : 0;
+            const long long own_units = P.L > 0 ? (long long)HS * __ldcg(W.base + P.B) : 0;
+            const long long U0 = two_lines ? UP : UP + own_units, U1 = first + own_units;
             int cnt0 = 0, c0 = 0, pair0 = 0, grp0 = 0, row0 = 0, cnt1 = 0, c1 = 0, pair1 = 0, grp1 = 0, row1 = 0;
             if (W.ppairs) {
                 const int wide = W.pre.tq * (1 + W.pre.two), tile = bt / wide, in = bt - tile * wide;
                 pair0 = h * W.pre.tiles + tile;
                 grp0 = in >= W.pre.tq;
                 row0 = (in - grp0 * W.pre.tq) * P.G + g;
-                c0 = attn_owner(pair0 * W.pu, U, ctas);
-                cnt0 = (attn_owner((pair0 + 1) * W.pu - 1, U, ctas) - c0 + 1) << (1 - W.pre.two);
+                c0 = attn_owner(pair0 * W.pu, U0, L.pre_ctas);
+                cnt0 = (attn_owner((pair0 + 1) * W.pu - 1, U0, L.pre_ctas) - c0 + 1) << (1 - W.pre.two);
             }
             if (len > 0) {
                 const int wide = W.own.tq * (1 + W.own.two), tile = t / wide, in = t - tile * wide;
-                const int ub = (len + AT_UNIT - 1) / AT_UNIT, i = h * W.own.tiles + tile, u = UP + before * HS + i * ub;
+                const int ub = (len + AT_UNIT - 1) / AT_UNIT, i = h * W.own.tiles + tile, u = first + before * HS + i * ub;
                 pair1 = b * HS + i;
                 grp1 = in >= W.own.tq;
                 row1 = (in - grp1 * W.own.tq) * P.G + g;
-                c1 = attn_owner(u, U, ctas);
-                cnt1 = (attn_owner(u + ub - 1, U, ctas) - c1 + 1) << (1 - W.own.two);
+                c1 = attn_owner(u, U1, L.own_ctas);
+                cnt1 = (attn_owner(u + ub - 1, U1, L.own_ctas) - c1 + 1) << (1 - W.own.two);
             }
             const int all = cnt0 + cnt1;   // may differ between the warp's rows
             for (int i0 = 0; __any_sync(0xffffffffu, i0 < all); i0 += STEP) {
@@ -219,7 +228,7 @@ __global__ void __launch_bounds__(FW * 32)
                     const float2 ml = __ldcg((own ? W.ml_s : W.ml_p) + at);
                     pm = ml.x;
                     pl = ml.y;
-                    gave_up = __ldcg(W.stat + c) != 0;
+                    gave_up = __ldcg(W.stat + (own && two_lines ? AT_MAX_CTAS : 0) + c) != 0;
                 }
                 if (__any_sync(0xffffffffu, gave_up))
                     code = 7;
@@ -325,7 +334,7 @@ __global__ void __launch_bounds__(FW * 32)
 }
 
 template <int D, bool WIDE>
-cudaError_t finish(const AttnParams &P, const AttnWork &W, int ctas, cudaStream_t stream)
+cudaError_t finish(const AttnParams &P, const AttnWork &W, const FinishLines &L, cudaStream_t stream)
 {
     const int per_token = WIDE ? P.Hq : (P.Hq + FW * 4 - 1) / (FW * 4);
     cudaLaunchConfig_t cfg{};
@@ -336,8 +345,8 @@ cudaError_t finish(const AttnParams &P, const AttnWork &W, int ctas, cudaStream_
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = ctas > 0 ? 1 : 0;   // behind the tile kernel; alone it starts like any other
-    return cudaLaunchKernelEx(&cfg, va_finish<D, WIDE>, P, W, ctas, per_token);
+    cfg.numAttrs = L.launches > 0 ? 1 : 0;   // behind the tile kernel; alone it starts like any other
+    return cudaLaunchKernelEx(&cfg, va_finish<D, WIDE>, P, W, L, per_token);
 }
 
 }  // namespace
@@ -351,7 +360,8 @@ bool attention_fits(int B, int T, int H, int G, int D, int P, int L)
 
 size_t attention_workspace(int B, int T, int H, int G, int D, int P, int L)
 {
-    return attn_plan(B, T, H, G, D, P, L, false).total;
+    const size_t a = attn_plan(B, T, H, G, D, P, L, false).total, b = attn_plan(B, T, H, G, D, P, L, true).total;
+    return a > b ? a : b;
 }
 
 cudaError_t launch_attention(const AttnParams &P, bool quant, void *workspace, int sms, uint32_t spin_limit,
@@ -377,18 +387,56 @@ cudaError_t launch_attention(const AttnParams &P, bool quant, void *workspace, i
     W.ml_s = reinterpret_cast<float2 *>(w + a.ml_s);
     W.o_s = reinterpret_cast<float *>(w + a.o_s);
     // one CTA per SM, fewer where even full caches have fewer units
-    const int most = sms < AT_MAX_CTAS ? sms : AT_MAX_CTAS;
-    const int ctas = (int)(a.max_units < most ? a.max_units : most);
-    if (ctas > 0) {
-        const cudaError_t e = launch_attn_tiles(P, W, quant, ctas, spin_limit, stream);
+    const long long most = sms < AT_MAX_CTAS ? sms : AT_MAX_CTAS;
+    FinishLines L{};
+    auto tiles = [&](const AttnParams &A, const AttnWork &V, bool q8, long long units, int &ctas) {
+        ctas = (int)(units < most ? units : most);
+        if (ctas == 0)
+            return cudaSuccess;
+        const cudaError_t e = launch_attn_tiles(A, V, q8, ctas, L.launches > 0, spin_limit, stream);
+        if (e == cudaSuccess) {
+            ++*launches;
+            ++L.launches;
+        }
+        return e;
+    };
+    cudaError_t e;
+    if (a.split) {
+        KvQuantParams R{};
+        R.cache = static_cast<uint8_t *>(const_cast<void *>(P.prefix));   // read only
+        R.scale = const_cast<uint8_t *>(P.pscale);
+        R.out = w + a.prefix;
+        R.NL = R.B = 1;
+        R.K = R.L = P.P;
+        R.H = P.H;
+        R.D = P.D;
+        e = launch_kvq_read(R, false, stream);
         if (e != cudaSuccess)
             return e;
         ++*launches;
+        AttnParams A = P;
+        AttnWork V = W;
+        A.prefix = w + a.prefix;
+        A.L = 0;
+        V.base = nullptr;
+        e = tiles(A, V, false, (long long)a.ppairs * a.pu, L.pre_ctas);
+        if (e != cudaSuccess)
+            return e;
+        A = P;
+        A.P = 0;
+        V = W;
+        V.ppairs = 0;
+        V.stat += AT_MAX_CTAS;
+        e = tiles(A, V, true, a.max_units - (long long)a.ppairs * a.pu, L.own_ctas);
+    } else {
+        e = tiles(P, W, quant, a.max_units, L.pre_ctas);
+        L.own_ctas = L.pre_ctas;
     }
+    if (e != cudaSuccess)
+        return e;
     const bool wide = (long long)P.B * P.T * P.Hq <= WIDE_ROWS;
-    const cudaError_t e = P.D == 128
-                              ? (wide ? finish<128, true>(P, W, ctas, stream) : finish<128, false>(P, W, ctas, stream))
-                              : (wide ? finish<64, true>(P, W, ctas, stream) : finish<64, false>(P, W, ctas, stream));
+    e = P.D == 128 ? (wide ? finish<128, true>(P, W, L, stream) : finish<128, false>(P, W, L, stream))
+                   : (wide ? finish<64, true>(P, W, L, stream) : finish<64, false>(P, W, L, stream));
     if (e == cudaSuccess)
         ++*launches;
     return e;

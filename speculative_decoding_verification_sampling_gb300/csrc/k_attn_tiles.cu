@@ -1221,7 +1221,7 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
         int at = before + upto - sum;   // units of the sequences before this thread's run
         for (int b = tid * run; b < min(B, (tid + 1) * run); ++b) {
             const int u = seq_units(P.A, b);
-            if (blockIdx.x == 0)
+            if (blockIdx.x == 0 && P.W.base)
                 P.W.base[b] = at;
             const int lo = UP + at * HS;
             if (start < end && start >= lo && start < lo + u * HS) {
@@ -1230,7 +1230,7 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
             }
             at += u;
         }
-        if (blockIdx.x == 0 && tid == 0)
+        if (blockIdx.x == 0 && tid == 0 && P.W.base)
             P.W.base[B] = total;
     }
     __syncthreads();
@@ -1259,6 +1259,7 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sh.tmem) : "memory");
     if (tid == 0)
         P.W.stat[blockIdx.x] = sh.abort ? (int)ST_TIMEOUT : 0;
+    pdl_wait();   // behind another launch of this kernel: whoever waits for this one waits for both
 }
 
 // ------------------------------------------------------------------ host
@@ -1299,7 +1300,7 @@ bool make_map(CUtensorMap *map, bool codes, const void *base, int rank, const cu
 }
 
 template <int D, bool Q8>
-cudaError_t launch_tiles(const TileParams &P, int grid, cudaStream_t stream)
+cudaError_t launch_tiles(const TileParams &P, int grid, bool second, cudaStream_t stream)
 {
     using C = TileCfg<D, Q8>;
     if (!encode_tiled())
@@ -1335,19 +1336,30 @@ cudaError_t launch_tiles(const TileParams &P, int grid, cudaStream_t stream)
             return e;
         raised.fetch_or(bit, std::memory_order_relaxed);
     }
-    va_tiles<D, Q8><<<grid, C::THREADS, tile_smem<D, Q8>(), stream>>>(mq_pre, mq_own, m_pre, m_own, P);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = tile_smem<D, Q8>();
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = second ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, va_tiles<D, Q8>, mq_pre, mq_own, m_pre, m_own, P);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_tiles(const AttnParams &A, const AttnWork &W, bool quant, int grid, uint32_t spin_limit,
-                              cudaStream_t stream)
+// `second`: behind the launch for the prefix, as whose CTAs finish it may begin
+// (it needs nothing of it).
+cudaError_t launch_attn_tiles(const AttnParams &A, const AttnWork &W, bool quant, int grid, bool second,
+                              uint32_t spin_limit, cudaStream_t stream)
 {
     TileParams P{A, W, spin_limit};
     if (A.D == 128)
-        return quant ? launch_tiles<128, true>(P, grid, stream) : launch_tiles<128, false>(P, grid, stream);
-    return quant ? launch_tiles<64, true>(P, grid, stream) : launch_tiles<64, false>(P, grid, stream);
+        return quant ? launch_tiles<128, true>(P, grid, second, stream) : launch_tiles<128, false>(P, grid, second, stream);
+    return quant ? launch_tiles<64, true>(P, grid, second, stream) : launch_tiles<64, false>(P, grid, second, stream);
 }
 
 }  // namespace sv

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(QT) kvq_read(const __grid_constant__ KvQuantPa
     const int ch = blockIdx.x % P.nch;
     const long long lb = blockIdx.x / P.nch;
     const int b = (int)(lb % P.B);
-    const int len = __ldg(P.len_in + b), start = P.start ? __ldg(P.start + b) : 0;
+    const int len = P.len_in ? __ldg(P.len_in + b) : P.L, start = P.start ? __ldg(P.start + b) : 0;
     const bool bad = len < 0 || len > P.L || start < 0;
     if (bad && threadIdx.x == 0 && P.status)
         atomicCAS(P.status, 0, 1);

@@ -13,6 +13,13 @@
 // CTAs take one each and the others none, so no CTA in between is idle.  CTA c leaves one partial result per
 // pair it touches: (c, pair) runs along a staircase, on which c + pair never
 // repeats, so c + pair is its slot.
+//
+// An 8-bit prefix under many rows is read back to bfloat16 first: the products
+// over it bound the call then, and the kernel for bfloat16 entries runs them at
+// 1.4 times the rate of the one for codes (64 sequences of 32 tokens, 32 heads,
+// 8192 entries: 190 us and 301 us), while reading back takes 6 bytes per
+// element once. That breaks even at about 700 rows per key/value head. Prefix
+// and caches are then two lines, of one launch each.
 #pragma once
 #include <cstdint>
 
@@ -45,18 +52,22 @@ inline AttnTiling attn_tiling(long long tokens, int G, bool quant)
     return t;
 }
 
+constexpr long long READ_BACK_ROWS = 1024;   // rows per key/value head from which an 8-bit prefix is read back
+
 struct AttnPlan {
     AttnTiling pre, own;
+    int split;           // an 8-bit prefix is read back, prefix and caches are lines of their own
     int ppairs;          // prefix pairs
     int pu;              // units of a prefix pair
     long long max_units; // with every sequence at its capacity
     // byte offsets into the workspace
-    size_t base, stat, ml_p, o_p, ml_s, o_s, total;
+    size_t base, stat, ml_p, o_p, ml_s, o_s, prefix, total;
 };
 
 inline AttnPlan attn_plan(int B, int T, int H, int G, int D, int P, int L, bool quant)
 {
     AttnPlan a{};
+    a.split = quant && P > 0 && (long long)B * T * G >= READ_BACK_ROWS;
     a.pre = attn_tiling((long long)B * T, G, quant);
     a.own = attn_tiling(T, G, quant);
     a.pu = (P + AT_UNIT - 1) / AT_UNIT;
@@ -70,13 +81,14 @@ inline AttnPlan attn_plan(int B, int T, int H, int G, int D, int P, int L, bool 
         return o;
     };
     a.base = take(((size_t)B + 1) * 4);
-    a.stat = take(AT_MAX_CTAS * 4);
+    a.stat = take(2 * AT_MAX_CTAS * 4);
     const size_t rp = a.ppairs ? ((size_t)a.ppairs + AT_MAX_CTAS) * 2 * a.pre.tq * G : 0;
     const size_t rs = spairs ? ((size_t)spairs + AT_MAX_CTAS) * 2 * a.own.tq * G : 0;
     a.ml_p = take(rp * 8);
     a.o_p = take(rp * D * 4);
     a.ml_s = take(rs * 8);
     a.o_s = take(rs * D * 4);
+    a.prefix = take(a.split ? (size_t)P * 2 * H * D * 2 : 0);
     a.total = at;
     return a;
 }
@@ -102,7 +114,7 @@ __device__ __forceinline__ int attn_owner(int u, long long U, int ctas)
 struct AttnWork {
     AttnTiling pre, own;
     int ppairs, pu;
-    int32_t *base;   // [B + 1] units of the sequences before b (one pair's worth), then their total
+    int32_t *base;   // [B + 1] units of the sequences before b (one pair's worth), then their total; nullptr: not here
     int32_t *stat;   // [CTAs] 0, or the code of a CTA that gave up
     float2 *ml_p, *ml_s;   // [slot][2][tq * G] reference exponent and sum of a partial row
     float *o_p, *o_s;      // [slot][2][tq * G][D] its weighted values

@@ -252,7 +252,7 @@ struct KvQuantParams {
     const int32_t *acc;      // commit: [B]
     const int32_t *nodes;    // commit: [B][K] staged entries after the lead, or nullptr
     int32_t *len;            // commit: [B], updated
-    const int32_t *len_in;   // read: [B]
+    const int32_t *len_in;   // read: [B], or nullptr (L)
     const int32_t *start;    // read: [B] or nullptr (0)
     void *out;               // read: [NL][B][K][2][H][D]
     int32_t *status;         // [1] or nullptr

@@ -131,7 +131,11 @@ SHAPES = [
     (1, 3, 129, 3, 64, 40, 90, [90]),
     (33, 4, 4, 1, 128, 260, 30, list(range(0, 31)) + [30, 0]),
     (40, 5, 8, 2, 64, 2100, 60, [(7 * i) % 61 for i in range(40)]),   # 800 rows over the prefix
+    (70, 4, 8, 2, 128, 1000, 300, [(11 * i) % 301 for i in range(70)]),   # 1120 rows over the prefix
+    (33, 8, 4, 1, 64, 515, 20, [(3 * i) % 21 for i in range(33)]),        # 1056
     (2, 1, 8, 8, 128, 0, 5000, [5000, 4111]),
+    (3, 9, 8, 2, 128, 0, 2500, [2500, 1300, 1025]),  # 36 rows to a key head, long stretches
+    (2, 20, 8, 2, 64, 300, 3000, [3000, 1025]),      # 80
 ]
 
 
@@ -142,6 +146,22 @@ def test_matches_oracle(shape, quant, kind):
     B, T, Hq, H, D, P, L, lens = shape
     a = _case(B, T, Hq, H, D, P, L, lens, quant, kind, seed=B * 31 + T)
     _run(a, f"{shape} {quant} {kind}")
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_a_prefix_and_no_cache(quant):
+    g = torch.Generator(device=DEV).manual_seed(21)
+    r = lambda *s: torch.randn(s, generator=g, device=DEV).to(BF)   # noqa: E731
+    for B in (2, 300):
+        a = dict(q=r(B, 4, 4, 64), cache=r(B, 0, 2, 1, 64),
+                 seq_len=torch.zeros(B, dtype=torch.int32, device=DEV), staged=r(B, 4, 2, 1, 64))
+        if quant:
+            a["cache"] = a["cache"].to(torch.float8_e4m3fn)
+            a["cache_scale"] = torch.zeros((B, 0, 2, 1), dtype=torch.uint8, device=DEV)
+            a["prefix"], a["prefix_scale"] = _codes(g, 700, 2, 1, 64)
+        else:
+            a["prefix"] = r(700, 2, 1, 64)
+        _run(a, f"prefix alone, {B}")
 
 
 def test_no_prefix_no_cache():
