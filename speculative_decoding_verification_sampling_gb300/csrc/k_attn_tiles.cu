@@ -381,6 +381,19 @@ __device__ __forceinline__ bool tile_wait(unsigned long long *bar, uint32_t pari
     }
 }
 
+// Whether the phase has completed, without waiting (a try_wait would suspend
+// the thread for a while).
+__device__ __forceinline__ bool mbar_poll(unsigned long long *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(saddr(bar)), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+
 // The same for a whole warp: every lane waits, and all come to one answer.
 __device__ __forceinline__ bool tile_wait_warp(unsigned long long *bar, uint32_t parity, uint32_t limit, TileShared &sh)
 {
@@ -413,7 +426,7 @@ __device__ void load_role(const TileParams &P, const CUtensorMap *mq_pre, const 
         for (int s = 0; ok && s < 2 * it.n; ++s) {
             // the item's Q, or the next item's as soon as its place is free (with one set of rows to both)
             const bool now = s == 0 && !have_q;
-            if (now || (!early && more && !it.two && !after.two && mbar_test(&sh.q_empty[q.slot], q.phase ^ 1))) {
+            if (now || (!early && more && !it.two && !after.two && mbar_poll(&sh.q_empty[q.slot], q.phase ^ 1))) {
                 const Item &x = now ? it : after;
                 const bool pre = x.b < 0;
                 const CUtensorMap *mq = pre ? mq_pre : mq_own;
@@ -573,7 +586,8 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint8_t *tiles, ui
             }
             __syncwarp();
         };
-        if (it.two) {
+        // Two sets of rows: S0 S1, then for each unit P0 V, the next S0, P1 V, the next S1.
+        if (it.two && !Q8) {
 #pragma unroll 1
             for (int j = -1; ok && j < it.n; ++j) {
                 const bool more = j + 1 < it.n;
@@ -587,13 +601,26 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint8_t *tiles, ui
                     scores(1, j + 1, false, true);
             }
         } else {
+            // one set: as its tiles come (or two, from the same few instructions)
 #pragma unroll 1
-            for (int i = 0; ok && i < 2 * it.n; ++i) {
-                const auto [j, kind] = item_tile(it, i);
+            for (int i = 0; ok && i < it.n << (1 + it.two); ++i) {
+                int g, j, kind;
+                if (it.two) {
+                    const int r = i - 2, u = r >> 2;
+                    if (r < 0)
+                        g = i, j = 0, kind = 0;
+                    else if (u < it.n - 1)
+                        g = (r >> 1) & 1, kind = 1 - (r & 1), j = u + 1 - kind;
+                    else
+                        g = r & 1, kind = 1, j = u;
+                } else {
+                    const TileRef x = item_tile(it, i);
+                    g = x.unit & 1, j = x.unit, kind = x.kind;
+                }
                 if (kind)
-                    values(j & 1, j, true, true);
+                    values(g, j, !it.two || g == 0, !it.two || g == 1);
                 else
-                    scores(j & 1, j, true, true);
+                    scores(g, j, !it.two || g == 0, !it.two || g == 1);
             }
         }
         // 8-bit entries: the softmax groups have read the rows' scales, too
@@ -947,8 +974,7 @@ __device__ __forceinline__ void scale_role(const TileParams &P, QuantShared &sh,
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 kf[i * 32 + lane] = fp8_factor(kb[i]);
-                // 2^(byte - top + 7) times the 2^8 that scale_e4m3 takes away
-                const int e = (int)vb[i] - (int)top + 15 + 127;
+                const int e = (int)vb[i] - (int)top + 7 + 127;   // 2^(byte - top + 7)
                 const float f = vb[i] == 255 ? __int_as_float(0x7fc00000) : __int_as_float(max(e, 0) << 23);
                 sh.v_fac[r.slot][i * 32 + lane] = (uint16_t)pack_f16(f, 0.0f);
             }
@@ -1107,7 +1133,7 @@ __device__ void convert_role(const TileParams &P, QuantShared &sh, uint8_t *tile
             int todo = j == 0 && !ready ? it.two + 1 : 0;
             const bool now = todo > 0;
             if (!now && more && !early && !it.two && !after.two &&
-                __all_sync(0xffffffffu, mbar_test(&sh.q_full[q.slot], q.phase))) {
+                __all_sync(0xffffffffu, mbar_poll(&sh.q_full[q.slot], q.phase))) {
                 todo = 1;
                 early = true;
             }

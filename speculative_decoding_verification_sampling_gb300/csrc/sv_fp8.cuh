@@ -72,18 +72,20 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b)
     return r;
 }
 
-// Four codes (none the NaN code) to four float16, each times the float16 pair
-// `f` times 2^-8.  A code's exponent and mantissa bits, moved one place to the
-// right of the high byte of a float16, are the number's times 2^-8, the
-// subnormal ones too; four integer operations do it for two codes, and the
-// conversion instruction is slower.
+// Four codes to four float16, each times the float16 pair `f`.
 __device__ __forceinline__ void scale_e4m3(uint32_t w, uint32_t f, uint32_t &lo, uint32_t &hi)
 {
-    uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);   // codes in the high bytes
-    a = (a & 0x80008000u) | ((a >> 1) & 0x3f803f80u);
-    b = (b & 0x80008000u) | ((b >> 1) & 0x3f803f80u);
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(f));
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(f));
+    asm("{\n"
+        ".reg .b16 a, b;\n"
+        ".reg .b32 p, q;\n"
+        "mov.b32 {a, b}, %2;\n"
+        "cvt.rn.f16x2.e4m3x2 p, a;\n"
+        "cvt.rn.f16x2.e4m3x2 q, b;\n"
+        "mul.rn.f16x2 %0, p, %3;\n"
+        "mul.rn.f16x2 %1, q, %3;\n"
+        "}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w), "r"(f));
 }
 
 }  // namespace sv
