@@ -188,27 +188,31 @@ __global__ void __launch_bounds__(FW * 32)
             // where this row's partial results are: over the prefix, then over its cache
             const int HS = P.H * W.own.tiles;
             // two lines: each kind of pair has its own; one: the prefix pairs come first on both's
-            const int two_lines = L.launches == 2, UP = W.ppairs * W.pu, first = two_lines ? 0 : UP;
-            const int before = P.L > 0 ? __ldcg(W.base + b) : 0;
-            const long long own_units = P.L > 0 ? (long long)HS * __ldcg(W.base + P.B) : 0;
-            const long long U0 = two_lines ? UP : UP + own_units, U1 = first + own_units;
+            const int two_lines = L.launches == 2;
+            const int2 before = P.L > 0 ? __ldcg(W.base + b) : make_int2(0, 0);
+            const int2 total = P.L > 0 ? __ldcg(W.base + P.B) : make_int2(0, 0);
+            const AttnLine line0(W.pre, W.own, W.ppairs, W.pu, HS, two_lines ? 0 : total.x, two_lines ? 0 : total.y,
+                                 L.pre_ctas);
+            const AttnLine line1(W.pre, W.own, two_lines ? 0 : W.ppairs, W.pu, HS, total.x, total.y, L.own_ctas);
             int cnt0 = 0, c0 = 0, pair0 = 0, grp0 = 0, row0 = 0, cnt1 = 0, c1 = 0, pair1 = 0, grp1 = 0, row1 = 0;
             if (W.ppairs) {
                 const int wide = W.pre.tq * (1 + W.pre.two), tile = bt / wide, in = bt - tile * wide;
                 pair0 = h * W.pre.tiles + tile;
                 grp0 = in >= W.pre.tq;
                 row0 = (in - grp0 * W.pre.tq) * P.G + g;
-                c0 = attn_owner(pair0 * W.pu, U0, L.pre_ctas);
-                cnt0 = (attn_owner((pair0 + 1) * W.pu - 1, U0, L.pre_ctas) - c0 + 1) << (1 - W.pre.two);
+                const int at = pair0 * line0.pre.pair(W.pu);
+                c0 = line0.owner(at);
+                cnt0 = (line0.owner(at + line0.pre.begin(W.pu - 1)) - c0 + 1) << (1 - W.pre.two);
             }
             if (len > 0) {
                 const int wide = W.own.tq * (1 + W.own.two), tile = t / wide, in = t - tile * wide;
-                const int ub = (len + AT_UNIT - 1) / AT_UNIT, i = h * W.own.tiles + tile, u = first + before * HS + i * ub;
+                const int ub = (len + AT_UNIT - 1) / AT_UNIT, i = h * W.own.tiles + tile;
+                const int at = line1.own + HS * line1.sequences(before.x, before.y) + i * line1.own_cost.pair(ub);
                 pair1 = b * HS + i;
                 grp1 = in >= W.own.tq;
                 row1 = (in - grp1 * W.own.tq) * P.G + g;
-                c1 = attn_owner(u, U1, L.own_ctas);
-                cnt1 = (attn_owner(u + ub - 1, U1, L.own_ctas) - c1 + 1) << (1 - W.own.two);
+                c1 = line1.owner(at);
+                cnt1 = (line1.owner(at + line1.own_cost.begin(ub - 1)) - c1 + 1) << (1 - W.own.two);
             }
             const int all = cnt0 + cnt1;   // may differ between the warp's rows
             for (int i0 = 0; __any_sync(0xffffffffu, i0 < all); i0 += STEP) {
@@ -355,7 +359,7 @@ bool attention_fits(int B, int T, int H, int G, int D, int P, int L)
 {
     // units of the whole call, and every slot index, in 31 bits
     const AttnPlan a = attn_plan(B, T, H, G, D, P, L, false);
-    return a.max_units < (1LL << 31) && (long long)B * H * a.own.tiles < (1LL << 30);
+    return a.max_line < (1LL << 31) && (long long)B * H * a.own.tiles < (1LL << 30);
 }
 
 size_t attention_workspace(int B, int T, int H, int G, int D, int P, int L)
@@ -380,7 +384,7 @@ cudaError_t launch_attention(const AttnParams &P, bool quant, void *workspace, i
     W.own = a.own;
     W.ppairs = a.ppairs;
     W.pu = a.pu;
-    W.base = reinterpret_cast<int32_t *>(w + a.base);
+    W.base = reinterpret_cast<int2 *>(w + a.base);
     W.stat = reinterpret_cast<int32_t *>(w + a.stat);
     W.ml_p = reinterpret_cast<float2 *>(w + a.ml_p);
     W.o_p = reinterpret_cast<float *>(w + a.o_p);

@@ -228,11 +228,11 @@ struct TileCfg {
 constexpr int W_LOAD = 8, W_MMA = 9, W_SCALE = 10, W_CVT = 12;   // warps 0-7: softmax, two groups; 12-15: conversion
 constexpr int FAC = 4;   // units whose scales are ready ahead
 
-// Where on the line of units a CTA's part starts: sequence (-1: the prefix),
-// head and tile of the pair, unit of its stretch.
+// A CTA's length of the line, and the pair in which it begins: where that is on
+// the line, its sequence (-1: the prefix), head and tile.
 struct Place {
-    int cur, end;
-    int b, h, tile, off;
+    int from, to, pair, b, h, tile;
+    AttnCost pre, own;
 };
 
 struct TileShared {
@@ -242,7 +242,7 @@ struct TileShared {
     uint32_t tmem;
     volatile int abort;
     Place start;
-    int sums[16];                // per warp
+    unsigned long long sums[16];   // per warp
 };
 struct QuantShared : TileShared {
     alignas(16) float4 k_fac[FAC][AT_UNIT / 4];   // what a unit's rows of K stand for
@@ -301,29 +301,30 @@ struct Walk {
     }
     __device__ bool next(Item &it)
     {
-        if (at.cur >= at.end)
-            return false;
 #pragma unroll 1
-        while (units == 0)   // sequences without entries
-            units = seq_units(P.A, ++at.b);
-        const bool pre = at.b < 0;
-        const AttnTiling &tl = pre ? P.W.pre : P.W.own;
-        const int t0 = at.tile * (tl.tq << tl.two);
-        it.h = at.h;
-        it.b = at.b;
-        it.two = tl.two;
-        it.row0 = pre ? t0 : at.b * P.A.T + t0;
-        it.tokens = (pre ? P.A.B * P.A.T : P.A.T) - t0;
-        it.e0 = at.off * AT_UNIT;
-        it.left = (pre ? P.A.P : __ldg(P.A.len + at.b)) - it.e0;
-        it.slot = blockIdx.x + ((pre ? 0 : at.b * P.A.H) + at.h) * tl.tiles + at.tile;
-        it.n = min(units - at.off, at.end - at.cur);
-        it.join = tl.join && it.n >= JOIN_UNITS;
-        it.copies = it.join ? tl.copies : 1;
-        at.cur += it.n;
-        at.off += it.n;
-        if (at.off == units) {
-            at.off = 0;
+        while (at.pair < at.to) {
+#pragma unroll 1
+            while (units == 0)   // sequences without entries
+                units = seq_units(P.A, ++at.b);
+            const bool pre = at.b < 0;
+            const AttnCost cost = pre ? at.pre : at.own;
+            // the units that begin in this CTA's length
+            const int u0 = at.from <= at.pair ? 0 : cost.ahead(at.from - at.pair);
+            const int u1 = min(units, cost.ahead(at.to - at.pair));
+            const AttnTiling &tl = pre ? P.W.pre : P.W.own;
+            const int t0 = at.tile * (tl.tq << tl.two);
+            it.h = at.h;
+            it.b = at.b;
+            it.two = tl.two;
+            it.row0 = pre ? t0 : at.b * P.A.T + t0;
+            it.tokens = (pre ? P.A.B * P.A.T : P.A.T) - t0;
+            it.e0 = u0 * AT_UNIT;
+            it.left = (pre ? P.A.P : __ldg(P.A.len + at.b)) - it.e0;
+            it.slot = blockIdx.x + ((pre ? 0 : at.b * P.A.H) + at.h) * tl.tiles + at.tile;
+            it.n = u1 - u0;
+            it.join = tl.join && it.n >= JOIN_UNITS;
+            it.copies = it.join ? tl.copies : 1;
+            at.pair += cost.pair(units);
             if (++at.tile == tl.tiles) {
                 at.tile = 0;
                 if (++at.h == P.A.H) {
@@ -332,8 +333,10 @@ struct Walk {
                     units = at.b < P.A.B ? seq_units(P.A, at.b) : 0;
                 }
             }
+            if (it.n > 0)
+                return true;
         }
-        return true;
+        return false;
     }
 };
 
@@ -1179,15 +1182,19 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
     const uint32_t smem = saddr(tiles);
     const uint32_t limit = hinted_limit(P.spin_limit > OWN_WAIT_MIN ? P.spin_limit : OWN_WAIT_MIN);
 
-    // ---- where this CTA's line starts: sums over runs of sequences, then the run
+    // ---- where this CTA's length begins: sums over runs of sequences, then the run.  Units in the
+    // low word, sequences that have any in the high one.
+    typedef unsigned long long u64;
     const int B = P.A.B, run = (B + C::THREADS - 1) / C::THREADS;
-    int sum = 0;
-    for (int b = tid * run; b < min(B, (tid + 1) * run); ++b)
-        sum += seq_units(P.A, b);
-    int upto = sum;   // inclusive scan in the warp
+    u64 sum = 0;
+    for (int b = tid * run; b < min(B, (tid + 1) * run); ++b) {
+        const int u = seq_units(P.A, b);
+        sum += (u64)u | (u64)(u > 0) << 32;
+    }
+    u64 upto = sum;   // inclusive scan in the warp
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        const u64 y = __shfl_up_sync(0xffffffffu, upto, o);
         upto += tid % 32 >= o ? y : 0;
     }
     if (tid % 32 == 31)
@@ -1230,34 +1237,36 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
     __syncthreads();
     tc_after();
     {
-        int before = 0, total = 0;
+        u64 before = 0, total = 0;
+#pragma unroll 1
         for (int k = 0; k < C::THREADS / 32; ++k) {
             before += k < warp ? sh.sums[k] : 0;
             total += sh.sums[k];
         }
-        const int HS = P.A.H * P.W.own.tiles, UP = P.W.ppairs * P.W.pu;
-        const long long U = UP + (long long)HS * total;
-        const int start = attn_start(blockIdx.x, U, gridDim.x), end = attn_start(blockIdx.x + 1, U, gridDim.x);
-        if (tid == 0 && start < UP) {
-            const int p = start / P.W.pu;
-            sh.start = Place{start, end, -1, p / P.W.pre.tiles, p % P.W.pre.tiles, start - p * P.W.pu};
-        } else if (tid == 0 && start == end) {
-            sh.start = Place{start, end, B, 0, 0, 0};   // nothing here
+        const int HS = P.A.H * P.W.own.tiles;
+        const AttnLine line(P.W.pre, P.W.own, P.W.ppairs, P.W.pu, HS, (int)total, (int)(total >> 32), gridDim.x);
+        const int from = line.start(blockIdx.x), to = line.start(blockIdx.x + 1);
+        if (tid == 0 && from < line.own) {
+            const int one = line.pre.pair(P.W.pu), p = from / one;
+            sh.start = Place{from, to, p * one, -1, p / P.W.pre.tiles, p % P.W.pre.tiles, line.pre, line.own_cost};
+        } else if (tid == 0 && from == to) {
+            sh.start = Place{from, to, to, B, 0, 0, line.pre, line.own_cost};   // nothing here
         }
-        int at = before + upto - sum;   // units of the sequences before this thread's run
+        u64 at = before + upto - sum;   // of the sequences before this thread's run
+#pragma unroll 1
         for (int b = tid * run; b < min(B, (tid + 1) * run); ++b) {
             const int u = seq_units(P.A, b);
             if (blockIdx.x == 0 && P.W.base)
-                P.W.base[b] = at;
-            const int lo = UP + at * HS;
-            if (start < end && start >= lo && start < lo + u * HS) {
-                const int p = (start - lo) / u;
-                sh.start = Place{start, end, b, p / P.W.own.tiles, p % P.W.own.tiles, start - lo - p * u};
+                P.W.base[b] = make_int2((int)at, (int)(at >> 32));
+            const int lo = line.own + HS * line.sequences((int)at, (int)(at >> 32)), one = line.own_cost.pair(u);
+            if (from < to && from >= lo && from < lo + one * HS) {
+                const int p = (from - lo) / one;
+                sh.start = Place{from, to, lo + p * one, b, p / P.W.own.tiles, p % P.W.own.tiles, line.pre, line.own_cost};
             }
-            at += u;
+            at += (u64)u | (u64)(u > 0) << 32;
         }
         if (blockIdx.x == 0 && tid == 0 && P.W.base)
-            P.W.base[B] = total;
+            P.W.base[B] = make_int2((int)total, (int)(total >> 32));
     }
     __syncthreads();
 

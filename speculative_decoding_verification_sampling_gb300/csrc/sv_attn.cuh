@@ -7,12 +7,17 @@
 //     over the P prefix entries;
 //   - sequence pairs: one sequence, one key/value head and a tile of its
 //     tokens, over its own cache entries.
-// A pair's entries come in units of 128.  The units of all pairs, prefix
-// pairs first, form one line that is cut into equal lengths, one per CTA, so
-// ragged lengths balance by themselves; with fewer units than CTAs, the first
-// CTAs take one each and the others none, so no CTA in between is idle.  CTA c leaves one partial result per
-// pair it touches: (c, pair) runs along a staircase, on which c + pair never
-// repeats, so c + pair is its slot.
+// A pair's entries come in units of 128.  All pairs, prefix pairs first, form
+// one line, on which a pair is as long as it takes: so much for each unit, and
+// so much for the pair (Q, the first product, the results).  The line is cut
+// into equal lengths, one per CTA, so ragged lengths balance by themselves; a
+// CTA takes the units that begin in its length (the first one begins with the
+// pair).  No length is shorter than the longest unit, so every CTA between a
+// pair's first and its last has units of it.  Where there are fewer than
+// SPREAD units per CTA, every unit counts 1 and a pair nothing: the call is
+// short, and all the CTAs are better used than evenly loaded.
+// CTA c leaves one partial result per pair it touches: (c, pair) runs along a
+// staircase, on which c + pair never repeats, so c + pair is its slot.
 //
 // An 8-bit prefix under many rows is read back to bfloat16 first: the products
 // over it bound the call then, and the kernel for bfloat16 entries runs them at
@@ -30,14 +35,18 @@ namespace sv {
 constexpr int AT_ROWS = 128;      // query rows of a tile (one accumulator)
 constexpr int AT_UNIT = 128;      // entries of a unit
 constexpr int AT_MAX_CTAS = 192;  // CTAs that the workspace is sized for
+constexpr int SPREAD = 4;
 
 // Tiles of one kind of pair: a tile holds tq tokens (tq * G <= 128 rows), an
 // item one or two tiles (two: both halves of the kernel work on the same
 // entries; one: they take turns).  With 8-bit entries and few rows, the rows lie
 // in their tile `copies` times in long stretches, each copy for a part of the
-// entries, and what they leave is joined (`join`).
+// entries, and what they leave is joined (`join`).  On the line, a unit is
+// 1 << shift long, and a pair `over` more; 1 is about 0.45 us, measured: a unit
+// of two tiles 1.8 us and its pair 5 us (256 rows of results), one of one tile
+// 1 us and 1 us, with 8-bit entries 1.2 us and 4 us.
 struct AttnTiling {
-    int tq, two, tiles, copies, join;
+    int tq, two, tiles, copies, join, shift, over;
 };
 inline AttnTiling attn_tiling(long long tokens, int G, bool quant)
 {
@@ -49,6 +58,8 @@ inline AttnTiling attn_tiling(long long tokens, int G, bool quant)
     t.tiles = (int)((tokens + per - 1) / per);
     t.copies = !quant || t.two || t.tq * G > 64 ? 1 : t.tq * G > 32 ? 2 : 4;
     t.join = quant && !t.two;
+    t.shift = t.two ? 2 : 1;
+    t.over = t.two ? 12 : quant ? 8 : 2;
     return t;
 }
 
@@ -59,7 +70,7 @@ struct AttnPlan {
     int split;           // an 8-bit prefix is read back, prefix and caches are lines of their own
     int ppairs;          // prefix pairs
     int pu;              // units of a prefix pair
-    long long max_units; // with every sequence at its capacity
+    long long max_units, max_line;   // with every sequence at its capacity
     // byte offsets into the workspace
     size_t base, stat, ml_p, o_p, ml_s, o_s, prefix, total;
 };
@@ -74,13 +85,14 @@ inline AttnPlan attn_plan(int B, int T, int H, int G, int D, int P, int L, bool 
     a.ppairs = P > 0 ? H * a.pre.tiles : 0;
     const long long spairs = L > 0 ? (long long)B * H * a.own.tiles : 0;
     a.max_units = (long long)a.ppairs * a.pu + spairs * ((L + AT_UNIT - 1) / AT_UNIT);
+    a.max_line = 4 * a.max_units + 12 * (a.ppairs + spairs);
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t o = at;
         at = (at + bytes + 255) & ~(size_t)255;
         return o;
     };
-    a.base = take(((size_t)B + 1) * 4);
+    a.base = take(((size_t)B + 1) * 8);
     a.stat = take(2 * AT_MAX_CTAS * 4);
     const size_t rp = a.ppairs ? ((size_t)a.ppairs + AT_MAX_CTAS) * 2 * a.pre.tq * G : 0;
     const size_t rs = spairs ? ((size_t)spairs + AT_MAX_CTAS) * 2 * a.own.tq * G : 0;
@@ -93,28 +105,64 @@ inline AttnPlan attn_plan(int B, int T, int H, int G, int D, int P, int L, bool 
     return a;
 }
 
-// The line of U units over at most `ctas` CTAs: where CTA c starts (and c - 1
-// ends), and which CTA works on unit u.
-__device__ __forceinline__ int attn_start(int c, long long U, int ctas)
-{
-    const long long n = U < ctas ? U : ctas;
-    return (int)(c < n ? c * U / n : U);
-}
-__device__ __forceinline__ int attn_owner(int u, long long U, int ctas)
-{
-    // the largest c with c U < (u + 1) n, from an estimate that is off by one at most
-    const long long n = U < ctas ? U : ctas, x = ((long long)u + 1) * n;
-    int c = (int)__fdividef((float)x, (float)U);
-    c -= c * U >= x;
-    c += (c + 1) * U < x;
-    return c;
-}
+// What a kind of pair takes on the line.
+struct AttnCost {
+    int shift, over;
+    __device__ __forceinline__ int pair(int units) const { return units > 0 ? (units << shift) + over : 0; }
+    // where unit i begins in its pair; how many units begin ahead of x > 0
+    __device__ __forceinline__ int begin(int i) const { return i == 0 ? 0 : (i << shift) + over; }
+    __device__ __forceinline__ int ahead(int x) const
+    {
+        const int n = (x - over + (1 << shift) - 1) >> shift;
+        return n > 1 ? n : 1;
+    }
+};
+
+// A line, and its cut.
+struct AttnLine {
+    AttnCost pre, own_cost;
+    long long length;
+    int ctas;   // that share it
+    int own;    // where the sequence pairs begin
+    // pu units and `ppairs` prefix pairs; HS pairs per sequence; `seqs` sequences with `units` in all
+    __device__ __forceinline__ AttnLine(const AttnTiling &p, const AttnTiling &o, int ppairs, int pu, int HS, int units,
+                                        int seqs, int most)
+    {
+        const long long all = (long long)ppairs * pu + (long long)HS * units;
+        const bool brief = all < (long long)SPREAD * most;
+        pre = brief ? AttnCost{0, 0} : AttnCost{p.shift, p.over};
+        own_cost = brief ? AttnCost{0, 0} : AttnCost{o.shift, o.over};
+        own = ppairs * pre.pair(pu);
+        length = own + (long long)HS * sequences(units, seqs);
+        // the longest unit is a first one
+        const int a = ppairs > 0 ? pre.over + (1 << pre.shift) : 1, b = seqs > 0 ? own_cost.over + (1 << own_cost.shift) : 1;
+        const long long n = length / (a > b ? a : b);
+        ctas = (int)(n < most ? (n > 1 ? n : 1) : most);
+    }
+    // one pair's worth of `seqs` sequences with `units` in all
+    __device__ __forceinline__ int sequences(int units, int seqs) const
+    {
+        return (units << own_cost.shift) + own_cost.over * seqs;
+    }
+    // where CTA c begins (and c - 1 ends)
+    __device__ __forceinline__ int start(int c) const { return (int)(c < ctas ? c * length / ctas : length); }
+    // which CTA has position x: the largest c with c length < (x + 1) ctas, from an estimate that is
+    // off by one at most
+    __device__ __forceinline__ int owner(int x) const
+    {
+        const long long y = ((long long)x + 1) * ctas;
+        int c = (int)__fdividef((float)y, (float)length);
+        c -= c * length >= y;
+        c += (c + 1) * length < y;
+        return c;
+    }
+};
 
 // Device view of the plan.
 struct AttnWork {
     AttnTiling pre, own;
     int ppairs, pu;
-    int32_t *base;   // [B + 1] units of the sequences before b (one pair's worth), then their total; nullptr: not here
+    int2 *base;      // [B + 1] of the sequences before b: units (one pair's worth), how many have any; nullptr: not here
     int32_t *stat;   // [CTAs] 0, or the code of a CTA that gave up
     float2 *ml_p, *ml_s;   // [slot][2][tq * G] reference exponent and sum of a partial row
     float *o_p, *o_s;      // [slot][2][tq * G][D] its weighted values
