@@ -190,10 +190,8 @@ __global__ void __launch_bounds__(FW * 32)
             // two lines: each kind of pair has its own; one: the prefix pairs come first on both's
             const int two_lines = L.launches == 2;
             const int2 before = P.L > 0 ? __ldcg(W.base + b) : make_int2(0, 0);
-            const int2 total = P.L > 0 ? __ldcg(W.base + P.B) : make_int2(0, 0);
-            const AttnLine line0(W.pre, W.own, W.ppairs, W.pu, HS, two_lines ? 0 : total.x, two_lines ? 0 : total.y,
-                                 L.pre_ctas);
-            const AttnLine line1(W.pre, W.own, two_lines ? 0 : W.ppairs, W.pu, HS, total.x, total.y, L.own_ctas);
+            // not read through the non-coherent path: the tile kernel has just written them
+            const AttnLine line0 = *W.line, line1 = two_lines ? W.line[1] : line0;
             int cnt0 = 0, c0 = 0, pair0 = 0, grp0 = 0, row0 = 0, cnt1 = 0, c1 = 0, pair1 = 0, grp1 = 0, row1 = 0;
             if (W.ppairs) {
                 const int wide = W.pre.tq * (1 + W.pre.two), tile = bt / wide, in = bt - tile * wide;
@@ -385,6 +383,7 @@ cudaError_t launch_attention(const AttnParams &P, bool quant, void *workspace, i
     W.ppairs = a.ppairs;
     W.pu = a.pu;
     W.base = reinterpret_cast<int2 *>(w + a.base);
+    W.line = reinterpret_cast<AttnLine *>(w + a.line);
     W.stat = reinterpret_cast<int32_t *>(w + a.stat);
     W.ml_p = reinterpret_cast<float2 *>(w + a.ml_p);
     W.o_p = reinterpret_cast<float *>(w + a.o_p);
@@ -431,6 +430,7 @@ cudaError_t launch_attention(const AttnParams &P, bool quant, void *workspace, i
         V = W;
         V.ppairs = 0;
         V.stat += AT_MAX_CTAS;
+        ++V.line;
         e = tiles(A, V, true, a.max_units - (long long)a.ppairs * a.pu, L.own_ctas);
     } else {
         e = tiles(P, W, quant, a.max_units, L.pre_ctas);

@@ -1265,8 +1265,8 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
             }
             at += (u64)u | (u64)(u > 0) << 32;
         }
-        if (blockIdx.x == 0 && tid == 0 && P.W.base)
-            P.W.base[B] = make_int2((int)total, (int)(total >> 32));
+        if (blockIdx.x == 0 && tid == 0)
+            *P.W.line = line;
     }
     __syncthreads();
 

@@ -72,7 +72,7 @@ struct AttnPlan {
     int pu;              // units of a prefix pair
     long long max_units, max_line;   // with every sequence at its capacity
     // byte offsets into the workspace
-    size_t base, stat, ml_p, o_p, ml_s, o_s, prefix, total;
+    size_t base, stat, line, ml_p, o_p, ml_s, o_s, prefix, total;
 };
 
 inline AttnPlan attn_plan(int B, int T, int H, int G, int D, int P, int L, bool quant)
@@ -92,8 +92,9 @@ inline AttnPlan attn_plan(int B, int T, int H, int G, int D, int P, int L, bool 
         at = (at + bytes + 255) & ~(size_t)255;
         return o;
     };
-    a.base = take(((size_t)B + 1) * 8);
+    a.base = take((size_t)B * 8);
     a.stat = take(2 * AT_MAX_CTAS * 4);
+    a.line = take(2 * 64);
     const size_t rp = a.ppairs ? ((size_t)a.ppairs + AT_MAX_CTAS) * 2 * a.pre.tq * G : 0;
     const size_t rs = spairs ? ((size_t)spairs + AT_MAX_CTAS) * 2 * a.own.tq * G : 0;
     a.ml_p = take(rp * 8);
@@ -124,6 +125,8 @@ struct AttnLine {
     long long length;
     int ctas;   // that share it
     int own;    // where the sequence pairs begin
+    int total;  // one pair's worth of units of all sequences
+    AttnLine() = default;
     // pu units and `ppairs` prefix pairs; HS pairs per sequence; `seqs` sequences with `units` in all
     __device__ __forceinline__ AttnLine(const AttnTiling &p, const AttnTiling &o, int ppairs, int pu, int HS, int units,
                                         int seqs, int most)
@@ -132,6 +135,7 @@ struct AttnLine {
         const bool brief = all < (long long)SPREAD * most;
         pre = brief ? AttnCost{0, 0} : AttnCost{p.shift, p.over};
         own_cost = brief ? AttnCost{0, 0} : AttnCost{o.shift, o.over};
+        total = units;
         own = ppairs * pre.pair(pu);
         length = own + (long long)HS * sequences(units, seqs);
         // the longest unit is a first one
@@ -158,11 +162,14 @@ struct AttnLine {
     }
 };
 
+static_assert(sizeof(AttnLine) <= 64, "its place in the workspace");
+
 // Device view of the plan.
 struct AttnWork {
     AttnTiling pre, own;
     int ppairs, pu;
-    int2 *base;      // [B + 1] of the sequences before b: units (one pair's worth), how many have any; nullptr: not here
+    int2 *base;      // [B] of the sequences before b: units (one pair's worth), how many have any; nullptr: not here
+    struct AttnLine *line;   // this launch's, for the kernel that finishes the rows
     int32_t *stat;   // [CTAs] 0, or the code of a CTA that gave up
     float2 *ml_p, *ml_s;   // [slot][2][tq * G] reference exponent and sum of a partial row
     float *o_p, *o_s;      // [slot][2][tq * G][D] its weighted values
