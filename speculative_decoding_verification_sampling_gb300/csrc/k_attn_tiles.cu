@@ -494,24 +494,36 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint8_t *tiles, ui
     using C = TileCfg<D, Q8>;
     constexpr uint32_t IS = mma_desc(128, false, Q8 ? MMA_E4M3 : MMA_BF16), IO = mma_desc(D, true, Q8 ? MMA_F16 : MMA_BF16);
     const int lane = threadIdx.x & 31;
-    const uint32_t tmem = (uint32_t)uniform((int)sh.tmem);
+    // with 8-bit entries one thread runs all of this; with others the warp does, and elects one to
+    // issue, since it clears V's tail together
+    auto wait = [&](unsigned long long *bar, uint32_t parity, uint32_t lim, TileShared &s) {
+        return Q8 ? tile_wait(bar, parity, lim, s) : tile_wait_warp(bar, parity, lim, s);
+    };
+    auto lead = [] { return Q8 || elect_one(); };
+    auto rejoin = [] {
+        if (!Q8)
+            __syncwarp();
+    };
+    const uint32_t tmem = Q8 ? sh.tmem : (uint32_t)uniform((int)sh.tmem);
     Ring q, kr, vr;
     uint32_t pphase = 0;   // a bit for each group
     bool ok = true;
     auto give = [&](unsigned long long *bar) {
-        if (elect_one())
+        if (lead())
             mma_commit(bar);
-        __syncwarp();
+        rejoin();
     };
     Walk walk(P, sh.start);
     Item it;
 #pragma unroll 1
     while (ok && walk.next(it)) {
-        it.n = uniform(it.n);
-        it.two = uniform(it.two);
+        if (!Q8) {
+            it.n = uniform(it.n);
+            it.two = uniform(it.two);
+        }
         const int q0 = q.slot;
         for (int g = 0; ok && g <= it.two; ++g) {
-            ok = tile_wait_warp(Q8 ? &sh.q_ready[q.slot] : &sh.q_full[q.slot], q.phase, limit, sh);
+            ok = wait(Q8 ? &sh.q_ready[q.slot] : &sh.q_full[q.slot], q.phase, limit, sh);
             q.next(2);
         }
         tc_after();
@@ -520,11 +532,11 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint8_t *tiles, ui
         auto scores = [&](int g, int j, bool takes, bool gives) {
             if (takes) {
                 ks = kr.slot;
-                ok = ok && tile_wait_warp(&sh.k_full[ks], kr.phase, limit, sh);
+                ok = ok && wait(&sh.k_full[ks], kr.phase, limit, sh);
                 kr.next(C::NK);
                 tc_after();
             }
-            if (ok && elect_one()) {
+            if (ok && lead()) {
                 const int qs = (q0 + (it.two ? g : 0)) & 1;
                 const uint32_t a = desc_lo(smem + qs * C::TILE, 16), b = desc_lo(smem + C::K0 + ks * C::KT, 16);
                 if constexpr (Q8) {
@@ -549,13 +561,13 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint8_t *tiles, ui
                 if (!Q8 && j + 1 == it.n)   // the last product with this Q
                     mma_commit(&sh.q_empty[qs]);
             }
-            __syncwarp();
+            rejoin();
         };
         // O of group g takes unit j
         auto values = [&](int g, int j, bool takes, bool gives) {
             if (takes) {
                 vs = vr.slot;
-                ok = ok && tile_wait_warp(&sh.v_full[vs], vr.phase, limit, sh);
+                ok = ok && wait(&sh.v_full[vs], vr.phase, limit, sh);
                 vr.next(C::NV);
                 tc_after();
                 const int nv = it.left - j * AT_UNIT;
@@ -568,14 +580,14 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint8_t *tiles, ui
                             *reinterpret_cast<uint4 *>(tiles + C::V0 + vs * C::TILE + k * C::BLOCK + x * 16) =
                                 make_uint4(0, 0, 0, 0);
                     async_fence();
-                    __syncwarp();
+                    rejoin();
                 }
             }
             // P of this group is in TMEM
-            ok = ok && tile_wait_warp(&sh.p_ready[g], (g ? pphase >> 1 : pphase) & 1, limit, sh);
+            ok = ok && wait(&sh.p_ready[g], (g ? pphase >> 1 : pphase) & 1, limit, sh);
             pphase ^= 1u << g;
             tc_after();
-            if (ok && elect_one()) {
+            if (ok && lead()) {
                 // V is read along its rows: blocks of 64 columns lie BLOCK apart, 16 rows are 2048 bytes
                 const uint32_t b = desc_lo(smem + C::V0 + vs * C::TILE, C::BLOCK);
                 const int step = it.two ? 1 : 2;
@@ -587,7 +599,7 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint8_t *tiles, ui
                 if (j + step >= it.n)
                     mma_commit(&sh.o_full[g]);
             }
-            __syncwarp();
+            rejoin();
         };
         // Two sets of rows: S0 S1, then for each unit P0 V, the next S0, P1 V, the next S1.
         if (it.two && !Q8) {
@@ -1180,7 +1192,7 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
     pdl_trigger();
     const int tid = threadIdx.x, warp = tid / 32;
     const uint32_t smem = saddr(tiles);
-    const uint32_t limit = hinted_limit(P.spin_limit > OWN_WAIT_MIN ? P.spin_limit : OWN_WAIT_MIN);
+    const uint32_t limit = P.spin_limit > OWN_WAIT_MIN ? P.spin_limit : OWN_WAIT_MIN;   // polls, of about 0.1 us
 
     // ---- where this CTA's length begins: sums over runs of sequences, then the run.  Units in the
     // low word, sequences that have any in the high one.
@@ -1279,7 +1291,8 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
             if (elect_one())
                 load_role<D, Q8>(P, &mq_pre, &mq_own, &m_pre, &m_own, sh, smem, limit);
         } else if (warp == W_MMA) {
-            mma_role<D, Q8>(P, sh, tiles, smem, limit);
+            if (!Q8 || elect_one())
+                mma_role<D, Q8>(P, sh, tiles, smem, limit);
         } else if (Q8 && warp == W_SCALE) {
             scale_role(P, sh, limit);
         } else if (Q8 && warp >= W_CVT) {
