@@ -313,3 +313,54 @@ def test_the_round_with_an_8_bit_cache():
         _hold(*y, ref, D, f"16 bits, step {step}")
         sv.spec_kv_commit_quant(c, s, staged, torch.tensor([4, 0, -2, step], dtype=torch.int32, device=DEV), n, lead=1)
     assert n.tolist() == [20, 4, 0, 10]
+
+
+def test_many_rows_with_bad_lengths():
+    """More rows than get a CTA each in the finishing kernel."""
+    lens = [(13 * i) % 41 for i in range(90)]
+    a = _case(90, 5, 8, 2, 64, 150, 40, lens, False, "tree", seed=13)
+    _run(a, "before")
+    a["seq_len"][7], a["seq_len"][89] = 41, -3
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out, lse = sv.spec_verify_attention(a["q"], a["cache"], a["seq_len"], staged=a["staged"], mask=a["mask"],
+                                        prefix=a["prefix"], device_status=st)
+    assert int(st.item()) == 1
+    keep = [b for b in range(90) if b not in (7, 89)]
+    assert bool(out[[7, 89]].isnan().all()) and bool(lse[[7, 89]].isnan().all())
+    lens[7] = lens[89] = 0
+    ref = {k: v[keep] for k, v in _reference({**a, "seq_len": torch.tensor(lens)}).items()}
+    _hold(out[keep], lse[keep], ref, 64, "the rest")
+
+
+def test_scales_far_apart_within_a_unit():
+    """Heads of very different magnitudes side by side: what a unit's largest scale leaves of the others."""
+    for big in (20, 60):
+        a = _case(2, 3, 8, 2, 128, 200, 300, [300, 170], True, "causal", seed=14)
+        a["cache_scale"][:, 5::7] -= big          # 2^-20, 2^-60 of the others
+        a["prefix_scale"][::3] -= big
+        _run(a, f"2^-{big}")
+        a["cache_scale"][:, :170] = a["cache_scale"][:, :170].clamp(min=60) - 50   # and everything small
+        a["prefix_scale"].clamp_(min=60).sub_(50)
+        a["staged"] *= 2.0 ** -50
+        _run(a, f"2^-{big}, small")
+
+
+def test_heads_that_read_back_as_nan():
+    """Scale byte 255 where a row sees it, in a key and in a value."""
+    a = _case(2, 2, 4, 2, 64, 10, 400, [200, 400], True, "causal", seed=15)
+    clean = _run(a, "clean")
+    a["cache_scale"][0, 130, 0, 1] = 255     # a key: the whole row
+    a["cache_scale"][1, 300, 1, 0] = 255     # a value: every column
+    out, lse = sv.spec_verify_attention(a["q"], a["cache"], a["seq_len"], staged=a["staged"], prefix=a["prefix"],
+                                        cache_scale=a["cache_scale"], prefix_scale=a["prefix_scale"])
+    assert bool(out[0, :, 2:].isnan().all()) and bool(lse[0, :, 2:].isnan().all())
+    assert bool(out[1, :, :2].isnan().all()) and torch.equal(lse[1], clean[1][1])
+    assert torch.equal(out[0, :, :2], clean[0][0, :, :2]) and torch.equal(out[1, :, 2:], clean[0][1, :, 2:])
+
+
+def test_the_example_runs():
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import verification_round
+    assert 1.0 <= verification_round.main(rounds=3) <= 5.0
