@@ -64,16 +64,21 @@ __device__ __forceinline__ f2 pair_of(const RawRow<E> &r, int k)
 {
     return pku(r.w[k] << 16, r.w[k] & 0xffff0000u);
 }
-// E float32 of a partial result's row
+// E float32 of a row of a partial result; `step` floats from eight columns to the next eight
 template <int E>
-__device__ __forceinline__ void load_values(const float *p, float (&y)[E])
+__device__ __forceinline__ void load_values(const float *p, int step, float (&y)[E])
 {
-    if constexpr (E >= 4) {
+    if constexpr (E >= 8) {
 #pragma unroll
-        for (int k = 0; k < E / 4; ++k) {
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + (k >> 1) * 64 + (k & 1) * 4));
-            y[4 * k] = v.x, y[4 * k + 1] = v.y, y[4 * k + 2] = v.z, y[4 * k + 3] = v.w;
-        }
+        for (int k = 0; k < E / 8; ++k)
+            asm volatile("ld.global.cg.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=f"(y[8 * k]), "=f"(y[8 * k + 1]), "=f"(y[8 * k + 2]), "=f"(y[8 * k + 3]),
+                           "=f"(y[8 * k + 4]), "=f"(y[8 * k + 5]), "=f"(y[8 * k + 6]), "=f"(y[8 * k + 7])
+                         : "l"(p + k * 8 * step)
+                         : "memory");
+    } else if constexpr (E == 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p));
+        y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
     } else {
         const float2 v = __ldcg(reinterpret_cast<const float2 *>(p));
         y[0] = v.x, y[1] = v.y;
@@ -88,16 +93,18 @@ struct FinishLines {
 
 // Many rows (WIDE = false): eight lanes per query row.  A warp works on four
 // heads of a token, and the index arithmetic and the loops over what they see
-// serve four rows.  Few rows (WIDE): a CTA per row, each of its warps taking a
-// quarter of what the row sees and of its partial results, of which there may
-// be hundreds; the four are joined in shared memory.
+// serve four rows.  Seven CTAs to an SM and two partial results in flight:
+// 124928 rows of 61-node trees take 66 us after the tile kernel so, 85 us with
+// four in flight and four CTAs (118 registers).  Few rows (WIDE): a CTA per row,
+// each of its warps taking a quarter of what the row sees and of its partial
+// results, of which there may be hundreds; the four are joined in shared memory.
 template <int D, bool WIDE>
-__global__ void __launch_bounds__(FW * 32)
+__global__ void __launch_bounds__(FW * 32, WIDE ? 1 : 7)
     va_finish(const __grid_constant__ AttnParams P, const __grid_constant__ AttnWork W, FinishLines L, int per_token)
 {
     constexpr int LPR = WIDE ? 32 : 8, E = D / LPR, NP = E / 2, AT = E < 8 ? E : 8;
     constexpr int STEP = WIDE ? LPR * FW : LPR;   // partial results looked up at a time
-    constexpr int FLY = WIDE ? 8 : 4;             // of their values in flight
+    constexpr int FLY = WIDE ? 8 : 2;             // of their values in flight
     const float inf = __int_as_float(0x7f800000), nan = __int_as_float(0x7fc00000);
     const int lane = threadIdx.x & 31, sub = lane % LPR;
     const int warp = threadIdx.x / 32;
@@ -213,28 +220,31 @@ __global__ void __launch_bounds__(FW * 32)
                 cnt1 = (line1.owner(at + line1.own_cost.begin(ub - 1)) - c1 + 1) << (1 - W.own.two);
             }
             const int all = cnt0 + cnt1;   // may differ between the warp's rows
+            const int rows0 = W.pre.tq * P.G, rows1 = W.own.tq * P.G;
+            const int column = sub * AT & ~7;
+            const float *const v0 = W.o_p + row0 * 8 + sub * AT % 8, *const v1 = W.o_s + row1 * 8 + sub * AT % 8;
             for (int i0 = 0; __any_sync(0xffffffffu, i0 < all); i0 += STEP) {
                 // each lane of a row looks up a partial result, then all of them read the values
                 const int at_i = i0 + (WIDE ? sub * FW + warp : sub);
                 const bool own = at_i >= cnt0;
                 const int i = at_i - (own ? cnt0 : 0), two = own ? W.own.two : W.pre.two;
                 float pm = -inf, pl = 0.0f;
-                size_t at = 0;
+                int part = 0;   // which partial result, and of which kind
                 bool gave_up = false;
                 if (at_i < all) {
                     // with one set of rows, a CTA has one of each group (an empty one if they were joined)
                     const int c = (own ? c1 : c0) + (two ? i : i >> 1);
                     const int gr = two ? (own ? grp1 : grp0) : i & 1;
-                    const int rows = (own ? W.own.tq : W.pre.tq) * P.G;
-                    at = ((size_t)(c + (own ? pair1 : pair0)) * 2 + gr) * rows + (own ? row1 : row0);
-                    const float2 ml = __ldcg((own ? W.ml_s : W.ml_p) + at);
+                    part = (c + (own ? pair1 : pair0)) * 2 + gr;
+                    const float2 ml = own ? __ldcg(W.ml_s + (size_t)part * rows1 + row1)
+                                          : __ldcg(W.ml_p + (size_t)part * rows0 + row0);
+                    part = part * 2 + own;
                     pm = ml.x;
                     pl = ml.y;
                     gave_up = __ldcg(W.stat + (own && two_lines ? AT_MAX_CTAS : 0) + c) != 0;
                 }
                 if (__any_sync(0xffffffffu, gave_up))
                     code = 7;
-                const float *src = (own ? W.o_s : W.o_p) + at * D;
                 float top = pm;
 #pragma unroll
                 for (int w = LPR / 2; w; w >>= 1)
@@ -257,15 +267,16 @@ __global__ void __launch_bounds__(FW * 32)
                     for (int n = 0; n < FLY; ++n) {
                         const int j = have ? __ffs(have) - 1 : 0;
                         const float w = __shfl_sync(0xffffffffu, wt, j, LPR);
-                        const float *sj = reinterpret_cast<const float *>(
-                            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), j, LPR));
+                        const int pj = __shfl_sync(0xffffffffu, part, j, LPR);
+                        const int rows = pj & 1 ? rows1 : rows0;
+                        const float *sj = (pj & 1 ? v1 : v0) + (size_t)(pj >> 1) * rows * D + column * rows;
                         wj[n] = have ? w : 0.0f;
                         have &= have - 1;
 #pragma unroll
                         for (int k = 0; k < E; ++k)
                             y[n][k] = 0.0f;
                         if (wj[n] != 0.0f)
-                            load_values<E>(sj + sub * AT, y[n]);
+                            load_values<E>(sj, 8 * rows, y[n]);
                     }
 #pragma unroll
                     for (int n = 0; n < FLY; ++n) {

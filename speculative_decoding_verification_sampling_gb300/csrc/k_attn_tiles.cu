@@ -792,10 +792,10 @@ __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;"
 // Joins the partial results of an item with one set of rows: both groups, and
 // every copy, in chunks of columns by way of the item's Q tile, which nothing
 // reads any more.  `weight` is that of this thread's part of its row, `any`
-// whether its warp has values at all.
+// whether its warp has values at all.  dst: a partial result's values, of `rows` rows.
 template <int D>
 __device__ __forceinline__ void join_parts(uint8_t *scratch, uint32_t to, int part, int parts, int row, int have,
-                                           bool any, float weight, float *dst)
+                                           bool any, float weight, float *dst, int rows)
 {
     constexpr int CW = D / 4;        // columns of a chunk: 256 rows of them fill the Q tile
     constexpr int V = CW / 4;        // 16-byte vectors of a row's chunk
@@ -822,7 +822,7 @@ __device__ __forceinline__ void join_parts(uint8_t *scratch, uint32_t to, int pa
                 const float4 z = *reinterpret_cast<const float4 *>(scratch + ((p * have + r) * V + (v ^ (r % V))) * 16);
                 y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
             }
-            *reinterpret_cast<float4 *>(dst + (size_t)r * D + k * CW + v * 4) = y;
+            *reinterpret_cast<float4 *>(dst + ((k * CW + v * 4) / 8 * rows + r) * 8 + v % 2 * 4) = y;
         }
         if (k == 3)
             async_fence();   // the tile is TMA's next
@@ -920,13 +920,13 @@ __device__ void softmax_role(const TileParams &P, QuantShared &sh, uint8_t *tile
                 ml[at + rows + row] = make_float2(-F_INF, 0.0f);
             }
             join_parts<D>(tiles + qs * C::TILE, to, copy * 2 + g, 2 * copies, row, have, ok && cnt > 0 && active,
-                          l == 0.0f ? 0.0f : ex2a(m - ref), o_all + at * D);
+                          l == 0.0f ? 0.0f : ex2a(m - ref), o_all + at * D, rows);
             if (ok && threadIdx.x == 0)
                 mbar_arrive(&sh.q_empty[qs]);
         } else {
-            const size_t at = ((size_t)it.slot * 2 + g) * rows + row;
+            const size_t at = ((size_t)it.slot * 2 + g) * rows;
             if (row < have)
-                ml[at] = make_float2(m, l);
+                ml[at + row] = make_float2(m, l);
             if (ok && cnt > 0 && active) {
 #pragma unroll 1
                 for (int k = 0; k < D; k += 32) {
@@ -935,7 +935,7 @@ __device__ void softmax_role(const TileParams &P, QuantShared &sh, uint8_t *tile
                     if (row < have) {
 #pragma unroll
                         for (int u = 0; u < 32; u += 8)
-                            store8(o_all + at * D + k + u, o + u);
+                            store8(o_all + at * D + ((k + u) / 8 * rows + row) * 8, o + u);
                     }
                 }
             }

@@ -43,8 +43,10 @@ constexpr int SPREAD = 4;
 // in their tile `copies` times in long stretches, each copy for a part of the
 // entries, and what they leave is joined (`join`).  On the line, a unit is
 // 1 << shift long, and a pair `over` more; 1 is about 0.45 us, measured: a unit
-// of two tiles 1.8 us and its pair 5 us (256 rows of results), one of one tile
-// 1 us and 1 us, with 8-bit entries 1.2 us and 4 us.
+// of two tiles 1.8 us, its pair 3.6 us; a unit of one tile 1 us, its pair 1.8 us
+// and up to 1.8 us more with the rows that are written (64 sequences of 32
+// tokens, 8192 shared and 512 own entries, 32 heads: 278 us a call so, 359 us
+// with 1 us a pair); with 8-bit entries 1.2 us and 4 us.  At most 12: max_line.
 struct AttnTiling {
     int tq, two, tiles, copies, join, shift, over;
 };
@@ -59,7 +61,7 @@ inline AttnTiling attn_tiling(long long tokens, int G, bool quant)
     t.copies = !quant || t.two || t.tq * G > 64 ? 1 : t.tq * G > 32 ? 2 : 4;
     t.join = quant && !t.two;
     t.shift = t.two ? 2 : 1;
-    t.over = t.two ? 12 : quant ? 8 : 2;
+    t.over = t.two ? 8 : quant ? 9 : 4 + t.tq * G / 32;
     return t;
 }
 
@@ -126,6 +128,7 @@ struct AttnLine {
     int ctas;   // that share it
     int own;    // where the sequence pairs begin
     int total;  // one pair's worth of units of all sequences
+    float rate; // ctas / length
     AttnLine() = default;
     // pu units and `ppairs` prefix pairs; HS pairs per sequence; `seqs` sequences with `units` in all
     __device__ __forceinline__ AttnLine(const AttnTiling &p, const AttnTiling &o, int ppairs, int pu, int HS, int units,
@@ -142,6 +145,7 @@ struct AttnLine {
         const int a = ppairs > 0 ? pre.over + (1 << pre.shift) : 1, b = seqs > 0 ? own_cost.over + (1 << own_cost.shift) : 1;
         const long long n = length / (a > b ? a : b);
         ctas = (int)(n < most ? (n > 1 ? n : 1) : most);
+        rate = __fdividef((float)ctas, (float)length);
     }
     // one pair's worth of `seqs` sequences with `units` in all
     __device__ __forceinline__ int sequences(int units, int seqs) const
@@ -155,7 +159,7 @@ struct AttnLine {
     __device__ __forceinline__ int owner(int x) const
     {
         const long long y = ((long long)x + 1) * ctas;
-        int c = (int)__fdividef((float)y, (float)length);
+        int c = (int)(((float)x + 1.0f) * rate);
         c -= c * length >= y;
         c += (c + 1) * length < y;
         return c;
@@ -172,7 +176,8 @@ struct AttnWork {
     struct AttnLine *line;   // this launch's, for the kernel that finishes the rows
     int32_t *stat;   // [CTAs] 0, or the code of a CTA that gave up
     float2 *ml_p, *ml_s;   // [slot][2][tq * G] reference exponent and sum of a partial row
-    float *o_p, *o_s;      // [slot][2][tq * G][D] its weighted values
+    float *o_p, *o_s;      // [slot][2][D / 8][tq * G][8] its weighted values: rows side by side, as the threads that
+                           // write them lie (with rows of D, 256 rows of results took 4 us; 1 us so)
 };
 
 }  // namespace sv
