@@ -171,3 +171,13 @@ def test_launch_counts():
     assert sv.spec_launch_count() == n0 + 2
     sv.spec_kv_read_quant(c, s, None, n, 3)
     assert sv.spec_launch_count() == n0 + 3
+
+
+@pytest.mark.parametrize("NL,B,K,H,D", [(1, 1, 2100, 2, 64), (2, 3, 701, 3, 128), (1, 1, 1, 1, 64), (3, 1, 150, 8, 128)])
+@pytest.mark.parametrize("nodes", [False, True])
+def test_commit_of_many_entries_by_few_sequences(NL, B, K, H, D, nodes):
+    """A prompt at once: more CTAs than (layer, sequence) pairs, each with a part of the pieces."""
+    codes, scale = _cache(NL, B, K + 7, H, D, K)
+    staged = torch.randn((NL, B, K, 2, H, D), generator=torch.Generator().manual_seed(K)).to(torch.bfloat16)
+    order = [[(7 * i + b) % K for i in range(K)] for b in range(B)] if nodes else None
+    _check_commit(codes, scale, staged, [max(K - 11 * b, 0) for b in range(B)], [(5 * b) % 8 for b in range(B)], order)
