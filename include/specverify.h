@@ -313,11 +313,18 @@ spec_status_t spec_kv_read_quant(const void *cache, const uint8_t *scale, const 
  *                 zero-fill needed), 16-byte aligned; one per call in flight
  *   device_status [1] set to 0, or the code of one failing sequence; may be NULL
  * seq_len[b] outside [0, L] is an error (SPEC_ERR_INVALID_ARG): that
- * sequence's outputs are NaN.  Scores, softmax statistics and sums are float32;
- * the weights are rounded to bfloat16 where they meet the values.
+ * sequence's outputs are NaN.  Scores, softmax statistics and sums are float32.
+ * What is rounded to fewer bits on the way: the weights where they meet prefix
+ * and cache values (to bfloat16, by 2^-8 of a weight at most; with 8-bit entries
+ * to float16), and with 8-bit entries q (elements below 2^-10 of their row's
+ * largest, by 2^-18 of that at most) and values of heads whose scale is more than
+ * 2^22 below the largest of their 128 entries (by 2^-40 of its range).  An
+ * 8-bit prefix under B T Hq / Hkv >= 1024 rows is read back to bfloat16 in the
+ * workspace, and then counts as bfloat16 here.
  * Limits: D = 64 or 128, Hq a multiple of Hkv, Hq / Hkv <= 128, sm_scale finite
  * and > 0, P, L >= 0, T <= 2048, B T Hq <= 2^30.  All arrays but the scales, mask and
- * lse 16-byte aligned.  Asynchronous on `stream`.                              */
+ * lse 16-byte aligned.  One launch without prefix and cache, else two, four when
+ * the prefix is read back (three without a cache).  Asynchronous on `stream`.  */
 size_t spec_attention_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int P, int L);
 spec_status_t spec_verify_attention(const void *q, const void *prefix, const uint8_t *prefix_scale, const void *cache,
                                     const uint8_t *cache_scale, int quant, const int32_t *seq_len,
@@ -377,7 +384,8 @@ spec_status_t spec_philox_words(uint64_t seed, uint32_t tag, int B, int P, uint3
  * or two to four when the row-parallel kernels serve it (large stochastic
  * batches: two from 1024 rows with aligned rows, where the residual pass runs
  * inside the statistics stream); spec_draft_sample and spec_philox_words
- * launch one each, spec_kv_commit two (one in place).  For accounting;
+ * launch one each, spec_kv_commit two (one in place), spec_kv_commit_quant two,
+ * spec_kv_read_quant one, spec_verify_attention one to four.  For accounting;
  * thread-safe.                                                               */
 uint64_t spec_launch_count(void);
 

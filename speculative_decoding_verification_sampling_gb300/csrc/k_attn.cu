@@ -32,6 +32,7 @@ namespace sv {
 namespace {
 
 constexpr int FW = 4;                  // warps of a CTA
+constexpr size_t WORK_ALIGN = 256;     // partial results are read and written 32 bytes at a time
 constexpr long long WIDE_ROWS = 2048;   // rows up to which each has a CTA of its own
 
 // E elements of a row per lane, as pairs.  Eight lanes to a row: lane s holds
@@ -374,7 +375,7 @@ bool attention_fits(int B, int T, int H, int G, int D, int P, int L)
 size_t attention_workspace(int B, int T, int H, int G, int D, int P, int L)
 {
     const size_t a = attn_plan(B, T, H, G, D, P, L, false).total, b = attn_plan(B, T, H, G, D, P, L, true).total;
-    return a > b ? a : b;
+    return (a > b ? a : b) + WORK_ALIGN - 16;   // the caller's is 16-byte aligned
 }
 
 cudaError_t launch_attention(const AttnParams &P, bool quant, void *workspace, int sms, uint32_t spin_limit,
@@ -387,7 +388,7 @@ cudaError_t launch_attention(const AttnParams &P, bool quant, void *workspace, i
             return e;
     }
     const AttnPlan a = attn_plan(P.B, P.T, P.H, P.G, P.D, P.P, P.L, quant);
-    char *w = static_cast<char *>(workspace);
+    char *w = reinterpret_cast<char *>(((uintptr_t)workspace + WORK_ALIGN - 1) & ~(uintptr_t)(WORK_ALIGN - 1));
     AttnWork W{};
     W.pre = a.pre;
     W.own = a.own;

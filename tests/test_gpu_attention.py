@@ -364,3 +364,21 @@ def test_the_example_runs():
     sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
     import verification_round
     assert 1.0 <= verification_round.main(rounds=3) <= 5.0
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_workspace_at_any_16_bytes_and_launches(quant):
+    """The workspace lies where the caller has room: 16-byte aligned, no further."""
+    a = _case(3, 5, 8, 2, 128, 150, 300, [300, 0, 131], quant, "tree", seed=16)
+    keys = ("q", "cache", "seq_len")
+    args = [a[k] for k in keys]
+    kw = {k: v for k, v in a.items() if k not in keys and isinstance(v, torch.Tensor)}
+    want = sv.spec_verify_attention(*args, **kw)
+    need = sv.spec_attention_workspace_bytes(3, 5, 8, 2, 128, 150, 300)
+    room = torch.full((need + 512,), 0xff, dtype=torch.uint8, device=DEV)
+    for at in (16, 48, 240):
+        before = sv.spec_launch_count()
+        got = sv.spec_verify_attention(*args, workspace=room[at:at + need], **kw)
+        assert sv.spec_launch_count() - before == 2
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert bool((room[:at] == 0xff).all()) and bool((room[at + need:] == 0xff).all())
