@@ -1004,7 +1004,7 @@ __device__ __forceinline__ void scale_role(const TileParams &P, QuantShared &sh,
 }
 
 // 8-bit entries: Q to two e4m3 terms, V's codes to float16; warp w of the four
-// takes rows 32 w .. 32 w + 31 of each tile.
+// takes rows 32 w .. 32 w + 31 of each tile of codes.
 template <int D>
 __device__ void convert_role(const TileParams &P, QuantShared &sh, uint8_t *tiles, uint32_t limit)
 {
@@ -1021,15 +1021,18 @@ __device__ void convert_role(const TileParams &P, QuantShared &sh, uint8_t *tile
         if (!tile_wait_warp(&sh.q_full[q.slot], q.phase, limit, sh))
             return false;
         uint8_t *tile = tiles + q.slot * C::TILE;
-        // rows of a copy in this warp's quarter
-        const int quarters = 4 / x.copies, here = (x.b < 0 ? P.W.pre.tq : P.W.own.tq) * P.A.G - (w % quarters) * 32;
+        // four rows to a warp in turn, so that few rows keep all four busy
+        const int rows = (x.b < 0 ? P.W.pre.tq : P.W.own.tq) * P.A.G, each = AT_ROWS / x.copies - 1;
 #pragma unroll 1
-        for (int p0 = 0; p0 < 8 && p0 * 4 < here; p0 += 2) {
+        for (int p0 = 0; p0 < 8; p0 += 2) {
+            const int r0 = p0 * 16 + w * 4;   // and 16 further on
+            if ((r0 & each) >= rows && (r0 + 16 & each) >= rows)
+                continue;
             uint4 v[2][D / 64];
             uint32_t top[2];
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                const uint8_t *at = tile + (w * 32 + (p0 + p) * 4 + lane / 8) * 128 + (lane % 8) * 16;
+                const uint8_t *at = tile + (r0 + p * 16 + lane / 8) * 128 + (lane % 8) * 16;
                 top[p] = 0;
 #pragma unroll
                 for (int k = 0; k < D / 64; ++k) {
@@ -1048,7 +1051,7 @@ __device__ void convert_role(const TileParams &P, QuantShared &sh, uint8_t *tile
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 // this lane's chunk of eight columns: half c & 1 of a term's 16-byte chunk 4 k + c / 2
-                const int row = w * 32 + (p0 + p) * 4 + lane / 8, c = (lane % 8) ^ (row & 7);
+                const int row = r0 + p * 16 + lane / 8, c = (lane % 8) ^ (row & 7);
                 uint8_t *at = tile + row * 128;
                 float inv;
                 const uint32_t byte = fp8_scale(top[p] << 16, inv);
