@@ -31,9 +31,9 @@
 namespace sv {
 namespace {
 
-constexpr int FW = 4;                  // warps of a CTA
 constexpr size_t WORK_ALIGN = 256;     // partial results are read and written 32 bytes at a time
 constexpr long long WIDE_ROWS = 2048;   // rows up to which each has a CTA of its own
+constexpr long long WIDER_ROWS = 256;   // rows up to which that has 16 warps, not four
 
 // E elements of a row per lane, as pairs.  Eight lanes to a row: lane s holds
 // elements 8 s .. 8 s + 7 and, with E = 16, the same 64 further on.  A warp to a
@@ -96,13 +96,17 @@ struct FinishLines {
 // heads of a token, and the index arithmetic and the loops over what they see
 // serve four rows.  Seven CTAs to an SM and two partial results in flight:
 // 124928 rows of 61-node trees take 66 us after the tile kernel so, 85 us with
-// four in flight and four CTAs (118 registers).  Few rows (WIDE): a CTA per row,
-// each of its warps taking a quarter of what the row sees and of its partial
-// results, of which there may be hundreds; the four are joined in shared memory.
-template <int D, bool WIDE>
-__global__ void __launch_bounds__(FW * 32, WIDE ? 1 : 7)
+// four in flight and four CTAs (118 registers).  Few rows: a CTA per row,
+// of WIDE warps, each taking a share of what the row sees and of its partial
+// results, of which there may be hundreds; the shares are joined in shared memory.
+// 16 warps where there are CTAs for a part of the SMs only (131072 entries under
+// 32 rows of one key/value head: 23 us a call, 46 us with four warps), else four
+// (1280 rows: 19 us, 42 us with 16).
+template <int D, int WIDE>
+__global__ void __launch_bounds__(WIDE ? WIDE * 32 : 128, WIDE ? 1 : 7)
     va_finish(const __grid_constant__ AttnParams P, const __grid_constant__ AttnWork W, FinishLines L, int per_token)
 {
+    constexpr int FW = WIDE ? WIDE : 4;   // warps
     constexpr int LPR = WIDE ? 32 : 8, E = D / LPR, NP = E / 2, AT = E < 8 ? E : 8;
     constexpr int STEP = WIDE ? LPR * FW : LPR;   // partial results looked up at a time
     constexpr int FLY = WIDE ? 8 : 2;             // of their values in flight
@@ -149,8 +153,8 @@ __global__ void __launch_bounds__(FW * 32, WIDE ? 1 : 7)
         for (int j0 = 0; j0 < end; j0 += 32) {
             const int j = j0 + lane;
             unsigned seen = __ballot_sync(0xffffffffu, j < end && (!mask || __ldg(mask + j)));
-            if constexpr (WIDE)
-                seen &= 0x11111111u << warp;   // this warp's quarter
+            if constexpr (WIDE != 0)
+                seen &= (0xffffffffu / ((1u << FW) - 1)) << warp;   // this warp's share
             while (seen) {
                 // two visible entries at a time
                 const int ja = __ffs(seen) - 1;
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(FW * 32, WIDE ? 1 : 7)
                 l += add;
                 // the partial results that some row of the warp has
                 unsigned have = __ballot_sync(0xffffffffu, wt != 0.0f);
-                if constexpr (!WIDE)
+                if constexpr (WIDE == 0)
                     have = (have | have >> 8 | have >> 16 | have >> 24) & 0xffu;
                 while (have) {
                     float wj[FLY], y[FLY][E];
@@ -290,7 +294,7 @@ __global__ void __launch_bounds__(FW * 32, WIDE ? 1 : 7)
             }
         }
     }
-    if constexpr (WIDE) {
+    if constexpr (WIDE != 0) {
         __shared__ float s_o[FW][D], s_m[FW], s_l[FW];
         __shared__ int s_code[FW];
 #pragma unroll
@@ -347,9 +351,10 @@ __global__ void __launch_bounds__(FW * 32, WIDE ? 1 : 7)
     }
 }
 
-template <int D, bool WIDE>
+template <int D, int WIDE>
 cudaError_t finish(const AttnParams &P, const AttnWork &W, const FinishLines &L, cudaStream_t stream)
 {
+    constexpr int FW = WIDE ? WIDE : 4;
     const int per_token = WIDE ? P.Hq : (P.Hq + FW * 4 - 1) / (FW * 4);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(P.B * P.T * per_token));
@@ -450,9 +455,14 @@ cudaError_t launch_attention(const AttnParams &P, bool quant, void *workspace, i
     }
     if (e != cudaSuccess)
         return e;
-    const bool wide = (long long)P.B * P.T * P.Hq <= WIDE_ROWS;
-    e = P.D == 128 ? (wide ? finish<128, true>(P, W, L, stream) : finish<128, false>(P, W, L, stream))
-                   : (wide ? finish<64, true>(P, W, L, stream) : finish<64, false>(P, W, L, stream));
+    const long long rows = (long long)P.B * P.T * P.Hq;
+    const int wide = rows <= WIDER_ROWS ? 16 : rows <= WIDE_ROWS ? 4 : 0;
+    if (P.D == 128)
+        e = wide == 16 ? finish<128, 16>(P, W, L, stream)
+                       : wide ? finish<128, 4>(P, W, L, stream) : finish<128, 0>(P, W, L, stream);
+    else
+        e = wide == 16 ? finish<64, 16>(P, W, L, stream)
+                       : wide ? finish<64, 4>(P, W, L, stream) : finish<64, 0>(P, W, L, stream);
     if (e == cudaSuccess)
         ++*launches;
     return e;

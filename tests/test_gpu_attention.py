@@ -382,3 +382,13 @@ def test_workspace_at_any_16_bytes_and_launches(quant):
         assert sv.spec_launch_count() - before == 2
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         assert bool((room[:at] == 0xff).all()) and bool((room[at + need:] == 0xff).all())
+
+
+@pytest.mark.parametrize("B,T,Hq,H,D,P,L,quant", [
+    (1, 1, 32, 1, 128, 0, 90001, False),    # one pair over every CTA: hundreds of partial results to a row
+    (1, 2, 48, 1, 64, 1000, 60000, True),
+    (2, 3, 86, 2, 128, 700, 20000, False),  # just past the rows that have 16 warps each
+])
+def test_few_rows_over_long_caches(B, T, Hq, H, D, P, L, quant):
+    a = _case(B, T, Hq, H, D, P, L, [L - 77 * b for b in range(B)], quant, "causal", seed=17)
+    _run(a, f"{B * T * Hq} rows over {L} entries")
