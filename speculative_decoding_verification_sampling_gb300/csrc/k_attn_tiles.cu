@@ -41,10 +41,10 @@
 // Measured, 32 query and 8 key/value heads of 128: 64 sequences of 32 tokens over
 // 8192 shared entries, 191 us, 1440 TFLOP/s (bound by the two groups' softmax, the
 // tensor cores 62 % active); 64 of 5 tokens over 4096 own entries each, 170 us,
-// 6.3 TB/s (HBM); 64 of 9 tokens over 8192 own 8-bit entries each, 304 us, 3.6
-// TB/s (the chain of a unit, and instruction fetch for six roles); 256 of 5
-// tokens over 512 own 8-bit entries each, 140 us (10 us to a pair of four units:
-// one warp's softmax over 128 columns is 1.8 us of each).
+// 6.3 TB/s (HBM); 64 of 9 tokens over 8192 own 8-bit entries each, 261 us, 4.1
+// TB/s (the chain of a unit, and the copies in flight beside tiles being
+// converted); 256 of 5 tokens over 512 own 8-bit entries each, 119 us (9 us to a
+// pair of four units: one warp's softmax over 128 columns is 1.8 us of each).
 //
 // The last unit of a stretch is ragged: scores past its end become -inf, and
 // V's rows past it are zeroed in shared memory, since 0 * NaN would reach O.
@@ -282,8 +282,10 @@ __device__ __forceinline__ int seq_units(const AttnParams &A, int b)
 }
 
 // Units from which a stretch of 8-bit entries with one set of rows uses copies of
-// them and joins what the groups and copies leave (a fixed cost per stretch).
-constexpr int JOIN_UNITS = 8;
+// them and joins what the groups and copies leave (a fixed cost per stretch: 8 units
+// each under 64 sequences of 5 tokens take 57 us without, 61 us with; 64 units each
+// under 64 of 9, 261 us with, 296 us without).
+constexpr int JOIN_UNITS = 12;
 
 // One stretch of one pair, as a CTA works on it.
 struct Item {

@@ -21,8 +21,8 @@
 //
 // An 8-bit prefix under many rows is read back to bfloat16 first: the products
 // over it bound the call then, and the kernel for bfloat16 entries runs them at
-// 1.4 times the rate of the one for codes (64 sequences of 32 tokens, 32 heads,
-// 8192 entries: 190 us and 301 us), while reading back takes 6 bytes per
+// 1.6 times the rate of the one for codes (64 sequences of 32 tokens, 32 heads,
+// 8192 entries: 190 us and 311 us), while reading back takes 6 bytes per
 // element once. That breaks even at about 700 rows per key/value head. Prefix
 // and caches are then two lines, of one launch each.
 #pragma once
