@@ -255,15 +255,21 @@ __global__ void __launch_bounds__(WIDE ? WIDE * 32 : 128, WIDE ? 1 : 7)
                 for (int w = LPR / 2; w; w >>= 1)
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
                 const float ref = rescale(top);
-                // a partial result over no entries has no values
-                const float wt = pl == 0.0f ? 0.0f : ex2a(pm - ref);
-                float add = wt == 0.0f ? 0.0f : wt * pl;
+                // A partial result over no entries has no values.  One whose weight underflows is -0: its
+                // values are read all the same, a NaN among them is the row's.  A sum that is NaN (every
+                // score may be, which leaves pm = -inf) is the row's, too.
+                float wt = 0.0f;
+                if (pl != 0.0f) {
+                    wt = pl == pl ? ex2a(pm - ref) : nan;
+                    wt = wt == 0.0f ? -0.0f : wt;
+                }
+                float add = pl == 0.0f ? 0.0f : wt * pl;
 #pragma unroll
                 for (int w = LPR / 2; w; w >>= 1)
                     add += __shfl_xor_sync(0xffffffffu, add, w);
                 l += add;
                 // the partial results that some row of the warp has
-                unsigned have = __ballot_sync(0xffffffffu, wt != 0.0f);
+                unsigned have = __ballot_sync(0xffffffffu, __float_as_uint(wt) != 0);
                 if constexpr (WIDE == 0)
                     have = (have | have >> 8 | have >> 16 | have >> 24) & 0xffu;
                 while (have) {
@@ -280,7 +286,7 @@ __global__ void __launch_bounds__(WIDE ? WIDE * 32 : 128, WIDE ? 1 : 7)
 #pragma unroll
                         for (int k = 0; k < E; ++k)
                             y[n][k] = 0.0f;
-                        if (wj[n] != 0.0f)
+                        if (__float_as_uint(wj[n]) != 0)
                             load_values<E>(sj, 8 * rows, y[n]);
                     }
 #pragma unroll

@@ -802,10 +802,11 @@ __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;"
 // Joins the partial results of an item with one set of rows: both groups, and
 // every copy, in chunks of columns by way of the item's Q tile, which nothing
 // reads any more.  `weight` is that of this thread's part of its row, `any`
-// whether its warp has values at all.  dst: a partial result's values, of `rows` rows.
+// whether its warp has values at all, `seen` whether its part does.  dst: a
+// partial result's values, of `rows` rows.
 template <int D>
 __device__ __forceinline__ void join_parts(uint8_t *scratch, uint32_t to, int part, int parts, int row, int have,
-                                           bool any, float weight, float *dst, int rows)
+                                           bool any, bool seen, float weight, float *dst, int rows)
 {
     constexpr int CW = D / 4;        // columns of a chunk: 256 rows of them fill the Q tile
     constexpr int V = CW / 4;        // 16-byte vectors of a row's chunk
@@ -819,7 +820,7 @@ __device__ __forceinline__ void join_parts(uint8_t *scratch, uint32_t to, int pa
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 *reinterpret_cast<float4 *>(scratch + ((part * have + row) * V + (v ^ (row % V))) * 16) =
-                    !any || weight == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                    !any || !seen ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
                                            : make_float4(o[4 * v] * weight, o[4 * v + 1] * weight,
                                                          o[4 * v + 2] * weight, o[4 * v + 3] * weight);
         }
@@ -930,7 +931,7 @@ __device__ void softmax_role(const TileParams &P, QuantShared &sh, uint8_t *tile
                 ml[at + rows + row] = make_float2(-F_INF, 0.0f);
             }
             join_parts<D>(tiles + qs * C::TILE, to, copy * 2 + g, 2 * copies, row, have, ok && cnt > 0 && active,
-                          l == 0.0f ? 0.0f : ex2a(m - ref), o_all + at * D, rows);
+                          l != 0.0f, ex2a(m - ref), o_all + at * D, rows);
             if (ok && threadIdx.x == 0)
                 mbar_arrive(&sh.q_empty[qs]);
         } else {
