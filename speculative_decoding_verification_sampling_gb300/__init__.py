@@ -165,18 +165,28 @@ def _dt(t):
     return SPEC_BF16 if t.dtype == torch.bfloat16 else SPEC_F32
 
 
-_ws_cache: dict = {}
+class _Kept(threading.local):
+    """Device memory kept from call to call, each thread its own: a call is more
+    than one launch, and those of two threads on one stream may interleave.
+    Freed as its thread ends."""
+
+    def __init__(self):
+        self.workspaces: dict = {}
+        self.scratch: dict = {}
+
+
+_kept = _Kept()
 
 
 def _workspace(device, stream, nbytes, sizes):
-    """A workspace cached per (device, stream).  The library leaves it ready
+    """This thread's workspace for (device, stream).  The library leaves it ready
     for the next call with the same sizes; when the sizes change, it is
     zero-filled again (on the same stream) before the call."""
     key = (device.index, stream)
-    ent = _ws_cache.get(key)
+    ent = _kept.workspaces.get(key)
     if ent is None or ent[0].numel() < nbytes:
         ent = [torch.zeros(max(nbytes, 1 << 16), dtype=torch.uint8, device=device), sizes]
-        _ws_cache[key] = ent
+        _kept.workspaces[key] = ent
     elif ent[1] != sizes:
         ent[0].zero_()
         ent[1] = sizes
@@ -452,12 +462,9 @@ def spec_attention_workspace_bytes(B: int, T: int, Hq: int, Hkv: int, D: int, P:
 _attention_bytes = functools.lru_cache(maxsize=256)(spec_attention_workspace_bytes)
 
 
-_scratch_cache: dict = {}
-
-
 def _scratch(nbytes, device, st, own_stream):
-    """Scratch that needs no zero-fill, kept per (device, stream) and handed to
-    one call after another of that stream.  It comes from the allocator's pool
+    """This thread's scratch for (device, stream), which needs no zero-fill and is
+    handed to one of its calls after another on that stream.  It comes from the allocator's pool
     of the stream that uses it, so a smaller one that is dropped is handed out
     again only to later work of that stream.  A call under capture gets scratch
     of its own from the graph's pool: the graph keeps the address."""
@@ -469,9 +476,9 @@ def _scratch(nbytes, device, st, own_stream):
     if torch.cuda.is_current_stream_capturing():
         return make(nbytes)
     key = (device.index, st)
-    buf = _scratch_cache.get(key)
+    buf = _kept.scratch.get(key)
     if buf is None or buf.numel() < nbytes:
-        buf = _scratch_cache[key] = make(max(nbytes, 1 << 20))
+        buf = _kept.scratch[key] = make(max(nbytes, 1 << 20))
     return buf
 
 
