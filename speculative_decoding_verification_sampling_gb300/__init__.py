@@ -12,6 +12,7 @@ target distribution, p the draft distribution, d_i the K drafted tokens.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -208,6 +209,21 @@ def _stream(device, stream):
         index = device.index
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device, stream):
+    """A context in which the stream that a call goes to is the current one: memory
+    for the call comes from that stream's pool, and what is asked of the current
+    stream is asked of it."""
+    if stream is None:
+        return _HERE
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = _stream(device, stream)
+        stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 def _ws_args(device, st, nbytes, workspace, sizes):
@@ -462,23 +478,18 @@ def spec_attention_workspace_bytes(B: int, T: int, Hq: int, Hkv: int, D: int, P:
 _attention_bytes = functools.lru_cache(maxsize=256)(spec_attention_workspace_bytes)
 
 
-def _scratch(nbytes, device, st, own_stream):
-    """This thread's scratch for (device, stream), which needs no zero-fill and is
-    handed to one of its calls after another on that stream.  It comes from the allocator's pool
-    of the stream that uses it, so a smaller one that is dropped is handed out
-    again only to later work of that stream.  A call under capture gets scratch
-    of its own from the graph's pool: the graph keeps the address."""
-    def make(n):
-        if not own_stream:
-            with torch.cuda.stream(torch.cuda.ExternalStream(st, device=device)):
-                return torch.empty(n, dtype=torch.uint8, device=device)
-        return torch.empty(n, dtype=torch.uint8, device=device)
+def _scratch(nbytes, device, st):
+    """This thread's scratch for (device, st), the current stream: it needs no
+    zero-fill and is handed to one of the thread's calls after another on that
+    stream.  It comes from the allocator's pool of the stream, so a smaller one that
+    is dropped is handed out again only to later work of it.  A call under capture
+    gets scratch of its own from the graph's pool: the graph keeps the address."""
     if torch.cuda.is_current_stream_capturing():
-        return make(nbytes)
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
     key = (device.index, st)
     buf = _kept.scratch.get(key)
     if buf is None or buf.numel() < nbytes:
-        buf = _kept.scratch[key] = make(max(nbytes, 1 << 20))
+        buf = _kept.scratch[key] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
     return buf
 
 
@@ -539,7 +550,8 @@ def spec_verify_attention(q: torch.Tensor, cache: torch.Tensor, seq_len: torch.T
         nbytes = _attention_bytes(B, T, Hq, H, D, P, L)
         if nbytes == 0:
             raise SpecVerifyError(1, "spec_verify_attention")
-        workspace = _scratch(nbytes, dev, st, stream is None)
+        with _on(dev, stream):
+            workspace = _scratch(nbytes, dev, st)
     elif not isinstance(workspace, torch.Tensor) or not workspace.is_cuda:
         raise TypeError("workspace must be a CUDA tensor")
 

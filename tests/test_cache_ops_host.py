@@ -15,7 +15,7 @@ def test_threads_on_one_stream_share_no_memory(monkeypatch):
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
 
     def hold():
-        return [sv._scratch(1 << 12, CPU, 77, True), sv._workspace(CPU, 77, 1 << 12, (1, 2, 3, 0))]
+        return [sv._scratch(1 << 12, CPU, 77), sv._workspace(CPU, 77, 1 << 12, (1, 2, 3, 0))]
     here, there = hold(), []
     t = threading.Thread(target=lambda: there.extend(hold()))
     t.start()

@@ -42,3 +42,47 @@ def test_two_threads_on_one_stream():
     for t in threads:
         t.join()
     assert not bad, bad[:10]
+
+
+def test_capture_on_a_stream_that_is_not_current():
+    """The graph has scratch of its own: a replay neither writes nor reads what the stream's other
+    calls keep, which a larger call has replaced meanwhile."""
+    a = _case(3, 5, 8, 2, 128, 300, 400, [400, 31, 260], True, "causal", seed=61)
+    big = _case(8, 61, 8, 2, 128, 300, 400, [400, 31, 260, 5, 6, 7, 8, 9], True, "causal", seed=62)
+    want = _call(a)
+    out, lse = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    side, other, graph = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    _call(a, stream=side, out=out, lse=lse)
+    side.synchronize()
+    out.zero_()
+    torch.cuda.synchronize()
+    kept = sv._kept.scratch[(0, side.cuda_stream)]
+    kept.fill_(0x55)
+    with torch.cuda.graph(graph, stream=side), torch.cuda.stream(other):
+        _call(a, stream=side, out=out, lse=lse)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert bool((kept == 0x55).all())
+    _call(big, stream=side)
+    side.synchronize()
+    assert sv._kept.scratch[(0, side.cuda_stream)].numel() > kept.numel()
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_streams_by_handle():
+    """A stream's handle serves as the stream does; 0 is the default stream."""
+    a = _case(3, 5, 8, 2, 128, 300, 400, [400, 31, 260], False, "causal", seed=63)
+    want = _call(a)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for s in (side.cuda_stream, 0, torch.cuda.default_stream()):
+        with sv._on(DEV, s):
+            assert torch.cuda.current_stream().cuda_stream == (s if isinstance(s, int) else 0)
+        got = _call(a, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
