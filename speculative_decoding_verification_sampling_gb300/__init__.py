@@ -166,51 +166,6 @@ def _dt(t):
     return SPEC_BF16 if t.dtype == torch.bfloat16 else SPEC_F32
 
 
-class _Kept(threading.local):
-    """Device memory kept from call to call, each thread its own: a call is more
-    than one launch, and those of two threads on one stream may interleave.
-    Freed as its thread ends."""
-
-    def __init__(self):
-        self.workspaces: dict = {}
-        self.scratch: dict = {}
-
-
-_kept = _Kept()
-
-
-def _workspace(device, stream, nbytes, sizes):
-    """This thread's workspace for (device, stream).  The library leaves it ready
-    for the next call with the same sizes; when the sizes change, it is
-    zero-filled again (on the same stream) before the call."""
-    key = (device.index, stream)
-    ent = _kept.workspaces.get(key)
-    if ent is None or ent[0].numel() < nbytes:
-        ent = [torch.zeros(max(nbytes, 1 << 16), dtype=torch.uint8, device=device), sizes]
-        _kept.workspaces[key] = ent
-    elif ent[1] != sizes:
-        ent[0].zero_()
-        ent[1] = sizes
-    return ent[0]
-
-
-def _outs(B, K, device, out_tokens, out_accept_len):
-    if out_tokens is None:
-        out_tokens = torch.empty((B, K + 1), dtype=torch.int32, device=device)
-    if out_accept_len is None:
-        out_accept_len = torch.empty((B,), dtype=torch.int32, device=device)
-    _check(out_tokens, (B, K + 1), (torch.int32,), "out_tokens")
-    _check(out_accept_len, (B,), (torch.int32,), "out_accept_len")
-    return out_tokens, out_accept_len
-
-
-def _stream(device, stream):
-    if stream is None:
-        index = device.index
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
 _HERE = contextlib.nullcontext()
 
 
@@ -226,9 +181,69 @@ def _on(device, stream):
     return torch.cuda.stream(stream)
 
 
-def _ws_args(device, st, nbytes, workspace, sizes):
+def _new(shape, dtype, device, stream):
+    """An output of a call that goes to `stream` (None: the current one).  It comes
+    from that stream's pool, as memory of another's may have work pending there, and
+    the allocator learns that the current stream is to use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(device, stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if _stream(device, None) != _stream(device, stream):
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+class _Kept(threading.local):
+    """Device memory kept from call to call, each thread its own: a call is more
+    than one launch, and those of two threads on one stream may interleave.
+    Freed as its thread ends."""
+
+    def __init__(self):
+        self.workspaces: dict = {}
+        self.scratch: dict = {}
+
+
+_kept = _Kept()
+
+
+def _workspace(device, st, nbytes, sizes, stream=None):
+    """This thread's workspace for (device, st), `stream` as the caller gave it.  The
+    library leaves it ready for the next call with the same sizes; when the sizes
+    change, it is zero-filled again (on the same stream) before the call."""
+    key = (device.index, st)
+    ent = _kept.workspaces.get(key)
+    if ent is None or ent[0].numel() < nbytes:
+        with _on(device, stream):
+            ent = [torch.zeros(max(nbytes, 1 << 16), dtype=torch.uint8, device=device), sizes]
+        _kept.workspaces[key] = ent
+    elif ent[1] != sizes:
+        with _on(device, stream):
+            ent[0].zero_()
+        ent[1] = sizes
+    return ent[0]
+
+
+def _outs(B, K, device, out_tokens, out_accept_len, stream):
+    if out_tokens is None:
+        out_tokens = _new((B, K + 1), torch.int32, device, stream)
+    if out_accept_len is None:
+        out_accept_len = _new((B,), torch.int32, device, stream)
+    _check(out_tokens, (B, K + 1), (torch.int32,), "out_tokens")
+    _check(out_accept_len, (B,), (torch.int32,), "out_accept_len")
+    return out_tokens, out_accept_len
+
+
+def _stream(device, stream):
+    if stream is None:
+        index = device.index
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _ws_args(device, st, nbytes, workspace, sizes, stream):
     if workspace is None:
-        workspace = _workspace(device, st, nbytes, sizes)
+        workspace = _workspace(device, st, nbytes, sizes, stream)
     elif not isinstance(workspace, torch.Tensor) or not workspace.is_cuda:
         raise TypeError("workspace must be a CUDA tensor")
     return workspace, workspace.numel() * workspace.element_size()
@@ -251,9 +266,9 @@ def spec_verify(target: torch.Tensor, draft: torch.Tensor, draft_tokens: torch.T
     _check(draft, (B, K, V), (torch.float32,) if draft_is_probs else (target.dtype,), "draft")
     _check(draft_tokens, (B, K), (torch.int32,), "draft_tokens")
     dev = target.device
-    out_tokens, out_accept_len = _outs(B, K, dev, out_tokens, out_accept_len)
+    out_tokens, out_accept_len = _outs(B, K, dev, out_tokens, out_accept_len, stream)
     st = _stream(dev, stream)
-    workspace, wsb = _ws_args(dev, st, spec_workspace_bytes(B, K, V, 0), workspace, (B, K, V, 0))
+    workspace, wsb = _ws_args(dev, st, spec_workspace_bytes(B, K, V, 0), workspace, (B, K, V, 0), stream)
     ax = aux._struct(B, K) if aux is not None else None
     rc = load().spec_verify(target.data_ptr(), _dt(target), draft.data_ptr(), _dt(draft), int(draft_is_probs),
                             draft_tokens.data_ptr(), B, K, V, float(T), int(seed) & (2**64 - 1),
@@ -272,9 +287,9 @@ def spec_verify_greedy(target: torch.Tensor, draft_tokens: torch.Tensor, *, out_
     _check(target, (B, K + 1, V), (torch.float32, torch.bfloat16), "target")
     _check(draft_tokens, (B, K), (torch.int32,), "draft_tokens")
     dev = target.device
-    out_tokens, out_accept_len = _outs(B, K, dev, out_tokens, out_accept_len)
+    out_tokens, out_accept_len = _outs(B, K, dev, out_tokens, out_accept_len, stream)
     st = _stream(dev, stream)
-    workspace, wsb = _ws_args(dev, st, spec_workspace_bytes(B, K, V, 0), workspace, (B, K, V, 0))
+    workspace, wsb = _ws_args(dev, st, spec_workspace_bytes(B, K, V, 0), workspace, (B, K, V, 0), stream)
     ax = aux._struct(B, K) if aux is not None else None
     rc = load().spec_verify_greedy(target.data_ptr(), _dt(target), draft_tokens.data_ptr(), B, K, V,
                                    out_tokens.data_ptr(), out_accept_len.data_ptr(), workspace.data_ptr(), wsb,
@@ -297,7 +312,7 @@ def spec_verify_static(target: torch.Tensor, draft: torch.Tensor | None, draft_t
         _check(draft, (B, K, V), (target.dtype,), "draft")
     _check(draft_tokens, (B, K), (torch.int32,), "draft_tokens")
     dev = target.device
-    out_tokens, out_accept_len = _outs(B, K, dev, out_tokens, out_accept_len)
+    out_tokens, out_accept_len = _outs(B, K, dev, out_tokens, out_accept_len, stream)
     st = _stream(dev, stream)
     ax = aux._struct(B, K) if aux is not None else None
     rc = load().spec_verify_static(target.data_ptr(), _dt(target), draft.data_ptr() if (draft is not None and T > 0)
@@ -325,9 +340,9 @@ def spec_verify_shortlist(target: torch.Tensor, draft_sl: torch.Tensor, shortlis
     _check(shortlist_idx, (B, S), (torch.int32,), "shortlist_idx")
     _check(draft_tokens, (B, K), (torch.int32,), "draft_tokens")
     dev = target.device
-    out_tokens, out_accept_len = _outs(B, K, dev, out_tokens, out_accept_len)
+    out_tokens, out_accept_len = _outs(B, K, dev, out_tokens, out_accept_len, stream)
     st = _stream(dev, stream)
-    workspace, wsb = _ws_args(dev, st, spec_workspace_bytes(B, K, V, S), workspace, (B, K, V, S))
+    workspace, wsb = _ws_args(dev, st, spec_workspace_bytes(B, K, V, S), workspace, (B, K, V, S), stream)
     ax = aux._struct(B, K) if aux is not None else None
     rc = load().spec_verify_shortlist(target.data_ptr(), _dt(target), draft_sl.data_ptr(), _dt(draft_sl),
                                       int(draft_is_probs), shortlist_idx.data_ptr(), S, draft_tokens.data_ptr(),
@@ -342,7 +357,7 @@ def spec_verify_shortlist(target: torch.Tensor, draft_sl: torch.Tensor, shortlis
 def spec_philox_words(seed: int, tag: int, B: int, P: int, device=None, stream=None) -> torch.Tensor:
     """The Philox4x32-10 words the kernels draw: [B][P][4] (int32 storage of uint32)."""
     device = torch.device(device if device is not None else "cuda")
-    out = torch.empty((B, P, 4), dtype=torch.int32, device=device)
+    out = _new((B, P, 4), torch.int32, device, stream)
     st = _stream(device, stream)
     rc = load().spec_philox_words(int(seed) & (2**64 - 1), int(tag), B, P, out.data_ptr(), st)
     if rc:
@@ -360,9 +375,9 @@ def spec_draft_sample(draft: torch.Tensor, T: float, seed: int, *, out_tokens=No
     _check(draft, (B, K, V), (torch.float32, torch.bfloat16), "draft")
     dev = draft.device
     if out_tokens is None:
-        out_tokens = torch.empty((B, K), dtype=torch.int32, device=dev)
+        out_tokens = _new((B, K), torch.int32, dev, stream)
     if out_prob is None:
-        out_prob = torch.empty((B, K), dtype=torch.float32, device=dev)
+        out_prob = _new((B, K), torch.float32, dev, stream)
     _check(out_tokens, (B, K), (torch.int32,), "out_tokens")
     _check(out_prob, (B, K), (torch.float32,), "out_prob")
     if device_status is not None:
@@ -458,7 +473,7 @@ def spec_kv_read_quant(cache: torch.Tensor, scale: torch.Tensor, start: torch.Te
     if out is None:
         if count < 1:
             raise ValueError("count must be at least 1")
-        out = torch.empty((NL, B, count, 2, H, D), dtype=dtype, device=cache.device)
+        out = _new((NL, B, count, 2, H, D), dtype, cache.device, stream)
     _check(out, (NL, B, count, 2, H, D), (torch.float32, torch.bfloat16), "out")
     if device_status is not None:
         _check(device_status, (1,), (torch.int32,), "device_status")
@@ -535,11 +550,11 @@ def spec_verify_attention(q: torch.Tensor, cache: torch.Tensor, seq_len: torch.T
     if mask is not None:
         _check(mask, (B, T, T), (torch.uint8,), "mask")
     if out is None:
-        out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=dev)
+        out = _new((B, T, Hq, D), torch.bfloat16, dev, stream)
     else:
         _check(out, (B, T, Hq, D), (torch.bfloat16,), "out")
     if lse is None:
-        lse = torch.empty((B, T, Hq), dtype=torch.float32, device=dev)
+        lse = _new((B, T, Hq), torch.float32, dev, stream)
     else:
         _check(lse, (B, T, Hq), (torch.float32,), "lse")
     if device_status is not None:
@@ -582,10 +597,10 @@ def spec_verify_tree_greedy(target: torch.Tensor, tree_tokens: torch.Tensor, par
     if nbytes == 0:
         raise SpecVerifyError(1, "spec_verify_tree_greedy")
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    out_t = torch.empty((B, N), dtype=torch.int32, device=dev)
-    out_n = torch.empty((B, N), dtype=torch.int32, device=dev)
-    out_l = torch.empty((B,), dtype=torch.int32, device=dev)
+        workspace = _new((nbytes,), torch.uint8, dev, stream)
+    out_t = _new((B, N), torch.int32, dev, stream)
+    out_n = _new((B, N), torch.int32, dev, stream)
+    out_l = _new((B,), torch.int32, dev, stream)
     if device_status is not None:
         _check(device_status, (1,), (torch.int32,), "device_status")
     st = _stream(dev, stream)
@@ -603,7 +618,7 @@ def spec_tree_mask(parent: torch.Tensor, *, out=None, device_status=None, stream
     B, N = parent.shape
     _check(parent, (B, N), (torch.int32,), "parent")
     if out is None:
-        out = torch.empty((B, N, N), dtype=torch.uint8, device=parent.device)
+        out = _new((B, N, N), torch.uint8, parent.device, stream)
     _check(out, (B, N, N), (torch.uint8,), "out")
     if device_status is not None:
         _check(device_status, (1,), (torch.int32,), "device_status")
@@ -642,9 +657,9 @@ def spec_verify_shortlist_pos(target: torch.Tensor, draft_sl: torch.Tensor, shor
     if shortlist_len is not None:
         lens = (ctypes.c_int32 * K)(*[int(x) for x in shortlist_len])
     dev = target.device
-    out_tokens, out_accept_len = _outs(B, K, dev, out_tokens, out_accept_len)
+    out_tokens, out_accept_len = _outs(B, K, dev, out_tokens, out_accept_len, stream)
     st = _stream(dev, stream)
-    workspace, wsb = _ws_args(dev, st, spec_workspace_bytes(B, K, V, S), workspace, (B, K, V, S))
+    workspace, wsb = _ws_args(dev, st, spec_workspace_bytes(B, K, V, S), workspace, (B, K, V, S), stream)
     ax = aux._struct(B, K) if aux is not None else None
     rc = load().spec_verify_shortlist_pos(target.data_ptr(), _dt(target), draft_sl.data_ptr(), _dt(draft_sl),
                                           shortlist_idx.data_ptr(), seq, pos, lens, S, draft_tokens.data_ptr(),

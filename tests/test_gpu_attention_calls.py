@@ -86,3 +86,57 @@ def test_streams_by_handle():
         got = _call(a, stream=s)
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def _spin(stream, ms=30):
+    """Keeps a stream busy for a while."""
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(int(ms * 1.5e6))
+
+
+def _side_calls():
+    from speculative_decoding_verification_sampling_gb300 import synth
+    a = _case(3, 5, 8, 2, 128, 300, 400, [400, 31, 260], False, "causal", seed=64)
+    codes = torch.full((1, 3, 40, 2, 2, 64), 56, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    scale = torch.full((1, 3, 40, 2, 2), 127, dtype=torch.uint8, device=DEV)
+    n = torch.tensor([40, 7, 0], dtype=torch.int32, device=DEV)
+    cfg = synth.stochastic_gaussian(6, 4, 5000, torch.bfloat16, 1.0, seed=3)
+    tgt, drf, tok = (cfg[k].to(DEV) for k in ("target", "draft", "draft_tokens"))
+    par = torch.tensor([[-1, 0, 0, 1, 1, 3]], dtype=torch.int32, device=DEV)
+    toks = torch.zeros_like(par)
+    tree = torch.randn((1, 6, 5000), generator=torch.Generator().manual_seed(1)).to(DEV)
+    return {
+        "attention": lambda **kw: _call(a, **kw),
+        "read": lambda **kw: (sv.spec_kv_read_quant(codes, scale, None, n, 40, **kw),),
+        "verify": lambda **kw: sv.spec_verify(tgt, drf, tok, 1.0, 7, **kw),
+        "draft": lambda **kw: sv.spec_draft_sample(drf, 1.0, 7, **kw),
+        "tree": lambda **kw: sv.spec_verify_tree_greedy(tree, toks, par, **kw),
+        "mask": lambda **kw: (sv.spec_tree_mask(par, **kw),),
+        "philox": lambda **kw: (sv.spec_philox_words(7, 0, 64, 64, device=DEV, **kw),),
+    }
+
+
+@pytest.mark.parametrize("name", ["attention", "read", "verify", "draft", "tree", "mask", "philox"])
+def test_outputs_of_a_call_on_another_stream_are_its_own(name):
+    """A result whose memory the current stream has work pending on, or that is dropped before the
+    other stream has written it, is nobody else's meanwhile."""
+    call = _side_calls()[name]
+    want = [x.clone() for x in call()]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    # blocks of the outputs' sizes, freed on the current stream with a late write pending
+    _spin(torch.cuda.current_stream())
+    for x in [torch.empty_like(w) for w in want for _ in range(4)]:
+        x.view(torch.uint8).fill_(0xee)
+    del x
+    got = call(stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+    # dropped at once: what the current stream allocates next is not written any more
+    del got
+    _spin(side)
+    got = call(stream=side)
+    del got
+    mine = [torch.full_like(w.view(torch.uint8), 0x33) for w in want for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(bool((x == 0x33).all()) for x in mine)
