@@ -169,28 +169,46 @@ def _dt(t):
 _HERE = contextlib.nullcontext()
 
 
+class _On:
+    """torch.cuda.stream in half its time."""
+    __slots__ = ("stream", "before", "device")
+
+    def __init__(self, stream, device):
+        self.stream, self.device = stream, torch.cuda.current_device()
+        self.before = torch.cuda.current_stream(device)
+
+    def __enter__(self):
+        torch.cuda.set_stream(self.stream)
+        return self.before
+
+    def __exit__(self, *exc):
+        torch.cuda.set_stream(self.before)
+        if self.device != self.before.device_index:
+            torch.cuda.set_device(self.device)
+
+
 def _on(device, stream):
-    """A context in which the stream that a call goes to is the current one: memory
-    for the call comes from that stream's pool, and what is asked of the current
-    stream is asked of it."""
+    """A context in which the stream that a call goes to (None: the current one) is
+    the current one: memory for the call comes from that stream's pool, and what is
+    asked of the current stream is asked of it.  Gives the stream that was current,
+    or None where that is the same."""
     if stream is None:
         return _HERE
+    raw = _stream(device, stream)
+    if raw == _stream(device, None):
+        return _HERE
     if not isinstance(stream, torch.cuda.Stream):
-        raw = _stream(device, stream)
         stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
-    return torch.cuda.stream(stream)
+    return _On(stream, device)
 
 
-def _new(shape, dtype, device, stream):
-    """An output of a call that goes to `stream` (None: the current one).  It comes
-    from that stream's pool, as memory of another's may have work pending there, and
-    the allocator learns that the current stream is to use it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with _on(device, stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    if _stream(device, None) != _stream(device, stream):
-        t.record_stream(torch.cuda.current_stream(device))
+def _new(shape, dtype, device, before):
+    """An output, made inside `_on`.  It comes from the pool of the stream that the
+    call goes to, as memory of another's may have work pending there, and the
+    allocator learns that the stream that was current, `before`, is to use it."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if before is not None:
+        t.record_stream(before)
     return t
 
 
@@ -207,28 +225,30 @@ class _Kept(threading.local):
 _kept = _Kept()
 
 
-def _workspace(device, st, nbytes, sizes, stream=None):
-    """This thread's workspace for (device, st), `stream` as the caller gave it.  The
-    library leaves it ready for the next call with the same sizes; when the sizes
-    change, it is zero-filled again (on the same stream) before the call."""
+def _workspace(device, st, nbytes, sizes):
+    """This thread's workspace for (device, st), the current stream.  The library
+    leaves it ready for the next call with the same sizes; when the sizes change, it
+    is zero-filled again (on the same stream) before the call.  A call under capture
+    gets one of its own from the graph's pool, zero-filled by every replay: other
+    calls may have used the kept one with other sizes since, or have replaced it."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
     key = (device.index, st)
     ent = _kept.workspaces.get(key)
     if ent is None or ent[0].numel() < nbytes:
-        with _on(device, stream):
-            ent = [torch.zeros(max(nbytes, 1 << 16), dtype=torch.uint8, device=device), sizes]
+        ent = [torch.zeros(max(nbytes, 1 << 16), dtype=torch.uint8, device=device), sizes]
         _kept.workspaces[key] = ent
     elif ent[1] != sizes:
-        with _on(device, stream):
-            ent[0].zero_()
+        ent[0].zero_()
         ent[1] = sizes
     return ent[0]
 
 
-def _outs(B, K, device, out_tokens, out_accept_len, stream):
+def _outs(B, K, device, out_tokens, out_accept_len, before):
     if out_tokens is None:
-        out_tokens = _new((B, K + 1), torch.int32, device, stream)
+        out_tokens = _new((B, K + 1), torch.int32, device, before)
     if out_accept_len is None:
-        out_accept_len = _new((B,), torch.int32, device, stream)
+        out_accept_len = _new((B,), torch.int32, device, before)
     _check(out_tokens, (B, K + 1), (torch.int32,), "out_tokens")
     _check(out_accept_len, (B,), (torch.int32,), "out_accept_len")
     return out_tokens, out_accept_len
@@ -241,9 +261,9 @@ def _stream(device, stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _ws_args(device, st, nbytes, workspace, sizes, stream):
+def _ws_args(device, st, nbytes, workspace, sizes):
     if workspace is None:
-        workspace = _workspace(device, st, nbytes, sizes, stream)
+        workspace = _workspace(device, st, nbytes, sizes)
     elif not isinstance(workspace, torch.Tensor) or not workspace.is_cuda:
         raise TypeError("workspace must be a CUDA tensor")
     return workspace, workspace.numel() * workspace.element_size()
@@ -266,9 +286,10 @@ def spec_verify(target: torch.Tensor, draft: torch.Tensor, draft_tokens: torch.T
     _check(draft, (B, K, V), (torch.float32,) if draft_is_probs else (target.dtype,), "draft")
     _check(draft_tokens, (B, K), (torch.int32,), "draft_tokens")
     dev = target.device
-    out_tokens, out_accept_len = _outs(B, K, dev, out_tokens, out_accept_len, stream)
     st = _stream(dev, stream)
-    workspace, wsb = _ws_args(dev, st, spec_workspace_bytes(B, K, V, 0), workspace, (B, K, V, 0), stream)
+    with _on(dev, stream) as before:
+        out_tokens, out_accept_len = _outs(B, K, dev, out_tokens, out_accept_len, before)
+        workspace, wsb = _ws_args(dev, st, spec_workspace_bytes(B, K, V, 0), workspace, (B, K, V, 0))
     ax = aux._struct(B, K) if aux is not None else None
     rc = load().spec_verify(target.data_ptr(), _dt(target), draft.data_ptr(), _dt(draft), int(draft_is_probs),
                             draft_tokens.data_ptr(), B, K, V, float(T), int(seed) & (2**64 - 1),
@@ -287,9 +308,10 @@ def spec_verify_greedy(target: torch.Tensor, draft_tokens: torch.Tensor, *, out_
     _check(target, (B, K + 1, V), (torch.float32, torch.bfloat16), "target")
     _check(draft_tokens, (B, K), (torch.int32,), "draft_tokens")
     dev = target.device
-    out_tokens, out_accept_len = _outs(B, K, dev, out_tokens, out_accept_len, stream)
     st = _stream(dev, stream)
-    workspace, wsb = _ws_args(dev, st, spec_workspace_bytes(B, K, V, 0), workspace, (B, K, V, 0), stream)
+    with _on(dev, stream) as before:
+        out_tokens, out_accept_len = _outs(B, K, dev, out_tokens, out_accept_len, before)
+        workspace, wsb = _ws_args(dev, st, spec_workspace_bytes(B, K, V, 0), workspace, (B, K, V, 0))
     ax = aux._struct(B, K) if aux is not None else None
     rc = load().spec_verify_greedy(target.data_ptr(), _dt(target), draft_tokens.data_ptr(), B, K, V,
                                    out_tokens.data_ptr(), out_accept_len.data_ptr(), workspace.data_ptr(), wsb,
@@ -312,8 +334,9 @@ def spec_verify_static(target: torch.Tensor, draft: torch.Tensor | None, draft_t
         _check(draft, (B, K, V), (target.dtype,), "draft")
     _check(draft_tokens, (B, K), (torch.int32,), "draft_tokens")
     dev = target.device
-    out_tokens, out_accept_len = _outs(B, K, dev, out_tokens, out_accept_len, stream)
     st = _stream(dev, stream)
+    with _on(dev, stream) as before:
+        out_tokens, out_accept_len = _outs(B, K, dev, out_tokens, out_accept_len, before)
     ax = aux._struct(B, K) if aux is not None else None
     rc = load().spec_verify_static(target.data_ptr(), _dt(target), draft.data_ptr() if (draft is not None and T > 0)
                                    else None, draft_tokens.data_ptr(), B, K, V, float(T), int(seed),
@@ -340,9 +363,10 @@ def spec_verify_shortlist(target: torch.Tensor, draft_sl: torch.Tensor, shortlis
     _check(shortlist_idx, (B, S), (torch.int32,), "shortlist_idx")
     _check(draft_tokens, (B, K), (torch.int32,), "draft_tokens")
     dev = target.device
-    out_tokens, out_accept_len = _outs(B, K, dev, out_tokens, out_accept_len, stream)
     st = _stream(dev, stream)
-    workspace, wsb = _ws_args(dev, st, spec_workspace_bytes(B, K, V, S), workspace, (B, K, V, S), stream)
+    with _on(dev, stream) as before:
+        out_tokens, out_accept_len = _outs(B, K, dev, out_tokens, out_accept_len, before)
+        workspace, wsb = _ws_args(dev, st, spec_workspace_bytes(B, K, V, S), workspace, (B, K, V, S))
     ax = aux._struct(B, K) if aux is not None else None
     rc = load().spec_verify_shortlist(target.data_ptr(), _dt(target), draft_sl.data_ptr(), _dt(draft_sl),
                                       int(draft_is_probs), shortlist_idx.data_ptr(), S, draft_tokens.data_ptr(),
@@ -357,8 +381,9 @@ def spec_verify_shortlist(target: torch.Tensor, draft_sl: torch.Tensor, shortlis
 def spec_philox_words(seed: int, tag: int, B: int, P: int, device=None, stream=None) -> torch.Tensor:
     """The Philox4x32-10 words the kernels draw: [B][P][4] (int32 storage of uint32)."""
     device = torch.device(device if device is not None else "cuda")
-    out = _new((B, P, 4), torch.int32, device, stream)
     st = _stream(device, stream)
+    with _on(device, stream) as before:
+        out = _new((B, P, 4), torch.int32, device, before)
     rc = load().spec_philox_words(int(seed) & (2**64 - 1), int(tag), B, P, out.data_ptr(), st)
     if rc:
         raise SpecVerifyError(rc, "spec_philox_words")
@@ -374,10 +399,11 @@ def spec_draft_sample(draft: torch.Tensor, T: float, seed: int, *, out_tokens=No
     B, K, V = draft.shape
     _check(draft, (B, K, V), (torch.float32, torch.bfloat16), "draft")
     dev = draft.device
-    if out_tokens is None:
-        out_tokens = _new((B, K), torch.int32, dev, stream)
-    if out_prob is None:
-        out_prob = _new((B, K), torch.float32, dev, stream)
+    with _on(dev, stream) as before:
+        if out_tokens is None:
+            out_tokens = _new((B, K), torch.int32, dev, before)
+        if out_prob is None:
+            out_prob = _new((B, K), torch.float32, dev, before)
     _check(out_tokens, (B, K), (torch.int32,), "out_tokens")
     _check(out_prob, (B, K), (torch.float32,), "out_prob")
     if device_status is not None:
@@ -473,7 +499,8 @@ def spec_kv_read_quant(cache: torch.Tensor, scale: torch.Tensor, start: torch.Te
     if out is None:
         if count < 1:
             raise ValueError("count must be at least 1")
-        out = _new((NL, B, count, 2, H, D), dtype, cache.device, stream)
+        with _on(cache.device, stream) as before:
+            out = _new((NL, B, count, 2, H, D), dtype, cache.device, before)
     _check(out, (NL, B, count, 2, H, D), (torch.float32, torch.bfloat16), "out")
     if device_status is not None:
         _check(device_status, (1,), (torch.int32,), "device_status")
@@ -549,26 +576,26 @@ def spec_verify_attention(q: torch.Tensor, cache: torch.Tensor, seq_len: torch.T
         _check(staged, (B, T, 2, H, D), (torch.bfloat16,), "staged")
     if mask is not None:
         _check(mask, (B, T, T), (torch.uint8,), "mask")
-    if out is None:
-        out = _new((B, T, Hq, D), torch.bfloat16, dev, stream)
-    else:
+    if out is not None:
         _check(out, (B, T, Hq, D), (torch.bfloat16,), "out")
-    if lse is None:
-        lse = _new((B, T, Hq), torch.float32, dev, stream)
-    else:
+    if lse is not None:
         _check(lse, (B, T, Hq), (torch.float32,), "lse")
     if device_status is not None:
         _check(device_status, (1,), (torch.int32,), "device_status")
+    if workspace is not None and (not isinstance(workspace, torch.Tensor) or not workspace.is_cuda):
+        raise TypeError("workspace must be a CUDA tensor")
+    nbytes = 0 if workspace is not None else _attention_bytes(B, T, Hq, H, D, P, L)
+    if workspace is None and nbytes == 0:
+        raise SpecVerifyError(1, "spec_verify_attention")
     st = _stream(dev, stream)
     lib = load()
-    if workspace is None:
-        nbytes = _attention_bytes(B, T, Hq, H, D, P, L)
-        if nbytes == 0:
-            raise SpecVerifyError(1, "spec_verify_attention")
-        with _on(dev, stream):
+    with _on(dev, stream) as before:
+        if out is None:
+            out = _new((B, T, Hq, D), torch.bfloat16, dev, before)
+        if lse is None:
+            lse = _new((B, T, Hq), torch.float32, dev, before)
+        if workspace is None:
             workspace = _scratch(nbytes, dev, st)
-    elif not isinstance(workspace, torch.Tensor) or not workspace.is_cuda:
-        raise TypeError("workspace must be a CUDA tensor")
 
     def ptr(t):
         return t.data_ptr() if t is not None else None
@@ -596,11 +623,12 @@ def spec_verify_tree_greedy(target: torch.Tensor, tree_tokens: torch.Tensor, par
     nbytes = int(load().spec_tree_workspace_bytes(B, N, V))
     if nbytes == 0:
         raise SpecVerifyError(1, "spec_verify_tree_greedy")
-    if workspace is None:
-        workspace = _new((nbytes,), torch.uint8, dev, stream)
-    out_t = _new((B, N), torch.int32, dev, stream)
-    out_n = _new((B, N), torch.int32, dev, stream)
-    out_l = _new((B,), torch.int32, dev, stream)
+    with _on(dev, stream) as before:
+        if workspace is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        out_t = _new((B, N), torch.int32, dev, before)
+        out_n = _new((B, N), torch.int32, dev, before)
+        out_l = _new((B,), torch.int32, dev, before)
     if device_status is not None:
         _check(device_status, (1,), (torch.int32,), "device_status")
     st = _stream(dev, stream)
@@ -618,7 +646,8 @@ def spec_tree_mask(parent: torch.Tensor, *, out=None, device_status=None, stream
     B, N = parent.shape
     _check(parent, (B, N), (torch.int32,), "parent")
     if out is None:
-        out = _new((B, N, N), torch.uint8, parent.device, stream)
+        with _on(parent.device, stream) as before:
+            out = _new((B, N, N), torch.uint8, parent.device, before)
     _check(out, (B, N, N), (torch.uint8,), "out")
     if device_status is not None:
         _check(device_status, (1,), (torch.int32,), "device_status")
@@ -657,9 +686,10 @@ def spec_verify_shortlist_pos(target: torch.Tensor, draft_sl: torch.Tensor, shor
     if shortlist_len is not None:
         lens = (ctypes.c_int32 * K)(*[int(x) for x in shortlist_len])
     dev = target.device
-    out_tokens, out_accept_len = _outs(B, K, dev, out_tokens, out_accept_len, stream)
     st = _stream(dev, stream)
-    workspace, wsb = _ws_args(dev, st, spec_workspace_bytes(B, K, V, S), workspace, (B, K, V, S), stream)
+    with _on(dev, stream) as before:
+        out_tokens, out_accept_len = _outs(B, K, dev, out_tokens, out_accept_len, before)
+        workspace, wsb = _ws_args(dev, st, spec_workspace_bytes(B, K, V, S), workspace, (B, K, V, S))
     ax = aux._struct(B, K) if aux is not None else None
     rc = load().spec_verify_shortlist_pos(target.data_ptr(), _dt(target), draft_sl.data_ptr(), _dt(draft_sl),
                                           shortlist_idx.data_ptr(), seq, pos, lens, S, draft_tokens.data_ptr(),

@@ -140,3 +140,38 @@ def test_outputs_of_a_call_on_another_stream_are_its_own(name):
     mine = [torch.full_like(w.view(torch.uint8), 0x33) for w in want for _ in range(4)]
     torch.cuda.synchronize()
     assert all(bool((x == 0x33).all()) for x in mine)
+
+
+@pytest.mark.parametrize("kernel", [None, "cluster", "general", "rows"])
+def test_a_captured_verification_has_its_own_workspace(kernel, monkeypatch):
+    """Replays between eager calls of other sizes on the same stream, one of which replaces the
+    workspace that the stream's calls share."""
+    from speculative_decoding_verification_sampling_gb300 import synth
+    if kernel:
+        monkeypatch.setenv("SPECVERIFY_KERNEL", kernel)
+
+    def inputs(B, K, V, seed):
+        cfg = synth.stochastic_gaussian(B, K, V, torch.bfloat16, 1.0, seed=seed)
+        return [cfg[k].to(DEV) for k in ("target", "draft", "draft_tokens")]
+    small, wide, large = inputs(6, 4, 8192, 3), inputs(3, 7, 16384, 4), inputs(24, 4, 32768, 5)
+    want = [[x.clone() for x in sv.spec_verify(*a, 1.0, 7)] for a in (small, wide, large)]
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        sv.spec_verify(*small, 1.0, 7)
+        side.synchronize()
+        kept = sv._kept.workspaces[(0, side.cuda_stream)][0]
+        before = kept.clone()
+        with torch.cuda.graph(graph, stream=side):
+            held = sv.spec_verify(*small, 1.0, 7)
+        for i, a in enumerate((None, wide, large)):
+            if a is not None:
+                got = sv.spec_verify(*a, 1.0, 7)
+                assert all(torch.equal(g, w) for g, w in zip(got, want[i]))
+            for x in held:
+                x.zero_()
+            graph.replay()
+            side.synchronize()
+            assert all(torch.equal(g, w) for g, w in zip(held, want[0]))
+            if a is None:
+                assert torch.equal(kept, before)
