@@ -31,9 +31,12 @@
 // unit's largest, which becomes 2^7: float16 holds a code times 2^s exactly
 // for s in [-15, 7], and a head whose scale is more than 2^22 below loses its
 // last bits (at 2^-40 of the unit's largest element).  What the largest stands
-// for goes back in exactly, into the exponent of the weights (they are
-// 2^(c S + bv - m), and l takes them times 2^-bv).  P is rounded to float16
-// here, 2^-11 of a weight.  With few rows, where HBM is the bound, one warp's
+// for, bv, goes back in exactly, into the exponent of the weights: O holds
+// 2^(c S + bv - m) V with a reference m of its own, while l holds 2^(c S - n)
+// with the row's maximum n, so a unit counts in l whatever its values' scale is.
+// A unit that is nothing beside m (2^-64 or less) is summed up relative to its
+// own maximum; its P are 0 in float16 either way.  The results leave with n
+// alone: O times 2^(m - n).  P is rounded to float16 here, 2^-11 of a weight.  With few rows, where HBM is the bound, one warp's
 // pass over 128 scores per row and their scales is too long a chain: the rows
 // then lie in their tile two or four times, and each warp of a group takes the
 // columns that fall to its copy.
@@ -257,7 +260,7 @@ struct QuantShared : TileShared {
     uint16_t v_fac[FAC][AT_UNIT];                 // float16 factors of its rows of V
     float v_unit[FAC];                            // log2 of what 1 stands for in its V
     uint8_t q_unit[2][AT_ROWS];                   // the scale bytes of Q's rows
-    float2 ml[2][AT_ROWS];                        // m and l of both groups' rows, as an item is joined
+    float2 nl[2][AT_ROWS];                        // n and l of both groups' rows, as an item is joined
 };
 
 constexpr uint32_t SMEM_MAX = 232448;
@@ -660,7 +663,7 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint8_t *tiles, ui
 }
 
 // Raises a row's reference exponent m to its scores' maximum s where that has
-// passed it by more than 8, and scales l and O down with it.
+// passed it by more than 8, and scales O and l down with it.
 template <int D>
 __device__ __forceinline__ void follow_maximum(uint32_t to, float s, bool first, bool real, float &m, float &l)
 {
@@ -732,12 +735,13 @@ __device__ __forceinline__ void softmax_unit(uint32_t ts, uint32_t to, int nv, f
 
 // The same with 8-bit entries, over this copy's `nc` columns from `col` on (nv
 // of them in the stretch): scores times the scales of their rows of K, V's unit
-// in the exponent, P in float16.  In steps of 32 columns, twice over S: the
+// in the exponent, P in float16; n and l are the row's maximum and its sum.  In steps of 32 columns, twice over S: the
 // loops are short on purpose, the warps of this kernel run six different
 // programs and have to share the instruction cache.
 template <int D>
 __device__ __forceinline__ void softmax_unit8(uint32_t ts, uint32_t to, int col, int nc, int nv, float c, float bv,
-                                              const float4 *k_fac, bool first, bool real, float &m, float &l)
+                                              const float4 *k_fac, bool first, bool real, float &m, float &n,
+                                              float &l)
 {
     float x[32];
     auto load = [&](int k0) {
@@ -764,8 +768,11 @@ __device__ __forceinline__ void softmax_unit8(uint32_t ts, uint32_t to, int col,
             for (int u = 0; u < 4; ++u)
                 top[u] = fmaxf(top[u], x[k + u]);
     }
-    follow_maximum<D>(to, fmaf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), c, bv), first, real, m, l);
-    const float ref = (m == -F_INF ? 0.0f : m) - bv;
+    const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+    float none = 0.0f;
+    follow_maximum<D>(to, most + bv, first, real, m, none);
+    const float up = fmaxf(n, most), base = up == -F_INF ? 0.0f : up;
+    const float ref = most == -F_INF ? base : fminf(m - bv, most + 64.0f);
     const f2 cc = pk(c, c), nref = pk(-ref, -ref);
     f2 sum[2] = {pk(0.0f, 0.0f), pk(0.0f, 0.0f)};
     uint32_t p[16];
@@ -792,7 +799,8 @@ __device__ __forceinline__ void softmax_unit8(uint32_t ts, uint32_t to, int col,
         tmem_st(ts + ((col + k0) & (AT_UNIT - 1)) / 2, p);
     float lo, hi;
     upk(add2(sum[0], sum[1]), lo, hi);
-    l += (lo + hi) * ex2a(-bv);   // a power of two: exact
+    l = fmaf(lo + hi, ex2a(ref - base), l * ex2a(n - base));
+    n = up;
     tmem_st_wait();
 }
 
@@ -801,12 +809,12 @@ __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;"
 
 // Joins the partial results of an item with one set of rows: both groups, and
 // every copy, in chunks of columns by way of the item's Q tile, which nothing
-// reads any more.  `weight` is that of this thread's part of its row, `any`
-// whether its warp has values at all, `seen` whether its part does.  dst: a
-// partial result's values, of `rows` rows.
+// reads any more.  `half` is the root of the weight of this thread's part of its
+// row, `any` whether its warp has values at all, `seen` whether its part does.
+// dst: a partial result's values, of `rows` rows.
 template <int D>
 __device__ __forceinline__ void join_parts(uint8_t *scratch, uint32_t to, int part, int parts, int row, int have,
-                                           bool any, bool seen, float weight, float *dst, int rows)
+                                           bool any, bool seen, float half, float *dst, int rows)
 {
     constexpr int CW = D / 4;        // columns of a chunk: 256 rows of them fill the Q tile
     constexpr int V = CW / 4;        // 16-byte vectors of a row's chunk
@@ -821,8 +829,8 @@ __device__ __forceinline__ void join_parts(uint8_t *scratch, uint32_t to, int pa
             for (int v = 0; v < V; ++v)
                 *reinterpret_cast<float4 *>(scratch + ((part * have + row) * V + (v ^ (row % V))) * 16) =
                     !any || !seen ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
-                                           : make_float4(o[4 * v] * weight, o[4 * v + 1] * weight,
-                                                         o[4 * v + 2] * weight, o[4 * v + 3] * weight);
+                                  : make_float4(o[4 * v] * half * half, o[4 * v + 1] * half * half,
+                                                o[4 * v + 2] * half * half, o[4 * v + 3] * half * half);
         }
         softmax_sync();
 #pragma unroll 1
@@ -872,7 +880,7 @@ __device__ void softmax_role(const TileParams &P, QuantShared &sh, uint8_t *tile
         const int have = min(max(it.tokens - (it.two ? g * tq : 0), 0), tq) * P.A.G;
         const bool active = row - lane < have;
         const int cnt = it.two ? it.n : (it.n - g + 1) / 2;
-        float m = -F_INF, l = 0.0f;
+        float m = -F_INF, n = -F_INF, l = 0.0f;   // n: with 8-bit entries, l's reference
 #pragma unroll 1
         for (int i = 0; ok && i < cnt; ++i) {
             const int j = it.two ? i : 2 * i + g, nv = it.left - j * AT_UNIT - col;
@@ -892,7 +900,7 @@ __device__ void softmax_role(const TileParams &P, QuantShared &sh, uint8_t *tile
                 }
                 if constexpr (Q8)
                     softmax_unit8<D>(ts, to, col, AT_UNIT / copies, nv, c, bv, sh.k_fac[fs] + col / 4, i == 0,
-                                     row < have, m, l);
+                                     row < have, m, n, l);
                 else
                     softmax_unit<D>(ts, to, nv, c, i == 0, row < have, m, l);
             }
@@ -914,16 +922,16 @@ __device__ void softmax_role(const TileParams &P, QuantShared &sh, uint8_t *tile
         float *const o_all = pre ? P.W.o_p : P.W.o_s;
         if (Q8 && it.join) {
             const size_t at = (size_t)it.slot * 2 * rows;
-            sh.ml[g][w * 32 + lane] = make_float2(m, l);
+            sh.nl[g][w * 32 + lane] = make_float2(n, l);
             softmax_sync();
             float top = -F_INF, sum = 0.0f;
 #pragma unroll 1
             for (int p = 0; p < 2 * copies; ++p)
-                top = fmaxf(top, sh.ml[p & 1][(p >> 1) * (AT_ROWS / copies) + row].x);
+                top = fmaxf(top, sh.nl[p & 1][(p >> 1) * (AT_ROWS / copies) + row].x);
             const float ref = top == -F_INF ? 0.0f : top;
 #pragma unroll 1
             for (int p = 0; p < 2 * copies; ++p) {
-                const float2 y = sh.ml[p & 1][(p >> 1) * (AT_ROWS / copies) + row];
+                const float2 y = sh.nl[p & 1][(p >> 1) * (AT_ROWS / copies) + row];
                 sum += y.y == 0.0f ? 0.0f : y.y * ex2a(y.x - ref);
             }
             if (g == 0 && copy == 0 && row < have) {
@@ -931,18 +939,24 @@ __device__ void softmax_role(const TileParams &P, QuantShared &sh, uint8_t *tile
                 ml[at + rows + row] = make_float2(-F_INF, 0.0f);
             }
             join_parts<D>(tiles + qs * C::TILE, to, copy * 2 + g, 2 * copies, row, have, ok && cnt > 0 && active,
-                          l != 0.0f, ex2a(m - ref), o_all + at * D, rows);
+                          l != 0.0f, ex2a(0.5f * (m - ref)), o_all + at * D, rows);
             if (ok && threadIdx.x == 0)
                 mbar_arrive(&sh.q_empty[qs]);
         } else {
             const size_t at = ((size_t)it.slot * 2 + g) * rows;
             if (row < have)
-                ml[at + row] = make_float2(m, l);
+                ml[at + row] = make_float2(Q8 ? n : m, l);
+            const float half = Q8 ? ex2a(0.5f * (m - n)) : 1.0f;   // 2^(m - n) itself may be out of range
             if (ok && cnt > 0 && active) {
 #pragma unroll 1
                 for (int k = 0; k < D; k += 32) {
                     float o[32];
                     tmem_ld(to + k, o);
+                    if (Q8) {
+#pragma unroll
+                        for (int u = 0; u < 32; ++u)
+                            o[u] = o[u] * half * half;
+                    }
                     if (row < have) {
 #pragma unroll
                         for (int u = 0; u < 32; u += 8)
@@ -979,7 +993,7 @@ __device__ __forceinline__ void scale_role(const TileParams &P, QuantShared &sh,
                     if (asked * AT_UNIT + i * 32 + lane < it.left)
                         asm volatile("prefetch.global.L2 [%0];" ::"l"(sc + (size_t)(asked * AT_UNIT + i * 32 + lane) * stride));
             const int nv = it.left - j * AT_UNIT;
-            uint32_t kb[4], vb[4], top = 27;
+            uint32_t kb[4], vb[4], top = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 kb[i] = vb[i] = 0;
@@ -989,7 +1003,7 @@ __device__ __forceinline__ void scale_role(const TileParams &P, QuantShared &sh,
                     vb[i] = __ldg(p + P.A.H);
                 }
             }
-            // V's are relative to the largest, no lower than 2^-100: l holds the weights times its reciprocal
+            // V's are relative to the largest
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 top = max(top, vb[i] == 255 ? 0u : vb[i]);

@@ -1,5 +1,8 @@
 """Attention of the verification pass (CUDA, through the C ABI): what NaN, scores
 and scales far from the ordinary do, against the float64 oracle.
+
+Tolerances are those of test_gpu_attention.py: they count roundings of weights and
+outputs (2^-8 each, relative to the weighted mean of |v|) and of scores and sums.
 """
 from __future__ import annotations
 
@@ -7,7 +10,7 @@ import pytest
 import torch
 
 import speculative_decoding_verification_sampling_gb300 as sv
-from test_gpu_attention import _case, _device   # noqa: F401
+from test_gpu_attention import DEV, _case, _device, _hold, _reference, _run   # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +69,82 @@ def test_a_nan_value_stays_beside_larger_weights(B, P, L, n, quant):
     hit.copy_(out[3, :, 2:] if quant else out[3, :, 2:, 7])
     assert torch.equal(got, out) and torch.equal(got_lse, lse)
 
+
+# ------------------------------------------------------------------ 8-bit entries: scales and scores
+def _scored(B, T, Hq, H, D, lens, score, seed, prefix=None):
+    """8-bit entries whose scores are given: q has element 0 alone, and so have the keys.  score [L]
+    (and prefix [P]): multiples of 1 / 8 that e4m3 holds; values are random, with scale bytes 117 .. 121."""
+    L = len(score)
+    P = 0 if prefix is None else len(prefix)
+    a = _case(B, T, Hq, H, D, P, L, lens, True, "none", seed=seed)
+    a["sm_scale"] = 0.125
+    a["q"].zero_()
+    a["q"][..., 0] = 1.0
+    for name, s in (("cache", score), ("prefix", prefix)):
+        if s is None:
+            continue
+        k = (8 * s).to(torch.float8_e4m3fn)
+        assert torch.equal(k.double(), 8 * s), "scores that e4m3 holds"
+        x, sc = a[name], a[name + "_scale"]
+        x[..., 0, :, :] = 0.0
+        x[..., 0, :, 0] = k[:, None]
+        if name == "cache":
+            for b, n in enumerate(lens):
+                sc[b, :n, 0] = 127
+                x[b, n:] = 448.0
+        else:
+            sc[:, 0] = 127
+    return a
+
+
+def _hold_scored(a, what):
+    scale = a["sm_scale"]
+    out, lse = _call(a)
+    _hold(out, lse, _reference({k: v for k, v in a.items() if k != "sm_scale"}, scale), a["q"].shape[-1], what)
+
+
+@pytest.mark.parametrize("kind", ["causal", "none"])
+@pytest.mark.parametrize("first", [200, 60])
+@pytest.mark.parametrize("B,T,P,L", [(2, 3, 0, 256), (3, 5, 256, 512), (40, 3, 256, 4096), (2, 61, 512, 300)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_units_whose_value_scales_lie_far_apart(B, T, P, L, D, first, kind):
+    """Values of 2^73 beside values of 2^-67, 128 entries each in turn: every entry has its weight,
+    in the output and in lse."""
+    lens = [L - 7 * b for b in range(B)]
+    a = _case(B, T, 4, 2, D, P, L, lens, True, kind, seed=41)
+    for name, dim in (("cache", 1), ("prefix", 0)):
+        if name in a:
+            n = a[name].shape[dim]
+            byte = torch.where(torch.arange(n, device=DEV) // 128 % 2 == 0, first, 260 - first).to(torch.uint8)
+            a[name + "_scale"][..., 1, :] = byte[:, None]
+    for b, n in enumerate(lens):
+        a["cache_scale"][b, n:] = 255
+    _run(a, f"{first} first")
+
+
+@pytest.mark.parametrize("low,high", [(60, 200), (60, 180), (100, 122), (2, 120)])
+def test_the_weight_lies_on_the_small_values(low, high):
+    """The entries with small values have the larger scores: what is left of the others is in range."""
+    for order in (0, 1):
+        score = torch.zeros(512, dtype=torch.float64, device=DEV)
+        unit = torch.arange(512, device=DEV) // 128 % 2 == order
+        score[unit] = -(min(high - low, 70) * 0.75 // 8 * 8)     # in nats: further than the values are apart, or 48
+        a = _scored(2, 5, 8, 2, 128, [512, 300], score, 42)
+        byte = torch.where(unit, high, low).to(torch.uint8)
+        a["cache_scale"][0, :, 1] = byte[:, None]
+        a["cache_scale"][1, :300, 1] = byte[:300, None]
+        _hold_scored(a, f"{low} {high} {order}")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_weight_lies_on_a_small_head_of_a_unit(D):
+    """One entry of a unit has nearly all of the weight and values 2^20 below its neighbours'."""
+    score = torch.full((300,), -36.0, dtype=torch.float64, device=DEV)
+    score[[5, 140, 290]] = 0.0
+    a = _scored(3, 5, 8, 2, D, [300, 291, 128], score, 43)
+    a["cache_scale"][:, :, 1] = torch.where(a["cache_scale"][:, :, 1] == 255, 255, 125)
+    for i in (5, 140, 290):
+        for b in range(3):
+            if i < [300, 291, 128][b]:
+                a["cache_scale"][b, i, 1] = 105
+    _hold_scored(a, "small heads")
