@@ -19,27 +19,27 @@
 // partial result each.  A loader thread feeds a ring of K and V tiles with
 // TMA; one warp issues every tcgen05.mma.
 //
-// Entries in 8 bits.  What such a kernel has least of is shared-memory
+// Entries in 8 bits. What such a kernel has least of is shared-memory
 // bandwidth: turning a tile of codes into 16-bit numbers reads and writes three
-// times its bytes there.  So K's codes go to the tensor cores as they are
+// times its bytes there. So K's codes go to the tensor cores as they are
 // (kind::f8f6f4), and Q meets them as a sum of two e4m3 numbers: each row times
 // a power of two that puts its largest element in (224, 448], then rounded, and
-// the remainder rounded again.  That is exact for elements down to 2^-10 of
-// the row's largest, and off by 2^-18 of the largest at most.  The scales of
-// K's rows multiply the columns of S.  V's codes become float16, by four warps,
-// in the layout that TMA would have written, with scales relative to the
-// unit's largest, which becomes 2^7: float16 holds a code times 2^s exactly
-// for s in [-15, 7], and a head whose scale is more than 2^22 below loses its
-// last bits (at 2^-40 of the unit's largest element).  What the largest stands
-// for, bv, goes back in exactly, into the exponent of the weights: O holds
-// 2^(c S + bv - m) V with a reference m of its own, while l holds 2^(c S - n)
-// with the row's maximum n, so a unit counts in l whatever its values' scale is.
-// A unit that is nothing beside m (2^-64 or less) is summed up relative to its
-// own maximum; its P are 0 in float16 either way.  The results leave with n
-// alone: O times 2^(m - n).  P is rounded to float16 here, 2^-11 of a weight.  With few rows, where HBM is the bound, one warp's
-// pass over 128 scores per row and their scales is too long a chain: the rows
-// then lie in their tile two or four times, and each warp of a group takes the
-// columns that fall to its copy.
+// the remainder rounded again. That is exact for elements down to 2^-10 of the
+// row's largest, and off by 2^-18 of the largest at most. The scales of K's
+// rows multiply the columns of S. V's codes become float16, by four warps, in
+// the layout that TMA would have written, with scales relative to the unit's
+// largest, which becomes 2^7: float16 holds a code times 2^s exactly for s in
+// [-15, 7], and a head whose scale is more than 2^22 below loses its last bits
+// (at 2^-40 of the unit's largest element). What the largest stands for, bv,
+// goes back in exactly, into the exponent of the weights: O holds 2^(c S + bv -
+// m) V with a reference m of its own, while l holds 2^(c S - n), n following
+// the scores alone, so a unit counts in l whatever its values' scale is. A unit
+// that is nothing beside m (2^-64 or less) is summed up relative to its own
+// maximum; its P are 0 in float16 either way. The results leave with n alone: O
+// times 2^(m - n). P is rounded to float16 here, 2^-11 of a weight. With few
+// rows, where HBM is the bound, one warp's pass over 128 scores per row and
+// their scales is too long a chain: the rows then lie in their tile two or four
+// times, and each warp of a group takes the columns that fall to its copy.
 //
 // Measured, 32 query and 8 key/value heads of 128: 64 sequences of 32 tokens over
 // 8192 shared entries, 191 us, 1440 TFLOP/s (bound by the two groups' softmax, the
@@ -733,11 +733,14 @@ __device__ __forceinline__ void softmax_unit(uint32_t ts, uint32_t to, int nv, f
     tmem_st_wait();
 }
 
+constexpr float FAR_BELOW = -3e38f;   // a score's reference where there is none yet; finite
+
 // The same with 8-bit entries, over this copy's `nc` columns from `col` on (nv
 // of them in the stretch): scores times the scales of their rows of K, V's unit
-// in the exponent, P in float16; n and l are the row's maximum and its sum.  In steps of 32 columns, twice over S: the
-// loops are short on purpose, the warps of this kernel run six different
-// programs and have to share the instruction cache.
+// in the exponent, P in float16; n and l are the row's maximum and its sum. In
+// steps of 32 columns, twice over S: the loops are short on purpose, the warps
+// of this kernel run six different programs and have to share the instruction
+// cache.
 template <int D>
 __device__ __forceinline__ void softmax_unit8(uint32_t ts, uint32_t to, int col, int nc, int nv, float c, float bv,
                                               const float4 *k_fac, bool first, bool real, float &m, float &n,
@@ -771,8 +774,11 @@ __device__ __forceinline__ void softmax_unit8(uint32_t ts, uint32_t to, int col,
     const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
     float none = 0.0f;
     follow_maximum<D>(to, most + bv, first, real, m, none);
-    const float up = fmaxf(n, most), base = up == -F_INF ? 0.0f : up;
-    const float ref = most == -F_INF ? base : fminf(m - bv, most + 64.0f);
+    if (most > n + 8.0f) {
+        l *= ex2a(n - most);
+        n = most;
+    }
+    const float ref = fmaxf(fminf(m - bv, most + 64.0f), FAR_BELOW);   // finite, also where every score is -inf
     const f2 cc = pk(c, c), nref = pk(-ref, -ref);
     f2 sum[2] = {pk(0.0f, 0.0f), pk(0.0f, 0.0f)};
     uint32_t p[16];
@@ -799,8 +805,7 @@ __device__ __forceinline__ void softmax_unit8(uint32_t ts, uint32_t to, int col,
         tmem_st(ts + ((col + k0) & (AT_UNIT - 1)) / 2, p);
     float lo, hi;
     upk(add2(sum[0], sum[1]), lo, hi);
-    l = fmaf(lo + hi, ex2a(ref - base), l * ex2a(n - base));
-    n = up;
+    l = fmaf(lo + hi, ex2a(ref - n), l);
     tmem_st_wait();
 }
 
@@ -880,7 +885,7 @@ __device__ void softmax_role(const TileParams &P, QuantShared &sh, uint8_t *tile
         const int have = min(max(it.tokens - (it.two ? g * tq : 0), 0), tq) * P.A.G;
         const bool active = row - lane < have;
         const int cnt = it.two ? it.n : (it.n - g + 1) / 2;
-        float m = -F_INF, n = -F_INF, l = 0.0f;   // n: with 8-bit entries, l's reference
+        float m = -F_INF, n = FAR_BELOW, l = 0.0f;   // n: with 8-bit entries, l's reference
 #pragma unroll 1
         for (int i = 0; ok && i < cnt; ++i) {
             const int j = it.two ? i : 2 * i + g, nv = it.left - j * AT_UNIT - col;
@@ -924,38 +929,38 @@ __device__ void softmax_role(const TileParams &P, QuantShared &sh, uint8_t *tile
             const size_t at = (size_t)it.slot * 2 * rows;
             sh.nl[g][w * 32 + lane] = make_float2(n, l);
             softmax_sync();
-            float top = -F_INF, sum = 0.0f;
+            float top = FAR_BELOW, sum = 0.0f;
 #pragma unroll 1
             for (int p = 0; p < 2 * copies; ++p)
                 top = fmaxf(top, sh.nl[p & 1][(p >> 1) * (AT_ROWS / copies) + row].x);
-            const float ref = top == -F_INF ? 0.0f : top;
 #pragma unroll 1
             for (int p = 0; p < 2 * copies; ++p) {
                 const float2 y = sh.nl[p & 1][(p >> 1) * (AT_ROWS / copies) + row];
-                sum += y.y == 0.0f ? 0.0f : y.y * ex2a(y.x - ref);
+                sum = fmaf(y.y, ex2a(y.x - top), sum);
             }
             if (g == 0 && copy == 0 && row < have) {
                 ml[at + row] = make_float2(top, sum);
                 ml[at + rows + row] = make_float2(-F_INF, 0.0f);
             }
             join_parts<D>(tiles + qs * C::TILE, to, copy * 2 + g, 2 * copies, row, have, ok && cnt > 0 && active,
-                          l != 0.0f, ex2a(0.5f * (m - ref)), o_all + at * D, rows);
+                          l != 0.0f, ex2a(0.5f * (m - top)), o_all + at * D, rows);
             if (ok && threadIdx.x == 0)
                 mbar_arrive(&sh.q_empty[qs]);
         } else {
             const size_t at = ((size_t)it.slot * 2 + g) * rows;
+            // in range: m - n lies in [-115, 128), as bv does in [-107, 120]
+            const float to_n = Q8 ? ex2a(m - n) : 1.0f;
             if (row < have)
                 ml[at + row] = make_float2(Q8 ? n : m, l);
-            const float half = Q8 ? ex2a(0.5f * (m - n)) : 1.0f;   // 2^(m - n) itself may be out of range
             if (ok && cnt > 0 && active) {
 #pragma unroll 1
                 for (int k = 0; k < D; k += 32) {
                     float o[32];
                     tmem_ld(to + k, o);
-                    if (Q8) {
+                    if constexpr (Q8) {
 #pragma unroll
-                        for (int u = 0; u < 32; ++u)
-                            o[u] = o[u] * half * half;
+                        for (int u = 0; u < 32; u += 2)
+                            upk(mul2(pk(o[u], o[u + 1]), pk(to_n, to_n)), o[u], o[u + 1]);
                     }
                     if (row < have) {
 #pragma unroll
@@ -993,7 +998,7 @@ __device__ __forceinline__ void scale_role(const TileParams &P, QuantShared &sh,
                     if (asked * AT_UNIT + i * 32 + lane < it.left)
                         asm volatile("prefetch.global.L2 [%0];" ::"l"(sc + (size_t)(asked * AT_UNIT + i * 32 + lane) * stride));
             const int nv = it.left - j * AT_UNIT;
-            uint32_t kb[4], vb[4], top = 0;
+            uint32_t kb[4], vb[4], top = 27;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 kb[i] = vb[i] = 0;
@@ -1003,7 +1008,7 @@ __device__ __forceinline__ void scale_role(const TileParams &P, QuantShared &sh,
                     vb[i] = __ldg(p + P.A.H);
                 }
             }
-            // V's are relative to the largest
+            // V's are relative to the largest, no lower than 2^-100
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 top = max(top, vb[i] == 255 ? 0u : vb[i]);
