@@ -36,8 +36,13 @@
 // the scores alone, so a unit counts in l whatever its values' scale is. A unit
 // that is nothing beside m (2^-64 or less) is summed up relative to its own
 // maximum; its P are 0 in float16 either way. The results leave with n alone: O
-// times 2^(m - n). P is rounded to float16 here, 2^-11 of a weight. With few
-// rows, where HBM is the bound, one warp's pass over 128 scores per row and
+// times 2^(m - n). P is rounded to float16 here: by 2^-11 of a weight, but
+// subnormal ones by 2^-25. So that these are far down, m stays 11 to 15 below
+// the row's maximum (of c S + bv), and P may reach 2^15: 2^-11 holds for
+// weights down to 2^-25 of the largest, and below that 2^-36 of it. A head of
+// zeros, whose byte is 127, counts for nothing in its unit: an entry with most
+// of a row's weight and zeros for values would push all the others down. With
+// few rows, where HBM is the bound, one warp's pass over 128 scores per row and
 // their scales is too long a chain: the rows then lie in their tile two or four
 // times, and each warp of a group takes the columns that fall to its copy.
 //
@@ -662,12 +667,13 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint8_t *tiles, ui
     }
 }
 
-// Raises a row's reference exponent m to its scores' maximum s where that has
-// passed it by more than 8, and scales O and l down with it.
+// Raises a row's reference exponent m to s where that has passed it by more than
+// `slack`, and scales O and l down with it.
 template <int D>
-__device__ __forceinline__ void follow_maximum(uint32_t to, float s, bool first, bool real, float &m, float &l)
+__device__ __forceinline__ void follow_maximum(uint32_t to, float s, float slack, bool first, bool real, float &m,
+                                               float &l)
 {
-    const bool up = real && s > m + 8.0f;
+    const bool up = real && s > m + slack;
     if (!__any_sync(0xffffffffu, up))
         return;
     const float f = up ? ex2a(m - s) : 1.0f;   // 2^(-inf) = 0 the first time
@@ -709,7 +715,7 @@ __device__ __forceinline__ void softmax_unit(uint32_t ts, uint32_t to, int nv, f
 #pragma unroll
         for (int u = 0; u < 4; ++u)
             top[u] = fmaxf(top[u], x[k + u]);
-    follow_maximum<D>(to, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c, first, real, m, l);
+    follow_maximum<D>(to, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c, 8.0f, first, real, m, l);
     const float ref = m == -F_INF ? 0.0f : m;
     const f2 cc = pk(c, c), nref = pk(-ref, -ref);
     f2 sum[2] = {pk(0.0f, 0.0f), pk(0.0f, 0.0f)};
@@ -734,6 +740,7 @@ __device__ __forceinline__ void softmax_unit(uint32_t ts, uint32_t to, int nv, f
 }
 
 constexpr float FAR_BELOW = -3e38f;   // a score's reference where there is none yet; finite
+constexpr float P_TOP = 11.0f, P_SLACK = 4.0f;   // float16: the largest P of a row lies in [2^11, 2^15] as m moves
 
 // The same with 8-bit entries, over this copy's `nc` columns from `col` on (nv
 // of them in the stretch): scores times the scales of their rows of K, V's unit
@@ -773,7 +780,7 @@ __device__ __forceinline__ void softmax_unit8(uint32_t ts, uint32_t to, int col,
     }
     const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
     float none = 0.0f;
-    follow_maximum<D>(to, most + bv, first, real, m, none);
+    follow_maximum<D>(to, most + bv - P_TOP, P_SLACK, first, real, m, none);
     if (most > n + 8.0f) {
         l *= ex2a(n - most);
         n = most;
@@ -948,7 +955,7 @@ __device__ void softmax_role(const TileParams &P, QuantShared &sh, uint8_t *tile
                 mbar_arrive(&sh.q_empty[qs]);
         } else {
             const size_t at = ((size_t)it.slot * 2 + g) * rows;
-            // in range: m - n lies in [-115, 128), as bv does in [-107, 120]
+            // in range: m - n lies in [-122, 117], as bv does in [-107, 120]
             const float to_n = Q8 ? ex2a(m - n) : 1.0f;
             if (row < have)
                 ml[at + row] = make_float2(Q8 ? n : m, l);
@@ -976,8 +983,32 @@ __device__ void softmax_role(const TileParams &P, QuantShared &sh, uint8_t *tile
     }
 }
 
+// Scale bytes of four heads, 32 entries apart: those that are 127 and whose codes
+// are all zeros (of either sign) become 0.  Rarely called, and kept out of line for
+// that: inlined, it took the calls around it from 381 us to 426 us (128 sequences
+// of 9 tokens to 8192 own entries), by its place in the instruction cache alone.
+template <int D>
+__device__ __noinline__ uint32_t without_zeros(uint32_t bytes, const uint8_t *codes, size_t step)
+{
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        const uint8_t *p = codes + i * step;
+        bool none = (bytes >> (8 * i) & 255) == 127;
+#pragma unroll 1
+        for (int k = 0; none && k < D; k += 16) {
+            const uint4 c = __ldg(reinterpret_cast<const uint4 *>(p + k));
+            none = ((c.x | c.y | c.z | c.w) & 0x7f7f7f7fu) == 0;
+        }
+        if (none)
+            bytes &= ~(255u << (8 * i));
+    }
+    __syncwarp();
+    return bytes;
+}
+
 // 8-bit entries: one warp turns the units' scale bytes into factors, up to FAC
 // units ahead; the bytes of later units are asked into the caches meanwhile.
+template <int D>
 __device__ __forceinline__ void scale_role(const TileParams &P, QuantShared &sh, uint32_t limit)
 {
     const int lane = threadIdx.x & 31;
@@ -987,7 +1018,11 @@ __device__ __forceinline__ void scale_role(const TileParams &P, QuantShared &sh,
     Ring r;
 #pragma unroll 1
     while (walk.next(it)) {
-        const uint8_t *sc = (it.b < 0 ? P.A.pscale : P.A.cscale + (size_t)it.b * P.A.L * stride) + (size_t)it.e0 * stride + it.h;
+        const size_t e0 = (it.b < 0 ? 0 : (size_t)it.b * P.A.L) + it.e0;
+        const uint8_t *sc = (it.b < 0 ? P.A.pscale : P.A.cscale) + e0 * stride + it.h;
+        // the values' codes of its first entry
+        const uint8_t *codes = static_cast<const uint8_t *>(it.b < 0 ? P.A.prefix : P.A.cache) +
+                               (e0 * stride + P.A.H + it.h) * D;
         int asked = 0;
 #pragma unroll 1
         for (int j = 0; j < it.n; ++j) {
@@ -998,7 +1033,7 @@ __device__ __forceinline__ void scale_role(const TileParams &P, QuantShared &sh,
                     if (asked * AT_UNIT + i * 32 + lane < it.left)
                         asm volatile("prefetch.global.L2 [%0];" ::"l"(sc + (size_t)(asked * AT_UNIT + i * 32 + lane) * stride));
             const int nv = it.left - j * AT_UNIT;
-            uint32_t kb[4], vb[4], top = 27;
+            uint32_t kb[4], vb[4], top;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 kb[i] = vb[i] = 0;
@@ -1009,10 +1044,23 @@ __device__ __forceinline__ void scale_role(const TileParams &P, QuantShared &sh,
                 }
             }
             // V's are relative to the largest, no lower than 2^-100
+            auto largest = [&] {
+                top = 27;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                top = max(top, vb[i] == 255 ? 0u : vb[i]);
-            top = __reduce_max_sync(0xffffffffu, top);
+                for (int i = 0; i < 4; ++i)
+                    top = max(top, vb[i] == 255 ? 0u : vb[i]);
+                top = __reduce_max_sync(0xffffffffu, top);
+            };
+            largest();
+            if (top == 127) {   // heads of zeros do not count
+                const uint32_t left = without_zeros<D>(vb[0] | vb[1] << 8 | vb[2] << 16 | vb[3] << 24,
+                                                       codes + (size_t)(j * AT_UNIT + lane) * stride * D,
+                                                       (size_t)32 * stride * D);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    vb[i] = left >> (8 * i) & 255;
+                largest();
+            }
             if (!tile_wait_warp(&sh.f_empty[r.slot], r.phase ^ 1, limit, sh))
                 return;
             float *kf = reinterpret_cast<float *>(sh.k_fac[r.slot]);
@@ -1320,7 +1368,7 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
             if (!Q8 || elect_one())
                 mma_role<D, Q8>(P, sh, tiles, smem, limit);
         } else if (Q8 && warp == W_SCALE) {
-            scale_role(P, sh, limit);
+            scale_role<D>(P, sh, limit);
         } else if (Q8 && warp >= W_CVT) {
             convert_role<D>(P, sh, tiles, limit);
         }

@@ -148,3 +148,34 @@ def test_the_weight_lies_on_a_small_head_of_a_unit(D):
             if i < [300, 291, 128][b]:
                 a["cache_scale"][b, i, 1] = 105
     _hold_scored(a, "small heads")
+
+
+@pytest.mark.parametrize("gap", [11.0, 12.0, 13.0, 14.0])
+@pytest.mark.parametrize("sink", ["zero", "small", "large"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_dominant_entry_and_a_flat_tail(D, sink, gap):
+    """One entry 2^16 to 2^20 above thousands of equal ones, whose values all agree: zeros (whose scale
+    byte is 127), or values of the neighbours' scale, or small ones."""
+    B, L = 40, 8193
+    score = torch.full((L,), -gap, dtype=torch.float64, device=DEV)
+    score[0] = 0.0
+    a = _scored(B, 5, 8, 2, D, [L - 130 * b for b in range(B)], score, 44)
+    a["cache"][:, :, 1] = 128.0
+    for b in range(B):
+        a["cache_scale"][b, :L - 130 * b, 1] = 120       # 1
+    a["cache"][:, 0, 1] = 0.0 if sink == "zero" else 0.125 if sink == "small" else 128.0
+    a["cache_scale"][:, 0, 1] = 127 if sink == "zero" else 120
+    a["cache"][:, 1::2, 1] = torch.where(torch.rand((B, L // 2, 1, D), device=DEV,
+                                                    generator=torch.Generator(device=DEV).manual_seed(3)) < 0.1,
+                                         -128.0, 128.0).to(torch.float8_e4m3fn)
+    if sink == "zero":
+        a["cache"][:, 0, 1, :, ::3] = -0.0
+    _hold_scored(a, f"{sink} {gap}")
+
+
+@pytest.mark.parametrize("T", [5, 61])
+@pytest.mark.parametrize("sm_scale", [1e-3, 0.5, 4.0])
+def test_peaked_rows_8_bits(T, sm_scale):
+    a = _case(3, T, 8, 2, 128, 600, 2500, [2500, 0, 257], True, "causal", seed=4)
+    a["q"][0] *= 4
+    _run(a, f"scale {sm_scale}", sm_scale)
