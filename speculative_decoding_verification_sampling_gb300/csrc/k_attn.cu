@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(WIDE ? WIDE * 32 : 128, WIDE ? 1 : 7)
             }
             if (len > 0) {
                 const int wide = W.own.tq * (1 + W.own.two), tile = t / wide, in = t - tile * wide;
-                const int ub = (len + AT_UNIT - 1) / AT_UNIT, i = h * W.own.tiles + tile;
+                const int ub = attn_units(len), i = h * W.own.tiles + tile;
                 const int at = line1.own + HS * line1.sequences(before.x, before.y) + i * line1.own_cost.pair(ub);
                 pair1 = b * HS + i;
                 grp1 = in >= W.own.tq;

@@ -286,7 +286,7 @@ struct TileParams {
 __device__ __forceinline__ int seq_units(const AttnParams &A, int b)
 {
     const int n = __ldg(A.len + b);
-    return n < 0 || n > A.L ? 0 : (n + AT_UNIT - 1) / AT_UNIT;
+    return n < 0 || n > A.L ? 0 : attn_units(n);
 }
 
 // Units from which a stretch of 8-bit entries with one set of rows uses copies of

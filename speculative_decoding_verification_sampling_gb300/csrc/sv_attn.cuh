@@ -65,6 +65,10 @@ inline AttnTiling attn_tiling(long long tokens, int G, bool quant)
     return t;
 }
 
+// Units of n >= 0 entries; n may lie just below 2^31.
+__host__ __device__ constexpr int attn_units(int n) { return ((n - 1) >> 7) + 1; }
+static_assert(AT_UNIT == 128 && attn_units(0) == 0 && attn_units(128) == 1 && attn_units(0x7fffffff) == 1 << 24, "units");
+
 constexpr long long READ_BACK_ROWS = 1024;   // rows per key/value head from which an 8-bit prefix is read back
 
 struct AttnPlan {
@@ -83,10 +87,10 @@ inline AttnPlan attn_plan(int B, int T, int H, int G, int D, int P, int L, bool 
     a.split = quant && P > 0 && (long long)B * T * G >= READ_BACK_ROWS;
     a.pre = attn_tiling((long long)B * T, G, quant);
     a.own = attn_tiling(T, G, quant);
-    a.pu = (P + AT_UNIT - 1) / AT_UNIT;
+    a.pu = attn_units(P);
     a.ppairs = P > 0 ? H * a.pre.tiles : 0;
     const long long spairs = L > 0 ? (long long)B * H * a.own.tiles : 0;
-    a.max_units = (long long)a.ppairs * a.pu + spairs * ((L + AT_UNIT - 1) / AT_UNIT);
+    a.max_units = (long long)a.ppairs * a.pu + spairs * attn_units(L);
     a.max_line = 4 * a.max_units + 12 * (a.ppairs + spairs);
     size_t at = 0;
     auto take = [&](size_t bytes) {
