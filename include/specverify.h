@@ -313,7 +313,8 @@ spec_status_t spec_kv_read_quant(const void *cache, const uint8_t *scale, const 
  *                 zero-fill needed), 16-byte aligned; one per call in flight
  *   device_status [1] set to 0, or the code of one failing sequence; may be NULL
  * seq_len[b] outside [0, L] is an error (SPEC_ERR_INVALID_ARG): that
- * sequence's outputs are NaN.  Scores, softmax statistics and sums are float32.
+ * sequence's outputs are NaN.  So are the rows that a CTA leaves unfinished when a
+ * bounded wait of its own runs out (SPEC_ERR_TIMEOUT).  Scores, softmax statistics and sums are float32.
  * What is rounded to fewer bits on the way: the weights where they meet prefix
  * and cache values (to bfloat16, by 2^-8 of a weight at most; with 8-bit entries
  * to float16), and with 8-bit entries q (elements below 2^-10 of their row's

@@ -257,6 +257,7 @@ struct TileShared {
     unsigned long long q_ready[2], f_full[FAC], f_empty[FAC];   // 8-bit entries: Q in e4m3, a unit's scales
     uint32_t tmem;
     volatile int abort;
+    int issued[3];   // copies, as the loader ends: Q, K, V (or its codes)
     Place start;
     unsigned long long sums[16];   // per warp
 };
@@ -494,15 +495,9 @@ __device__ void load_role(const TileParams &P, const CUtensorMap *mq_pre, const 
         have_q = early;
         it = after;
     }
-    if (!ok) {
-        // copies in flight land before the CTA ends
-        for (int i = 1; i <= 2 && i <= nq; ++i)
-            (void)ring_wait(&sh.q_full[(nq - i) % 2], ((nq - i) / 2) & 1, limit);
-        for (int i = 1; i <= C::NK && i <= nk; ++i)
-            (void)ring_wait(&sh.k_full[(nk - i) % C::NK], ((nk - i) / C::NK) & 1, limit);
-        for (int i = 1; i <= NV && i <= nv; ++i)
-            (void)ring_wait(&vfull[(nv - i) % NV], ((nv - i) / NV) & 1, limit);
-    }
+    sh.issued[0] = nq;
+    sh.issued[1] = nk;
+    sh.issued[2] = nv;
 }
 
 // The issuer of every tcgen05.mma: one warp, one elected lane issues.
@@ -661,10 +656,31 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint8_t *tiles, ui
             for (int g = 0; ok && g <= it.two; ++g)
                 give(&sh.q_empty[it.two ? (q0 + g) & 1 : q0]);
     }
-    if (!ok) {
-        give(&sh.drain);
+}
+
+// Where a role of the CTA has given up, and all of them have ended: waits for the
+// copies and the products in flight, which the others may have issued without a
+// wait of their own running out.  `warp`: this thread's.
+template <int D, bool Q8>
+__device__ void wind_down(TileShared &sh, int warp, uint32_t limit)
+{
+    using C = TileCfg<D, Q8>;
+    constexpr int NV = Q8 ? C::NR : C::NV;
+    if (warp == W_LOAD && elect_one()) {
+        const int nq = sh.issued[0], nk = sh.issued[1], nv = sh.issued[2];
+        unsigned long long *const vfull = Q8 ? sh.r_full : sh.v_full;
+        for (int i = 1; i <= 2 && i <= nq; ++i)
+            (void)ring_wait(&sh.q_full[(nq - i) % 2], ((nq - i) / 2) & 1, limit);
+        for (int i = 1; i <= C::NK && i <= nk; ++i)
+            (void)ring_wait(&sh.k_full[(nk - i) % C::NK], ((nk - i) / C::NK) & 1, limit);
+        for (int i = 1; i <= NV && i <= nv; ++i)
+            (void)ring_wait(&vfull[(nv - i) % NV], ((nv - i) / NV) & 1, limit);
+    }
+    if (warp == W_MMA && elect_one()) {   // the thread that issued them
+        mma_commit(&sh.drain);
         (void)ring_wait(&sh.drain, 0, limit);
     }
+    __syncthreads();
 }
 
 // Raises a row's reference exponent m to s where that has passed it by more than
@@ -877,6 +893,14 @@ __device__ void softmax_role(const TileParams &P, QuantShared &sh, uint8_t *tile
     Ring q;
     Walk walk(P, sh.start);
     Item it;
+    if (P.spin_limit < CL_PLAIN_POLLS && sh.start.from < sh.start.to) {
+        // the first wait, in that many plain polls: a test's way to giving up
+        ok = mbar_poll(&sh.s_full[g], 0);
+        for (uint32_t k = 1; !ok && k < P.spin_limit; ++k)
+            ok = mbar_poll(&sh.s_full[g], 0);
+        if (!(ok = __all_sync(0xffffffffu, ok)))
+            sh.abort = 1;
+    }
 #pragma unroll 1
     for (; walk.next(it); unit += it.n) {
         // the slot of this group's Q tile: the second of two, or the only one
@@ -1266,7 +1290,9 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
     pdl_trigger();
     const int tid = threadIdx.x, warp = tid / 32;
     const uint32_t smem = saddr(tiles);
-    const uint32_t limit = P.spin_limit > OWN_WAIT_MIN ? P.spin_limit : OWN_WAIT_MIN;   // polls, of about 0.1 us
+    // Polls, of about 0.1 us.  A spin limit below CL_PLAIN_POLLS reaches the softmax's first wait for
+    // scores alone.
+    const uint32_t limit = P.spin_limit > OWN_WAIT_MIN ? P.spin_limit : OWN_WAIT_MIN;
 
     // ---- where this CTA's length begins: sums over runs of sequences, then the run.  Units in the
     // low word, sequences that have any in the high one.
@@ -1376,6 +1402,8 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
     __syncwarp();
     tc_before();
     __syncthreads();
+    if (sh.abort)
+        wind_down<D, Q8>(sh, warp, limit);
     tc_after();
     if (warp == W_MMA)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sh.tmem) : "memory");

@@ -175,3 +175,34 @@ def test_a_captured_verification_has_its_own_workspace(kernel, monkeypatch):
             assert all(torch.equal(g, w) for g, w in zip(held, want[0]))
             if a is None:
                 assert torch.equal(kept, before)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("B,T,Hq,H,D,P,L,lens", [
+    (5, 5, 8, 2, 128, 0, 6000, [6000, 0, 31, 4100, 2048]),              # one set of rows, results joined
+    (4, 5, 8, 2, 64, 700, 300, [300, 0, 128, 7]),
+    (3, 61, 16, 2, 128, 300, 900, [900, 0, 129]),                      # two sets of rows
+    (64, 8, 8, 2, 128, 400, 60, [(7 * i) % 61 for i in range(64)]),    # an 8-bit prefix read back: two lines
+])
+def test_waits_run_out_then_recover(B, T, Hq, H, D, P, L, lens, quant, monkeypatch):
+    """A spin limit of 1: the softmax's first wait for scores runs out.  The CTA winds down (its copies
+    and products land, its TMEM is freed), its rows are NaN, the status is SPEC_ERR_TIMEOUT; rows that
+    see no prefix and no cache are right.  The next call is right again."""
+    a = _case(B, T, Hq, H, D, P, L, lens, quant, "causal", seed=71)
+    want, want_lse = _call(a)
+    for _ in range(3):
+        monkeypatch.setenv("SPECVERIFY_SPIN_LIMIT", "1")
+        st = torch.full((1,), -5, dtype=torch.int32, device=DEV)
+        out, lse = _call(a, device_status=st)
+        torch.cuda.synchronize()
+        gone = lse.isnan()
+        assert int(st.item()) == 7 and bool(gone.any())
+        assert bool(out[gone].isnan().all())
+        assert torch.equal(out[~gone], want[~gone]) and torch.equal(lse[~gone], want_lse[~gone])
+        if P == 0:
+            assert not bool(gone[[b for b in range(B) if lens[b] == 0]].any())
+        monkeypatch.delenv("SPECVERIFY_SPIN_LIMIT")
+        st.fill_(-5)
+        out, lse = _call(a, device_status=st)
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0 and torch.equal(out, want) and torch.equal(lse, want_lse)
