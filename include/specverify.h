@@ -247,7 +247,9 @@ spec_status_t spec_kv_commit(void *cache, const void *staged, int NL, int B, int
  * A head with the largest magnitude amax gets the least e >= -126 with
  * amax <= 448 * 2^e, byte e + 127 (127 when amax == 0), and the codes
  * e4m3(x * 2^-e), rounded to nearest even; a head with a NaN or an infinity
- * gets byte 255.  An element is exact in bfloat16 and in float32.
+ * gets byte 255.  Read back, an element is exact in float32 up to that type's
+ * largest number (bytes to 246, whatever the code), and in bfloat16 from byte 3 on
+ * as well: bfloat16's smallest step is 2^-133, a code's at byte 0 2^-136.
  *
  * spec_kv_commit_quant commits the accepted entries of a verification pass as
  * spec_kv_commit does (the same sections), quantising them on the way:
@@ -278,7 +280,8 @@ spec_status_t spec_kv_commit_quant(void *cache, uint8_t *scale, const void *stag
  *   out [NL][B][count][2][Hkv][D], dtype `odt`: entry i of sequence b is the
  *   cache's entry start[b] + i (start NULL: 0), zero at and past seq_len[b].
  * seq_len[b] outside [0, L] or start[b] < 0 gives zeros and sets *device_status
- * to SPEC_ERR_INVALID_ARG (set to 0 first; may be NULL).  Exact.  16-byte
+ * to SPEC_ERR_INVALID_ARG (set to 0 first; may be NULL).  Elements that
+ * `odt` does not hold are rounded to it, past its largest number to infinity.  16-byte
  * aligned arrays (scale: any).  Asynchronous on `stream`, one launch.          */
 spec_status_t spec_kv_read_quant(const void *cache, const uint8_t *scale, const int32_t *start,
                                  const int32_t *seq_len, int NL, int B, int L, int count, int Hkv, int D, void *out,
@@ -316,12 +319,17 @@ spec_status_t spec_kv_read_quant(const void *cache, const uint8_t *scale, const 
  * sequence's outputs are NaN.  So are the rows that a CTA leaves unfinished when a
  * bounded wait of its own runs out (SPEC_ERR_TIMEOUT).  Scores, softmax statistics and sums are float32.
  * What is rounded to fewer bits on the way: the weights where they meet prefix
- * and cache values (to bfloat16, by 2^-8 of a weight at most; with 8-bit entries
- * to float16), and with 8-bit entries q (elements below 2^-10 of their row's
- * largest, by 2^-18 of that at most) and values of heads whose scale is more than
- * 2^22 below the largest of their 128 entries (by 2^-40 of its range).  An
- * 8-bit prefix under B T Hq / Hkv >= 1024 rows is read back to bfloat16 in the
- * workspace, and then counts as bfloat16 here.
+ * and cache values, to bfloat16, by 2^-8 of a weight at most.  With 8-bit entries:
+ *   - the weights to float16, by 2^-11 of a weight, or 2^-36 of the row's largest
+ *     where that is more (a weight counts here times the largest value scale of
+ *     its unit of 128 entries, heads of zeros left out);
+ *   - values of heads whose scale is far below that of their unit, 2^s: from
+ *     2^(s-23) on by 2^-40 of 448 * 2^s, and from 2^(s-32) on they are taken for
+ *     0 (s < -100 counts as -100);
+ *   - elements of q below 2^-10 of their row's largest, by 2^-18 of that.
+ * Key scales above 2^103 may take a score out of float32's range.  An 8-bit
+ * prefix under B T Hq / Hkv >= 1024 rows is read back to bfloat16 in the
+ * workspace, as spec_kv_read_quant does, and then counts as bfloat16 here.
  * Limits: D = 64 or 128, Hq a multiple of Hkv, Hq / Hkv <= 128, sm_scale finite
  * and > 0, P, L >= 0, T <= 2048, B T Hq <= 2^30.  All arrays but the scales, mask and
  * lse 16-byte aligned.  One launch without prefix and cache, else two, four when

@@ -485,8 +485,8 @@ def spec_kv_read_quant(cache: torch.Tensor, scale: torch.Tensor, start: torch.Te
                        count: int, *, dtype=torch.bfloat16, out=None, device_status=None,
                        stream=None) -> torch.Tensor:
     """Entries start[b] .. start[b] + count - 1 (start None: from 0) of an 8-bit
-    cache [NL][B][L][2][Hkv][D] in bfloat16 or float32 (exact), zero at and past
-    seq_len[b].  Returns [NL][B][count][2][Hkv][D]."""
+    cache [NL][B][L][2][Hkv][D] in bfloat16 (exact for scale bytes 3 to 246) or
+    float32 (exact to 246), zero at and past seq_len[b].  Returns [NL][B][count][2][Hkv][D]."""
     if not isinstance(cache, torch.Tensor) or cache.dim() != 6:
         raise TypeError("cache must be a CUDA tensor [NL][B][L][2][Hkv][D]")
     NL, B, L, _, H, D = cache.shape

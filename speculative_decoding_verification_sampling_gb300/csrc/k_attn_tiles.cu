@@ -30,21 +30,23 @@
 // the layout that TMA would have written, with scales relative to the unit's
 // largest, which becomes 2^7: float16 holds a code times 2^s exactly for s in
 // [-15, 7], and a head whose scale is more than 2^22 below loses its last bits
-// (at 2^-40 of the unit's largest element). What the largest stands for, bv,
-// goes back in exactly, into the exponent of the weights: O holds 2^(c S + bv -
-// m) V with a reference m of its own, while l holds 2^(c S - n), n following
-// the scores alone, so a unit counts in l whatever its values' scale is. A unit
-// that is nothing beside m (2^-64 or less) is summed up relative to its own
-// maximum; its P are 0 in float16 either way. The results leave with n alone: O
-// times 2^(m - n). P is rounded to float16 here: by 2^-11 of a weight, but
-// subnormal ones by 2^-25. So that these are far down, m stays 11 to 15 below
-// the row's maximum (of c S + bv), and P may reach 2^15: 2^-11 holds for
-// weights down to 2^-25 of the largest, and below that 2^-36 of it. A head of
-// zeros, whose byte is 127, counts for nothing in its unit: an entry with most
-// of a row's weight and zeros for values would push all the others down. With
-// few rows, where HBM is the bound, one warp's pass over 128 scores per row and
-// their scales is too long a chain: the rows then lie in their tile two or four
-// times, and each warp of a group takes the columns that fall to its copy.
+// (at 2^-40 of the unit's largest element); from 2^32 below on its factor is 0
+// in float16, and so are its values (2^-32 of the largest). What the largest
+// stands for, bv, goes back in exactly, into the exponent of the weights: O
+// holds 2^(c S + bv - m) V with a reference m of its own, while l holds 2^(c S
+// - n), n following the scores alone, so a unit counts in l whatever its
+// values' scale is. A unit that is nothing beside m (2^-64 or less) is summed
+// up relative to its own maximum; its P are 0 in float16 either way. The
+// results leave with n alone: O times 2^(m - n). P is rounded to float16 here:
+// by 2^-11 of a weight, but subnormal ones by 2^-25. So that these are far
+// down, m stays 11 to 15 below the row's maximum (of c S + bv), and P may reach
+// 2^15: 2^-11 holds for weights down to 2^-25 of the largest, and below that
+// 2^-36 of it. A head of zeros, whose byte is 127, counts for nothing in its
+// unit: an entry with most of a row's weight and zeros for values would push
+// all the others down. With few rows, where HBM is the bound, one warp's pass
+// over 128 scores per row and their scales is too long a chain: the rows then
+// lie in their tile two or four times, and each warp of a group takes the
+// columns that fall to its copy.
 //
 // Measured, 32 query and 8 key/value heads of 128: 64 sequences of 32 tokens over
 // 8192 shared entries, 191 us, 1440 TFLOP/s (bound by the two groups' softmax, the

@@ -5,10 +5,11 @@
 // with amax the largest magnitude, e is the least integer with
 // amax <= 448 * 2^e (448 is the largest e4m3 number), clamped to >= -126; the
 // entry holds code(x) = e4m3(x * 2^-e), rounded to nearest even, and the byte
-// e + 127.  x * 2^-e is exact in float32, so a code is off by at most half a
-// step of its format and nothing else, and it depends on no order of
-// evaluation.  code * 2^e is exact in bfloat16 as well as in float32 (4
-// significant bits), so reading back and attending to the cache lose nothing.
+// e + 127.  x * 2^-e is exact in float32 (or so small that its code is 0), so a
+// code is off by at most half a step of its format and nothing else, and it
+// depends on no order of evaluation.  code * 2^e has 4 significant bits: exact in
+// float32 up to byte 246, past which it may overflow, and in bfloat16 from byte 3
+// on as well (its smallest step is 2^-133, the smallest code is 2^-9).
 // A head whose elements include a NaN or an infinity gets the byte 255, which
 // reads back as NaN everywhere.
 //
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(QT) kvq_read(const __grid_constant__ KvQuantPa
         for (int k = 0; k < 8; ++k)
             x[k] *= f;
         if constexpr (sizeof(E) == 2) {
-            uint4 w;   // exact: four significant bits
+            uint4 w;   // exact from byte 3 on: four significant bits
             w.x = pack_bf16(x[0], x[1]);
             w.y = pack_bf16(x[2], x[3]);
             w.z = pack_bf16(x[4], x[5]);

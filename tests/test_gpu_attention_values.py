@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import speculative_decoding_verification_sampling_gb300 as sv
-from test_gpu_attention import DEV, _case, _device, _hold, _reference, _run   # noqa: F401
+from test_gpu_attention import BF, DEV, _case, _device, _hold, _reference, _run   # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -179,3 +179,25 @@ def test_peaked_rows_8_bits(T, sm_scale):
     a = _case(3, T, 8, 2, 128, 600, 2500, [2500, 0, 257], True, "causal", seed=4)
     a["q"][0] *= 4
     _run(a, f"scale {sm_scale}", sm_scale)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("below", [22, 23, 27, 31, 32, 33, 60])
+def test_values_far_below_their_units(below, D):
+    """A head 2^22 below its unit's scale is exact; further down it loses 2^-40 of the unit's range,
+    and from 2^32 below on it counts as 0, 2^-32 of that."""
+    top, n = 127, 300
+    score = torch.full((n,), -48.0, dtype=torch.float64, device=DEV)
+    score[[5, 140, 290]] = 0.0
+    a = _scored(2, 5, 8, 2, D, [n, 291], score, 47)
+    a["cache_scale"][..., 1, :] = torch.where(a["cache_scale"][..., 1, :] == 255, 255, top)
+    for i in (5, 140, 290):
+        a["cache_scale"][:, i, 1] = top - below
+    scale = a["sm_scale"]
+    out, lse = _call(a)
+    ref = _reference({k: v for k, v in a.items() if k != "sm_scale"}, scale)
+    lost = 0.0 if below <= 22 else 2.0 ** -40 if below < 32 else 2.0 ** -32
+    tol = 1.01 * (2.0 ** -8 * ref["out"].abs() + (2.0 ** -8 + 2.0 ** -19) * ref["mass"]) + lost * 448.0
+    err = (out.double() - ref["out"]).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+    _hold(ref["out"].to(BF), lse, ref, D, "lse")

@@ -181,3 +181,22 @@ def test_commit_of_many_entries_by_few_sequences(NL, B, K, H, D, nodes):
     staged = torch.randn((NL, B, K, 2, H, D), generator=torch.Generator().manual_seed(K)).to(torch.bfloat16)
     order = [[(7 * i + b) % K for i in range(K)] for b in range(B)] if nodes else None
     _check_commit(codes, scale, staged, [max(K - 11 * b, 0) for b in range(B)], [(5 * b) % 8 for b in range(B)], order)
+
+
+def test_every_code_at_every_byte():
+    """Which elements reading back gives exactly: float32 up to byte 246, bfloat16 from byte 3 on as
+    well.  Below that bfloat16 has no such number for some, and rounds; above, the largest are infinite."""
+    codes = torch.arange(256, dtype=torch.int32).to(torch.uint8).view(1, 1, 1, 2, 2, 64).repeat(1, 1, 255, 1, 1, 1)
+    byte = torch.arange(255, dtype=torch.int32).to(torch.uint8).view(1, 1, 255, 1, 1).repeat(1, 1, 1, 2, 2)
+    exact = torch.from_numpy(kq.values(codes.numpy(), byte.numpy()))
+    code = torch.from_numpy(kq.decode(codes[0, 0, 0].numpy()))
+    for dtype, low in ((torch.float32, 0), (torch.bfloat16, 3)):
+        got = sv.spec_kv_read_quant(codes.to(DEV).view(torch.float8_e4m3fn), byte.to(DEV), None, _i32([255]), 255,
+                                    dtype=dtype).cpu().double()
+        assert torch.equal(got.isnan(), exact.isnan())
+        inside = slice(low, 247)
+        assert torch.equal(got[:, :, inside].nan_to_num(), exact[:, :, inside].nan_to_num())
+        assert bool(got[0, 0, 247][code.abs() == 448].isinf().all())
+        if low:
+            near = (got[:, :, :low] - exact[:, :, :low]).abs().nan_to_num()
+            assert bool((near <= 2.0 ** -134).all()) and bool((near > 0).any())     # half a step of 2^-133
