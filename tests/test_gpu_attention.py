@@ -392,3 +392,13 @@ def test_workspace_at_any_16_bytes_and_launches(quant):
 def test_few_rows_over_long_caches(B, T, Hq, H, D, P, L, quant):
     a = _case(B, T, Hq, H, D, P, L, [L - 77 * b for b in range(B)], quant, "causal", seed=17)
     _run(a, f"{B * T * Hq} rows over {L} entries")
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("kind", ["causal", "holes"])
+@pytest.mark.parametrize("B,T,Hq,H,D,P,L", [(2, 62, 4, 1, 64, 130, 300), (2, 129, 4, 2, 128, 70, 140), (1, 512, 8, 2, 64, 300, 129),
+                                            (1, 513, 2, 2, 128, 0, 0), (1, 2048, 2, 1, 64, 129, 257)])
+def test_many_tokens(B, T, Hq, H, D, P, L, kind, quant):
+    """Passes longer than a draft tree's, to the most that a call takes."""
+    a = _case(B, T, Hq, H, D, P, L, [L - 100 * b for b in range(B)], quant, kind, seed=18)
+    _run(a, f"{T} tokens")

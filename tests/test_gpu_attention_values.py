@@ -181,6 +181,33 @@ def test_peaked_rows_8_bits(T, sm_scale):
     _run(a, f"scale {sm_scale}", sm_scale)
 
 
+@pytest.mark.parametrize("B,T", [(2, 5), (2, 61), (40, 3)])
+@pytest.mark.parametrize("down", [False, True])
+def test_rising_scores_8_bits(B, T, down):
+    """Each run of entries scores higher than the ones before: the running maximum moves all along."""
+    grid = torch.arange(256, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn).double() / 8
+    grid = grid[~grid.isnan()].sort().values
+    up = grid[(torch.arange(2900, device=DEV) * len(grid)) // 2900]
+    up = up.flip(0) if down else up
+    a = _scored(B, T, 8, 2, 64, [2000 - 40 * b for b in range(B)], up[900:], 45, prefix=up[:900])
+    a["q"][..., 0] = torch.rand((B, T, 8), device=DEV, generator=torch.Generator(device=DEV).manual_seed(6)).to(BF) + 0.5
+    a["sm_scale"] = 1.0
+    _hold_scored(a, "rising")
+
+
+def test_scores_of_minus_infinity_8_bits():
+    """Products below float32's lowest number: no weight."""
+    score = torch.zeros(300, dtype=torch.float64, device=DEV)
+    a = _scored(2, 3, 4, 2, 64, [300, 129], score, 46)
+    want, want_lse = _call({**a, "seq_len": torch.tensor([2, 2], dtype=torch.int32, device=DEV)})
+    a["cache"][:, 2:, 0, :, 0] = -448.0
+    a["cache_scale"][0, 2:, 0] = a["cache_scale"][1, 2:129, 0] = 254
+    ref = _reference({**{k: v for k, v in a.items() if k != "sm_scale"}, "seq_len": torch.tensor([2, 2])}, 0.125)
+    ref["count"] += 298
+    _hold(*_call(a), ref, 64, "minus infinity")
+    _hold(want, want_lse, ref, 64, "without them")
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("below", [22, 23, 27, 31, 32, 33, 60])
 def test_values_far_below_their_units(below, D):
