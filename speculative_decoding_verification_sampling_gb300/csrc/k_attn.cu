@@ -86,12 +86,6 @@ __device__ __forceinline__ void load_values(const float *p, int step, float (&y)
     }
 }
 
-// The launches of the tile kernel ahead: none, one for all pairs, or one for the
-// prefix and one for the caches; and their CTAs.
-struct FinishLines {
-    int launches, pre_ctas, own_ctas;
-};
-
 // Many rows (WIDE = false): eight lanes per query row.  A warp works on four
 // heads of a token, and the index arithmetic and the loops over what they see
 // serve four rows.  Seven CTAs to an SM and two partial results in flight:
@@ -104,7 +98,7 @@ struct FinishLines {
 // (1280 rows: 19 us, 42 us with 16).
 template <int D, int WIDE>
 __global__ void __launch_bounds__(WIDE ? WIDE * 32 : 128, WIDE ? 1 : 7)
-    va_finish(const __grid_constant__ AttnParams P, const __grid_constant__ AttnWork W, FinishLines L, int per_token)
+    va_finish(const __grid_constant__ AttnParams P, const __grid_constant__ AttnWork W, int launches, int per_token)
 {
     constexpr int FW = WIDE ? WIDE : 4;   // warps
     constexpr int LPR = WIDE ? 32 : 8, E = D / LPR, NP = E / 2, AT = E < 8 ? E : 8;
@@ -194,13 +188,14 @@ __global__ void __launch_bounds__(WIDE ? WIDE * 32 : 128, WIDE ? 1 : 7)
         }
     }
     int code = bad ? 1 : 0;
-    if (L.launches > 0) {
+    // of the tile kernel ahead: none, one for all pairs, or one for the prefix and one for the caches
+    if (launches > 0) {
         asm volatile("griddepcontrol.wait;" ::: "memory");   // the tile kernel's results
         if (!bad) {
             // where this row's partial results are: over the prefix, then over its cache
             const int HS = P.H * W.own.tiles;
             // two lines: each kind of pair has its own; one: the prefix pairs come first on both's
-            const int two_lines = L.launches == 2;
+            const int two_lines = launches == 2;
             const int2 before = P.L > 0 ? __ldcg(W.base + b) : make_int2(0, 0);
             // not read through the non-coherent path: the tile kernel has just written them
             const AttnLine line0 = *W.line, line1 = two_lines ? W.line[1] : line0;
@@ -358,7 +353,7 @@ __global__ void __launch_bounds__(WIDE ? WIDE * 32 : 128, WIDE ? 1 : 7)
 }
 
 template <int D, int WIDE>
-cudaError_t finish(const AttnParams &P, const AttnWork &W, const FinishLines &L, cudaStream_t stream)
+cudaError_t finish(const AttnParams &P, const AttnWork &W, int launches, cudaStream_t stream)
 {
     constexpr int FW = WIDE ? WIDE : 4;
     const int per_token = WIDE ? P.Hq : (P.Hq + FW * 4 - 1) / (FW * 4);
@@ -370,8 +365,8 @@ cudaError_t finish(const AttnParams &P, const AttnWork &W, const FinishLines &L,
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = L.launches > 0 ? 1 : 0;   // behind the tile kernel; alone it starts like any other
-    return cudaLaunchKernelEx(&cfg, va_finish<D, WIDE>, P, W, L, per_token);
+    cfg.numAttrs = launches > 0 ? 1 : 0;   // behind the tile kernel; alone it starts like any other
+    return cudaLaunchKernelEx(&cfg, va_finish<D, WIDE>, P, W, launches, per_token);
 }
 
 }  // namespace
@@ -414,15 +409,15 @@ cudaError_t launch_attention(const AttnParams &P, bool quant, void *workspace, i
     W.o_s = reinterpret_cast<float *>(w + a.o_s);
     // one CTA per SM, fewer where even full caches have fewer units
     const long long most = sms < AT_MAX_CTAS ? sms : AT_MAX_CTAS;
-    FinishLines L{};
-    auto tiles = [&](const AttnParams &A, const AttnWork &V, bool q8, long long units, int &ctas) {
-        ctas = (int)(units < most ? units : most);
+    int lines = 0;
+    auto tiles = [&](const AttnParams &A, const AttnWork &V, bool q8, long long units) {
+        const int ctas = (int)(units < most ? units : most);
         if (ctas == 0)
             return cudaSuccess;
-        const cudaError_t e = launch_attn_tiles(A, V, q8, ctas, L.launches > 0, spin_limit, stream);
+        const cudaError_t e = launch_attn_tiles(A, V, q8, ctas, lines > 0, spin_limit, stream);
         if (e == cudaSuccess) {
             ++*launches;
-            ++L.launches;
+            ++lines;
         }
         return e;
     };
@@ -445,7 +440,7 @@ cudaError_t launch_attention(const AttnParams &P, bool quant, void *workspace, i
         A.prefix = w + a.prefix;
         A.L = 0;
         V.base = nullptr;
-        e = tiles(A, V, false, (long long)a.ppairs * a.pu, L.pre_ctas);
+        e = tiles(A, V, false, (long long)a.ppairs * a.pu);
         if (e != cudaSuccess)
             return e;
         A = P;
@@ -454,21 +449,20 @@ cudaError_t launch_attention(const AttnParams &P, bool quant, void *workspace, i
         V.ppairs = 0;
         V.stat += AT_MAX_CTAS;
         ++V.line;
-        e = tiles(A, V, true, a.max_units - (long long)a.ppairs * a.pu, L.own_ctas);
+        e = tiles(A, V, true, a.max_units - (long long)a.ppairs * a.pu);
     } else {
-        e = tiles(P, W, quant, a.max_units, L.pre_ctas);
-        L.own_ctas = L.pre_ctas;
+        e = tiles(P, W, quant, a.max_units);
     }
     if (e != cudaSuccess)
         return e;
     const long long rows = (long long)P.B * P.T * P.Hq;
     const int wide = rows <= WIDER_ROWS ? 16 : rows <= WIDE_ROWS ? 4 : 0;
     if (P.D == 128)
-        e = wide == 16 ? finish<128, 16>(P, W, L, stream)
-                       : wide ? finish<128, 4>(P, W, L, stream) : finish<128, 0>(P, W, L, stream);
+        e = wide == 16 ? finish<128, 16>(P, W, lines, stream)
+                       : wide ? finish<128, 4>(P, W, lines, stream) : finish<128, 0>(P, W, lines, stream);
     else
-        e = wide == 16 ? finish<64, 16>(P, W, L, stream)
-                       : wide ? finish<64, 4>(P, W, L, stream) : finish<64, 0>(P, W, L, stream);
+        e = wide == 16 ? finish<64, 16>(P, W, lines, stream)
+                       : wide ? finish<64, 4>(P, W, lines, stream) : finish<64, 0>(P, W, lines, stream);
     if (e == cudaSuccess)
         ++*launches;
     return e;
