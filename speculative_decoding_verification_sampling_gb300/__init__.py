@@ -22,6 +22,12 @@ import torch
 
 from .build import LIB as _LIB_PATH
 
+try:   # the current stream's handle, in a twentieth of the public way's 2 us
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+except ImportError:
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
+
 __all__ = [
     "SpecVerifyError", "Aux", "spec_verify", "spec_verify_greedy", "spec_verify_shortlist",
     "spec_workspace_bytes", "spec_philox_words", "spec_draft_sample", "spec_kv_commit", "spec_verify_tree_greedy", "spec_tree_mask",
@@ -257,7 +263,7 @@ def _outs(B, K, device, out_tokens, out_accept_len, before):
 def _stream(device, stream):
     if stream is None:
         index = device.index
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
+        return _raw_stream(torch.cuda.current_device() if index is None else index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -547,7 +553,11 @@ def spec_verify_attention(q: torch.Tensor, cache: torch.Tensor, seq_len: torch.T
     (spec_tree_mask) or causally.  Prefix and cache are bfloat16, or both
     float8_e4m3fn with cache_scale [B][L][2][Hkv] and prefix_scale [P][2][Hkv]
     uint8.  sm_scale defaults to 1 / sqrt(D).  Returns (out [B][T][Hq][D]
-    bfloat16, lse [B][T][Hq] float32); a row that sees nothing has 0 and -inf."""
+    bfloat16, lse [B][T][Hq] float32); a row that sees nothing has 0 and -inf.
+    There is no backward pass: the outputs carry no gradient.  Without workspace
+    (uint8, spec_attention_workspace_bytes(...) elements, one per call in flight) the
+    call takes scratch that its thread keeps for the stream, as large as the largest
+    call so far, until the thread ends."""
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise TypeError("q must be a CUDA tensor [B][T][Hq][D]")
     if not isinstance(cache, torch.Tensor) or cache.dim() != 5:
