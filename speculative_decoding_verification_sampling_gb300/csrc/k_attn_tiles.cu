@@ -49,11 +49,11 @@
 // columns that fall to its copy.
 //
 // Measured, 32 query and 8 key/value heads of 128: 64 sequences of 32 tokens over
-// 8192 shared entries, 191 us, 1440 TFLOP/s (bound by the two groups' softmax, the
-// tensor cores 62 % active); 64 of 5 tokens over 4096 own entries each, 170 us,
-// 6.3 TB/s (HBM); 64 of 9 tokens over 8192 own 8-bit entries each, 261 us, 4.1
+// 8192 shared entries, 190 us, 1448 TFLOP/s (bound by the two groups' softmax, the
+// tensor cores 62 % active); 64 of 5 tokens over 4096 own entries each, 174 us,
+// 6.2 TB/s (HBM); 64 of 9 tokens over 8192 own 8-bit entries each, 265 us, 4.1
 // TB/s (the chain of a unit, and the copies in flight beside tiles being
-// converted); 256 of 5 tokens over 512 own 8-bit entries each, 119 us (9 us to a
+// converted); 256 of 5 tokens over 512 own 8-bit entries each, 117 us (9 us to a
 // pair of four units: one warp's softmax over 128 columns is 1.8 us of each).
 //
 // The last unit of a stretch is ragged: scores past its end become -inf, and
@@ -294,8 +294,9 @@ __device__ __forceinline__ int seq_units(const AttnParams &A, int b)
 
 // Units from which a stretch of 8-bit entries with one set of rows uses copies of
 // them and joins what the groups and copies leave (a fixed cost per stretch: 8 units
-// each under 64 sequences of 5 tokens take 57 us without, 61 us with; 64 units each
-// under 64 of 9, 261 us with, 296 us without).
+// each under 64 sequences of 5 tokens take 56 us without, 67 us with; 12 each 73 us
+// and 75 us, 16 each 89 us either way; 64 each under 64 of 9, 265 us with, 304 us
+// without).
 constexpr int JOIN_UNITS = 12;
 
 // One stretch of one pair, as a CTA works on it.
@@ -1111,7 +1112,7 @@ __device__ __forceinline__ void scale_role(const TileParams &P, QuantShared &sh,
 // takes rows 32 w .. 32 w + 31 of each tile of codes.  What runs rarely is kept short
 // (four rows of Q at a time, the tail's zeros in a loop): the roles share the
 // instruction cache, and with eight rows of Q at a time and the tail unrolled 64
-// sequences of 9 tokens over 8192 own entries take 312 us, not 261 us.
+// sequences of 9 tokens over 8192 own entries took 312 us where they took 261 us so.
 template <int D>
 __device__ void convert_role(const TileParams &P, QuantShared &sh, uint8_t *tiles, uint32_t limit)
 {

@@ -91,8 +91,8 @@ __device__ __forceinline__ float piece_at(const Piece<E> &x, int k)
 
 // One CTA per (layer, sequence), QU pieces in flight per thread; where these are
 // fewer than QC, several, which take its pieces in turn (a prompt of 16384
-// entries, one layer and sequence, 8 heads of 128: 23 us, 4.4 TB/s; 15 ms by one
-// CTA).  32 layers x 256 sequences with 3 entries each: 35 us with the length
+// entries, one layer and sequence, 8 heads of 128: 24.6 us with the length update,
+// 4.1 TB/s; 15 ms by one CTA).  32 layers x 256 sequences with 3 entries each: 35 us with the length
 // update, 4.3 TB/s, about 6 us of it the second launch.
 template <class E, int D>
 __global__ void __launch_bounds__(QT, sizeof(E) == 2 ? 12 : 8) kvq_commit(const __grid_constant__ KvQuantParams P)

@@ -21,10 +21,15 @@
 //
 // An 8-bit prefix under many rows is read back to bfloat16 first: the products
 // over it bound the call then, and the kernel for bfloat16 entries runs them at
-// 1.6 times the rate of the one for codes (64 sequences of 32 tokens, 32 heads,
-// 8192 entries: 190 us and 311 us), while reading back takes 6 bytes per
-// element once. That breaks even at about 700 rows per key/value head. Prefix
-// and caches are then two lines, of one launch each.
+// 1.6 times the rate of the one for codes, while reading back takes 6 bytes per
+// element once.  Whole calls, heads 32/8 x 128, read back and by codes: 64
+// sequences of 32 tokens over 8192 entries, 290 us and 410 us; over 16384 entries
+// and caches to 512, 1280 rows per key/value head, 134 us and 158 us, 1020 rows
+// 117 us and 131 us, 640 rows 98 us and 105 us; over 8192, 1020 rows 88 us and
+// 94 us, 520 rows 74 us and 73 us.  So it breaks even at about 600 rows, but from
+// there to 1023 rows the codes stay, up to a tenth slower: their weights are
+// float16, which is eight times as exact as bfloat16.  Prefix and caches are then
+// two lines, of one launch each.
 #pragma once
 #include <cstdint>
 
@@ -46,7 +51,10 @@ constexpr int SPREAD = 4;
 // of two tiles 1.8 us, its pair 3.6 us; a unit of one tile 1 us, its pair 1.8 us
 // and up to 1.8 us more with the rows that are written (64 sequences of 32
 // tokens, 8192 shared and 512 own entries, 32 heads: 278 us a call so, 359 us
-// with 1 us a pair); with 8-bit entries 1.2 us and 4 us.  At most 12: max_line.
+// with 1 us a pair); with 8-bit entries a unit is taken for 0.9 us and a
+// pair for 4 us (1.0 to 1.3 us a unit, where 1216 pairs of 8 to 32 units share the
+// HBM).  Heads of 64 count the same; their units take 0.85 us in bfloat16 and 1 us
+// in 8 bits.  At most 12: max_line.
 struct AttnTiling {
     int tq, two, tiles, copies, join, shift, over;
 };
