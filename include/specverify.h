@@ -317,7 +317,9 @@ spec_status_t spec_kv_read_quant(const void *cache, const uint8_t *scale, const 
  *   device_status [1] set to 0, or the code of one failing sequence; may be NULL
  * seq_len[b] outside [0, L] is an error (SPEC_ERR_INVALID_ARG): that
  * sequence's outputs are NaN.  So are the rows that a CTA leaves unfinished when a
- * bounded wait of its own runs out (SPEC_ERR_TIMEOUT).  Scores, softmax statistics and sums are float32.
+ * bounded wait of its own runs out (SPEC_ERR_TIMEOUT).  Scores, softmax
+ * statistics and sums are float32; a weight below 2^-117 of its row's largest may
+ * count as 0.
  * What is rounded to fewer bits on the way: the weights where they meet prefix
  * and cache values, to bfloat16, by 2^-8 of a weight at most.  With 8-bit entries:
  *   - the weights to float16, by 2^-11 of a weight, or 2^-36 of the row's largest
