@@ -211,6 +211,70 @@ spec_status_t spec_draft_sample(const void *draft_logits, spec_dtype_t ddt, int 
                                 uint64_t seed, int32_t *out_tokens, float *out_prob, int32_t *device_status,
                                 void *stream);
 
+/* What requests ask for beside the temperature: device arrays of B entries, one
+ * per sequence; NULL: off for all.  A row's tokens in descending order of the
+ * logit z, the lowest index first among equals, have the weights
+ * w = e^((z - max z) / T).  In turn:
+ *   top_k  keeps the first k (k <= 0: all);
+ *   top_p  keeps, of those, a token if the sum of the weights ahead of it is
+ *          less than p times the sum of what top_k left (p >= 1: all);
+ *   min_p  keeps w >= min_p (min_p <= 0: all).
+ * The first token stays in any case; what is kept is normalised.  T == 0 is the
+ * first token alone.  A temperature that is negative, infinite or NaN, a top_p of
+ * NaN and a min_p above 1 or NaN are data errors (SPEC_ERR_INVALID_ARG) of the
+ * sequence.  Temperatures below 2^-100 count as that, above 2^100 as that.
+ * Weights are held to 2^-31 of their own and 2^-44 of the row's largest, their
+ * sums exactly: results do not depend on how the work is split.               */
+typedef struct {
+    const float *temperature;   /* NULL: 1 */
+    const int32_t *top_k;
+    const float *top_p;
+    const float *min_p;
+} spec_filters_t;
+
+/* Tokens drawn from filtered rows of logits by given random numbers (the
+ * drafting step of spec_draft_sample's sections, and plain decoding):
+ *   logits        [B][K][V]  dtype `ldt`; row (b, i) under sequence b's filters
+ *   uniforms      [B][K]     float32 in [0, 1)
+ *   filters       NULL: none
+ *   out_tokens    [B][K]     int32: the smallest x whose running sum of kept weights
+ *                            in ascending token order exceeds uniform * their total
+ *   out_prob      [B][K]     float: the token's probability among the kept (may be NULL)
+ *   device_status [1]        set to 0, or the code of one failing row; may be NULL
+ * A row with a NaN or +inf logit, or -inf everywhere (SPEC_ERR_NONFINITE), with
+ * filters as above or a uniform outside [0, 1) (SPEC_ERR_INVALID_ARG) gets token -1
+ * and probability NaN.  -inf logits are never drawn.
+ * Limits: B, K, V >= 1, B * K <= 2^26, V <= 524288.  No workspace; one launch,
+ * asynchronous on `stream`.                                                   */
+spec_status_t spec_filter_sample(const void *logits, spec_dtype_t ldt, const float *uniforms, int B, int K, int V,
+                                 const spec_filters_t *filters, int32_t *out_tokens, float *out_prob,
+                                 int32_t *device_status, void *stream);
+
+/* Verification between filtered distributions (the rule of the top of this
+ * file, with q_i the target's row i under `filters` and p_i the draft's row i
+ * under `draft_filters`): accept d_i iff u_i p_i(d_i) < q_i(d_i), so a token that
+ * neither keeps is rejected; at the first rejection j a token from (q_j - p_j)+,
+ * from q_j itself when that is nothing; after K accepted drafts one from q_{K+1}.
+ *   target_logits  [B][K+1][V], draft_logits [B][K][V]  dtype `tdt`
+ *   draft_tokens   [B][K]       int32, drawn from p_i (spec_filter_sample)
+ *   uniforms       [B][K+1][2]  float32 in [0, 1): u_i, and the number that the
+ *                               emitted token is drawn with when the round ends at i
+ *   draft_filters  NULL: the same as `filters`
+ *   out_tokens     [B][K+1], out_accept_len [B]  as spec_verify's, with its data errors:
+ *                  those of the rows that the left-to-right rule reaches, and of
+ *                  filters and uniforms (SPEC_ERR_INVALID_ARG)
+ *   workspace      device scratch of spec_filter_workspace_bytes(B, K, V) bytes (no
+ *                  zero-fill needed), 16-byte aligned; one per call in flight
+ *   device_status  [1] set to 0, or the code of one failing sequence; may be NULL
+ * Drawing is spec_filter_sample's.  Limits: B >= 1, 1 <= K <= 31, 1 <= V <= 524288,
+ * B (2K + 1) <= 2^26.  Two launches, asynchronous on `stream`.                 */
+size_t spec_filter_workspace_bytes(int B, int K, int V);
+spec_status_t spec_verify_filtered(const void *target_logits, spec_dtype_t tdt, const void *draft_logits,
+                                   const int32_t *draft_tokens, const float *uniforms, int B, int K, int V,
+                                   const spec_filters_t *filters, const spec_filters_t *draft_filters,
+                                   int32_t *out_tokens, int32_t *out_accept_len, void *workspace,
+                                   size_t workspace_bytes, int32_t *device_status, void *stream);
+
 /* KV-cache commit (and rollback) after verification (nextadmin.net lesson
  * "Speculative Decoding", § KV cache management: the verification pass
  * appends the K drafts' entries; when drafts are rejected the cache returns
@@ -396,7 +460,8 @@ spec_status_t spec_philox_words(uint64_t seed, uint32_t tag, int B, int P, uint3
  * batches: two from 1024 rows with aligned rows, where the residual pass runs
  * inside the statistics stream); spec_draft_sample and spec_philox_words
  * launch one each, spec_kv_commit two (one in place), spec_kv_commit_quant two,
- * spec_kv_read_quant one, spec_verify_attention one to four.  For accounting;
+ * spec_kv_read_quant one, spec_verify_attention one to four, spec_filter_sample
+ * one, spec_verify_filtered two.  For accounting;
  * thread-safe.                                                               */
 uint64_t spec_launch_count(void);
 

@@ -29,7 +29,8 @@ except ImportError:
         return torch.cuda.current_stream(index).cuda_stream
 
 __all__ = [
-    "SpecVerifyError", "Aux", "spec_verify", "spec_verify_greedy", "spec_verify_shortlist",
+    "SpecVerifyError", "Aux", "Filters", "spec_filter_sample", "spec_verify_filtered", "spec_filter_workspace_bytes",
+    "spec_verify", "spec_verify_greedy", "spec_verify_shortlist",
     "spec_workspace_bytes", "spec_philox_words", "spec_draft_sample", "spec_kv_commit", "spec_verify_tree_greedy", "spec_tree_mask",
     "spec_kv_commit_quant", "spec_kv_read_quant", "spec_verify_attention", "spec_attention_workspace_bytes",
     "spec_verify_shortlist_pos", "spec_status_string", "spec_launch_count", "spec_verify_static", "library_path", "load",
@@ -107,6 +108,12 @@ def load():
             lib.spec_verify_attention.restype = I
             lib.spec_draft_sample.argtypes = [P, I, I, I, I, F, U64, P, P, P, P]
             lib.spec_draft_sample.restype = I
+            lib.spec_filter_sample.argtypes = [P, I, P, I, I, I, P, P, P, P, P]
+            lib.spec_filter_sample.restype = I
+            lib.spec_filter_workspace_bytes.argtypes = [I, I, I]
+            lib.spec_filter_workspace_bytes.restype = Z
+            lib.spec_verify_filtered.argtypes = [P, I, P, P, P, I, I, I, P, P, P, P, P, Z, P, P]
+            lib.spec_verify_filtered.restype = I
             lib.spec_launch_count.argtypes = []
             lib.spec_launch_count.restype = U64
             _lib = lib
@@ -156,6 +163,42 @@ class Aux:
                           ptr(self.device_status, (1,), torch.int32))
 
 
+class _FiltersStruct(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+                ("min_p", ctypes.c_void_p)]
+
+
+class Filters:
+    """What each sequence asks for: device tensors [B], or None where it is off.
+    temperature float32 (0: the largest logit alone; None: 1), top_k int32 (<= 0:
+    all), top_p float32 (>= 1: all), min_p float32 (<= 0: all).  They apply in this
+    order: see spec_filters_t in include/specverify.h."""
+    __slots__ = ("temperature", "top_k", "top_p", "min_p")
+
+    def __init__(self, temperature=None, top_k=None, top_p=None, min_p=None):
+        self.temperature, self.top_k, self.top_p, self.min_p = temperature, top_k, top_p, min_p
+
+    @classmethod
+    def fill(cls, B: int, device, temperature: float = 1.0, top_k: int = 0, top_p: float = 1.0,
+             min_p: float = 0.0) -> "Filters":
+        """The same for B sequences."""
+        return cls(torch.full((B,), temperature, dtype=torch.float32, device=device),
+                   torch.full((B,), top_k, dtype=torch.int32, device=device),
+                   torch.full((B,), top_p, dtype=torch.float32, device=device),
+                   torch.full((B,), min_p, dtype=torch.float32, device=device))
+
+    def _struct(self, B, device, name):
+        def ptr(t, dtype, what):
+            if t is None:
+                return None
+            _check(t, (B,), (dtype,), f"{name}.{what}")
+            _beside(device, t)
+            return t.data_ptr()
+        return _FiltersStruct(ptr(self.temperature, torch.float32, "temperature"),
+                              ptr(self.top_k, torch.int32, "top_k"), ptr(self.top_p, torch.float32, "top_p"),
+                              ptr(self.min_p, torch.float32, "min_p"))
+
+
 # ------------------------------------------------------------------ helpers
 def _check(t, shape, dtypes, name):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -166,6 +209,15 @@ def _check(t, shape, dtypes, name):
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _beside(device, *tensors):
+    """The tensors of a call lie on one device, the current one: the launches go there."""
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {t.device} and {device} in one call")
+    if device.index is not None and device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {device}, but cuda:{torch.cuda.current_device()} is the current device")
 
 
 def _dt(t):
@@ -421,6 +473,87 @@ def spec_draft_sample(draft: torch.Tensor, T: float, seed: int, *, out_tokens=No
     if rc:
         raise SpecVerifyError(rc, "spec_draft_sample")
     return out_tokens, out_prob
+
+
+def spec_filter_sample(logits: torch.Tensor, uniforms: torch.Tensor, filters: Filters | None = None, *,
+                       out_tokens=None, out_prob=None, device_status=None, stream=None):
+    """Tokens drawn from rows of logits under each sequence's filters by given
+    random numbers: logits [B][K][V] float32 or bfloat16, uniforms [B][K] float32 in
+    [0, 1).  Returns (out_tokens [B][K] int32, out_prob [B][K] float32, the tokens'
+    probabilities among what the filters keep) on the device."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 3:
+        raise TypeError("logits must be a CUDA tensor [B][K][V]")
+    B, K, V = logits.shape
+    _check(logits, (B, K, V), (torch.float32, torch.bfloat16), "logits")
+    _check(uniforms, (B, K), (torch.float32,), "uniforms")
+    dev = logits.device
+    if device_status is not None:
+        _check(device_status, (1,), (torch.int32,), "device_status")
+    fs = filters._struct(B, dev, "filters") if filters is not None else None
+    with _on(dev, stream) as before:
+        if out_tokens is None:
+            out_tokens = _new((B, K), torch.int32, dev, before)
+        if out_prob is None:
+            out_prob = _new((B, K), torch.float32, dev, before)
+    _check(out_tokens, (B, K), (torch.int32,), "out_tokens")
+    _check(out_prob, (B, K), (torch.float32,), "out_prob")
+    _beside(dev, uniforms, out_tokens, out_prob, device_status)
+    rc = load().spec_filter_sample(logits.data_ptr(), _dt(logits), uniforms.data_ptr(), B, K, V,
+                                   ctypes.byref(fs) if fs is not None else None, out_tokens.data_ptr(),
+                                   out_prob.data_ptr(), device_status.data_ptr() if device_status is not None else None,
+                                   _stream(dev, stream))
+    if rc:
+        raise SpecVerifyError(rc, "spec_filter_sample")
+    return out_tokens, out_prob
+
+
+def spec_filter_workspace_bytes(B: int, K: int, V: int) -> int:
+    return int(load().spec_filter_workspace_bytes(int(B), int(K), int(V)))
+
+
+def spec_verify_filtered(target: torch.Tensor, draft: torch.Tensor, draft_tokens: torch.Tensor,
+                         uniforms: torch.Tensor, filters: Filters | None = None, *,
+                         draft_filters: Filters | None = None, out_tokens=None, out_accept_len=None, workspace=None,
+                         device_status=None, stream=None):
+    """Verification between filtered distributions: target [B][K+1][V] and draft
+    [B][K][V] float32 or bfloat16 logits, draft_tokens [B][K] int32 drawn from the
+    draft's rows under draft_filters (default: filters; spec_filter_sample draws
+    them), uniforms [B][K+1][2] float32 in [0, 1): at position i the acceptance
+    number, and the number that draws the emitted token if the round ends there.
+    Returns (out_tokens [B][K+1], out_accept_len [B]) as spec_verify does.  Without
+    workspace (uint8, spec_filter_workspace_bytes(...) elements, one per call in flight)
+    the call takes scratch that its thread keeps for the stream, as
+    spec_verify_attention does."""
+    if not isinstance(target, torch.Tensor) or target.dim() != 3:
+        raise TypeError("target must be a CUDA tensor [B][K+1][V]")
+    B, K1, V = target.shape
+    K = K1 - 1
+    _check(target, (B, K + 1, V), (torch.float32, torch.bfloat16), "target")
+    _check(draft, (B, K, V), (target.dtype,), "draft")
+    _check(draft_tokens, (B, K), (torch.int32,), "draft_tokens")
+    _check(uniforms, (B, K + 1, 2), (torch.float32,), "uniforms")
+    dev = target.device
+    if device_status is not None:
+        _check(device_status, (1,), (torch.int32,), "device_status")
+    if workspace is not None and (not isinstance(workspace, torch.Tensor) or not workspace.is_cuda):
+        raise TypeError("workspace must be a CUDA tensor")
+    fs = filters._struct(B, dev, "filters") if filters is not None else None
+    ds = draft_filters._struct(B, dev, "draft_filters") if draft_filters is not None else None
+    st = _stream(dev, stream)
+    with _on(dev, stream) as before:
+        out_tokens, out_accept_len = _outs(B, K, dev, out_tokens, out_accept_len, before)
+        _beside(dev, draft, draft_tokens, uniforms, out_tokens, out_accept_len, workspace, device_status)
+        if workspace is None:
+            workspace = _scratch(spec_filter_workspace_bytes(B, K, V), dev, st)
+    rc = load().spec_verify_filtered(target.data_ptr(), _dt(target), draft.data_ptr(), draft_tokens.data_ptr(),
+                                     uniforms.data_ptr(), B, K, V, ctypes.byref(fs) if fs is not None else None,
+                                     ctypes.byref(ds) if ds is not None else None, out_tokens.data_ptr(),
+                                     out_accept_len.data_ptr(), workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(),
+                                     device_status.data_ptr() if device_status is not None else None, st)
+    if rc:
+        raise SpecVerifyError(rc, "spec_verify_filtered")
+    return out_tokens, out_accept_len
 
 
 def spec_kv_commit(cache: torch.Tensor, staged: torch.Tensor | None, accept_len: torch.Tensor,

@@ -12,6 +12,7 @@
 #include <tuple>
 
 #include "specverify.h"
+#include "sv_filter.cuh"
 #include "sv_launch.h"
 #include "sv_params.h"
 
@@ -179,6 +180,11 @@ spec_status_t quant_cache_check(int NL, int B, int K, int L, int H, int D)
     if ((double)K * 2.0 * H * D > 2147483647.0 || (double)NL * B * (double)sv::kvq_chunks(K, H, D) > 2147483647.0)
         return SPEC_ERR_UNSUPPORTED;
     return SPEC_OK;
+}
+
+sv::FilterSet filter_set(const spec_filters_t *f)
+{
+    return f ? sv::FilterSet{f->temperature, f->top_k, f->top_p, f->min_p} : sv::FilterSet{};
 }
 
 bool attention_sizes_ok(int B, int T, int Hq, int Hkv, int D, int P, int L)
@@ -699,6 +705,80 @@ spec_status_t spec_draft_sample(const void *draft_logits, spec_dtype_t ddt, int 
         return SPEC_ERR_CUDA;
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return SPEC_OK;
+}
+
+spec_status_t spec_filter_sample(const void *logits, spec_dtype_t ldt, const float *uniforms, int B, int K, int V,
+                                 const spec_filters_t *filters, int32_t *out_tokens, float *out_prob,
+                                 int32_t *device_status, void *stream)
+{
+    if (!logits || !uniforms || !out_tokens || B < 1 || K < 1 || V < 1 || (ldt != SPEC_F32 && ldt != SPEC_BF16) ||
+        (long long)B * K > (1LL << 26))
+        return SPEC_ERR_INVALID_ARG;
+    if (V > sv::filter_max_v())
+        return SPEC_ERR_UNSUPPORTED;
+    int sms = 0;
+    if (!device_sms(&sms))
+        return SPEC_ERR_CUDA;
+    sv::FilterParams P{};
+    P.logits = logits;
+    P.uniforms = uniforms;
+    P.f = filter_set(filters);
+    P.out_tokens = out_tokens;
+    P.out_prob = out_prob;
+    P.status = device_status;
+    P.B = B;
+    P.K = K;
+    P.V = V;
+    int launches = 0;
+    const cudaError_t e = sv::launch_filter_sample(P, ldt == SPEC_BF16 ? 1 : 0, sms,
+                                                   static_cast<cudaStream_t>(stream), &launches);
+    g_launches.fetch_add((uint64_t)launches, std::memory_order_relaxed);
+    return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+size_t spec_filter_workspace_bytes(int B, int K, int V)
+{
+    if (B < 1 || K < 1 || K > 31 || V < 1 || V > sv::filter_max_v() || (long long)B * (2 * K + 1) > (1LL << 26))
+        return 0;
+    return sv::filter_workspace(B, K);
+}
+
+spec_status_t spec_verify_filtered(const void *target_logits, spec_dtype_t tdt, const void *draft_logits,
+                                   const int32_t *draft_tokens, const float *uniforms, int B, int K, int V,
+                                   const spec_filters_t *filters, const spec_filters_t *draft_filters,
+                                   int32_t *out_tokens, int32_t *out_accept_len, void *workspace,
+                                   size_t workspace_bytes, int32_t *device_status, void *stream)
+{
+    if (!target_logits || !draft_logits || !draft_tokens || !uniforms || !out_tokens || !out_accept_len ||
+        !workspace || B < 1 || K < 1 || K > 31 || V < 1 || (tdt != SPEC_F32 && tdt != SPEC_BF16) ||
+        (long long)B * (2 * K + 1) > (1LL << 26) || misaligned(workspace))
+        return SPEC_ERR_INVALID_ARG;
+    if (V > sv::filter_max_v())
+        return SPEC_ERR_UNSUPPORTED;
+    if (workspace_bytes < spec_filter_workspace_bytes(B, K, V))
+        return SPEC_ERR_INVALID_ARG;
+    int sms = 0;
+    if (!device_sms(&sms))
+        return SPEC_ERR_CUDA;
+    sv::FilterParams P{};
+    P.logits = target_logits;
+    P.draft = draft_logits;
+    P.tokens = draft_tokens;
+    P.uniforms = uniforms;
+    P.f = filter_set(filters);
+    P.df = filter_set(draft_filters ? draft_filters : filters);
+    P.out_tokens = out_tokens;
+    P.out_len = out_accept_len;
+    P.status = device_status;
+    P.B = B;
+    P.K = K;
+    P.V = V;
+    sv::filter_place(P, workspace);
+    int launches = 0;
+    const cudaError_t e = sv::launch_filter_verify(P, tdt == SPEC_BF16 ? 1 : 0, sms,
+                                                   static_cast<cudaStream_t>(stream), &launches);
+    g_launches.fetch_add((uint64_t)launches, std::memory_order_relaxed);
+    return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 spec_status_t spec_kv_commit(void *cache, const void *staged, int NL, int B, int K, int L, size_t entry_bytes,

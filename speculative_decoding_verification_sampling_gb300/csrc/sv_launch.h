@@ -81,6 +81,15 @@ cudaError_t launch_attention(const AttnParams &P, bool quant, void *workspace, i
 cudaError_t launch_attn_tiles(const AttnParams &A, const AttnWork &W, bool quant, int grid, bool second,
                               uint32_t spin_limit, cudaStream_t stream);
 
+// Filtered rows of logits (k_filter.cu): drawing from them (one launch), and
+// the rule between them (two).
+struct FilterParams;
+int filter_max_v();
+size_t filter_workspace(int B, int K);
+void filter_place(FilterParams &P, void *workspace);   // the arrays in it
+cudaError_t launch_filter_sample(const FilterParams &P, int tdt, int sms, cudaStream_t stream, int *launches);
+cudaError_t launch_filter_verify(const FilterParams &P, int tdt, int sms, cudaStream_t stream, int *launches);
+
 // Greedy tree verification and the tree mask (k_tree.cu).
 int tree_max_nodes();
 cudaError_t launch_tree_walk(const int32_t *tokens, const int32_t *parent, const int32_t *g, int B, int N, int V,
