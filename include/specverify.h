@@ -407,6 +407,25 @@ spec_status_t spec_verify_attention(const void *q, const void *prefix, const uin
                                     int P, int L, float sm_scale, void *out, float *lse, void *workspace,
                                     size_t workspace_bytes, int32_t *device_status, void *stream);
 
+/* The same for a layer whose tokens see a sliding window and a few first tokens
+ * (sinks).  A token's entries, in order, are its sequence's cache entries
+ * [0, seq_len[b]) and those of this pass that mask shows it (without a mask j <= t),
+ * itself included; it sees the first `sinks` and the last `window` of them, and
+ * nothing else is read into its result, whatever it holds.  There is no shared
+ * prefix: the sinks lie in the sequence's own cache.  Of a long cache, only the
+ * entries that some token sees are read, beside up to 127 behind each of the two
+ * stretches.
+ * Arguments, results, errors and roundings are spec_verify_attention's, with the
+ * workspace of spec_attention_workspace_bytes(B, T, Hq, Hkv, D, 0, L); weights of
+ * cache entries that not all of a sequence's tokens see, and of 16 sinks or fewer,
+ * are not rounded.  Limits: window >= 1, sinks >= 0.  Two launches, one more with a
+ * mask (without a cache: one).  Asynchronous on `stream`.                      */
+spec_status_t spec_verify_window_attention(const void *q, const void *cache, const uint8_t *cache_scale, int quant,
+                                           const int32_t *seq_len, const void *staged, const uint8_t *mask, int window,
+                                           int sinks, int B, int T, int Hq, int Hkv, int D, int L, float sm_scale,
+                                           void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                           int32_t *device_status, void *stream);
+
 /* Greedy tree verification (aiengineeringfromscratch.com Phase 10 lesson 25,
  * § Tree attention verification: one target pass over a draft tree under a
  * mask where each token sees only its ancestors; the output is the longest
@@ -461,7 +480,8 @@ spec_status_t spec_philox_words(uint64_t seed, uint32_t tag, int B, int P, uint3
  * inside the statistics stream); spec_draft_sample and spec_philox_words
  * launch one each, spec_kv_commit two (one in place), spec_kv_commit_quant two,
  * spec_kv_read_quant one, spec_verify_attention one to four, spec_filter_sample
- * one, spec_verify_filtered two.  For accounting;
+ * one, spec_verify_filtered two, spec_verify_window_attention one to three.  For
+ * accounting;
  * thread-safe.                                                               */
 uint64_t spec_launch_count(void);
 

@@ -57,3 +57,40 @@ def attention(q, cache, seq_len, staged=None, mask=None, prefix=None, scale=None
                 res["reach"][at] = scale * (x.abs() @ k.abs().T).amax(-1)
                 res["count"][at] = len(k)
     return res
+
+
+def window_attention(q, cache, seq_len, window, sinks=0, staged=None, mask=None, scale=None):
+    """The same where a token sees the first `sinks` and the last `window` of its
+    entries: those of its sequence's cache, then those of the pass that mask shows
+    it (causal without one)."""
+    B, T, Hq, D = q.shape
+    H = cache.shape[3]
+    G = Hq // H
+    scale = D ** -0.5 if scale is None else scale
+    f = dict(dtype=torch.float64, device=q.device)
+    res = {"out": torch.zeros((B, T, Hq, D), **f), "mass": torch.zeros((B, T, Hq, D), **f),
+           "lse": torch.full((B, T, Hq), -math.inf, **f), "reach": torch.zeros((B, T, Hq), **f),
+           "count": torch.zeros((B, T, Hq), **f)}
+    for b in range(B):
+        n = int(seq_len[b])
+        for t in range(T):
+            line = cache[b, :n]
+            if staged is not None:
+                shown = [j for j in range(T) if (mask[b, t, j] != 0 if mask is not None else j <= t)]
+                line = torch.cat([line.double(), staged[b, shown].double()])
+            at = [i for i in range(len(line)) if i < sinks or i >= len(line) - window]
+            if not at:
+                continue
+            kv = line[at].double()
+            for h in range(H):
+                rows = (b, t, slice(h * G, (h + 1) * G))
+                x, k, v = q[rows].double(), kv[:, 0, h], kv[:, 1, h]
+                s = scale * (x @ k.T)
+                z = torch.logsumexp(s, -1)
+                p = torch.exp(s - z[:, None])
+                res["out"][rows] = p @ v
+                res["mass"][rows] = p @ v.abs()
+                res["lse"][rows] = z
+                res["reach"][rows] = scale * (x.abs() @ k.abs().T).amax(-1)
+                res["count"][rows] = len(at)
+    return res

@@ -30,6 +30,7 @@ except ImportError:
 
 __all__ = [
     "SpecVerifyError", "Aux", "Filters", "spec_filter_sample", "spec_verify_filtered", "spec_filter_workspace_bytes",
+    "spec_verify_window_attention",
     "spec_verify", "spec_verify_greedy", "spec_verify_shortlist",
     "spec_workspace_bytes", "spec_philox_words", "spec_draft_sample", "spec_kv_commit", "spec_verify_tree_greedy", "spec_tree_mask",
     "spec_kv_commit_quant", "spec_kv_read_quant", "spec_verify_attention", "spec_attention_workspace_bytes",
@@ -106,6 +107,8 @@ def load():
             lib.spec_attention_workspace_bytes.restype = Z
             lib.spec_verify_attention.argtypes = [P, P, P, P, P, I, P, P, P, I, I, I, I, I, I, I, F, P, P, P, Z, P, P]
             lib.spec_verify_attention.restype = I
+            lib.spec_verify_window_attention.argtypes = [P, P, P, I, P, P, P, I, I, I, I, I, I, I, I, F, P, P, P, Z, P, P]
+            lib.spec_verify_window_attention.restype = I
             lib.spec_draft_sample.argtypes = [P, I, I, I, I, F, U64, P, P, P, P]
             lib.spec_draft_sample.restype = I
             lib.spec_filter_sample.argtypes = [P, I, P, I, I, I, P, P, P, P, P]
@@ -749,6 +752,77 @@ def spec_verify_attention(q: torch.Tensor, cache: torch.Tensor, seq_len: torch.T
                                    workspace.numel() * workspace.element_size(), ptr(device_status), st)
     if rc:
         raise SpecVerifyError(rc, "spec_verify_attention")
+    return out, lse
+
+
+def spec_verify_window_attention(q: torch.Tensor, cache: torch.Tensor, seq_len: torch.Tensor, window: int, *,
+                                 sinks: int = 0, staged: torch.Tensor | None = None,
+                                 mask: torch.Tensor | None = None, cache_scale: torch.Tensor | None = None,
+                                 sm_scale: float | None = None, out=None, lse=None, workspace=None,
+                                 device_status=None, stream=None):
+    """spec_verify_attention for a layer with a sliding window and sinks: q
+    [B][T][Hq][D] bfloat16, cache [B][L][2][Hkv][D] bfloat16, or float8_e4m3fn with
+    cache_scale [B][L][2][Hkv] uint8, staged [B][T][2][Hkv][D] bfloat16 under mask
+    [B][T][T] uint8 or causally.  Of its sequence's entries [0, seq_len[b]) and the
+    pass's that it is shown, in this order, a token sees the first ``sinks`` and the
+    last ``window``, itself included.  Returns (out [B][T][Hq][D] bfloat16, lse
+    [B][T][Hq] float32); a row that sees nothing has 0 and -inf.  No backward pass;
+    workspace and scratch as in spec_verify_attention (P = 0)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise TypeError("q must be a CUDA tensor [B][T][Hq][D]")
+    if not isinstance(cache, torch.Tensor) or cache.dim() != 5:
+        raise TypeError("cache must be a CUDA tensor [B][L][2][Hkv][D]")
+    B, T, Hq, D = q.shape
+    L, H = cache.shape[1], cache.shape[3]
+    dev = q.device
+    quant = cache.dtype == torch.float8_e4m3fn
+    _check(q, (B, T, Hq, D), (torch.bfloat16,), "q")
+    _check(cache, (B, L, 2, H, D), (cache.dtype,) if quant else (torch.bfloat16,), "cache")
+    _check(seq_len, (B,), (torch.int32,), "seq_len")
+    if quant != (cache_scale is not None):
+        raise ValueError("cache_scale goes with a float8_e4m3fn cache")
+    if quant:
+        _check(cache_scale, (B, L, 2, H), (torch.uint8,), "cache_scale")
+    if staged is not None:
+        _check(staged, (B, T, 2, H, D), (torch.bfloat16,), "staged")
+    if mask is not None:
+        _check(mask, (B, T, T), (torch.uint8,), "mask")
+    if out is not None:
+        _check(out, (B, T, Hq, D), (torch.bfloat16,), "out")
+    if lse is not None:
+        _check(lse, (B, T, Hq), (torch.float32,), "lse")
+    if device_status is not None:
+        _check(device_status, (1,), (torch.int32,), "device_status")
+    if workspace is not None and (not isinstance(workspace, torch.Tensor) or not workspace.is_cuda):
+        raise TypeError("workspace must be a CUDA tensor")
+    window, sinks = int(window), int(sinks)
+    if window < 1 or sinks < 0:
+        raise ValueError("window must be at least 1 and sinks at least 0")
+    _beside(dev, cache, seq_len, cache_scale, staged, mask, out, lse, workspace, device_status)
+    nbytes = 0 if workspace is not None else _attention_bytes(B, T, Hq, H, D, 0, L)
+    if workspace is None and nbytes == 0:
+        raise SpecVerifyError(1, "spec_verify_window_attention")
+    st = _stream(dev, stream)
+    lib = load()
+    with _on(dev, stream) as before:
+        if out is None:
+            out = _new((B, T, Hq, D), torch.bfloat16, dev, before)
+        if lse is None:
+            lse = _new((B, T, Hq), torch.float32, dev, before)
+        if workspace is None:
+            workspace = _scratch(nbytes, dev, st)
+
+    def ptr(t):
+        return t.data_ptr() if t is not None else None
+    # past 2^31 a window or sinks are everything
+    rc = lib.spec_verify_window_attention(q.data_ptr(), cache.data_ptr(), ptr(cache_scale), int(quant),
+                                          seq_len.data_ptr(), ptr(staged), ptr(mask), min(window, 2**31 - 1),
+                                          min(sinks, 2**31 - 1), B, T, Hq, H, D, L,
+                                          float(sm_scale) if sm_scale is not None else D ** -0.5, out.data_ptr(),
+                                          lse.data_ptr(), workspace.data_ptr(),
+                                          workspace.numel() * workspace.element_size(), ptr(device_status), st)
+    if rc:
+        raise SpecVerifyError(rc, "spec_verify_window_attention")
     return out, lse
 
 

@@ -918,6 +918,54 @@ spec_status_t spec_verify_attention(const void *q, const void *prefix, const uin
     return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
+spec_status_t spec_verify_window_attention(const void *q, const void *cache, const uint8_t *cache_scale, int quant,
+                                           const int32_t *seq_len, const void *staged, const uint8_t *mask, int window,
+                                           int sinks, int B, int T, int Hq, int Hkv, int D, int L, float sm_scale,
+                                           void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                           int32_t *device_status, void *stream)
+{
+    const size_t need = spec_attention_workspace_bytes(B, T, Hq, Hkv, D, 0, L);
+    if (need == 0 || !q || !seq_len || !out || !workspace || workspace_bytes < need || !std::isfinite(sm_scale) ||
+        sm_scale <= 0.0f || window < 1 || sinks < 0)
+        return SPEC_ERR_INVALID_ARG;
+    // sinks that end inside a unit may make one more of it
+    if (!sv::attention_fits(B, T, Hkv, Hq / Hkv, D, 0, L < 0x7fffffff - 128 ? L + 128 : L))
+        return SPEC_ERR_INVALID_ARG;
+    if ((L > 0 && (!cache || (quant && !cache_scale))) || (mask && !staged))
+        return SPEC_ERR_INVALID_ARG;
+    if (misaligned(q) || misaligned(out) || misaligned(workspace) || (L > 0 && misaligned(cache)) ||
+        (staged && misaligned(staged)))
+        return SPEC_ERR_INVALID_ARG;
+    sv::AttnParams A{};
+    A.q = q;
+    A.cache = cache;
+    A.cscale = quant ? cache_scale : nullptr;
+    A.len = seq_len;
+    A.staged = staged;
+    A.mask = mask;
+    A.out = out;
+    A.lse = lse;
+    A.status = device_status;
+    A.B = B;
+    A.T = T;
+    A.Hq = Hq;
+    A.H = Hkv;
+    A.G = Hq / Hkv;
+    A.D = D;
+    A.L = L;
+    A.c = (float)(1.4426950408889634 * (double)sm_scale);
+    A.window = window;
+    A.sinks = sinks;
+    int launches = 0;
+    int sms = 0;
+    if (!device_sms(&sms))
+        return SPEC_ERR_CUDA;
+    const cudaError_t e = sv::launch_attention(A, quant != 0, workspace, sms, spin_limit(),
+                                               static_cast<cudaStream_t>(stream), &launches);
+    g_launches.fetch_add((uint64_t)launches, std::memory_order_relaxed);
+    return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
 size_t spec_tree_workspace_bytes(int B, int N, int V)
 {
     if (B < 1 || N < 1 || V < 1 || N > sv::tree_max_nodes() || (long long)B * N > (1LL << 30))

@@ -20,6 +20,7 @@
 // for that, so it overlaps the tile kernel's tail), joins the partial results
 // (sums of 2^(m - max) l and 2^(m - max) o) and writes the row.
 #include <cstdint>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -65,6 +66,33 @@ __device__ __forceinline__ f2 pair_of(const RawRow<E> &r, int k)
 {
     return pku(r.w[k] << 16, r.w[k] & 0xffff0000u);
 }
+// The same of a row of e4m3 codes, as bfloat16 (which holds them).
+template <int E>
+__device__ __forceinline__ RawRow<E> load_codes(const uint8_t *p)
+{
+    RawRow<E> r;
+    uint32_t w[E / 4 > 0 ? E / 4 : 1];
+    if constexpr (E >= 8) {
+#pragma unroll
+        for (int k = 0; k < E / 8; ++k) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p + k * 64));
+            w[2 * k] = v.x, w[2 * k + 1] = v.y;
+        }
+    } else if constexpr (E == 4) {
+        w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+    } else {
+        w[0] = __ldg(reinterpret_cast<const uint16_t *>(p));
+    }
+#pragma unroll
+    for (int k = 0; k < E / 2; k += 2) {
+        float x[4];
+        unpack_e4m3(w[k / 2], x);
+        r.w[k] = pack_bf16(x[0], x[1]);
+        if (k + 1 < E / 2)
+            r.w[k + 1] = pack_bf16(x[2], x[3]);
+    }
+    return r;
+}
 // E float32 of a row of a partial result; `step` floats from eight columns to the next eight
 template <int E>
 __device__ __forceinline__ void load_values(const float *p, int step, float (&y)[E])
@@ -96,8 +124,8 @@ __device__ __forceinline__ void load_values(const float *p, int step, float (&y)
 // 16 warps where there are CTAs for a part of the SMs only (131072 entries under
 // 32 rows of one key/value head: 23 us a call, 46 us with four warps), else four
 // (1280 rows: 19 us, 42 us with 16).
-template <int D, int WIDE>
-__global__ void __launch_bounds__(WIDE ? WIDE * 32 : 128, WIDE ? 1 : 7)
+template <int D, int WIDE, int WIN>
+__global__ void __launch_bounds__(WIDE ? WIDE * 32 : 128, WIDE ? 1 : WIN ? 6 : 7)
     va_finish(const __grid_constant__ AttnParams P, const __grid_constant__ AttnWork W, int launches, int per_token)
 {
     constexpr int FW = WIDE ? WIDE : 4;   // warps
@@ -131,7 +159,67 @@ __global__ void __launch_bounds__(WIDE ? WIDE * 32 : 128, WIDE ? 1 : 7)
             o[k] = mul2(o[k], ff);
         return ref;
     };
-    if (P.staged && !bad) {
+    if constexpr (WIN == 0) {
+        if (P.staged && !bad) {
+            f2 q[NP];
+            {
+                const RawRow<E> raw = load_row<E>(static_cast<const uint16_t *>(P.q) + r * D + sub * AT);
+                const f2 cc = pk(P.c, P.c);
+    #pragma unroll
+                for (int k = 0; k < NP; ++k)
+                    q[k] = mul2(pair_of<E>(raw, k), cc);
+            }
+            const uint8_t *mask = P.mask ? P.mask + (size_t)bt * P.T : nullptr;
+            const size_t step = (size_t)2 * P.H * D;
+            const uint16_t *x = static_cast<const uint16_t *>(P.staged) + (size_t)b * P.T * step + (size_t)h * D + sub * AT;
+            const int end = mask ? P.T : t + 1;
+            for (int j0 = 0; j0 < end; j0 += 32) {
+                const int j = j0 + lane;
+                unsigned seen = __ballot_sync(0xffffffffu, j < end && (!mask || __ldg(mask + j)));
+                if constexpr (WIDE != 0)
+                    seen &= (0xffffffffu / ((1u << FW) - 1)) << warp;   // this warp's share
+                while (seen) {
+                    // two visible entries at a time
+                    const int ja = __ffs(seen) - 1;
+                    seen &= seen - 1;
+                    const bool two = seen != 0;
+                    const int jb = two ? __ffs(seen) - 1 : ja;
+                    seen &= seen - 1;
+                    const uint16_t *ea = x + (size_t)(j0 + ja) * step, *eb = x + (size_t)(j0 + jb) * step;
+                    const RawRow<E> ka = load_row<E>(ea), kb = load_row<E>(eb);
+                    const RawRow<E> va = load_row<E>(ea + (size_t)P.H * D), vb = load_row<E>(eb + (size_t)P.H * D);
+                    f2 da = pk(0.0f, 0.0f), db = da;
+    #pragma unroll
+                    for (int k = 0; k < NP; ++k) {
+                        da = fma2(q[k], pair_of<E>(ka, k), da);
+                        db = fma2(q[k], pair_of<E>(kb, k), db);
+                    }
+                    float a0, a1, b0, b1;
+                    upk(da, a0, a1);
+                    upk(db, b0, b1);
+                    float sa = a0 + a1, sb = b0 + b1;
+    #pragma unroll
+                    for (int w = LPR / 2; w; w >>= 1) {
+                        sa += __shfl_xor_sync(0xffffffffu, sa, w);
+                        sb += __shfl_xor_sync(0xffffffffu, sb, w);
+                    }
+                    const float ref = rescale(two ? fmaxf(sa, sb) : sa);
+                    const float pa = ex2a(sa - ref), pb = two ? ex2a(sb - ref) : 0.0f;
+                    l += pa + pb;
+                    const f2 wa = pk(pa, pa), wb = pk(pb, pb);
+    #pragma unroll
+                    for (int k = 0; k < NP; ++k) {
+                        o[k] = fma2(wa, pair_of<E>(va, k), o[k]);
+                        if (two)
+                            o[k] = fma2(wb, pair_of<E>(vb, k), o[k]);
+                    }
+                }
+            }
+        }
+    } else if (!bad) {
+        // entries that the tile kernel leaves to the rows: few sinks, what only some windows reach, and
+        // this pass's own; in this order, each `fk` and `fv` times its key and value
+        const AttnWindow win(P, b);
         f2 q[NP];
         {
             const RawRow<E> raw = load_row<E>(static_cast<const uint16_t *>(P.q) + r * D + sub * AT);
@@ -140,49 +228,102 @@ __global__ void __launch_bounds__(WIDE ? WIDE * 32 : 128, WIDE ? 1 : 7)
             for (int k = 0; k < NP; ++k)
                 q[k] = mul2(pair_of<E>(raw, k), cc);
         }
+        auto attend = [&](const RawRow<E> &ka, const RawRow<E> &va, float fka, float fva, const RawRow<E> &kb,
+                          const RawRow<E> &vb, float fkb, float fvb, bool two) {
+            f2 da = pk(0.0f, 0.0f), db = da;
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                da = fma2(q[k], pair_of<E>(ka, k), da);
+                db = fma2(q[k], pair_of<E>(kb, k), db);
+            }
+            float a0, a1, b0, b1;
+            upk(da, a0, a1);
+            upk(db, b0, b1);
+            float sa = a0 + a1, sb = b0 + b1;
+#pragma unroll
+            for (int w = LPR / 2; w; w >>= 1) {
+                sa += __shfl_xor_sync(0xffffffffu, sa, w);
+                sb += __shfl_xor_sync(0xffffffffu, sb, w);
+            }
+            sa *= fka;
+            sb *= fkb;
+            const float ref = rescale(two ? fmaxf(sa, sb) : sa);
+            const float pa = ex2a(sa - ref), pb = two ? ex2a(sb - ref) : 0.0f;
+            l += pa + pb;
+            const f2 wa = pk(pa * fva, pa * fva), wb = pk(pb * fvb, pb * fvb);
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                o[k] = fma2(wa, pair_of<E>(va, k), o[k]);
+                if (two)
+                    o[k] = fma2(wb, pair_of<E>(vb, k), o[k]);
+            }
+        };
         const uint8_t *mask = P.mask ? P.mask + (size_t)bt * P.T : nullptr;
-        const size_t step = (size_t)2 * P.H * D;
-        const uint16_t *x = static_cast<const uint16_t *>(P.staged) + (size_t)b * P.T * step + (size_t)h * D + sub * AT;
-        const int end = mask ? P.T : t + 1;
-        for (int j0 = 0; j0 < end; j0 += 32) {
-            const int j = j0 + lane;
-            unsigned seen = __ballot_sync(0xffffffffu, j < end && (!mask || __ldg(mask + j)));
-            if constexpr (WIDE != 0)
-                seen &= (0xffffffffu / ((1u << FW) - 1)) << warp;   // this warp's share
-            while (seen) {
-                // two visible entries at a time
-                const int ja = __ffs(seen) - 1;
-                seen &= seen - 1;
-                const bool two = seen != 0;
-                const int jb = two ? __ffs(seen) - 1 : ja;
-                seen &= seen - 1;
-                const uint16_t *ea = x + (size_t)(j0 + ja) * step, *eb = x + (size_t)(j0 + jb) * step;
-                const RawRow<E> ka = load_row<E>(ea), kb = load_row<E>(eb);
-                const RawRow<E> va = load_row<E>(ea + (size_t)P.H * D), vb = load_row<E>(eb + (size_t)P.H * D);
-                f2 da = pk(0.0f, 0.0f), db = da;
-#pragma unroll
-                for (int k = 0; k < NP; ++k) {
-                    da = fma2(q[k], pair_of<E>(ka, k), da);
-                    db = fma2(q[k], pair_of<E>(kb, k), db);
+        // how many entries of this pass the token sees
+        int seen_all = 0;
+        if (P.staged && mask) {
+            for (int j0 = 0; j0 < P.T; j0 += 32)
+                seen_all += __popc(__ballot_sync(0xffffffffu, j0 + lane < P.T && __ldg(mask + j0 + lane)));
+        } else if (P.staged) {
+            seen_all = t + 1;
+        }
+        const int back = P.window - seen_all;   // of the cache's last entries
+        // of the cache: [0, few) and [low, from)
+        const int low = win.from > 0 ? max(P.sinks, win.n - max(min(back, win.n), 0)) : 0;
+        const int some = win.few + max(win.from - low, 0);
+        {
+            const size_t step = (size_t)2 * P.H * D;
+            const uint8_t *scale = P.cscale ? P.cscale + (size_t)b * P.L * 2 * P.H + h : nullptr;
+            const size_t at0 = (size_t)b * P.L * step + (size_t)h * D + sub * AT;
+            auto fetch = [&](int i, RawRow<E> &k, RawRow<E> &v, float &fk, float &fv) {
+                const int e = i < win.few ? i : low + i - win.few;
+                const size_t at = at0 + (size_t)e * step;
+                if (scale) {
+                    const uint8_t *p = static_cast<const uint8_t *>(P.cache) + at;
+                    k = load_codes<E>(p);
+                    v = load_codes<E>(p + (size_t)P.H * D);
+                    fk = fp8_factor(__ldg(scale + (size_t)e * 2 * P.H));
+                    fv = fp8_factor(__ldg(scale + (size_t)e * 2 * P.H + P.H));
+                } else {
+                    const uint16_t *p = static_cast<const uint16_t *>(P.cache) + at;
+                    k = load_row<E>(p);
+                    v = load_row<E>(p + (size_t)P.H * D);
+                    fk = fv = 1.0f;
                 }
-                float a0, a1, b0, b1;
-                upk(da, a0, a1);
-                upk(db, b0, b1);
-                float sa = a0 + a1, sb = b0 + b1;
-#pragma unroll
-                for (int w = LPR / 2; w; w >>= 1) {
-                    sa += __shfl_xor_sync(0xffffffffu, sa, w);
-                    sb += __shfl_xor_sync(0xffffffffu, sb, w);
-                }
-                const float ref = rescale(two ? fmaxf(sa, sb) : sa);
-                const float pa = ex2a(sa - ref), pb = two ? ex2a(sb - ref) : 0.0f;
-                l += pa + pb;
-                const f2 wa = pk(pa, pa), wb = pk(pb, pb);
-#pragma unroll
-                for (int k = 0; k < NP; ++k) {
-                    o[k] = fma2(wa, pair_of<E>(va, k), o[k]);
-                    if (two)
-                        o[k] = fma2(wb, pair_of<E>(vb, k), o[k]);
+            };
+            constexpr int SHARE = WIDE ? FW : 1;
+            for (int i = WIDE ? warp : 0; i < some; i += 2 * SHARE) {
+                RawRow<E> ka, va, kb, vb;
+                float fka, fva, fkb, fvb;
+                const bool two = i + SHARE < some;
+                fetch(i, ka, va, fka, fva);
+                fetch(two ? i + SHARE : i, kb, vb, fkb, fvb);
+                attend(ka, va, fka, fva, kb, vb, fkb, fvb, two);
+            }
+        }
+        if (P.staged) {
+            const size_t step = (size_t)2 * P.H * D;
+            const uint16_t *x = static_cast<const uint16_t *>(P.staged) + (size_t)b * P.T * step + (size_t)h * D + sub * AT;
+            const int end = mask ? P.T : t + 1;
+            int ahead = 0;   // that the token sees, ahead of j0
+            for (int j0 = 0; j0 < end; j0 += 32) {
+                const int j = j0 + lane;
+                unsigned seen = __ballot_sync(0xffffffffu, j < end && (!mask || __ldg(mask + j)));
+                const int rank = ahead + __popc(seen & ((1u << lane) - 1));
+                ahead += __popc(seen);
+                // by its place among all the token's entries
+                seen &= __ballot_sync(0xffffffffu, rank >= seen_all - P.window || win.n < P.sinks - rank);
+                if constexpr (WIDE != 0)
+                    seen &= (0xffffffffu / ((1u << FW) - 1)) << warp;   // this warp's share
+                while (seen) {
+                    const int ja = __ffs(seen) - 1;
+                    seen &= seen - 1;
+                    const bool two = seen != 0;
+                    const int jb = two ? __ffs(seen) - 1 : ja;
+                    seen &= seen - 1;
+                    const uint16_t *ea = x + (size_t)(j0 + ja) * step, *eb = x + (size_t)(j0 + jb) * step;
+                    attend(load_row<E>(ea), load_row<E>(ea + (size_t)P.H * D), 1.0f, 1.0f, load_row<E>(eb),
+                           load_row<E>(eb + (size_t)P.H * D), 1.0f, 1.0f, two);
                 }
             }
         }
@@ -209,9 +350,10 @@ __global__ void __launch_bounds__(WIDE ? WIDE * 32 : 128, WIDE ? 1 : 7)
                 c0 = line0.owner(at);
                 cnt0 = (line0.owner(at + line0.pre.begin(W.pu - 1)) - c0 + 1) << (1 - W.pre.two);
             }
-            if (len > 0) {
+            const int ub = WIN ? AttnWindow(P, b).units() : attn_units(len);
+            if (ub > 0) {
                 const int wide = W.own.tq * (1 + W.own.two), tile = t / wide, in = t - tile * wide;
-                const int ub = attn_units(len), i = h * W.own.tiles + tile;
+                const int i = h * W.own.tiles + tile;
                 const int at = line1.own + HS * line1.sequences(before.x, before.y) + i * line1.own_cost.pair(ub);
                 pair1 = b * HS + i;
                 grp1 = in >= W.own.tq;
@@ -352,7 +494,32 @@ __global__ void __launch_bounds__(WIDE ? WIDE * 32 : 128, WIDE ? 1 : 7)
     }
 }
 
-template <int D, int WIDE>
+// Where a window begins that all tokens of a sequence share, under a mask: the token that sees the most
+// entries of this pass has the shortest one over the cache.  A CTA per sequence.
+__global__ void __launch_bounds__(128) va_window(const __grid_constant__ AttnParams P, int32_t *from)
+{
+    const int b = blockIdx.x, lane = threadIdx.x & 31;
+    __shared__ int most;
+    if (threadIdx.x == 0)
+        most = 0;
+    __syncthreads();
+    for (int t = threadIdx.x / 32; t < P.T; t += 4) {
+        const uint8_t *mask = P.mask + ((size_t)b * P.T + t) * P.T;
+        int seen = 0;
+        for (int j0 = 0; j0 < P.T; j0 += 32)
+            seen += __popc(__ballot_sync(0xffffffffu, j0 + lane < P.T && __ldg(mask + j0 + lane)));
+        if (lane == 0)
+            atomicMax(&most, seen);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int n = __ldg(P.len + b);
+        n = n < 0 || n > P.L ? 0 : n;
+        from[b] = n - max(min(P.window - most, n), 0);
+    }
+}
+
+template <int D, int WIDE, int WIN>
 cudaError_t finish(const AttnParams &P, const AttnWork &W, int launches, cudaStream_t stream)
 {
     constexpr int FW = WIDE ? WIDE : 4;
@@ -366,7 +533,7 @@ cudaError_t finish(const AttnParams &P, const AttnWork &W, int launches, cudaStr
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = launches > 0 ? 1 : 0;   // behind the tile kernel; alone it starts like any other
-    return cudaLaunchKernelEx(&cfg, va_finish<D, WIDE>, P, W, launches, per_token);
+    return cudaLaunchKernelEx(&cfg, va_finish<D, WIDE, WIN>, P, W, launches, per_token);
 }
 
 }  // namespace
@@ -384,7 +551,7 @@ size_t attention_workspace(int B, int T, int H, int G, int D, int P, int L)
     return (a > b ? a : b) + WORK_ALIGN - 16;   // the caller's is 16-byte aligned
 }
 
-cudaError_t launch_attention(const AttnParams &P, bool quant, void *workspace, int sms, uint32_t spin_limit,
+cudaError_t launch_attention(AttnParams P, bool quant, void *workspace, int sms, uint32_t spin_limit,
                              cudaStream_t stream, int *launches)
 {
     *launches = 0;
@@ -407,6 +574,15 @@ cudaError_t launch_attention(const AttnParams &P, bool quant, void *workspace, i
     W.o_p = reinterpret_cast<float *>(w + a.o_p);
     W.ml_s = reinterpret_cast<float2 *>(w + a.ml_s);
     W.o_s = reinterpret_cast<float *>(w + a.o_s);
+    if (P.window > 0 && P.mask && P.L > 0) {
+        int32_t *from = reinterpret_cast<int32_t *>(w + a.from);
+        va_window<<<P.B, 128, 0, stream>>>(P, from);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess)
+            return e;
+        ++*launches;
+        P.from = from;
+    }
     // one CTA per SM, fewer where even full caches have fewer units
     const long long most = sms < AT_MAX_CTAS ? sms : AT_MAX_CTAS;
     int lines = 0;
@@ -457,12 +633,15 @@ cudaError_t launch_attention(const AttnParams &P, bool quant, void *workspace, i
         return e;
     const long long rows = (long long)P.B * P.T * P.Hq;
     const int wide = rows <= WIDER_ROWS ? 16 : rows <= WIDE_ROWS ? 4 : 0;
-    if (P.D == 128)
-        e = wide == 16 ? finish<128, 16>(P, W, lines, stream)
-                       : wide ? finish<128, 4>(P, W, lines, stream) : finish<128, 0>(P, W, lines, stream);
-    else
-        e = wide == 16 ? finish<64, 16>(P, W, lines, stream)
-                       : wide ? finish<64, 4>(P, W, lines, stream) : finish<64, 0>(P, W, lines, stream);
+    auto of = [&](auto win) {
+        constexpr int WIN = decltype(win)::value;
+        if (P.D == 128)
+            return wide == 16 ? finish<128, 16, WIN>(P, W, lines, stream)
+                              : wide ? finish<128, 4, WIN>(P, W, lines, stream) : finish<128, 0, WIN>(P, W, lines, stream);
+        return wide == 16 ? finish<64, 16, WIN>(P, W, lines, stream)
+                          : wide ? finish<64, 4, WIN>(P, W, lines, stream) : finish<64, 0, WIN>(P, W, lines, stream);
+    };
+    e = P.window > 0 ? of(std::integral_constant<int, 1>{}) : of(std::integral_constant<int, 0>{});
     if (e == cudaSuccess)
         ++*launches;
     return e;

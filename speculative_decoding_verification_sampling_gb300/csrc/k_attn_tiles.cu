@@ -58,8 +58,13 @@
 //
 // The last unit of a stretch is ragged: scores past its end become -inf, and
 // V's rows past it are zeroed in shared memory, since 0 * NaN would reach O.
+// With a sliding window (WIN) a sequence's units are those of its sinks, ragged
+// at their end too, and of what every one of its tokens' windows reaches
+// (AttnWindow); for the same reason what only some of them reach is left to the
+// kernel that finishes the rows.
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -286,8 +291,11 @@ struct TileParams {
     uint32_t spin_limit;
 };
 
+template <bool WIN>
 __device__ __forceinline__ int seq_units(const AttnParams &A, int b)
 {
+    if constexpr (WIN)
+        return AttnWindow(A, b).units();
     const int n = __ldg(A.len + b);
     return n < 0 || n > A.L ? 0 : attn_units(n);
 }
@@ -310,16 +318,35 @@ struct Item {
     int copies;      // of the rows in a tile
     bool join;       // both groups' and all copies' results become one
     int slot;
+    int u0, su, sinks, from, end;   // with a window: the stretch's first unit, units of sinks, their entries, the others'
 };
+// The first entry of unit j of an item, and how many of the 128 from there belong to it (or more).
+template <bool WIN>
+__device__ __forceinline__ int unit_first(const Item &it, int j)
+{
+    if constexpr (WIN) {
+        const int u = it.u0 + j;
+        return u < it.su ? u * AT_UNIT : it.from + (u - it.su) * AT_UNIT;
+    }
+    return it.e0 + j * AT_UNIT;
+}
+template <bool WIN>
+__device__ __forceinline__ int unit_valid(const Item &it, int j)
+{
+    if constexpr (WIN)
+        return (it.u0 + j < it.su ? it.sinks : it.end) - unit_first<WIN>(it, j);
+    return it.left - j * AT_UNIT;
+}
 
 // The items of one CTA, in order.  Every role walks them by itself.
+template <bool WIN>
 struct Walk {
     const TileParams &P;
     Place at;
     int units;   // of the pair's stretch
     __device__ Walk(const TileParams &p, const Place &start) : P(p), at(start)
     {
-        units = at.b < 0 ? P.W.pu : at.b < P.A.B ? seq_units(P.A, at.b) : 0;
+        units = at.b < 0 ? P.W.pu : at.b < P.A.B ? seq_units<WIN>(P.A, at.b) : 0;
     }
     __device__ bool next(Item &it)
     {
@@ -327,7 +354,7 @@ struct Walk {
         while (at.pair < at.to) {
 #pragma unroll 1
             while (units == 0)   // sequences without entries
-                units = seq_units(P.A, ++at.b);
+                units = seq_units<WIN>(P.A, ++at.b);
             const bool pre = at.b < 0;
             const AttnCost cost = pre ? at.pre : at.own;
             // the units that begin in this CTA's length
@@ -340,8 +367,17 @@ struct Walk {
             it.two = tl.two;
             it.row0 = pre ? t0 : at.b * P.A.T + t0;
             it.tokens = (pre ? P.A.B * P.A.T : P.A.T) - t0;
-            it.e0 = u0 * AT_UNIT;
-            it.left = (pre ? P.A.P : __ldg(P.A.len + at.b)) - it.e0;
+            if constexpr (WIN) {
+                const AttnWindow w(P.A, at.b);
+                it.u0 = u0;
+                it.su = w.sink_units();
+                it.sinks = w.sinks;
+                it.from = w.from;
+                it.end = w.n;
+            } else {
+                it.e0 = u0 * AT_UNIT;
+                it.left = (pre ? P.A.P : __ldg(P.A.len + at.b)) - it.e0;
+            }
             it.slot = blockIdx.x + ((pre ? 0 : at.b * P.A.H) + at.h) * tl.tiles + at.tile;
             it.n = u1 - u0;
             it.join = tl.join && it.n >= JOIN_UNITS;
@@ -352,7 +388,7 @@ struct Walk {
                 if (++at.h == P.A.H) {
                     at.h = 0;
                     ++at.b;
-                    units = at.b < P.A.B ? seq_units(P.A, at.b) : 0;
+                    units = at.b < P.A.B ? seq_units<WIN>(P.A, at.b) : 0;
                 }
             }
             if (it.n > 0)
@@ -428,7 +464,7 @@ __device__ __forceinline__ bool tile_wait_warp(unsigned long long *bar, uint32_t
 // ------------------------------------------------------------------ roles
 // The loader: one thread.  Q tiles as an item begins, then K and V tiles in
 // the order in which the tensor cores use them.
-template <int D, bool Q8>
+template <int D, bool Q8, bool WIN>
 __device__ void load_role(const TileParams &P, const CUtensorMap *mq_pre, const CUtensorMap *mq_own,
                           const CUtensorMap *m_pre, const CUtensorMap *m_own, TileShared &sh, uint32_t smem,
                           uint32_t limit)
@@ -440,7 +476,7 @@ __device__ void load_role(const TileParams &P, const CUtensorMap *mq_pre, const 
     unsigned long long *const vfull = Q8 ? sh.r_full : sh.v_full, *const vempty = Q8 ? sh.r_empty : sh.v_empty;
     Ring q, k, v;
     int nq = 0, nk = 0, nv = 0;   // copies issued
-    Walk walk(P, sh.start);
+    Walk<WIN> walk(P, sh.start);
     Item it, after;
     bool ok = true, more = walk.next(it), have_q = false;
 #pragma unroll 1
@@ -478,7 +514,7 @@ __device__ void load_role(const TileParams &P, const CUtensorMap *mq_pre, const 
             if (!ok || !(ok = tile_wait(kind ? &vempty[v.slot] : &sh.k_empty[k.slot], ring.phase ^ 1, limit, sh)))
                 break;
             const uint32_t dst = smem + (kind ? V0 + v.slot * VT : C::K0 + k.slot * C::KT);
-            const int e = it.e0 + j * AT_UNIT;
+            const int e = unit_first<WIN>(it, j);
             mbar_arrive_tx(full, VT);
 #pragma unroll 1
             for (int x = 0; x < (Q8 ? 1 : D / 64); ++x) {
@@ -504,7 +540,7 @@ __device__ void load_role(const TileParams &P, const CUtensorMap *mq_pre, const 
 }
 
 // The issuer of every tcgen05.mma: one warp, one elected lane issues.
-template <int D, bool Q8>
+template <int D, bool Q8, bool WIN>
 __device__ void mma_role(const TileParams &P, TileShared &sh, uint8_t *tiles, uint32_t smem, uint32_t limit)
 {
     using C = TileCfg<D, Q8>;
@@ -529,7 +565,7 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint8_t *tiles, ui
             mma_commit(bar);
         rejoin();
     };
-    Walk walk(P, sh.start);
+    Walk<WIN> walk(P, sh.start);
     Item it;
 #pragma unroll 1
     while (ok && walk.next(it)) {
@@ -586,7 +622,7 @@ __device__ void mma_role(const TileParams &P, TileShared &sh, uint8_t *tiles, ui
                 ok = ok && wait(&sh.v_full[vs], vr.phase, limit, sh);
                 vr.next(C::NV);
                 tc_after();
-                const int nv = it.left - j * AT_UNIT;
+                const int nv = unit_valid<WIN>(it, j);
                 if (!Q8 && ok && nv < AT_UNIT) {
                     // V's rows past the stretch (the conversion from 8 bits leaves zeros there by itself)
 #pragma unroll 1
@@ -882,7 +918,7 @@ __device__ __forceinline__ void join_parts(uint8_t *scratch, uint32_t to, int pa
 
 // Softmax of group g: a thread owns a row of the group's tile (a warp reaches
 // only its own quarter of the TMEM lanes).
-template <int D, bool Q8>
+template <int D, bool Q8, bool WIN>
 __device__ void softmax_role(const TileParams &P, QuantShared &sh, uint8_t *tiles, int g, uint32_t limit)
 {
     using C = TileCfg<D, Q8>;
@@ -894,7 +930,7 @@ __device__ void softmax_role(const TileParams &P, QuantShared &sh, uint8_t *tile
     uint32_t sphase = 0, ophase = 0;
     bool ok = true;
     Ring q;
-    Walk walk(P, sh.start);
+    Walk<WIN> walk(P, sh.start);
     Item it;
     if (P.spin_limit < CL_PLAIN_POLLS && sh.start.from < sh.start.to) {
         // the first wait, in that many plain polls: a test's way to giving up
@@ -922,7 +958,7 @@ __device__ void softmax_role(const TileParams &P, QuantShared &sh, uint8_t *tile
         float m = -F_INF, n = FAR_BELOW, l = 0.0f;   // n: with 8-bit entries, l's reference
 #pragma unroll 1
         for (int i = 0; ok && i < cnt; ++i) {
-            const int j = it.two ? i : 2 * i + g, nv = it.left - j * AT_UNIT - col;
+            const int j = it.two ? i : 2 * i + g, nv = unit_valid<WIN>(it, j) - col;
             if (!(ok = tile_wait_warp(&sh.s_full[g], sphase, limit, sh)))
                 break;
             sphase ^= 1;
@@ -1035,21 +1071,23 @@ __device__ __noinline__ uint32_t without_zeros(uint32_t bytes, const uint8_t *co
 
 // 8-bit entries: one warp turns the units' scale bytes into factors, up to FAC
 // units ahead; the bytes of later units are asked into the caches meanwhile.
-template <int D>
+template <int D, bool WIN>
 __device__ __forceinline__ void scale_role(const TileParams &P, QuantShared &sh, uint32_t limit)
 {
     const int lane = threadIdx.x & 31;
     const int stride = 2 * P.A.H;   // bytes from an entry to the next
-    Walk walk(P, sh.start);
+    Walk<WIN> walk(P, sh.start);
     Item it;
     Ring r;
 #pragma unroll 1
     while (walk.next(it)) {
-        const size_t e0 = (it.b < 0 ? 0 : (size_t)it.b * P.A.L) + it.e0;
+        // a window's units do not lie in a row: from the sequence's first entry there
+        const size_t e0 = (it.b < 0 ? 0 : (size_t)it.b * P.A.L) + (WIN ? 0 : it.e0);
         const uint8_t *sc = (it.b < 0 ? P.A.pscale : P.A.cscale) + e0 * stride + it.h;
         // the values' codes of its first entry
         const uint8_t *codes = static_cast<const uint8_t *>(it.b < 0 ? P.A.prefix : P.A.cache) +
                                (e0 * stride + P.A.H + it.h) * D;
+        auto row_of = [&](int j) { return WIN ? unit_first<WIN>(it, j) : j * AT_UNIT; };
         int asked = 0;
 #pragma unroll 1
         for (int j = 0; j < it.n; ++j) {
@@ -1057,15 +1095,15 @@ __device__ __forceinline__ void scale_role(const TileParams &P, QuantShared &sh,
             for (; asked < min(it.n, j + 2 * FAC); ++asked)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (asked * AT_UNIT + i * 32 + lane < it.left)
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(sc + (size_t)(asked * AT_UNIT + i * 32 + lane) * stride));
-            const int nv = it.left - j * AT_UNIT;
+                    if (i * 32 + lane < unit_valid<WIN>(it, asked))
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(sc + (size_t)(row_of(asked) + i * 32 + lane) * stride));
+            const int nv = unit_valid<WIN>(it, j);
             uint32_t kb[4], vb[4], top;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 kb[i] = vb[i] = 0;
                 if (i * 32 + lane < nv) {
-                    const uint8_t *p = sc + (size_t)(j * AT_UNIT + i * 32 + lane) * stride;
+                    const uint8_t *p = sc + (size_t)(row_of(j) + i * 32 + lane) * stride;
                     kb[i] = __ldg(p);
                     vb[i] = __ldg(p + P.A.H);
                 }
@@ -1081,7 +1119,7 @@ __device__ __forceinline__ void scale_role(const TileParams &P, QuantShared &sh,
             largest();
             if (top == 127) {   // heads of zeros do not count
                 const uint32_t left = without_zeros<D>(vb[0] | vb[1] << 8 | vb[2] << 16 | vb[3] << 24,
-                                                       codes + (size_t)(j * AT_UNIT + lane) * stride * D,
+                                                       codes + (size_t)(row_of(j) + lane) * stride * D,
                                                        (size_t)32 * stride * D);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -1113,13 +1151,13 @@ __device__ __forceinline__ void scale_role(const TileParams &P, QuantShared &sh,
 // (four rows of Q at a time, the tail's zeros in a loop): the roles share the
 // instruction cache, and with eight rows of Q at a time and the tail unrolled 64
 // sequences of 9 tokens over 8192 own entries took 312 us where they took 261 us so.
-template <int D>
+template <int D, bool WIN>
 __device__ void convert_role(const TileParams &P, QuantShared &sh, uint8_t *tiles, uint32_t limit)
 {
     using C = TileCfg<D, true>;
     const int lane = threadIdx.x & 31, w = (threadIdx.x / 32) & 3;
     Ring r, s, q;
-    Walk walk(P, sh.start);
+    Walk<WIN> walk(P, sh.start);
     Item it;
     int unit = 0;   // of the CTA, as the item starts
 
@@ -1263,7 +1301,7 @@ __device__ void convert_role(const TileParams &P, QuantShared &sh, uint8_t *tile
                   tile_wait_warp(&sh.v_empty[s.slot], s.phase ^ 1, limit, sh)))
                 return;
             convert(tiles + C::R0 + r.slot * C::RAW, tiles + C::V0 + s.slot * C::TILE, sh.v_fac[fs],
-                    it.left - j * AT_UNIT);
+                    unit_valid<WIN>(it, j));
             async_fence();
             __syncwarp();
             if (lane == 0) {
@@ -1280,7 +1318,7 @@ __device__ void convert_role(const TileParams &P, QuantShared &sh, uint8_t *tile
     }
 }
 
-template <int D, bool Q8>
+template <int D, bool Q8, bool WIN>
 __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
     va_tiles(const __grid_constant__ CUtensorMap mq_pre, const __grid_constant__ CUtensorMap mq_own,
              const __grid_constant__ CUtensorMap m_pre, const __grid_constant__ CUtensorMap m_own,
@@ -1303,7 +1341,7 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
     const int B = P.A.B, run = (B + C::THREADS - 1) / C::THREADS;
     u64 sum = 0;
     for (int b = tid * run; b < min(B, (tid + 1) * run); ++b) {
-        const int u = seq_units(P.A, b);
+        const int u = seq_units<WIN>(P.A, b);
         sum += (u64)u | (u64)(u > 0) << 32;
     }
     u64 upto = sum;   // inclusive scan in the warp
@@ -1370,7 +1408,7 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
         u64 at = before + upto - sum;   // of the sequences before this thread's run
 #pragma unroll 1
         for (int b = tid * run; b < min(B, (tid + 1) * run); ++b) {
-            const int u = seq_units(P.A, b);
+            const int u = seq_units<WIN>(P.A, b);
             if (blockIdx.x == 0 && P.W.base)
                 P.W.base[b] = make_int2((int)at, (int)(at >> 32));
             const int lo = line.own + HS * line.sequences((int)at, (int)(at >> 32)), one = line.own_cost.pair(u);
@@ -1387,19 +1425,19 @@ __global__ void __launch_bounds__(TileCfg<D, Q8>::THREADS, 1)
 
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFT));
-        softmax_role<D, Q8>(P, sh, tiles, warp / 4, limit);
+        softmax_role<D, Q8, WIN>(P, sh, tiles, warp / 4, limit);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_REST));
         if (warp == W_LOAD) {
             if (elect_one())
-                load_role<D, Q8>(P, &mq_pre, &mq_own, &m_pre, &m_own, sh, smem, limit);
+                load_role<D, Q8, WIN>(P, &mq_pre, &mq_own, &m_pre, &m_own, sh, smem, limit);
         } else if (warp == W_MMA) {
             if (!Q8 || elect_one())
-                mma_role<D, Q8>(P, sh, tiles, smem, limit);
+                mma_role<D, Q8, WIN>(P, sh, tiles, smem, limit);
         } else if (Q8 && warp == W_SCALE) {
-            scale_role<D>(P, sh, limit);
+            scale_role<D, WIN>(P, sh, limit);
         } else if (Q8 && warp >= W_CVT) {
-            convert_role<D>(P, sh, tiles, limit);
+            convert_role<D, WIN>(P, sh, tiles, limit);
         }
     }
     __syncwarp();
@@ -1452,7 +1490,7 @@ bool make_map(CUtensorMap *map, bool codes, const void *base, int rank, const cu
                           CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool Q8>
+template <int D, bool Q8, bool WIN>
 cudaError_t launch_tiles(const TileParams &P, int grid, bool second, cudaStream_t stream)
 {
     using C = TileCfg<D, Q8>;
@@ -1484,7 +1522,7 @@ cudaError_t launch_tiles(const TileParams &P, int grid, bool second, cudaStream_
         return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(raised.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(va_tiles<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tile_smem<D, Q8>());
+        e = cudaFuncSetAttribute(va_tiles<D, Q8, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tile_smem<D, Q8>());
         if (e != cudaSuccess)
             return e;
         raised.fetch_or(bit, std::memory_order_relaxed);
@@ -1499,7 +1537,7 @@ cudaError_t launch_tiles(const TileParams &P, int grid, bool second, cudaStream_
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = second ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, va_tiles<D, Q8>, mq_pre, mq_own, m_pre, m_own, P);
+    return cudaLaunchKernelEx(&cfg, va_tiles<D, Q8, WIN>, mq_pre, mq_own, m_pre, m_own, P);
 }
 
 }  // namespace
@@ -1510,9 +1548,15 @@ cudaError_t launch_attn_tiles(const AttnParams &A, const AttnWork &W, bool quant
                               uint32_t spin_limit, cudaStream_t stream)
 {
     TileParams P{A, W, spin_limit};
-    if (A.D == 128)
-        return quant ? launch_tiles<128, true>(P, grid, second, stream) : launch_tiles<128, false>(P, grid, second, stream);
-    return quant ? launch_tiles<64, true>(P, grid, second, stream) : launch_tiles<64, false>(P, grid, second, stream);
+    auto of = [&](auto win) {
+        constexpr bool WIN = decltype(win)::value;
+        if (A.D == 128)
+            return quant ? launch_tiles<128, true, WIN>(P, grid, second, stream)
+                         : launch_tiles<128, false, WIN>(P, grid, second, stream);
+        return quant ? launch_tiles<64, true, WIN>(P, grid, second, stream)
+                     : launch_tiles<64, false, WIN>(P, grid, second, stream);
+    };
+    return A.window > 0 ? of(std::true_type{}) : of(std::false_type{});
 }
 
 }  // namespace sv

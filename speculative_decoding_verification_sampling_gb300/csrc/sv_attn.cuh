@@ -77,6 +77,33 @@ inline AttnTiling attn_tiling(long long tokens, int G, bool quant)
 __host__ __device__ constexpr int attn_units(int n) { return ((n - 1) >> 7) + 1; }
 static_assert(AT_UNIT == 128 && attn_units(0) == 0 && attn_units(128) == 1 && attn_units(0x7fffffff) == 1 << 24, "units");
 
+// A sliding window: of sequence b's cache entries, all its tokens see [0, sinks)
+// and [from, n); what only some of them see, up to T - 1 entries ahead of `from`,
+// the kernel that finishes the rows adds row by row, with their own bounds, and
+// FEW_SINKS sinks or fewer as well, which would take a unit each.  In units, the
+// sinks come first, then the entries from `from` on, wherever that lies, so a
+// window of 128 entries is one unit.
+constexpr int FEW_SINKS = 16;
+struct AttnWindow {
+    int n;      // entries of the sequence (0 where its length is out of range)
+    int from;   // 0: every token sees all of them
+    int sinks;  // in units; the others see to min(sinks, from)
+    int few;    // row by row
+    __device__ __forceinline__ AttnWindow(const AttnParams &A, int b)
+    {
+        n = __ldg(A.len + b);
+        n = n < 0 || n > A.L ? 0 : n;
+        // the last token sees T entries of this pass, itself included
+        const int back = A.window - (A.staged ? A.T : 0);
+        from = A.from ? A.from[b] : n - max(min(back, n), 0);
+        from = from <= A.sinks ? 0 : from;
+        sinks = from > 0 && A.sinks > FEW_SINKS ? A.sinks : 0;
+        few = from > 0 && A.sinks <= FEW_SINKS ? A.sinks : 0;
+    }
+    __device__ __forceinline__ int sink_units() const { return attn_units(sinks); }
+    __device__ __forceinline__ int units() const { return attn_units(sinks) + attn_units(n - from); }
+};
+
 constexpr long long READ_BACK_ROWS = 1024;   // rows per key/value head from which an 8-bit prefix is read back
 
 struct AttnPlan {
@@ -86,7 +113,7 @@ struct AttnPlan {
     int pu;              // units of a prefix pair
     long long max_units, max_line;   // with every sequence at its capacity
     // byte offsets into the workspace
-    size_t base, stat, line, ml_p, o_p, ml_s, o_s, prefix, total;
+    size_t base, stat, line, from, ml_p, o_p, ml_s, o_s, prefix, total;
 };
 
 inline AttnPlan attn_plan(int B, int T, int H, int G, int D, int P, int L, bool quant)
@@ -109,6 +136,7 @@ inline AttnPlan attn_plan(int B, int T, int H, int G, int D, int P, int L, bool 
     a.base = take((size_t)B * 8);
     a.stat = take(2 * AT_MAX_CTAS * 4);
     a.line = take(2 * 64);
+    a.from = take((size_t)B * 4);
     const size_t rp = a.ppairs ? ((size_t)a.ppairs + AT_MAX_CTAS) * 2 * a.pre.tq * G : 0;
     const size_t rs = spairs ? ((size_t)spairs + AT_MAX_CTAS) * 2 * a.own.tq * G : 0;
     a.ml_p = take(rp * 8);

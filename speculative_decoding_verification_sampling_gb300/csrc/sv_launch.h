@@ -76,7 +76,7 @@ cudaError_t launch_kvq_read(KvQuantParams P, bool wide, cudaStream_t stream);
 struct AttnWork;
 bool attention_fits(int B, int T, int H, int G, int D, int P, int L);
 size_t attention_workspace(int B, int T, int H, int G, int D, int P, int L);   // either kind of entries
-cudaError_t launch_attention(const AttnParams &P, bool quant, void *workspace, int sms, uint32_t spin_limit,
+cudaError_t launch_attention(AttnParams P, bool quant, void *workspace, int sms, uint32_t spin_limit,
                              cudaStream_t stream, int *launches);
 cudaError_t launch_attn_tiles(const AttnParams &A, const AttnWork &W, bool quant, int grid, bool second,
                               uint32_t spin_limit, cudaStream_t stream);

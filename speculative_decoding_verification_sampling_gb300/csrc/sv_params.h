@@ -276,6 +276,9 @@ struct AttnParams {
     int32_t *status;            // [1] or nullptr
     int B, T, Hq, H, G, D, P, L;
     float c;                    // scale * log2(e)
+    // a sliding window (0: none): a token sees the first `sinks` and the last `window` of its entries
+    int window, sinks;
+    const int32_t *from;        // [B] the first entry that all tokens' windows reach, or nullptr (no mask)
 };
 
 }  // namespace sv
