@@ -6,18 +6,23 @@
 // with q and p the filtered distributions; sv_filter.cuh states the filters and
 // the arithmetic.
 //
-// A cluster of CTAs takes a row (filter_rows): each CTA copies its part to
-// shared memory, and everything else works on that copy, so HBM is read once.
-//   - The row's maximum, by one exchange.
-//   - T = 0: its first index.
-//   - top-k, k up to a few hundred: a threshold that at least k logits reach
-//     comes from the threads' own maxima (a histogram of one value per thread);
-//     what reaches it, a little more than k tokens, goes to the first CTA's
-//     list, which is ranked there, cut and drawn from.
-//   - otherwise the cut is found by histograms of counts (top-k) or of weights
-//     (top-p) over the whole row: the tokens of the bin that holds the cut are
-//     ranked, or where they are too many (equal logits), sorted into finer bins
-//     of (logit, index) again.
+// A cluster of CTAs takes a row (filter_rows).  The row is read from HBM once,
+// for its maximum; what else is read of it comes from L2, which holds the rows in
+// flight (they are not kept in shared memory: that would leave room for three
+// CTAs to an SM, each waiting for the others of its cluster most of the time).
+//   - T = 0: the maximum's first index.
+//   - top-k, k up to about a thousand, and min-p: a threshold that what is kept
+//     reaches, for top-k from the threads' own maxima (a histogram of one value per
+//     thread: at least k logits reach the k-th of them); what reaches it, a few more
+//     tokens than are kept, goes to the first CTA's list, which is ranked, cut and
+//     drawn from there.
+//   - top-p alone: a histogram of the weights, in bins of 1/64 octave of the
+//     weight.  A bin holds the sum of 1 + q, the weights' ratios to the bin's own,
+//     in fixed point: two additions of 32 bits per token, in any order.  The bin
+//     with the cut goes to the first CTA's list; meanwhile each warp sums up the
+//     weights of its segment above that bin, for the draw.
+//   - what is left (larger k, lists that are too long, as under equal logits): the
+//     cut by histograms of (logit, index) in finer and finer bins.
 // Exchanges go through shared memory of the cluster: each CTA publishes, all
 // read after one cluster barrier, all come to the same answer.
 //
@@ -44,19 +49,10 @@ constexpr int BINS = 2048, BIN_EACH = BINS / FT;
 constexpr int COARSE = 256;             // bins of the threads' maxima, a thread each
 constexpr float RANGE = 64.0f;          // what the bins span: weights to 2^-64 of the largest
 constexpr int ST_INVALID = 1;
+constexpr long long FLIGHT = 56 << 20;  // bytes of the rows in flight
 
 __device__ const FilterTable kFilterTable = filter_table();
 
-struct Vec16 {
-    static __device__ __forceinline__ uint4 load(const void *p)
-    {
-        uint4 v;
-        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "l"(p));
-        return v;
-    }
-};
 __device__ __forceinline__ float max_nan(float a, float b)
 {
     float r;
@@ -68,6 +64,7 @@ __device__ __forceinline__ float max_nan(float a, float b)
 struct RowF32 {
     static constexpr int N = 4, ES = 4;
     static constexpr uint32_t NONE = 0xff800000u;   // words of minus infinity
+    static __device__ __forceinline__ uint4 load(const void *p) { return __ldg(static_cast<const uint4 *>(p)); }
     static __device__ __forceinline__ float get(const uint4 &v, int k)
     {
         return __uint_as_float(k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w);
@@ -85,6 +82,7 @@ struct RowF32 {
 struct RowBF16 {
     static constexpr int N = 8, ES = 2;
     static constexpr uint32_t NONE = 0xff80ff80u;
+    static __device__ __forceinline__ uint4 load(const void *p) { return __ldg(static_cast<const uint4 *>(p)); }
     static __device__ __forceinline__ float get(const uint4 &v, int k)
     {
         const uint32_t w = k < 2 ? v.x : k < 4 ? v.y : k < 6 ? v.z : v.w;
@@ -114,20 +112,32 @@ struct RowBF16 {
     }
 };
 
+constexpr int OCTAVES = 43;               // down to half a unit
+constexpr int FINE = OCTAVES * 64;        // bins of the weights' histogram
+constexpr int LISTS = 16;                 // lists of a row, at most
 struct RowShared {
     u64 slot[2][4][FW];   // published, by round parity: up to four numbers per warp
     u64 sums[FW], sums2[FW];
+    u64 seg[MAX_C * FW];  // the segments' weights
     float2 table[64];
-    uint32_t hist[BINS], hist_hi[BINS];   // counts, or sums in two words
-    u64 key[FILTER_CAP];  // the list: (logit, order) keys,
-    u64 w[FILTER_CAP];    // weights,
-    int32_t x[FILTER_CAP];   // tokens
+    float top[FT];        // the threads' maxima
+    uint32_t coarse[COARSE];
+    uint32_t n[LISTS];    // lengths of lists
     u64 cut, base;
     double least;         // T ln(min_p)
-    float c_hi, c_lo, cut_x;
-    int lo, hi, cut_token;
+    float c_hi, c_lo;
+    int lo, hi;
+    union {
+        struct {
+            uint32_t lo[FINE], hi[FINE];   // counts, or sums in two words
+        } h;
+        struct {
+            u64 key[FILTER_CAP];           // (logit, ~token)
+            u64 w[FILTER_CAP];
+        } l;                               // of the first CTA
+    };
 };
-constexpr size_t ROW_HDR = (sizeof(RowShared) + 127) & ~(size_t)127;
+constexpr size_t ROW_SMEM = sizeof(RowShared);
 
 // ------------------------------------------------------------------ sums
 __device__ __forceinline__ u64 shfl_up64(u64 v, int o)
@@ -169,38 +179,163 @@ __device__ __forceinline__ u64 block_scan64(u64 v, u64 *sums, u64 &total)
     return before + in - v;
 }
 
+// ------------------------------------------------------------------ lists
+// Sorts n keys, largest first.
+__device__ __forceinline__ void sort_keys(u64 *key, int n)
+{
+    int size = 32;
+    while (size < n)
+        size *= 2;
+    for (int i = n + threadIdx.x; i < size; i += FT)
+        key[i] = 0;
+    for (int a = 2; a <= size; a *= 2)
+        for (int b = a / 2; b; b /= 2) {
+            __syncthreads();
+            for (int i = threadIdx.x; i < size / 2; i += FT) {
+                const int lo = 2 * i - (i & (b - 1)), hi = lo + b;
+                const u64 x = key[lo], y = key[hi];
+                if ((x < y) == ((lo & a) == 0)) {
+                    key[lo] = y;
+                    key[hi] = x;
+                }
+            }
+        }
+    __syncthreads();
+}
+// The same for few keys: each thread counts the keys ahead of its own.
+__device__ __forceinline__ void rank_keys(u64 *key, int n)
+{
+    if (n > FT) {
+        sort_keys(key, n);
+        return;
+    }
+    __syncthreads();
+    const u64 mine = (int)threadIdx.x < n ? key[threadIdx.x] : 0;
+    int at = 0;
+    if ((int)(threadIdx.x & ~31u) < n)
+        for (int i = 0; i < n; ++i)
+            at += key[i] > mine;
+    __syncthreads();
+    if ((int)threadIdx.x < n)
+        key[at] = mine;
+    __syncthreads();
+}
+// Of n entries with tokens and weights, in any order: the first, in ascending order of the token, at which the
+// running sum exceeds `at`.  hit(entry, token) is called by one thread.
+template <class F>
+__device__ __forceinline__ void pick(u64 *key, const u64 *w, int n, u64 at, u64 *sums, F hit)
+{
+    // key[i]: ~token in the upper word, i in the lower
+    if (n <= FT) {
+        __syncthreads();
+        if ((int)(threadIdx.x & ~31u) < n) {
+            const int i = min((int)threadIdx.x, n - 1);
+            const u64 mine = key[i];
+            u64 before = 0;
+            for (int j = 0; j < n; ++j)
+                before += key[j] > mine ? w[j] : 0;
+            if ((int)threadIdx.x < n && before <= at && before + w[i] > at)
+                hit(i, (int)(0xffffffffu - (uint32_t)(mine >> 32)));
+        }
+        return;
+    }
+    sort_keys(key, n);
+    constexpr int E = FILTER_CAP / FT;
+    u64 s = 0, all;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int i = threadIdx.x * E + e;
+        s += i < n ? w[(uint32_t)key[i]] : 0;
+    }
+    u64 before = block_scan64(s, sums, all);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int i = threadIdx.x * E + e;
+        if (i < n) {
+            const u64 x = w[(uint32_t)key[i]];
+            if (before <= at && before + x > at)
+                hit((int)(uint32_t)key[i], (int)(0xffffffffu - (uint32_t)(key[i] >> 32)));
+            before += x;
+        }
+    }
+}
+
 // ------------------------------------------------------------------ one row
+__device__ __forceinline__ void cl_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cl_wait_all() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 template <class T>
 struct Row {
+    static constexpr bool SHORT = T::ES == 2;
     RowShared &S;
     cg::cluster_group cl;
-    const uint4 *data;      // this CTA's part
+    const uint8_t *base;    // a 16-byte boundary at or ahead of the row
     int C, rank, lane, warp;
-    int v0, seg0, seg1;     // vectors: of the part, of this warp's segment
-    int off, V;             // tokens ahead of the row in its first vector
-    int len;                // vectors of a segment
-    uint32_t round = 0;
+    int seg0, seg1, len;    // vectors: of this warp's segment, of any
+    int off, V, nv;         // tokens ahead of the row in its first vector; of the row; its vectors
+    bool ragged;
+    uint32_t round = 0, lists = 0;
 
-    __device__ __forceinline__ Row(RowShared &s, const uint4 *d, int nv, int o, int vocab)
-        : S(s), cl(cg::this_cluster()), data(d), C((int)cl_size()), rank((int)cl_rank()), lane(threadIdx.x & 31),
-          warp(threadIdx.x >> 5), off(o), V(vocab)
+    __device__ __forceinline__ Row(RowShared &s, const uint8_t *row, int vocab)
+        : S(s), cl(cg::this_cluster()), C((int)cl_size()), rank((int)cl_rank()), lane(threadIdx.x & 31),
+          warp(threadIdx.x >> 5), V(vocab)
     {
+        off = (int)((reinterpret_cast<uintptr_t>(row) & 15) / T::ES);
+        base = row - off * T::ES;
+        nv = (off + V + T::N - 1) / T::N;
+        ragged = off != 0 || (off + V) % T::N != 0;
         len = ((nv + C * FW - 1) / (C * FW) + 31) & ~31;
-        v0 = min(rank * FW * len, nv);
-        seg0 = min((rank * FW + warp) * len, nv);
+        seg0 = min(segment() * len, nv);
         seg1 = min(seg0 + len, nv);
     }
     __device__ __forceinline__ int segment() const { return rank * FW + warp; }
-    // f(logit, token) for every token of this warp's segment, in any order
-    template <class F>
-    __device__ __forceinline__ void each(F f) const
+    __device__ __forceinline__ int token(int v, int k) const { return v * T::N + k - off; }
+    // Vector v; what is not the row's is minus infinity.
+    __device__ __forceinline__ uint4 vector(int v) const
     {
-        for (int v = seg0 + lane; v < seg1; v += 32) {
-            const uint4 q = data[v - v0];
+        if (ragged && (v == 0 || v == nv - 1)) {
+            float x[T::N];
 #pragma unroll
-            for (int k = 0; k < T::N; ++k)
-                f(T::get(q, k), v * T::N + k - off);
+            for (int k = 0; k < T::N; ++k) {
+                const int i = token(v, k);
+                x[k] = i >= 0 && i < V ? T::one(base, (size_t)(i + off)) : -F_INF;
+            }
+            return T::pack(x);
         }
+        return T::load(base + (size_t)v * 16);
+    }
+    // f(vector, its number) for every vector of vectors a .. b - 1 that falls to this lane of `lanes`, U loads in
+    // flight
+    template <int U, class F>
+    __device__ __forceinline__ void vectors(int a, int b, int lane_, int lanes, F f) const
+    {
+#pragma unroll 1
+        for (int v = a + lane_; v < b; v += lanes * U) {
+            uint4 q[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (v + lanes * u < b)
+                    q[u] = vector(v + lanes * u);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (v + lanes * u < b)
+                    f(q[u], v + lanes * u);
+        }
+    }
+    // f(logit, token) for the tokens of this warp's segment with logits of at least `from` and above minus infinity
+    template <class F>
+    __device__ __forceinline__ void each(float from, F f) const
+    {
+        vectors<4>(seg0, seg1, lane, 32, [&](const uint4 &q, int v) {
+            if (!(T::largest(q) >= from))
+                return;
+#pragma unroll
+            for (int k = 0; k < T::N; ++k) {
+                const float x = T::get(q, k);
+                if (x >= from && x > -F_INF)
+                    f(x, token(v, k));
+            }
+        });
     }
     // Publishes n numbers per warp (the same in every lane) and returns where warp w of CTA r has them.
     struct Board {
@@ -257,93 +392,69 @@ struct Row {
     {
         return (u64)filter_key(x) << 32 | (0xffffffffu - (uint32_t)token);
     }
+    static __device__ __forceinline__ float value_of(u64 key) { return filter_value((uint32_t)(key >> 32)); }
+    static __device__ __forceinline__ int token_of(u64 key) { return (int)(0xffffffffu - (uint32_t)key); }
 
-    // The tokens for which keep(x, token) holds, `n` in all and `before` of them ahead of this warp, go to
-    // the first CTA's list in ascending order.  by_place: the key's low word tells the place in the list.
+    // The tokens with logits of at least `from` for which keep(x, token) holds go to the first CTA's list, in any
+    // order.  Returns how many there are; where these are more than the list holds, they are not all in it.
+    // Ends with an arrival at the cluster's barrier: cl_wait_all is next.
     template <class F>
-    __device__ __forceinline__ void collect(F keep, int before, bool by_place)
+    __device__ __forceinline__ int collect(float from, F keep)
     {
-        u64 *key = cl.map_shared_rank(S.key, 0);
-        int32_t *tok = cl.map_shared_rank(S.x, 0);
-        for (int v = seg0; v < seg1; v += 32) {
-            uint32_t mine = 0;
-            uint4 q = make_uint4(0, 0, 0, 0);
-            if (v + lane < seg1) {
-                q = data[v + lane - v0];
+        u64 *key = cl.map_shared_rank(S.l.key, 0);
+        uint32_t *n = cl.map_shared_rank(&S.n[lists++], 0);
+        uint32_t mine = 0;
+        vectors<4>(seg0, seg1, lane, 32, [&](const uint4 &q, int v) {
+            if (!(T::largest(q) >= from))
+                return;
+            uint32_t has = 0;
 #pragma unroll
-                for (int k = 0; k < T::N; ++k)
-                    mine |= (keep(T::get(q, k), (v + lane) * T::N + k - off) ? 1u : 0u) << k;
+            for (int k = 0; k < T::N; ++k) {
+                const float x = T::get(q, k);
+                has |= (x >= from && x > -F_INF && keep(x, token(v, k)) ? 1u : 0u) << k;
             }
-            if (!__any_sync(0xffffffffu, mine))
-                continue;
-            int cnt = __popc(mine), in = cnt;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, in, o);
-                in += lane >= o ? y : 0;
-            }
-            int at = before + in - cnt;
-            before += __shfl_sync(0xffffffffu, in, 31);
+            if (!has)
+                return;
+            mine += __popc(has);
+            uint32_t at = atomicAdd(n, __popc(has));
 #pragma unroll
             for (int k = 0; k < T::N; ++k)
-                if ((mine >> k & 1) && at < FILTER_CAP) {
-                    const int token = (v + lane) * T::N + k - off;
-                    key[at] = by_place ? (u64)filter_key(T::get(q, k)) << 32 | (0xffffffffu - (uint32_t)at)
-                                       : key_of(T::get(q, k), token);
-                    tok[at] = token;
+                if (has >> k & 1) {
+                    if (at < FILTER_CAP)
+                        key[at] = key_of(T::get(q, k), token(v, k));
                     ++at;
                 }
-        }
-        cl_sync();
-    }
-
-    // The first CTA sorts the n keys of its list, largest first.
-    __device__ __forceinline__ void sort(int n)
-    {
-        int size = 32;
-        while (size < n)
-            size *= 2;
-        for (int i = n + threadIdx.x; i < size; i += FT)
-            S.key[i] = 0;
-        for (int a = 2; a <= size; a *= 2)
-            for (int b = a / 2; b; b /= 2) {
-                __syncthreads();
-                for (int i = threadIdx.x; i < size / 2; i += FT) {
-                    const int lo = 2 * i - (i & (b - 1)), hi = lo + b;
-                    const u64 x = S.key[lo], y = S.key[hi];
-                    if ((x < y) == ((lo & a) == 0)) {
-                        S.key[lo] = y;
-                        S.key[hi] = x;
-                    }
-                }
-            }
-        __syncthreads();
+        });
+        const u64 x[1] = {warp_sum64(mine)};
+        const int all = (int)sum(publish(x), 0);
+        cl_arrive();
+        return all;
     }
 
     // The cut by a count (the first `share` tokens) or by a sum (the tokens ahead of which less than `share` of
     // the whole lies), among the tokens with keys from `floor` on: the key of the last token that stays.
     template <bool SUM>
-    __device__ u64 cut(const FilterWeight &W, double share, u64 floor)
+    __device__ __noinline__ u64 cut(const FilterWeight &W, double share, u64 floor)
     {
-        u64 from = 0, to = ~0ull, base = 0, target = SUM ? 0 : (u64)share;   // keys in question; what lies ahead of them
+        u64 from = 0, to = ~0ull, ahead_ = 0, target = SUM ? 0 : (u64)share;   // keys in question; what lies ahead of them
         int shift = 0;
         const float step = W.c_hi * ((float)BINS / RANGE);
+        lists = SUM ? LISTS - 1 : LISTS - 2;
 #pragma unroll 1
         for (int level = 0; level < 10; ++level) {
+            __syncthreads();
             for (int i = threadIdx.x; i < BINS; i += FT)
-                S.hist[i] = S.hist_hi[i] = 0;
+                S.h.lo[i] = S.h.hi[i] = 0;
             if (threadIdx.x == 0)
                 S.lo = -1;
             __syncthreads();
             auto bin_of = [&](float x, int token) {
-                if (!(x > -F_INF))
-                    return -1;
                 const u64 k = key_of(x, token);
                 if (k < floor || k < from || k > to)
                     return -1;
                 return level ? (int)((to - k) >> shift) : min(BINS - 1, (int)((W.m - x) * step));
             };
-            each([&](float x, int token) {
+            each(-F_INF, [&](float x, int token) {
                 const int b = bin_of(x, token);
                 if (b < 0)
                     return;
@@ -352,11 +463,11 @@ struct Row {
                     if (w == 0)
                         return;
                     const uint32_t lo = (uint32_t)w;
-                    const uint32_t hi = (uint32_t)(w >> 32) + (atomicAdd(&S.hist[b], lo) > ~lo);
+                    const uint32_t hi = (uint32_t)(w >> 32) + (atomicAdd(&S.h.lo[b], lo) > ~lo);
                     if (hi)
-                        atomicAdd(&S.hist_hi[b], hi);
+                        atomicAdd(&S.h.hi[b], hi);
                 } else {
-                    atomicAdd(&S.hist[b], 1u);
+                    atomicAdd(&S.h.lo[b], 1u);
                 }
             });
             __syncthreads();
@@ -367,8 +478,8 @@ struct Row {
             for (int k = 0; k < BIN_EACH; ++k)
                 bins[k] = 0;
             for (int r = 0; r < C; ++r) {
-                const uint32_t *lo = cl.map_shared_rank(S.hist, r) + threadIdx.x * BIN_EACH;
-                const uint32_t *hi = cl.map_shared_rank(S.hist_hi, r) + threadIdx.x * BIN_EACH;
+                const uint32_t *lo = cl.map_shared_rank(S.h.lo, r) + threadIdx.x * BIN_EACH;
+                const uint32_t *hi = cl.map_shared_rank(S.h.hi, r) + threadIdx.x * BIN_EACH;
 #pragma unroll
                 for (int k = 0; k < BIN_EACH; ++k)
                     bins[k] += lo[k] | (SUM ? (u64)hi[k] << 32 : 0);
@@ -376,7 +487,7 @@ struct Row {
 #pragma unroll
             for (int k = 0; k < BIN_EACH; ++k)
                 mine += bins[k];
-            u64 at = base + block_scan64(mine, S.sums, all);
+            u64 at = ahead_ + block_scan64(mine, S.sums, all);
             if (SUM && level == 0)
                 target = max((u64)ceil(share * (double)all), 1ull);   // less than it: the same as less than the share
             if (at < target && at + mine >= target) {
@@ -395,9 +506,9 @@ struct Row {
                 cl_sync();      // the others may still read this CTA's bins
                 return floor;   // there are no more
             }
-            base = S.base;
+            ahead_ = S.base;
             u64 n = 0, least = ~0ull, most = 0;
-            each([&](float x, int token) {
+            each(-F_INF, [&](float x, int token) {
                 if (bin_of(x, token) == bin) {
                     const u64 k = key_of(x, token);
                     ++n;
@@ -414,39 +525,17 @@ struct Row {
             }
             const u64 told[3] = {n, least, most};
             const Board board = publish(told);
-            u64 total;
-            const int before = (int)ahead(board, 0, total);
+            const u64 total = sum(board, 0);
             from = fold(board, 1, ~0ull, [](u64 a, u64 b) { return a < b ? a : b; });
             to = fold(board, 2, 0, [](u64 a, u64 b) { return a > b ? a : b; });
             if (total <= FILTER_CAP) {
-                collect([&](float x, int token) {
+                const int count = collect(value_of(from), [&](float x, int token) {
                     const u64 k = key_of(x, token);
-                    return x > -F_INF && k >= from && k <= to;
-                }, before, false);
-                if (rank == 0) {
-                    const int count = (int)total;
-                    sort(count);
-                    if constexpr (SUM) {
-                        constexpr int E = FILTER_CAP / FT;
-                        u64 w[E], s = 0;
-#pragma unroll
-                        for (int k = 0; k < E; ++k) {
-                            const int i = threadIdx.x * E + k;
-                            w[k] = i < count ? W(filter_value((uint32_t)(S.key[i] >> 32))) : 0;
-                            s += w[k];
-                        }
-                        at = base + block_scan64(s, S.sums, all);
-                        // the token whose weight reaches the target is the last
-#pragma unroll
-                        for (int k = 0; k < E; ++k) {
-                            if (at < target && at + w[k] >= target)
-                                S.cut = S.key[threadIdx.x * E + k];
-                            at += w[k];
-                        }
-                    } else if (threadIdx.x == 0) {
-                        S.cut = S.key[min((int)(target - base), count) - 1];
-                    }
-                }
+                    return k >= from && k <= to;
+                });
+                cl_wait_all();
+                if (rank == 0)
+                    cut_list<SUM>(W, count, ahead_, target);
                 cl_sync();
                 return *cl.map_shared_rank(&S.cut, 0);
             }
@@ -455,64 +544,57 @@ struct Row {
         }
         return from;
     }
+    // The same among the n tokens of this CTA's list, behind `ahead_`: S.cut.
+    template <bool SUM>
+    __device__ __forceinline__ void cut_list(const FilterWeight &W, int n, u64 ahead_, u64 target)
+    {
+        rank_keys(S.l.key, n);
+        if constexpr (SUM) {
+            constexpr int E = FILTER_CAP / FT;
+            u64 w[E], s = 0, all;
+            if (threadIdx.x == 0)
+                S.cut = S.l.key[n - 1];   // where roundings leave the target behind the last
+#pragma unroll
+            for (int k = 0; k < E; ++k) {
+                const int i = threadIdx.x * E + k;
+                w[k] = i < n ? W(value_of(S.l.key[i])) : 0;
+                s += w[k];
+            }
+            u64 at = ahead_ + block_scan64(s, S.sums, all);
+            // the token whose weight reaches the target is the last
+#pragma unroll
+            for (int k = 0; k < E; ++k) {
+                if (at < target && at + w[k] >= target)
+                    S.cut = S.l.key[threadIdx.x * E + k];
+                at += w[k];
+            }
+            __syncthreads();
+        } else {
+            if (threadIdx.x == 0)
+                S.cut = S.l.key[min((int)(target - ahead_), n) - 1];
+            __syncthreads();
+        }
+    }
 
-    // The sum of the weights from `cut` on.
+    // The sum of the weights from `cut` on, of this warp's segment.
     __device__ __forceinline__ u64 mass(const FilterWeight &W, u64 cut) const
     {
-        const float x0 = filter_value((uint32_t)(cut >> 32));
-        const uint32_t last = 0xffffffffu - (uint32_t)cut;
-        u64 s = 0;
-        each([&](float x, int token) {
-            if (cut == 0 || x > x0 || (x == x0 && (uint32_t)token <= last))
-                s += W(x);
+        const float x0 = cut ? value_of(cut) : -F_INF;
+        FilterSum s;
+        each(x0, [&](float x, int token) {
+            if (x > x0 || (uint32_t)token <= (uint32_t)token_of(cut))
+                s.add(W.template pair<SHORT>(x));
         });
-        return warp_sum64(s);
+        return warp_sum64(s.units());
     }
 };
 
-// Copies this CTA's part of a row to shared memory: 16 bytes at a time, the vectors at the row's ends element
-// by element (what is not the row's becomes minus infinity).  Returns the thread's largest logit (NaN if any is).
-template <class T>
-__device__ __forceinline__ float load_part(const Row<T> &R, const void *row, uint4 *data, int nv)
-{
-    const uint8_t *base = reinterpret_cast<const uint8_t *>(row) - R.off * T::ES;   // a 16-byte boundary
-    float top = -F_INF;
-    auto edge = [&](int v) {
-        float x[T::N];
-#pragma unroll
-        for (int k = 0; k < T::N; ++k) {
-            const int i = v * T::N + k - R.off;
-            x[k] = i >= 0 && i < R.V ? T::one(row, i) : -F_INF;
-        }
-        return T::pack(x);
-    };
-    constexpr int FLY = 8;
-    const bool ragged = R.off != 0 || (R.off + R.V) % T::N != 0;
-    for (int v = R.seg0 + R.lane; v < R.seg1; v += 32 * FLY) {
-        uint4 q[FLY];
-#pragma unroll
-        for (int u = 0; u < FLY; ++u) {
-            const int at = v + 32 * u;
-            q[u] = make_uint4(T::NONE, T::NONE, T::NONE, T::NONE);
-            if (at < R.seg1)
-                q[u] = ragged && (at == 0 || at == nv - 1) ? edge(at) : Vec16::load(base + (size_t)at * 16);
-        }
-#pragma unroll
-        for (int u = 0; u < FLY; ++u) {
-            if (v + 32 * u < R.seg1)
-                data[v + 32 * u - R.v0] = q[u];
-            top = max_nan(top, T::largest(q[u]));
-        }
-    }
-    return top;
-}
-
 template <class T, bool VERIFY>
-__global__ void __launch_bounds__(FT) filter_rows(const __grid_constant__ FilterParams P)
+__global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ FilterParams P)
 {
     extern __shared__ __align__(128) uint8_t smem[];
     RowShared &S = *reinterpret_cast<RowShared *>(smem);
-    uint4 *data = reinterpret_cast<uint4 *>(smem + ROW_HDR);
+    using R_ = Row<T>;
     const int row = (int)cl_id(), V = P.V, tid = threadIdx.x;
     const int per = VERIFY ? 2 * P.K + 1 : P.K;
     const int b = row / per, i = row - b * per;
@@ -520,9 +602,7 @@ __global__ void __launch_bounds__(FT) filter_rows(const __grid_constant__ Filter
     const FilterSet &F = draft ? P.df : P.f;
     const uint8_t *src = static_cast<const uint8_t *>(draft ? P.draft : P.logits) +
                          (size_t)(VERIFY ? draft ? b * P.K + i - P.K - 1 : b * (P.K + 1) + i : row) * V * T::ES;
-    const int off = (int)((reinterpret_cast<uintptr_t>(src) & 15) / T::ES);
-    const int nv = (off + V + T::N - 1) / T::N;
-    Row<T> R(S, data, nv, off, V);
+    R_ R(S, src, V);
     const int rank = R.rank;
 
     const float temp = F.T ? __ldg(F.T + b) : 1.0f, p = F.p ? __ldg(F.p + b) : 1.0f;
@@ -536,6 +616,9 @@ __global__ void __launch_bounds__(FT) filter_rows(const __grid_constant__ Filter
 
     if (tid < 64)
         S.table[tid] = kFilterTable.t[tid];
+    else if (tid < 64 + LISTS)
+        S.n[tid - 64] = 0;
+    S.coarse[tid] = 0;
     if (tid == FT - 32) {
         // temperatures beyond 2^-100 and 2^100 count as these
         const double t = fmin(fmax((double)temp, 0x1p-100), 0x1p100), c = 1.4426950408889634 / t;
@@ -543,8 +626,9 @@ __global__ void __launch_bounds__(FT) filter_rows(const __grid_constant__ Filter
         S.c_lo = temp > 0.0f ? (float)(c - (double)S.c_hi) : 0.0f;
         S.least = least > 0.0f ? t * log((double)least) : 0.0;
     }
-    const float mine = load_part<T>(R, src, data, nv);
-    float m = mine;
+    float m = -F_INF;
+    R.template vectors<8>(R.seg0, R.seg1, R.lane, 32, [&](const uint4 &q, int) { m = max_nan(m, T::largest(q)); });
+    S.top[tid] = m;
 #pragma unroll
     for (int o = 16; o; o >>= 1)
         m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -586,10 +670,7 @@ __global__ void __launch_bounds__(FT) filter_rows(const __grid_constant__ Filter
 
     if (temp == 0.0f) {
         u64 first = ~0ull;
-        R.each([&](float x, int token) {
-            if (x == m && (u64)token < first)
-                first = (u64)token;
-        });
+        R.each(m, [&](float, int token) { first = (u64)token < first ? (u64)token : first; });
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
             const u64 a = __shfl_xor_sync(0xffffffffu, first, o);
@@ -609,21 +690,21 @@ __global__ void __launch_bounds__(FT) filter_rows(const __grid_constant__ Filter
 
     const float xmin = least > 0.0f ? __double2float_ru((double)m + S.least) : -F_INF;
     // ---- a threshold that what is kept reaches, for lists
-    const bool few = k <= FILTER_CAP / 4 && k <= 32 * R.C;   // there are 256 C threads' maxima
+    const bool few = k <= FILTER_CAP / 2 && k <= FT / 2 * R.C;
     bool listed = V <= FILTER_CAP;
     float t0 = p < 1.0f ? -F_INF : xmin;   // top-p's total counts what min-p drops
     if (!listed && few) {
-        S.hist[tid] = 0;
-        __syncthreads();
-        if (mine > -F_INF)
-            atomicAdd(&S.hist[min(COARSE - 1, (int)((m - mine) * (W.c_hi * (COARSE / RANGE))))], 1u);
         if (tid == 0)
             S.lo = COARSE - 1;
         __syncthreads();
-        cl_sync();
-        u64 n = 0, all;
-        for (int r = 0; r < R.C; ++r)
-            n += R.cl.map_shared_rank(S.hist, r)[tid];
+        for (int r = 0; r < R.C; ++r) {
+            const float x = R.cl.map_shared_rank(S.top, r)[tid];
+            if (x > -F_INF)
+                atomicAdd(&S.coarse[min(COARSE - 1, (int)((m - x) * (W.c_hi * (COARSE / RANGE))))], 1u);
+        }
+        __syncthreads();
+        const u64 n = S.coarse[tid];
+        u64 all;
         const u64 before = block_scan64(n, S.sums, all);
         if (before < (u64)k && before + n >= (u64)k)
             S.lo = tid;
@@ -637,113 +718,197 @@ __global__ void __launch_bounds__(FT) filter_rows(const __grid_constant__ Filter
         listed = true;
     }
     if (listed) {
-        auto keep = [&](float x, int) { return x >= t0 && x > -F_INF; };
-        u64 n = 0;
-        R.each([&](float x, int token) { n += keep(x, token); });
-        const u64 x[1] = {warp_sum64(n)};
-        const auto board = R.publish(x);
-        u64 total;
-        const int before = (int)R.ahead(board, 0, total);
-        if (total > FILTER_CAP) {
-            listed = false;
-        } else {
-            R.collect(keep, before, true);
-            if (rank != 0)
-                return;   // nothing of this CTA is read any more
-            const int count = (int)total;
-            R.sort(count);
+        const int count = R.collect(t0, [](float, int) { return true; });
+        if (count <= FILTER_CAP) {
+            if (rank != 0) {
+                cl_wait_all();
+                return;
+            }
+            rank_keys(S.l.key, count);
             constexpr int E = FILTER_CAP / FT;
-            u64 w[E], s = 0, ones;
-            int place[E];
-            float xs[E];
+            u64 w[E], s = 0, all;
+#pragma unroll
             for (int e = 0; e < E; ++e) {
                 const int r = tid * E + e;
-                const u64 key = r < count ? S.key[r] : 0;
-                xs[e] = filter_value((uint32_t)(key >> 32));
-                place[e] = (int)(0xffffffffu - (uint32_t)key);
-                w[e] = r < count && r < k ? W(xs[e]) : 0;
+                w[e] = r < count && r < k ? W(R_::value_of(S.l.key[r])) : 0;
                 s += w[e];
             }
-            u64 at = block_scan64(s, S.sums, ones);
+            u64 at = block_scan64(s, S.sums, all);
             // less than p of the total: the same as less than the next whole number
-            const u64 target = p >= 1.0f ? ~0ull : (u64)ceil((double)fmaxf(p, 0.0f) * (double)ones);
+            const u64 target = p >= 1.0f ? ~0ull : (u64)ceil((double)fmaxf(p, 0.0f) * (double)all);
             int stay = 0;
-            bool kept[E];
+            s = 0;
+#pragma unroll
             for (int e = 0; e < E; ++e) {
                 const int r = tid * E + e;
-                kept[e] = r < count && (r == 0 || (r < k && at < target && xs[e] >= xmin));
+                if (r < count && (r == 0 || (r < k && at < target && R_::value_of(S.l.key[r]) >= xmin))) {
+                    ++stay;
+                    s += w[e];
+                }
                 at += w[e];
-                stay += kept[e];
-            }
-            for (int e = 0; e < E; ++e)
-                if (tid * E + e < count)
-                    S.w[place[e]] = kept[e] ? w[e] : 0;
-            // the last kept key's token is the cut
-            const int last = (int)block_scan64(stay, S.sums2, ones) + stay;
-            if (stay > 0 && last == (int)ones)
-                for (int e = 0; e < E; ++e)
-                    if (kept[e] && (e == E - 1 || !kept[e + 1])) {
-                        S.cut_x = xs[e];
-                        S.cut_token = S.x[place[e]];
-                    }
-            __syncthreads();
-            s = 0;
-            for (int e = 0; e < E; ++e) {
-                w[e] = tid * E + e < count ? S.w[tid * E + e] : 0;
-                s += w[e];
+                if (r < count)
+                    S.l.w[r] = w[e];
             }
             u64 Z;
-            u64 upto = block_scan64(s, S.sums, Z);
+            block_scan64(s, S.sums, Z);
+            block_scan64(stay, S.sums2, all);
+            const int n = (int)all;
             if (VERIFY) {
-                rec.cut = S.cut_x;
-                rec.last = (uint32_t)S.cut_token;
-                rec.Z = Z;
-                rec.n = draft ? -1 : 0;
                 if (!draft) {
-                    // tokens of no weight need not be listed
-                    int c = 0;
-                    for (int e = 0; e < E; ++e)
-                        c += w[e] != 0;
-                    u64 kept_all;
-                    int to = (int)block_scan64(c, S.sums2, kept_all);
                     const size_t list = (size_t)(b * (P.K + 1) + i) * FILTER_CAP;
-                    for (int e = 0; e < E; ++e)
-                        if (w[e]) {
-                            P.list_x[list + to] = S.x[tid * E + e];
-                            P.list_w[list + to++] = w[e];
-                        }
-                    rec.n = (int)kept_all;
+                    for (int e = tid; e < n; e += FT) {
+                        P.list_x[list + e] = R_::token_of(S.l.key[e]);
+                        P.list_w[list + e] = S.l.w[e];
+                    }
+                    rec.n = n;
                 }
+                rec.cut = R_::value_of(S.l.key[n - 1]);
+                rec.last = (uint32_t)R_::token_of(S.l.key[n - 1]);
+                rec.Z = Z;
                 if (tid == 0)
                     finish(-1, 0.0f);
             } else {
-                const u64 v = (u64)((double)u * (double)Z);
-                for (int e = 0; e < E; ++e) {
-                    if (w[e] && upto <= v && upto + w[e] > v)
-                        finish(S.x[tid * E + e], (float)((double)w[e] / (double)Z));
-                    upto += w[e];
-                }
+                for (int e = tid; e < n; e += FT)
+                    S.l.key[e] = S.l.key[e] << 32 | (uint32_t)e;
+                pick(S.l.key, S.l.w, n, (u64)((double)u * (double)Z), S.sums, [&](int e, int token) {
+                    finish(token, (float)((double)S.l.w[e] / (double)Z));
+                });
             }
+            __syncthreads();
+            cl_wait_all();
             return;
         }
+        cl_wait_all();
     }
 
-    // ---- the cut by histograms over the row
-    u64 cut = 0;
-    if (k < V)
-        cut = R.template cut<false>(W, (double)k, 0);
-    if (p < 1.0f)
-        cut = R.template cut<true>(W, (double)fmaxf(p, 0.0f), cut);
-    if (least > 0.0f) {
-        const u64 c = (u64)filter_key(xmin) << 32;
+    u64 cut = 0, mine = 0;
+    bool done = false;   // `mine`, the segment's weights, and S.seg are those of `cut`
+    if (p < 1.0f && k == V) {
+        // ---- top-p alone: the weights' histogram
+        for (int e = tid; e < FINE; e += FT)
+            S.h.lo[e] = S.h.hi[e] = 0;
+        __syncthreads();
+        R.each(-F_INF, [&](float x, int) {
+            float q;
+            const int at = -W.template split<R_::SHORT>(x, q);
+            if (at < FINE) {
+                // (1 + q) 2^29, |q| < 0.0055
+                const uint32_t v = (uint32_t)__float_as_int(fmaf(q, 0x1p29f, 12582912.0f)) - 0x4b400000u + 0x20000000u;
+                atomicAdd(&S.h.lo[max(at, 0)], v & 0xffffu);
+                atomicAdd(&S.h.hi[max(at, 0)], v >> 16);
+            }
+        });
+        cl_sync();
+        // this CTA's share of the bins, a thread's in a row
+        const int each = (FINE + R.C * FT - 1) / (R.C * FT), first = (rank * FT + tid) * each;
+        auto weight_of = [&](int bin) -> u64 {
+            if (bin >= FINE)
+                return 0;
+            u64 v = 0;
+            for (int r = 0; r < R.C; ++r)
+                v += R.cl.map_shared_rank(S.h.lo, r)[bin] + ((u64)R.cl.map_shared_rank(S.h.hi, r)[bin] << 16);
+            const float2 e = S.table[-bin & 63];
+            return (u64)__double2ll_rn((double)v * ((double)e.x + (double)e.y) *
+                                       (double)__int_as_float((127 + 43 - 29 + (-bin >> 6)) << 23));
+        };
+        u64 s = 0;
+        for (int e = 0; e < each; ++e)
+            s += weight_of(first + e);
+        const u64 in = warp_scan64(s, R.lane);
+        const u64 x[1] = {__shfl_sync(0xffffffffu, in, 31)};
+        u64 Z;
+        u64 at = R.ahead(R.publish(x), 0, Z) + in - s;
+        const u64 target = max((u64)ceil((double)fmaxf(p, 0.0f) * (double)Z), 1ull);
+        u64 found = 0, ahead = 0;
+        if (at < target && at + s >= target)
+            for (int e = 0; e < each && !found; ++e) {
+                const u64 w = weight_of(first + e);
+                if (at + w >= target)
+                    found = (u64)(first + e) + 1, ahead = at;
+                at += w;
+            }
+        {
+            const unsigned who = __ballot_sync(0xffffffffu, found != 0);
+            const int from = who ? __ffs(who) - 1 : 0;
+            const u64 y[2] = {__shfl_sync(0xffffffffu, found, from), __shfl_sync(0xffffffffu, ahead, from)};
+            const auto board = R.publish(y);
+            auto most = [](u64 a, u64 b) { return a > b ? a : b; };
+            found = R.fold(board, 0, 0, most);
+            ahead = R.fold(board, 1, 0, most);
+        }
+        const int bin = (int)found - 1;
+        if (xmin > -F_INF && -W.place(xmin) < bin) {
+            cut = (u64)filter_key(xmin) << 32;   // min-p cuts ahead of that bin
+        } else {
+            // weights above the bin, by segment; its tokens
+            FilterSum above;
+            // a little below the bin's lower end
+            const float low = m - ((float)bin + 0.51f) * (1.0f / 64.0f) / W.c_hi * 1.00001f - fabsf(m) * 0x1p-21f;
+            const int count = R.collect(low, [&](float y, int) {
+                const int at = -W.place(y);
+                if (at < bin)
+                    above.add(W.template pair<R_::SHORT>(y));
+                return at == bin;
+            });
+            mine = warp_sum64(above.units());
+            cl_wait_all();
+            const u64 y[1] = {mine};
+            const auto board = R.publish(y);
+            if (count <= FILTER_CAP) {
+                if (rank == 0) {
+                    for (int g = tid; g < R.C * FW; g += FT)
+                        S.seg[g] = board.get(0, g);
+                    R.template cut_list<true>(W, count, ahead, target);
+                    u64 c = S.cut;
+                    const u64 c_min = (u64)filter_key(xmin) << 32;
+                    c = c > c_min ? c : c_min;
+                    for (int e = tid; e < count; e += FT) {
+                        const u64 key = S.l.key[e];
+                        if (key >= c)
+                            atomicAdd(&S.seg[((R_::token_of(key) + R.off) / T::N) / R.len], W(R_::value_of(key)));
+                    }
+                    __syncthreads();
+                    if (tid == 0)
+                        S.cut = c;
+                }
+                done = true;
+                cl_sync();
+                cut = *R.cl.map_shared_rank(&S.cut, 0);
+            } else {
+                cut = R.template cut<true>(W, (double)fmaxf(p, 0.0f), 0);
+                const u64 c = (u64)filter_key(xmin) << 32;
+                cut = c > cut ? c : cut;
+            }
+        }
+    } else {
+        // ---- the cut by histograms of (logit, index)
+        if (k < V)
+            cut = R.template cut<false>(W, (double)k, 0);
+        if (p < 1.0f)
+            cut = R.template cut<true>(W, (double)fmaxf(p, 0.0f), cut);
+        const u64 c = least > 0.0f ? (u64)filter_key(xmin) << 32 : 0;
         cut = c > cut ? c : cut;
     }
-    const u64 x[1] = {R.mass(W, cut)};
-    const auto board = R.publish(x);
-    u64 Z;
-    const u64 before = R.ahead(board, 0, Z);
-    rec.cut = cut ? filter_value((uint32_t)(cut >> 32)) : -F_INF;
-    rec.last = 0xffffffffu - (uint32_t)cut;
+    u64 Z, before;
+    if (done) {
+        // the first CTA has the segments' weights
+        u64 all = 0, part = 0;
+        const u64 *seg = R.cl.map_shared_rank(S.seg, 0);
+        for (int g = R.lane; g < R.C * FW; g += 32) {
+            const u64 x = seg[g];
+            all += x;
+            part += g < R.segment() ? x : 0;
+        }
+        Z = warp_sum64(all);
+        before = warp_sum64(part);
+        mine = seg[R.segment()];
+    } else {
+        mine = R.mass(W, cut);
+        const u64 x[1] = {mine};
+        before = R.ahead(R.publish(x), 0, Z);
+    }
+    rec.cut = cut ? R_::value_of(cut) : -F_INF;
+    rec.last = (uint32_t)R_::token_of(cut);
     rec.Z = Z;
     if (VERIFY) {
         if (rank == 0 && tid == 0)
@@ -754,32 +919,46 @@ __global__ void __launch_bounds__(FT) filter_rows(const __grid_constant__ Filter
         if (tid == 0)
             S.hi = 0;
         __syncthreads();
-        if (R.lane == 0 && before <= v && before + x[0] > v) {
+        if (R.lane == 0 && before <= v && before + mine > v) {
             S.hi = 1;
             S.lo = R.warp;
-            S.cut = before;
+            S.base = before;
         }
         __syncthreads();
         if (S.hi) {
-            const int a0 = min((rank * FW + S.lo) * R.len, nv), a1 = min(a0 + R.len, nv);
-            u64 at = S.cut;
-            for (int a = a0; a < a1; a += FT) {
-                u64 w[T::N], s = 0;
-                const bool in = a + tid < a1;
-                const uint4 q = in ? data[a + tid - R.v0] : make_uint4(0, 0, 0, 0);
+            const int a0 = min((rank * FW + S.lo) * R.len, R.nv), a1 = min(a0 + R.len, R.nv);
+            const u64 base = S.base;
+            u64 w[T::N], all;
+            // this thread's weights in the FT vectors from `a` on, `more` in units added to what is kept
+            auto weights = [&](int a, u64 more) {
+                u64 s = 0;
+                const uint4 q = a + tid < a1 ? R.vector(a + tid) : make_uint4(T::NONE, T::NONE, T::NONE, T::NONE);
 #pragma unroll
                 for (int e = 0; e < T::N; ++e) {
                     const float y = T::get(q, e);
-                    const int token = (a + tid) * T::N + e - off;
-                    w[e] = in && (y > rec.cut || (y == rec.cut && (uint32_t)token <= rec.last)) ? W(y) : 0;
+                    const bool in = y > -F_INF && (y > rec.cut || (y == rec.cut && (uint32_t)R.token(a + tid, e) <= rec.last));
+                    w[e] = in ? W(y) + more : 0;
                     s += w[e];
                 }
-                u64 all;
-                u64 upto = at + block_scan64(s, S.sums, all);
+                return s;
+            };
+            u64 sum = 0;
+            for (int a = a0; a < a1; a += FT) {
+                block_scan64(weights(a, 0), S.sums, all);
+                sum += all;
+            }
+            // the segment's sum and its tokens' differ by roundings; tokens of less than a unit
+            // each may sum up to one
+            const u64 more = sum == 0;
+            const u64 to = sum == 0 ? 0 : min(v - base, sum - 1);
+            u64 at = 0;
+            for (int a = a0; a < a1; a += FT) {
+                u64 upto = weights(a, more);
+                upto = at + block_scan64(upto, S.sums, all);
 #pragma unroll
                 for (int e = 0; e < T::N; ++e) {
-                    if (w[e] && upto <= v && upto + w[e] > v)
-                        finish((a + tid) * T::N + e - off, (float)((double)w[e] / (double)Z));
+                    if (w[e] && upto <= to && upto + w[e] > to)
+                        finish(R.token(a + tid, e), (float)((double)w[e] / (double)Z));
                     upto += w[e];
                 }
                 at += all;
@@ -796,6 +975,7 @@ struct DecideShared {
     float2 table[64];
     int j, code, seg;
     u64 before;
+    u64 key[FILTER_CAP], w[FILTER_CAP];
 };
 
 template <class T>
@@ -880,41 +1060,23 @@ __global__ void __launch_bounds__(FT) filter_decide(const __grid_constant__ Filt
     if (q.n >= 0) {
         if (rank != 0)
             return;
-        constexpr int E = FILTER_CAP / FT;
         const size_t list = ((size_t)b * (K + 1) + j) * FILTER_CAP;
-        u64 wq[E], r[E], s = 0, sq = 0;
-        int x[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int i = tid * E + e;
-            wq[e] = r[e] = 0;
-            x[e] = 0;
-            if (i < q.n) {
-                x[e] = P.list_x[list + i];
-                wq[e] = P.list_w[list + i];
-                r[e] = bonus ? wq[e] : left(wq[e], weight(p, Wp, T::one(drf, row_q + x[e]), x[e]));
-            }
-            s += r[e];
-            sq += wq[e];
+        u64 sum = 0, all;
+        for (int e = tid; e < q.n; e += FT) {
+            const int x = P.list_x[list + e];
+            const u64 wq = P.list_w[list + e];
+            S.key[e] = (u64)(0xffffffffu - (uint32_t)x) << 32 | (uint32_t)e;
+            S.w[e] = bonus ? wq : left(wq, weight(p, Wp, T::one(drf, row_q + x), x));
+            sum += S.w[e];
         }
-        u64 all, all_q;
-        u64 upto = block_scan64(s, S.sums, all);
-        const u64 upto_q = block_scan64(sq, S.sums, all_q);
+        block_scan64(sum, S.sums, all);
         if (all == 0) {
             // nothing is left of the target beside the draft: from the target itself
-            upto = upto_q;
-            all = all_q;
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                r[e] = wq[e];
+            for (int e = tid; e < q.n; e += FT)
+                S.w[e] = P.list_w[list + e];
+            all = q.Z;
         }
-        const u64 at = (u64)(v * (double)all);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            if (r[e] && upto <= at && upto + r[e] > at)
-                *out = x[e];
-            upto += r[e];
-        }
+        pick(S.key, S.w, q.n, (u64)(v * (double)all), S.sums, [&](int, int token) { *out = token; });
         return;
     }
     // over the vocabulary: a segment per warp, then the segment on which the uniform falls
@@ -1006,13 +1168,11 @@ cudaError_t rows(const FilterParams &P, int sms, cudaStream_t stream)
 {
     const long long n = (long long)P.B * (VERIFY ? 2 * P.K + 1 : P.K);
     const long long bytes = ((long long)P.V + T::N) * T::ES;
-    // parts of 48 KB at most, so that several CTAs share an SM; smaller ones where there are few rows
+    // four CTAs to an SM: as many rows in flight as L2 holds beside other things, all CTAs busy where
+    // there are few rows, and no part so short that the barriers are all there is
     int C = 1;
-    while (C < MAX_C && (bytes / C > 48 * 1024 || (n * C < 2 * sms && bytes / C > 4096)))
+    while (C < MAX_C && ((4 * sms / C) * bytes > FLIGHT || bytes / C > 65536 * T::ES || (n * C < 4 * sms && bytes / C > 4096)))
         C *= 2;
-    const long long nv = (P.V + T::N - 1) / T::N + 1;
-    const long long part = ((nv + (long long)C * FW - 1) / ((long long)C * FW) + 31) / 32 * 32 * FW;
-    const size_t smem = ROW_HDR + (size_t)part * 16;
     static std::atomic<uint64_t> raised{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1020,14 +1180,12 @@ cudaError_t rows(const FilterParams &P, int sms, cudaStream_t stream)
         return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(raised.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(filter_rows<T, VERIFY>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(filter_rows<T, VERIFY>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        e = cudaFuncSetAttribute(filter_rows<T, VERIFY>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess)
             return e;
         raised.fetch_or(bit, std::memory_order_relaxed);
     }
-    return launch_clusters(filter_rows<T, VERIFY>, n, C, smem, false, stream, P);
+    return launch_clusters(filter_rows<T, VERIFY>, n, C, ROW_SMEM, false, stream, P);
 }
 
 }  // namespace

@@ -46,7 +46,7 @@ struct FilterRow {
 };
 static_assert(sizeof(FilterRow) == 64, "a row's record");
 
-constexpr int FILTER_CAP = 1024;   // tokens of a row that are ranked together, and listed
+constexpr int FILTER_CAP = 2048;   // tokens of a row that are ranked together, and listed
 constexpr int FILTER_MAX_V = 524288;
 
 struct FilterParams {
@@ -59,7 +59,7 @@ struct FilterParams {
     float *out_prob;
     int32_t *status;
     FilterRow *rows;         // verify: [B][2K + 1], target rows first
-    int32_t *list_x;         // verify: [B][K + 1][FILTER_CAP], ascending
+    int32_t *list_x;         // verify: [B][K + 1][FILTER_CAP], in the row's order
     u64 *list_w;
     int B, K, V;
 };
@@ -95,34 +95,76 @@ constexpr float FILTER_UNIT = 8796093022208.0f;   // 2^43
 struct FilterWeight {
     float m, c_hi, c_lo, least;   // `least`: a z - m from which on weights are nothing, 2^-120
     const float2 *table;          // in shared memory
-    __device__ __forceinline__ FilterWeight() = default;
+    FilterWeight() = default;
     __device__ __forceinline__ FilterWeight(float m_, float hi, float lo, const float2 *t)
         : m(m_), c_hi(hi), c_lo(lo), least(hi > 0.0f ? -120.0f / hi : -3e38f), table(t)
     {
     }
-    // 2^((x - m) c) in units.  The exponent is the sum of a multiple of 1/64 and a rest r, |r| <= 1/128,
-    // both exact up to the last bits of r: 2^r - 1 = y + y^2/2 + y^3/6 with y = r ln 2, off by 2^-34.
-    __device__ __forceinline__ u64 operator()(float x) const
+    // 2^((x - m) c) = 2^(i / 64) (1 + q).  The exponent is the sum of a multiple of 1/64 and a rest r,
+    // |r| <= 1/128, both exact up to the last bits of r: 2^r - 1 = y + y^2/2 + y^3/6 with y = r ln 2, off by
+    // 2^-34.
+    static constexpr float ROUND = 196608.0f;   // 1.5 2^17: steps of 1/64
+    // SHORT: logits of 8 bits.  Their difference is exact where they lie within 2^16 of each other; where x is
+    // the smaller one, what is lost is x - (d + m).  (Where m is, 2^-16 of the other logits: 2^-24 of them is lost.)
+    template <bool SHORT>
+    __device__ __forceinline__ int split(float x, float &q) const
     {
         float d = x - m;
-        const float back = d - x;
-        float rest = (x - (d - back)) + (-m - back);   // of the difference; 0 for most bfloat16 logits
-        if (!(d > least)) {
-            d = least;
-            rest = 0.0f;
+        float rest;
+        if constexpr (SHORT) {
+            rest = x - (d + m);
+        } else {
+            const float back = d - x;
+            rest = (x - (d - back)) + (-m - back);
         }
+        rest = d > least ? rest : 0.0f;
+        d = fmaxf(d, least);
         const float zh = __fmul_rn(d, c_hi);   // not to be fused with what follows
         float zl = fmaf(d, c_hi, -zh);
         zl = fmaf(d, c_lo, zl);
         zl = fmaf(rest, c_hi, zl);
-        constexpr float ROUND = 196608.0f;   // 1.5 2^17: steps of 1/64
         const float t = zh + ROUND;
-        const int i = __float_as_int(t) - __float_as_int(ROUND);
         const float r = (zh - (t - ROUND)) + zl;
-        const float q = r * fmaf(r, fmaf(r, 0.055504109f, 0.24022651f), 0.69314718f);
+        q = r * fmaf(r, fmaf(r, 0.055504109f, 0.24022651f), 0.69314718f);
+        return __float_as_int(t) - __float_as_int(ROUND);
+    }
+    // the same i alone
+    __device__ __forceinline__ int place(float x) const
+    {
+        return __float_as_int(__fadd_rn(__fmul_rn(fmaxf(x - m, least), c_hi), ROUND)) - __float_as_int(ROUND);
+    }
+    // as two floats, of which the second is small
+    template <bool SHORT>
+    __device__ __forceinline__ float2 pair(float x) const
+    {
+        float q;
+        const int i = split<SHORT>(x, q);
         const float2 e = table[i & 63];
-        const float s = __int_as_float(((i >> 6) + 127 + 43) << 23);
-        return (u64)(__float2ll_rn(e.x * s) + __float2ll_rn(fmaf(e.x, q, e.y) * s));
+        const float s = __int_as_float(((i >> 6) + 127) << 23);
+        return make_float2(e.x * s, fmaf(e.x, q, e.y) * s);
+    }
+    // in units
+    __device__ __forceinline__ u64 operator()(float x) const
+    {
+        const float2 w = pair<false>(x);
+        return (u64)(__float2ll_rn(w.x * FILTER_UNIT) + __float2ll_rn(w.y * FILTER_UNIT));
+    }
+};
+
+// A thread's sum of weights: the rounding errors of the larger halves go with the smaller ones, so the sum is
+// right to 2^-24 of those.  `s` begins at the largest weight there is.
+struct FilterSum {
+    float s = 1.0f, c = 0.0f;
+    __device__ __forceinline__ void add(float2 w)
+    {
+        const float t = s + w.x;
+        c += (s - t) + w.x;
+        c += w.y;
+        s = t;
+    }
+    __device__ __forceinline__ u64 units() const
+    {
+        return (u64)(__float2ll_rn((s - 1.0f) * FILTER_UNIT) + __float2ll_rn(c * FILTER_UNIT));
     }
 };
 
