@@ -47,7 +47,7 @@ constexpr int FT = 256, FW = FT / 32;   // threads and warps of a CTA
 constexpr int MAX_C = 16;               // CTAs of a cluster
 constexpr int BINS = 2048, BIN_EACH = BINS / FT;
 constexpr int COARSE = 256;             // bins of the threads' maxima, a thread each
-constexpr float RANGE = 64.0f;          // what the bins span: weights to 2^-64 of the largest
+constexpr float RANGE = 64.0f;          // what these span: weights to 2^-64 of the largest
 constexpr int ST_INVALID = 1;
 constexpr long long FLIGHT = 56 << 20;  // bytes of the rows in flight
 
@@ -114,7 +114,8 @@ struct RowBF16 {
 
 constexpr int OCTAVES = 43;               // down to half a unit
 constexpr int FINE = OCTAVES * 64;        // bins of the weights' histogram
-constexpr int LISTS = 16;                 // lists of a row, at most
+constexpr int LISTS = 32;                 // lists of a row, at most: 3, and one for each step of `refine`
+constexpr int RANKED = 1024;              // tokens of a bin that are ranked; more are sorted into finer bins first
 struct RowShared {
     u64 slot[2][4][FW];   // published, by round parity: up to four numbers per warp
     u64 sums[FW], sums2[FW];
@@ -431,17 +432,96 @@ struct Row {
         return all;
     }
 
-    // The cut by a count (the first `share` tokens) or by a sum (the tokens ahead of which less than `share` of
-    // the whole lies), among the tokens with keys from `floor` on: the key of the last token that stays.
+    // Where the head ends that has `share` tokens (SUM = false), or ahead of whose last token less than `share` of
+    // the whole lies, among the tokens with keys from `floor` on: the bin of 1/64 octave that holds its last token,
+    // with what lies ahead of the bin, and the whole (`target`: of which that is to be reached).  -1: there are no
+    // more tokens of any weight.
     template <bool SUM>
-    __device__ __noinline__ u64 cut(const FilterWeight &W, double share, u64 floor)
+    __device__ __forceinline__ int bin_of_cut(const FilterWeight &W, double share, u64 floor, u64 &ahead_, u64 &target)
     {
-        u64 from = 0, to = ~0ull, ahead_ = 0, target = SUM ? 0 : (u64)share;   // keys in question; what lies ahead of them
-        int shift = 0;
-        const float step = W.c_hi * ((float)BINS / RANGE);
-        lists = SUM ? LISTS - 1 : LISTS - 2;
+        __syncthreads();
+        for (int i = threadIdx.x; i < FINE; i += FT) {
+            S.h.lo[i] = 0;
+            if (SUM)
+                S.h.hi[i] = 0;
+        }
+        __syncthreads();
+        const float x0 = floor ? value_of(floor) : -F_INF;
+        const uint32_t last = (uint32_t)token_of(floor);
+        each(x0, [&](float x, int token) {
+            if (!(x > x0 || (uint32_t)token <= last))
+                return;
+            if constexpr (SUM) {
+                float q;
+                const int at = -W.template split<SHORT>(x, q);
+                if (at < FINE) {
+                    // (1 + q) 2^29, |q| < 0.0055
+                    const uint32_t v = (uint32_t)__float_as_int(fmaf(q, 0x1p29f, 12582912.0f)) - 0x4b400000u + 0x20000000u;
+                    atomicAdd(&S.h.lo[at], v & 0xffffu);
+                    atomicAdd(&S.h.hi[at], v >> 16);
+                }
+            } else {
+                const int at = -W.place(x);
+                if (at < FINE)
+                    atomicAdd(&S.h.lo[at], 1u);
+            }
+        });
+        __syncthreads();
+        cl_sync();
+        // this CTA's share of the bins, a thread's in a row
+        const int per = (FINE + C * FT - 1) / (C * FT), first = (rank * FT + threadIdx.x) * per;
+        auto of_bin = [&](int bin) -> u64 {
+            if (bin >= FINE)
+                return 0;
+            u64 v = 0;
+            for (int r = 0; r < C; ++r)
+                v += cl.map_shared_rank(S.h.lo, r)[bin] + (SUM ? (u64)cl.map_shared_rank(S.h.hi, r)[bin] << 16 : 0);
+            if (!SUM)
+                return v;
+            const float2 e = S.table[-bin & 63];
+            return (u64)__double2ll_rn((double)v * ((double)e.x + (double)e.y) *
+                                       (double)__int_as_float((127 + 43 - 29 + (-bin >> 6)) << 23));
+        };
+        u64 s = 0;
+        for (int e = 0; e < per; ++e)
+            s += of_bin(first + e);
+        const u64 in = warp_scan64(s, lane);
+        const u64 x[1] = {__shfl_sync(0xffffffffu, in, 31)};
+        u64 all;
+        u64 at = ahead(publish(x), 0, all) + in - s;
+        target = SUM ? max((u64)ceil(share * (double)all), 1ull) : (u64)share;
+        u64 found = 0, before = 0;
+        if (at < target && at + s >= target)
+            for (int e = 0; e < per && !found; ++e) {
+                const u64 w = of_bin(first + e);
+                if (at + w >= target)
+                    found = (u64)(first + e) + 1, before = at;
+                at += w;
+            }
+        const unsigned who = __ballot_sync(0xffffffffu, found != 0);
+        const int from = who ? __ffs(who) - 1 : 0;
+        const u64 y[2] = {__shfl_sync(0xffffffffu, found, from), __shfl_sync(0xffffffffu, before, from)};
+        const auto board = publish(y);
+        auto most = [](u64 a, u64 b) { return a > b ? a : b; };
+        found = fold(board, 0, 0, most);
+        ahead_ = fold(board, 1, 0, most);
+        return (int)found - 1;
+    }
+    // A logit a little below those of the bin.
+    static __device__ __forceinline__ float below_bin(const FilterWeight &W, int bin)
+    {
+        return W.m - ((float)bin + 0.51f) * (1.0f / 64.0f) / W.c_hi * 1.00001f - fabsf(W.m) * 0x1p-21f;
+    }
+
+    // The key of the head's last token, among those with keys in [from, to], `ahead_` lying ahead of them.
+    template <bool SUM>
+    __device__ __noinline__ u64 refine(const FilterWeight &W, u64 from, u64 to, u64 ahead_, u64 target)
+    {
 #pragma unroll 1
-        for (int level = 0; level < 10; ++level) {
+        for (int level = 0; level < 10; ++level) {   // each takes 11 bits of the keys, of 64
+            const u64 span = to - from;
+            const int shift = max(0, 64 - __clzll((long long)span) - 11);
+            const float low = value_of(from), high = value_of(to);
             __syncthreads();
             for (int i = threadIdx.x; i < BINS; i += FT)
                 S.h.lo[i] = S.h.hi[i] = 0;
@@ -450,18 +530,16 @@ struct Row {
             __syncthreads();
             auto bin_of = [&](float x, int token) {
                 const u64 k = key_of(x, token);
-                if (k < floor || k < from || k > to)
-                    return -1;
-                return level ? (int)((to - k) >> shift) : min(BINS - 1, (int)((W.m - x) * step));
+                return k < from || k > to ? -1 : (int)((to - k) >> shift);
             };
-            each(-F_INF, [&](float x, int token) {
+            each(low, [&](float x, int token) {
+                if (x > high)
+                    return;
                 const int b = bin_of(x, token);
                 if (b < 0)
                     return;
                 if constexpr (SUM) {
                     const u64 w = W(x);
-                    if (w == 0)
-                        return;
                     const uint32_t lo = (uint32_t)w;
                     const uint32_t hi = (uint32_t)(w >> 32) + (atomicAdd(&S.h.lo[b], lo) > ~lo);
                     if (hi)
@@ -488,8 +566,8 @@ struct Row {
             for (int k = 0; k < BIN_EACH; ++k)
                 mine += bins[k];
             u64 at = ahead_ + block_scan64(mine, S.sums, all);
-            if (SUM && level == 0)
-                target = max((u64)ceil(share * (double)all), 1ull);   // less than it: the same as less than the share
+            // roundings may leave the target behind the last
+            target = min(target, ahead_ + all);
             if (at < target && at + mine >= target) {
 #pragma unroll
                 for (int k = 0; k < BIN_EACH; ++k) {
@@ -503,46 +581,43 @@ struct Row {
             __syncthreads();
             const int bin = S.lo;
             if (bin < 0) {
-                cl_sync();      // the others may still read this CTA's bins
-                return floor;   // there are no more
+                cl_sync();     // the others may still read this CTA's bins
+                return from;   // nothing of any weight
             }
             ahead_ = S.base;
-            u64 n = 0, least = ~0ull, most = 0;
-            each(-F_INF, [&](float x, int token) {
-                if (bin_of(x, token) == bin) {
-                    const u64 k = key_of(x, token);
-                    ++n;
-                    least = k < least ? k : least;
-                    most = k > most ? k : most;
-                }
+            u64 least = ~0ull, most = 0;
+            const int count = collect(low, [&](float x, int token) {
+                const u64 k = key_of(x, token);
+                if (k < from || k > to || (int)((to - k) >> shift) != bin)
+                    return false;
+                least = k < least ? k : least;
+                most = k > most ? k : most;
+                return true;
             });
-            n = warp_sum64(n);
-#pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                const u64 a = __shfl_xor_sync(0xffffffffu, least, o), b = __shfl_xor_sync(0xffffffffu, most, o);
-                least = a < least ? a : least;
-                most = b > most ? b : most;
-            }
-            const u64 told[3] = {n, least, most};
-            const Board board = publish(told);
-            const u64 total = sum(board, 0);
-            from = fold(board, 1, ~0ull, [](u64 a, u64 b) { return a < b ? a : b; });
-            to = fold(board, 2, 0, [](u64 a, u64 b) { return a > b ? a : b; });
-            if (total <= FILTER_CAP) {
-                const int count = collect(value_of(from), [&](float x, int token) {
-                    const u64 k = key_of(x, token);
-                    return k >= from && k <= to;
-                });
-                cl_wait_all();
+            cl_wait_all();
+            if (count <= RANKED) {
                 if (rank == 0)
                     cut_list<SUM>(W, count, ahead_, target);
                 cl_sync();
                 return *cl.map_shared_rank(&S.cut, 0);
             }
-            const u64 span = to - from;
-            shift = max(0, 64 - __clzll((long long)span) - 11);
+            limits(least, most, from, to);
         }
         return from;
+    }
+    // The least and the largest key of the cluster's threads'.
+    __device__ __forceinline__ void limits(u64 least, u64 most, u64 &from, u64 &to)
+    {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const u64 a = __shfl_xor_sync(0xffffffffu, least, o), b = __shfl_xor_sync(0xffffffffu, most, o);
+            least = a < least ? a : least;
+            most = b > most ? b : most;
+        }
+        const u64 told[2] = {least, most};
+        const Board board = publish(told);
+        from = fold(board, 0, ~0ull, [](u64 a, u64 b) { return a < b ? a : b; });
+        to = fold(board, 1, 0, [](u64 a, u64 b) { return a > b ? a : b; });
     }
     // The same among the n tokens of this CTA's list, behind `ahead_`: S.cut.
     template <bool SUM>
@@ -781,86 +856,63 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
         cl_wait_all();
     }
 
-    u64 cut = 0, mine = 0;
-    bool done = false;   // `mine`, the segment's weights, and S.seg are those of `cut`
-    if (p < 1.0f && k == V) {
-        // ---- top-p alone: the weights' histogram
-        for (int e = tid; e < FINE; e += FT)
-            S.h.lo[e] = S.h.hi[e] = 0;
-        __syncthreads();
-        R.each(-F_INF, [&](float x, int) {
-            float q;
-            const int at = -W.template split<R_::SHORT>(x, q);
-            if (at < FINE) {
-                // (1 + q) 2^29, |q| < 0.0055
-                const uint32_t v = (uint32_t)__float_as_int(fmaf(q, 0x1p29f, 12582912.0f)) - 0x4b400000u + 0x20000000u;
-                atomicAdd(&S.h.lo[max(at, 0)], v & 0xffffu);
-                atomicAdd(&S.h.hi[max(at, 0)], v >> 16);
+    // ---- the cut by histograms over the row
+    u64 cut = 0, mine = 0, ahead, target;
+    bool done = false;   // S.seg of the first CTA holds the segments' weights
+    if (k < V) {
+        const int bin = R.template bin_of_cut<false>(W, (double)k, 0, ahead, target);
+        if (bin >= 0) {
+            u64 from = ~0ull, to = 0;
+            const int count = R.collect(R_::below_bin(W, bin), [&](float y, int token) {
+                if (-W.place(y) != bin)
+                    return false;
+                const u64 key = R_::key_of(y, token);
+                from = key < from ? key : from;
+                to = key > to ? key : to;
+                return true;
+            });
+            cl_wait_all();
+            if (count <= RANKED) {
+                if (rank == 0)
+                    R.template cut_list<false>(W, count, ahead, target);
+                cl_sync();
+                cut = *R.cl.map_shared_rank(&S.cut, 0);
+            } else {
+                R.limits(from, to, from, to);
+                cut = R.template refine<false>(W, from, to, ahead, target);
             }
-        });
-        cl_sync();
-        // this CTA's share of the bins, a thread's in a row
-        const int each = (FINE + R.C * FT - 1) / (R.C * FT), first = (rank * FT + tid) * each;
-        auto weight_of = [&](int bin) -> u64 {
-            if (bin >= FINE)
-                return 0;
-            u64 v = 0;
-            for (int r = 0; r < R.C; ++r)
-                v += R.cl.map_shared_rank(S.h.lo, r)[bin] + ((u64)R.cl.map_shared_rank(S.h.hi, r)[bin] << 16);
-            const float2 e = S.table[-bin & 63];
-            return (u64)__double2ll_rn((double)v * ((double)e.x + (double)e.y) *
-                                       (double)__int_as_float((127 + 43 - 29 + (-bin >> 6)) << 23));
-        };
-        u64 s = 0;
-        for (int e = 0; e < each; ++e)
-            s += weight_of(first + e);
-        const u64 in = warp_scan64(s, R.lane);
-        const u64 x[1] = {__shfl_sync(0xffffffffu, in, 31)};
-        u64 Z;
-        u64 at = R.ahead(R.publish(x), 0, Z) + in - s;
-        const u64 target = max((u64)ceil((double)fmaxf(p, 0.0f) * (double)Z), 1ull);
-        u64 found = 0, ahead = 0;
-        if (at < target && at + s >= target)
-            for (int e = 0; e < each && !found; ++e) {
-                const u64 w = weight_of(first + e);
-                if (at + w >= target)
-                    found = (u64)(first + e) + 1, ahead = at;
-                at += w;
-            }
-        {
-            const unsigned who = __ballot_sync(0xffffffffu, found != 0);
-            const int from = who ? __ffs(who) - 1 : 0;
-            const u64 y[2] = {__shfl_sync(0xffffffffu, found, from), __shfl_sync(0xffffffffu, ahead, from)};
-            const auto board = R.publish(y);
-            auto most = [](u64 a, u64 b) { return a > b ? a : b; };
-            found = R.fold(board, 0, 0, most);
-            ahead = R.fold(board, 1, 0, most);
         }
-        const int bin = (int)found - 1;
-        if (xmin > -F_INF && -W.place(xmin) < bin) {
-            cut = (u64)filter_key(xmin) << 32;   // min-p cuts ahead of that bin
+    }
+    const u64 c_min = least > 0.0f ? (u64)filter_key(xmin) << 32 : 0;
+    if (p < 1.0f) {
+        const int bin = R.template bin_of_cut<true>(W, (double)fmaxf(p, 0.0f), cut, ahead, target);
+        if (least > 0.0f && -W.place(xmin) < bin) {
+            cut = c_min > cut ? c_min : cut;   // min-p cuts ahead of that bin
         } else {
             // weights above the bin, by segment; its tokens
+            const u64 floor = cut;
             FilterSum above;
-            // a little below the bin's lower end
-            const float low = m - ((float)bin + 0.51f) * (1.0f / 64.0f) / W.c_hi * 1.00001f - fabsf(m) * 0x1p-21f;
-            const int count = R.collect(low, [&](float y, int) {
+            u64 from = ~0ull, to = 0;
+            const int count = R.collect(R_::below_bin(W, bin), [&](float y, int token) {
                 const int at = -W.place(y);
                 if (at < bin)
                     above.add(W.template pair<R_::SHORT>(y));
-                return at == bin;
+                const u64 key = R_::key_of(y, token);
+                if (at != bin || key < floor)
+                    return false;
+                from = key < from ? key : from;
+                to = key > to ? key : to;
+                return true;
             });
-            mine = warp_sum64(above.units());
             cl_wait_all();
-            const u64 y[1] = {mine};
-            const auto board = R.publish(y);
-            if (count <= FILTER_CAP) {
+            if (count <= RANKED) {
+                const u64 y[1] = {warp_sum64(above.units())};
+                const auto board = R.publish(y);
                 if (rank == 0) {
                     for (int g = tid; g < R.C * FW; g += FT)
                         S.seg[g] = board.get(0, g);
                     R.template cut_list<true>(W, count, ahead, target);
                     u64 c = S.cut;
-                    const u64 c_min = (u64)filter_key(xmin) << 32;
                     c = c > c_min ? c : c_min;
                     for (int e = tid; e < count; e += FT) {
                         const u64 key = S.l.key[e];
@@ -875,20 +927,12 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
                 cl_sync();
                 cut = *R.cl.map_shared_rank(&S.cut, 0);
             } else {
-                cut = R.template cut<true>(W, (double)fmaxf(p, 0.0f), 0);
-                const u64 c = (u64)filter_key(xmin) << 32;
-                cut = c > cut ? c : cut;
+                R.limits(from, to, from, to);
+                cut = R.template refine<true>(W, from, to, ahead, target);
             }
         }
-    } else {
-        // ---- the cut by histograms of (logit, index)
-        if (k < V)
-            cut = R.template cut<false>(W, (double)k, 0);
-        if (p < 1.0f)
-            cut = R.template cut<true>(W, (double)fmaxf(p, 0.0f), cut);
-        const u64 c = least > 0.0f ? (u64)filter_key(xmin) << 32 : 0;
-        cut = c > cut ? c : cut;
     }
+    cut = c_min > cut ? c_min : cut;
     u64 Z, before;
     if (done) {
         // the first CTA has the segments' weights
