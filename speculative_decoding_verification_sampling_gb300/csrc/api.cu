@@ -12,7 +12,6 @@
 #include <tuple>
 
 #include "specverify.h"
-#include "sv_filter.cuh"
 #include "sv_launch.h"
 #include "sv_params.h"
 

@@ -29,6 +29,7 @@
 // The verification (filter_decide) reads the rows' records, walks the positions
 // of a sequence in one warp, and draws from (q_j - p_j)+ over the tokens that
 // the target row keeps: from its list, or else over the vocabulary.
+#include <algorithm>
 #include <atomic>
 #include <cooperative_groups.h>
 #include <cstdint>
@@ -45,11 +46,13 @@ namespace cg = cooperative_groups;
 
 constexpr int FT = 256, FW = FT / 32;   // threads and warps of a CTA
 constexpr int MAX_C = 16;               // CTAs of a cluster
-constexpr int BINS = 2048, BIN_EACH = BINS / FT;
 constexpr int COARSE = 256;             // bins of the threads' maxima, a thread each
 constexpr float RANGE = 64.0f;          // what these span: weights to 2^-64 of the largest
 constexpr int ST_INVALID = 1;
-constexpr long long FLIGHT = 56 << 20;  // bytes of the rows in flight
+#ifndef FILTER_FLIGHT
+#define FILTER_FLIGHT 56
+#endif
+constexpr long long FLIGHT = (long long)FILTER_FLIGHT << 20;  // bytes of the rows in flight
 
 __device__ const FilterTable kFilterTable = filter_table();
 
@@ -69,6 +72,7 @@ struct RowF32 {
     {
         return __uint_as_float(k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w);
     }
+    static __device__ __forceinline__ f2 two(const uint4 &v, int k) { return k ? pku(v.z, v.w) : pku(v.x, v.y); }
     static __device__ __forceinline__ float one(const void *p, size_t i) { return __ldg(static_cast<const float *>(p) + i); }
     static __device__ __forceinline__ uint4 pack(const float (&x)[N])
     {
@@ -87,6 +91,11 @@ struct RowBF16 {
     {
         const uint32_t w = k < 2 ? v.x : k < 4 ? v.y : k < 6 ? v.z : v.w;
         return __uint_as_float(k & 1 ? w & 0xffff0000u : w << 16);
+    }
+    static __device__ __forceinline__ f2 two(const uint4 &v, int k)   // the k-th pair
+    {
+        const uint32_t w = k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w;
+        return pku(w << 16, w & 0xffff0000u);
     }
     static __device__ __forceinline__ float one(const void *p, size_t i)
     {
@@ -111,34 +120,6 @@ struct RowBF16 {
         return max_nan(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     }
 };
-
-constexpr int OCTAVES = 43;               // down to half a unit
-constexpr int FINE = OCTAVES * 64;        // bins of the weights' histogram
-constexpr int LISTS = 32;                 // lists of a row, at most: 3, and one for each step of `refine`
-constexpr int RANKED = 1024;              // tokens of a bin that are ranked; more are sorted into finer bins first
-struct RowShared {
-    u64 slot[2][4][FW];   // published, by round parity: up to four numbers per warp
-    u64 sums[FW], sums2[FW];
-    u64 seg[MAX_C * FW];  // the segments' weights
-    float2 table[64];
-    float top[FT];        // the threads' maxima
-    uint32_t coarse[COARSE];
-    uint32_t n[LISTS];    // lengths of lists
-    u64 cut, base;
-    double least;         // T ln(min_p)
-    float c_hi, c_lo;
-    int lo, hi;
-    union {
-        struct {
-            uint32_t lo[FINE], hi[FINE];   // counts, or sums in two words
-        } h;
-        struct {
-            u64 key[FILTER_CAP];           // (logit, ~token)
-            u64 w[FILTER_CAP];
-        } l;                               // of the first CTA
-    };
-};
-constexpr size_t ROW_SMEM = sizeof(RowShared);
 
 // ------------------------------------------------------------------ sums
 __device__ __forceinline__ u64 shfl_up64(u64 v, int o)
@@ -181,35 +162,73 @@ __device__ __forceinline__ u64 block_scan64(u64 v, u64 *sums, u64 &total)
 }
 
 // ------------------------------------------------------------------ lists
-// Sorts n keys, largest first.
-__device__ __forceinline__ void sort_keys(u64 *key, int n)
-{
-    int size = 32;
-    while (size < n)
-        size *= 2;
-    for (int i = n + threadIdx.x; i < size; i += FT)
-        key[i] = 0;
-    for (int a = 2; a <= size; a *= 2)
-        for (int b = a / 2; b; b /= 2) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < size / 2; i += FT) {
-                const int lo = 2 * i - (i & (b - 1)), hi = lo + b;
-                const u64 x = key[lo], y = key[hi];
-                if ((x < y) == ((lo & a) == 0)) {
-                    key[lo] = y;
-                    key[hi] = x;
-                }
-            }
+// 256 bins for a search, a thread each.
+struct Search {
+    uint32_t lo[FT], hi[FT];   // a bin's sum in two words
+    u64 sums[FW], base;
+    int bin;
+    __device__ __forceinline__ void add(int b, u64 w)
+    {
+        const uint32_t l = (uint32_t)w;
+        const uint32_t h = (uint32_t)(w >> 32) + (atomicAdd(&lo[b], l) > ~l);
+        if (h)
+            atomicAdd(&hi[b], h);
+    }
+    // `v`: this thread's bin.  The bin at which the running sum from `ahead` on reaches `target` (which it does;
+    // -1 where there is nothing); `ahead` becomes what lies ahead of it.  No barrier ahead of the return.
+    __device__ __forceinline__ int find(u64 v, u64 &ahead, u64 target)
+    {
+        u64 all;
+        const u64 at = ahead + block_scan64(v, sums, all);
+        target = min(target, ahead + all);   // roundings may leave it behind the last
+        if (threadIdx.x == 0)
+            bin = -1;
+        __syncthreads();
+        if (at < target && at + v >= target) {
+            bin = (int)threadIdx.x;
+            base = at;
         }
-    __syncthreads();
+        __syncthreads();
+        if (bin >= 0)
+            ahead = base;
+        return bin;
+    }
+};
+// How the keys in [from, to] are cut into 256 parts, largest first; the b-th part.
+__device__ __forceinline__ int part_shift(u64 from, u64 to) { return max(0, 56 - __clzll((long long)(to - from))); }
+__device__ __forceinline__ void part(int b, int shift, u64 &from, u64 &to)
+{
+    to -= (u64)b << shift;
+    const u64 len = (1ull << shift) - 1;
+    from = to - from <= len ? from : to - len;
 }
-// The same for few keys: each thread counts the keys ahead of its own.
+// Of n keys of this CTA, all different, with weights (an entry's number to a number): the one, largest first, at
+// which the running sum over the keys in [from, to] reaches `target`, or the last of any weight.
+template <class F>
+__device__ __forceinline__ u64 select_key(const u64 *key, int n, u64 from, u64 to, u64 target, F weight, Search &S)
+{
+    u64 ahead = 0;
+#pragma unroll 1
+    while (from < to) {
+        const int shift = part_shift(from, to);
+        __syncthreads();
+        S.lo[threadIdx.x] = S.hi[threadIdx.x] = 0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < n; i += FT)
+            if (key[i] >= from && key[i] <= to)
+                S.add((int)((to - key[i]) >> shift), weight(i));
+        __syncthreads();
+        const int b = S.find(S.lo[threadIdx.x] | (u64)S.hi[threadIdx.x] << 32, ahead, target);
+        if (b < 0)
+            break;
+        part(b, shift, from, to);
+    }
+    __syncthreads();
+    return from;
+}
+// Sorts n <= FT keys, all different, largest first: each thread counts the keys ahead of its own.
 __device__ __forceinline__ void rank_keys(u64 *key, int n)
 {
-    if (n > FT) {
-        sort_keys(key, n);
-        return;
-    }
     __syncthreads();
     const u64 mine = (int)threadIdx.x < n ? key[threadIdx.x] : 0;
     int at = 0;
@@ -223,12 +242,16 @@ __device__ __forceinline__ void rank_keys(u64 *key, int n)
 }
 // Of n entries with tokens and weights, in any order: the first, in ascending order of the token, at which the
 // running sum exceeds `at`.  hit(entry, token) is called by one thread.
-template <class F>
-__device__ __forceinline__ void pick(u64 *key, const u64 *w, int n, u64 at, u64 *sums, F hit)
+__device__ __forceinline__ u64 pick_key(int token, int entry)
 {
-    // key[i]: ~token in the upper word, i in the lower
+    return (u64)(0xffffffffu - (uint32_t)token) * FILTER_CAP + (uint32_t)entry;
+}
+template <class F>
+__device__ __forceinline__ void pick(const u64 *key, const u64 *w, int n, int V, u64 at, Search &S, F hit)
+{
+    auto is = [&](u64 k) { hit((int)(k % FILTER_CAP), (int)(0xffffffffu - (uint32_t)(k / FILTER_CAP))); };
+    __syncthreads();
     if (n <= FT) {
-        __syncthreads();
         if ((int)(threadIdx.x & ~31u) < n) {
             const int i = min((int)threadIdx.x, n - 1);
             const u64 mine = key[i];
@@ -236,30 +259,43 @@ __device__ __forceinline__ void pick(u64 *key, const u64 *w, int n, u64 at, u64 
             for (int j = 0; j < n; ++j)
                 before += key[j] > mine ? w[j] : 0;
             if ((int)threadIdx.x < n && before <= at && before + w[i] > at)
-                hit(i, (int)(0xffffffffu - (uint32_t)(mine >> 32)));
+                is(mine);
         }
         return;
     }
-    sort_keys(key, n);
-    constexpr int E = FILTER_CAP / FT;
-    u64 s = 0, all;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int i = threadIdx.x * E + e;
-        s += i < n ? w[(uint32_t)key[i]] : 0;
-    }
-    u64 before = block_scan64(s, sums, all);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int i = threadIdx.x * E + e;
-        if (i < n) {
-            const u64 x = w[(uint32_t)key[i]];
-            if (before <= at && before + x > at)
-                hit((int)(uint32_t)key[i], (int)(0xffffffffu - (uint32_t)(key[i] >> 32)));
-            before += x;
-        }
-    }
+    const u64 k = select_key(key, n, pick_key(V, 0), pick_key(0, FILTER_CAP - 1), at + 1, [&](int i) { return w[i]; }, S);
+    if (threadIdx.x == 0)
+        is(k);
 }
+
+constexpr int OCTAVES = 43;               // down to half a unit
+constexpr int FINE = OCTAVES * 64 + 64;   // bins of the weights' histogram
+constexpr int LISTS = 8;                  // lists of a row, at most
+constexpr int RANKED = FT;                // tokens of a bin that are ranked; more are sorted into finer bins first
+struct RowShared {
+    u64 slot[2][4][FW];   // published, by round parity: up to four numbers per warp
+    u64 sums[FW], sums2[FW];
+    u64 seg[MAX_C * FW];  // the segments' weights
+    Search search;
+    float2 table[64];
+    float top[FT];        // the threads' maxima
+    uint32_t coarse[COARSE];
+    uint32_t n[2 * LISTS];   // lengths of lists, and of a CTA's own
+    u64 cut, base;
+    double least;         // T ln(min_p)
+    float c_hi, c_lo;
+    int lo, hi;
+    union {
+        struct {
+            uint32_t lo[FINE], hi[FINE];   // counts, or sums in two words
+        } h;
+        struct {
+            u64 key[FILTER_CAP];           // (logit, ~token)
+            u64 w[FILTER_CAP];
+        } l;                               // of the first CTA
+    };
+};
+constexpr size_t ROW_SMEM = sizeof(RowShared);
 
 // ------------------------------------------------------------------ one row
 __device__ __forceinline__ void cl_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -338,6 +374,25 @@ struct Row {
             }
         });
     }
+    // f(x0, x1, i, j, q, token): pairs of logits of this warp's segment, their split weights, and the first one's
+    // token, from vectors with a logit of at least `from`
+    template <class F>
+    __device__ __forceinline__ void weights(const FilterWeight &W, float from, F f) const
+    {
+        vectors<4>(seg0, seg1, lane, 32, [&](const uint4 &q, int v) {
+            if (!(T::largest(q) >= from))
+                return;
+#pragma unroll
+            for (int k = 0; k < T::N / 2; ++k) {
+                const f2 x = T::two(q, k);
+                float x0, x1;
+                upk(x, x0, x1);
+                uint32_t i, j;
+                const f2 y = W.template split<SHORT>(x, i, j);
+                f(x0, x1, i, j, y, token(v, 2 * k));
+            }
+        });
+    }
     // Publishes n numbers per warp (the same in every lane) and returns where warp w of CTA r has them.
     struct Board {
         u64 *at;
@@ -362,14 +417,22 @@ struct Row {
     // A number per warp: their sum ahead of this warp's, and in all
     __device__ __forceinline__ u64 ahead(const Board &b, int i, u64 &total) const
     {
-        u64 all = 0, mine = 0;
-        for (int s = lane; s < C * FW; s += 32) {
-            const u64 x = b.get(i, s);
-            all += x;
-            mine += s < segment() ? x : 0;
+        u64 x[MAX_C * FW / 32], all = 0, mine = 0;
+        read(b, i, x);
+#pragma unroll
+        for (int k = 0; k < MAX_C * FW / 32; ++k) {
+            all += x[k];
+            mine += lane + 32 * k < segment() ? x[k] : 0;
         }
         total = warp_sum64(all);
         return warp_sum64(mine);
+    }
+    // This lane's part of the numbers of all warps, 0 where there are no more: all loads in flight at once
+    __device__ __forceinline__ void read(const Board &b, int i, u64 (&x)[MAX_C * FW / 32]) const
+    {
+#pragma unroll
+        for (int k = 0; k < MAX_C * FW / 32; ++k)
+            x[k] = lane + 32 * k < C * FW ? b.get(i, lane + 32 * k) : 0;
     }
     __device__ __forceinline__ u64 sum(const Board &b, int i) const
     {
@@ -377,16 +440,39 @@ struct Row {
         ahead(b, i, total);
         return total;
     }
+    // f associative, 0 its neutral element
     template <class F>
-    __device__ __forceinline__ u64 fold(const Board &b, int i, u64 start, F f) const
+    __device__ __forceinline__ u64 fold(const Board &b, int i, F f) const
     {
-        u64 x = start;
-        for (int s = lane; s < C * FW; s += 32)
-            x = f(x, b.get(i, s));
+        u64 x[MAX_C * FW / 32];
+        read(b, i, x);
+        u64 y = x[0];
+#pragma unroll
+        for (int k = 1; k < MAX_C * FW / 32; ++k)
+            y = f(y, x[k]);
 #pragma unroll
         for (int o = 16; o; o >>= 1)
-            x = f(x, (u64)__shfl_xor_sync(0xffffffffu, x, o));
-        return x;
+            y = f(y, (u64)__shfl_xor_sync(0xffffffffu, y, o));
+        return y;
+    }
+    __device__ __forceinline__ u64 most(const Board &b, int i) const
+    {
+        return fold(b, i, [](u64 a, u64 c) { return a > c ? a : c; });
+    }
+    // The sum over the cluster's CTAs of what lies at `p` in their shared memory, eight loads in flight
+    __device__ __forceinline__ u64 of_all(const uint32_t *p) const
+    {
+        u64 v = 0;
+        for (int r = 0; r < C; r += 8) {
+            uint32_t x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                x[k] = r + k < C ? *cl.map_shared_rank(const_cast<uint32_t *>(p), r + k) : 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v += x[k];
+        }
+        return v;
     }
 
     static __device__ __forceinline__ u64 key_of(float x, int token)
@@ -396,15 +482,12 @@ struct Row {
     static __device__ __forceinline__ float value_of(u64 key) { return filter_value((uint32_t)(key >> 32)); }
     static __device__ __forceinline__ int token_of(u64 key) { return (int)(0xffffffffu - (uint32_t)key); }
 
-    // The tokens with logits of at least `from` for which keep(x, token) holds go to the first CTA's list, in any
-    // order.  Returns how many there are; where these are more than the list holds, they are not all in it.
-    // Ends with an arrival at the cluster's barrier: cl_wait_all is next.
+    // The tokens with logits of at least `from` for which keep(x, token) holds go to this CTA's list, in any order.
+    // Returns how many there are; where these are more than the list holds, they are not all in it.
     template <class F>
-    __device__ __forceinline__ int collect(float from, F keep)
+    __device__ __forceinline__ int stage(float from, F keep)
     {
-        u64 *key = cl.map_shared_rank(S.l.key, 0);
-        uint32_t *n = cl.map_shared_rank(&S.n[lists++], 0);
-        uint32_t mine = 0;
+        uint32_t *const n = &S.n[LISTS + lists];
         vectors<4>(seg0, seg1, lane, 32, [&](const uint4 &q, int v) {
             if (!(T::largest(q) >= from))
                 return;
@@ -416,17 +499,41 @@ struct Row {
             }
             if (!has)
                 return;
-            mine += __popc(has);
             uint32_t at = atomicAdd(n, __popc(has));
 #pragma unroll
             for (int k = 0; k < T::N; ++k)
                 if (has >> k & 1) {
                     if (at < FILTER_CAP)
-                        key[at] = key_of(T::get(q, k), token(v, k));
+                        S.l.w[at] = key_of(T::get(q, k), token(v, k));
                     ++at;
                 }
         });
-        const u64 x[1] = {warp_sum64(mine)};
+        ++lists;
+        __syncthreads();
+        return (int)*n;
+    }
+    // The keys in [from, to] of this CTA's list of n, `some` of them, go to the first CTA's list, in any order (one
+    // remote atomic per CTA: it takes about 50 ns, and all meet at one place).  Returns how many there are; where
+    // these are more than the list holds, they are not all in it.  Ends with an arrival at the cluster's barrier:
+    // cl_wait_all is next.
+    __device__ __forceinline__ int send(int n, int some, u64 from, u64 to)
+    {
+        if (threadIdx.x == 0) {
+            S.hi = (int)atomicAdd(cl.map_shared_rank(&S.n[lists - 1], 0), (uint32_t)some);
+            S.lo = 0;
+        }
+        __syncthreads();
+        const int at = S.hi;
+        u64 *key = cl.map_shared_rank(S.l.key, 0);
+        for (int i = threadIdx.x; i < n && i < FILTER_CAP; i += FT) {
+            const u64 k = S.l.w[i];
+            if (k < from || k > to)
+                continue;
+            const int j = at + (some == n ? i : atomicAdd(&S.lo, 1));
+            if (j < FILTER_CAP)
+                key[j] = k;
+        }
+        const u64 x[1] = {warp == 0 ? (u64)some : 0};
         const int all = (int)sum(publish(x), 0);
         cl_arrive();
         return all;
@@ -446,26 +553,31 @@ struct Row {
                 S.h.hi[i] = 0;
         }
         __syncthreads();
-        const float x0 = floor ? value_of(floor) : -F_INF;
-        const uint32_t last = (uint32_t)token_of(floor);
-        each(x0, [&](float x, int token) {
-            if (!(x > x0 || (uint32_t)token <= last))
-                return;
-            if constexpr (SUM) {
-                float q;
-                const int at = -W.template split<SHORT>(x, q);
-                if (at < FINE) {
-                    // (1 + q) 2^29, |q| < 0.0055
-                    const uint32_t v = (uint32_t)__float_as_int(fmaf(q, 0x1p29f, 12582912.0f)) - 0x4b400000u + 0x20000000u;
-                    atomicAdd(&S.h.lo[at], v & 0xffffu);
-                    atomicAdd(&S.h.hi[at], v >> 16);
+        const float x0 = floor ? fmaxf(value_of(floor), W.low) : W.low;
+        auto stays = [&](float x, int token) { return x >= x0 && (x > x0 || key_of(x, token) >= floor); };
+        constexpr uint32_t BASE = 0x48400000u;   // ROUND's bits
+        if constexpr (SUM) {
+            weights(W, x0, [&](float a, float b, uint32_t i, uint32_t j, f2 q, int token) {
+                // (1 + q) 2^29, |q| < 0.0055
+                float v, w;
+                upk(fma2(q, pk(0x1p29f, 0x1p29f), pk(12582912.0f, 12582912.0f)), v, w);
+                const uint32_t y = __float_as_uint(v) - 0x4b400000u + 0x20000000u;
+                const uint32_t z = __float_as_uint(w) - 0x4b400000u + 0x20000000u;
+                if (stays(a, token)) {
+                    atomicAdd(&S.h.lo[BASE - i], y & 0xffffu);
+                    atomicAdd(&S.h.hi[BASE - i], y >> 16);
                 }
-            } else {
-                const int at = -W.place(x);
-                if (at < FINE)
-                    atomicAdd(&S.h.lo[at], 1u);
-            }
-        });
+                if (stays(b, token + 1)) {
+                    atomicAdd(&S.h.lo[BASE - j], z & 0xffffu);
+                    atomicAdd(&S.h.hi[BASE - j], z >> 16);
+                }
+            });
+        } else {
+            each(x0, [&](float x, int token) {
+                if (stays(x, token))
+                    atomicAdd(&S.h.lo[-W.place(x)], 1u);
+            });
+        }
         __syncthreads();
         cl_sync();
         // this CTA's share of the bins, a thread's in a row
@@ -473,9 +585,7 @@ struct Row {
         auto of_bin = [&](int bin) -> u64 {
             if (bin >= FINE)
                 return 0;
-            u64 v = 0;
-            for (int r = 0; r < C; ++r)
-                v += cl.map_shared_rank(S.h.lo, r)[bin] + (SUM ? (u64)cl.map_shared_rank(S.h.hi, r)[bin] << 16 : 0);
+            const u64 v = of_all(&S.h.lo[bin]) + (SUM ? of_all(&S.h.hi[bin]) << 16 : 0);
             if (!SUM)
                 return v;
             const float2 e = S.table[-bin & 63];
@@ -502,9 +612,8 @@ struct Row {
         const int from = who ? __ffs(who) - 1 : 0;
         const u64 y[2] = {__shfl_sync(0xffffffffu, found, from), __shfl_sync(0xffffffffu, before, from)};
         const auto board = publish(y);
-        auto most = [](u64 a, u64 b) { return a > b ? a : b; };
-        found = fold(board, 0, 0, most);
-        ahead_ = fold(board, 1, 0, most);
+        found = most(board, 0);
+        ahead_ = most(board, 1);
         return (int)found - 1;
     }
     // A logit a little below those of the bin.
@@ -513,152 +622,144 @@ struct Row {
         return W.m - ((float)bin + 0.51f) * (1.0f / 64.0f) / W.c_hi * 1.00001f - fabsf(W.m) * 0x1p-21f;
     }
 
-    // The key of the head's last token, among those with keys in [from, to], `ahead_` lying ahead of them.
-    template <bool SUM>
-    __device__ __noinline__ u64 refine(const FilterWeight &W, u64 from, u64 to, u64 ahead_, u64 target)
+    // The key of the head's last token, among those with keys in [from, to], `ahead_` lying ahead of them: these
+    // are in the CTAs' lists, `n` in this one's, or (LIST = false) only in the row.
+    template <bool SUM, bool LIST>
+    __device__ __noinline__ u64 refine(const FilterWeight &W, int n, u64 from, u64 to, u64 ahead_, u64 target)
     {
+        Search &Q = S.search;
 #pragma unroll 1
-        for (int level = 0; level < 10; ++level) {   // each takes 11 bits of the keys, of 64
-            const u64 span = to - from;
-            const int shift = max(0, 64 - __clzll((long long)span) - 11);
-            const float low = value_of(from), high = value_of(to);
+        for (;;) {
+            const int shift = part_shift(from, to);
             __syncthreads();
-            for (int i = threadIdx.x; i < BINS; i += FT)
-                S.h.lo[i] = S.h.hi[i] = 0;
-            if (threadIdx.x == 0)
-                S.lo = -1;
+            Q.lo[threadIdx.x] = Q.hi[threadIdx.x] = 0;
             __syncthreads();
-            auto bin_of = [&](float x, int token) {
-                const u64 k = key_of(x, token);
-                return k < from || k > to ? -1 : (int)((to - k) >> shift);
-            };
-            each(low, [&](float x, int token) {
-                if (x > high)
-                    return;
-                const int b = bin_of(x, token);
-                if (b < 0)
-                    return;
-                if constexpr (SUM) {
-                    const u64 w = W(x);
-                    const uint32_t lo = (uint32_t)w;
-                    const uint32_t hi = (uint32_t)(w >> 32) + (atomicAdd(&S.h.lo[b], lo) > ~lo);
-                    if (hi)
-                        atomicAdd(&S.h.hi[b], hi);
+            auto put = [&](u64 k) { Q.add((int)((to - k) >> shift), SUM ? W(value_of(k)) : 1); };
+            auto over = [&](auto f) {
+                if constexpr (LIST) {
+                    for (int i = threadIdx.x; i < n; i += FT)
+                        if (S.l.w[i] >= from && S.l.w[i] <= to)
+                            f(S.l.w[i]);
                 } else {
-                    atomicAdd(&S.h.lo[b], 1u);
+                    const float high = value_of(to);
+                    each(value_of(from), [&](float x, int token) {
+                        const u64 k = x > high ? 0 : key_of(x, token);
+                        if (k >= from && k <= to)
+                            f(k);
+                    });
                 }
-            });
-            __syncthreads();
+            };
+            over(put);
             cl_sync();
-            // all CTAs' bins, a thread's in a row
-            u64 bins[BIN_EACH], mine = 0, all;
-#pragma unroll
-            for (int k = 0; k < BIN_EACH; ++k)
-                bins[k] = 0;
-            for (int r = 0; r < C; ++r) {
-                const uint32_t *lo = cl.map_shared_rank(S.h.lo, r) + threadIdx.x * BIN_EACH;
-                const uint32_t *hi = cl.map_shared_rank(S.h.hi, r) + threadIdx.x * BIN_EACH;
-#pragma unroll
-                for (int k = 0; k < BIN_EACH; ++k)
-                    bins[k] += lo[k] | (SUM ? (u64)hi[k] << 32 : 0);
-            }
-#pragma unroll
-            for (int k = 0; k < BIN_EACH; ++k)
-                mine += bins[k];
-            u64 at = ahead_ + block_scan64(mine, S.sums, all);
-            // roundings may leave the target behind the last
-            target = min(target, ahead_ + all);
-            if (at < target && at + mine >= target) {
-#pragma unroll
-                for (int k = 0; k < BIN_EACH; ++k) {
-                    if (at < target && at + bins[k] >= target) {
-                        S.lo = threadIdx.x * BIN_EACH + k;
-                        S.base = at;
-                    }
-                    at += bins[k];
-                }
-            }
-            __syncthreads();
-            const int bin = S.lo;
+            const int bin = Q.find(of_all(&Q.lo[threadIdx.x]) + (of_all(&Q.hi[threadIdx.x]) << 32), ahead_, target);
             if (bin < 0) {
                 cl_sync();     // the others may still read this CTA's bins
                 return from;   // nothing of any weight
             }
-            ahead_ = S.base;
-            u64 least = ~0ull, most = 0;
-            const int count = collect(low, [&](float x, int token) {
-                const u64 k = key_of(x, token);
-                if (k < from || k > to || (int)((to - k) >> shift) != bin)
-                    return false;
-                least = k < least ? k : least;
-                most = k > most ? k : most;
-                return true;
-            });
-            cl_wait_all();
-            if (count <= RANKED) {
-                if (rank == 0)
-                    cut_list<SUM>(W, count, ahead_, target);
-                cl_sync();
-                return *cl.map_shared_rank(&S.cut, 0);
+            part(bin, shift, from, to);
+            int some = 0;
+            over([&](u64) { ++some; });
+            const u64 x[1] = {warp_sum64((u64)some)};
+            const Board board = publish(x);
+            const int all = (int)sum(board, 0);
+            if (all > RANKED)
+                continue;   // different keys, so they come to fewer
+            if constexpr (!LIST) {
+                n = stage(value_of(from), [&](float y, int token) {
+                    const u64 k = key_of(y, token);
+                    return k >= from && k <= to;
+                });
+                some = n;
+            } else {
+                __syncthreads();
+                if (threadIdx.x == 0)
+                    S.lo = 0;
+                __syncthreads();
+                if (some)
+                    atomicAdd(&S.lo, some);
+                __syncthreads();
+                some = S.lo;
+                __syncthreads();
             }
-            limits(least, most, from, to);
+            const int count = send(n, some, from, to);
+            cl_wait_all();
+            if (rank == 0)
+                cut_list<SUM>(W, count, ahead_, target);
+            cl_sync();
+            return *cl.map_shared_rank(&S.cut, 0);
         }
-        return from;
     }
-    // The least and the largest key of the cluster's threads'.
-    __device__ __forceinline__ void limits(u64 least, u64 most, u64 &from, u64 &to)
+    // The least and the largest key of the cluster's threads', and the largest n.
+    __device__ __forceinline__ int limits(u64 least, u64 most_, int n, u64 &from, u64 &to)
     {
+        u64 none = ~least;
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
-            const u64 a = __shfl_xor_sync(0xffffffffu, least, o), b = __shfl_xor_sync(0xffffffffu, most, o);
-            least = a < least ? a : least;
-            most = b > most ? b : most;
+            const u64 a = __shfl_xor_sync(0xffffffffu, none, o), b = __shfl_xor_sync(0xffffffffu, most_, o);
+            none = a > none ? a : none;
+            most_ = b > most_ ? b : most_;
         }
-        const u64 told[2] = {least, most};
+        const u64 told[3] = {none, most_, (u64)n};
         const Board board = publish(told);
-        from = fold(board, 0, ~0ull, [](u64 a, u64 b) { return a < b ? a : b; });
-        to = fold(board, 1, 0, [](u64 a, u64 b) { return a > b ? a : b; });
+        from = ~most(board, 0);
+        to = most(board, 1);
+        return (int)most(board, 2);
     }
-    // The same among the n tokens of this CTA's list, behind `ahead_`: S.cut.
+    // The cut among the tokens of one bin: `n` of them in this CTA's list, with keys from `least` to `most_` as
+    // this thread has seen them.  In the first CTA's list, ranked, where they are few (returns how many these are,
+    // and leaves the cut in its S.cut), otherwise -1 and the cut.
+    template <bool SUM>
+    __device__ __forceinline__ int cut_in_bin(const FilterWeight &W, int n, u64 least, u64 most_, u64 ahead_, u64 target,
+                                              u64 &cut)
+    {
+        u64 from, to;
+        const int longest = limits(least, most_, n, from, to);
+        const u64 x[1] = {warp == 0 ? (u64)n : 0};
+        const int all = (int)sum(publish(x), 0);
+        if (all <= RANKED) {
+            const int count = send(n, n, 0, ~0ull);
+            cl_wait_all();
+            if (rank == 0)
+                cut_list<SUM>(W, count, ahead_, target);
+            return count;
+        }
+        cut = longest <= FILTER_CAP ? refine<SUM, true>(W, n, from, to, ahead_, target)
+                                    : refine<SUM, false>(W, n, from, to, ahead_, target);
+        return -1;
+    }
+    // Among the n <= RANKED tokens of this CTA's list, behind `ahead_`: S.cut.
     template <bool SUM>
     __device__ __forceinline__ void cut_list(const FilterWeight &W, int n, u64 ahead_, u64 target)
     {
         rank_keys(S.l.key, n);
         if constexpr (SUM) {
-            constexpr int E = FILTER_CAP / FT;
-            u64 w[E], s = 0, all;
             if (threadIdx.x == 0)
                 S.cut = S.l.key[n - 1];   // where roundings leave the target behind the last
-#pragma unroll
-            for (int k = 0; k < E; ++k) {
-                const int i = threadIdx.x * E + k;
-                w[k] = i < n ? W(value_of(S.l.key[i])) : 0;
-                s += w[k];
-            }
-            u64 at = ahead_ + block_scan64(s, S.sums, all);
+            const u64 w = (int)threadIdx.x < n ? W(value_of(S.l.key[threadIdx.x])) : 0;
+            u64 all;
+            const u64 at = ahead_ + block_scan64(w, S.sums, all);
             // the token whose weight reaches the target is the last
-#pragma unroll
-            for (int k = 0; k < E; ++k) {
-                if (at < target && at + w[k] >= target)
-                    S.cut = S.l.key[threadIdx.x * E + k];
-                at += w[k];
-            }
-            __syncthreads();
-        } else {
-            if (threadIdx.x == 0)
-                S.cut = S.l.key[min((int)(target - ahead_), n) - 1];
-            __syncthreads();
+            if (at < target && at + w >= target)
+                S.cut = S.l.key[threadIdx.x];
+        } else if (threadIdx.x == 0) {
+            S.cut = S.l.key[min((int)(target - ahead_), n) - 1];
         }
+        __syncthreads();
     }
 
     // The sum of the weights from `cut` on, of this warp's segment.
     __device__ __forceinline__ u64 mass(const FilterWeight &W, u64 cut) const
     {
-        const float x0 = cut ? value_of(cut) : -F_INF;
+        const float x0 = cut ? fmaxf(value_of(cut), W.low) : W.low;
         FilterSum s;
-        each(x0, [&](float x, int token) {
-            if (x > x0 || (uint32_t)token <= (uint32_t)token_of(cut))
-                s.add(W.template pair<SHORT>(x));
+        weights(W, x0, [&](float a, float b, uint32_t i, uint32_t j, f2 y, int token) {
+            float q, r;
+            upk(y, q, r);
+            const bool in_a = a >= x0 && (a > x0 || key_of(a, token) >= cut);
+            const bool in_b = b >= x0 && (b > x0 || key_of(b, token + 1) >= cut);
+            const float2 none = make_float2(0.0f, 0.0f);
+            if (in_a || in_b)
+                s.add(in_a ? W.value(i, q) : none, in_b ? W.value(j, r) : none);
         });
         return warp_sum64(s.units());
     }
@@ -691,7 +792,7 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
 
     if (tid < 64)
         S.table[tid] = kFilterTable.t[tid];
-    else if (tid < 64 + LISTS)
+    else if (tid < 64 + 2 * LISTS)
         S.n[tid - 64] = 0;
     S.coarse[tid] = 0;
     if (tid == FT - 32) {
@@ -709,10 +810,10 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
         m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     {
         __syncthreads();
-        const u64 x[1] = {__float_as_uint(m)};
-        const auto board = R.publish(x);
-        m = __uint_as_float((uint32_t)R.fold(board, 0, 0xff800000u, [](u64 a, u64 b) {
-            return (u64)__float_as_uint(max_nan(__uint_as_float((uint32_t)a), __uint_as_float((uint32_t)b)));
+        const u64 x[1] = {1ull << 32 | __float_as_uint(m)};
+        m = __uint_as_float((uint32_t)R.fold(R.publish(x), 0, [](u64 a, u64 c) {
+            return a == 0 || c == 0 ? a | c
+                                    : 1ull << 32 | __float_as_uint(max_nan(__uint_as_float((uint32_t)a), __uint_as_float((uint32_t)c)));
         }));
     }
     if (code == 0 && !(m > -F_INF && m < F_INF))
@@ -744,16 +845,13 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
     rec.c_lo = S.c_lo;
 
     if (temp == 0.0f) {
-        u64 first = ~0ull;
-        R.each(m, [&](float, int token) { first = (u64)token < first ? (u64)token : first; });
+        u64 first = 0;   // ~token
+        R.each(m, [&](float, int token) { first = max(first, (u64)(0xffffffffu - (uint32_t)token)); });
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            const u64 a = __shfl_xor_sync(0xffffffffu, first, o);
-            first = a < first ? a : first;
-        }
+        for (int o = 16; o; o >>= 1)
+            first = max(first, (u64)__shfl_xor_sync(0xffffffffu, first, o));
         const u64 x[1] = {first};
-        const auto board = R.publish(x);
-        first = R.fold(board, 0, ~0ull, [](u64 a, u64 b) { return a < b ? a : b; });
+        first = 0xffffffffu - (uint32_t)R.most(R.publish(x), 0);
         rec.cut = m;
         rec.last = (uint32_t)first;
         rec.Z = 1ull << 43;
@@ -772,10 +870,15 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
         if (tid == 0)
             S.lo = COARSE - 1;
         __syncthreads();
-        for (int r = 0; r < R.C; ++r) {
-            const float x = R.cl.map_shared_rank(S.top, r)[tid];
-            if (x > -F_INF)
-                atomicAdd(&S.coarse[min(COARSE - 1, (int)((m - x) * (W.c_hi * (COARSE / RANGE))))], 1u);
+        for (int r = 0; r < R.C; r += 8) {
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                x[j] = r + j < R.C ? R.cl.map_shared_rank(S.top, r + j)[tid] : -F_INF;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (x[j] > -F_INF)
+                    atomicAdd(&S.coarse[min(COARSE - 1, (int)((m - x[j]) * (W.c_hi * (COARSE / RANGE))))], 1u);
         }
         __syncthreads();
         const u64 n = S.coarse[tid];
@@ -793,59 +896,79 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
         listed = true;
     }
     if (listed) {
-        const int count = R.collect(t0, [](float, int) { return true; });
+        const int own = R.stage(t0, [](float, int) { return true; });
+        const int count = R.send(own, own, 0, ~0ull);
         if (count <= FILTER_CAP) {
             if (rank != 0) {
                 cl_wait_all();
                 return;
             }
-            rank_keys(S.l.key, count);
-            constexpr int E = FILTER_CAP / FT;
-            u64 w[E], s = 0, all;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int r = tid * E + e;
-                w[e] = r < count && r < k ? W(R_::value_of(S.l.key[r])) : 0;
-                s += w[e];
-            }
-            u64 at = block_scan64(s, S.sums, all);
-            // less than p of the total: the same as less than the next whole number
-            const u64 target = p >= 1.0f ? ~0ull : (u64)ceil((double)fmaxf(p, 0.0f) * (double)all);
-            int stay = 0;
-            s = 0;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int r = tid * E + e;
-                if (r < count && (r == 0 || (r < k && at < target && R_::value_of(S.l.key[r]) >= xmin))) {
-                    ++stay;
-                    s += w[e];
+            // less than p of a total: the same as less than the next whole number
+            auto reach = [&](u64 total) { return max((u64)ceil((double)fmaxf(p, 0.0f) * (double)total), 1ull); };
+            u64 Z, all, last;
+            if (count <= FT) {
+                // ranked, a token per thread
+                rank_keys(S.l.key, count);
+                const u64 key = tid < count ? S.l.key[tid] : 0;
+                u64 w = tid < count && tid < k ? W(R_::value_of(key)) : 0;
+                const u64 at = block_scan64(w, S.sums, all);
+                const bool stays = tid < count && (tid == 0 || (tid < k && (p >= 1.0f || at < reach(all)) && R_::value_of(key) >= xmin));
+                w = stays ? w : 0;
+                S.l.w[tid] = w;
+                block_scan64(w, S.sums, Z);
+                block_scan64(stays, S.search.sums, all);
+                last = S.l.key[all - 1];
+            } else {
+                u64 s = 0;
+                for (int e = tid; e < count; e += FT)
+                    S.l.w[e] = W(R_::value_of(S.l.key[e]));
+                const u64 to = (u64)filter_key(m) << 32 | 0xffffffffu;
+                last = (u64)filter_key(t0) << 32;
+                if (k < count)
+                    last = select_key(S.l.key, count, last, to, (u64)k, [](int) { return 1ull; }, S.search);
+                if (p < 1.0f) {
+                    __syncthreads();
+                    for (int e = tid; e < count; e += FT)
+                        s += S.l.key[e] >= last ? S.l.w[e] : 0;
+                    block_scan64(s, S.sums, all);
+                    last = select_key(S.l.key, count, last, to, reach(all), [&](int e) { return S.l.w[e]; }, S.search);
                 }
-                at += w[e];
-                if (r < count)
-                    S.l.w[r] = w[e];
+                const u64 c = least > 0.0f ? (u64)filter_key(xmin) << 32 : 0;
+                last = max(last, c);
+                s = 0;
+                __syncthreads();
+                for (int e = tid; e < count; e += FT) {
+                    if (S.l.key[e] < last)
+                        S.l.w[e] = 0;
+                    s += S.l.w[e];
+                }
+                block_scan64(s, S.sums, Z);
             }
-            u64 Z;
-            block_scan64(s, S.sums, Z);
-            block_scan64(stay, S.sums2, all);
-            const int n = (int)all;
             if (VERIFY) {
+                if (tid == 0)
+                    S.lo = 0;
+                __syncthreads();
                 if (!draft) {
                     const size_t list = (size_t)(b * (P.K + 1) + i) * FILTER_CAP;
-                    for (int e = tid; e < n; e += FT) {
-                        P.list_x[list + e] = R_::token_of(S.l.key[e]);
-                        P.list_w[list + e] = S.l.w[e];
-                    }
-                    rec.n = n;
+                    for (int e = tid; e < count; e += FT)
+                        if (S.l.w[e]) {
+                            const int to = atomicAdd(&S.lo, 1);
+                            P.list_x[list + to] = R_::token_of(S.l.key[e]);
+                            P.list_w[list + to] = S.l.w[e];
+                        }
+                    __syncthreads();
+                    rec.n = S.lo;
                 }
-                rec.cut = R_::value_of(S.l.key[n - 1]);
-                rec.last = (uint32_t)R_::token_of(S.l.key[n - 1]);
+                rec.cut = R_::value_of(last);
+                rec.last = (uint32_t)R_::token_of(last);
                 rec.Z = Z;
                 if (tid == 0)
                     finish(-1, 0.0f);
             } else {
-                for (int e = tid; e < n; e += FT)
-                    S.l.key[e] = S.l.key[e] << 32 | (uint32_t)e;
-                pick(S.l.key, S.l.w, n, (u64)((double)u * (double)Z), S.sums, [&](int e, int token) {
+                __syncthreads();
+                for (int e = tid; e < count; e += FT)
+                    S.l.key[e] = pick_key(R_::token_of(S.l.key[e]), e);
+                pick(S.l.key, S.l.w, count, V, (u64)((double)u * (double)Z), S.search, [&](int e, int token) {
                     finish(token, (float)((double)S.l.w[e] / (double)Z));
                 });
             }
@@ -863,7 +986,7 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
         const int bin = R.template bin_of_cut<false>(W, (double)k, 0, ahead, target);
         if (bin >= 0) {
             u64 from = ~0ull, to = 0;
-            const int count = R.collect(R_::below_bin(W, bin), [&](float y, int token) {
+            const int n = R.stage(fmaxf(R_::below_bin(W, bin), W.low), [&](float y, int token) {
                 if (-W.place(y) != bin)
                     return false;
                 const u64 key = R_::key_of(y, token);
@@ -871,32 +994,31 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
                 to = key > to ? key : to;
                 return true;
             });
-            cl_wait_all();
-            if (count <= RANKED) {
-                if (rank == 0)
-                    R.template cut_list<false>(W, count, ahead, target);
+            if (R.template cut_in_bin<false>(W, n, from, to, ahead, target, cut) >= 0) {
                 cl_sync();
                 cut = *R.cl.map_shared_rank(&S.cut, 0);
-            } else {
-                R.limits(from, to, from, to);
-                cut = R.template refine<false>(W, from, to, ahead, target);
             }
         }
     }
     const u64 c_min = least > 0.0f ? (u64)filter_key(xmin) << 32 : 0;
     if (p < 1.0f) {
         const int bin = R.template bin_of_cut<true>(W, (double)fmaxf(p, 0.0f), cut, ahead, target);
-        if (least > 0.0f && -W.place(xmin) < bin) {
+        if (least > 0.0f && (xmin >= W.low ? -W.place(xmin) : FINE) < bin) {
             cut = c_min > cut ? c_min : cut;   // min-p cuts ahead of that bin
         } else {
             // weights above the bin, by segment; its tokens
             const u64 floor = cut;
             FilterSum above;
+            const float2 none = make_float2(0.0f, 0.0f);
             u64 from = ~0ull, to = 0;
-            const int count = R.collect(R_::below_bin(W, bin), [&](float y, int token) {
+            const int n = R.stage(fmaxf(R_::below_bin(W, bin), W.low), [&](float y, int token) {
                 const int at = -W.place(y);
-                if (at < bin)
-                    above.add(W.template pair<R_::SHORT>(y));
+                if (at < bin) {
+                    uint32_t i0, i1;
+                    float q0, q1;
+                    upk(W.template split<R_::SHORT>(pk(y, y), i0, i1), q0, q1);
+                    above.add(W.value(i0, q0), none);
+                }
                 const u64 key = R_::key_of(y, token);
                 if (at != bin || key < floor)
                     return false;
@@ -904,21 +1026,17 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
                 to = key > to ? key : to;
                 return true;
             });
-            cl_wait_all();
-            if (count <= RANKED) {
-                const u64 y[1] = {warp_sum64(above.units())};
+            const u64 y[1] = {warp_sum64(above.units())};
+            const int count = R.template cut_in_bin<true>(W, n, from, to, ahead, target, cut);
+            if (count >= 0) {
                 const auto board = R.publish(y);
                 if (rank == 0) {
                     for (int g = tid; g < R.C * FW; g += FT)
                         S.seg[g] = board.get(0, g);
-                    R.template cut_list<true>(W, count, ahead, target);
-                    u64 c = S.cut;
-                    c = c > c_min ? c : c_min;
-                    for (int e = tid; e < count; e += FT) {
-                        const u64 key = S.l.key[e];
-                        if (key >= c)
-                            atomicAdd(&S.seg[((R_::token_of(key) + R.off) / T::N) / R.len], W(R_::value_of(key)));
-                    }
+                    __syncthreads();
+                    const u64 c = max(S.cut, c_min);
+                    if (tid < count && S.l.key[tid] >= c)
+                        atomicAdd(&S.seg[((R_::token_of(S.l.key[tid]) + R.off) / T::N) / R.len], W(R_::value_of(S.l.key[tid])));
                     __syncthreads();
                     if (tid == 0)
                         S.cut = c;
@@ -926,9 +1044,6 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
                 done = true;
                 cl_sync();
                 cut = *R.cl.map_shared_rank(&S.cut, 0);
-            } else {
-                R.limits(from, to, from, to);
-                cut = R.template refine<true>(W, from, to, ahead, target);
             }
         }
     }
@@ -1020,6 +1135,7 @@ struct DecideShared {
     int j, code, seg;
     u64 before;
     u64 key[FILTER_CAP], w[FILTER_CAP];
+    Search search;
 };
 
 template <class T>
@@ -1109,7 +1225,7 @@ __global__ void __launch_bounds__(FT) filter_decide(const __grid_constant__ Filt
         for (int e = tid; e < q.n; e += FT) {
             const int x = P.list_x[list + e];
             const u64 wq = P.list_w[list + e];
-            S.key[e] = (u64)(0xffffffffu - (uint32_t)x) << 32 | (uint32_t)e;
+            S.key[e] = pick_key(x, e);
             S.w[e] = bonus ? wq : left(wq, weight(p, Wp, T::one(drf, row_q + x), x));
             sum += S.w[e];
         }
@@ -1120,7 +1236,7 @@ __global__ void __launch_bounds__(FT) filter_decide(const __grid_constant__ Filt
                 S.w[e] = P.list_w[list + e];
             all = q.Z;
         }
-        pick(S.key, S.w, q.n, (u64)(v * (double)all), S.sums, [&](int, int token) { *out = token; });
+        pick(S.key, S.w, q.n, V, (u64)(v * (double)all), S.search, [&](int, int token) { *out = token; });
         return;
     }
     // over the vocabulary: a segment per warp, then the segment on which the uniform falls
@@ -1215,7 +1331,7 @@ cudaError_t rows(const FilterParams &P, int sms, cudaStream_t stream)
     // four CTAs to an SM: as many rows in flight as L2 holds beside other things, all CTAs busy where
     // there are few rows, and no part so short that the barriers are all there is
     int C = 1;
-    while (C < MAX_C && ((4 * sms / C) * bytes > FLIGHT || bytes / C > 65536 * T::ES || (n * C < 4 * sms && bytes / C > 4096)))
+    while (C < MAX_C && (std::min(n, (long long)(4 * sms / C)) * bytes > FLIGHT || bytes / C > 65536 * T::ES || (n * C < 4 * sms && bytes / C > 4096)))
         C *= 2;
     static std::atomic<uint64_t> raised{0};
     int dev = 0;

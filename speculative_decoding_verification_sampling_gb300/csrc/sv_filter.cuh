@@ -19,50 +19,10 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "sv_kernel.cuh"
 #include "sv_params.h"
 
 namespace sv {
-
-typedef unsigned long long u64;
-
-// One set of filters, an entry per sequence; nullptr: off (T: 1).
-struct FilterSet {
-    const float *T;
-    const int32_t *k;
-    const float *p;
-    const float *least;
-};
-
-// What is kept of a row, for the kernel that verifies: the tokens with
-// (z, index) at the cut or ahead of it.
-struct FilterRow {
-    float m, c_hi, c_lo;   // the largest logit; log2(e) / T as two floats
-    float cut;             // kept: z > cut, or z == cut and index <= last
-    uint32_t last;
-    int32_t n;             // tokens kept, listed in the workspace; -1: not listed
-    u64 Z;                 // their weights' sum
-    int32_t code;          // 0, or a status
-    int32_t pad[7];
-};
-static_assert(sizeof(FilterRow) == 64, "a row's record");
-
-constexpr int FILTER_CAP = 2048;   // tokens of a row that are ranked together, and listed
-constexpr int FILTER_MAX_V = 524288;
-
-struct FilterParams {
-    const void *logits;      // [B][rows][V]: sample: [B][K]; verify: the target's [B][K + 1]
-    const void *draft;       // verify: [B][K][V]
-    const float *uniforms;   // sample: [B][K]; verify: [B][K + 1][2]
-    const int32_t *tokens;   // verify: [B][K]
-    FilterSet f, df;         // of the logits, and of the draft
-    int32_t *out_tokens, *out_len;
-    float *out_prob;
-    int32_t *status;
-    FilterRow *rows;         // verify: [B][2K + 1], target rows first
-    int32_t *list_x;         // verify: [B][K + 1][FILTER_CAP], in the row's order
-    u64 *list_w;
-    int B, K, V;
-};
 
 // 2^(j / 64) as two floats.
 struct FilterTable {
@@ -84,87 +44,99 @@ constexpr FilterTable filter_table()
     for (int j = 0; j < 64; ++j) {
         const double v = filter_pow2(j);
         t.t[j].x = (float)v;
-        t.t[j].y = (float)(v - (double)(float)v);
+        t.t[j].y = j ? (float)(v - (double)(float)v) : 1e-20f;   // not 0: its exponent is added to
     }
     return t;
 }
 
 constexpr float FILTER_UNIT = 8796093022208.0f;   // 2^43
 
-// The weights of one row.
+// The weights of one row.  2^((x - m) c) = 2^(i / 64) (1 + q): the exponent is the
+// sum of a multiple of 1/64 and a rest r, |r| <= 1/128, exact up to its last bit;
+// 2^r - 1 = y + y^2/2 + y^3/6 with y = r ln 2, off by 2^-34.
 struct FilterWeight {
-    float m, c_hi, c_lo, least;   // `least`: a z - m from which on weights are nothing, 2^-120
-    const float2 *table;          // in shared memory
+    static constexpr float ROUND = 196608.0f;   // 1.5 2^17: steps of 1/64
+    float m, c_hi, c_lo;
+    float low;              // logits below have weights below half a unit
+    const float2 *table;    // in shared memory
     FilterWeight() = default;
     __device__ __forceinline__ FilterWeight(float m_, float hi, float lo, const float2 *t)
-        : m(m_), c_hi(hi), c_lo(lo), least(hi > 0.0f ? -120.0f / hi : -3e38f), table(t)
     {
+        m = m_, c_hi = hi, c_lo = lo, table = t;
+        low = hi > 0.0f ? __fadd_ru(m, __fdiv_rn(-43.75f, hi)) : m;
     }
-    // 2^((x - m) c) = 2^(i / 64) (1 + q).  The exponent is the sum of a multiple of 1/64 and a rest r,
-    // |r| <= 1/128, both exact up to the last bits of r: 2^r - 1 = y + y^2/2 + y^3/6 with y = r ln 2, off by
-    // 2^-34.
-    static constexpr float ROUND = 196608.0f;   // 1.5 2^17: steps of 1/64
+    // Two logits at or above `low` (others come to nothing that may be used): the bits of i / 64 + ROUND, and q.
     // SHORT: logits of 8 bits.  Their difference is exact where they lie within 2^16 of each other; where x is
     // the smaller one, what is lost is x - (d + m).  (Where m is, 2^-16 of the other logits: 2^-24 of them is lost.)
     template <bool SHORT>
-    __device__ __forceinline__ int split(float x, float &q) const
+    __device__ __forceinline__ f2 split(f2 x, uint32_t &i0, uint32_t &i1) const
     {
-        float d = x - m;
-        float rest;
+        const f2 mm = pk(m, m), nm = pk(-m, -m), one = pk(-1.0f, -1.0f), ch = pk(c_hi, c_hi), cl = pk(c_lo, c_lo);
+        const f2 round = pk(ROUND, ROUND);
+        const f2 d = add2(x, nm);
+        f2 rest;
         if constexpr (SHORT) {
-            rest = x - (d + m);
+            rest = fma2(add2(d, mm), one, x);
         } else {
-            const float back = d - x;
-            rest = (x - (d - back)) + (-m - back);
+            const f2 back = fma2(x, one, d);
+            rest = add2(fma2(fma2(back, one, d), one, x), fma2(back, one, nm));
         }
-        rest = d > least ? rest : 0.0f;
-        d = fmaxf(d, least);
-        const float zh = __fmul_rn(d, c_hi);   // not to be fused with what follows
-        float zl = fmaf(d, c_hi, -zh);
-        zl = fmaf(d, c_lo, zl);
-        zl = fmaf(rest, c_hi, zl);
-        const float t = zh + ROUND;
-        const float r = (zh - (t - ROUND)) + zl;
-        q = r * fmaf(r, fmaf(r, 0.055504109f, 0.24022651f), 0.69314718f);
-        return __float_as_int(t) - __float_as_int(ROUND);
+        const f2 t = fma2(d, ch, round);
+        f2 r = fma2(d, ch, fma2(t, one, round));
+        r = fma2(d, cl, r);
+        r = fma2(rest, ch, r);
+        float a, b;
+        upk(t, a, b);
+        i0 = __float_as_uint(a);
+        i1 = __float_as_uint(b);
+        return mul2(r, fma2(r, fma2(r, pk(0.055504109f, 0.055504109f), pk(0.24022651f, 0.24022651f)),
+                            pk(0.69314718f, 0.69314718f)));
     }
-    // the same i alone
+    // i alone, for a logit at or above `low`
     __device__ __forceinline__ int place(float x) const
     {
-        return __float_as_int(__fadd_rn(__fmul_rn(fmaxf(x - m, least), c_hi), ROUND)) - __float_as_int(ROUND);
+        return __float_as_int(__fmaf_rn(__fadd_rn(x, -m), c_hi, ROUND)) - __float_as_int(ROUND);
     }
-    // as two floats, of which the second is small
-    template <bool SHORT>
-    __device__ __forceinline__ float2 pair(float x) const
+    // 2^(i / 64) (1 + q) as two floats, of which the second is small
+    __device__ __forceinline__ float2 value(uint32_t i, float q) const
     {
-        float q;
-        const int i = split<SHORT>(x, q);
         const float2 e = table[i & 63];
-        const float s = __int_as_float(((i >> 6) + 127) << 23);
-        return make_float2(e.x * s, fmaf(e.x, q, e.y) * s);
+        const uint32_t up = (i << 17) & 0xff800000u;   // ROUND's bits leave the word
+        const float hi = __uint_as_float(__float_as_uint(e.x) + up), lo = __uint_as_float(__float_as_uint(e.y) + up);
+        return make_float2(hi, fmaf(hi, q, lo));
     }
-    // in units
+    // in units; 0 below `low`
     __device__ __forceinline__ u64 operator()(float x) const
     {
-        const float2 w = pair<false>(x);
+        if (!(x >= low))
+            return 0;
+        uint32_t i, j;
+        float q, r;
+        upk(split<false>(pk(x, x), i, j), q, r);
+        const float2 w = value(i, q);
         return (u64)(__float2ll_rn(w.x * FILTER_UNIT) + __float2ll_rn(w.y * FILTER_UNIT));
     }
 };
 
-// A thread's sum of weights: the rounding errors of the larger halves go with the smaller ones, so the sum is
+// A thread's two sums of weights: the rounding errors of the larger halves go with the smaller ones, so a sum is
 // right to 2^-24 of those.  `s` begins at the largest weight there is.
 struct FilterSum {
-    float s = 1.0f, c = 0.0f;
-    __device__ __forceinline__ void add(float2 w)
+    f2 s = pk(1.0f, 1.0f), c = pk(0.0f, 0.0f);
+    __device__ __forceinline__ void add(float2 a, float2 b)
     {
-        const float t = s + w.x;
-        c += (s - t) + w.x;
-        c += w.y;
+        const f2 w = pk(a.x, b.x), one = pk(-1.0f, -1.0f);
+        const f2 t = add2(s, w);
+        c = add2(c, add2(fma2(t, one, s), w));
+        c = add2(c, pk(a.y, b.y));
         s = t;
     }
     __device__ __forceinline__ u64 units() const
     {
-        return (u64)(__float2ll_rn((s - 1.0f) * FILTER_UNIT) + __float2ll_rn(c * FILTER_UNIT));
+        float a, b, x, y;
+        upk(s, a, b);
+        upk(c, x, y);
+        return (u64)(__float2ll_rn((a - 1.0f) * FILTER_UNIT) + __float2ll_rn((b - 1.0f) * FILTER_UNIT) +
+                     __float2ll_rn(x * FILTER_UNIT) + __float2ll_rn(y * FILTER_UNIT));
     }
 };
 

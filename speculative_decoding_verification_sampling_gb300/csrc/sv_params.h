@@ -281,4 +281,46 @@ struct AttnParams {
     const int32_t *from;        // [B] the first entry that all tokens' windows reach, or nullptr (no mask)
 };
 
+// Filtered rows of logits (k_filter.cu).
+typedef unsigned long long u64;
+
+// One set of filters, an entry per sequence; nullptr: off (T: 1).
+struct FilterSet {
+    const float *T;
+    const int32_t *k;
+    const float *p;
+    const float *least;
+};
+
+// What is kept of a row, for the kernel that verifies: the tokens with
+// (z, index) at the cut or ahead of it.
+struct FilterRow {
+    float m, c_hi, c_lo;   // the largest logit; log2(e) / T as two floats
+    float cut;             // kept: z > cut, or z == cut and index <= last
+    uint32_t last;
+    int32_t n;             // tokens kept, listed in the workspace; -1: not listed
+    u64 Z;                 // their weights' sum
+    int32_t code;          // 0, or a status
+    int32_t pad[7];
+};
+static_assert(sizeof(FilterRow) == 64, "a row's record");
+
+constexpr int FILTER_CAP = 2048;   // tokens of a row that are ranked together, and listed
+constexpr int FILTER_MAX_V = 524288;
+
+struct FilterParams {
+    const void *logits;      // [B][rows][V]: sample: [B][K]; verify: the target's [B][K + 1]
+    const void *draft;       // verify: [B][K][V]
+    const float *uniforms;   // sample: [B][K]; verify: [B][K + 1][2]
+    const int32_t *tokens;   // verify: [B][K]
+    FilterSet f, df;         // of the logits, and of the draft
+    int32_t *out_tokens, *out_len;
+    float *out_prob;
+    int32_t *status;
+    FilterRow *rows;         // verify: [B][2K + 1], target rows first
+    int32_t *list_x;         // verify: [B][K + 1][FILTER_CAP], in the row's order
+    u64 *list_w;
+    int B, K, V;
+};
+
 }  // namespace sv
