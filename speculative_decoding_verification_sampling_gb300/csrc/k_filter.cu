@@ -275,7 +275,6 @@ constexpr int RANKED = FT;                // tokens of a bin that are ranked; mo
 struct RowShared {
     u64 slot[2][4][FW];   // published, by round parity: up to four numbers per warp
     u64 sums[FW], sums2[FW];
-    u64 seg[MAX_C * FW];  // the segments' weights
     Search search;
     float2 table[64];
     float top[FT];        // the threads' maxima
@@ -359,11 +358,28 @@ struct Row {
                     f(q[u], v + lanes * u);
         }
     }
+    // The same for this warp's segment, one vector at a time, the next one on its way: for longer f, which would
+    // fill the instruction cache several times over
+    template <class F>
+    __device__ __forceinline__ void in_turn(F f) const
+    {
+        int v = seg0 + lane;
+        uint4 next = make_uint4(0, 0, 0, 0);
+        if (v < seg1)
+            next = vector(v);
+#pragma unroll 1
+        for (; v < seg1; v += 32) {
+            const uint4 q = next;
+            if (v + 32 < seg1)
+                next = vector(v + 32);
+            f(q, v);
+        }
+    }
     // f(logit, token) for the tokens of this warp's segment with logits of at least `from` and above minus infinity
     template <class F>
     __device__ __forceinline__ void each(float from, F f) const
     {
-        vectors<4>(seg0, seg1, lane, 32, [&](const uint4 &q, int v) {
+        in_turn([&](const uint4 &q, int v) {
             if (!(T::largest(q) >= from))
                 return;
 #pragma unroll
@@ -379,7 +395,7 @@ struct Row {
     template <class F>
     __device__ __forceinline__ void weights(const FilterWeight &W, float from, F f) const
     {
-        vectors<4>(seg0, seg1, lane, 32, [&](const uint4 &q, int v) {
+        in_turn([&](const uint4 &q, int v) {
             if (!(T::largest(q) >= from))
                 return;
 #pragma unroll
@@ -512,31 +528,33 @@ struct Row {
         __syncthreads();
         return (int)*n;
     }
-    // The keys in [from, to] of this CTA's list of n, `some` of them, go to the first CTA's list, in any order (one
-    // remote atomic per CTA: it takes about 50 ns, and all meet at one place).  Returns how many there are; where
-    // these are more than the list holds, they are not all in it.  Ends with an arrival at the cluster's barrier:
-    // cl_wait_all is next.
-    __device__ __forceinline__ int send(int n, int some, u64 from, u64 to)
+    // Puts a key into this CTA's list of number `lists`, as `stage` does.
+    __device__ __forceinline__ void put(float x, int token)
     {
-        if (threadIdx.x == 0) {
-            S.hi = (int)atomicAdd(cl.map_shared_rank(&S.n[lists - 1], 0), (uint32_t)some);
-            S.lo = 0;
+        const uint32_t at = atomicAdd(&S.n[lists], 1u);
+        if (at < FILTER_CAP)
+            S.l.w[at] = key_of(x, token);
+    }
+    // All CTAs' lists, n_r keys in the r-th (number i of the board's, of warp 0), up to FILTER_CAP together, to this
+    // CTA's S.l.key.
+    __device__ __forceinline__ void gather(const Board &b, int i)
+    {
+        // where the CTAs' lists begin
+        u64 n = lane < C ? b.get(i, lane * FW) : 0;
+        const int end = (int)warp_scan64(n, lane), all = __shfl_sync(0xffffffffu, end, 31);
+        const int begin = end - (int)n;
+        for (int k0 = 0; k0 < all; k0 += FT) {
+            const int k = k0 + threadIdx.x;
+            int r = 0, at = k;
+            for (int c = 1; c < C; ++c) {
+                const int o = __shfl_sync(0xffffffffu, begin, c);
+                if (k >= o)
+                    r = c, at = k - o;
+            }
+            if (k < all)
+                S.l.key[k] = cl.map_shared_rank(S.l.w, r)[at];
         }
         __syncthreads();
-        const int at = S.hi;
-        u64 *key = cl.map_shared_rank(S.l.key, 0);
-        for (int i = threadIdx.x; i < n && i < FILTER_CAP; i += FT) {
-            const u64 k = S.l.w[i];
-            if (k < from || k > to)
-                continue;
-            const int j = at + (some == n ? i : atomicAdd(&S.lo, 1));
-            if (j < FILTER_CAP)
-                key[j] = k;
-        }
-        const u64 x[1] = {warp == 0 ? (u64)some : 0};
-        const int all = (int)sum(publish(x), 0);
-        cl_arrive();
-        return all;
     }
 
     // Where the head ends that has `share` tokens (SUM = false), or ahead of whose last token less than `share` of
@@ -629,122 +647,128 @@ struct Row {
     {
         Search &Q = S.search;
 #pragma unroll 1
-        for (;;) {
+        while (from < to) {
             const int shift = part_shift(from, to);
             __syncthreads();
             Q.lo[threadIdx.x] = Q.hi[threadIdx.x] = 0;
             __syncthreads();
-            auto put = [&](u64 k) { Q.add((int)((to - k) >> shift), SUM ? W(value_of(k)) : 1); };
-            auto over = [&](auto f) {
-                if constexpr (LIST) {
-                    for (int i = threadIdx.x; i < n; i += FT)
-                        if (S.l.w[i] >= from && S.l.w[i] <= to)
-                            f(S.l.w[i]);
-                } else {
-                    const float high = value_of(to);
-                    each(value_of(from), [&](float x, int token) {
-                        const u64 k = x > high ? 0 : key_of(x, token);
-                        if (k >= from && k <= to)
-                            f(k);
-                    });
-                }
-            };
-            over(put);
+            auto add = [&](u64 k) { Q.add((int)((to - k) >> shift), SUM ? W(value_of(k)) : 1); };
+            if constexpr (LIST) {
+                for (int i = threadIdx.x; i < n; i += FT)
+                    if (S.l.w[i] >= from && S.l.w[i] <= to)
+                        add(S.l.w[i]);
+            } else {
+                const float high = value_of(to);
+                each(value_of(from), [&](float x, int token) {
+                    const u64 k = x > high ? 0 : key_of(x, token);
+                    if (k >= from && k <= to)
+                        add(k);
+                });
+            }
             cl_sync();
             const int bin = Q.find(of_all(&Q.lo[threadIdx.x]) + (of_all(&Q.hi[threadIdx.x]) << 32), ahead_, target);
-            if (bin < 0) {
-                cl_sync();     // the others may still read this CTA's bins
-                return from;   // nothing of any weight
-            }
+            cl_sync();     // all have read the bins
+            if (bin < 0)
+                break;     // nothing of any weight
             part(bin, shift, from, to);
-            int some = 0;
-            over([&](u64) { ++some; });
-            const u64 x[1] = {warp_sum64((u64)some)};
-            const Board board = publish(x);
-            const int all = (int)sum(board, 0);
-            if (all > RANKED)
-                continue;   // different keys, so they come to fewer
-            if constexpr (!LIST) {
-                n = stage(value_of(from), [&](float y, int token) {
-                    const u64 k = key_of(y, token);
-                    return k >= from && k <= to;
-                });
-                some = n;
-            } else {
-                __syncthreads();
-                if (threadIdx.x == 0)
-                    S.lo = 0;
-                __syncthreads();
-                if (some)
-                    atomicAdd(&S.lo, some);
-                __syncthreads();
-                some = S.lo;
-                __syncthreads();
-            }
-            const int count = send(n, some, from, to);
-            cl_wait_all();
-            if (rank == 0)
-                cut_list<SUM>(W, count, ahead_, target);
-            cl_sync();
-            return *cl.map_shared_rank(&S.cut, 0);
         }
+        return from;
     }
-    // The least and the largest key of the cluster's threads', and the largest n.
-    __device__ __forceinline__ int limits(u64 least, u64 most_, int n, u64 &from, u64 &to)
-    {
-        u64 none = ~least;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            const u64 a = __shfl_xor_sync(0xffffffffu, none, o), b = __shfl_xor_sync(0xffffffffu, most_, o);
-            none = a > none ? a : none;
-            most_ = b > most_ ? b : most_;
-        }
-        const u64 told[3] = {none, most_, (u64)n};
-        const Board board = publish(told);
-        from = ~most(board, 0);
-        to = most(board, 1);
-        return (int)most(board, 2);
-    }
-    // The cut among the tokens of one bin: `n` of them in this CTA's list, with keys from `least` to `most_` as
-    // this thread has seen them.  In the first CTA's list, ranked, where they are few (returns how many these are,
-    // and leaves the cut in its S.cut), otherwise -1 and the cut.
+
+    // The key of the head's last token, which is in the bin (bin_of_cut).  By sums, where the bin has few tokens, the
+    // segments' weights as well: the sum of those that stay (keys from the cut and from `c_min` on), what lies ahead
+    // of this warp's segment, and its own.
     template <bool SUM>
-    __device__ __forceinline__ int cut_in_bin(const FilterWeight &W, int n, u64 least, u64 most_, u64 ahead_, u64 target,
-                                              u64 &cut)
+    __device__ __forceinline__ u64 cut_in_bin(const FilterWeight &W, int bin, u64 floor, u64 ahead_, u64 target, u64 c_min,
+                                              bool &done, u64 &Z, u64 &before, u64 &mine)
     {
-        u64 from, to;
-        const int longest = limits(least, most_, n, from, to);
-        const u64 x[1] = {warp == 0 ? (u64)n : 0};
-        const int all = (int)sum(publish(x), 0);
-        if (all <= RANKED) {
-            const int count = send(n, n, 0, ~0ull);
-            cl_wait_all();
-            if (rank == 0)
-                cut_list<SUM>(W, count, ahead_, target);
-            return count;
-        }
-        cut = longest <= FILTER_CAP ? refine<SUM, true>(W, n, from, to, ahead_, target)
-                                    : refine<SUM, false>(W, n, from, to, ahead_, target);
-        return -1;
-    }
-    // Among the n <= RANKED tokens of this CTA's list, behind `ahead_`: S.cut.
-    template <bool SUM>
-    __device__ __forceinline__ void cut_list(const FilterWeight &W, int n, u64 ahead_, u64 target)
-    {
-        rank_keys(S.l.key, n);
+        FilterSum above;   // the bin
+        u64 none = 0, most_ = 0;   // ~ the least and the largest key in it
+        const float low = fmaxf(below_bin(W, bin), W.low);
+        auto in_bin = [&](float x, int token) {
+            const u64 k = key_of(x, token);
+            if (k < floor)
+                return;
+            put(x, token);
+            none = max(none, ~k);
+            most_ = max(most_, k);
+        };
+        constexpr uint32_t BASE = 0x48400000u;   // ROUND's bits
         if constexpr (SUM) {
-            if (threadIdx.x == 0)
-                S.cut = S.l.key[n - 1];   // where roundings leave the target behind the last
-            const u64 w = (int)threadIdx.x < n ? W(value_of(S.l.key[threadIdx.x])) : 0;
-            u64 all;
-            const u64 at = ahead_ + block_scan64(w, S.sums, all);
-            // the token whose weight reaches the target is the last
-            if (at < target && at + w >= target)
-                S.cut = S.l.key[threadIdx.x];
-        } else if (threadIdx.x == 0) {
-            S.cut = S.l.key[min((int)(target - ahead_), n) - 1];
+            weights(W, low, [&](float x0, float x1, uint32_t i, uint32_t j, f2 y, int token) {
+                const int a = x0 >= low ? (int)(BASE - i) : FINE, b = x1 >= low ? (int)(BASE - j) : FINE;
+                if (min(a, b) < bin) {
+                    float q, r;
+                    upk(y, q, r);
+                    const float2 zero = make_float2(0.0f, 0.0f);
+                    above.add(a < bin ? W.value(i, q) : zero, b < bin ? W.value(j, r) : zero);
+                }
+                if (a == bin)
+                    in_bin(x0, token);
+                if (b == bin)
+                    in_bin(x1, token + 1);
+            });
+        } else {
+            each(low, [&](float x, int token) {
+                if (-W.place(x) == bin)
+                    in_bin(x, token);
+            });
         }
         __syncthreads();
+        const int n = (int)S.n[lists++];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            none = max(none, (u64)__shfl_xor_sync(0xffffffffu, none, o));
+            most_ = max(most_, (u64)__shfl_xor_sync(0xffffffffu, most_, o));
+        }
+        const u64 seg = SUM ? warp_sum64(above.units()) : 0;
+        const u64 told[4] = {warp == 0 ? (u64)n : 0, none, most_, seg};
+        const Board board = publish(told);
+        const int all = (int)sum(board, 0);
+        if (all > RANKED) {
+            const u64 from = ~most(board, 1), to = most(board, 2);
+            return most(board, 0) <= FILTER_CAP ? refine<SUM, true>(W, n, from, to, ahead_, target)
+                                                : refine<SUM, false>(W, n, from, to, ahead_, target);
+        }
+        // every CTA ranks all of them
+        gather(board, 0);
+        if constexpr (!SUM)
+            cl_sync();   // the lists have been read: bins take their place
+        if (all == 0)
+            return floor;
+        rank_keys(S.l.key, all);
+        if constexpr (!SUM)
+            return S.l.key[min((int)(target - ahead_), all) - 1];
+        const u64 key = (int)threadIdx.x < all ? S.l.key[threadIdx.x] : 0;
+        u64 w = key ? W(value_of(key)) : 0, sum_;
+        const u64 at = ahead_ + block_scan64(w, S.sums, sum_);
+        if (threadIdx.x == 0)
+            S.cut = S.l.key[all - 1];   // where roundings leave the target behind the last
+        __syncthreads();
+        // the token whose weight reaches the target is the last
+        if (at < target && at + w >= target)
+            S.cut = key;
+        __syncthreads();
+        const u64 cut = max(S.cut, c_min);
+        // what stays of the bin, by segment
+        const int s = key >= cut && key ? ((token_of(key) + off) / T::N) / len : -1;
+        w = s >= 0 ? w : 0;
+        u64 total;
+        before = ahead(board, 3, total);
+        block_scan64(w, S.sums, sum_);
+        Z = total + sum_;
+        // ahead of this CTA's segments, and in them
+        block_scan64(s < rank * FW ? w : 0, S.sums, sum_);
+        before += sum_;
+        mine = seg;
+#pragma unroll 1
+        for (int k = 0; k < FW; ++k) {
+            block_scan64(s == rank * FW + k ? w : 0, S.sums, sum_);
+            before += k < warp ? sum_ : 0;
+            mine += k == warp ? sum_ : 0;
+        }
+        done = true;
+        return cut;
     }
 
     // The sum of the weights from `cut` on, of this warp's segment.
@@ -897,10 +921,15 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
     }
     if (listed) {
         const int own = R.stage(t0, [](float, int) { return true; });
-        const int count = R.send(own, own, 0, ~0ull);
+        const u64 x[1] = {R.warp == 0 ? (u64)own : 0};
+        const auto board = R.publish(x);
+        const int count = (int)R.sum(board, 0);
         if (count <= FILTER_CAP) {
+            if (rank == 0)
+                R.gather(board, 0);
+            cl_arrive();
             if (rank != 0) {
-                cl_wait_all();
+                cl_wait_all();   // their lists have been read
                 return;
             }
             // less than p of a total: the same as less than the next whole number
@@ -976,96 +1005,29 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
             cl_wait_all();
             return;
         }
-        cl_wait_all();
     }
 
     // ---- the cut by histograms over the row
-    u64 cut = 0, mine = 0, ahead, target;
-    bool done = false;   // S.seg of the first CTA holds the segments' weights
+    u64 cut = 0, mine = 0, ahead, target, Z = 0, before = 0;
+    bool done = false;   // Z and `before`, the weights ahead of this warp's segment, are known
     if (k < V) {
         const int bin = R.template bin_of_cut<false>(W, (double)k, 0, ahead, target);
-        if (bin >= 0) {
-            u64 from = ~0ull, to = 0;
-            const int n = R.stage(fmaxf(R_::below_bin(W, bin), W.low), [&](float y, int token) {
-                if (-W.place(y) != bin)
-                    return false;
-                const u64 key = R_::key_of(y, token);
-                from = key < from ? key : from;
-                to = key > to ? key : to;
-                return true;
-            });
-            if (R.template cut_in_bin<false>(W, n, from, to, ahead, target, cut) >= 0) {
-                cl_sync();
-                cut = *R.cl.map_shared_rank(&S.cut, 0);
-            }
-        }
+        if (bin >= 0)
+            cut = R.template cut_in_bin<false>(W, bin, 0, ahead, target, 0, done, Z, before, mine);
     }
     const u64 c_min = least > 0.0f ? (u64)filter_key(xmin) << 32 : 0;
     if (p < 1.0f) {
         const int bin = R.template bin_of_cut<true>(W, (double)fmaxf(p, 0.0f), cut, ahead, target);
-        if (least > 0.0f && (xmin >= W.low ? -W.place(xmin) : FINE) < bin) {
-            cut = c_min > cut ? c_min : cut;   // min-p cuts ahead of that bin
-        } else {
-            // weights above the bin, by segment; its tokens
-            const u64 floor = cut;
-            FilterSum above;
-            const float2 none = make_float2(0.0f, 0.0f);
-            u64 from = ~0ull, to = 0;
-            const int n = R.stage(fmaxf(R_::below_bin(W, bin), W.low), [&](float y, int token) {
-                const int at = -W.place(y);
-                if (at < bin) {
-                    uint32_t i0, i1;
-                    float q0, q1;
-                    upk(W.template split<R_::SHORT>(pk(y, y), i0, i1), q0, q1);
-                    above.add(W.value(i0, q0), none);
-                }
-                const u64 key = R_::key_of(y, token);
-                if (at != bin || key < floor)
-                    return false;
-                from = key < from ? key : from;
-                to = key > to ? key : to;
-                return true;
-            });
-            const u64 y[1] = {warp_sum64(above.units())};
-            const int count = R.template cut_in_bin<true>(W, n, from, to, ahead, target, cut);
-            if (count >= 0) {
-                const auto board = R.publish(y);
-                if (rank == 0) {
-                    for (int g = tid; g < R.C * FW; g += FT)
-                        S.seg[g] = board.get(0, g);
-                    __syncthreads();
-                    const u64 c = max(S.cut, c_min);
-                    if (tid < count && S.l.key[tid] >= c)
-                        atomicAdd(&S.seg[((R_::token_of(S.l.key[tid]) + R.off) / T::N) / R.len], W(R_::value_of(S.l.key[tid])));
-                    __syncthreads();
-                    if (tid == 0)
-                        S.cut = c;
-                }
-                done = true;
-                cl_sync();
-                cut = *R.cl.map_shared_rank(&S.cut, 0);
-            }
-        }
+        if (!(least > 0.0f && (xmin >= W.low ? -W.place(xmin) : FINE) < bin))   // else min-p cuts ahead of that bin
+            cut = R.template cut_in_bin<true>(W, bin, cut, ahead, target, c_min, done, Z, before, mine);
     }
     cut = c_min > cut ? c_min : cut;
-    u64 Z, before;
-    if (done) {
-        // the first CTA has the segments' weights
-        u64 all = 0, part = 0;
-        const u64 *seg = R.cl.map_shared_rank(S.seg, 0);
-        for (int g = R.lane; g < R.C * FW; g += 32) {
-            const u64 x = seg[g];
-            all += x;
-            part += g < R.segment() ? x : 0;
-        }
-        Z = warp_sum64(all);
-        before = warp_sum64(part);
-        mine = seg[R.segment()];
-    } else {
+    if (!done) {
         mine = R.mass(W, cut);
         const u64 x[1] = {mine};
         before = R.ahead(R.publish(x), 0, Z);
     }
+    cl_arrive();   // nothing of another CTA is read from here on
     rec.cut = cut ? R_::value_of(cut) : -F_INF;
     rec.last = (uint32_t)R_::token_of(cut);
     rec.Z = Z;
@@ -1087,44 +1049,46 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
         if (S.hi) {
             const int a0 = min((rank * FW + S.lo) * R.len, R.nv), a1 = min(a0 + R.len, R.nv);
             const u64 base = S.base;
-            u64 w[T::N], all;
-            // this thread's weights in the FT vectors from `a` on, `more` in units added to what is kept
-            auto weights = [&](int a, u64 more) {
-                u64 s = 0;
-                const uint4 q = a + tid < a1 ? R.vector(a + tid) : make_uint4(T::NONE, T::NONE, T::NONE, T::NONE);
+            // the segment's sum and its tokens' differ by roundings: where the uniform falls behind the last, it
+            // takes the last that has a weight; where none has one (half a unit), the first
+            u64 to = v - base, sum = 0;
+#pragma unroll 1
+            for (int again = 0; again < 3; ++again) {
+                u64 at = 0, all;
+                bool hit = false;
+#pragma unroll 1
+                for (int a = a0; a < a1 && !hit; a += FT) {
+                    u64 w[T::N], s = 0;
+                    const uint4 q = a + tid < a1 ? R.vector(a + tid) : make_uint4(T::NONE, T::NONE, T::NONE, T::NONE);
 #pragma unroll
-                for (int e = 0; e < T::N; ++e) {
-                    const float y = T::get(q, e);
-                    const bool in = y > -F_INF && (y > rec.cut || (y == rec.cut && (uint32_t)R.token(a + tid, e) <= rec.last));
-                    w[e] = in ? W(y) + more : 0;
-                    s += w[e];
-                }
-                return s;
-            };
-            u64 sum = 0;
-            for (int a = a0; a < a1; a += FT) {
-                block_scan64(weights(a, 0), S.sums, all);
-                sum += all;
-            }
-            // the segment's sum and its tokens' differ by roundings; tokens of less than a unit
-            // each may sum up to one
-            const u64 more = sum == 0;
-            const u64 to = sum == 0 ? 0 : min(v - base, sum - 1);
-            u64 at = 0;
-            for (int a = a0; a < a1; a += FT) {
-                u64 upto = weights(a, more);
-                upto = at + block_scan64(upto, S.sums, all);
+                    for (int e = 0; e < T::N; ++e) {
+                        const float y = T::get(q, e);
+                        const bool in = y > -F_INF && (y > rec.cut || (y == rec.cut && (uint32_t)R.token(a + tid, e) <= rec.last));
+                        w[e] = in ? W(y) + (again == 2) : 0;
+                        s += w[e];
+                    }
+                    u64 upto = at + block_scan64(s, S.sums, all);
+                    at += all;
+                    if (upto <= to && upto + s > to) {
 #pragma unroll
-                for (int e = 0; e < T::N; ++e) {
-                    if (w[e] && upto <= to && upto + w[e] > to)
-                        finish(R.token(a + tid, e), (float)((double)w[e] / (double)Z));
-                    upto += w[e];
+                        for (int e = 0; e < T::N; ++e) {
+                            if (w[e] && upto <= to && upto + w[e] > to)
+                                finish(R.token(a + tid, e), (float)((double)w[e] / (double)Z));
+                            upto += w[e];
+                        }
+                    }
+                    hit = to < at;
                 }
-                at += all;
+                if (hit)
+                    break;
+                sum = at;
+                to = sum ? sum - 1 : 0;
+                again += sum == 0;
             }
         }
     }
-    cl_sync();
+    __syncthreads();
+    cl_wait_all();
 }
 
 // ------------------------------------------------------------------ the rule

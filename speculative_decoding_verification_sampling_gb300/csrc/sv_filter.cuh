@@ -113,8 +113,12 @@ struct FilterWeight {
         uint32_t i, j;
         float q, r;
         upk(split<false>(pk(x, x), i, j), q, r);
-        const float2 w = value(i, q);
-        return (u64)(__float2ll_rn(w.x * FILTER_UNIT) + __float2ll_rn(w.y * FILTER_UNIT));
+        // 2^(i mod 64 / 64) (1 + q) in units, its correction in steps of 2^-33; then the rest of i as a shift
+        const float2 e = table[i & 63];
+        const long long v = (long long)((__float_as_uint(e.x) & 0x7fffffu) | 0x800000u) * (1 << 20) +
+                            (long long)__float2int_rn(fmaf(e.x, q, e.y) * 0x1p33f) * 1024;
+        const int n = (int)(__float_as_uint(ROUND) - i + 63) >> 6;   // ROUND's bits end in 22 zeros
+        return (u64)(v + (1ll << n >> 1)) >> n;
     }
 };
 
