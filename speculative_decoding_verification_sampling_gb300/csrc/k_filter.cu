@@ -202,30 +202,6 @@ __device__ __forceinline__ void part(int b, int shift, u64 &from, u64 &to)
     const u64 len = (1ull << shift) - 1;
     from = to - from <= len ? from : to - len;
 }
-// Of n keys of this CTA, all different, with weights (an entry's number to a number): the one, largest first, at
-// which the running sum over the keys in [from, to] reaches `target`, or the last of any weight.
-template <class F>
-__device__ __forceinline__ u64 select_key(const u64 *key, int n, u64 from, u64 to, u64 target, F weight, Search &S)
-{
-    u64 ahead = 0;
-#pragma unroll 1
-    while (from < to) {
-        const int shift = part_shift(from, to);
-        __syncthreads();
-        S.lo[threadIdx.x] = S.hi[threadIdx.x] = 0;
-        __syncthreads();
-        for (int i = threadIdx.x; i < n; i += FT)
-            if (key[i] >= from && key[i] <= to)
-                S.add((int)((to - key[i]) >> shift), weight(i));
-        __syncthreads();
-        const int b = S.find(S.lo[threadIdx.x] | (u64)S.hi[threadIdx.x] << 32, ahead, target);
-        if (b < 0)
-            break;
-        part(b, shift, from, to);
-    }
-    __syncthreads();
-    return from;
-}
 // Sorts n <= FT keys, all different, largest first: each thread counts the keys ahead of its own.
 __device__ __forceinline__ void rank_keys(u64 *key, int n)
 {
@@ -240,38 +216,28 @@ __device__ __forceinline__ void rank_keys(u64 *key, int n)
         key[at] = mine;
     __syncthreads();
 }
-// Of n entries with tokens and weights, in any order: the first, in ascending order of the token, at which the
-// running sum exceeds `at`.  hit(entry, token) is called by one thread.
-__device__ __forceinline__ u64 pick_key(int token, int entry)
-{
-    return (u64)(0xffffffffu - (uint32_t)token) * FILTER_CAP + (uint32_t)entry;
-}
+// Of n <= FT entries with tokens (the low words of the keys, inverted) and weights, in any order: the first, in
+// ascending order of the token, at which the running sum exceeds `at`.  hit(entry, token) is called by one thread.
 template <class F>
-__device__ __forceinline__ void pick(const u64 *key, const u64 *w, int n, int V, u64 at, Search &S, F hit)
+__device__ __forceinline__ void pick(const u64 *key, const u64 *w, int n, u64 at, F hit)
 {
-    auto is = [&](u64 k) { hit((int)(k % FILTER_CAP), (int)(0xffffffffu - (uint32_t)(k / FILTER_CAP))); };
-    __syncthreads();
-    if (n <= FT) {
-        if ((int)(threadIdx.x & ~31u) < n) {
-            const int i = min((int)threadIdx.x, n - 1);
-            const u64 mine = key[i];
-            u64 before = 0;
-            for (int j = 0; j < n; ++j)
-                before += key[j] > mine ? w[j] : 0;
-            if ((int)threadIdx.x < n && before <= at && before + w[i] > at)
-                is(mine);
-        }
+    if ((int)(threadIdx.x & ~31u) >= n)
         return;
-    }
-    const u64 k = select_key(key, n, pick_key(V, 0), pick_key(0, FILTER_CAP - 1), at + 1, [&](int i) { return w[i]; }, S);
-    if (threadIdx.x == 0)
-        is(k);
+    const int i = min((int)threadIdx.x, n - 1);
+    const uint32_t mine = (uint32_t)key[i];
+    u64 before = 0;
+    for (int j = 0; j < n; ++j)
+        before += (uint32_t)key[j] > mine ? w[j] : 0;
+    if ((int)threadIdx.x < n && before <= at && before + w[i] > at)
+        hit(i, (int)(0xffffffffu - mine));
 }
 
 constexpr int OCTAVES = 43;               // down to half a unit
 constexpr int FINE = OCTAVES * 64 + 64;   // bins of the weights' histogram
 constexpr int LISTS = 8;                  // lists of a row, at most
 constexpr int RANKED = FT;                // tokens of a bin that are ranked; more are sorted into finer bins first
+constexpr int STAGED = 2048;              // tokens in a CTA's own list
+constexpr int FEW = FILTER_CAP / 2;       // top-k by a list: a quarter of an octave more may reach the threshold
 struct RowShared {
     u64 slot[2][4][FW];   // published, by round parity: up to four numbers per warp
     u64 sums[FW], sums2[FW];
@@ -289,9 +255,8 @@ struct RowShared {
             uint32_t lo[FINE], hi[FINE];   // counts, or sums in two words
         } h;
         struct {
-            u64 key[FILTER_CAP];           // (logit, ~token)
-            u64 w[FILTER_CAP];
-        } l;                               // of the first CTA
+            u64 key[FT], w[STAGED];        // the cluster's list, (logit, ~token) keys; this CTA's own, and weights
+        } l;
     };
 };
 constexpr size_t ROW_SMEM = sizeof(RowShared);
@@ -519,7 +484,7 @@ struct Row {
 #pragma unroll
             for (int k = 0; k < T::N; ++k)
                 if (has >> k & 1) {
-                    if (at < FILTER_CAP)
+                    if (at < STAGED)
                         S.l.w[at] = key_of(T::get(q, k), token(v, k));
                     ++at;
                 }
@@ -532,10 +497,10 @@ struct Row {
     __device__ __forceinline__ void put(float x, int token)
     {
         const uint32_t at = atomicAdd(&S.n[lists], 1u);
-        if (at < FILTER_CAP)
+        if (at < STAGED)
             S.l.w[at] = key_of(x, token);
     }
-    // All CTAs' lists, n_r keys in the r-th (number i of the board's, of warp 0), up to FILTER_CAP together, to this
+    // All CTAs' lists, n_r keys in the r-th (number i of the board's, of warp 0), up to FT together, to this
     // CTA's S.l.key.
     __device__ __forceinline__ void gather(const Board &b, int i)
     {
@@ -543,17 +508,15 @@ struct Row {
         u64 n = lane < C ? b.get(i, lane * FW) : 0;
         const int end = (int)warp_scan64(n, lane), all = __shfl_sync(0xffffffffu, end, 31);
         const int begin = end - (int)n;
-        for (int k0 = 0; k0 < all; k0 += FT) {
-            const int k = k0 + threadIdx.x;
-            int r = 0, at = k;
-            for (int c = 1; c < C; ++c) {
-                const int o = __shfl_sync(0xffffffffu, begin, c);
-                if (k >= o)
-                    r = c, at = k - o;
-            }
-            if (k < all)
-                S.l.key[k] = cl.map_shared_rank(S.l.w, r)[at];
+        const int k = threadIdx.x;
+        int r = 0, at = k;
+        for (int c = 1; c < C; ++c) {
+            const int o = __shfl_sync(0xffffffffu, begin, c);
+            if (k >= o)
+                r = c, at = k - o;
         }
+        if (k < all)
+            S.l.key[k] = cl.map_shared_rank(S.l.w, r)[at];
         __syncthreads();
     }
 
@@ -727,8 +690,8 @@ struct Row {
         const int all = (int)sum(board, 0);
         if (all > RANKED) {
             const u64 from = ~most(board, 1), to = most(board, 2);
-            return most(board, 0) <= FILTER_CAP ? refine<SUM, true>(W, n, from, to, ahead_, target)
-                                                : refine<SUM, false>(W, n, from, to, ahead_, target);
+            return most(board, 0) <= STAGED ? refine<SUM, true>(W, n, from, to, ahead_, target)
+                                            : refine<SUM, false>(W, n, from, to, ahead_, target);
         }
         // every CTA ranks all of them
         gather(board, 0);
@@ -887,7 +850,7 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
 
     const float xmin = least > 0.0f ? __double2float_ru((double)m + S.least) : -F_INF;
     // ---- a threshold that what is kept reaches, for lists
-    const bool few = k <= FILTER_CAP / 2 && k <= FT / 2 * R.C;
+    const bool few = k <= FEW;
     bool listed = V <= FILTER_CAP;
     float t0 = p < 1.0f ? -F_INF : xmin;   // top-p's total counts what min-p drops
     if (!listed && few) {
@@ -934,70 +897,33 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
             }
             // less than p of a total: the same as less than the next whole number
             auto reach = [&](u64 total) { return max((u64)ceil((double)fmaxf(p, 0.0f) * (double)total), 1ull); };
-            u64 Z, all, last;
-            if (count <= FT) {
-                // ranked, a token per thread
-                rank_keys(S.l.key, count);
-                const u64 key = tid < count ? S.l.key[tid] : 0;
-                u64 w = tid < count && tid < k ? W(R_::value_of(key)) : 0;
-                const u64 at = block_scan64(w, S.sums, all);
-                const bool stays = tid < count && (tid == 0 || (tid < k && (p >= 1.0f || at < reach(all)) && R_::value_of(key) >= xmin));
-                w = stays ? w : 0;
-                S.l.w[tid] = w;
-                block_scan64(w, S.sums, Z);
-                block_scan64(stays, S.search.sums, all);
-                last = S.l.key[all - 1];
-            } else {
-                u64 s = 0;
-                for (int e = tid; e < count; e += FT)
-                    S.l.w[e] = W(R_::value_of(S.l.key[e]));
-                const u64 to = (u64)filter_key(m) << 32 | 0xffffffffu;
-                last = (u64)filter_key(t0) << 32;
-                if (k < count)
-                    last = select_key(S.l.key, count, last, to, (u64)k, [](int) { return 1ull; }, S.search);
-                if (p < 1.0f) {
-                    __syncthreads();
-                    for (int e = tid; e < count; e += FT)
-                        s += S.l.key[e] >= last ? S.l.w[e] : 0;
-                    block_scan64(s, S.sums, all);
-                    last = select_key(S.l.key, count, last, to, reach(all), [&](int e) { return S.l.w[e]; }, S.search);
-                }
-                const u64 c = least > 0.0f ? (u64)filter_key(xmin) << 32 : 0;
-                last = max(last, c);
-                s = 0;
-                __syncthreads();
-                for (int e = tid; e < count; e += FT) {
-                    if (S.l.key[e] < last)
-                        S.l.w[e] = 0;
-                    s += S.l.w[e];
-                }
-                block_scan64(s, S.sums, Z);
-            }
+            u64 Z, all;
+            // ranked, a token per thread
+            rank_keys(S.l.key, count);
+            const u64 key = tid < count ? S.l.key[tid] : 0;
+            u64 w = tid < count && tid < k ? W(R_::value_of(key)) : 0;
+            const u64 at = block_scan64(w, S.sums, all);
+            const bool stays = tid < count && (tid == 0 || (tid < k && (p >= 1.0f || at < reach(all)) && R_::value_of(key) >= xmin));
+            w = stays ? w : 0;
+            S.l.w[tid] = w;
+            block_scan64(w, S.sums, Z);
+            block_scan64(stays, S.search.sums, all);
+            const int n = (int)all;
+            const u64 last = S.l.key[n - 1];
             if (VERIFY) {
-                if (tid == 0)
-                    S.lo = 0;
-                __syncthreads();
-                if (!draft) {
+                if (!draft && tid < n) {
                     const size_t list = (size_t)(b * (P.K + 1) + i) * FILTER_CAP;
-                    for (int e = tid; e < count; e += FT)
-                        if (S.l.w[e]) {
-                            const int to = atomicAdd(&S.lo, 1);
-                            P.list_x[list + to] = R_::token_of(S.l.key[e]);
-                            P.list_w[list + to] = S.l.w[e];
-                        }
-                    __syncthreads();
-                    rec.n = S.lo;
+                    P.list_x[list + tid] = R_::token_of(key);
+                    P.list_w[list + tid] = w;
                 }
+                rec.n = draft ? -1 : n;
                 rec.cut = R_::value_of(last);
                 rec.last = (uint32_t)R_::token_of(last);
                 rec.Z = Z;
                 if (tid == 0)
                     finish(-1, 0.0f);
             } else {
-                __syncthreads();
-                for (int e = tid; e < count; e += FT)
-                    S.l.key[e] = pick_key(R_::token_of(S.l.key[e]), e);
-                pick(S.l.key, S.l.w, count, V, (u64)((double)u * (double)Z), S.search, [&](int e, int token) {
+                pick(S.l.key, S.l.w, n, (u64)((double)u * (double)Z), [&](int e, int token) {
                     finish(token, (float)((double)S.l.w[e] / (double)Z));
                 });
             }
@@ -1099,7 +1025,6 @@ struct DecideShared {
     int j, code, seg;
     u64 before;
     u64 key[FILTER_CAP], w[FILTER_CAP];
-    Search search;
 };
 
 template <class T>
@@ -1185,22 +1110,23 @@ __global__ void __launch_bounds__(FT) filter_decide(const __grid_constant__ Filt
         if (rank != 0)
             return;
         const size_t list = ((size_t)b * (K + 1) + j) * FILTER_CAP;
-        u64 sum = 0, all;
-        for (int e = tid; e < q.n; e += FT) {
-            const int x = P.list_x[list + e];
-            const u64 wq = P.list_w[list + e];
-            S.key[e] = pick_key(x, e);
-            S.w[e] = bonus ? wq : left(wq, weight(p, Wp, T::one(drf, row_q + x), x));
-            sum += S.w[e];
+        u64 w = 0, all;
+        if (tid < q.n) {
+            const int x = P.list_x[list + tid];
+            w = P.list_w[list + tid];
+            S.key[tid] = 0xffffffffu - (uint32_t)x;
+            S.w[tid] = w;
+            if (!bonus)
+                w = left(w, weight(p, Wp, T::one(drf, row_q + x), x));
         }
-        block_scan64(sum, S.sums, all);
-        if (all == 0) {
-            // nothing is left of the target beside the draft: from the target itself
-            for (int e = tid; e < q.n; e += FT)
-                S.w[e] = P.list_w[list + e];
+        block_scan64(w, S.sums, all);
+        // where nothing is left of the target beside the draft, from the target itself
+        if (all == 0)
             all = q.Z;
-        }
-        pick(S.key, S.w, q.n, V, (u64)(v * (double)all), S.search, [&](int, int token) { *out = token; });
+        else if (tid < q.n)
+            S.w[tid] = w;
+        __syncthreads();
+        pick(S.key, S.w, q.n, (u64)(v * (double)all), [&](int, int token) { *out = token; });
         return;
     }
     // over the vocabulary: a segment per warp, then the segment on which the uniform falls
@@ -1295,6 +1221,10 @@ cudaError_t rows(const FilterParams &P, int sms, cudaStream_t stream)
     // four CTAs to an SM: as many rows in flight as L2 holds beside other things, all CTAs busy where
     // there are few rows, and no part so short that the barriers are all there is
     int C = 1;
+#ifdef FILTER_C
+    C = FILTER_C;
+    if (0)
+#endif
     while (C < MAX_C && (std::min(n, (long long)(4 * sms / C)) * bytes > FLIGHT || bytes / C > 65536 * T::ES || (n * C < 4 * sms && bytes / C > 4096)))
         C *= 2;
     static std::atomic<uint64_t> raised{0};

@@ -305,7 +305,7 @@ struct FilterRow {
 };
 static_assert(sizeof(FilterRow) == 64, "a row's record");
 
-constexpr int FILTER_CAP = 2048;   // tokens of a row that are ranked together, and listed
+constexpr int FILTER_CAP = 256;    // tokens of a row that are ranked together, and listed
 constexpr int FILTER_MAX_V = 524288;
 
 struct FilterParams {
