@@ -50,7 +50,7 @@ constexpr int COARSE = 256;             // bins of the threads' maxima, a thread
 constexpr float RANGE = 64.0f;          // what these span: weights to 2^-64 of the largest
 constexpr int ST_INVALID = 1;
 #ifndef FILTER_FLIGHT
-#define FILTER_FLIGHT 56
+#define FILTER_FLIGHT 80
 #endif
 constexpr long long FLIGHT = (long long)FILTER_FLIGHT << 20;  // bytes of the rows in flight
 
@@ -78,6 +78,11 @@ struct RowF32 {
     {
         return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
     }
+    // a running maximum (NaN if any is)
+    typedef float Max;
+    static __device__ __forceinline__ Max start() { return -F_INF; }
+    static __device__ __forceinline__ Max larger(Max m, const uint4 &v) { return max_nan(m, largest(v)); }
+    static __device__ __forceinline__ float value(Max m) { return m; }
     static __device__ __forceinline__ float largest(const uint4 &v)
     {
         return max_nan(max_nan(get(v, 0), get(v, 1)), max_nan(get(v, 2), get(v, 3)));
@@ -113,6 +118,13 @@ struct RowBF16 {
         uint32_t r;
         asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
         return r;
+    }
+    typedef uint32_t Max;
+    static __device__ __forceinline__ Max start() { return NONE; }
+    static __device__ __forceinline__ Max larger(Max m, const uint4 &v) { return max2(max2(max2(m, v.x), max2(v.y, v.z)), v.w); }
+    static __device__ __forceinline__ float value(Max m)
+    {
+        return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
     }
     static __device__ __forceinline__ float largest(const uint4 &v)
     {
@@ -305,22 +317,41 @@ struct Row {
         }
         return T::load(base + (size_t)v * 16);
     }
-    // f(vector, its number) for every vector of vectors a .. b - 1 that falls to this lane of `lanes`, U loads in
-    // flight
+    // f(vector, its number) for every vector of this warp's segment that is this lane's, U loads in flight: for short
+    // f, with nothing to be asked of a vector but in the last round
     template <int U, class F>
-    __device__ __forceinline__ void vectors(int a, int b, int lane_, int lanes, F f) const
+    __device__ __forceinline__ void vectors(F f) const
     {
+        int v = seg0 + lane;
+        const int full = seg1 - (ragged && seg1 == nv);   // vectors that lie in the row
+        if (ragged && seg0 == 0 && seg1 > 0) {            // the row's first one
+            if (lane == 0) {
+                f(vector(0), 0);
+                v += 32;
+            }
+            __syncwarp();
+        }
+        const uint8_t *at = base + (size_t)v * 16;
 #pragma unroll 1
-        for (int v = a + lane_; v < b; v += lanes * U) {
+        for (; v + 32 * (U - 1) < full; v += 32 * U, at += 512 * U) {
             uint4 q[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (v + lanes * u < b)
-                    q[u] = vector(v + lanes * u);
+                q[u] = T::load(at + 512 * u);
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (v + lanes * u < b)
-                    f(q[u], v + lanes * u);
+                f(q[u], v + 32 * u);
+        }
+        if (v < seg1) {
+            uint4 q[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (v + 32 * u < seg1)
+                    q[u] = vector(v + 32 * u);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (v + 32 * u < seg1)
+                    f(q[u], v + 32 * u);
         }
     }
     // The same for this warp's segment, one vector at a time, the next one on its way: for longer f, which would
@@ -469,7 +500,7 @@ struct Row {
     __device__ __forceinline__ int stage(float from, F keep)
     {
         uint32_t *const n = &S.n[LISTS + lists];
-        vectors<4>(seg0, seg1, lane, 32, [&](const uint4 &q, int v) {
+        vectors<4>([&](const uint4 &q, int v) {
             if (!(T::largest(q) >= from))
                 return;
             uint32_t has = 0;
@@ -789,8 +820,9 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
         S.c_lo = temp > 0.0f ? (float)(c - (double)S.c_hi) : 0.0f;
         S.least = least > 0.0f ? t * log((double)least) : 0.0;
     }
-    float m = -F_INF;
-    R.template vectors<8>(R.seg0, R.seg1, R.lane, 32, [&](const uint4 &q, int) { m = max_nan(m, T::largest(q)); });
+    typename T::Max most = T::start();
+    R.template vectors<8>([&](const uint4 &q, int) { most = T::larger(most, q); });
+    float m = T::value(most);
     S.top[tid] = m;
 #pragma unroll
     for (int o = 16; o; o >>= 1)
