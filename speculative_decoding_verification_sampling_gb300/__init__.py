@@ -190,16 +190,17 @@ class Filters:
                    torch.full((B,), top_p, dtype=torch.float32, device=device),
                    torch.full((B,), min_p, dtype=torch.float32, device=device))
 
-    def _struct(self, B, device, name):
+    def _struct(self, B, index, name):
+        shape = (B,)
+
         def ptr(t, dtype, what):
             if t is None:
                 return None
-            _check(t, (B,), (dtype,), f"{name}.{what}")
-            _beside(device, t)
+            _need(t, shape, dtype, index, name, what)
             return t.data_ptr()
-        return _FiltersStruct(ptr(self.temperature, torch.float32, "temperature"),
-                              ptr(self.top_k, torch.int32, "top_k"), ptr(self.top_p, torch.float32, "top_p"),
-                              ptr(self.min_p, torch.float32, "min_p"))
+        return _FiltersStruct(ptr(self.temperature, torch.float32, ".temperature"),
+                              ptr(self.top_k, torch.int32, ".top_k"), ptr(self.top_p, torch.float32, ".top_p"),
+                              ptr(self.min_p, torch.float32, ".min_p"))
 
 
 # ------------------------------------------------------------------ helpers
@@ -214,13 +215,25 @@ def _check(t, shape, dtypes, name):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _beside(device, *tensors):
-    """The tensors of a call lie on one device, the current one: the launches go there."""
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on {t.device} and {device} in one call")
-    if device.index is not None and device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {device}, but cuda:{torch.cuda.current_device()} is the current device")
+def _index(t, name):
+    """The device of a call's first tensor, which must be the current one: the launches go there."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    index = t.get_device()
+    if index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{index}, but cuda:{torch.cuda.current_device()} is the current device")
+    return index
+
+
+def _need(t, shape, dtype, index, name, more=""):
+    """_check for one type, and the tensors of a call lie on one device."""
+    try:
+        if t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _check(t, shape, (dtype,), name + more)
+    raise ValueError(f"{name}{more} is on {t.device}, the call's other tensors on cuda:{index}")
 
 
 def _dt(t):
@@ -486,25 +499,28 @@ def spec_filter_sample(logits: torch.Tensor, uniforms: torch.Tensor, filters: Fi
     probabilities among what the filters keep) on the device."""
     if not isinstance(logits, torch.Tensor) or logits.dim() != 3:
         raise TypeError("logits must be a CUDA tensor [B][K][V]")
-    B, K, V = logits.shape
-    _check(logits, (B, K, V), (torch.float32, torch.bfloat16), "logits")
-    _check(uniforms, (B, K), (torch.float32,), "uniforms")
-    dev = logits.device
+    B, K, V = shape = logits.shape
+    index, dtype = _index(logits, "logits"), logits.dtype
+    if dtype is not torch.float32 and dtype is not torch.bfloat16 or not logits.is_contiguous():
+        _check(logits, shape, (torch.float32, torch.bfloat16), "logits")
+    rows = (B, K)
+    _need(uniforms, rows, torch.float32, index, "uniforms")
     if device_status is not None:
-        _check(device_status, (1,), (torch.int32,), "device_status")
-    fs = filters._struct(B, dev, "filters") if filters is not None else None
-    with _on(dev, stream) as before:
-        if out_tokens is None:
-            out_tokens = _new((B, K), torch.int32, dev, before)
-        if out_prob is None:
-            out_prob = _new((B, K), torch.float32, dev, before)
-    _check(out_tokens, (B, K), (torch.int32,), "out_tokens")
-    _check(out_prob, (B, K), (torch.float32,), "out_prob")
-    _beside(dev, uniforms, out_tokens, out_prob, device_status)
-    rc = load().spec_filter_sample(logits.data_ptr(), _dt(logits), uniforms.data_ptr(), B, K, V,
-                                   ctypes.byref(fs) if fs is not None else None, out_tokens.data_ptr(),
-                                   out_prob.data_ptr(), device_status.data_ptr() if device_status is not None else None,
-                                   _stream(dev, stream))
+        _need(device_status, (1,), torch.int32, index, "device_status")
+    fs = ctypes.byref(filters._struct(B, index, "filters")) if filters is not None else None
+    if out_tokens is None or out_prob is None:
+        dev = logits.device
+        with _on(dev, stream) as before:
+            if out_tokens is None:
+                out_tokens = _new(rows, torch.int32, dev, before)
+            if out_prob is None:
+                out_prob = _new(rows, torch.float32, dev, before)
+    _need(out_tokens, rows, torch.int32, index, "out_tokens")
+    _need(out_prob, rows, torch.float32, index, "out_prob")
+    st = _raw_stream(index) if stream is None else _stream(logits.device, stream)
+    rc = (_lib or load()).spec_filter_sample(
+        logits.data_ptr(), 1 if dtype is torch.bfloat16 else 0, uniforms.data_ptr(), B, K, V, fs,
+        out_tokens.data_ptr(), out_prob.data_ptr(), None if device_status is None else device_status.data_ptr(), st)
     if rc:
         raise SpecVerifyError(rc, "spec_filter_sample")
     return out_tokens, out_prob
@@ -512,6 +528,9 @@ def spec_filter_sample(logits: torch.Tensor, uniforms: torch.Tensor, filters: Fi
 
 def spec_filter_workspace_bytes(B: int, K: int, V: int) -> int:
     return int(load().spec_filter_workspace_bytes(int(B), int(K), int(V)))
+
+
+_filter_bytes = functools.lru_cache(maxsize=256)(spec_filter_workspace_bytes)
 
 
 def spec_verify_filtered(target: torch.Tensor, draft: torch.Tensor, draft_tokens: torch.Tensor,
@@ -529,31 +548,35 @@ def spec_verify_filtered(target: torch.Tensor, draft: torch.Tensor, draft_tokens
     spec_verify_attention does."""
     if not isinstance(target, torch.Tensor) or target.dim() != 3:
         raise TypeError("target must be a CUDA tensor [B][K+1][V]")
-    B, K1, V = target.shape
+    B, K1, V = shape = target.shape
     K = K1 - 1
-    _check(target, (B, K + 1, V), (torch.float32, torch.bfloat16), "target")
-    _check(draft, (B, K, V), (target.dtype,), "draft")
-    _check(draft_tokens, (B, K), (torch.int32,), "draft_tokens")
-    _check(uniforms, (B, K + 1, 2), (torch.float32,), "uniforms")
-    dev = target.device
+    index, dtype = _index(target, "target"), target.dtype
+    if dtype is not torch.float32 and dtype is not torch.bfloat16 or not target.is_contiguous():
+        _check(target, shape, (torch.float32, torch.bfloat16), "target")
+    _need(draft, (B, K, V), dtype, index, "draft")
+    _need(draft_tokens, (B, K), torch.int32, index, "draft_tokens")
+    _need(uniforms, (B, K1, 2), torch.float32, index, "uniforms")
     if device_status is not None:
-        _check(device_status, (1,), (torch.int32,), "device_status")
-    if workspace is not None and (not isinstance(workspace, torch.Tensor) or not workspace.is_cuda):
-        raise TypeError("workspace must be a CUDA tensor")
-    fs = filters._struct(B, dev, "filters") if filters is not None else None
-    ds = draft_filters._struct(B, dev, "draft_filters") if draft_filters is not None else None
+        _need(device_status, (1,), torch.int32, index, "device_status")
+    fs = ctypes.byref(filters._struct(B, index, "filters")) if filters is not None else None
+    ds = ctypes.byref(draft_filters._struct(B, index, "draft_filters")) if draft_filters is not None else None
+    dev = target.device
     st = _stream(dev, stream)
     with _on(dev, stream) as before:
-        out_tokens, out_accept_len = _outs(B, K, dev, out_tokens, out_accept_len, before)
-        _beside(dev, draft, draft_tokens, uniforms, out_tokens, out_accept_len, workspace, device_status)
+        if out_tokens is None:
+            out_tokens = _new((B, K1), torch.int32, dev, before)
+        if out_accept_len is None:
+            out_accept_len = _new((B,), torch.int32, dev, before)
         if workspace is None:
-            workspace = _scratch(spec_filter_workspace_bytes(B, K, V), dev, st)
-    rc = load().spec_verify_filtered(target.data_ptr(), _dt(target), draft.data_ptr(), draft_tokens.data_ptr(),
-                                     uniforms.data_ptr(), B, K, V, ctypes.byref(fs) if fs is not None else None,
-                                     ctypes.byref(ds) if ds is not None else None, out_tokens.data_ptr(),
-                                     out_accept_len.data_ptr(), workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(),
-                                     device_status.data_ptr() if device_status is not None else None, st)
+            workspace = _scratch(_filter_bytes(B, K, V), dev, st)
+        elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != index:
+            raise TypeError(f"workspace must be a CUDA tensor on cuda:{index}")
+    _need(out_tokens, (B, K1), torch.int32, index, "out_tokens")
+    _need(out_accept_len, (B,), torch.int32, index, "out_accept_len")
+    rc = (_lib or load()).spec_verify_filtered(
+        target.data_ptr(), 1 if dtype is torch.bfloat16 else 0, draft.data_ptr(), draft_tokens.data_ptr(),
+        uniforms.data_ptr(), B, K, V, fs, ds, out_tokens.data_ptr(), out_accept_len.data_ptr(), workspace.data_ptr(),
+        workspace.nbytes, None if device_status is None else device_status.data_ptr(), st)
     if rc:
         raise SpecVerifyError(rc, "spec_verify_filtered")
     return out_tokens, out_accept_len
@@ -772,55 +795,51 @@ def spec_verify_window_attention(q: torch.Tensor, cache: torch.Tensor, seq_len: 
         raise TypeError("q must be a CUDA tensor [B][T][Hq][D]")
     if not isinstance(cache, torch.Tensor) or cache.dim() != 5:
         raise TypeError("cache must be a CUDA tensor [B][L][2][Hkv][D]")
-    B, T, Hq, D = q.shape
-    L, H = cache.shape[1], cache.shape[3]
-    dev = q.device
-    quant = cache.dtype == torch.float8_e4m3fn
-    _check(q, (B, T, Hq, D), (torch.bfloat16,), "q")
-    _check(cache, (B, L, 2, H, D), (cache.dtype,) if quant else (torch.bfloat16,), "cache")
-    _check(seq_len, (B,), (torch.int32,), "seq_len")
+    B, T, Hq, D = shape = q.shape
+    _, L, _, H, _ = cache.shape
+    index = _index(q, "q")
+    quant = cache.dtype is torch.float8_e4m3fn
+    _need(q, shape, torch.bfloat16, index, "q")
+    _need(cache, (B, L, 2, H, D), cache.dtype if quant else torch.bfloat16, index, "cache")
+    _need(seq_len, (B,), torch.int32, index, "seq_len")
     if quant != (cache_scale is not None):
         raise ValueError("cache_scale goes with a float8_e4m3fn cache")
     if quant:
-        _check(cache_scale, (B, L, 2, H), (torch.uint8,), "cache_scale")
+        _need(cache_scale, (B, L, 2, H), torch.uint8, index, "cache_scale")
     if staged is not None:
-        _check(staged, (B, T, 2, H, D), (torch.bfloat16,), "staged")
+        _need(staged, (B, T, 2, H, D), torch.bfloat16, index, "staged")
     if mask is not None:
-        _check(mask, (B, T, T), (torch.uint8,), "mask")
-    if out is not None:
-        _check(out, (B, T, Hq, D), (torch.bfloat16,), "out")
-    if lse is not None:
-        _check(lse, (B, T, Hq), (torch.float32,), "lse")
+        _need(mask, (B, T, T), torch.uint8, index, "mask")
     if device_status is not None:
-        _check(device_status, (1,), (torch.int32,), "device_status")
-    if workspace is not None and (not isinstance(workspace, torch.Tensor) or not workspace.is_cuda):
-        raise TypeError("workspace must be a CUDA tensor")
+        _need(device_status, (1,), torch.int32, index, "device_status")
     window, sinks = int(window), int(sinks)
     if window < 1 or sinks < 0:
         raise ValueError("window must be at least 1 and sinks at least 0")
-    _beside(dev, cache, seq_len, cache_scale, staged, mask, out, lse, workspace, device_status)
-    nbytes = 0 if workspace is not None else _attention_bytes(B, T, Hq, H, D, 0, L)
-    if workspace is None and nbytes == 0:
-        raise SpecVerifyError(1, "spec_verify_window_attention")
+    dev = q.device
     st = _stream(dev, stream)
-    lib = load()
     with _on(dev, stream) as before:
         if out is None:
-            out = _new((B, T, Hq, D), torch.bfloat16, dev, before)
+            out = _new(shape, torch.bfloat16, dev, before)
         if lse is None:
             lse = _new((B, T, Hq), torch.float32, dev, before)
         if workspace is None:
+            nbytes = _attention_bytes(B, T, Hq, H, D, 0, L)
+            if nbytes == 0:
+                raise SpecVerifyError(1, "spec_verify_window_attention")
             workspace = _scratch(nbytes, dev, st)
+        elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != index:
+            raise TypeError(f"workspace must be a CUDA tensor on cuda:{index}")
+    _need(out, shape, torch.bfloat16, index, "out")
+    _need(lse, (B, T, Hq), torch.float32, index, "lse")
 
     def ptr(t):
         return t.data_ptr() if t is not None else None
     # past 2^31 a window or sinks are everything
-    rc = lib.spec_verify_window_attention(q.data_ptr(), cache.data_ptr(), ptr(cache_scale), int(quant),
-                                          seq_len.data_ptr(), ptr(staged), ptr(mask), min(window, 2**31 - 1),
-                                          min(sinks, 2**31 - 1), B, T, Hq, H, D, L,
-                                          float(sm_scale) if sm_scale is not None else D ** -0.5, out.data_ptr(),
-                                          lse.data_ptr(), workspace.data_ptr(),
-                                          workspace.numel() * workspace.element_size(), ptr(device_status), st)
+    rc = (_lib or load()).spec_verify_window_attention(
+        q.data_ptr(), cache.data_ptr(), ptr(cache_scale), int(quant), seq_len.data_ptr(), ptr(staged), ptr(mask),
+        min(window, 2**31 - 1), min(sinks, 2**31 - 1), B, T, Hq, H, D, L,
+        D ** -0.5 if sm_scale is None else float(sm_scale), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+        workspace.nbytes, ptr(device_status), st)
     if rc:
         raise SpecVerifyError(rc, "spec_verify_window_attention")
     return out, lse

@@ -48,7 +48,7 @@ def test_binding_rejects_what_is_not_a_cuda_tensor_of_the_right_kind():
     with pytest.raises(TypeError):
         sv.spec_verify_filtered(z, z, torch.zeros(2, 0, dtype=torch.int32), u)
     with pytest.raises(TypeError):
-        sv.Filters(temperature=torch.ones(2))._struct(2, z.device, "filters")
+        sv.Filters(temperature=torch.ones(2))._struct(2, 0, "filters")
 
 
 def test_oracle_keeps_by_the_definition():
