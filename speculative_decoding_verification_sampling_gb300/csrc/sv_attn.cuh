@@ -79,11 +79,14 @@ static_assert(AT_UNIT == 128 && attn_units(0) == 0 && attn_units(128) == 1 && at
 
 // A sliding window: of sequence b's cache entries, all its tokens see [0, sinks)
 // and [from, n); what only some of them see, up to T - 1 entries ahead of `from`,
-// the kernel that finishes the rows adds row by row, with their own bounds, and
-// FEW_SINKS sinks or fewer as well, which would take a unit each.  In units, the
-// sinks come first, then the entries from `from` on, wherever that lies, so a
-// window of 128 entries is one unit.
-constexpr int FEW_SINKS = 16;
+// the kernel that finishes the rows adds row by row, with their own bounds.  In
+// units, the sinks come first, then the entries from `from` on, wherever that lies,
+// so a window of 128 entries is one unit.  Few sinks under few rows are left to the
+// other kernel as well: a unit of its own takes a pair 1 to 1.8 us of one SM, an entry
+// of a row there 0.016 ns of the whole GPU (32 trees of 61 nodes, 64/8 heads, 16
+// sinks: 179 us a call row by row, 139 us in units; 256 sequences of 5 tokens, 32/8
+// heads, 4 sinks: 2048 units more are 13 us).
+constexpr int FEW_SINKS = 640;   // times a pair's rows
 struct AttnWindow {
     int n;      // entries of the sequence (0 where its length is out of range)
     int from;   // 0: every token sees all of them
@@ -97,8 +100,9 @@ struct AttnWindow {
         const int back = A.window - (A.staged ? A.T : 0);
         from = A.from ? A.from[b] : n - max(min(back, n), 0);
         from = from <= A.sinks ? 0 : from;
-        sinks = from > 0 && A.sinks > FEW_SINKS ? A.sinks : 0;
-        few = from > 0 && A.sinks <= FEW_SINKS ? A.sinks : 0;
+        const bool rows = A.sinks <= FEW_SINKS && A.sinks * min(A.T * A.G, 2 * AT_ROWS) <= FEW_SINKS;
+        sinks = from > 0 && !rows ? A.sinks : 0;
+        few = from > 0 && rows ? A.sinks : 0;
     }
     __device__ __forceinline__ int sink_units() const { return attn_units(sinks); }
     __device__ __forceinline__ int units() const { return attn_units(sinks) + attn_units(n - from); }
