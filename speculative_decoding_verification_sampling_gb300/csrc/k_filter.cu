@@ -277,20 +277,18 @@ constexpr size_t ROW_SMEM = sizeof(RowShared);
 __device__ __forceinline__ void cl_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cl_wait_all() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
+// A row in vectors of 16 bytes, cut into a segment per warp of the cluster.
 template <class T>
-struct Row {
-    static constexpr bool SHORT = T::ES == 2;
-    RowShared &S;
+struct RowView {
     cg::cluster_group cl;
     const uint8_t *base;    // a 16-byte boundary at or ahead of the row
     int C, rank, lane, warp;
     int seg0, seg1, len;    // vectors: of this warp's segment, of any
     int off, V, nv;         // tokens ahead of the row in its first vector; of the row; its vectors
     bool ragged;
-    uint32_t round = 0, lists = 0;
 
-    __device__ __forceinline__ Row(RowShared &s, const uint8_t *row, int vocab)
-        : S(s), cl(cg::this_cluster()), C((int)cl_size()), rank((int)cl_rank()), lane(threadIdx.x & 31),
+    __device__ __forceinline__ RowView(const uint8_t *row, int vocab)
+        : cl(cg::this_cluster()), C((int)cl_size()), rank((int)cl_rank()), lane(threadIdx.x & 31),
           warp(threadIdx.x >> 5), V(vocab)
     {
         off = (int)((reinterpret_cast<uintptr_t>(row) & 15) / T::ES);
@@ -371,6 +369,24 @@ struct Row {
             f(q, v);
         }
     }
+};
+
+template <class T>
+struct Row : RowView<T> {
+    static constexpr bool SHORT = T::ES == 2;
+    using RowView<T>::cl;
+    using RowView<T>::C;
+    using RowView<T>::rank;
+    using RowView<T>::lane;
+    using RowView<T>::warp;
+    using RowView<T>::len;
+    using RowView<T>::off;
+    using RowView<T>::segment;
+    using RowView<T>::token;
+    using RowView<T>::in_turn;
+    RowShared &S;
+    uint32_t round = 0, lists = 0;
+    __device__ __forceinline__ Row(RowShared &s, const uint8_t *row, int vocab) : RowView<T>(row, vocab), S(s) {}
     // f(logit, token) for the tokens of this warp's segment with logits of at least `from` and above minus infinity
     template <class F>
     __device__ __forceinline__ void each(float from, F f) const
@@ -500,7 +516,7 @@ struct Row {
     __device__ __forceinline__ int stage(float from, F keep)
     {
         uint32_t *const n = &S.n[LISTS + lists];
-        vectors<4>([&](const uint4 &q, int v) {
+        this->template vectors<4>([&](const uint4 &q, int v) {
             if (!(T::largest(q) >= from))
                 return;
             uint32_t has = 0;
@@ -551,12 +567,12 @@ struct Row {
         __syncthreads();
     }
 
-    // Where the head ends that has `share` tokens (SUM = false), or ahead of whose last token less than `share` of
+    // Where the head ends that has `count` tokens (SUM = false), or ahead of whose last token less than `p` of
     // the whole lies, among the tokens with keys from `floor` on: the bin of 1/64 octave that holds its last token,
     // with what lies ahead of the bin, and the whole (`target`: of which that is to be reached).  -1: there are no
     // more tokens of any weight.
     template <bool SUM>
-    __device__ __forceinline__ int bin_of_cut(const FilterWeight &W, double share, u64 floor, u64 &ahead_, u64 &target)
+    __device__ __forceinline__ int bin_of_cut(const FilterWeight &W, float p, int count, u64 floor, u64 &ahead_, u64 &target)
     {
         __syncthreads();
         for (int i = threadIdx.x; i < FINE; i += FT) {
@@ -600,9 +616,7 @@ struct Row {
             const u64 v = of_all(&S.h.lo[bin]) + (SUM ? of_all(&S.h.hi[bin]) << 16 : 0);
             if (!SUM)
                 return v;
-            const float2 e = S.table[-bin & 63];
-            return (u64)__double2ll_rn((double)v * ((double)e.x + (double)e.y) *
-                                       (double)__int_as_float((127 + 43 - 29 + (-bin >> 6)) << 23));
+            return W.of_bin(v, bin);
         };
         u64 s = 0;
         for (int e = 0; e < per; ++e)
@@ -611,7 +625,8 @@ struct Row {
         const u64 x[1] = {__shfl_sync(0xffffffffu, in, 31)};
         u64 all;
         u64 at = ahead(publish(x), 0, all) + in - s;
-        target = SUM ? max((u64)ceil(share * (double)all), 1ull) : (u64)share;
+        // less than p of the whole: the same as less than the next whole number
+        target = SUM ? max(share_up(p, all), 1ull) : (u64)count;
         u64 found = 0, before = 0;
         if (at < target && at + s >= target)
             for (int e = 0; e < per && !found; ++e) {
@@ -927,15 +942,13 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
                 cl_wait_all();   // their lists have been read
                 return;
             }
-            // less than p of a total: the same as less than the next whole number
-            auto reach = [&](u64 total) { return max((u64)ceil((double)fmaxf(p, 0.0f) * (double)total), 1ull); };
             u64 Z, all;
             // ranked, a token per thread
             rank_keys(S.l.key, count);
             const u64 key = tid < count ? S.l.key[tid] : 0;
             u64 w = tid < count && tid < k ? W(R_::value_of(key)) : 0;
             const u64 at = block_scan64(w, S.sums, all);
-            const bool stays = tid < count && (tid == 0 || (tid < k && (p >= 1.0f || at < reach(all)) && R_::value_of(key) >= xmin));
+            const bool stays = tid < count && (tid == 0 || (tid < k && (p >= 1.0f || at < max(share_up(fmaxf(p, 0.0f), all), 1ull)) && R_::value_of(key) >= xmin));
             w = stays ? w : 0;
             S.l.w[tid] = w;
             block_scan64(w, S.sums, Z);
@@ -955,7 +968,7 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
                 if (tid == 0)
                     finish(-1, 0.0f);
             } else {
-                pick(S.l.key, S.l.w, n, (u64)((double)u * (double)Z), [&](int e, int token) {
+                pick(S.l.key, S.l.w, n, share_down(u, Z), [&](int e, int token) {
                     finish(token, (float)((double)S.l.w[e] / (double)Z));
                 });
             }
@@ -969,13 +982,13 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
     u64 cut = 0, mine = 0, ahead, target, Z = 0, before = 0;
     bool done = false;   // Z and `before`, the weights ahead of this warp's segment, are known
     if (k < V) {
-        const int bin = R.template bin_of_cut<false>(W, (double)k, 0, ahead, target);
+        const int bin = R.template bin_of_cut<false>(W, 0.0f, k, 0, ahead, target);
         if (bin >= 0)
             cut = R.template cut_in_bin<false>(W, bin, 0, ahead, target, 0, done, Z, before, mine);
     }
     const u64 c_min = least > 0.0f ? (u64)filter_key(xmin) << 32 : 0;
     if (p < 1.0f) {
-        const int bin = R.template bin_of_cut<true>(W, (double)fmaxf(p, 0.0f), cut, ahead, target);
+        const int bin = R.template bin_of_cut<true>(W, fmaxf(p, 0.0f), 0, cut, ahead, target);
         if (!(least > 0.0f && (xmin >= W.low ? -W.place(xmin) : FINE) < bin))   // else min-p cuts ahead of that bin
             cut = R.template cut_in_bin<true>(W, bin, cut, ahead, target, c_min, done, Z, before, mine);
     }
@@ -994,7 +1007,7 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
             finish(-1, 0.0f);
     } else {
         // the segment on which the uniform falls, then the vector, by its whole CTA
-        const u64 v = (u64)((double)u * (double)Z);
+        const u64 v = share_down(u, Z);
         if (tid == 0)
             S.hi = 0;
         __syncthreads();
@@ -1056,6 +1069,7 @@ struct DecideShared {
     float2 table[64];
     int j, code, seg;
     u64 before;
+    FilterShare sq, sp;
     u64 key[FILTER_CAP], w[FILTER_CAP];
 };
 
@@ -1129,13 +1143,18 @@ __global__ void __launch_bounds__(FT) filter_decide(const __grid_constant__ Filt
     if (!bonus)
         p = rows[K + 1 + j];
     const FilterWeight Wq = of(q), Wp = of(p);
-    const double iq = 1.0 / (double)q.Z, ip = bonus ? 0.0 : 1.0 / (double)p.Z;
-    const double v = (double)__ldg(P.uniforms + ((size_t)b * (K + 1) + j) * 2 + 1);
+    if (tid == 0)
+        S.sq = FilterShare(q.Z);
+    else if (tid == 32 && !bonus)
+        S.sp = FilterShare(p.Z);
+    __syncthreads();
+    const FilterShare share_q = S.sq, share_p = S.sp;
+    const float v = __ldg(P.uniforms + ((size_t)b * (K + 1) + j) * 2 + 1);
     const size_t row_q = (size_t)j * V;
-    // (q - p)+ in units of 2^-62; nothing for equal ones, so the products are not to be fused with the difference
+    // (q - p)+ in units of 2^-62; nothing for equal ones
     auto left = [&](u64 wq, u64 wp) -> u64 {
-        const double r = __dsub_rn(__dmul_rn((double)wq, iq), __dmul_rn((double)wp, ip));
-        return r > 0.0 ? (u64)__double2ll_rn(r * 0x1p62) : 0;
+        const u64 x = share_q(wq), y = share_p(wp);
+        return x > y ? x - y : 0;
     };
     int32_t *out = P.out_tokens + (size_t)b * (K + 1) + j;
     if (q.n >= 0) {
@@ -1158,22 +1177,30 @@ __global__ void __launch_bounds__(FT) filter_decide(const __grid_constant__ Filt
         else if (tid < q.n)
             S.w[tid] = w;
         __syncthreads();
-        pick(S.key, S.w, q.n, (u64)(v * (double)all), [&](int, int token) { *out = token; });
+        pick(S.key, S.w, q.n, share_down(v, all), [&](int, int token) { *out = token; });
         return;
     }
     // over the vocabulary: a segment per warp, then the segment on which the uniform falls
-    const int each = (V + C * FW - 1) / (C * FW);
-    const int me = rank * FW + warp, e0 = min(me * each, V), e1 = min(e0 + each, V);
-    auto rest = [&](int token, u64 &wq) -> u64 {
-        wq = weight(q, Wq, T::one(tgt, row_q + token), token);
+    const RowView<T> R(tgt + row_q * T::ES, V);
+    const int me = R.segment();
+    auto rest = [&](float x, int token, u64 &wq) -> u64 {
+        wq = weight(q, Wq, x, token);
         return bonus || wq == 0 ? wq : left(wq, weight(p, Wp, T::one(drf, row_q + token), token));
     };
     u64 s = 0, sq = 0;
-    for (int x = e0 + lane; x < e1; x += 32) {
-        u64 wq;
-        s += rest(x, wq);
-        sq += wq;
-    }
+    R.in_turn([&](const uint4 &y, int at) {
+        if (!(T::largest(y) >= q.cut))
+            return;
+#pragma unroll
+        for (int k = 0; k < T::N; ++k) {
+            const float x = T::get(y, k);
+            if (x >= q.cut && x > -F_INF) {
+                u64 wq;
+                s += rest(x, R.token(at, k), wq);
+                sq += wq;
+            }
+        }
+    });
     s = warp_sum64(s);
     sq = warp_sum64(sq);
     if (lane == 0) {
@@ -1201,24 +1228,37 @@ __global__ void __launch_bounds__(FT) filter_decide(const __grid_constant__ Filt
         before = before_q;
         s = sq;
     }
-    const u64 at = (u64)(v * (double)all);
+    const u64 at = share_down(v, all);
     if (lane == 0 && before <= at && before + s > at) {
         S.seg = warp;
         S.before = before;
     }
     __syncthreads();
     if (S.seg >= 0) {
-        const int a0 = min((rank * FW + S.seg) * each, V), a1 = min(a0 + each, V);
+        // the same weights as above, so the uniform falls on one of them
+        const int a0 = min((rank * FW + S.seg) * R.len, R.nv), a1 = min(a0 + R.len, R.nv);
         u64 upto = S.before;
         for (int a = a0; a < a1; a += FT) {
-            u64 r = 0, wq, sum;
-            if (a + tid < a1) {
-                r = rest(a + tid, wq);
-                r = whole ? wq : r;
+            u64 r[T::N], sum, mine = 0;
+            const uint4 y = a + tid < a1 ? R.vector(a + tid) : make_uint4(T::NONE, T::NONE, T::NONE, T::NONE);
+#pragma unroll
+            for (int k = 0; k < T::N; ++k) {
+                const float x = T::get(y, k);
+                r[k] = 0;
+                if (x >= q.cut && x > -F_INF) {
+                    u64 wq;
+                    r[k] = rest(x, R.token(a + tid, k), wq);
+                    r[k] = whole ? wq : r[k];
+                }
+                mine += r[k];
             }
-            const u64 mine = upto + block_scan64(r, S.sums, sum);
-            if (r && mine <= at && mine + r > at)
-                *out = a + tid;
+            u64 to = upto + block_scan64(mine, S.sums, sum);
+#pragma unroll
+            for (int k = 0; k < T::N; ++k) {
+                if (r[k] && to <= at && to + r[k] > at)
+                    *out = R.token(a + tid, k);
+                to += r[k];
+            }
             upto += sum;
         }
     }

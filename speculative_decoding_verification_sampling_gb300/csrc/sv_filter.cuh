@@ -120,6 +120,14 @@ struct FilterWeight {
         const int n = (int)(__float_as_uint(ROUND) - i + 63) >> 6;   // ROUND's bits end in 22 zeros
         return (u64)(v + (1ll << n >> 1)) >> n;
     }
+    // The weights whose sum of 1 + q is v 2^-29 and whose i is -bin, in units
+    __device__ __forceinline__ u64 of_bin(u64 v, int bin) const
+    {
+        const float2 e = table[-bin & 63];
+        const u64 t = (u64)((__float_as_uint(e.x) & 0x7fffffu) | 0x800000u) * (1u << 20) +
+                      (long long)__float2int_rn(e.y * 0x1p33f) * 1024;
+        return __umul64hi(v << 15, t << 20) >> ((bin + 63) >> 6);   // v < 2^48
+    }
 };
 
 // A thread's two sums of weights: the rounding errors of the larger halves go with the smaller ones, so a sum is
@@ -142,6 +150,27 @@ struct FilterSum {
         return (u64)(__float2ll_rn((a - 1.0f) * FILTER_UNIT) + __float2ll_rn((b - 1.0f) * FILTER_UNIT) +
                      __float2ll_rn(x * FILTER_UNIT) + __float2ll_rn(y * FILTER_UNIT));
     }
+};
+
+// What a number in [0, 1) is of a sum, downward and upward: exact products, without the 64-bit floating-point unit
+// (16 clocks of an SM to a warp's instruction).
+__device__ __forceinline__ u64 share_down(float u, u64 sum) { return __umul64hi(sum, __float2ull_rz(u * 0x1p64f)); }
+__device__ __forceinline__ u64 share_up(float u, u64 sum)
+{
+    const u64 f = __float2ull_rz(u * 0x1p64f);
+    return __umul64hi(sum, f) + (sum * f != 0);
+}
+// w / Z in units of 2^-62, for w <= Z: the same number for the same w and Z.
+struct FilterShare {
+    u64 r;
+    int e;
+    FilterShare() = default;
+    __device__ __forceinline__ explicit FilterShare(u64 Z)
+    {
+        e = __clzll((long long)Z);
+        r = (u64)(0x1p126 / (double)(Z << e));
+    }
+    __device__ __forceinline__ u64 operator()(u64 w) const { return __umul64hi(w << e, r); }
 };
 
 // Floats in their order, as unsigned numbers; -0 counts as 0.
