@@ -249,6 +249,8 @@ constexpr int FINE = OCTAVES * 64 + 64;   // bins of the weights' histogram
 constexpr int LISTS = 8;                  // lists of a row, at most
 constexpr int RANKED = FT;                // tokens of a bin that are ranked; more are sorted into finer bins first
 constexpr int STAGED = 2048;              // tokens in a CTA's own list
+constexpr int KEYS = 2048;                // 16 bits: the values of 16 octaves, of either sign
+constexpr int ODD = 1024;                 // logits closer to 0 in a CTA's part
 constexpr int FEW = FILTER_CAP / 2;       // top-k by a list: a quarter of an octave more may reach the threshold
 struct RowShared {
     u64 slot[2][4][FW];   // published, by round parity: up to four numbers per warp
@@ -258,6 +260,8 @@ struct RowShared {
     float top[FT];        // the threads' maxima
     uint32_t coarse[COARSE];
     uint32_t n[2 * LISTS];   // lengths of lists, and of a CTA's own
+    float seg_cut;           // where the segment is cut that the uniform falls on
+    uint32_t seg_last;
     u64 cut, base;
     double least;         // T ln(min_p)
     float c_hi, c_lo;
@@ -266,6 +270,11 @@ struct RowShared {
         struct {
             uint32_t lo[FINE], hi[FINE];   // counts, or sums in two words
         } h;
+        struct {
+            uint32_t n[2 * KEYS + 2];      // how often each value occurs
+            u64 odd[ODD];
+        } v;
+        float2 value[2 * KEYS + 2];        // weights of the values
         struct {
             u64 key[FT], w[STAGED];        // the cluster's list, (logit, ~token) keys; this CTA's own, and weights
         } l;
@@ -384,6 +393,8 @@ struct Row : RowView<T> {
     using RowView<T>::segment;
     using RowView<T>::token;
     using RowView<T>::in_turn;
+    using RowView<T>::seg0;
+    using RowView<T>::seg1;
     RowShared &S;
     uint32_t round = 0, lists = 0;
     __device__ __forceinline__ Row(RowShared &s, const uint8_t *row, int vocab) : RowView<T>(row, vocab), S(s) {}
@@ -780,6 +791,227 @@ struct Row : RowView<T> {
         return cut;
     }
 
+    // ---- logits of 16 bits take few values: how often each occurs says all that a cut needs, and a value's weight is
+    // computed once, not once a token.  Values in their order, largest first: 16 octaves of positive ones, those
+    // closer to 0 (one place for all, and a list: about 1 in 2^11 of a row's), 16 octaves of negative ones.
+    struct Values {
+        int base;   // of the 16 octaves' absolute bits
+        __device__ __forceinline__ explicit Values(const FilterWeight &W)
+        {
+            base = (int)((__float_as_uint(fmaxf(fabsf(W.m), fabsf(W.low))) + 0xffffu) >> 16) - (KEYS - 1);
+        }
+        // of a logit at or above W.low
+        __device__ __forceinline__ int place(float x) const
+        {
+            const uint32_t b = __float_as_uint(x + 0.0f);   // -0 is 0
+            const int t = (int)((b >> 16) & 0x7fffu) - base + 1;   // 1 .. KEYS, or less
+            return t <= 0 ? KEYS : (int)b < 0 ? KEYS + t : KEYS - t;
+        }
+        __device__ __forceinline__ float at(int place) const
+        {
+            const int t = place < KEYS ? KEYS - place : place - KEYS;
+            const int a = max(t - 1 + base, 0);
+            return __uint_as_float((uint32_t)(a << 16) | (place > KEYS ? 0x80000000u : 0u));
+        }
+    };
+    // The cut by top-k (k <= 0: none), top-p (p >= 1: none) and min-p: Z, what lies ahead of this warp's segment and in
+    // it, and where the cut lies in this segment.  `owner`: this lane tells the row's cut.  False: not found this way.
+    __device__ __forceinline__ bool by_values(const FilterWeight &W, int k, float p, float xmin, u64 &Z, u64 &before,
+                                              u64 &mine, float &cut_x, uint32_t &cut_last, bool &owner)
+    {
+        const Values values(W);
+        constexpr int N = 2 * KEYS + 1;
+        __syncthreads();
+        for (int i = threadIdx.x; i < N; i += FT)
+            S.v.n[i] = 0;
+        uint32_t *const odd = &S.n[LISTS + lists++];
+        __syncthreads();
+        in_turn([&](const uint4 &q, int v) {
+            if (!(T::largest(q) >= W.low))
+                return;
+#pragma unroll
+            for (int e = 0; e < T::N; ++e) {
+                const float x = T::get(q, e);
+                if (!(x >= W.low))
+                    continue;
+                const int at = values.place(x);
+                if (at != KEYS) {
+                    atomicAdd(&S.v.n[at], 1u);
+                } else {
+                    const uint32_t i = atomicAdd(odd, 1u);
+                    if (i < ODD)
+                        S.v.odd[i] = key_of(x, token(v, e));
+                }
+            }
+        });
+        __syncthreads();
+        const int nodd = (int)*odd;
+        u64 w_odd = 0;
+        for (int i = threadIdx.x; i < min(nodd, ODD); i += FT)
+            w_odd += W(value_of(S.v.odd[i]));
+        const u64 told[2] = {(u64)nodd, warp_sum64(w_odd)};
+        const Board board = publish(told);
+        if (most(board, 0) > ODD)
+            return false;
+        const u64 all_odd = sum(board, 0) / FW, sum_odd = sum(board, 1);
+        // this CTA's share of the values, a thread's in a row: their numbers and weights
+        const int per = (N + C * FT - 1) / (C * FT), first = (rank * FT + threadIdx.x) * per;
+        auto value_at = [&](int i, u64 &n, u64 &w) {
+            n = w = 0;
+            if (i == KEYS) {
+                n = all_odd;
+                w = sum_odd;
+            } else if (i < N) {
+                n = of_all(&S.v.n[i]);
+                w = n ? n * W(values.at(i)) : 0;
+            }
+        };
+        u64 sn = 0, sw = 0;
+        for (int e = 0; e < per; ++e) {
+            u64 n, w;
+            value_at(first + e, n, w);
+            sn += n;
+            sw += w;
+        }
+        const u64 in_n = warp_scan64(sn, lane), in_w = warp_scan64(sw, lane);
+        const u64 ours[2] = {__shfl_sync(0xffffffffu, in_n, 31), __shfl_sync(0xffffffffu, in_w, 31)};
+        const Board b2 = publish(ours);
+        u64 total, total_n;
+        const u64 at_n = ahead(b2, 0, total_n) + in_n - sn, at_w = ahead(b2, 1, total) + in_w - sw;
+        // the value that holds the cut: found by one thread, told to all with what lies ahead of it
+        auto find = [&](bool here, auto reached, u64 &n0, u64 &w0) {
+            u64 found = 0, n_ahead = at_n, w_ahead = at_w;
+            if (here)
+                for (int e = 0; e < per && !found; ++e) {
+                    u64 n, w;
+                    value_at(first + e, n, w);
+                    if (reached(n_ahead + n, w_ahead + w)) {
+                        found = (u64)(first + e) + 1;
+                    } else {
+                        n_ahead += n;
+                        w_ahead += w;
+                    }
+                }
+            const unsigned who = __ballot_sync(0xffffffffu, found != 0);
+            const int from = who ? __ffs(who) - 1 : 0;
+            const u64 x[3] = {__shfl_sync(0xffffffffu, found, from), who ? (u64)__shfl_sync(0xffffffffu, n_ahead, from) : 0,
+                              who ? (u64)__shfl_sync(0xffffffffu, w_ahead, from) : 0};
+            const Board b = publish(x);
+            found = most(b, 0);
+            n0 = most(b, 1);
+            w0 = most(b, 2);
+            return (int)found - 1;
+        };
+        int place = -1;
+        u64 ties = ~0ull, n0, w0;   // tokens of that value that stay
+        if (k > 0 && (u64)k < total_n) {
+            place = find(at_n < (u64)k && at_n + sn >= (u64)k, [&](u64 n, u64) { return n >= (u64)k; }, n0, w0);
+            if (place == KEYS)
+                return false;
+            ties = (u64)k - n0;
+            total = w0 + ties * W(values.at(place));
+        }
+        if (p < 1.0f) {
+            // less than p of the whole: the same as less than the next whole number
+            const u64 target = max(share_up(fmaxf(p, 0.0f), total), 1ull);
+            place = find(at_w < target && at_w + sw >= target, [&](u64, u64 w) { return w >= target; }, n0, w0);
+            if (place == KEYS)
+                return false;
+            const u64 w = W(values.at(place));
+            ties = (target - w0 + w - 1) / w;
+        }
+        float x0 = place >= 0 ? values.at(place) : W.low;
+        if (place < 0)
+            ties = ~0ull;
+        if (xmin > x0) {
+            x0 = xmin;
+            ties = ~0ull;
+        }
+        x0 = fmaxf(x0, W.low);
+        // ---- the weights of the values that stay, then each segment's
+        const int top = values.place(W.m), end = values.place(x0);
+        cl_sync();   // all have read the numbers
+        for (int i = top + threadIdx.x; i <= end; i += FT)
+            if (i != KEYS) {
+                uint32_t a, b;
+                float y, z;
+                upk(W.template split<SHORT>(pk(values.at(i), values.at(i)), a, b), y, z);
+                S.value[i] = W.value(a, y);
+            }
+        __syncthreads();
+        FilterSum above;
+        u64 tied = 0;
+        in_turn([&](const uint4 &q, int) {
+            if (!(T::largest(q) >= x0))
+                return;
+#pragma unroll
+            for (int e = 0; e < T::N; e += 2) {
+                const float a = T::get(q, e), b = T::get(q, e + 1);
+                float2 u = make_float2(0.0f, 0.0f), v = u;
+                auto look = [&](float x) {
+                    const int at = values.place(x);
+                    if (at != KEYS)
+                        return S.value[at];
+                    uint32_t i, j;
+                    float y, z;
+                    upk(W.template split<SHORT>(pk(x, x), i, j), y, z);
+                    return W.value(i, y);
+                };
+                if (a > x0)
+                    u = look(a);
+                if (b > x0)
+                    v = look(b);
+                above.add(u, v);
+                tied += (a == x0) + (b == x0);
+            }
+        });
+        tied = warp_sum64(tied);
+        const u64 w = W(x0), seg = warp_sum64(above.units());
+        const u64 last[2] = {seg, tied};
+        const Board b3 = publish(last);
+        u64 all, all_tied;
+        before = ahead(b3, 0, all);
+        const u64 tied_ahead = ahead(b3, 1, all_tied);
+        ties = min(ties, all_tied);
+        const u64 here = tied_ahead >= ties ? 0 : min(ties - tied_ahead, tied);   // of this segment's
+        before += min(tied_ahead, ties) * w;
+        mine = seg + here * w;
+        Z = all + ties * w;
+        cut_x = x0;
+        cut_last = 0xffffffffu;
+        owner = rank == 0 && threadIdx.x == 0 && ties == all_tied;
+        if (here == 0 && ties < all_tied) {
+            cut_x = __int_as_float(__float_as_int(x0 + 0.0f) + (x0 >= 0.0f ? 1 : -1));   // nothing at x0 stays
+        } else if (tied_ahead + here == ties && ties < all_tied) {
+            // the token of the last one that stays
+            u64 seen = 0;
+            for (int v = seg0; v < seg1; v += 32) {
+                const uint4 q = v + lane < seg1 ? this->vector(v + lane) : make_uint4(T::NONE, T::NONE, T::NONE, T::NONE);
+                int n = 0;
+#pragma unroll
+                for (int e = 0; e < T::N; ++e)
+                    n += T::get(q, e) == x0;
+                u64 upto = seen + warp_scan64((u64)n, lane);
+                const unsigned who = __ballot_sync(0xffffffffu, upto >= here);
+                if (who == 0) {
+                    seen = __shfl_sync(0xffffffffu, upto, 31);
+                    continue;
+                }
+                const int l = __ffs(who) - 1;
+                int t = -1;
+                upto -= n;
+#pragma unroll
+                for (int e = 0; e < T::N; ++e)
+                    if (T::get(q, e) == x0 && ++upto == here)
+                        t = token(v + lane, e);
+                cut_last = (uint32_t)__shfl_sync(0xffffffffu, t, l);
+                break;
+            }
+            owner = lane == 0;
+        }
+        return true;
+    }
+
     // The sum of the weights from `cut` on, of this warp's segment.
     __device__ __forceinline__ u64 mass(const FilterWeight &W, u64 cut) const
     {
@@ -981,13 +1213,17 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
     // ---- the cut by histograms over the row
     u64 cut = 0, mine = 0, ahead, target, Z = 0, before = 0;
     bool done = false;   // Z and `before`, the weights ahead of this warp's segment, are known
-    if (k < V) {
+    bool owner = rank == 0 && tid == 0;   // writes the record
+    if (R_::SHORT && (k < V || p < 1.0f))
+        done = R.by_values(W, k < V ? k : 0, p, xmin, Z, before, mine, rec.cut, rec.last, owner);
+    const bool valued = done;
+    if (!done && k < V) {
         const int bin = R.template bin_of_cut<false>(W, 0.0f, k, 0, ahead, target);
         if (bin >= 0)
             cut = R.template cut_in_bin<false>(W, bin, 0, ahead, target, 0, done, Z, before, mine);
     }
     const u64 c_min = least > 0.0f ? (u64)filter_key(xmin) << 32 : 0;
-    if (p < 1.0f) {
+    if (!done && p < 1.0f) {
         const int bin = R.template bin_of_cut<true>(W, fmaxf(p, 0.0f), 0, cut, ahead, target);
         if (!(least > 0.0f && (xmin >= W.low ? -W.place(xmin) : FINE) < bin))   // else min-p cuts ahead of that bin
             cut = R.template cut_in_bin<true>(W, bin, cut, ahead, target, c_min, done, Z, before, mine);
@@ -999,11 +1235,13 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
         before = R.ahead(R.publish(x), 0, Z);
     }
     cl_arrive();   // nothing of another CTA is read from here on
-    rec.cut = cut ? R_::value_of(cut) : -F_INF;
-    rec.last = (uint32_t)R_::token_of(cut);
+    if (!valued) {
+        rec.cut = cut ? R_::value_of(cut) : -F_INF;
+        rec.last = (uint32_t)R_::token_of(cut);
+    }
     rec.Z = Z;
     if (VERIFY) {
-        if (rank == 0 && tid == 0)
+        if (owner)
             finish(-1, 0.0f);
     } else {
         // the segment on which the uniform falls, then the vector, by its whole CTA
@@ -1015,9 +1253,13 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
             S.hi = 1;
             S.lo = R.warp;
             S.base = before;
+            S.seg_cut = rec.cut;   // as that segment has it
+            S.seg_last = rec.last;
         }
         __syncthreads();
         if (S.hi) {
+            rec.cut = S.seg_cut;
+            rec.last = S.seg_last;
             const int a0 = min((rank * FW + S.lo) * R.len, R.nv), a1 = min(a0 + R.len, R.nv);
             const u64 base = S.base;
             // the segment's sum and its tokens' differ by roundings: where the uniform falls behind the last, it
