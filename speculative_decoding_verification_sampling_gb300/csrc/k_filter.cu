@@ -453,15 +453,16 @@ struct Row : RowView<T> {
         cl_sync();
         return Board{at, cl};
     }
-    // A number per warp: their sum ahead of this warp's, and in all
-    __device__ __forceinline__ u64 ahead(const Board &b, int i, u64 &total) const
+    // A number per warp: their sum ahead of this warp's (or of the first `end`), and in all
+    __device__ __forceinline__ u64 ahead(const Board &b, int i, u64 &total) const { return ahead(b, i, total, segment()); }
+    __device__ __forceinline__ u64 ahead(const Board &b, int i, u64 &total, int end) const
     {
         u64 x[MAX_C * FW / 32], all = 0, mine = 0;
         read(b, i, x);
 #pragma unroll
         for (int k = 0; k < MAX_C * FW / 32; ++k) {
             all += x[k];
-            mine += lane + 32 * k < segment() ? x[k] : 0;
+            mine += lane + 32 * k < end ? x[k] : 0;
         }
         total = warp_sum64(all);
         return warp_sum64(mine);
@@ -814,9 +815,11 @@ struct Row : RowView<T> {
             return __uint_as_float((uint32_t)(a << 16) | (place > KEYS ? 0x80000000u : 0u));
         }
     };
-    // The cut by top-k (k <= 0: none), top-p (p >= 1: none) and min-p: Z, what lies ahead of this warp's segment and in
-    // it, and where the cut lies in this segment.  `owner`: this lane tells the row's cut.  False: not found this way.
-    __device__ __forceinline__ bool by_values(const FilterWeight &W, int k, float p, float xmin, u64 &Z, u64 &before,
+    // The cut by top-k (k <= 0: none), top-p (p >= 1: none) and min-p, and Z.  DRAW: in the CTA on which the uniform u
+    // falls, what lies ahead of this warp's segment and in it (`mine`; 0 elsewhere), and where the cut lies in the
+    // segment.  `owner`: this lane has the row's cut.  False: not found this way.
+    template <bool DRAW>
+    __device__ __forceinline__ bool by_values(const FilterWeight &W, int k, float p, float xmin, float u, u64 &Z, u64 &before,
                                               u64 &mine, float &cut_x, uint32_t &cut_last, bool &owner)
     {
         const Values values(W);
@@ -928,61 +931,100 @@ struct Row : RowView<T> {
             ties = ~0ull;
         }
         x0 = fmaxf(x0, W.low);
-        // ---- the weights of the values that stay, then each segment's
-        const int top = values.place(W.m), end = values.place(x0);
-        cl_sync();   // all have read the numbers
-        for (int i = top + threadIdx.x; i <= end; i += FT)
-            if (i != KEYS) {
-                uint32_t a, b;
-                float y, z;
-                upk(W.template split<SHORT>(pk(values.at(i), values.at(i)), a, b), y, z);
-                S.value[i] = W.value(a, y);
+        // ---- each CTA's weights above x0, and how many of its tokens have x0, from its own numbers
+        const u64 w0_ = W(x0);
+        u64 m = 0, tied = 0;
+        for (int i = threadIdx.x; i < N; i += FT) {
+            const uint32_t n = S.v.n[i];
+            const float x = values.at(i);
+            if (n && x >= x0) {
+                if (x > x0)
+                    m += n * W(x);
+                else
+                    tied += n;
             }
+        }
+        for (int i = threadIdx.x; i < nodd; i += FT) {
+            const float x = value_of(S.v.odd[i]);
+            if (x > x0)
+                m += W(x);
+            tied += x == x0;
+        }
+        const u64 parts[2] = {warp_sum64(m), warp_sum64(tied)};
+        const Board b3 = publish(parts);
+        u64 all, all_tied;
+        const u64 m_ahead = ahead(b3, 0, all, rank * FW), tied_ahead = ahead(b3, 1, all_tied, rank * FW);
+        const u64 m_to = ahead(b3, 0, all, rank * FW + FW), tied_to = ahead(b3, 1, all_tied, rank * FW + FW);
+        ties = min(ties, all_tied);
+        Z = all + ties * w0_;
+        cut_x = x0;
+        cut_last = 0xffffffffu;
+        owner = rank == 0 && threadIdx.x == 0 && ties == all_tied;
+        before = m_ahead + min(tied_ahead, ties) * w0_;
+        mine = 0;
+        const bool splits = ties < all_tied && tied_ahead < ties && ties <= tied_to;   // the last tie that stays is here
+        const bool drawn = DRAW && before <= share_down(u, Z) && share_down(u, Z) < m_to + min(tied_to, ties) * w0_;
+        if (!splits && !drawn)
+            return true;
+        // ---- the same for each warp's segment of this CTA: by a pass over its part, the values' weights at hand
+        const int top = values.place(W.m), end = values.place(x0);
+        __syncthreads();
+        if (DRAW)
+            for (int i = top + threadIdx.x; i <= end; i += FT)
+                if (i != KEYS) {
+                    uint32_t a, b;
+                    float y, z;
+                    upk(W.template split<SHORT>(pk(values.at(i), values.at(i)), a, b), y, z);
+                    S.value[i] = W.value(a, y);
+                }
         __syncthreads();
         FilterSum above;
-        u64 tied = 0;
+        tied = 0;
         in_turn([&](const uint4 &q, int) {
             if (!(T::largest(q) >= x0))
                 return;
 #pragma unroll
             for (int e = 0; e < T::N; e += 2) {
                 const float a = T::get(q, e), b = T::get(q, e + 1);
-                float2 u = make_float2(0.0f, 0.0f), v = u;
-                auto look = [&](float x) {
-                    const int at = values.place(x);
-                    if (at != KEYS)
-                        return S.value[at];
-                    uint32_t i, j;
-                    float y, z;
-                    upk(W.template split<SHORT>(pk(x, x), i, j), y, z);
-                    return W.value(i, y);
-                };
-                if (a > x0)
-                    u = look(a);
-                if (b > x0)
-                    v = look(b);
-                above.add(u, v);
+                if (DRAW) {
+                    float2 u0 = make_float2(0.0f, 0.0f), u1 = u0;
+                    auto look = [&](float x) {
+                        const int at = values.place(x);
+                        if (at != KEYS)
+                            return S.value[at];
+                        uint32_t i, j;
+                        float y, z;
+                        upk(W.template split<SHORT>(pk(x, x), i, j), y, z);
+                        return W.value(i, y);
+                    };
+                    if (a > x0)
+                        u0 = look(a);
+                    if (b > x0)
+                        u1 = look(b);
+                    above.add(u0, u1);
+                }
                 tied += (a == x0) + (b == x0);
             }
         });
         tied = warp_sum64(tied);
-        const u64 w = W(x0), seg = warp_sum64(above.units());
-        const u64 last[2] = {seg, tied};
-        const Board b3 = publish(last);
-        u64 all, all_tied;
-        before = ahead(b3, 0, all);
-        const u64 tied_ahead = ahead(b3, 1, all_tied);
-        ties = min(ties, all_tied);
-        const u64 here = tied_ahead >= ties ? 0 : min(ties - tied_ahead, tied);   // of this segment's
-        before += min(tied_ahead, ties) * w;
-        mine = seg + here * w;
-        Z = all + ties * w;
-        cut_x = x0;
-        cut_last = 0xffffffffu;
-        owner = rank == 0 && threadIdx.x == 0 && ties == all_tied;
+        const u64 seg = DRAW ? warp_sum64(above.units()) : 0;
+        if (lane == 0) {
+            S.slot[round & 1][2][warp] = seg;    // of this CTA alone; published numbers lie elsewhere
+            S.slot[round & 1][3][warp] = tied;
+        }
+        __syncthreads();
+        u64 t_ahead = tied_ahead;
+        before = m_ahead;
+        for (int k = 0; k < warp; ++k) {
+            before += S.slot[round & 1][2][k];
+            t_ahead += S.slot[round & 1][3][k];
+        }
+        const u64 here = t_ahead >= ties ? 0 : min(ties - t_ahead, tied);   // of this segment's
+        before += min(t_ahead, ties) * w0_;
+        mine = seg + here * w0_;
         if (here == 0 && ties < all_tied) {
             cut_x = __int_as_float(__float_as_int(x0 + 0.0f) + (x0 >= 0.0f ? 1 : -1));   // nothing at x0 stays
-        } else if (tied_ahead + here == ties && ties < all_tied) {
+        } else if (t_ahead + here == ties && ties < all_tied) {
             // the token of the last one that stays
             u64 seen = 0;
             for (int v = seg0; v < seg1; v += 32) {
@@ -1215,7 +1257,7 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
     bool done = false;   // Z and `before`, the weights ahead of this warp's segment, are known
     bool owner = rank == 0 && tid == 0;   // writes the record
     if (R_::SHORT && (k < V || p < 1.0f))
-        done = R.by_values(W, k < V ? k : 0, p, xmin, Z, before, mine, rec.cut, rec.last, owner);
+        done = R.template by_values<!VERIFY>(W, k < V ? k : 0, p, xmin, u, Z, before, mine, rec.cut, rec.last, owner);
     const bool valued = done;
     if (!done && k < V) {
         const int bin = R.template bin_of_cut<false>(W, 0.0f, k, 0, ahead, target);
