@@ -253,7 +253,8 @@ constexpr int KEYS = 2048;                // 16 bits: the values of 16 octaves, 
 constexpr int ODD = 1024;                 // logits closer to 0 in a CTA's part
 constexpr int FEW = FILTER_CAP / 2;       // top-k by a list: a quarter of an octave more may reach the threshold
 struct RowShared {
-    u64 slot[2][4][FW];   // published, by round parity: up to four numbers per warp
+    u64 board[2][4][MAX_C * FW];   // published, by round parity: up to four numbers of every warp of the cluster
+    u64 seg[2][FW];                // of this CTA's warps
     u64 sums[FW], sums2[FW];
     Search search;
     float2 table[64];
@@ -432,26 +433,25 @@ struct Row : RowView<T> {
             }
         });
     }
-    // Publishes n numbers per warp (the same in every lane) and returns where warp w of CTA r has them.
+    // Publishes n numbers per warp (the same in every lane): each warp writes its own to every CTA of the cluster, so
+    // that they are at hand behind the barrier (read from their owners instead, each exchange took 1000 clocks more).
     struct Board {
-        u64 *at;
-        cg::cluster_group cl;
-        __device__ __forceinline__ u64 get(int i, int segment) const
-        {
-            return *cl.map_shared_rank(at + i * FW + segment % FW, segment / FW);
-        }
+        const u64 *at;
+        __device__ __forceinline__ u64 get(int i, int segment) const { return at[i * MAX_C * FW + segment]; }
     };
     template <int N>
     __device__ __forceinline__ Board publish(const u64 (&x)[N])
     {
-        u64 *at = &S.slot[round & 1][0][0];
+        u64 *at = &S.board[round & 1][0][0];
         ++round;
-        if (lane == 0)
+        if (lane < C) {
+            u64 *to = cl.map_shared_rank(at + segment(), lane);
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                at[i * FW + warp] = x[i];
+                to[i * MAX_C * FW] = x[i];
+        }
         cl_sync();
-        return Board{at, cl};
+        return Board{at};
     }
     // A number per warp: their sum ahead of this warp's (or of the first `end`), and in all
     __device__ __forceinline__ u64 ahead(const Board &b, int i, u64 &total) const { return ahead(b, i, total, segment()); }
@@ -467,7 +467,7 @@ struct Row : RowView<T> {
         total = warp_sum64(all);
         return warp_sum64(mine);
     }
-    // This lane's part of the numbers of all warps, 0 where there are no more: all loads in flight at once
+    // This lane's part of the numbers of all warps, 0 where there are no more
     __device__ __forceinline__ void read(const Board &b, int i, u64 (&x)[MAX_C * FW / 32]) const
     {
 #pragma unroll
@@ -1009,15 +1009,15 @@ struct Row : RowView<T> {
         tied = warp_sum64(tied);
         const u64 seg = DRAW ? warp_sum64(above.units()) : 0;
         if (lane == 0) {
-            S.slot[round & 1][2][warp] = seg;    // of this CTA alone; published numbers lie elsewhere
-            S.slot[round & 1][3][warp] = tied;
+            S.seg[0][warp] = seg;
+            S.seg[1][warp] = tied;
         }
         __syncthreads();
         u64 t_ahead = tied_ahead;
         before = m_ahead;
         for (int k = 0; k < warp; ++k) {
-            before += S.slot[round & 1][2][k];
-            t_ahead += S.slot[round & 1][3][k];
+            before += S.seg[0][k];
+            t_ahead += S.seg[1][k];
         }
         const u64 here = t_ahead >= ties ? 0 : min(ties - t_ahead, tied);   // of this segment's
         before += min(t_ahead, ties) * w0_;
