@@ -1087,6 +1087,8 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
                          (size_t)(VERIFY ? draft ? b * P.K + i - P.K - 1 : b * (P.K + 1) + i : row) * V * T::ES;
     R_ R(S, src, V);
     const int rank = R.rank;
+    if (VERIFY)
+        pdl_trigger();   // the kernel behind waits for this one's results itself
 
     const float temp = F.T ? __ldg(F.T + b) : 1.0f, p = F.p ? __ldg(F.p + b) : 1.0f;
     const float least = F.least ? __ldg(F.least + b) : 0.0f;
@@ -1637,7 +1639,8 @@ cudaError_t launch_filter_verify(const FilterParams &P, int tdt, int sms, cudaSt
     if (e != cudaSuccess)
         return e;
     ++*launches;
-    const int C = 8;
+    // a row that is not listed keeps a cluster busy; there are CTAs enough from 128 sequences on
+    const int C = P.B >= 128 ? 4 : 8;
     e = tdt ? launch_clusters(filter_decide<RowBF16>, P.B, C, 0, true, stream, P)
             : launch_clusters(filter_decide<RowF32>, P.B, C, 0, true, stream, P);
     if (e == cudaSuccess)
