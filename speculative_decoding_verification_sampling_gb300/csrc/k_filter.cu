@@ -35,7 +35,7 @@
 // logits, top-k 20 and top-p 0.8: 10.3 us, of which the launch and the first pass
 // are 4 us and each exchange 1 us; top-p 0.9 alone: 25 us (ten exchanges, and 64
 // tokens to a thread).  256 such rows: 26 us (2.5 TB/s: two waves of CTAs, each a
-// copy and then a second pass) and 104 us (the instructions of the count, 14 a token,
+// first pass and then a second one) and 104 us (the instructions of the count, 14 a token,
 // and of the values' weights, and the exchanges, 42 % of the issue slots taken).
 // 256 rows without filters: 72 us (a weight a token, 40 instructions).
 //
@@ -64,7 +64,10 @@ constexpr int MAX_C = 16;               // CTAs of a cluster
 constexpr int COARSE = 256;             // bins of the threads' maxima, a thread each
 constexpr float RANGE = 64.0f;          // what these span: weights to 2^-64 of the largest
 constexpr int ST_INVALID = 1;
-constexpr long long FLIGHT = 80 << 20;  // bytes of the rows in flight, at most
+// Bytes of the rows in flight, at most.  Smaller clusters have fewer barriers for the same bytes, but the second
+// pass has to find its row in L2: 2304 rows of 256 KB, 200 us a call with clusters of two (78 MB in flight), 250 us of
+// four, 232 us of one (156 MB); 480 rows of 304 KB, 234 us of four, 249 us of two.
+constexpr long long FLIGHT = 80 << 20;
 
 __device__ const FilterTable kFilterTable = filter_table();
 
@@ -263,7 +266,9 @@ constexpr int RANKED = FT;                // tokens of a bin that are ranked; mo
 constexpr int STAGED = 2048;              // tokens in a CTA's own list
 constexpr int KEYS = 2048;                // 16 bits: the values of 16 octaves, of either sign
 constexpr int ODD = 1024;                 // logits closer to 0 in a CTA's part
-constexpr int FEW = FILTER_CAP / 2;       // top-k by a list: a quarter of an octave more may reach the threshold
+// Top-k by a list: a quarter of an octave more may reach the threshold than are kept.  256 rows of 128256: top-k 20
+// with top-p by lists 26 us, k = 1000 with top-p by lists of 1200 tokens 143 us, by the rows' values 103 us.
+constexpr int FEW = FILTER_CAP / 2;
 struct RowShared {
     u64 board[2][4][MAX_C * FW];   // published, by round parity: up to four numbers of every warp of the cluster
     u64 seg[2][FW];                // of this CTA's warps
@@ -805,7 +810,8 @@ struct Row : RowView<T> {
     }
 
     // ---- logits of 16 bits take few values: how often each occurs says all that a cut needs, and a value's weight is
-    // computed once, not once a token.  Values in their order, largest first: 16 octaves of positive ones, those
+    // computed once, not once a token (128 rows of 262144 under top-p: 104 us, 147 us by the histogram of weights).
+    // Values in their order, largest first: 16 octaves of positive ones, those
     // closer to 0 (one place for all, and a list: about 1 in 2^11 of a row's), 16 octaves of negative ones.
     struct Values {
         int base;   // of the 16 octaves' absolute bits
@@ -1654,7 +1660,8 @@ cudaError_t launch_filter_verify(const FilterParams &P, int tdt, int sms, cudaSt
     if (e != cudaSuccess)
         return e;
     ++*launches;
-    // a row that is not listed keeps a cluster busy; there are CTAs enough from 128 sequences on
+    // a row that is not listed keeps a cluster busy; there are CTAs enough from 128 sequences on (256: 189 us a call
+    // with clusters of four, 198 us with eight)
     const int C = P.B >= 128 ? 4 : 8;
     e = tdt ? launch_clusters(filter_decide<RowBF16>, P.B, C, 0, true, stream, P)
             : launch_clusters(filter_decide<RowF32>, P.B, C, 0, true, stream, P);
