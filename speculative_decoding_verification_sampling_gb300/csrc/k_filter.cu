@@ -264,6 +264,7 @@ constexpr int FINE = OCTAVES * 64 + 64;   // bins of the weights' histogram
 constexpr int LISTS = 8;                  // lists of a row, at most
 constexpr int RANKED = FT;                // tokens of a bin that are ranked; more are sorted into finer bins first
 constexpr int STAGED = 2048;              // tokens in a CTA's own list
+constexpr int MANY = 8192;                // 16 bits: tokens from which a row's values are counted
 constexpr int KEYS = 2048;                // 16 bits: the values of 16 octaves, of either sign
 constexpr int ODD = 1024;                 // logits closer to 0 in a CTA's part
 // Top-k by a list: a quarter of an octave more may reach the threshold than are kept.  256 rows of 128256: top-k 20
@@ -1283,7 +1284,7 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
     u64 cut = 0, mine = 0, ahead, target, Z = 0, before = 0;
     bool done = false;   // Z and `before`, the weights ahead of this warp's segment, are known
     bool owner = rank == 0 && tid == 0;   // writes the record
-    if (R_::SHORT && (k < V || p < 1.0f))
+    if (R_::SHORT && V >= MANY && (k < V || p < 1.0f))
         done = R.template by_values<!VERIFY>(W, k < V ? k : 0, p, xmin, u, Z, before, mine, rec.cut, rec.last, owner);
     const bool valued = done;
     if (!done && k < V) {
@@ -1601,10 +1602,11 @@ cudaError_t rows(const FilterParams &P, int sms, cudaStream_t stream)
 {
     const long long n = (long long)P.B * (VERIFY ? 2 * P.K + 1 : P.K);
     const long long bytes = ((long long)P.V + T::N) * T::ES;
-    // four CTAs to an SM: as many rows in flight as L2 holds beside other things, all CTAs busy where
-    // there are few rows, and no part so short that the barriers are all there is
+    // four CTAs to an SM: as many rows in flight as L2 holds beside other things, and where there are few rows,
+    // clusters as large as all run at once (60 rows of 122187: 46 us under top-p, 71 us with twice as large ones, which
+    // do not), with no part so short that the barriers are all there is; one step further for parts above 64 KB
     int C = 1;
-    while (C < MAX_C && (std::min(n, (long long)(4 * sms / C)) * bytes > FLIGHT || bytes / C > 65536 * T::ES || (n * C < 4 * sms && bytes / C > 4096)))
+    while (C < MAX_C && (std::min(n, (long long)(4 * sms / C)) * bytes > FLIGHT || bytes / C > 65536 * T::ES || (bytes / C > (2 * n * C <= 4 * sms ? 4096 : n * C < 4 * sms ? 65536 : bytes))))
         C *= 2;
     static std::atomic<uint64_t> raised{0};
     int dev = 0;
