@@ -17,11 +17,11 @@
 //     least k logits reach the k-th of them); what reaches it, a few more tokens
 //     than are kept, goes to lists, which the first CTA gathers, ranks, cuts and
 //     draws from.
-//   - larger k and top-p alone, 16-bit logits: how often each value occurs, in
+//   - larger k and top-p alone, rows of 8192 16-bit logits or more: how often each value occurs, in
 //     counts of 32 bits; a value's weight is computed once.  Counts and weights
 //     give the cut and every CTA's share of what is kept, and only the CTA on which
 //     the uniform falls looks at its tokens once more.
-//   - the same, float32: a histogram of the weights, in bins of 1/64 octave of the
+//   - the same, other rows: a histogram of the weights, in bins of 1/64 octave of the
 //     weight.  A bin holds the sum of 1 + q, the weights' ratios to the bin's own,
 //     in fixed point: two additions of 32 bits per token, in any order.  The tokens
 //     of the bin with the cut go to lists and are ranked; meanwhile each warp sums
@@ -49,6 +49,7 @@
 #include <cooperative_groups.h>
 #include <cstdint>
 #include <cuda_runtime.h>
+#include <type_traits>
 
 #include "sv_cluster.cuh"
 #include "sv_filter.cuh"
@@ -264,7 +265,9 @@ constexpr int FINE = OCTAVES * 64 + 64;   // bins of the weights' histogram
 constexpr int LISTS = 8;                  // lists of a row, at most
 constexpr int RANKED = FT;                // tokens of a bin that are ranked; more are sorted into finer bins first
 constexpr int STAGED = 2048;              // tokens in a CTA's own list
-constexpr int MANY = 8192;                // 16 bits: tokens from which a row's values are counted
+// 16 bits: tokens from which a row's values are counted (378 rows of 1570, most under top-p: 50 us by the histogram of
+// weights, 57 us by values; 375 of 10826 52 us by values)
+constexpr int MANY = 8192;
 constexpr int KEYS = 2048;                // 16 bits: the values of 16 octaves, of either sign
 constexpr int ODD = 1024;                 // logits closer to 0 in a CTA's part
 // Top-k by a list: a quarter of an octave more may reach the threshold than are kept.  256 rows of 128256: top-k 20
@@ -517,19 +520,34 @@ struct Row : RowView<T> {
     {
         return fold(b, i, [](u64 a, u64 c) { return a > c ? a : c; });
     }
-    // The sum over the cluster's CTAs of what lies at `p` in their shared memory, eight loads in flight
-    __device__ __forceinline__ u64 of_all(const uint32_t *p) const
+    // f(what lies at `p` in the shared memory of a CTA) for every CTA of the cluster, eight loads in flight, and none
+    // for CTAs that a smaller cluster does not have
+    template <class V_, class F>
+    __device__ __forceinline__ void each_cta(V_ *p, F f) const
+    {
+        auto some = [&](int r, auto n) {
+            V_ x[decltype(n)::value];
+#pragma unroll
+            for (int k = 0; k < decltype(n)::value; ++k)
+                x[k] = *cl.map_shared_rank(p, r + k);
+#pragma unroll
+            for (int k = 0; k < decltype(n)::value; ++k)
+                f(x[k]);
+        };
+        if (C == 1)
+            f(*p);
+        else if (C == 2)
+            some(0, std::integral_constant<int, 2>{});
+        else if (C == 4)
+            some(0, std::integral_constant<int, 4>{});
+        else
+            for (int r = 0; r < C; r += 8)   // C is a power of two
+                some(r, std::integral_constant<int, 8>{});
+    }
+    __device__ __forceinline__ u64 of_all(uint32_t *p) const   // their sum
     {
         u64 v = 0;
-        for (int r = 0; r < C; r += 8) {
-            uint32_t x[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                x[k] = r + k < C ? *cl.map_shared_rank(const_cast<uint32_t *>(p), r + k) : 0;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                v += x[k];
-        }
+        each_cta(p, [&](uint32_t x) { v += x; });
         return v;
     }
 
@@ -1206,16 +1224,10 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
         if (tid == 0)
             S.lo = COARSE - 1;
         __syncthreads();
-        for (int r = 0; r < R.C; r += 8) {
-            float x[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                x[j] = r + j < R.C ? R.cl.map_shared_rank(S.top, r + j)[tid] : -F_INF;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (x[j] > -F_INF)
-                    atomicAdd(&S.coarse[min(COARSE - 1, (int)((m - x[j]) * (W.c_hi * (COARSE / RANGE))))], 1u);
-        }
+        R.each_cta(&S.top[tid], [&](float x) {
+            if (x > -F_INF)
+                atomicAdd(&S.coarse[min(COARSE - 1, (int)((m - x) * (W.c_hi * (COARSE / RANGE))))], 1u);
+        });
         __syncthreads();
         const u64 n = S.coarse[tid];
         u64 all;
