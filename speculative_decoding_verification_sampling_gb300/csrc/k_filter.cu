@@ -296,7 +296,7 @@ struct RowShared {
             uint32_t n[2 * KEYS + 2];      // how often each value occurs
             u64 odd[ODD];
         } v;
-        float2 value[2 * KEYS + 2];        // weights of the values
+        u64 weight[2 * KEYS + 2];          // of the values
         struct {
             u64 key[FT], w[STAGED];        // the cluster's list, (logit, ~token) keys; this CTA's own, and weights
         } l;
@@ -1003,48 +1003,33 @@ struct Row : RowView<T> {
         const bool drawn = DRAW && before <= share_down(u, Z) && share_down(u, Z) < m_to + min(tied_to, ties) * w0_;
         if (!splits && !drawn)
             return true;
-        // ---- the same for each warp's segment of this CTA: by a pass over its part, the values' weights at hand
+        // ---- the same for each warp's segment of this CTA: by a pass over its part, the values' weights at hand.  They
+        // are the numbers that the CTA's share is made of, so the segments end where it ends: a uniform on this CTA
+        // falls on one of its segments, and on no other CTA's.
         const int top = values.place(W.m), end = values.place(x0);
         __syncthreads();
         if (DRAW)
             for (int i = top + threadIdx.x; i <= end; i += FT)
-                if (i != KEYS) {
-                    uint32_t a, b;
-                    float y, z;
-                    upk(W.template split<SHORT>(pk(values.at(i), values.at(i)), a, b), y, z);
-                    S.value[i] = W.value(a, y);
-                }
+                if (i != KEYS)
+                    S.weight[i] = W(values.at(i));
         __syncthreads();
-        FilterSum above;
+        u64 above = 0;
         tied = 0;
         in_turn([&](const uint4 &q, int) {
             if (!(T::largest(q) >= x0))
                 return;
 #pragma unroll
-            for (int e = 0; e < T::N; e += 2) {
-                const float a = T::get(q, e), b = T::get(q, e + 1);
-                if (DRAW) {
-                    float2 u0 = make_float2(0.0f, 0.0f), u1 = u0;
-                    auto look = [&](float x) {
-                        const int at = values.place(x);
-                        if (at != KEYS)
-                            return S.value[at];
-                        uint32_t i, j;
-                        float y, z;
-                        upk(W.template split<SHORT>(pk(x, x), i, j), y, z);
-                        return W.value(i, y);
-                    };
-                    if (a > x0)
-                        u0 = look(a);
-                    if (b > x0)
-                        u1 = look(b);
-                    above.add(u0, u1);
+            for (int e = 0; e < T::N; ++e) {
+                const float x = T::get(q, e);
+                if (DRAW && x > x0) {
+                    const int at = values.place(x);
+                    above += at != KEYS ? S.weight[at] : W(x);
                 }
-                tied += (a == x0) + (b == x0);
+                tied += x == x0;
             }
         });
         tied = warp_sum64(tied);
-        const u64 seg = DRAW ? warp_sum64(above.units()) : 0;
+        const u64 seg = DRAW ? warp_sum64(above) : 0;
         if (lane == 0) {
             S.seg[0][warp] = seg;
             S.seg[1][warp] = tied;

@@ -1,0 +1,92 @@
+"""Draws at the borders between the parts of a row: those that the CTAs of a
+cluster, and their warps, take.  Oracle and tolerances as in test_gpu_filters.py.
+Outputs are filled ahead with what no call returns."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import speculative_decoding_verification_sampling_gb300 as sv
+from oracle import filters as oracle
+from test_gpu_filters import BF, DEV, NEAR, _filters
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    torch.cuda.set_device(DEV)
+    sv.load()
+
+
+def _row(V, parts, dtype=BF):
+    """[V] with parts = (value, first, end) in turn, the rest far below."""
+    z = torch.full((V,), -10000.0, device=DEV)
+    for x, first, end in parts:
+        z[first:end] = x
+    return z.to(dtype)
+
+
+def _draw(z, ask, uniforms, what):
+    """One row [V] drawn from with every uniform, as many sequences of one call."""
+    n = len(uniforms)
+    f, exact = _filters([ask] * n)
+    u = torch.tensor(uniforms, dtype=torch.float32, device=DEV)[:, None]
+    tokens = torch.full((n, 1), -7, dtype=torch.int32, device=DEV)
+    prob = torch.full((n, 1), -7.0, device=DEV)
+    sv.spec_filter_sample(z.expand(n, 1, -1).contiguous(), u, f, out_tokens=tokens, out_prob=prob)
+    tokens, prob = tokens[:, 0].cpu().numpy(), prob[:, 0].double().cpu().numpy()
+    assert (tokens != -7).all() and (prob != -7).all(), f"{what}: no token for {u[:, 0].cpu().numpy()[tokens == -7]}"
+    x, w, m0 = oracle.kept(z.double().cpu().numpy(), *exact[0])
+    at = {int(t): float(p) for t, p in zip(x, w)}
+    for i, v in enumerate(u[:, 0].double().tolist()):
+        t, m = oracle.pick(x, w, v)
+        if min(m, m0) < NEAR:
+            continue
+        assert tokens[i] == t, f"{what}: {tokens[i]} not {t} at {v!r}"
+        assert abs(prob[i] - at[t]) <= 1.01 * (2.0 ** -24 + 2.0 ** -30) * at[t] + 2.0 ** -43, what
+
+
+def _borders(z, ask, steps=2):
+    """Uniforms (multiples of 2^-24) at and next to the running sum of what is kept ahead of every 256th token:
+    whatever the size of the cluster, a CTA's or a warp's part begins at one of them (32 vectors of 16 bytes)."""
+    x, w, _ = oracle.kept(z.double().cpu().numpy(), *_filters([ask])[1][0])
+    c = np.concatenate([[0.0], np.cumsum(w)])
+    ends = c[np.searchsorted(x, np.arange(0, len(z) + 256, 256))]
+    ends = np.unique(np.floor(ends * 2.0 ** 24).astype(np.int64))
+    u = np.unique(np.clip(np.concatenate([ends + k for k in range(-steps, steps + 1)]), 0, 2 ** 24 - 1))
+    return (u * 2.0 ** -24).tolist()
+
+
+STEPS = [(6.5, 0, 2048), (12.0, 2048, 2049), (3.5, 4096, 8192)]
+LOW = [(-2.0, 0, 2048), (2.9951334e-06, 2048, 2049), (-5.0, 4096, 8192)]   # the largest logit near 0
+
+
+@pytest.mark.parametrize("parts,T,u", [(STEPS, 0.563560605, 0.105760962), (LOW, 1.0, 0.907368362)], ids=["steps", "low"])
+def test_between_the_warps_and_their_cta(parts, T, u):
+    """Sums of the warps' parts in floats fell short of their CTA's here, and the uniform between the two."""
+    z = _row(16384, parts)
+    for n in (1, 3, 40, 700):
+        _draw(z, (T, 0, 0.999, 0.0), [u] * n, f"{n} rows")
+
+
+@pytest.mark.parametrize("kind", ["steps", "low", "zipf", "values", "ties"])
+@pytest.mark.parametrize("ask", [(1.0, 0, 0.999, 0.0), (0.7, 0, 0.9, 0.0), (0.9, 3000, 1.0, 0.0), (1.1, 5000, 0.97, 0.001)])
+def test_borders_between_parts(kind, ask):
+    V = 16384
+    g = torch.Generator(device=DEV).manual_seed(3)
+    if kind in ("steps", "low"):
+        z = _row(V, STEPS if kind == "steps" else LOW)
+    elif kind == "zipf":
+        z = (12 - 1.5 * torch.log(torch.rand(V, generator=g, device=DEV) * V + 1)).to(BF)
+    elif kind == "values":
+        z = (torch.round(4 * torch.randn(V, generator=g, device=DEV)) / 8).to(BF)
+    else:
+        z = torch.full((V,), -3.25, device=DEV).to(BF)
+    uniforms = _borders(z, ask)
+    _draw(z, ask, uniforms, f"{kind} {ask}")
+    for i in range(0, len(uniforms), 7):      # alone: larger clusters
+        _draw(z, ask, uniforms[i:i + 1], f"{kind} {ask} alone")
