@@ -1006,7 +1006,7 @@ struct Row : RowView<T> {
         // ---- the same for each warp's segment of this CTA: by a pass over its part, the values' weights at hand.  They
         // are the numbers that the CTA's share is made of, so the segments end where it ends: a uniform on this CTA
         // falls on one of its segments, and on no other CTA's.
-        const int top = values.place(W.m), end = values.place(x0);
+        const int top = values.place(W.highest()), end = values.place(x0);
         __syncthreads();
         if (DRAW)
             for (int i = top + threadIdx.x; i <= end; i += FT)

@@ -54,20 +54,27 @@ constexpr float FILTER_UNIT = 8796093022208.0f;   // 2^43
 // The weights of one row.  2^((x - m) c) = 2^(i / 64) (1 + q): the exponent is the
 // sum of a multiple of 1/64 and a rest r, |r| <= 1/128, exact up to its last bit;
 // 2^r - 1 = y + y^2/2 + y^3/6 with y = r ln 2, off by 2^-34.
+//
+// m is the largest logit, or 0 where that is so near that its token's weight comes
+// to within 2^-10 octaves of 1: all weights of the row have the one factor 2^(m c) then.
 struct FilterWeight {
     static constexpr float ROUND = 196608.0f;   // 1.5 2^17: steps of 1/64
     float m, c_hi, c_lo;
-    float low;              // logits below have weights below half a unit
+    float low;              // logits below have weights below 2^-43.75, 0.6 of a unit, and count as none
     const float2 *table;    // in shared memory
     FilterWeight() = default;
-    __device__ __forceinline__ FilterWeight(float m_, float hi, float lo, const float2 *t)
+    __device__ __forceinline__ FilterWeight(float top, float hi, float lo, const float2 *t)
     {
-        m = m_, c_hi = hi, c_lo = lo, table = t;
+        m = hi > 0.0f && fabsf(top) * hi < 0x1p-10f ? 0.0f : top;
+        c_hi = hi, c_lo = lo, table = t;
         low = hi > 0.0f ? __fadd_ru(m, __fdiv_rn(-43.75f, hi)) : m;
     }
+    // A logit at or above the row's largest
+    __device__ __forceinline__ float highest() const { return m != 0.0f || c_hi == 0.0f ? m : __fdiv_ru(0x1p-10f, c_hi); }
     // Two logits at or above `low` (others come to nothing that may be used): the bits of i / 64 + ROUND, and q.
-    // SHORT: logits of 8 bits.  Their difference is exact where they lie within 2^16 of each other; where x is
-    // the smaller one, what is lost is x - (d + m).  (Where m is, 2^-16 of the other logits: 2^-24 of them is lost.)
+    // What d = x - m has lost is `rest`, exactly.  SHORT, logits of 8 bits: x - (d + m), which is exact where m is
+    // the larger one, and where x is, since it is less than 2^16 times m: a multiple of m's last bit, d has 25 bits
+    // at most and d + m 24.  (Nearer to 0 than that, m is 0.)
     template <bool SHORT>
     __device__ __forceinline__ f2 split(f2 x, uint32_t &i0, uint32_t &i1) const
     {

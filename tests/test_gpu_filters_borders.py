@@ -90,3 +90,32 @@ def test_borders_between_parts(kind, ask):
     _draw(z, ask, uniforms, f"{kind} {ask}")
     for i in range(0, len(uniforms), 7):      # alone: larger clusters
         _draw(z, ask, uniforms[i:i + 1], f"{kind} {ask} alone")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("ask", [(1.0, 0, 1.0, 0.0), (1.0, 0, 0.98, 0.0), (0.5, 700, 1.0, 0.0), (2.0, 700, 0.9, 0.0)])
+@pytest.mark.parametrize("V", [2000, 9000])
+def test_largest_logit_near_zero(V, ask, dtype):
+    """A logit far from 0 less one near 0 needs more bits than a float has: weights keep their 2^-31 all the same.
+    Uniforms next to the borders of the largest logit's token, which holds about half of the weight."""
+    g = torch.Generator().manual_seed(V)
+    B = 300
+    z = torch.full((B, 1, V), -10000.0, dtype=torch.float64)
+    for b in range(B):
+        m = (1.0 if b % 3 else -1.0) * 2.0 ** (-23 + 8 * float(torch.rand((), generator=g)))
+        x = -ask[0] * (5.0 + 2.0 * float(torch.rand((), generator=g)))
+        z[b, 0, :V // 2] = x
+        z[b, 0, V // 4] = m
+    z = z.to(dtype)
+    u = torch.empty((B, 1))
+    f, exact = _filters([ask] * B)
+    for b in range(B):
+        x, w, _ = oracle.kept(z[b, 0].double().numpy(), *exact[b])
+        c = np.concatenate([[0.0], np.cumsum(w)])
+        at = int(np.searchsorted(x, V // 4)) + b % 2
+        u[b, 0] = min(np.floor(c[at] * 2.0 ** 24) + b // 2 % 2, 2.0 ** 24 - 1) * 2.0 ** -24
+    tokens, prob = sv.spec_filter_sample(z.to(DEV), u.to(DEV), f)
+    t, p, margin, _ = oracle.sample(z.double().numpy(), u.double().numpy(), exact)
+    bad = (tokens.cpu().numpy() != t) & (margin >= NEAR)
+    assert (margin >= NEAR).mean() > 0.5
+    assert not bad.any(), f"{bad.sum()} of {B}: {tokens.cpu().numpy()[bad][:4]} not {t[bad][:4]}"
