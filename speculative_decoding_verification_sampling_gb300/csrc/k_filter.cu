@@ -69,6 +69,8 @@ constexpr int ST_INVALID = 1;
 // pass has to find its row in L2: 2304 rows of 256 KB, 200 us a call with clusters of two (78 MB in flight), 250 us of
 // four, 232 us of one (156 MB); 480 rows of 304 KB, 234 us of four, 249 us of two.
 constexpr long long FLIGHT = 80 << 20;
+// Tokens of a CTA's part, at most: so many 16-bit halves of a bin's sums make less than 2^32.
+constexpr int PART = 65536;
 
 __device__ const FilterTable kFilterTable = filter_table();
 
@@ -1599,11 +1601,16 @@ cudaError_t rows(const FilterParams &P, int sms, cudaStream_t stream)
 {
     const long long n = (long long)P.B * (VERIFY ? 2 * P.K + 1 : P.K);
     const long long bytes = ((long long)P.V + T::N) * T::ES;
+    // of a cluster of C, where the row begins at the last element of a vector: RowView's segments
+    auto part = [&](int C) {
+        const int nv = (T::N - 1 + P.V + T::N - 1) / T::N;
+        return (((nv + C * FW - 1) / (C * FW) + 31) & ~31) * FW * T::N;
+    };
     // four CTAs to an SM: as many rows in flight as L2 holds beside other things, and where there are few rows,
     // clusters as large as all run at once (60 rows of 122187: 46 us under top-p, 71 us with twice as large ones, which
     // do not), with no part so short that the barriers are all there is; one step further for parts above 64 KB
     int C = 1;
-    while (C < MAX_C && (std::min(n, (long long)(4 * sms / C)) * bytes > FLIGHT || bytes / C > 65536 * T::ES || (bytes / C > (2 * n * C <= 4 * sms ? 4096 : n * C < 4 * sms ? 65536 : bytes))))
+    while (C < MAX_C && (std::min(n, (long long)(4 * sms / C)) * bytes > FLIGHT || part(C) > PART || (bytes / C > (2 * n * C <= 4 * sms ? 4096 : n * C < 4 * sms ? 65536 : bytes))))
         C *= 2;
     static std::atomic<uint64_t> raised{0};
     int dev = 0;

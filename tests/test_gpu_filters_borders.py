@@ -119,3 +119,28 @@ def test_largest_logit_near_zero(V, ask, dtype):
     bad = (tokens.cpu().numpy() != t) & (margin >= NEAR)
     assert (margin >= NEAR).mean() > 0.5
     assert not bad.any(), f"{bad.sum()} of {B}: {tokens.cpu().numpy()[bad][:4]} not {t[bad][:4]}"
+
+
+def test_parts_of_most_tokens():
+    """Rows cut into parts of up to 65536 tokens whose weights' low halves are nearly all ones: sums of them in 32
+    bits.  Nearly all tokens are equal and near 0, so their values are not counted; rows begin anywhere in a vector."""
+    B, V = 80, 524283
+    x = float(torch.tensor(2.0 ** -20).to(BF))
+    for T in np.linspace(0.5, 1.0, 4000, dtype=np.float32):
+        e = (x - 1.0) / float(T) / np.log(2.0)
+        y = np.exp2(e - np.rint(64 * e) / 64) * 2.0 ** 29     # a weight, as its bin has it
+        if y % 65536 > 65400 and y % 65536 < 65500:
+            break
+    else:
+        raise AssertionError("no temperature")
+    z = torch.full((B, 1, V), x, device=DEV).to(BF)
+    z[:, 0, V // 3] = 1.0
+    u = torch.full((B, 1), 0.625, device=DEV)
+    f, exact = _filters([(float(T), 0, 0.7, 0.0)] * B)
+    tokens, prob = sv.spec_filter_sample(z, u, f)
+    t, p, margin, _ = oracle.sample(z[:1].double().cpu().numpy(), u[:1].double().cpu().numpy(), exact[:1])
+    assert margin[0, 0] >= NEAR
+    assert (tokens == int(t[0, 0])).all(), f"{sorted(set(tokens[:, 0].tolist()))} not {t[0, 0]}"
+    assert ((prob.double() - p[0, 0]).abs() <= 1.01 * (2.0 ** -24 + 2.0 ** -30) * p[0, 0] + 2.0 ** -43).all()
+
+
