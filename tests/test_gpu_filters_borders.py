@@ -144,3 +144,21 @@ def test_parts_of_most_tokens():
     assert ((prob.double() - p[0, 0]).abs() <= 1.01 * (2.0 ** -24 + 2.0 ** -30) * p[0, 0] + 2.0 ** -43).all()
 
 
+
+
+@pytest.mark.parametrize("dtype,sizes", [(BF, (2100, 4200, 9000, 20000, 40000)), (torch.float32, (1100, 2100, 4300, 9000, 20000))],
+                         ids=["bf16", "f32"])
+def test_first_exchange_of_short_rows(dtype, sizes):
+    """Clusters of 2 to 16 CTAs with little to read ahead of their first exchange, many of them in a row."""
+    g = torch.Generator(device=DEV).manual_seed(1)
+    for V in sizes:
+        for B in (1, 7):
+            z = torch.randn((B, 1, V), generator=g, device=DEV).to(dtype)
+            z[:, 0, V - 1] = 30.0                     # in the last CTA that has tokens
+            f, _ = _filters([(1.0, 0, 1.0, 0.0), (0.0, 0, 1.0, 0.0), (1.0, 9, 1.0, 0.0)][:B] * 3 if B > 1 else [(1.0, 9, 0.9, 0.0)])
+            f = sv.Filters(*[getattr(f, n)[:B].clone() for n in sv.Filters.__slots__])
+            u = torch.full((B, 1), 0.5, device=DEV)
+            out = [torch.full((B, 1), -7, dtype=torch.int32, device=DEV) for _ in range(200)]
+            for tokens in out:
+                sv.spec_filter_sample(z, u, f, out_tokens=tokens)
+            assert all((tokens == V - 1).all() for tokens in out), f"{V} {B}"
