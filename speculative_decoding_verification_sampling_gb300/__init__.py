@@ -236,6 +236,14 @@ def _need(t, shape, dtype, index, name, more=""):
     raise ValueError(f"{name}{more} is on {t.device}, the call's other tensors on cuda:{index}")
 
 
+def _own_workspace(workspace, index):
+    """The caller's: its bytes are counted by its elements, so these lie side by side."""
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != index:
+        raise TypeError(f"workspace must be a CUDA tensor on cuda:{index}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
 def _dt(t):
     return SPEC_BF16 if t.dtype == torch.bfloat16 else SPEC_F32
 
@@ -569,8 +577,8 @@ def spec_verify_filtered(target: torch.Tensor, draft: torch.Tensor, draft_tokens
             out_accept_len = _new((B,), torch.int32, dev, before)
         if workspace is None:
             workspace = _scratch(_filter_bytes(B, K, V), dev, st)
-        elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != index:
-            raise TypeError(f"workspace must be a CUDA tensor on cuda:{index}")
+        else:
+            _own_workspace(workspace, index)
     _need(out_tokens, (B, K1), torch.int32, index, "out_tokens")
     _need(out_accept_len, (B,), torch.int32, index, "out_accept_len")
     rc = (_lib or load()).spec_verify_filtered(
@@ -827,8 +835,8 @@ def spec_verify_window_attention(q: torch.Tensor, cache: torch.Tensor, seq_len: 
             if nbytes == 0:
                 raise SpecVerifyError(1, "spec_verify_window_attention")
             workspace = _scratch(nbytes, dev, st)
-        elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != index:
-            raise TypeError(f"workspace must be a CUDA tensor on cuda:{index}")
+        else:
+            _own_workspace(workspace, index)
     _need(out, shape, torch.bfloat16, index, "out")
     _need(lse, (B, T, Hq), torch.float32, index, "lse")
 

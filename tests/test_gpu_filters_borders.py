@@ -162,3 +162,18 @@ def test_first_exchange_of_short_rows(dtype, sizes):
             for tokens in out:
                 sv.spec_filter_sample(z, u, f, out_tokens=tokens)
             assert all((tokens == V - 1).all() for tokens in out), f"{V} {B}"
+
+
+def test_a_workspace_with_gaps_is_refused():
+    """Its elements do not tell how much memory there is: one repeated element has that of one."""
+    B, K, V = 2, 2, 500
+    target, draft = torch.randn((B, K + 1, V), device=DEV), torch.randn((B, K, V), device=DEV)
+    d, u = torch.zeros((B, K), dtype=torch.int32, device=DEV), torch.rand((B, K + 1, 2), device=DEV)
+    n = sv.spec_filter_workspace_bytes(B, K, V)
+    with pytest.raises(ValueError):
+        sv.spec_verify_filtered(target, draft, d, u, workspace=torch.empty(2 * n, dtype=torch.uint8, device=DEV)[::2])
+    q = torch.zeros((1, 2, 2, 64), dtype=BF, device=DEV)
+    cache, length = torch.zeros((1, 4, 2, 1, 64), dtype=BF, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    n = sv.spec_attention_workspace_bytes(1, 2, 2, 1, 64, 0, 4)
+    with pytest.raises(ValueError):
+        sv.spec_verify_window_attention(q, cache, length, 4, workspace=torch.empty(2 * n, dtype=torch.uint8, device=DEV)[::2])
