@@ -223,8 +223,11 @@ spec_status_t spec_draft_sample(const void *draft_logits, spec_dtype_t ddt, int 
  * first token alone.  A temperature that is negative, infinite or NaN, a top_p of
  * NaN and a min_p above 1 or NaN are data errors (SPEC_ERR_INVALID_ARG) of the
  * sequence.  Temperatures below 2^-100 count as that, above 2^100 as that.
- * Weights are held to 2^-31 of their own and 2^-44 of the row's largest, their
- * sums exactly: results do not depend on how the work is split.               */
+ * Weights are whole numbers of 2^-43 of the row's largest, right to half of one and
+ * to 2^-31 of their own (those below 2^-43.75 of the largest are none), so sums of
+ * them are exact.  The total that top-p takes its share of is right to 2^-29 of
+ * itself.  Results do not depend on how the work is split, but for a top-p border
+ * that lies nearer than that.                                                 */
 typedef struct {
     const float *temperature;   /* NULL: 1 */
     const int32_t *top_k;

@@ -12,7 +12,10 @@
 // sums of up to V weights, and one token more or less changes a draw.  So the
 // weights are held in 64-bit integers, in units of 2^-43 of the largest: their
 // sums are exact, the same in every order, and depend on no split of the work.
-// A weight itself is right to 2^-31.5 (and to half a unit).  With float32
+// A weight itself is right to 2^-31.5 (and to half a unit).  (The total that top-p
+// takes its share of, where it comes from a histogram: every 1 + q rounded to 2^-29
+// and every bin down to a unit, so right to 2^-29.)  With sums of float pairs, 2^-24
+// of the smaller halves, many equal weights summed up to 2^-27 off.  With float32
 // throughout, 2^-24 of a weight, the head of a row of 128256 tokens ends one
 // token off about once in a thousand rows.
 #pragma once
@@ -24,7 +27,7 @@
 
 namespace sv {
 
-// 2^(j / 64) as two floats.
+// 2^(j / 64) as two floats, the second in units of 2^-33.
 struct FilterTable {
     float2 t[64];
 };
@@ -44,12 +47,10 @@ constexpr FilterTable filter_table()
     for (int j = 0; j < 64; ++j) {
         const double v = filter_pow2(j);
         t.t[j].x = (float)v;
-        t.t[j].y = j ? (float)(v - (double)(float)v) : 1e-20f;   // not 0: its exponent is added to
+        t.t[j].y = (float)((v - (double)(float)v) * 0x1p33);
     }
     return t;
 }
-
-constexpr float FILTER_UNIT = 8796093022208.0f;   // 2^43
 
 // The weights of one row.  2^((x - m) c) = 2^(i / 64) (1 + q): the exponent is the
 // sum of a multiple of 1/64 and a rest r, |r| <= 1/128, exact up to its last bit;
@@ -71,7 +72,7 @@ struct FilterWeight {
     }
     // A logit at or above the row's largest
     __device__ __forceinline__ float highest() const { return m != 0.0f || c_hi == 0.0f ? m : __fdiv_ru(0x1p-10f, c_hi); }
-    // Two logits at or above `low` (others come to nothing that may be used): the bits of i / 64 + ROUND, and q.
+    // Two logits at or above `low` (others come to nothing that may be used): the bits of i / 64 + ROUND, and 2^33 q.
     // What d = x - m has lost is `rest`, exactly.  SHORT, logits of 8 bits: x - (d + m), which is exact where m is
     // the larger one, and where x is, since it is less than 2^16 times m: a multiple of m's last bit, d has 25 bits
     // at most and d + m 24.  (Nearer to 0 than that, m is 0.)
@@ -96,21 +97,26 @@ struct FilterWeight {
         upk(t, a, b);
         i0 = __float_as_uint(a);
         i1 = __float_as_uint(b);
-        return mul2(r, fma2(r, fma2(r, pk(0.055504109f, 0.055504109f), pk(0.24022651f, 0.24022651f)),
-                            pk(0.69314718f, 0.69314718f)));
+        constexpr float a1 = 0.69314718f * 0x1p33f, a2 = 0.24022651f * 0x1p33f, a3 = 0.055504109f * 0x1p33f;
+        return mul2(r, fma2(r, fma2(r, pk(a3, a3), pk(a2, a2)), pk(a1, a1)));
     }
     // i alone, for a logit at or above `low`
     __device__ __forceinline__ int place(float x) const
     {
         return __float_as_int(__fmaf_rn(__fadd_rn(x, -m), c_hi, ROUND)) - __float_as_int(ROUND);
     }
-    // 2^(i / 64) (1 + q) as two floats, of which the second is small
-    __device__ __forceinline__ float2 value(uint32_t i, float q) const
+    // 2^(i / 64) (1 + q) in units, for a logit at or above `low` (another comes to nothing that may be used): 2^(i mod
+    // 64 / 64) to half a unit, its correction in steps of 2^-33; then the rest of i as a shift, to half a unit
+    __device__ __forceinline__ u64 units(uint32_t i, float q) const
     {
         const float2 e = table[i & 63];
-        const uint32_t up = (i << 17) & 0xff800000u;   // ROUND's bits leave the word
-        const float hi = __uint_as_float(__float_as_uint(e.x) + up), lo = __uint_as_float(__float_as_uint(e.y) + up);
-        return make_float2(hi, fmaf(hi, q, lo));
+        const int n = (int)(__float_as_uint(ROUND) - i + 63) >> 6;   // ROUND's bits end in 22 zeros
+        u64 w;
+        asm("shl.b64 %0, %1, %2;" : "=l"(w) : "l"(1ull), "r"(n - 1));   // half of what is shifted out; 0 if nothing is
+        w += (u64)((__float_as_uint(e.x) & 0x7fffffu) | 0x800000u) * (1u << 20);
+        w += (u64)((long long)__float2int_rn(fmaf(e.x, q, e.y)) * 1024);
+        asm("shr.u64 %0, %1, %2;" : "=l"(w) : "l"(w), "r"(n));
+        return w;
     }
     // in units; 0 below `low`
     __device__ __forceinline__ u64 operator()(float x) const
@@ -120,42 +126,15 @@ struct FilterWeight {
         uint32_t i, j;
         float q, r;
         upk(split<false>(pk(x, x), i, j), q, r);
-        // 2^(i mod 64 / 64) (1 + q) in units, its correction in steps of 2^-33; then the rest of i as a shift
-        const float2 e = table[i & 63];
-        const long long v = (long long)((__float_as_uint(e.x) & 0x7fffffu) | 0x800000u) * (1 << 20) +
-                            (long long)__float2int_rn(fmaf(e.x, q, e.y) * 0x1p33f) * 1024;
-        const int n = (int)(__float_as_uint(ROUND) - i + 63) >> 6;   // ROUND's bits end in 22 zeros
-        return (u64)(v + (1ll << n >> 1)) >> n;
+        return units(i, q);
     }
     // The weights whose sum of 1 + q is v 2^-29 and whose i is -bin, in units
     __device__ __forceinline__ u64 of_bin(u64 v, int bin) const
     {
         const float2 e = table[-bin & 63];
         const u64 t = (u64)((__float_as_uint(e.x) & 0x7fffffu) | 0x800000u) * (1u << 20) +
-                      (long long)__float2int_rn(e.y * 0x1p33f) * 1024;
+                      (long long)__float2int_rn(e.y) * 1024;
         return __umul64hi(v << 15, t << 20) >> ((bin + 63) >> 6);   // v < 2^48
-    }
-};
-
-// A thread's two sums of weights: the rounding errors of the larger halves go with the smaller ones, so a sum is
-// right to 2^-24 of those.  `s` begins at the largest weight there is.
-struct FilterSum {
-    f2 s = pk(1.0f, 1.0f), c = pk(0.0f, 0.0f);
-    __device__ __forceinline__ void add(float2 a, float2 b)
-    {
-        const f2 w = pk(a.x, b.x), one = pk(-1.0f, -1.0f);
-        const f2 t = add2(s, w);
-        c = add2(c, add2(fma2(t, one, s), w));
-        c = add2(c, pk(a.y, b.y));
-        s = t;
-    }
-    __device__ __forceinline__ u64 units() const
-    {
-        float a, b, x, y;
-        upk(s, a, b);
-        upk(c, x, y);
-        return (u64)(__float2ll_rn((a - 1.0f) * FILTER_UNIT) + __float2ll_rn((b - 1.0f) * FILTER_UNIT) +
-                     __float2ll_rn(x * FILTER_UNIT) + __float2ll_rn(y * FILTER_UNIT));
     }
 };
 

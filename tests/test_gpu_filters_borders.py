@@ -177,3 +177,29 @@ def test_a_workspace_with_gaps_is_refused():
     n = sv.spec_attention_workspace_bytes(1, 2, 2, 1, 64, 0, 4)
     with pytest.raises(ValueError):
         sv.spec_verify_window_attention(q, cache, length, 4, workspace=torch.empty(2 * n, dtype=torch.uint8, device=DEV)[::2])
+
+
+@pytest.mark.parametrize("ask", [(1.0, 0, 1.0, 0.0), (1.0, 0, 0.97, 0.0), (0.8, 30000, 1.0, 0.0)])
+@pytest.mark.parametrize("dtype", [torch.float32, BF], ids=["f32", "bf16"])
+def test_equal_logits_alone_and_among_others(dtype, ask):
+    """Sums of many equal weights, where roundings would add up: the same probabilities, to the last bit, whatever the
+    size of the cluster, and right to half a step of float32."""
+    B, V = 96, 100003
+    g = torch.Generator(device=DEV).manual_seed(7)
+    z = (-4.0 * torch.rand((B, 1, 1), generator=g, device=DEV) - 1.0).expand(B, 1, V).contiguous()
+    z[:, 0, V // 2] = 2.0
+    z[:, 0, V // 3:V // 3 + 5000] += 0.5
+    z = z.to(dtype)
+    u = torch.rand((B, 1), generator=g, device=DEV)
+    f, exact = _filters([ask] * B)
+    one, _ = _filters([ask])
+    tokens, prob = sv.spec_filter_sample(z, u, f)
+    alone = [sv.spec_filter_sample(z[b:b + 1], u[b:b + 1], one) for b in range(B)]
+    assert torch.equal(torch.cat([t for t, _ in alone]), tokens)
+    assert torch.equal(torch.cat([p for _, p in alone]), prob)
+    t, p, margin, _ = oracle.sample(z[:24].double().cpu().numpy(), u[:24].double().cpu().numpy(), exact[:24])
+    near = margin < NEAR
+    assert near.sum() <= 2
+    assert ((tokens[:24].cpu().numpy() == t) | near).all()
+    off = np.abs(prob[:24].double().cpu().numpy() - p)[~near]
+    assert (off <= (1.01 * (2.0 ** -24 + 2.0 ** -30) * p + 2.0 ** -43)[~near]).all()
