@@ -420,9 +420,10 @@ spec_status_t spec_verify_attention(const void *q, const void *prefix, const uin
  * stretches.
  * Arguments, results, errors and roundings are spec_verify_attention's, with the
  * workspace of spec_attention_workspace_bytes(B, T, Hq, Hkv, D, 0, L); weights of
- * cache entries that not all of a sequence's tokens see, and of sinks where sinks x T
- * x Hq / Hkv <= 640, are not rounded.  Limits: window >= 1, sinks >= 0.  Two launches, one more with a
- * mask (without a cache: one).  Asynchronous on `stream`.                      */
+ * cache entries that not all of a sequence's tokens see are not rounded, nor those
+ * of sinks ahead of entries that no or not every token sees, where sinks x
+ * min(T x Hq / Hkv, 256) <= 640.  Limits: window >= 1, sinks >= 0.  Two launches, one
+ * more with a mask (without a cache: one).  Asynchronous on `stream`.           */
 spec_status_t spec_verify_window_attention(const void *q, const void *cache, const uint8_t *cache_scale, int quant,
                                            const int32_t *seq_len, const void *staged, const uint8_t *mask, int window,
                                            int sinks, int B, int T, int Hq, int Hkv, int D, int L, float sm_scale,
