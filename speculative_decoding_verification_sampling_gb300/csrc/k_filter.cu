@@ -279,7 +279,7 @@ constexpr int FEW = FILTER_CAP / 2;
 struct RowShared {
     u64 board[2][4][MAX_C * FW];   // published, by round parity: up to four numbers of every warp of the cluster
     u64 seg[2][FW];                // of this CTA's warps
-    u64 sums[FW], sums2[FW];
+    u64 sums[FW];
     Search search;
     float2 table[64];
     float top[FT];        // the threads' maxima
@@ -306,6 +306,7 @@ struct RowShared {
     };
 };
 constexpr size_t ROW_SMEM = sizeof(RowShared);
+static_assert(ROW_SMEM <= 48 << 10, "more has to be asked for");
 
 // ------------------------------------------------------------------ one row
 __device__ __forceinline__ void cl_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -1369,7 +1370,7 @@ __global__ void __launch_bounds__(FT, 4) filter_rows(const __grid_constant__ Fil
 
 // ------------------------------------------------------------------ the rule
 struct DecideShared {
-    u64 slot[2][2][FW];
+    u64 slot[2][FW];
     u64 sums[FW];
     float2 table[64];
     int j, code, seg;
@@ -1509,15 +1510,15 @@ __global__ void __launch_bounds__(FT) filter_decide(const __grid_constant__ Filt
     s = warp_sum64(s);
     sq = warp_sum64(sq);
     if (lane == 0) {
-        S.slot[0][0][warp] = s;
-        S.slot[0][1][warp] = sq;
+        S.slot[0][warp] = s;
+        S.slot[1][warp] = sq;
     }
     if (tid == 0)
         S.seg = -1;
     cl_sync();
     u64 all = 0, all_q = 0, before = 0, before_q = 0;
     for (int g = lane; g < C * FW; g += 32) {
-        const u64 a = *cl.map_shared_rank(&S.slot[0][0][g % FW], g / FW), c = *cl.map_shared_rank(&S.slot[0][1][g % FW], g / FW);
+        const u64 a = *cl.map_shared_rank(&S.slot[0][g % FW], g / FW), c = *cl.map_shared_rank(&S.slot[1][g % FW], g / FW);
         all += a;
         all_q += c;
         before += g < me ? a : 0;
