@@ -423,7 +423,12 @@ spec_status_t spec_verify_attention(const void *q, const void *prefix, const uin
  * cache entries that not all of a sequence's tokens see are not rounded, nor those
  * of sinks ahead of entries that no or not every token sees, where sinks x
  * min(T x Hq / Hkv, 256) <= 640.  Limits: window >= 1, sinks >= 0.  Two launches, one
- * more with a mask (without a cache: one).  Asynchronous on `stream`.           */
+ * more with a mask (without a cache: one).  Asynchronous on `stream`.
+ * Made for the passes of a verification, a chain or a tree.  A longer one, a part of
+ * a prompt, is taken too, but slowly: what only some tokens' windows reach, and the
+ * pass's own entries, are added row by row, T x min(T, window) of them to a head
+ * (one sequence, 32/8 heads of 128, windows of 4096 over 8192 entries: 61 tokens 61
+ * us, 128 113 us, 512 363 us, 2048 3.9 ms, under a mask 4.3 ms).              */
 spec_status_t spec_verify_window_attention(const void *q, const void *cache, const uint8_t *cache_scale, int quant,
                                            const int32_t *seq_len, const void *staged, const uint8_t *mask, int window,
                                            int sinks, int B, int T, int Hq, int Hkv, int D, int L, float sm_scale,
