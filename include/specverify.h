@@ -264,8 +264,8 @@ spec_status_t spec_filter_sample(const void *logits, spec_dtype_t ldt, const flo
  *                               emitted token is drawn with when the round ends at i
  *   draft_filters  NULL: the same as `filters`
  *   out_tokens     [B][K+1], out_accept_len [B]  as spec_verify's, with its data errors:
- *                  those of the rows that the left-to-right rule reaches, and of
- *                  filters and uniforms (SPEC_ERR_INVALID_ARG)
+ *                  those of the rows and uniforms that the left-to-right rule
+ *                  reaches, and of filters (SPEC_ERR_INVALID_ARG, as uniforms)
  *   workspace      device scratch of spec_filter_workspace_bytes(B, K, V) bytes (no
  *                  zero-fill needed), 16-byte aligned; one per call in flight
  *   device_status  [1] set to 0, or the code of one failing sequence; may be NULL

@@ -159,67 +159,7 @@ __global__ void __launch_bounds__(WIDE ? WIDE * 32 : 128, WIDE ? 1 : WIN ? 6 : 7
             o[k] = mul2(o[k], ff);
         return ref;
     };
-    if constexpr (WIN == 0) {
-        if (P.staged && !bad) {
-            f2 q[NP];
-            {
-                const RawRow<E> raw = load_row<E>(static_cast<const uint16_t *>(P.q) + r * D + sub * AT);
-                const f2 cc = pk(P.c, P.c);
-    #pragma unroll
-                for (int k = 0; k < NP; ++k)
-                    q[k] = mul2(pair_of<E>(raw, k), cc);
-            }
-            const uint8_t *mask = P.mask ? P.mask + (size_t)bt * P.T : nullptr;
-            const size_t step = (size_t)2 * P.H * D;
-            const uint16_t *x = static_cast<const uint16_t *>(P.staged) + (size_t)b * P.T * step + (size_t)h * D + sub * AT;
-            const int end = mask ? P.T : t + 1;
-            for (int j0 = 0; j0 < end; j0 += 32) {
-                const int j = j0 + lane;
-                unsigned seen = __ballot_sync(0xffffffffu, j < end && (!mask || __ldg(mask + j)));
-                if constexpr (WIDE != 0)
-                    seen &= (0xffffffffu / ((1u << FW) - 1)) << warp;   // this warp's share
-                while (seen) {
-                    // two visible entries at a time
-                    const int ja = __ffs(seen) - 1;
-                    seen &= seen - 1;
-                    const bool two = seen != 0;
-                    const int jb = two ? __ffs(seen) - 1 : ja;
-                    seen &= seen - 1;
-                    const uint16_t *ea = x + (size_t)(j0 + ja) * step, *eb = x + (size_t)(j0 + jb) * step;
-                    const RawRow<E> ka = load_row<E>(ea), kb = load_row<E>(eb);
-                    const RawRow<E> va = load_row<E>(ea + (size_t)P.H * D), vb = load_row<E>(eb + (size_t)P.H * D);
-                    f2 da = pk(0.0f, 0.0f), db = da;
-    #pragma unroll
-                    for (int k = 0; k < NP; ++k) {
-                        da = fma2(q[k], pair_of<E>(ka, k), da);
-                        db = fma2(q[k], pair_of<E>(kb, k), db);
-                    }
-                    float a0, a1, b0, b1;
-                    upk(da, a0, a1);
-                    upk(db, b0, b1);
-                    float sa = a0 + a1, sb = b0 + b1;
-    #pragma unroll
-                    for (int w = LPR / 2; w; w >>= 1) {
-                        sa += __shfl_xor_sync(0xffffffffu, sa, w);
-                        sb += __shfl_xor_sync(0xffffffffu, sb, w);
-                    }
-                    const float ref = rescale(two ? fmaxf(sa, sb) : sa);
-                    const float pa = ex2a(sa - ref), pb = two ? ex2a(sb - ref) : 0.0f;
-                    l += pa + pb;
-                    const f2 wa = pk(pa, pa), wb = pk(pb, pb);
-    #pragma unroll
-                    for (int k = 0; k < NP; ++k) {
-                        o[k] = fma2(wa, pair_of<E>(va, k), o[k]);
-                        if (two)
-                            o[k] = fma2(wb, pair_of<E>(vb, k), o[k]);
-                    }
-                }
-            }
-        }
-    } else if (!bad) {
-        // entries that the tile kernel leaves to the rows: few sinks, what only some windows reach, and
-        // this pass's own; in this order, each `fk` and `fv` times its key and value
-        const AttnWindow win(P, b);
+    if (!bad && (WIN || P.staged)) {
         f2 q[NP];
         {
             const RawRow<E> raw = load_row<E>(static_cast<const uint16_t *>(P.q) + r * D + sub * AT);
@@ -228,6 +168,8 @@ __global__ void __launch_bounds__(WIDE ? WIDE * 32 : 128, WIDE ? 1 : WIN ? 6 : 7
             for (int k = 0; k < NP; ++k)
                 q[k] = mul2(pair_of<E>(raw, k), cc);
         }
+        // two entries at a time (`two` false: the second is the first once more), each `fk` and `fv` times its key
+        // and value
         auto attend = [&](const RawRow<E> &ka, const RawRow<E> &va, float fka, float fva, const RawRow<E> &kb,
                           const RawRow<E> &vb, float fkb, float fvb, bool two) {
             f2 da = pk(0.0f, 0.0f), db = da;
@@ -258,21 +200,23 @@ __global__ void __launch_bounds__(WIDE ? WIDE * 32 : 128, WIDE ? 1 : WIN ? 6 : 7
                     o[k] = fma2(wb, pair_of<E>(vb, k), o[k]);
             }
         };
+        const size_t step = (size_t)2 * P.H * D;
         const uint8_t *mask = P.mask ? P.mask + (size_t)bt * P.T : nullptr;
-        // how many entries of this pass the token sees
-        int seen_all = 0;
-        if (P.staged && mask) {
-            for (int j0 = 0; j0 < P.T; j0 += 32)
-                seen_all += __popc(__ballot_sync(0xffffffffu, j0 + lane < P.T && __ldg(mask + j0 + lane)));
-        } else if (P.staged) {
-            seen_all = t + 1;
-        }
-        const int back = P.window - seen_all;   // of the cache's last entries
-        // of the cache: [0, few) and [low, from)
-        const int low = win.from > 0 ? max(P.sinks, win.n - max(min(back, win.n), 0)) : 0;
-        const int some = win.few + max(win.from - low, 0);
-        {
-            const size_t step = (size_t)2 * P.H * D;
+        int cached = 0, seen_all = 0;   // the sequence's entries in the cache; how many of this pass the token sees
+        if constexpr (WIN != 0) {
+            // entries of the cache that the tile kernel leaves to the rows: few sinks, and what only some windows reach
+            const AttnWindow win(P, b);
+            cached = win.n;
+            if (P.staged && mask) {
+                for (int j0 = 0; j0 < P.T; j0 += 32)
+                    seen_all += __popc(__ballot_sync(0xffffffffu, j0 + lane < P.T && __ldg(mask + j0 + lane)));
+            } else if (P.staged) {
+                seen_all = t + 1;
+            }
+            const int back = P.window - seen_all;   // of the cache's last entries
+            // [0, few) and [low, from)
+            const int low = win.from > 0 ? max(P.sinks, win.n - max(min(back, win.n), 0)) : 0;
+            const int some = win.few + max(win.from - low, 0);
             const uint8_t *scale = P.cscale ? P.cscale + (size_t)b * P.L * 2 * P.H + h : nullptr;
             const size_t at0 = (size_t)b * P.L * step + (size_t)h * D + sub * AT;
             auto fetch = [&](int i, RawRow<E> &k, RawRow<E> &v, float &fk, float &fv) {
@@ -302,17 +246,19 @@ __global__ void __launch_bounds__(WIDE ? WIDE * 32 : 128, WIDE ? 1 : WIN ? 6 : 7
             }
         }
         if (P.staged) {
-            const size_t step = (size_t)2 * P.H * D;
+            // this pass's own
             const uint16_t *x = static_cast<const uint16_t *>(P.staged) + (size_t)b * P.T * step + (size_t)h * D + sub * AT;
             const int end = mask ? P.T : t + 1;
             int ahead = 0;   // that the token sees, ahead of j0
             for (int j0 = 0; j0 < end; j0 += 32) {
                 const int j = j0 + lane;
                 unsigned seen = __ballot_sync(0xffffffffu, j < end && (!mask || __ldg(mask + j)));
-                const int rank = ahead + __popc(seen & ((1u << lane) - 1));
-                ahead += __popc(seen);
-                // by its place among all the token's entries
-                seen &= __ballot_sync(0xffffffffu, rank >= seen_all - P.window || win.n < P.sinks - rank);
+                if constexpr (WIN != 0) {
+                    // by its place among all the token's entries
+                    const int rank = ahead + __popc(seen & ((1u << lane) - 1));
+                    ahead += __popc(seen);
+                    seen &= __ballot_sync(0xffffffffu, rank >= seen_all - P.window || cached < P.sinks - rank);
+                }
                 if constexpr (WIDE != 0)
                     seen &= (0xffffffffu / ((1u << FW) - 1)) << warp;   // this warp's share
                 while (seen) {
