@@ -43,7 +43,7 @@
 // The verification (filter_decide) reads the rows' records, walks the positions
 // of a sequence in one warp, and draws from (q_j - p_j)+ over the tokens that
 // the target row keeps: from its list, or else over the vocabulary, where a
-// cluster shares it.  256 sequences, K = 4, 128256, top-k 20 to 50: 189 us, of which
+// cluster shares it.  256 sequences, K = 4, 128256, top-k 20 to 50: 190 us, of which
 // it takes 20 us; 3.1 TB/s.
 #include <algorithm>
 #include <atomic>
