@@ -38,7 +38,7 @@
 // tokens to a thread).  256 such rows: 26 us (2.5 TB/s: two waves of CTAs, each a
 // first pass and then a second one) and 104 us (the instructions of the count, 14 a token,
 // and of the values' weights, and the exchanges, 42 % of the issue slots taken).
-// 256 rows without filters: 71 us (a weight a token, 40 instructions).
+// 256 rows without filters: 71 us (a weight a token, 45 instructions).
 //
 // The verification (filter_decide) reads the rows' records, walks the positions
 // of a sequence in one warp, and draws from (q_j - p_j)+ over the tokens that
